@@ -145,7 +145,7 @@ def _layout(d, device):
     if d == 256:
         v = v ^ (32 * (r & 3))
     s = torch.arange(ng, device=device)[None, :]
-    return {"k": p * (d // 2) + k + 0 * r, "v": 8 * d + r * (d // 2) + v, "ks": 8 * d + p * 2 * ng + s,
+    return {"k": p * (d // 2) + k, "v": 8 * d + r * (d // 2) + v, "ks": 8 * d + p * 2 * ng + s,
             "vs": 8 * d + p * 2 * ng + ng + s}  # scales in 2-byte units
 
 
