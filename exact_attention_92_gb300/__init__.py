@@ -8,6 +8,7 @@ also allocate the outputs.  PyTorch provides device memory and streams only.
 """
 
 from ._binding import (  # noqa: F401
+    FA_ERR_BAD_INDEX,
     FA_ERR_CUDA,
     FA_ERR_INVALID_ARG,
     FA_BWD_NOALLOC_SCRATCH_BYTES,
@@ -33,6 +34,10 @@ from ._binding import (  # noqa: F401
     fa_fwd_general,
     fa_fwd_gqa,
     fa_fwd_plan,
+    fa_kv4_cache_bytes,
+    fa_kv4_fwd,
+    fa_kv4_read,
+    fa_kv4_write,
     fa_poll_status,
     fa_selftest_wait_timeout,
     fa_set_wait_timeout_ns,
@@ -42,6 +47,8 @@ from ._binding import (  # noqa: F401
     fa_timing_read,
     fa_trim_workspace,
     forward,
+    kv4_cache,
+    kv4_forward,
     load,
 )
 
@@ -50,3 +57,7 @@ FA_KERNEL_COMBINE = 1
 FA_KERNEL_BWD_PRE = 2
 FA_KERNEL_BWD = 3
 FA_KERNEL_BWD_DQ = 4
+FA_KERNEL_KV4_WRITE = 8
+FA_KERNEL_KV4_READ = 9
+FA_KERNEL_KV4_FWD = 10
+FA_KERNEL_KV4_MERGE = 11

@@ -26,6 +26,7 @@ FA_ERR_CUDA = 3
 FA_ERR_NO_MEMORY = 4
 FA_ERR_TIMEOUT = 5
 FA_ERR_SCRATCH_TOO_SMALL = 6
+FA_ERR_BAD_INDEX = 7
 FA_BWD_NOALLOC_SCRATCH_BYTES = 64 << 20
 FA_CAUSAL_NONE = 0
 FA_CAUSAL_TOP_LEFT = 1
@@ -57,6 +58,10 @@ _SIGNATURES = {
     "fa_bwd_noalloc": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp], _i),
     "fa_fwd_general": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp], _i),
     "fa_bwd_general": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp], _i),
+    "fa_kv4_cache_bytes": ([_i, _i, _i, _i, ctypes.POINTER(_u64)], _i),
+    "fa_kv4_write": ([_vp] * 6 + [_i] * 7 + [_vp], _i),
+    "fa_kv4_read": ([_vp] * 6 + [_i] * 7 + [_vp], _i),
+    "fa_kv4_fwd": ([_vp] * 6 + [_i] * 9 + [_f, _vp], _i),
     "fa_poll_status": ([_vp], _i),
     "fa_set_wait_timeout_ns": ([_u64], _u64),
     "fa_selftest_wait_timeout": ([_u64, _vp], _i),
@@ -297,6 +302,94 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, causal=False, scale=None, 
     _check(st, "fa_bwd_noalloc")
 
 
+def _check_on_device(name, t):
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _check_int32(name, t, shape):
+    import torch
+
+    _check_on_device(name, t)
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or any(
+            w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be a contiguous int32 tensor {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _check_cache(cache, d):
+    """(num_pages, Hkv, page_size) of a cache tensor for head dim d."""
+    import torch
+
+    _check_on_device("cache", cache)
+    if cache.dtype != torch.uint8 or cache.dim() != 3 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 [num_pages, Hkv, page_size * 9 d / 8] tensor")
+    num_pages, Hkv, page_bytes = cache.shape
+    page_size, rest = divmod(page_bytes * 8, 9 * d)
+    if rest or page_size < 1:
+        raise ValueError(f"cache has {page_bytes} bytes a page and head, not a multiple of 9 * {d} / 8")
+    return num_pages, Hkv, page_size
+
+
+def fa_kv4_cache_bytes(num_pages, Hkv, page_size, d) -> int:
+    """C fa_kv4_cache_bytes: bytes of a 4-bit key/value cache."""
+    n = ctypes.c_uint64(0)
+    _check(load().fa_kv4_cache_bytes(int(num_pages), int(Hkv), int(page_size), int(d), ctypes.byref(n)),
+           "fa_kv4_cache_bytes")
+    return n.value
+
+
+def _kv4_move(what, k, v, cache, block_table, start, count):
+    _check_bhnd("k", k)
+    B, Hkv, N, d = k.shape
+    _check_bhnd("v", v, k.shape)
+    num_pages, heads, page_size = _check_cache(cache, d)
+    if heads != Hkv:
+        raise ValueError(f"cache has {heads} heads, k has {Hkv}")
+    _check_int32("block_table", block_table, (B, None))
+    _check_int32("start", start, (B,))
+    if count is not None:
+        _check_int32("count", count, (B,))
+    return B, Hkv, N, d, num_pages, page_size, block_table.shape[1]
+
+
+def fa_kv4_write(k, v, cache, block_table, start, count=None, stream=None):
+    """C fa_kv4_write: quantise tokens k, v [B, Hkv, N, d] into the 4-bit
+    cache [num_pages, Hkv, page_size * 9 d / 8] (uint8), token i < count[b]
+    (all N without count) of sequence b to position start[b] + i."""
+    sizes = _kv4_move("fa_kv4_write", k, v, cache, block_table, start, count)
+    _check(load().fa_kv4_write(_ptr(k), _ptr(v), _ptr(cache), _ptr(block_table), _ptr(start),
+                               None if count is None else _ptr(count), *sizes, _stream_ptr(stream, k.device)),
+           "fa_kv4_write")
+
+
+def fa_kv4_read(cache, block_table, start, k, v, count=None, stream=None):
+    """C fa_kv4_read: the held values of positions start[b] + i to rows
+    i < count[b] of k, v [B, Hkv, N, d]; other rows are left as they were."""
+    sizes = _kv4_move("fa_kv4_read", k, v, cache, block_table, start, count)
+    _check(load().fa_kv4_read(_ptr(cache), _ptr(block_table), _ptr(start), None if count is None else _ptr(count),
+                              _ptr(k), _ptr(v), *sizes, _stream_ptr(stream, k.device)), "fa_kv4_read")
+
+
+def fa_kv4_fwd(q, cache, block_table, lens, o, lse, causal=False, scale=None, stream=None):
+    """C fa_kv4_fwd: attention of q [B, H, Nq, d] over the first lens[b]
+    tokens of each sequence in the 4-bit cache; causal as fa_fwd_general."""
+    _check_bhnd("q", q)
+    B, H, Nq, d = q.shape
+    num_pages, Hkv, page_size = _check_cache(cache, d)
+    _check_int32("block_table", block_table, (B, None))
+    _check_int32("lens", lens, (B,))
+    _check_bhnd("o", o, q.shape)
+    _check_lse(lse, (B, H, Nq))
+    _check_on_device("lse", lse)
+    _check(load().fa_kv4_fwd(_ptr(q), _ptr(cache), _ptr(block_table), _ptr(lens), _ptr(o), _ptr(lse), B, H, Hkv, Nq,
+                             d, num_pages, page_size, block_table.shape[1], _causal_code(causal), _scale(scale, d),
+                             _stream_ptr(stream, q.device)), "fa_kv4_fwd")
+
+
 def fa_poll_status(stream=None):
     """C fa_poll_status: synchronise the stream, return and clear the device status."""
     import torch
@@ -402,3 +495,22 @@ def backward(q, k, v, o, lse, dout, causal=False, scale=None):
     else:
         fa_bwd_general(q, k, v, o, lse, dout, dq, dk, dv, causal, scale)
     return dq, dk, dv
+
+
+def kv4_cache(num_pages, Hkv, page_size, d, device="cuda"):
+    """A 4-bit key/value cache of num_pages pages, zeroed (every value reads
+    as 0): uint8 [num_pages, Hkv, page_size * 9 d / 8]."""
+    import torch
+
+    fa_kv4_cache_bytes(num_pages, Hkv, page_size, d)  # refuses bad sizes
+    return torch.zeros((num_pages, Hkv, page_size * 9 * d // 8), dtype=torch.uint8, device=device)
+
+
+def kv4_forward(q, cache, block_table, lens, causal=False, scale=None):
+    """Allocate O and LSE and run fa_kv4_fwd; returns (o, lse)."""
+    import torch
+
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    fa_kv4_fwd(q, cache, block_table, lens, o, lse, causal, scale)
+    return o, lse

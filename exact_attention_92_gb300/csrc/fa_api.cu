@@ -38,9 +38,12 @@ cudaError_t launch_bwd_preprocess(int d, const void* o, const void* dout, float*
 cudaError_t launch_selftest_wait(unsigned int* status, unsigned long long timeout_ns, cudaStream_t stream);
 }  // namespace fa
 
-// One status word per device that loads the library.  Kernels record the
-// first failing wait here; fa_poll_status reads and clears it.
-static __device__ unsigned int g_fa_status_word;
+// Two status words per device that loads the library; fa_poll_status reads
+// and clears them.  Word 0: kernels record the first failing wait here, and a
+// slow wait of any kernel that finds it set gives up too.  Word 1: the 4-bit
+// cache kernels record that they skipped an index out of range (no wait
+// looks at it, so a bad index disturbs no other call).
+static __device__ unsigned int g_fa_status_word[2];
 
 namespace {
 
@@ -53,7 +56,7 @@ struct DeviceState {
   bool ready = false;
   int sm_count = 0;
   double l2_bytes = 0.0;
-  unsigned int* status = nullptr;  // device address of g_fa_status_word
+  unsigned int* status = nullptr;  // device address of g_fa_status_word (2 words)
   cudaMemPool_t pool = nullptr;    // the library's workspace pool on this device
 };
 
@@ -93,7 +96,7 @@ int device_state(DeviceState** out) {
         cudaGetLastError();
         return FA_ERR_CUDA;
       }
-      if (cudaMemset(addr, 0, sizeof(unsigned int)) != cudaSuccess) {
+      if (cudaMemset(addr, 0, sizeof(g_fa_status_word)) != cudaSuccess) {
         cudaGetLastError();
         return FA_ERR_CUDA;
       }
@@ -414,7 +417,12 @@ struct TimingRec {
 std::mutex g_tmu;
 bool g_timing = false;
 // Launches of each library kernel since the library was loaded (always on).
-std::atomic<unsigned long long> g_launches[FA_KERNEL_BWD_DQ + 1];
+std::atomic<unsigned long long> g_launches[FA_KERNEL_KV4_MERGE + 1];
+
+bool kernel_id(int k) {
+  return (k >= FA_KERNEL_FWD && k <= FA_KERNEL_BWD_DQ) || (k >= FA_KERNEL_KV4_WRITE && k <= FA_KERNEL_KV4_MERGE);
+}
+
 std::vector<TimingRec> g_recs;
 std::vector<cudaEvent_t> g_pool;
 
@@ -468,6 +476,12 @@ int internal_validate(int B, int H, int N, int d, float scale) { return validate
 int internal_encode_bhnd(CUtensorMap* m, const void* ptr, int BH, int N, int d, int box_rows) {
   return encode_bhnd(m, ptr, BH, N, d, box_rows);
 }
+// Workspace from the library's pool on the current device (set up before).
+cudaError_t internal_workspace(void** ptr, size_t bytes, cudaStream_t st) {
+  DeviceState* s = nullptr;
+  if (device_state(&s) != FA_OK) return cudaErrorUnknown;
+  return ws_alloc(s->pool, ptr, bytes, st);
+}
 unsigned long long internal_wait_timeout_ns() { return g_timeout_ns.load(); }
 // A launch of library kernel `kernel` by another file of the library, counted
 // and (while timing is on) bracketed by events like the launches here.
@@ -491,13 +505,13 @@ int fa_timing_enable(int on) {
 }
 
 int fa_launch_count(int kernel, uint64_t* count) {
-  if (!count || kernel < 0 || kernel > FA_KERNEL_BWD_DQ) return FA_ERR_INVALID_ARG;
+  if (!count || !kernel_id(kernel)) return FA_ERR_INVALID_ARG;
   *count = g_launches[kernel].load(std::memory_order_relaxed);
   return FA_OK;
 }
 
 int fa_timing_read(int kernel, int* launches, double* total_ms) {
-  if (!launches || !total_ms || kernel < 0 || kernel > FA_KERNEL_BWD_DQ) return FA_ERR_INVALID_ARG;
+  if (!launches || !total_ms || !kernel_id(kernel)) return FA_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> g(g_tmu);
   int n = 0;
   double ms = 0.0;
@@ -541,6 +555,8 @@ const char* fa_strerror(int status) {
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: a device-side wait gave up";
     case FA_ERR_SCRATCH_TOO_SMALL:
       return "FA_ERR_SCRATCH_TOO_SMALL: problem needs more than the static scratch of fa_bwd_noalloc";
+    case FA_ERR_BAD_INDEX:
+      return "FA_ERR_BAD_INDEX: a page, position or length on the device was out of range and was skipped";
     default: return "unknown fa_status";
   }
 }
@@ -553,10 +569,10 @@ int fa_poll_status(void* stream) {
   if (e) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return FA_ERR_CUDA;
-  unsigned int word = 0;
-  if (cudaMemcpy(&word, s->status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return FA_ERR_CUDA;
-  if (word != 0u && cudaMemset(s->status, 0, sizeof(word)) != cudaSuccess) return FA_ERR_CUDA;
-  return (int)(word & 0xffu);
+  unsigned int word[2] = {0u, 0u};
+  if (cudaMemcpy(word, s->status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return FA_ERR_CUDA;
+  if ((word[0] | word[1]) != 0u && cudaMemset(s->status, 0, sizeof(word)) != cudaSuccess) return FA_ERR_CUDA;
+  return word[0] != 0u ? (int)(word[0] & 0xffu) : (int)word[1];
 }
 
 int fa_selftest_wait_timeout(uint64_t timeout_ns, void* stream) {

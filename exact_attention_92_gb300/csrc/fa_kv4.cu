@@ -1,0 +1,164 @@
+// Host side of the 4-bit key/value cache calls (include/fa.h): argument
+// checks and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "fa_common.h"
+#include "kv4_fwd.h"
+
+namespace fa {
+int internal_device_setup(unsigned int** status, int* sm_count);
+cudaError_t internal_timed_launch(int kernel, cudaStream_t stream, cudaError_t (*launch)(void*), void* ctx);
+cudaError_t launch_kv4_move(int d, bool write, const Kv4Cache& c, const int* start, const int* count, const void* k_in,
+                            const void* v_in, void* k_out, void* v_out, int N, cudaStream_t stream);
+cudaError_t launch_kv4_fwd(int d, const Kv4FwdParams& p, cudaStream_t stream);
+}  // namespace fa
+
+namespace {
+
+constexpr int kMinPage = 16, kMaxPage = 1024;
+constexpr int kMaxRows = 128;  // query rows of a key/value head's group (fa_kv4_fwd)
+
+bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool head_dim(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
+
+// Sizes that every call over a cache has; `rows` counts the rows of its bf16
+// tensors per (batch, head).
+int check_sizes(int B, int heads, int Hkv, int rows, int d, int num_pages, int page_size, int max_pages) {
+  if (B < 1 || heads < 1 || Hkv < 1 || rows < 1 || num_pages < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (page_size < kMinPage || page_size > kMaxPage || (page_size & (page_size - 1)) != 0) return FA_ERR_INVALID_ARG;
+  if (!head_dim(d)) return FA_ERR_UNSUPPORTED;
+  const long long most = 0x7fffffffLL;
+  if ((long long)max_pages * page_size > most) return FA_ERR_INVALID_ARG;
+  if ((long long)B * heads > most || (long long)B * heads * rows > most) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa::Kv4Cache view(const void* cache, const int* table, int B, int Hkv, int num_pages, int page_size, int max_pages,
+                  unsigned int* status) {
+  fa::Kv4Cache c;
+  c.pages = static_cast<uint8_t*>(const_cast<void*>(cache));
+  c.table = table;
+  c.num_pages = num_pages;
+  c.max_pages = max_pages;
+  c.Hkv = Hkv;
+  c.page_shift = 0;
+  while ((1 << c.page_shift) < page_size) ++c.page_shift;
+  c.B = B;
+  c.status = status;
+  return c;
+}
+
+struct Move {
+  int d;
+  bool write;
+  fa::Kv4Cache c;
+  const int *start, *count;
+  const void *k_in, *v_in;
+  void *k_out, *v_out;
+  int N;
+  cudaStream_t st;
+};
+
+cudaError_t run_move(void* ctx) {
+  const Move& m = *static_cast<const Move*>(ctx);
+  return fa::launch_kv4_move(m.d, m.write, m.c, m.start, m.count, m.k_in, m.v_in, m.k_out, m.v_out, m.N, m.st);
+}
+
+int move(bool write, const void* k_in, const void* v_in, void* k_out, void* v_out, const void* cache,
+         const int* block_table, const int* start, const int* count, int B, int Hkv, int N, int d, int num_pages,
+         int page_size, int max_pages, void* stream) {
+  const void* k = write ? k_in : k_out;
+  const void* v = write ? v_in : v_out;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cache, 16) || !aligned(block_table, 4) || !aligned(start, 4) ||
+      (count != nullptr && !aligned(count, 4)))
+    return FA_ERR_INVALID_ARG;
+  int e = check_sizes(B, Hkv, Hkv, N, d, num_pages, page_size, max_pages);
+  if (e) return e;
+  unsigned int* status = nullptr;
+  int sm_count = 0;
+  e = fa::internal_device_setup(&status, &sm_count);
+  if (e) return e;
+  Move m{d, write, view(cache, block_table, B, Hkv, num_pages, page_size, max_pages, status), start, count, k_in, v_in,
+         k_out, v_out, N, static_cast<cudaStream_t>(stream)};
+  const int id = write ? FA_KERNEL_KV4_WRITE : FA_KERNEL_KV4_READ;
+  return fa::internal_timed_launch(id, m.st, run_move, &m) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+struct Fwd {
+  int d;
+  fa::Kv4FwdParams p;
+  cudaStream_t st;
+};
+
+cudaError_t run_fwd(void* ctx) {
+  const Fwd& f = *static_cast<const Fwd*>(ctx);
+  return fa::launch_kv4_fwd(f.d, f.p, f.st);
+}
+
+int check_fwd_sizes(int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size, int max_pages, int causal) {
+  const int e = check_sizes(B, H, Hkv, Nq, d, num_pages, page_size, max_pages);
+  if (e) return e;
+  if (H % Hkv != 0 || causal < FA_CAUSAL_NONE || causal > FA_CAUSAL_BOTTOM_RIGHT) return FA_ERR_INVALID_ARG;
+  if ((long long)(H / Hkv) * Nq > kMaxRows) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d, uint64_t* bytes) {
+  if (bytes == nullptr) return FA_ERR_INVALID_ARG;
+  const int e = check_sizes(1, 1, Hkv, 1, d, num_pages, page_size, 1);
+  if (e) return e;
+  *bytes = (uint64_t)num_pages * Hkv * page_size * (9 * d / 8);
+  return FA_OK;
+}
+
+int fa_kv4_write(const void* k, const void* v, void* cache, const int* block_table, const int* start,
+                 const int* count, int B, int Hkv, int N, int d, int num_pages, int page_size, int max_pages,
+                 void* stream) {
+  return move(true, k, v, nullptr, nullptr, cache, block_table, start, count, B, Hkv, N, d, num_pages, page_size,
+              max_pages, stream);
+}
+
+int fa_kv4_read(const void* cache, const int* block_table, const int* start, const int* count, void* k, void* v,
+                int B, int Hkv, int N, int d, int num_pages, int page_size, int max_pages, void* stream) {
+  return move(false, nullptr, nullptr, k, v, cache, block_table, start, count, B, Hkv, N, d, num_pages, page_size,
+              max_pages, stream);
+}
+
+int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const int* lens, void* o, float* lse,
+               int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size, int max_pages, int causal,
+               float scale, void* stream) {
+  if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(block_table, 4) ||
+      !aligned(lens, 4))
+    return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
+  int e = check_fwd_sizes(B, H, Hkv, Nq, d, num_pages, page_size, max_pages, causal);
+  if (e) return e;
+  unsigned int* status = nullptr;
+  int sm_count = 0;
+  e = fa::internal_device_setup(&status, &sm_count);
+  if (e) return e;
+  Fwd f;
+  f.d = d;
+  f.p.c = view(cache, block_table, B, Hkv, num_pages, page_size, max_pages, status);
+  f.p.q = static_cast<const __nv_bfloat16*>(q);
+  f.p.lens = lens;
+  f.p.o = static_cast<__nv_bfloat16*>(o);
+  f.p.lse = lse;
+  f.p.H = H;
+  f.p.Nq = Nq;
+  f.p.causal = causal;
+  f.p.scale_log2 = scale * 1.4426950408889634f;
+  f.st = static_cast<cudaStream_t>(stream);
+  return fa::internal_timed_launch(FA_KERNEL_KV4_FWD, f.st, run_fwd, &f) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

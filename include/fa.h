@@ -65,7 +65,9 @@ typedef enum {
   FA_ERR_CUDA = 3,        /* a CUDA runtime call or kernel launch failed     */
   FA_ERR_NO_MEMORY = 4,   /* workspace allocation failed                     */
   FA_ERR_TIMEOUT = 5,     /* a device-side wait gave up (fa_poll_status)     */
-  FA_ERR_SCRATCH_TOO_SMALL = 6 /* fa_bwd_noalloc: problem exceeds its scratch */
+  FA_ERR_SCRATCH_TOO_SMALL = 6, /* fa_bwd_noalloc: problem exceeds its scratch */
+  FA_ERR_BAD_INDEX = 7 /* fa_kv4_*: a page, position or length on the device was
+                          out of range and was skipped (fa_poll_status) */
 } fa_status;
 
 /*
@@ -300,9 +302,102 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
                    float scale, void* stream);
 
 /*
+ * Key/value cache held in 4 bits, in pages.
+ *
+ * The cache is one buffer of bytes, [num_pages, Hkv, page_bytes] with
+ * page_bytes = page_size * 9 d / 8: keys and values of page_size tokens of
+ * one key/value head, 4.5 bits a value.  The pages have no counterpart (the
+ * papers' K and V are bf16 or fp16): this is the library's form of a serving
+ * cache.  Sequence b's token at position i lives in page
+ * block_table[b][i / page_size], at i % page_size in it.
+ *
+ * Format.  The d channels of a token's key (and of its value) are held in
+ * groups of 32.  A group has a scale s = bf16(max|x| / 6), and each channel
+ * a 4-bit code of e2m1 (sign, two exponent bits, one mantissa bit: 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6) of x / s, rounded to nearest, ties to even, saturating at
+ * 6 (a zero may carry either sign).  The value held is code * s.  A scale
+ * below 2^-126 is stored as 0 (the group reads as 0); a group with a NaN or
+ * an infinity gets the scale NaN and reads as NaN throughout.
+ * Tokens are stored in blocks of 16 (18 d bytes).  Within a block, with
+ * NG = d / 32 and p the token's place in it (0..15):
+ *   bytes [0, 8d)    keys: row p of d/2 bytes.  The 4-byte word at index
+ *                    (g / 4) * 16 + t * min(NG, 4) + g % 4 of the row holds
+ *                    channels 32 g + 8 t + 0..7, lowest nibble first.  At
+ *                    d = 256 the byte offset in the row is xor'd with
+ *                    64 * (p & 1).
+ *   bytes [8d, 16d)  values: row r = 4 ((p & 1) + 2 (p >> 3)) + ((p >> 1) & 3)
+ *                    of d/2 bytes.  The 2-byte unit at index u * NG + g of
+ *                    the row holds channels 32 g + 4 u + 0..3.  The byte
+ *                    offset in the row is xor'd with 32 * ((r >> 1) & 1) at
+ *                    d = 128 and with 32 * (r & 3) at d = 256.
+ *   bytes [16d, 18d) scales: for each p the NG bf16 scales of the key, then
+ *                    those of the value.
+ * The order of words and rows is the one in which the lanes of a warp feed
+ * m16n8k16 matrix instructions straight from shared memory, without bank
+ * conflicts.  A block never spans two pages.
+ *
+ * Conventions of the fa_kv4_* calls, besides those above:
+ *   page_size   : a power of two from 16 to 1024
+ *   block_table : int32 [B, max_pages], device memory, 4-byte aligned.  Only
+ *                 the entries of pages that hold a position in use are read
+ *                 or used; they must lie in [0, num_pages).
+ *   start, count, lens : int32 [B], device memory, 4-byte aligned
+ *   B * Hkv * N (B * H * Nq) and max_pages * page_size at most 2^31 - 1
+ * These arrays are read on the device, so the host cannot refuse a bad entry:
+ * the kernels check each one, skip what it points to (a token is not written,
+ * a row not read, the keys of that page not attended to; lengths are clamped
+ * to [0, max_pages * page_size]) and record FA_ERR_BAD_INDEX, which
+ * fa_poll_status reports.
+ */
+
+/* Bytes of a cache: num_pages * Hkv * page_size * 9 d / 8 in *bytes. */
+int fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d, uint64_t* bytes);
+
+/*
+ * Quantise tokens into the cache.  Token i < count[b] of sequence b goes to
+ * position start[b] + i.
+ *   k, v  : in, bf16 [B,Hkv,N,d]
+ *   cache : in/out; only the bytes of the tokens written change
+ *   count : tokens of each sequence, 0 <= count[b] <= N, or null: N of each
+ *           (rows past count[b] are not read)
+ * Two tokens of one call that go to the same place (sequences that share a
+ * page, or a page listed twice) leave a mixture of the two there.
+ */
+int fa_kv4_write(const void* k, const void* v, void* cache, const int* block_table, const int* start,
+                 const int* count, int B, int Hkv, int N, int d, int num_pages, int page_size, int max_pages,
+                 void* stream);
+
+/*
+ * Read tokens back: position start[b] + i to row i < count[b] of k and v
+ * (code * scale rounded once to bf16).  Rows past count[b] are left as they
+ * were.  Arguments as fa_kv4_write, with k and v as outputs; a prompt's
+ * history read back this way feeds fa_fwd_general for the next chunk.
+ */
+int fa_kv4_read(const void* cache, const int* block_table, const int* start, const int* count, void* k, void* v,
+                int B, int Hkv, int N, int d, int num_pages, int page_size, int max_pages, void* stream);
+
+/*
+ * Forward attention over the cache: the computation of fa_fwd_general with
+ * the keys and values that the cache holds, each sequence with its own
+ * length.  For decoding: a few query rows per sequence over many keys.
+ *   q, o   : bf16 [B,H,Nq,d];  lse : fp32 [B,H,Nq]
+ *   lens   : tokens of each sequence in the cache, the Nq new ones included
+ *   Hkv    : divides H; (H / Hkv) * Nq <= 128 (FA_ERR_UNSUPPORTED above:
+ *            read the keys back and call fa_fwd_general)
+ *   causal : with Nk = lens[b] for sequence b: FA_CAUSAL_NONE, _TOP_LEFT or
+ *            _BOTTOM_RIGHT.  A row that sees no key gets O = 0, L = -inf
+ *            (all rows of a sequence of length 0).
+ * Scores, softmax and sums are fp32 on the exact held values.
+ */
+int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const int* lens, void* o, float* lse,
+               int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size, int max_pages, int causal,
+               float scale, void* stream);
+
+/*
  * Synchronise `stream`, then return and clear the device status word of the
  * current device: FA_OK, FA_ERR_TIMEOUT if a kernel's bounded wait gave up
- * since the last poll, or FA_ERR_CUDA if the synchronisation failed.
+ * since the last poll, FA_ERR_BAD_INDEX if a fa_kv4_* kernel skipped an index
+ * out of range, or FA_ERR_CUDA if the synchronisation failed.
  */
 int fa_poll_status(void* stream);
 
@@ -341,6 +436,11 @@ int fa_selftest_wait_timeout(uint64_t timeout_ns, void* stream);
 #define FA_KERNEL_BWD_PRE 2
 #define FA_KERNEL_BWD 3
 #define FA_KERNEL_BWD_DQ 4
+/* Kernels over the 4-bit cache (5 to 7 are not ids). */
+#define FA_KERNEL_KV4_WRITE 8
+#define FA_KERNEL_KV4_READ 9
+#define FA_KERNEL_KV4_FWD 10
+#define FA_KERNEL_KV4_MERGE 11
 int fa_timing_enable(int on);
 int fa_timing_read(int kernel, int* launches, double* total_ms);
 

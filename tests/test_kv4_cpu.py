@@ -1,0 +1,227 @@
+"""The 4-bit key/value cache without a GPU: pins of its oracle, and the
+refusals that the host makes before any device work."""
+
+import ctypes
+import itertools
+
+import numpy as np
+import pytest
+
+import exact_attention_92_gb300 as fa
+from exact_attention_92_gb300 import _binding, build
+from oracle import kv4
+
+P = ctypes.c_void_p
+DIMS = (64, 96, 128, 256)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return fa.load()
+
+
+# ------------------------------------------------------------------ oracle
+
+@pytest.mark.parametrize("d", DIMS)
+def test_a_block_has_a_place_for_everything(d):
+    """Every nibble and every scale byte of a block belongs to exactly one
+    channel of one token."""
+    seen = set()
+    for p, c in itertools.product(range(16), range(d)):
+        for place in (kv4.key_place(d, p, c), kv4.value_place(d, p, c)):
+            assert place not in seen
+            seen.add(place)
+    assert seen == {(b, s) for b in range(16 * d) for s in (0, 4)}
+    scales = {kv4.scale_place(d, p, w, g) for p in range(16) for w in range(2) for g in range(d // 32)}
+    assert scales == set(range(16 * d, 18 * d, 2))
+
+
+def test_levels_round_to_nearest_with_ties_to_even():
+    """With a largest value of 6 the scale is 1, so the codes are those of
+    e2m1 itself: each border between two levels goes to the even code."""
+    x = np.zeros(32)
+    x[:15] = [6, 0.25, 0.26, 0.75, 0.74, 1.25, 1.26, 1.75, 2.5, 2.52, 3.5, 3.48, 5.0, 5.03, -0.75]
+    code, bits = kv4.quantise(x)
+    assert kv4.bits_value(bits).tolist() == [1.0]
+    assert code[:15].tolist() == [7, 0, 1, 2, 1, 2, 3, 4, 4, 5, 6, 5, 6, 7, 8 | 2]
+    assert (code[15:] == 0).all()
+    assert kv4.values(code, bits)[:8].tolist() == [6, 0, 0.5, 1, 0.5, 1, 1.5, 2]
+
+
+def test_scale_is_the_rounded_sixth_of_the_largest():
+    x = np.zeros((3, 32))
+    x[0, 3], x[1, 4], x[2, 5] = -7.0, 1.0, 2.0 ** -125
+    code, bits = kv4.quantise(x)
+    s = kv4.bits_value(bits)[:, 0]
+    assert abs(s[0] - 7 / 6) <= 2.0 ** -8 and abs(s[1] - 1 / 6) <= 2.0 ** -11
+    assert s[2] == 0.0 and (code[2] == 0).all()  # a scale below 2^-126
+    assert code[0, 3] == 15 and code[1, 4] == 7
+
+
+def test_a_group_with_a_non_finite_value_reads_as_nan():
+    x = np.ones((2, 64))
+    x[0, 5], x[1, 40] = np.inf, np.nan
+    v = kv4.held(x)
+    assert np.isnan(v[0, :32]).all() and np.isfinite(v[0, 32:]).all()
+    assert np.isfinite(v[1, :32]).all() and np.isnan(v[1, 32:]).all()
+
+
+def test_error_of_a_held_value():
+    """A value below the largest level is off by at most half the widest gap
+    (one scale), and the scale by half a step of bf16."""
+    x = kv4.to_bf16(np.random.default_rng(0).standard_normal((200, 128)) * 3)
+    top = np.abs(x.reshape(200, 4, 32)).max(-1)
+    err = np.abs(kv4.held(x) - x).reshape(200, 4, 32).max(-1)
+    # Half the gap from 4 to 6 is one scale, a sixth of the largest value;
+    # the scale's rounding moves the largest level by at most 2^-8 of itself.
+    assert (err <= top / 6 * (1 + 2.0 ** -8)).all()
+
+
+@pytest.mark.parametrize("d", DIMS)
+def test_write_then_read(d):
+    rng = np.random.default_rng(d)
+    page, Hkv = 32, 2
+    cache = np.full((5, Hkv, page * 9 * d // 8), 0xAB, np.uint8)
+    before = cache.copy()
+    table = [[3, 1], [4, 0]]
+    k, v = (kv4.to_bf16(rng.standard_normal((2, Hkv, 20, d))) for _ in range(2))
+    kv4.write(cache, table, [25, 0], [20, 7], k, v, page)
+    for b, first, n in ((0, 25, 20), (1, 0, 7)):
+        rk, rv = kv4.read(cache, table[b], n, page, d, first)
+        assert np.array_equal(rk, kv4.held(k[b, :, :n])) and np.array_equal(rv, kv4.held(v[b, :, :n]))
+    assert np.array_equal(cache[2], before[2])
+    # 27 tokens of 2 heads, 9 d / 8 bytes each, may have changed.
+    assert (cache != before).sum() <= 27 * Hkv * 9 * d // 8
+    assert (cache != before).any(axis=(1, 2)).tolist() == [False, True, False, True, True]
+
+
+def test_bf16_rounding_of_the_oracle():
+    torch = pytest.importorskip("torch")
+    x = np.random.default_rng(1).standard_normal(4000).astype(np.float32) * np.float32(2.0) ** np.arange(-100, 100).repeat(20)
+    want = torch.from_numpy(x).to(torch.bfloat16).double().numpy()
+    assert np.array_equal(kv4.to_bf16(x.astype(np.float64)), want)
+
+
+def test_planted_mistakes_in_the_oracle_show():
+    """Two places exchanged, or a level changed, do not survive the pins."""
+    assert kv4.value_place(128, 2, 0) != kv4.value_place(128, 4, 0)
+    wrong = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 5.0])
+    x = np.zeros(32)
+    x[0] = 6
+    code, bits = kv4.quantise(x)
+    keep = kv4.LEVELS
+    try:
+        kv4.LEVELS = wrong
+        assert kv4.values(code, bits)[0] != 6
+    finally:
+        kv4.LEVELS = keep
+
+
+# ---------------------------------------------------------------- refusals
+
+def test_cache_bytes(lib):
+    for d in DIMS:
+        assert fa.fa_kv4_cache_bytes(10, 8, 64, d) == 10 * 8 * 64 * 9 * d // 8
+    assert fa.fa_kv4_cache_bytes(2 ** 31 - 1, 64, 1024, 256) == (2 ** 31 - 1) * 64 * 1024 * 288
+    n = ctypes.c_uint64()
+    for args, want in (((0, 8, 64, 128), fa.FA_ERR_INVALID_ARG), ((1, 0, 64, 128), fa.FA_ERR_INVALID_ARG),
+                       ((1, 1, 8, 128), fa.FA_ERR_INVALID_ARG), ((1, 1, 48, 128), fa.FA_ERR_INVALID_ARG),
+                       ((1, 1, 2048, 128), fa.FA_ERR_INVALID_ARG), ((1, 1, -16, 128), fa.FA_ERR_INVALID_ARG),
+                       ((1, 1, 64, 80), fa.FA_ERR_UNSUPPORTED), ((1, 1, 64, 0), fa.FA_ERR_UNSUPPORTED)):
+        assert lib.fa_kv4_cache_bytes(*args, ctypes.byref(n)) == want
+    assert lib.fa_kv4_cache_bytes(1, 1, 64, 128, None) == fa.FA_ERR_INVALID_ARG
+    with pytest.raises(fa.FaError):
+        fa.fa_kv4_cache_bytes(1, 1, 64, 80)
+
+
+SIZES = dict(B=2, Hkv=4, N=8, d=128, num_pages=100, page_size=64, max_pages=10)
+
+
+def _bad_sizes():
+    for name in ("B", "Hkv", "N", "num_pages", "max_pages"):
+        for x in (0, -1):
+            yield {name: x}, "FA_ERR_INVALID_ARG"
+    for x in (0, 8, 17, 96, 2048, -64):
+        yield {"page_size": x}, "FA_ERR_INVALID_ARG"
+    for x in (0, 32, 80, 512, -128):
+        yield {"d": x}, "FA_ERR_UNSUPPORTED"
+    yield {"max_pages": 1 << 26, "page_size": 32}, "FA_ERR_INVALID_ARG"   # 2^31 positions
+    yield {"B": 1 << 16, "Hkv": 1 << 10, "N": 1 << 10}, "FA_ERR_INVALID_ARG"  # 2^36 rows
+
+
+@pytest.mark.parametrize("change,want", list(_bad_sizes()))
+def test_write_and_read_refuse_sizes(lib, change, want):
+    s = list({**SIZES, **change}.values())
+    ptrs = [P(0x1000 * (i + 1)) for i in range(6)]
+    assert lib.fa_kv4_write(*ptrs, *s, None) == getattr(fa, want)
+    assert lib.fa_kv4_read(*ptrs, *s, None) == getattr(fa, want)
+
+
+def test_write_and_read_refuse_pointers(lib):
+    s = list(SIZES.values())
+    good = [P(0x1000 * (i + 1)) for i in range(6)]
+    # Order: k, v, cache, table, start, count / cache, table, start, count, k, v.
+    for call, wide, optional in ((lib.fa_kv4_write, {0, 1, 2}, 5), (lib.fa_kv4_read, {0, 4, 5}, 3)):
+        for i in range(6):
+            bad = list(good)
+            bad[i] = P(0x1000 * (i + 1) + (8 if i in wide else 2))
+            assert call(*bad, *s, None) == fa.FA_ERR_INVALID_ARG, i
+            if i != optional:
+                bad[i] = P(0)
+                assert call(*bad, *s, None) == fa.FA_ERR_INVALID_ARG, i
+
+
+FWD = dict(B=2, H=32, Hkv=4, Nq=2, d=128, num_pages=100, page_size=64, max_pages=10, causal=2)
+
+
+def _fwd(lib, ptrs=None, scale=0.1, **change):
+    s = list({**FWD, **change}.values())
+    return lib.fa_kv4_fwd(*(ptrs or [P(0x1000 * (i + 1)) for i in range(6)]), *s, scale, None)
+
+
+def test_fwd_refusals(lib):
+    for name in ("B", "H", "Hkv", "Nq", "num_pages", "max_pages"):
+        assert _fwd(lib, **{name: 0}) == fa.FA_ERR_INVALID_ARG, name
+        assert _fwd(lib, **{name: -4}) == fa.FA_ERR_INVALID_ARG, name
+    assert _fwd(lib, Hkv=3) == fa.FA_ERR_INVALID_ARG
+    assert _fwd(lib, page_size=24) == fa.FA_ERR_INVALID_ARG
+    for causal in (-1, 3):
+        assert _fwd(lib, causal=causal) == fa.FA_ERR_INVALID_ARG
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert _fwd(lib, scale=scale) == fa.FA_ERR_INVALID_ARG
+    assert _fwd(lib, d=80) == fa.FA_ERR_UNSUPPORTED
+    assert _fwd(lib, Nq=17) == fa.FA_ERR_UNSUPPORTED       # 8 * 17 rows > 128
+    assert _fwd(lib, B=1 << 20, H=1 << 10, Hkv=1 << 10, Nq=4) == fa.FA_ERR_INVALID_ARG  # 2^32 rows
+    for i in range(6):
+        ptrs = [P(0x1000 * (j + 1)) for j in range(6)]
+        ptrs[i] = P(0)
+        assert _fwd(lib, ptrs) == fa.FA_ERR_INVALID_ARG
+        ptrs[i] = P(0x1000 * (i + 1) + (2 if i in (2, 3) else 8))
+        assert _fwd(lib, ptrs) == fa.FA_ERR_INVALID_ARG
+
+
+def test_launch_count_and_status_name(lib):
+    assert fa.fa_strerror(fa.FA_ERR_BAD_INDEX).startswith("FA_ERR_BAD_INDEX")
+    n = ctypes.c_uint64(7)
+    for kid in (fa.FA_KERNEL_KV4_WRITE, fa.FA_KERNEL_KV4_READ, fa.FA_KERNEL_KV4_FWD, fa.FA_KERNEL_KV4_MERGE):
+        assert lib.fa_launch_count(kid, ctypes.byref(n)) == fa.FA_OK
+    for kid in (5, 6, 7, 12):
+        assert lib.fa_launch_count(kid, ctypes.byref(n)) == fa.FA_ERR_INVALID_ARG
+
+
+def test_binding_refuses_host_tensors(lib):
+    torch = pytest.importorskip("torch")
+    k = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    cache = torch.zeros(3, 2, 16 * 72, dtype=torch.uint8)
+    table = torch.zeros(1, 1, dtype=torch.int32)
+    lens = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        fa.fa_kv4_write(k, k, cache, table, lens)
+    with pytest.raises(ValueError):
+        fa.fa_kv4_read(cache, table, lens, k, k)
+    with pytest.raises(ValueError):
+        fa.kv4_forward(k, cache, table, lens)
+    assert fa.kv4_cache(3, 2, 16, 64, device="cpu").shape == cache.shape
+    with pytest.raises(fa.FaError):
+        fa.kv4_cache(3, 2, 24, 64, device="cpu")
