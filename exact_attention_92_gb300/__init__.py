@@ -36,6 +36,7 @@ from ._binding import (  # noqa: F401
     fa_fwd_plan,
     fa_kv4_cache_bytes,
     fa_kv4_fwd,
+    fa_kv4_fwd_plan,
     fa_kv4_read,
     fa_kv4_write,
     fa_poll_status,

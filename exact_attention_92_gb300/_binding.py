@@ -88,6 +88,13 @@ class BwdPlan(ctypes.Structure):
         (n, _u64) for n in ("zeroed_dq_bytes", "zeroed_dkdv_bytes", "workspace_bytes")]
 
 
+class Kv4Plan(ctypes.Structure):
+    """fa_kv4_plan_t (include/fa.h)."""
+    _fields_ = [(n, _i) for n in ("rows", "unit_rows", "row_blocks", "units", "step_keys", "max_steps", "whole", "grid",
+                                  "launches")] + [("workspace_bytes", _u64)]
+
+
+_SIGNATURES["fa_kv4_fwd_plan"] = ([_i] * 8 + [ctypes.POINTER(Kv4Plan)], _i)
 _SIGNATURES["fa_fwd_plan"] = ([_i] * 9 + [_u64, ctypes.POINTER(FwdPlan)], _i)
 _SIGNATURES["fa_bwd_plan"] = ([_i] * 8 + [ctypes.POINTER(BwdPlan)], _i)
 
@@ -461,6 +468,15 @@ def fa_bwd_plan(B, H, Hkv, Nq, Nk, d, causal, sm_count):
     plan = BwdPlan()
     _check(load().fa_bwd_plan(int(B), int(H), int(Hkv), int(Nq), int(Nk), int(d), _causal_code(causal),
                               int(sm_count), ctypes.byref(plan)), "fa_bwd_plan")
+    return _plan_dict(plan)
+
+
+def fa_kv4_fwd_plan(B, H, Hkv, Nq, d, page_size, max_pages, sm_count):
+    """C fa_kv4_fwd_plan: the launch plan of fa_kv4_fwd, as a dict of the
+    fa_kv4_plan_t fields.  Host only; raises FaError on a refused size."""
+    plan = Kv4Plan()
+    _check(load().fa_kv4_fwd_plan(int(B), int(H), int(Hkv), int(Nq), int(d), int(page_size), int(max_pages),
+                                  int(sm_count), ctypes.byref(plan)), "fa_kv4_fwd_plan")
     return _plan_dict(plan)
 
 

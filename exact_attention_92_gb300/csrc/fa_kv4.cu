@@ -3,8 +3,10 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "fa_common.h"
 #include "kv4_fwd.h"
@@ -14,12 +16,18 @@ int internal_device_setup(unsigned int** status, int* sm_count);
 cudaError_t internal_timed_launch(int kernel, cudaStream_t stream, cudaError_t (*launch)(void*), void* ctx);
 cudaError_t launch_kv4_move(int d, bool write, const Kv4Cache& c, const int* start, const int* count, const void* k_in,
                             const void* v_in, void* k_out, void* v_out, int N, cudaStream_t stream);
-cudaError_t launch_kv4_fwd(int d, const Kv4FwdParams& p, cudaStream_t stream);
+void kv4_fwd_shape(int d, int rows, int* unit_rows, int* ctas_per_sm, int* step_keys);
+cudaError_t launch_kv4_fwd(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_kv4_merge(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
+cudaError_t internal_workspace(void** ptr, size_t bytes, cudaStream_t st);
+unsigned long long internal_wait_timeout_ns();
 }  // namespace fa
 
 namespace {
 
 constexpr int kMinPage = 16, kMaxPage = 1024;
+// Units of at most this many steps are not cut: a step for each warp of a CTA.
+constexpr int kWholeSteps = 8;
 constexpr int kMaxRows = 128;  // query rows of a key/value head's group (fa_kv4_fwd)
 
 bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -91,13 +99,20 @@ int move(bool write, const void* k_in, const void* v_in, void* k_out, void* v_ou
 
 struct Fwd {
   int d;
+  int unit_rows;
   fa::Kv4FwdParams p;
+  int grid;
   cudaStream_t st;
 };
 
 cudaError_t run_fwd(void* ctx) {
   const Fwd& f = *static_cast<const Fwd*>(ctx);
-  return fa::launch_kv4_fwd(f.d, f.p, f.st);
+  return fa::launch_kv4_fwd(f.d, f.unit_rows, f.p, f.grid, f.st);
+}
+
+cudaError_t run_merge(void* ctx) {
+  const Fwd& f = *static_cast<const Fwd*>(ctx);
+  return fa::launch_kv4_merge(f.d, f.unit_rows, f.p, f.grid, f.st);
 }
 
 int check_fwd_sizes(int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size, int max_pages, int causal) {
@@ -106,6 +121,27 @@ int check_fwd_sizes(int B, int H, int Hkv, int Nq, int d, int num_pages, int pag
   if (H % Hkv != 0 || causal < FA_CAUSAL_NONE || causal > FA_CAUSAL_BOTTOM_RIGHT) return FA_ERR_INVALID_ARG;
   if ((long long)(H / Hkv) * Nq > kMaxRows) return FA_ERR_UNSUPPORTED;
   return FA_OK;
+}
+
+// How a call is carried out (fa_kv4_plan_t), for sizes that passed
+// check_fwd_sizes.  The lengths are known on the device only, so this goes by
+// what the table can hold.
+void plan_fwd(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages, int sm_count, fa_kv4_plan_t* pl) {
+  std::memset(pl, 0, sizeof(*pl));
+  int ctas = 0;
+  pl->rows = (H / Hkv) * Nq;
+  fa::kv4_fwd_shape(d, pl->rows, &pl->unit_rows, &ctas, &pl->step_keys);
+  pl->row_blocks = (pl->rows + pl->unit_rows - 1) / pl->unit_rows;
+  pl->units = B * Hkv * pl->row_blocks;
+  const long long held = (long long)max_pages * page_size;
+  pl->max_steps = (int)((held + pl->step_keys - 1) / pl->step_keys);
+  pl->whole = pl->max_steps <= kWholeSteps ? 1 : 0;
+  const long long most = (long long)pl->units * (pl->whole ? 1 : pl->max_steps);
+  pl->grid = (int)std::min<long long>(most, (long long)ctas * sm_count);
+  pl->launches = pl->whole ? 1 : 2;
+  if (!pl->whole)
+    pl->workspace_bytes = (uint64_t)pl->grid * (2ull * pl->unit_rows * (d * sizeof(float) + sizeof(float2)) +
+                                                sizeof(fa::Kv4Cut));
 }
 
 }  // namespace
@@ -146,8 +182,12 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
   int sm_count = 0;
   e = fa::internal_device_setup(&status, &sm_count);
   if (e) return e;
+  fa_kv4_plan_t pl;
+  plan_fwd(B, H, Hkv, Nq, d, page_size, max_pages, sm_count, &pl);
   Fwd f;
   f.d = d;
+  f.unit_rows = pl.unit_rows;
+  f.grid = pl.grid;
   f.p.c = view(cache, block_table, B, Hkv, num_pages, page_size, max_pages, status);
   f.p.q = static_cast<const __nv_bfloat16*>(q);
   f.p.lens = lens;
@@ -155,10 +195,40 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
   f.p.lse = lse;
   f.p.H = H;
   f.p.Nq = Nq;
+  f.p.rows = pl.rows;
+  f.p.row_blocks = pl.row_blocks;
   f.p.causal = causal;
   f.p.scale_log2 = scale * 1.4426950408889634f;
+  f.p.whole = pl.whole;
+  f.p.part_o = nullptr;
+  f.p.part_ml = nullptr;
+  f.p.cuts = nullptr;
+  f.p.timeout_ns = fa::internal_wait_timeout_ns();
   f.st = static_cast<cudaStream_t>(stream);
-  return fa::internal_timed_launch(FA_KERNEL_KV4_FWD, f.st, run_fwd, &f) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  void* ws = nullptr;
+  if (pl.workspace_bytes > 0) {
+    if (fa::internal_workspace(&ws, pl.workspace_bytes, f.st) != cudaSuccess) {
+      cudaGetLastError();
+      return FA_ERR_NO_MEMORY;
+    }
+    const size_t parts = (size_t)2 * pl.grid * pl.unit_rows;
+    f.p.part_o = static_cast<float*>(ws);
+    f.p.part_ml = reinterpret_cast<float2*>(f.p.part_o + parts * d);
+    f.p.cuts = reinterpret_cast<fa::Kv4Cut*>(f.p.part_ml + parts);
+  }
+  cudaError_t ce = fa::internal_timed_launch(FA_KERNEL_KV4_FWD, f.st, run_fwd, &f);
+  if (ce == cudaSuccess && ws != nullptr) ce = fa::internal_timed_launch(FA_KERNEL_KV4_MERGE, f.st, run_merge, &f);
+  if (ws != nullptr) cudaFreeAsync(ws, f.st);
+  return ce == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_kv4_fwd_plan(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages, int sm_count,
+                    fa_kv4_plan_t* plan) {
+  if (plan == nullptr || sm_count < 1) return FA_ERR_INVALID_ARG;
+  const int e = check_fwd_sizes(B, H, Hkv, Nq, d, 1, page_size, max_pages, FA_CAUSAL_NONE);
+  if (e) return e;
+  plan_fwd(B, H, Hkv, Nq, d, page_size, max_pages, sm_count, plan);
+  return FA_OK;
 }
 
 }  // extern "C"

@@ -1,5 +1,35 @@
-// Attention over the 4-bit key/value cache (fa_kv4_fwd): one query row a CTA,
-// tiles of 128 keys, fp32 throughout.
+// Attention over the 4-bit key/value cache (fa_kv4_fwd).
+//
+// A unit is a (sequence, key/value head, block of 8 or 16 of the group's query
+// rows); its keys are walked in steps of 32.  The steps of all units form one
+// list, in the order of the units, of which every CTA takes an equal stretch
+// whatever the sequences' lengths; the warps of a CTA take its steps in turn.
+// A unit that a border between two CTAs cuts leaves fp32 partial results, which
+// a second kernel merges in a fixed order.
+//
+// Each warp fetches its own steps: bulk copies of whole 16-token blocks into a
+// ring in shared memory, ahead of use, so no warp waits for another within a
+// unit.  A step computes S^T = K Q^T and O^T += V^T P^T with m16n8k16
+// instructions on fp16 (16 keys, or 16 channels, by 8 query rows): the keys and
+// values are the row operand, so the decoding of 8 query rows wastes nothing,
+// and their codes go from shared memory through one conversion instruction per
+// two values into the operand's registers.  (A tcgen05 product would want the
+// 128-row operand in shared memory, decoded: 512 bytes written and read back a
+// token for 144 bytes of cache.)
+//
+// Numbers.  Codes are exact in fp16.  A query row is scaled by a power of two
+// to lie just below 2^16, where fp16 holds its bf16 values exactly down to
+// 2^-29 of the row's largest; the products of one group of 32 channels are
+// summed by the matrix instruction in fp32, multiplied by the group's scale in
+// fp32 and added, so scores are those of the exact held values.  The weights
+// p = 2^(s - ref) are multiplied by the values' scale in fp32 and rounded once
+// to fp16 (11 bits) for the P V product.  To keep p * scale within fp16 the
+// running reference is that of s + log2(the largest scale of the token's
+// value), not of s: p * scale starts at 2^4 for the largest key seen and may
+// grow to 2^14 before the reference is moved (and the sums rescaled); what
+// falls below 2^-14 of that loses relative, not absolute, precision.  The sum
+// of p is fp32.  log2(scale) is taken at 2^-80 at least, which keeps the sum
+// of p below 2^121.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -13,85 +43,733 @@ namespace fa {
 
 using namespace dev;
 
-template <int D>
-__global__ void __launch_bounds__(128) kv4_fwd_kernel(const Kv4FwdParams p) {
-  using F = Kv4<D>;
-  constexpr int kT = 128;
-  __shared__ float qs[D], sc[kT], red[4];
-  const int tid = threadIdx.x, row = blockIdx.x;  // row of [B, H, Nq]
-  const int qi = row % p.Nq, h = (row / p.Nq) % p.H, b = row / p.Nq / p.H;
-  const int head = h / (p.H / p.c.Hkv);
-  for (int c = tid; c < D; c += kT) qs[c] = __bfloat162float(p.q[(size_t)row * D + c]);
-  __syncthreads();
-  const int len = kv4_length(p.c, p.lens, b);
-  const int seen = kv4_seen(p, len, qi);  // keys this row sees
-  float m = -INFINITY, l = 0.f, acc[(D + kT - 1) / kT] = {};
-  for (int j0 = 0; j0 < seen; j0 += kT) {
-    const int j = j0 + tid;
-    float s = -INFINITY;
-    if (j < seen) {
-      const int page = kv4_page(p.c, b, j);
-      if (page >= 0) {
-        const uint8_t* blk = kv4_block<D>(p.c, page, head, j);
-        s = 0.f;
-        for (int g = 0; g < F::kGroups; ++g) {
-          float part = 0.f;
-          for (int t = 0; t < 4; ++t) {
-            uint32_t x[4];
-            kv4_decode8(*reinterpret_cast<const uint32_t*>(blk + F::key_word(j & 15, g, t)), x);
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
-              part = fmaf(qs[32 * g + 8 * t + 2 * i], f.x, fmaf(qs[32 * g + 8 * t + 2 * i + 1], f.y, part));
-            }
-          }
-          s = fmaf(part, bf16_lo(*reinterpret_cast<const uint16_t*>(blk + F::scale(j & 15, 0, g))), s);
-        }
-        s *= p.scale_log2;
-      }
-    }
-    float mx = s;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (tid % 32 == 0) red[tid / 32] = mx;
-    __syncthreads();
-    const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float pr = s == -INFINITY ? 0.f : exp2f(s - mn);
-    sc[tid] = pr;
-    __syncthreads();
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
-    l *= f;
-    for (int k = 0; k < kT; ++k) l += sc[k];
-    for (int c = tid, a = 0; c < D; c += kT, ++a) {
-      acc[a] *= f;
-      for (int k = 0; k < kT; ++k) {
-        if (sc[k] == 0.f) continue;  // keys not seen, pages out of range
-        const int jj = j0 + k;
-        const uint8_t* blk = kv4_block<D>(p.c, kv4_page(p.c, b, jj), head, jj);
-        const int g = c / 32, u = c % 32 / 4;
-        uint32_t x[4];
-        kv4_decode8(*reinterpret_cast<const uint16_t*>(blk + F::value_unit(jj & 15, g, u)), x);
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x[c % 4 / 2]));
-        acc[a] = fmaf(sc[k] * bf16_lo(*reinterpret_cast<const uint16_t*>(blk + F::scale(jj & 15, 1, g))),
-                      c % 2 ? v.y : v.x, acc[a]);
-      }
-    }
-    m = mn;
-    __syncthreads();
-  }
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
-  for (int c = tid, a = 0; c < D; c += kT, ++a) p.o[(size_t)row * D + c] = __float2bfloat16_rn(acc[a] * inv);
-  if (tid == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+namespace {
+
+template <int D, int NR>
+struct Cfg {
+  static constexpr int kWarps = 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kCtas = D <= 128 && NR == 1 ? 2 : 1;     // per SM
+  static constexpr int kBlocks = 2;                             // 16-token blocks a step
+  static constexpr int kKeys = kBlocks * kKv4Block;
+  static constexpr int kStages = D == 256 ? 2 : (NR == 1 ? 2 : 3);
+  static constexpr int kStageBytes = kBlocks * Kv4<D>::kBlockBytes;
+  static constexpr int kRows = NR * kKv4Rows;
+  static constexpr int kLens = 512;                             // sequence lengths kept in shared memory
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kSums = (kWarps / 2) * kRows * D * 4;    // O of half the warps, for the merge
+  static constexpr int kStats = kWarps * kRows * 8;
+  static constexpr int kBars = kWarps * kStages * 8;
+  static constexpr int kFlags = kWarps * kStages * 4;
+  static constexpr int kSmem = kRing + kSums + kStats + kBars + kFlags + kLens * 4 + 64;
+  static_assert(kSmem * kCtas <= 227 * 1024, "shared memory of an SM");
+};
+
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-cudaError_t launch_kv4_fwd(int d, const Kv4FwdParams& p, cudaStream_t stream) {
-  const int grid = p.c.B * p.H * p.Nq;
+// Transpose of an 8 x 8 matrix of 16-bit values held by a warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// N consecutive words of shared memory (N words are N * 4 bytes aligned for
+// N = 1, 2, 4, else 4).
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(w + i) = *reinterpret_cast<const uint4*>(p + 4 * i);
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
+  }
+}
+
+// Words g = 0..NG-1 of lane t of the key in row `slot` of a block.
+template <int D>
+__device__ __forceinline__ void load_key(const uint8_t* block, int slot, int t, uint32_t* w) {
+  using F = Kv4<D>;
+  if constexpr (D == 256) {
+    load_words<4>(block + F::key_word(slot, 0, t), w);
+    load_words<4>(block + F::key_word(slot, 4, t), w + 4);
+  } else {
+    load_words<F::kQuad>(block + F::key_word(slot, 0, t), w);
+  }
+}
+
+// Channels 4 u .. 4 u + 3 of every group of row `row` of the values: group g in
+// half g % 2 of word g / 2.
+template <int D>
+__device__ __forceinline__ void load_value(const uint8_t* block, int row, int u, uint32_t* w) {
+  using F = Kv4<D>;
+  const uint8_t* p = block + F::kValues + row * F::kRowBytes + ((u * F::kGroups * 2) ^ F::value_xor(row));
+  if constexpr (D == 96) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    w[0] = h[0] | ((uint32_t)h[1] << 16);
+    w[1] = h[2];
+  } else {
+    load_words<F::kGroups / 2>(p, w);
+  }
+}
+
+// Scales of a token: NG of the key, NG of the value, as bf16 pairs.
+template <int D>
+__device__ __forceinline__ void load_scales(const uint8_t* block, int token, uint32_t* w) {
+  load_words<Kv4<D>::kGroups>(block + Kv4<D>::kScales + token * Kv4<D>::kScaleBytes, w);
+}
+__device__ __forceinline__ float scale_of(const uint32_t* w, int i) { return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]); }
+
+// The list of steps, as far as a walk along it has come.
+struct Place {
+  int b;        // sequence
+  int u;        // unit within it: head * row_blocks + row block
+  int step;     // step within the unit
+};
+
+}  // namespace
+
+template <int D, int NR>
+__global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_fwd_kernel(const Kv4FwdParams p) {
+  using F = Kv4<D>;
+  using C = Cfg<D, NR>;
+  constexpr int NG = F::kGroups, W = C::kWarps;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* const ring = smem;
+  float* const sums = reinterpret_cast<float*>(smem + C::kRing);
+  float2* const stats = reinterpret_cast<float2*>(smem + C::kRing + C::kSums);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + C::kRing + C::kSums + C::kStats);
+  uint32_t* const flags = reinterpret_cast<uint32_t*>(bars + W * C::kStages);
+  int* const lens = reinterpret_cast<int*>(flags + W * C::kStages);
+  int* const misc = lens + C::kLens;
+
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const int units = p.c.Hkv * p.row_blocks;  // of a sequence
+  const WaitCtl ctl{p.c.status, p.timeout_ns};
+
+  if (tid < W * C::kStages) {
+    mbar_init(&bars[tid], 1);
+    fence_barrier_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // Steps of a unit of a sequence of n tokens; one at least, so that its rows
+  // are written.
+  auto steps_of = [&](int n) {
+    if (p.causal == FA_CAUSAL_TOP_LEFT && n > p.Nq) n = p.Nq;
+    return n == 0 ? 1 : (n + C::kKeys - 1) / C::kKeys;
+  };
+
+  // This CTA's stretch of the list: [first, end) in steps, or in units where
+  // they are not cut.
+  long long total, first, end;
+  int active = gridDim.x;
+  Place at;
+  if (p.whole) {
+    total = (long long)p.c.B * units;
+    first = total * blockIdx.x / active;
+    end = total * (blockIdx.x + 1) / active;
+    at.b = (int)(first / units);
+    at.u = (int)(first - (long long)at.b * units);
+    at.step = 0;
+  } else {
+    // Sum of the sequences' steps, each thread a run of sequences.
+    const int run = (p.c.B + C::kThreads - 1) / C::kThreads;
+    const int b0 = min(p.c.B, tid * run), b1 = min(p.c.B, b0 + run);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += steps_of(kv4_length(p.c, p.lens, b));
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    long long* const warp_sum = reinterpret_cast<long long*>(sums);
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+    upto += before;  // steps of one unit each, of the sequences up to b1
+    // CTAs that take part: a step for every warp, or a unit each.
+    const long long want = max(total * units / W, (long long)p.c.B * units);
+    active = (int)min((long long)gridDim.x, max(1ll, want));
+    total *= units;
+    const long long c = min((int)blockIdx.x, active);
+    first = total * c / active;
+    end = total * min(c + 1, (long long)active) / active;
+    if (mine > 0 && first < end && (upto - mine) * units <= first && first < upto * units) {
+      long long rest = first - (upto - mine) * units;
+      int b = b0, n = steps_of(kv4_length(p.c, p.lens, b));
+      while (rest >= (long long)n * units && b + 1 < b1) {
+        rest -= (long long)n * units;
+        n = steps_of(kv4_length(p.c, p.lens, ++b));
+      }
+      misc[0] = b;
+      misc[1] = (int)(rest / n);
+      misc[2] = (int)(rest % n);
+    }
+    __syncthreads();
+    at = Place{misc[0], misc[1], misc[2]};
+    if (tid == 0) p.cuts[blockIdx.x].row = -1;
+  }
+  if (first >= end) return;
+
+  const int base_b = at.b;
+  for (int i = tid; i < C::kLens && base_b + i < p.c.B; i += C::kThreads) lens[i] = kv4_length(p.c, p.lens, base_b + i);
+  __syncthreads();
+  auto length = [&](int b) { return b - base_b < C::kLens ? lens[b - base_b] : kv4_length(p.c, p.lens, b); };
+
+  // Walks `n` steps along the list; `left` counts the steps (or units, where
+  // they are whole) that remain to the stretch's end, at the walk's place.
+  struct Walk {
+    Place at;
+    long long left;
+    int steps;  // of the unit
+    int len;
+  };
+  auto advance = [&](Walk& w, int n) {
+    while (n > 0 && w.left > 0) {
+      const int rest = w.steps - w.at.step;
+      if (!p.whole && n >= w.left) {
+        w.left = 0;
+        return;
+      }
+      if (n < rest) {
+        w.at.step += n;
+        if (!p.whole) w.left -= n;
+        return;
+      }
+      n -= rest;
+      w.left -= p.whole ? 1 : rest;
+      if (w.left <= 0) return;
+      w.at.step = 0;
+      if (++w.at.u == units) {
+        w.at.u = 0;
+        if (++w.at.b == p.c.B) {
+          w.left = 0;
+          return;
+        }
+        w.len = length(w.at.b);
+        w.steps = steps_of(w.len);
+      }
+    }
+  };
+  Walk now{at, end - first, 0, length(at.b)};
+  now.steps = steps_of(now.len);
+
+  // ---- this warp's copies
+  Walk ahead = now;
+  advance(ahead, warp);
+  uint8_t* const my_ring = ring + warp * C::kStages * C::kStageBytes;
+  uint64_t* const my_bars = bars + warp * C::kStages;
+  uint32_t* const my_flags = flags + warp * C::kStages;
+  // Lane i < kBlocks fetches block i of the next step; its page is looked up a
+  // step ahead of the copy.
+  int page = -1;
+  auto look_up = [&] {
+    page = -1;
+    if (lane < C::kBlocks && ahead.left > 0) {
+      const int pos = ahead.at.step * C::kKeys + lane * kKv4Block;
+      if (pos < ahead.len) page = p.c.table[(size_t)ahead.at.b * p.c.max_pages + (pos >> p.c.page_shift)];
+    }
+  };
+  auto issue = [&](int stage) {
+    if (ahead.left <= 0) return;
+    const int pos = ahead.at.step * C::kKeys + lane * kKv4Block;
+    const bool want = lane < C::kBlocks && pos < ahead.len;
+    const bool good = want && (unsigned)page < (unsigned)p.c.num_pages;
+    if (want && !good) kv4_bad_index(p.c);
+    const uint32_t have = __ballot_sync(0xffffffffu, good);
+    if (lane == 0) {
+      my_flags[stage] = have;
+      mbar_arrive_expect_tx(&my_bars[stage], __popc(have) * F::kBlockBytes);
+    }
+    __syncwarp();
+    if (good)
+      bulk_load(my_ring + stage * C::kStageBytes + lane * F::kBlockBytes,
+                kv4_block<D>(p.c, page, ahead.at.u / p.row_blocks, pos), F::kBlockBytes, &my_bars[stage]);
+    advance(ahead, W);
+    look_up();
+  };
+  look_up();
+#pragma unroll 1
+  for (int s = 0; s < C::kStages; ++s) issue(s);
+
+  bool ok = true;
+  int stage = 0;
+  uint32_t phase = 0;
+  int turn = 0;  // steps of the CTA so far: warp turn % W has the next one
+
+  // ---- units
+  while (now.left > 0) {
+    const int len = now.len;
+    const int head = now.at.u / p.row_blocks, row0 = (now.at.u % p.row_blocks) * C::kRows;
+    const int s0 = now.at.step;
+    const int s1 = p.whole ? now.steps : (int)min((long long)now.steps, s0 + now.left);
+    const int n_rows = min(C::kRows, p.rows - row0);
+    const size_t row_at = ((size_t)now.at.b * p.c.Hkv + head) * p.rows + row0;  // in [B, H, Nq]
+
+    // Query rows g (and g + 8) as the column operand: channels 32 gr + 8 t .. + 7.
+    uint32_t q[NR][NG][4];
+    float cc[NR][2];   // what turns a column's sums into base-2 scores
+    int lim[NR][2];    // keys that the columns 2 t, 2 t + 1 see
+    int low = len;     // keys that all rows see
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int row = r * 8 + g;
+      uint4 raw[NG];
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (row < n_rows) raw[i] = *reinterpret_cast<const uint4*>(p.q + (row_at + row) * D + 32 * i + 8 * t);
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^15 over the power of two of the row's largest value (at most 2^126).
+      const int e = (int)(__float_as_uint(top) >> 23);
+      const int f = min(127 + 126, 127 + 15 + 127 - e);
+      const float up = top > 0.f ? __uint_as_float((uint32_t)f << 23) : 1.f;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[r][i][k] = pack_f16(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
+      }
+      const float back = p.scale_log2 / up;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        cc[r][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c));
+        const int col = r * 8 + 2 * t + c;
+        lim[r][c] = col < n_rows ? kv4_seen(p, len, (row0 + col) % p.Nq) : len;
+        low = min(low, lim[r][c]);
+      }
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+
+    float o[NR][NG][2][4];
+    float ref[NR][2], l[NR][2];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[r][i][h][k] = 0.f;
+      ref[r][0] = ref[r][1] = -3.402823466e38f;
+      l[r][0] = l[r][1] = 0.f;
+    }
+
+    const int rank = (warp - turn % W + W) % W;  // 0: has the unit's first step here
+#pragma unroll 1
+    for (int s = s0 + rank; s < s1; s += W) {
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(&my_bars[stage], phase, ctl, kWaitKvFull));
+      if (!ok) break;
+      const uint8_t* const st = my_ring + stage * C::kStageBytes;
+      const uint32_t have = my_flags[stage];
+      const int key0 = s * C::kKeys;
+      const bool full = key0 + C::kKeys <= low && have == (1u << C::kBlocks) - 1;
+
+      // S^T, in base 2, of keys g and g + 8 of each block and columns 2 t, 2 t + 1.
+      float sc[C::kBlocks][NR][4];
+      float top[NR][2];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) top[r][0] = top[r][1] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < C::kBlocks; ++k) {
+        const uint8_t* const blk = st + k * F::kBlockBytes;
+        uint32_t ka[NG], kb[NG], wa[NG], wb[NG];
+        load_key<D>(blk, g, t, ka);
+        load_key<D>(blk, g + 8, t, kb);
+        load_scales<D>(blk, g, wa);
+        load_scales<D>(blk, g + 8, wb);
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[k][r][x] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          uint32_t ha[4], hb[4];
+          kv4_decode8(ka[i], ha);
+          kv4_decode8(kb[i], hb);
+          const float fa_ = scale_of(wa, i), fb_ = scale_of(wb, i);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(c, ha[0], hb[0], ha[1], hb[1], q[r][i][0], q[r][i][1]);
+            mma16816(c, ha[2], hb[2], ha[3], hb[3], q[r][i][2], q[r][i][3]);
+            sc[k][r][0] = fmaf(fa_, c[0], sc[k][r][0]);
+            sc[k][r][1] = fmaf(fa_, c[1], sc[k][r][1]);
+            sc[k][r][2] = fmaf(fb_, c[2], sc[k][r][2]);
+            sc[k][r][3] = fmaf(fb_, c[3], sc[k][r][3]);
+          }
+        }
+        float va = 8.271806125530277e-25f, vb = va;  // 2^-80
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          va = fmaxf(va, scale_of(wa, NG + i));
+          vb = fmaxf(vb, scale_of(wb, NG + i));
+        }
+        va = lg2_approx(va);
+        vb = lg2_approx(vb);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            sc[k][r][x] *= cc[r][x & 1];
+            if (!full) {
+              const int key = key0 + k * kKv4Block + g + (x & 2) * 4;
+              if (key >= lim[r][x & 1] || !((have >> k) & 1)) sc[k][r][x] = -INFINITY;
+            }
+          }
+          top[r][0] = fmaxf(top[r][0], fmaxf(sc[k][r][0] + va, sc[k][r][2] + vb));
+          top[r][1] = fmaxf(top[r][1], fmaxf(sc[k][r][1] + va, sc[k][r][3] + vb));
+        }
+      }
+
+      // Move the references of columns that have outgrown them.
+      bool grow = false;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) grow |= top[r][0] > ref[r][0] + 14.f || top[r][1] > ref[r][1] + 14.f;
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = top[r][c];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float next = x > ref[r][c] + 14.f ? x - 4.f : ref[r][c];
+            const float f = ex2_approx(ref[r][c] - next);
+            ref[r][c] = next;
+            l[r][c] *= f;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+              o[r][i][0][c] *= f;
+              o[r][i][0][c + 2] *= f;
+              o[r][i][1][c] *= f;
+              o[r][i][1][c + 2] *= f;
+            }
+          }
+        }
+      }
+
+      // Weights, and O^T += V^T P^T.
+#pragma unroll
+      for (int k = 0; k < C::kBlocks; ++k) {
+        const uint8_t* const blk = st + k * F::kBlockBytes;
+        uint32_t wa[NG], wb[NG];
+        load_scales<D>(blk, g, wa);
+        load_scales<D>(blk, g + 8, wb);
+        constexpr int NW = (NG + 1) / 2;
+        uint32_t v0[NW], v1[NW], v2[NW], v3[NW];  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+        load_value<D>(blk, t, g, v0);
+        load_value<D>(blk, 4 + t, g, v1);
+        load_value<D>(blk, 8 + t, g, v2);
+        load_value<D>(blk, 12 + t, g, v3);
+        bool dark[NR][4];  // not seen: whatever the scale is
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            dark[r][x] = !full && sc[k][r][x] == -INFINITY;
+            sc[k][r][x] = ex2_approx(sc[k][r][x] - ref[r][x & 1]);
+            l[r][x & 1] += sc[k][r][x];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+          // Bytes of two tokens' codes for one channel: even channels, odd channels.
+          const uint32_t lo01 = (v0[j] & 0x0f0f0f0fu) | ((v1[j] << 4) & 0xf0f0f0f0u);
+          const uint32_t hi01 = ((v0[j] >> 4) & 0x0f0f0f0fu) | (v1[j] & 0xf0f0f0f0u);
+          const uint32_t lo23 = (v2[j] & 0x0f0f0f0fu) | ((v3[j] << 4) & 0xf0f0f0f0u);
+          const uint32_t hi23 = ((v2[j] >> 4) & 0x0f0f0f0fu) | (v3[j] & 0xf0f0f0f0u);
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          kv4_decode8(lo01, a0);
+          kv4_decode8(hi01, a1);
+          kv4_decode8(lo23, a2);
+          kv4_decode8(hi23, a3);
+#pragma unroll
+          for (int i = 2 * j; i < 2 * j + 2 && i < NG; ++i) {
+            const float fa_ = scale_of(wa, NG + i), fb_ = scale_of(wb, NG + i);
+            const int y = 2 * (i & 1);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              float x0 = sc[k][r][0] * fa_, x1 = sc[k][r][1] * fa_, x2 = sc[k][r][2] * fb_, x3 = sc[k][r][3] * fb_;
+              if (!full) {
+                x0 = dark[r][0] ? 0.f : x0;
+                x1 = dark[r][1] ? 0.f : x1;
+                x2 = dark[r][2] ? 0.f : x2;
+                x3 = dark[r][3] ? 0.f : x3;
+              }
+              const uint32_t b0 = transpose8(pack_f16(x0, x1)), b1 = transpose8(pack_f16(x2, x3));
+              mma16816(o[r][i][0], a0[y], a1[y], a2[y], a3[y], b0, b1);
+              mma16816(o[r][i][1], a0[y + 1], a1[y + 1], a2[y + 1], a3[y + 1], b0, b1);
+            }
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      issue(stage);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+
+    // ---- join the warps' results: rank r + half adds to rank r
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], 4);
+        l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], 8);
+        l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], 16);
+      }
+    const int n_steps = s1 - s0;
+    const int busy = min(W, n_steps);  // ranks that had a step
+    if (busy > 1) {
+      if (g == 0) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) stats[rank * C::kRows + r * 8 + 2 * t + c] = make_float2(ref[r][c], l[r][c]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float m = ref[r][c];
+          for (int w = 0; w < busy; ++w) m = fmaxf(m, stats[w * C::kRows + r * 8 + 2 * t + c].x);
+          float all = 0.f;
+          for (int w = 0; w < busy; ++w) {
+            const float2 x = stats[w * C::kRows + r * 8 + 2 * t + c];
+            all = fmaf(x.y, ex2_approx(x.x - m), all);
+          }
+          const float f = ex2_approx(ref[r][c] - m);
+          ref[r][c] = m;
+          l[r][c] = all;
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            o[r][i][0][c] *= f;
+            o[r][i][0][c + 2] *= f;
+            o[r][i][1][c] *= f;
+            o[r][i][1][c + 2] *= f;
+          }
+        }
+#pragma unroll 1
+      for (int half = W / 2; half >= 1; half >>= 1) {
+        if (busy <= half) continue;
+        // Slots are those of the reading ranks of the first round, which a
+        // rank has read before it writes to one of them.
+        constexpr int kVec = NR * NG * 2;  // float4 of a lane
+        float4* const buf = reinterpret_cast<float4*>(sums);
+        if (rank >= half && rank < 2 * half && rank < busy) {
+          const int slot = half == W / 2 ? rank - half : rank;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            const float* x = &o[0][0][0][0] + 4 * i;
+            buf[(slot * kVec + i) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
+          }
+        }
+        __syncthreads();
+        if (rank < half && rank + half < busy) {
+          const int slot = half == W / 2 ? rank : rank + half;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            float* x = &o[0][0][0][0] + 4 * i;
+            const float4 y = buf[(slot * kVec + i) * 32 + lane];
+            x[0] += y.x;
+            x[1] += y.y;
+            x[2] += y.z;
+            x[3] += y.w;
+          }
+        }
+      }
+    }
+
+    // ---- results of the unit, or of this CTA's part of it
+    if (rank == 0) {
+      const bool starts = s0 == 0, ends = s1 == now.steps;
+      if (starts && ends) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = r * 8 + 2 * t + c;
+            if (col >= n_rows) continue;
+            const float inv = l[r][c] == 0.f ? 0.f : 1.0f / l[r][c];
+            __nv_bfloat16* dst = p.o + (row_at + col) * D + 4 * g;
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+              *reinterpret_cast<uint2*>(dst + 32 * i) =
+                  make_uint2(pack_bf16(o[r][i][0][c] * inv, o[r][i][0][c + 2] * inv),
+                             pack_bf16(o[r][i][1][c] * inv, o[r][i][1][c + 2] * inv));
+            if (g == 0)
+              p.lse[row_at + col] = l[r][c] == 0.f ? -INFINITY : (ref[r][c] + lg2_approx(l[r][c])) * 0.69314718055994530942f;
+          }
+      } else {
+        const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = r * 8 + 2 * t + c;
+            float* dst = p.part_o + ((size_t)slot * C::kRows + col) * D + 4 * g;
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+              *reinterpret_cast<float4*>(dst + 32 * i) =
+                  make_float4(o[r][i][0][c], o[r][i][0][c + 2], o[r][i][1][c], o[r][i][1][c + 2]);
+            if (g == 0) p.part_ml[(size_t)slot * C::kRows + col] = make_float2(ref[r][c], l[r][c]);
+          }
+        if (starts && lane == 0) {
+          // The unit's last step is `rest` steps behind this CTA's end.
+          const long long x = end + (now.steps - s1);  // one past it, in the list
+          Kv4Cut cut;
+          cut.row = (int)row_at;
+          cut.rows = n_rows;
+          cut.last = (int)((x * active + total - 1) / total) - 1;
+          cut.pad = 0;
+          p.cuts[blockIdx.x] = cut;
+        }
+      }
+    }
+    turn += n_steps;
+    advance(now, n_steps);
+  }
+
+  // After a wait that gave up, copies may still be in flight into this CTA's
+  // shared memory: wait for them (bounded) before it is given back.
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    for (int s = 0; s < C::kStages; ++s)
+      while (!mbar_try_wait(smem_u32(&my_bars[s]), s < stage ? phase ^ 1 : phase) &&
+             globaltimer_ns() - t0 < p.timeout_ns) {
+      }
+  }
+}
+
+// Merge of the parts of the units that CTA borders cut: a CTA per main CTA, a
+// warp per row.  O = sum_k 2^(ref_k - m) O_k / sum_k 2^(ref_k - m) l_k, the
+// parts in the order of the CTAs.
+template <int D, int NR>
+__global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4FwdParams p) {
+  constexpr int kRows = NR * kKv4Rows, kPer = D / 32;
+  pdl_wait();
+  const Kv4Cut cut = p.cuts[blockIdx.x];
+  if (cut.row < 0) return;
+  const int lane = threadIdx.x % 32;
+  const int parts = cut.last - (int)blockIdx.x + 1;
+  for (int row = threadIdx.x / 32; row < cut.rows; row += 8) {
+    // Part k: the tail of this CTA, then the heads of those behind it.
+    auto at = [&](int k) { return (size_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * kRows + row; };
+    float m = -3.402823466e38f;
+    for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.part_ml[at(k)].x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    float acc[kPer] = {}, l = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float2 ml = p.part_ml[at(k)];
+      const float f = ex2_approx(ml.x - m);
+      l = fmaf(ml.y, f, l);
+      const float* src = p.part_o + at(k) * D + lane;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(src[32 * i], f, acc[i]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      p.o[((size_t)cut.row + row) * D + lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv);
+    if (lane == 0) p.lse[cut.row + row] = l == 0.f ? -INFINITY : (m + lg2_approx(l)) * 0.69314718055994530942f;
+  }
+}
+
+namespace {
+
+template <int D, int NR>
+cudaError_t launch_fwd_t(const Kv4FwdParams& p, int grid, cudaStream_t stream) {
+  using C = Cfg<D, NR>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv4_fwd_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv4_fwd_kernel<D, NR>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, p);
+}
+
+}  // namespace
+
+// Rows of a unit, CTAs an SM and keys a step for head dim d and `rows` query
+// rows a key/value head.  Two row tiles a unit only where one does not hold
+// the rows, and not at d = 256, whose sums take 64 registers a tile.
+void kv4_fwd_shape(int d, int rows, int* unit_rows, int* ctas_per_sm, int* step_keys) {
+  const bool two = rows > kKv4Rows && d != 256;
+  *unit_rows = two ? 2 * kKv4Rows : kKv4Rows;
   switch (d) {
-    case 64: kv4_fwd_kernel<64><<<grid, 128, 0, stream>>>(p); break;
-    case 96: kv4_fwd_kernel<96><<<grid, 128, 0, stream>>>(p); break;
-    case 128: kv4_fwd_kernel<128><<<grid, 128, 0, stream>>>(p); break;
-    case 256: kv4_fwd_kernel<256><<<grid, 128, 0, stream>>>(p); break;
+    case 64: *ctas_per_sm = two ? Cfg<64, 2>::kCtas : Cfg<64, 1>::kCtas; break;
+    case 96: *ctas_per_sm = two ? Cfg<96, 2>::kCtas : Cfg<96, 1>::kCtas; break;
+    case 128: *ctas_per_sm = two ? Cfg<128, 2>::kCtas : Cfg<128, 1>::kCtas; break;
+    default: *ctas_per_sm = Cfg<256, 1>::kCtas; break;
+  }
+  *step_keys = Cfg<64, 1>::kKeys;
+}
+
+cudaError_t launch_kv4_fwd(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream) {
+  const bool two = unit_rows == 2 * kKv4Rows;
+  switch (d) {
+    case 64: return two ? launch_fwd_t<64, 2>(p, grid, stream) : launch_fwd_t<64, 1>(p, grid, stream);
+    case 96: return two ? launch_fwd_t<96, 2>(p, grid, stream) : launch_fwd_t<96, 1>(p, grid, stream);
+    case 128: return two ? launch_fwd_t<128, 2>(p, grid, stream) : launch_fwd_t<128, 1>(p, grid, stream);
+    case 256: return two ? cudaErrorInvalidValue : launch_fwd_t<256, 1>(p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_merge(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream) {
+  const bool two = unit_rows == 2 * kKv4Rows;
+  const dim3 g(grid), b(256);
+  switch (d) {
+    case 64: return launch_pdl(two ? kv4_merge_kernel<64, 2> : kv4_merge_kernel<64, 1>, g, b, 0, stream, p);
+    case 96: return launch_pdl(two ? kv4_merge_kernel<96, 2> : kv4_merge_kernel<96, 1>, g, b, 0, stream, p);
+    case 128: return launch_pdl(two ? kv4_merge_kernel<128, 2> : kv4_merge_kernel<128, 1>, g, b, 0, stream, p);
+    case 256: return launch_pdl(kv4_merge_kernel<256, 1>, g, b, 0, stream, p);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace fa

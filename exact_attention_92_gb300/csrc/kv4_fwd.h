@@ -8,6 +8,18 @@
 
 namespace fa {
 
+// Query rows of a tile: the N of the m16n8k16 matrix instructions.
+constexpr int kKv4Rows = 8;
+
+// A unit that more than one CTA works on: written by the CTA that holds its
+// first step, for the merge.
+struct Kv4Cut {
+  int row;    // first of its rows in [B, H, Nq]; -1: none starts here
+  int rows;
+  int last;   // the last CTA that holds a part of it
+  int pad;
+};
+
 struct Kv4FwdParams {
   Kv4Cache c;
   const __nv_bfloat16* q;  // [B, H, Nq, d]
@@ -16,8 +28,15 @@ struct Kv4FwdParams {
   float* lse;              // [B, H, Nq]
   int H;
   int Nq;
+  int rows;                // (H / Hkv) * Nq: query rows that share a key/value head
+  int row_blocks;          // ceil(rows / rows of a unit)
   int causal;              // FA_CAUSAL_*
   float scale_log2;        // scale * log2(e)
+  int whole;               // 1: units are not cut
+  float* part_o;           // [2 * grid][rows of a unit][d]: partial sums (not whole)
+  float2* part_ml;         // [2 * grid][rows of a unit]: reference and sum
+  Kv4Cut* cuts;            // [grid]
+  unsigned long long timeout_ns;
 };
 
 namespace dev {

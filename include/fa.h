@@ -394,6 +394,29 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
                float scale, void* stream);
 
 /*
+ * How fa_kv4_fwd carries out a call of these sizes, worked out on the host
+ * alone (as fa_fwd_plan; the call follows it with the current device's
+ * sm_count).  The lengths are on the device, so the plan goes by what the
+ * block table can hold: every CTA takes an equal stretch of the list of all
+ * units' steps, which the device works out from lens.
+ */
+typedef struct {
+  int rows;        /* query rows that share a key/value head: (H / Hkv) * Nq */
+  int unit_rows;   /* query rows of a unit: 8, or 16 when rows > 8 and d < 256 */
+  int row_blocks;  /* units per (sequence, key/value head): ceil(rows / unit_rows) */
+  int units;       /* B * Hkv * row_blocks */
+  int step_keys;   /* keys that a warp takes at a time */
+  int max_steps;   /* ceil(max_pages * page_size / step_keys) */
+  int whole;       /* 1: units are not cut between CTAs (few steps each) */
+  int grid;        /* CTAs of the main kernel at most */
+  int launches;    /* 1, or 2 with the merge of cut units */
+  uint64_t workspace_bytes; /* partial results of two units a CTA (0 when whole) */
+} fa_kv4_plan_t;
+
+int fa_kv4_fwd_plan(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages, int sm_count,
+                    fa_kv4_plan_t* plan);
+
+/*
  * Synchronise `stream`, then return and clear the device status word of the
  * current device: FA_OK, FA_ERR_TIMEOUT if a kernel's bounded wait gave up
  * since the last poll, FA_ERR_BAD_INDEX if a fa_kv4_* kernel skipped an index

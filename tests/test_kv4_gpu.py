@@ -14,7 +14,14 @@ Tolerances, derived from the arithmetic:
             significant ones (2^-11), its sums are fp32 (2^-13 covers 2^10
             steps), O is rounded once to bf16 (2^-8):
               |dO| <= 2^-8 |O| + (2^-11 + 2^-13 + 2^-20 + 2 e) sum_j P_j |v_j|
+                      + n 2^-29 max_j P_j max_c |v_jc|
               |dL| <= e + 2^-20 max(1, |L|).
+            The last term of |dO|: the 16 bits are fp16's, whose step is
+            2^-24 below 2^-14, so a weight times its value's scale s is off by
+            at most 2^-25 there, times a code of at most 6.  The reference is
+            such that the largest P s of the row stands at 2^4 at least, and
+            6 s_j is the largest |v_jc| of the group: n keys give at most
+            n 6 2^-25 / 2^4 max_j P_j s_j = n 2^-29 max_j P_j max_c |v_jc|.
 """
 
 import numpy as np
@@ -205,6 +212,7 @@ def check_attend(o, lse, q, k, v, lens, scale, causal, what=""):
             A = scale * np.abs(q[b, h]) @ np.abs(kk).T
             e = 2.0 ** -19 * A.max(1)
             bound = 2.0 ** -8 * np.abs(O[h]) + (2.0 ** -11 + 2.0 ** -13 + 2.0 ** -20 + 2 * e)[:, None] * (P @ np.abs(vv))
+            bound += n * 2.0 ** -29 * (P * np.abs(vv).max(1)).max(1)[:, None]
             err = np.abs(o[b, h] - O[h])
             assert (err <= bound + 1e-38).all(), (
                 f"{what} b={b} h={h}: O off by {np.nanmax(err / (bound + 1e-38)):.3g} of the bound, {err.max():.3g}")
