@@ -31,6 +31,8 @@
 // of p is fp32.  log2(scale) is taken at 2^-80 at least, which keeps the sum
 // of p below 2^121.
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -141,14 +143,23 @@ template <int D>
 __device__ __forceinline__ void load_scales(const uint8_t* block, int token, uint32_t* w) {
   load_words<Kv4<D>::kGroups>(block + Kv4<D>::kScales + token * Kv4<D>::kScaleBytes, w);
 }
+// The largest scale of a token's value, 2^-80 at least; NaN does not count.
+template <int NG>
+__device__ __forceinline__ float largest_scale(const uint32_t* w) {
+  constexpr float kLeast = 8.271806125530277e-25f;
+  if constexpr (NG % 2 == 0) {
+    uint32_t m = w[NG / 2];
+#pragma unroll
+    for (int i = NG / 2 + 1; i < NG; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+    return fmax3(bf16_lo(m), bf16_hi(m), kLeast);
+  } else {
+    float m = kLeast;
+#pragma unroll
+    for (int i = NG; i < 2 * NG; ++i) m = fmaxf(m, i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]));
+    return m;
+  }
+}
 __device__ __forceinline__ float scale_of(const uint32_t* w, int i) { return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]); }
-
-// The list of steps, as far as a walk along it has come.
-struct Place {
-  int b;        // sequence
-  int u;        // unit within it: head * row_blocks + row block
-  int step;     // step within the unit
-};
 
 }  // namespace
 
@@ -188,7 +199,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
   // they are not cut.
   long long total, first, end;
   int active = gridDim.x;
-  Place at;
+  struct {
+    int b, u, step;  // sequence, unit within it, step within that
+  } at;
   if (p.whole) {
     total = (long long)p.c.B * units;
     first = total * blockIdx.x / active;
@@ -238,7 +251,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
       misc[2] = (int)(rest % n);
     }
     __syncthreads();
-    at = Place{misc[0], misc[1], misc[2]};
+    at.b = misc[0];
+    at.u = misc[1];
+    at.step = misc[2];
     if (tid == 0) p.cuts[blockIdx.x].row = -1;
   }
   if (first >= end) return;
@@ -248,43 +263,50 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
   __syncthreads();
   auto length = [&](int b) { return b - base_b < C::kLens ? lens[b - base_b] : kv4_length(p.c, p.lens, b); };
 
-  // Walks `n` steps along the list; `left` counts the steps (or units, where
-  // they are whole) that remain to the stretch's end, at the walk's place.
+  // A place in this CTA's stretch of the list: steps [lo, hi) of a unit are
+  // still ahead, and `rest` steps (units, where they are whole) behind it.
   struct Walk {
-    Place at;
-    long long left;
-    int steps;  // of the unit
-    int len;
+    int b, u, head;  // sequence; unit within it; key/value head
+    int len, steps;  // of the sequence, of each of its units
+    int lo, hi;
+    long long rest;
+    const int* row;  // of the block table
   };
+  auto enter = [&](Walk& w, int step) {
+    w.head = p.row_blocks == 1 ? w.u : w.u / p.row_blocks;
+    w.lo = step;
+    w.hi = p.whole ? w.steps : (int)min((long long)w.steps, step + w.rest);
+    w.rest -= p.whole ? 1 : w.hi - step;
+  };
+  auto sequence = [&](Walk& w) {
+    w.len = length(w.b);
+    w.steps = steps_of(w.len);
+    w.row = p.c.table + (size_t)w.b * p.c.max_pages;
+  };
+  // n steps on; at the stretch's end lo = hi.
   auto advance = [&](Walk& w, int n) {
-    while (n > 0 && w.left > 0) {
-      const int rest = w.steps - w.at.step;
-      if (!p.whole && n >= w.left) {
-        w.left = 0;
-        return;
-      }
-      if (n < rest) {
-        w.at.step += n;
-        if (!p.whole) w.left -= n;
-        return;
-      }
-      n -= rest;
-      w.left -= p.whole ? 1 : rest;
-      if (w.left <= 0) return;
-      w.at.step = 0;
-      if (++w.at.u == units) {
-        w.at.u = 0;
-        if (++w.at.b == p.c.B) {
-          w.left = 0;
+    while (n >= w.hi - w.lo) {
+      n -= w.hi - w.lo;
+      w.lo = w.hi;
+      if (w.rest <= 0) return;
+      if (++w.u == units) {
+        w.u = 0;
+        if (++w.b == p.c.B) {
+          w.rest = 0;
           return;
         }
-        w.len = length(w.at.b);
-        w.steps = steps_of(w.len);
+        sequence(w);
       }
+      enter(w, 0);
     }
+    w.lo += n;
   };
-  Walk now{at, end - first, 0, length(at.b)};
-  now.steps = steps_of(now.len);
+  Walk now;
+  now.b = at.b;
+  now.u = at.u;
+  now.rest = end - first;
+  sequence(now);
+  enter(now, at.step);
 
   // ---- this warp's copies
   Walk ahead = now;
@@ -292,34 +314,36 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
   uint8_t* const my_ring = ring + warp * C::kStages * C::kStageBytes;
   uint64_t* const my_bars = bars + warp * C::kStages;
   uint32_t* const my_flags = flags + warp * C::kStages;
-  // Lane i < kBlocks fetches block i of the next step; its page is looked up a
-  // step ahead of the copy.
+  // A copy takes the blocks of a step that lie in one page, all of them where
+  // pages are long enough; lane i issues the step's copy i, whose page it has
+  // looked up a step before.
+  const int copy_blocks = min(C::kBlocks, 1 << (p.c.page_shift - 4));
+  const bool copies = lane * copy_blocks < C::kBlocks;
   int page = -1;
   auto look_up = [&] {
     page = -1;
-    if (lane < C::kBlocks && ahead.left > 0) {
-      const int pos = ahead.at.step * C::kKeys + lane * kKv4Block;
-      if (pos < ahead.len) page = p.c.table[(size_t)ahead.at.b * p.c.max_pages + (pos >> p.c.page_shift)];
-    }
+    const int pos = ahead.lo * C::kKeys + lane * copy_blocks * kKv4Block;
+    if (copies && ahead.lo < ahead.hi && pos < ahead.len) page = ahead.row[pos >> p.c.page_shift];
   };
   auto issue = [&](int stage) {
-    if (ahead.left <= 0) return;
-    const int pos = ahead.at.step * C::kKeys + lane * kKv4Block;
-    const bool want = lane < C::kBlocks && pos < ahead.len;
+    if (ahead.lo == ahead.hi) return;
+    const int pos = ahead.lo * C::kKeys + lane * copy_blocks * kKv4Block;
+    const bool want = copies && pos < ahead.len;
     const bool good = want && (unsigned)page < (unsigned)p.c.num_pages;
     if (want && !good) kv4_bad_index(p.c);
     const uint32_t have = __ballot_sync(0xffffffffu, good);
     if (lane == 0) {
       my_flags[stage] = have;
-      mbar_arrive_expect_tx(&my_bars[stage], __popc(have) * F::kBlockBytes);
+      mbar_arrive_expect_tx(&my_bars[stage], __popc(have) * copy_blocks * F::kBlockBytes);
     }
     __syncwarp();
     if (good)
-      bulk_load(my_ring + stage * C::kStageBytes + lane * F::kBlockBytes,
-                kv4_block<D>(p.c, page, ahead.at.u / p.row_blocks, pos), F::kBlockBytes, &my_bars[stage]);
+      bulk_load(my_ring + stage * C::kStageBytes + lane * copy_blocks * F::kBlockBytes,
+                kv4_block<D>(p.c, page, ahead.head, pos), copy_blocks * F::kBlockBytes, &my_bars[stage]);
     advance(ahead, W);
     look_up();
   };
+  const uint32_t have_all = (1u << (C::kBlocks / copy_blocks)) - 1;
   look_up();
 #pragma unroll 1
   for (int s = 0; s < C::kStages; ++s) issue(s);
@@ -330,13 +354,12 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
   int turn = 0;  // steps of the CTA so far: warp turn % W has the next one
 
   // ---- units
-  while (now.left > 0) {
+  while (now.lo < now.hi) {
     const int len = now.len;
-    const int head = now.at.u / p.row_blocks, row0 = (now.at.u % p.row_blocks) * C::kRows;
-    const int s0 = now.at.step;
-    const int s1 = p.whole ? now.steps : (int)min((long long)now.steps, s0 + now.left);
+    const int head = now.head, row0 = (now.u - head * p.row_blocks) * C::kRows;
+    const int s0 = now.lo, s1 = now.hi;
     const int n_rows = min(C::kRows, p.rows - row0);
-    const size_t row_at = ((size_t)now.at.b * p.c.Hkv + head) * p.rows + row0;  // in [B, H, Nq]
+    const size_t row_at = ((size_t)now.b * p.c.Hkv + head) * p.rows + row0;  // in [B, H, Nq]
 
     // Query rows g (and g + 8) as the column operand: channels 32 gr + 8 t .. + 7.
     uint32_t q[NR][NG][4];
@@ -393,22 +416,19 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
       l[r][0] = l[r][1] = 0.f;
     }
 
-    const int rank = (warp - turn % W + W) % W;  // 0: has the unit's first step here
-#pragma unroll 1
-    for (int s = s0 + rank; s < s1; s += W) {
-      if (!ok) break;
-      ok = __all_sync(0xffffffffu, mbar_wait(&my_bars[stage], phase, ctl, kWaitKvFull));
-      if (!ok) break;
-      const uint8_t* const st = my_ring + stage * C::kStageBytes;
-      const uint32_t have = my_flags[stage];
-      const int key0 = s * C::kKeys;
-      const bool full = key0 + C::kKeys <= low && have == (1u << C::kBlocks) - 1;
-
-      // S^T, in base 2, of keys g and g + 8 of each block and columns 2 t, 2 t + 1.
+    const int rank = (warp - turn) & (W - 1);  // 0: has the unit's first step here
+    // One step: MASK where some row does not see some of the keys.
+    auto step = [&](auto mask, const uint8_t* const st, int key0, uint32_t have) {
+      constexpr bool MASK = decltype(mask)::value;
+      // Keys g and g + 8 of each block, columns 2 t and 2 t + 1: scores as the
+      // matrix products have them (to be multiplied by cc).
       float sc[C::kBlocks][NR][4];
-      float top[NR][2];
+      float top[NR][2];  // largest score + log2(largest scale of the value)
 #pragma unroll
       for (int r = 0; r < NR; ++r) top[r][0] = top[r][1] = -INFINITY;
+      auto seen = [&](int k, int r, int x) {
+        return key0 + k * kKv4Block + g + (x & 2) * 4 < lim[r][x & 1] && ((have >> (k / copy_blocks)) & 1) != 0;
+      };
 #pragma unroll
       for (int k = 0; k < C::kBlocks; ++k) {
         const uint8_t* const blk = st + k * F::kBlockBytes;
@@ -438,27 +458,18 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
             sc[k][r][3] = fmaf(fb_, c[3], sc[k][r][3]);
           }
         }
-        float va = 8.271806125530277e-25f, vb = va;  // 2^-80
+        const float va = lg2_approx(largest_scale<NG>(wa)), vb = lg2_approx(largest_scale<NG>(wb));
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          va = fmaxf(va, scale_of(wa, NG + i));
-          vb = fmaxf(vb, scale_of(wb, NG + i));
-        }
-        va = lg2_approx(va);
-        vb = lg2_approx(vb);
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            sc[k][r][x] *= cc[r][x & 1];
-            if (!full) {
-              const int key = key0 + k * kKv4Block + g + (x & 2) * 4;
-              if (key >= lim[r][x & 1] || !((have >> k) & 1)) sc[k][r][x] = -INFINITY;
+          for (int c = 0; c < 2; ++c) {
+            float x = fmaf(sc[k][r][c], cc[r][c], va), y = fmaf(sc[k][r][c + 2], cc[r][c], vb);
+            if constexpr (MASK) {
+              x = seen(k, r, c) ? x : -INFINITY;
+              y = seen(k, r, c + 2) ? y : -INFINITY;
             }
+            top[r][c] = fmax3(top[r][c], x, y);
           }
-          top[r][0] = fmaxf(top[r][0], fmaxf(sc[k][r][0] + va, sc[k][r][2] + vb));
-          top[r][1] = fmaxf(top[r][1], fmaxf(sc[k][r][1] + va, sc[k][r][3] + vb));
-        }
       }
 
       // Move the references of columns that have outgrown them.
@@ -502,16 +513,15 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
         load_value<D>(blk, 4 + t, g, v1);
         load_value<D>(blk, 8 + t, g, v2);
         load_value<D>(blk, 12 + t, g, v3);
-        bool dark[NR][4];  // not seen: whatever the scale is
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            dark[r][x] = !full && sc[k][r][x] == -INFINITY;
-            sc[k][r][x] = ex2_approx(sc[k][r][x] - ref[r][x & 1]);
-            l[r][x & 1] += sc[k][r][x];
+            float y = ex2_approx(fmaf(sc[k][r][x], cc[r][x & 1], -ref[r][x & 1]));
+            if constexpr (MASK) y = seen(k, r, x) ? y : 0.f;
+            sc[k][r][x] = y;
+            l[r][x & 1] += y;
           }
-        }
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
           // Bytes of two tokens' codes for one channel: even channels, odd channels.
@@ -530,20 +540,31 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
             const int y = 2 * (i & 1);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-              float x0 = sc[k][r][0] * fa_, x1 = sc[k][r][1] * fa_, x2 = sc[k][r][2] * fb_, x3 = sc[k][r][3] * fb_;
-              if (!full) {
-                x0 = dark[r][0] ? 0.f : x0;
-                x1 = dark[r][1] ? 0.f : x1;
-                x2 = dark[r][2] ? 0.f : x2;
-                x3 = dark[r][3] ? 0.f : x3;
+              float x[4] = {sc[k][r][0] * fa_, sc[k][r][1] * fa_, sc[k][r][2] * fb_, sc[k][r][3] * fb_};
+              if constexpr (MASK) {  // whatever the scale is
+#pragma unroll
+                for (int z = 0; z < 4; ++z) x[z] = seen(k, r, z) ? x[z] : 0.f;
               }
-              const uint32_t b0 = transpose8(pack_f16(x0, x1)), b1 = transpose8(pack_f16(x2, x3));
+              const uint32_t b0 = transpose8(pack_f16(x[0], x[1])), b1 = transpose8(pack_f16(x[2], x[3]));
               mma16816(o[r][i][0], a0[y], a1[y], a2[y], a3[y], b0, b1);
               mma16816(o[r][i][1], a0[y + 1], a1[y + 1], a2[y + 1], a3[y + 1], b0, b1);
             }
           }
         }
       }
+    };
+#pragma unroll 1
+    for (int s = s0 + rank; s < s1; s += W) {
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(&my_bars[stage], phase, ctl, kWaitKvFull));
+      if (!ok) break;
+      const uint8_t* const st = my_ring + stage * C::kStageBytes;
+      const uint32_t have = my_flags[stage];
+      const int key0 = s * C::kKeys;
+      if (key0 + C::kKeys <= low && have == have_all)
+        step(std::false_type{}, st, key0, have);
+      else
+        step(std::true_type{}, st, key0, have);
       __syncwarp();  // every lane has read the stage
       issue(stage);
       if (++stage == C::kStages) {
@@ -659,8 +680,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
             if (g == 0) p.part_ml[(size_t)slot * C::kRows + col] = make_float2(ref[r][c], l[r][c]);
           }
         if (starts && lane == 0) {
-          // The unit's last step is `rest` steps behind this CTA's end.
-          const long long x = end + (now.steps - s1);  // one past it, in the list
+          const long long x = end + (now.steps - s1);  // one past the unit's last step, in the list
           Kv4Cut cut;
           cut.row = (int)row_at;
           cut.rows = n_rows;
