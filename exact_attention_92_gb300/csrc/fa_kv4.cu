@@ -16,7 +16,7 @@ int internal_device_setup(unsigned int** status, int* sm_count);
 cudaError_t internal_timed_launch(int kernel, cudaStream_t stream, cudaError_t (*launch)(void*), void* ctx);
 cudaError_t launch_kv4_move(int d, bool write, const Kv4Cache& c, const int* start, const int* count, const void* k_in,
                             const void* v_in, void* k_out, void* v_out, int N, cudaStream_t stream);
-void kv4_fwd_shape(int d, int rows, int* unit_rows, int* ctas_per_sm, int* step_keys);
+void kv4_fwd_shape(int d, int rows, int* unit_rows, int* step_keys);
 cudaError_t launch_kv4_fwd(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_kv4_merge(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
 cudaError_t internal_workspace(void** ptr, size_t bytes, cudaStream_t st);
@@ -128,16 +128,15 @@ int check_fwd_sizes(int B, int H, int Hkv, int Nq, int d, int num_pages, int pag
 // what the table can hold.
 void plan_fwd(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages, int sm_count, fa_kv4_plan_t* pl) {
   std::memset(pl, 0, sizeof(*pl));
-  int ctas = 0;
   pl->rows = (H / Hkv) * Nq;
-  fa::kv4_fwd_shape(d, pl->rows, &pl->unit_rows, &ctas, &pl->step_keys);
+  fa::kv4_fwd_shape(d, pl->rows, &pl->unit_rows, &pl->step_keys);
   pl->row_blocks = (pl->rows + pl->unit_rows - 1) / pl->unit_rows;
   pl->units = B * Hkv * pl->row_blocks;
   const long long held = (long long)max_pages * page_size;
   pl->max_steps = (int)((held + pl->step_keys - 1) / pl->step_keys);
   pl->whole = pl->max_steps <= kWholeSteps ? 1 : 0;
   const long long most = (long long)pl->units * (pl->whole ? 1 : pl->max_steps);
-  pl->grid = (int)std::min<long long>(most, (long long)ctas * sm_count);
+  pl->grid = (int)std::min<long long>(most, sm_count);
   pl->launches = pl->whole ? 1 : 2;
   if (!pl->whole)
     pl->workspace_bytes = (uint64_t)pl->grid * (2ull * pl->unit_rows * (d * sizeof(float) + sizeof(float2)) +

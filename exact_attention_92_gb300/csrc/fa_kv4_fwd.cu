@@ -49,22 +49,39 @@ namespace {
 
 template <int D, int NR>
 struct Cfg {
-  static constexpr int kWarps = 8;
+  // One CTA an SM; its warps as many as their registers allow.
+  static constexpr int kWarps = NR == 1 && D < 256 ? (D == 64 ? 16 : 12) : 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kCtas = D <= 128 && NR == 1 ? 2 : 1;     // per SM
   static constexpr int kBlocks = 2;                             // 16-token blocks a step
   static constexpr int kKeys = kBlocks * kKv4Block;
-  static constexpr int kStages = D == 256 ? 2 : (NR == 1 ? 2 : 3);
+  static constexpr int kStages = D == 256 ? 2 : (D == 128 ? 3 : 4);
   static constexpr int kStageBytes = kBlocks * Kv4<D>::kBlockBytes;
   static constexpr int kRows = NR * kKv4Rows;
   static constexpr int kLens = 512;                             // sequence lengths kept in shared memory
-  static constexpr int kRing = kWarps * kStages * kStageBytes;
-  static constexpr int kSums = (kWarps / 2) * kRows * D * 4;    // O of half the warps, for the merge
-  static constexpr int kStats = kWarps * kRows * 8;
-  static constexpr int kBars = kWarps * kStages * 8;
-  static constexpr int kFlags = kWarps * kStages * 4;
-  static constexpr int kSmem = kRing + kSums + kStats + kBars + kFlags + kLens * 4 + 64;
-  static_assert(kSmem * kCtas <= 227 * 1024, "shared memory of an SM");
+  // What a unit costs a warp besides its steps, in steps.
+  static constexpr int kUnitCost = 1;
+  // Shared memory: a ring of steps and the sums of a unit's head for each
+  // warp (the sums of a tail go to the ring, which is empty by then).
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kSums = kRows * D * 4;
+  static constexpr int kSmem = kWarps * (kRing + kSums);
+  static_assert(kRing >= kSums, "a tail's sums go where the ring was");
+};
+
+// A unit, or a stretch of its steps, that a warp has to do.
+struct Piece {
+  int b, u, head;  // sequence; unit within it; key/value head
+  int len, steps;  // of the sequence, of each of its units
+  int lo, hi;      // steps to do
+};
+
+// What a warp leaves to be joined with its neighbours' results.
+struct Left {
+  int head;        // 1: the end or the middle of a unit that began before; 2: the end
+  int tail;        // 1: the beginning of a unit that goes on
+  int row, rows;   // rows of the tail's unit, or of the head's where there is no tail
+  int head_row, head_rows;
+  long long past;  // one past the last step of the tail's unit, in the list
 };
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -164,20 +181,25 @@ __device__ __forceinline__ float scale_of(const uint32_t* w, int i) { return i &
 }  // namespace
 
 template <int D, int NR>
-__global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_fwd_kernel(const Kv4FwdParams p) {
+__global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const Kv4FwdParams p) {
   using F = Kv4<D>;
   using C = Cfg<D, NR>;
   constexpr int NG = F::kGroups, W = C::kWarps;
+  constexpr int kQueue = 8;  // pieces between the copies and the products
+  static_assert(kQueue >= C::kStages + 2, "a piece has a step at least");
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* const ring = smem;
-  float* const sums = reinterpret_cast<float*>(smem + C::kRing);
-  float2* const stats = reinterpret_cast<float2*>(smem + C::kRing + C::kSums);
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + C::kRing + C::kSums + C::kStats);
-  uint32_t* const flags = reinterpret_cast<uint32_t*>(bars + W * C::kStages);
-  int* const lens = reinterpret_cast<int*>(flags + W * C::kStages);
-  int* const misc = lens + C::kLens;
+  __shared__ uint64_t bars[W * C::kStages];
+  __shared__ Piece queue[W * kQueue];
+  __shared__ Left left[W];
+  __shared__ float2 stats[2][W * C::kRows];  // reference and sum of heads, of tails
+  __shared__ int lims[W * C::kRows];
+  __shared__ int lens[C::kLens];
+  __shared__ long long warp_sum[W];
+  __shared__ int found[2][4];
 
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  // Through a shuffle, so that what follows from it stays in uniform registers.
+  auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+  const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32, g = lane / 4, t = lane % 4;
   const int units = p.c.Hkv * p.row_blocks;  // of a sequence
   const WaitCtl ctl{p.c.status, p.timeout_ns};
 
@@ -195,135 +217,134 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
     return n == 0 ? 1 : (n + C::kKeys - 1) / C::kKeys;
   };
 
-  // This CTA's stretch of the list: [first, end) in steps, or in units where
-  // they are not cut.
-  long long total, first, end;
-  int active = gridDim.x;
-  struct {
-    int b, u, step;  // sequence, unit within it, step within that
-  } at;
-  if (p.whole) {
-    total = (long long)p.c.B * units;
-    first = total * blockIdx.x / active;
-    end = total * (blockIdx.x + 1) / active;
-    at.b = (int)(first / units);
-    at.u = (int)(first - (long long)at.b * units);
-    at.step = 0;
-  } else {
-    // Sum of the sequences' steps, each thread a run of sequences.
-    const int run = (p.c.B + C::kThreads - 1) / C::kThreads;
-    const int b0 = min(p.c.B, tid * run), b1 = min(p.c.B, b0 + run);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += steps_of(kv4_length(p.c, p.lens, b));
-    long long upto = mine;
+  // ---- this CTA's stretch [first, end) of the list.  A unit takes kUnitCost
+  // places and then one for each step.  Each thread adds up a run of sequences.
+  const int run = (p.c.B + C::kThreads - 1) / C::kThreads;
+  const int b0 = min(p.c.B, tid * run), b1 = min(p.c.B, b0 + run);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += C::kUnitCost + steps_of(kv4_length(p.c, p.lens, b));
+  long long upto = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    long long* const warp_sum = reinterpret_cast<long long*>(sums);
-    if (lane == 31) warp_sum[warp] = upto;
-    __syncthreads();
-    long long before = 0;
-    total = 0;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  long long total = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) before += warp_sum[w];
-      total += warp_sum[w];
-    }
-    upto += before;  // steps of one unit each, of the sequences up to b1
-    // CTAs that take part: a step for every warp, or a unit each.
-    const long long want = max(total * units / W, (long long)p.c.B * units);
-    active = (int)min((long long)gridDim.x, max(1ll, want));
-    total *= units;
-    const long long c = min((int)blockIdx.x, active);
-    first = total * c / active;
-    end = total * min(c + 1, (long long)active) / active;
-    if (mine > 0 && first < end && (upto - mine) * units <= first && first < upto * units) {
-      long long rest = first - (upto - mine) * units;
-      int b = b0, n = steps_of(kv4_length(p.c, p.lens, b));
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) upto += warp_sum[w];
+    total += warp_sum[w];
+  }
+  // CTAs that take part: two places for every warp, or a unit each.
+  const long long want = max(total * units / (2 * W), (long long)p.c.B * units);
+  const int active = (int)min((long long)gridDim.x, want);
+  total *= units;
+  if (tid == 0 && !p.whole) p.cuts[blockIdx.x].row = -1;
+  if ((int)blockIdx.x >= active) return;
+  long long first = total * blockIdx.x / active, end = total * (blockIdx.x + 1) / active;
+  // Sequence, unit, place within it and places of the unit at list place x.
+  auto find = [&](long long x, int* f) {
+    if (mine > 0 && (upto - mine) * units <= x && x < upto * units) {
+      long long rest = x - (upto - mine) * units;
+      int b = b0, n = C::kUnitCost + steps_of(kv4_length(p.c, p.lens, b));
       while (rest >= (long long)n * units && b + 1 < b1) {
         rest -= (long long)n * units;
-        n = steps_of(kv4_length(p.c, p.lens, ++b));
+        n = C::kUnitCost + steps_of(kv4_length(p.c, p.lens, ++b));
       }
-      misc[0] = b;
-      misc[1] = (int)(rest / n);
-      misc[2] = (int)(rest % n);
+      f[0] = b;
+      f[1] = (int)(rest / n);
+      f[2] = (int)(rest % n);
+      f[3] = n;
     }
-    __syncthreads();
-    at.b = misc[0];
-    at.u = misc[1];
-    at.step = misc[2];
-    if (tid == 0) p.cuts[blockIdx.x].row = -1;
+  };
+  find(first, found[0]);
+  if (p.whole && end < total) find(end, found[1]);
+  __syncthreads();
+  int at_b = uniform(found[0][0]), at_u = uniform(found[0][1]), at_off = uniform(found[0][2]);
+  if (p.whole) {  // units that begin in the stretch
+    if (at_off > 0) {
+      first += uniform(found[0][3]) - at_off;
+      at_off = 0;
+      if (++at_u == units) {
+        at_u = 0;
+        ++at_b;
+      }
+    }
+    if (end < total && found[1][2] > 0) end += found[1][3] - found[1][2];
   }
   if (first >= end) return;
-
-  const int base_b = at.b;
+  const int base_b = at_b;
   for (int i = tid; i < C::kLens && base_b + i < p.c.B; i += C::kThreads) lens[i] = kv4_length(p.c, p.lens, base_b + i);
   __syncthreads();
-  auto length = [&](int b) { return b - base_b < C::kLens ? lens[b - base_b] : kv4_length(p.c, p.lens, b); };
+  auto length = [&](int b) { return uniform(b - base_b < C::kLens ? lens[b - base_b] : kv4_length(p.c, p.lens, b)); };
 
-  // A place in this CTA's stretch of the list: steps [lo, hi) of a unit are
-  // still ahead, and `rest` steps (units, where they are whole) behind it.
-  struct Walk {
-    int b, u, head;  // sequence; unit within it; key/value head
-    int len, steps;  // of the sequence, of each of its units
-    int lo, hi;
-    long long rest;
-    const int* row;  // of the block table
+  // ---- this warp's stretch of it, walked by the copies
+  const long long my_end = first + (end - first) * (warp + 1) / W;
+  long long at = first + (end - first) * warp / W;
+  long long skip = at - first + at_off;  // places from the beginning of unit at_u
+  Piece ahead;
+  ahead.b = at_b;
+  ahead.u = at_u;
+  const int* row = nullptr;  // of the block table
+  auto sequence = [&] {
+    ahead.len = length(ahead.b);
+    ahead.steps = steps_of(ahead.len);
+    row = p.c.table + (size_t)ahead.b * p.c.max_pages;
   };
-  auto enter = [&](Walk& w, int step) {
-    w.head = p.row_blocks == 1 ? w.u : w.u / p.row_blocks;
-    w.lo = step;
-    w.hi = p.whole ? w.steps : (int)min((long long)w.steps, step + w.rest);
-    w.rest -= p.whole ? 1 : w.hi - step;
-  };
-  auto sequence = [&](Walk& w) {
-    w.len = length(w.b);
-    w.steps = steps_of(w.len);
-    w.row = p.c.table + (size_t)w.b * p.c.max_pages;
-  };
-  // n steps on; at the stretch's end lo = hi.
-  auto advance = [&](Walk& w, int n) {
-    while (n >= w.hi - w.lo) {
-      n -= w.hi - w.lo;
-      w.lo = w.hi;
-      if (w.rest <= 0) return;
-      if (++w.u == units) {
-        w.u = 0;
-        if (++w.b == p.c.B) {
-          w.rest = 0;
-          return;
-        }
-        sequence(w);
-      }
-      enter(w, 0);
+  sequence();
+  while (skip >= (long long)(units - ahead.u) * (C::kUnitCost + ahead.steps) && ahead.b + 1 < p.c.B) {
+    skip -= (long long)(units - ahead.u) * (C::kUnitCost + ahead.steps);
+    ahead.u = 0;
+    ++ahead.b;
+    sequence();
+  }
+  const int jump = (int)(skip / (C::kUnitCost + ahead.steps));
+  ahead.u += jump;
+  int made = 0, taken = 0;  // pieces put into the queue, and taken out
+  auto enter = [&](int off) {
+    ahead.head = p.row_blocks == 1 ? ahead.u : ahead.u / p.row_blocks;
+    const int upto_off = (int)min((long long)ahead.steps + C::kUnitCost, off + my_end - at);
+    ahead.lo = max(0, off - C::kUnitCost);
+    ahead.hi = max(ahead.lo, upto_off - C::kUnitCost);
+    at += upto_off - off;
+    if (ahead.lo < ahead.hi) {
+      if (lane == 0) queue[warp * kQueue + made % kQueue] = ahead;
+      ++made;
     }
-    w.lo += n;
   };
-  Walk now;
-  now.b = at.b;
-  now.u = at.u;
-  now.rest = end - first;
-  sequence(now);
-  enter(now, at.step);
+  // To the next unit; where the stretch is at its end, lo = hi.
+  auto next_unit = [&] {
+    ahead.lo = ahead.hi;
+    if (at >= my_end) return;
+    if (++ahead.u == units) {
+      ahead.u = 0;
+      if (++ahead.b == p.c.B) {
+        at = my_end;
+        return;
+      }
+      sequence();
+    }
+    enter(0);
+  };
+  ahead.lo = ahead.hi = 0;
+  if (at < my_end) enter((int)(skip - (long long)jump * (C::kUnitCost + ahead.steps)));
 
-  // ---- this warp's copies
-  Walk ahead = now;
-  advance(ahead, warp);
-  uint8_t* const my_ring = ring + warp * C::kStages * C::kStageBytes;
-  uint64_t* const my_bars = bars + warp * C::kStages;
-  uint32_t* const my_flags = flags + warp * C::kStages;
   // A copy takes the blocks of a step that lie in one page, all of them where
   // pages are long enough; lane i issues the step's copy i, whose page it has
   // looked up a step before.
+  uint8_t* const ring = smem + warp * C::kRing;
+  uint64_t* const bar = bars + warp * C::kStages;
   const int copy_blocks = min(C::kBlocks, 1 << (p.c.page_shift - 4));
   const bool copies = lane * copy_blocks < C::kBlocks;
+  const uint32_t have_all = (1u << (C::kBlocks / copy_blocks)) - 1;
+  uint32_t have = 0;  // copies that were made, four bits a stage
   int page = -1;
   auto look_up = [&] {
-    page = -1;
     const int pos = ahead.lo * C::kKeys + lane * copy_blocks * kKv4Block;
-    if (copies && ahead.lo < ahead.hi && pos < ahead.len) page = ahead.row[pos >> p.c.page_shift];
+    page = -1;
+    if (copies && ahead.lo < ahead.hi && pos < ahead.len) page = row[pos >> p.c.page_shift];
   };
   auto issue = [&](int stage) {
     if (ahead.lo == ahead.hi) return;
@@ -331,19 +352,17 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
     const bool want = copies && pos < ahead.len;
     const bool good = want && (unsigned)page < (unsigned)p.c.num_pages;
     if (want && !good) kv4_bad_index(p.c);
-    const uint32_t have = __ballot_sync(0xffffffffu, good);
-    if (lane == 0) {
-      my_flags[stage] = have;
-      mbar_arrive_expect_tx(&my_bars[stage], __popc(have) * copy_blocks * F::kBlockBytes);
-    }
+    const uint32_t ones = __ballot_sync(0xffffffffu, good);
+    have = (have & ~(15u << (4 * stage))) | (ones << (4 * stage));
+    if (lane == 0) mbar_arrive_expect_tx(&bar[stage], __popc(ones) * copy_blocks * F::kBlockBytes);
     __syncwarp();
     if (good)
-      bulk_load(my_ring + stage * C::kStageBytes + lane * copy_blocks * F::kBlockBytes,
-                kv4_block<D>(p.c, page, ahead.head, pos), copy_blocks * F::kBlockBytes, &my_bars[stage]);
-    advance(ahead, W);
+      bulk_load(ring + stage * C::kStageBytes + lane * copy_blocks * F::kBlockBytes,
+                kv4_block<D>(p.c, page, ahead.head, pos), copy_blocks * F::kBlockBytes, &bar[stage]);
+    if (++ahead.lo == ahead.hi) next_unit();
     look_up();
   };
-  const uint32_t have_all = (1u << (C::kBlocks / copy_blocks)) - 1;
+  if (ahead.lo == ahead.hi) next_unit();  // only the cost of a unit's beginning was left of it
   look_up();
 #pragma unroll 1
   for (int s = 0; s < C::kStages; ++s) issue(s);
@@ -351,33 +370,38 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
   bool ok = true;
   int stage = 0;
   uint32_t phase = 0;
-  int turn = 0;  // steps of the CTA so far: warp turn % W has the next one
+  Left mine_left = {};
 
   // ---- units
-  while (now.lo < now.hi) {
-    const int len = now.len;
-    const int head = now.head, row0 = (now.u - head * p.row_blocks) * C::kRows;
-    const int s0 = now.lo, s1 = now.hi;
+  while (taken < made) {
+    __syncwarp();
+    const Piece& now = queue[warp * kQueue + taken % kQueue];
+    const int s0 = uniform(now.lo), s1 = uniform(now.hi), len = uniform(now.len);
+    const bool starts = s0 == 0, ends = s1 == uniform(now.steps);
+    const int row0 = uniform((now.u - now.head * p.row_blocks) * C::kRows);
     const int n_rows = min(C::kRows, p.rows - row0);
-    const size_t row_at = ((size_t)now.b * p.c.Hkv + head) * p.rows + row0;  // in [B, H, Nq]
+    const int row_at = uniform((now.b * p.c.Hkv + now.head) * p.rows + row0);  // in [B, H, Nq]
+    ++taken;
 
-    // Query rows g (and g + 8) as the column operand: channels 32 gr + 8 t .. + 7.
-    uint32_t q[NR][NG][4];
-    float cc[NR][2];   // what turns a column's sums into base-2 scores
-    int lim[NR][2];    // keys that the columns 2 t, 2 t + 1 see
-    int low = len;     // keys that all rows see
+    uint32_t q[NR][NG][4];  // as the column operand
+    float cc[NR][2];        // what turns the sums of columns 2 t, 2 t + 1 into base-2 scores
+    int low = len;          // keys that all rows see
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const int row = r * 8 + g;
+      // Query rows g (and g + 8), channels 32 i + 8 t .. + 7.
       uint4 raw[NG];
-      float top = 0.f;
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         raw[i] = make_uint4(0, 0, 0, 0);
-        if (row < n_rows) raw[i] = *reinterpret_cast<const uint4*>(p.q + (row_at + row) * D + 32 * i + 8 * t);
+        if (r * 8 + g < n_rows)
+          raw[i] = *reinterpret_cast<const uint4*>(p.q + (size_t)(row_at + r * 8 + g) * D + 32 * i + 8 * t);
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+        for (int k = 0; k < 4; ++k) top = fmax3(top, fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k])));
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -393,14 +417,20 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
       }
       const float back = p.scale_log2 / up;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        cc[r][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c));
-        const int col = r * 8 + 2 * t + c;
-        lim[r][c] = col < n_rows ? kv4_seen(p, len, (row0 + col) % p.Nq) : len;
-        low = min(low, lim[r][c]);
-      }
+      for (int c = 0; c < 2; ++c) cc[r][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c));
     }
-    low = __reduce_min_sync(0xffffffffu, low);
+    // Keys that each row sees; padding rows see all.
+    if (p.causal != FA_CAUSAL_NONE) {
+      if (lane < C::kRows) {
+        const int lim = lane < n_rows ? kv4_seen(p, len, (row0 + lane) % p.Nq) : len;
+        lims[warp * C::kRows + lane] = lim;
+        low = lim;
+      }
+      low = __reduce_min_sync(0xffffffffu, low);
+    } else if (lane < C::kRows) {
+      lims[warp * C::kRows + lane] = len;
+    }
+    __syncwarp();
 
     float o[NR][NG][2][4];
     float ref[NR][2], l[NR][2];
@@ -416,9 +446,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
       l[r][0] = l[r][1] = 0.f;
     }
 
-    const int rank = (warp - turn) & (W - 1);  // 0: has the unit's first step here
     // One step: MASK where some row does not see some of the keys.
-    auto step = [&](auto mask, const uint8_t* const st, int key0, uint32_t have) {
+    auto step = [&](auto mask, const uint8_t* const st, int key0, uint32_t there) {
       constexpr bool MASK = decltype(mask)::value;
       // Keys g and g + 8 of each block, columns 2 t and 2 t + 1: scores as the
       // matrix products have them (to be multiplied by cc).
@@ -427,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
 #pragma unroll
       for (int r = 0; r < NR; ++r) top[r][0] = top[r][1] = -INFINITY;
       auto seen = [&](int k, int r, int x) {
-        return key0 + k * kKv4Block + g + (x & 2) * 4 < lim[r][x & 1] && ((have >> (k / copy_blocks)) & 1) != 0;
+        return key0 + k * kKv4Block + g + (x & 2) * 4 < lims[warp * C::kRows + r * 8 + 2 * t + (x & 1)] && ((there >> (k / copy_blocks)) & 1) != 0;
       };
 #pragma unroll
       for (int k = 0; k < C::kBlocks; ++k) {
@@ -554,17 +583,17 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
       }
     };
 #pragma unroll 1
-    for (int s = s0 + rank; s < s1; s += W) {
+    for (int s = s0; s < s1; ++s) {
       if (!ok) break;
-      ok = __all_sync(0xffffffffu, mbar_wait(&my_bars[stage], phase, ctl, kWaitKvFull));
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar[stage], phase, ctl, kWaitKvFull));
       if (!ok) break;
-      const uint8_t* const st = my_ring + stage * C::kStageBytes;
-      const uint32_t have = my_flags[stage];
+      const uint8_t* const st = ring + stage * C::kStageBytes;
+      const uint32_t there = (have >> (4 * stage)) & 15u;
       const int key0 = s * C::kKeys;
-      if (key0 + C::kKeys <= low && have == have_all)
-        step(std::false_type{}, st, key0, have);
+      if (key0 + C::kKeys <= low && there == have_all)
+        step(std::false_type{}, st, key0, there);
       else
-        step(std::true_type{}, st, key0, have);
+        step(std::true_type{}, st, key0, there);
       __syncwarp();  // every lane has read the stage
       issue(stage);
       if (++stage == C::kStages) {
@@ -573,7 +602,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
       }
     }
 
-    // ---- join the warps' results: rank r + half adds to rank r
+    // ---- results
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -582,116 +611,126 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
         l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], 8);
         l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], 16);
       }
-    const int n_steps = s1 - s0;
-    const int busy = min(W, n_steps);  // ranks that had a step
-    if (busy > 1) {
-      if (g == 0) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) stats[rank * C::kRows + r * 8 + 2 * t + c] = make_float2(ref[r][c], l[r][c]);
-      }
-      __syncthreads();
+    if (starts && ends) {
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float m = ref[r][c];
-          for (int w = 0; w < busy; ++w) m = fmaxf(m, stats[w * C::kRows + r * 8 + 2 * t + c].x);
-          float all = 0.f;
-          for (int w = 0; w < busy; ++w) {
-            const float2 x = stats[w * C::kRows + r * 8 + 2 * t + c];
-            all = fmaf(x.y, ex2_approx(x.x - m), all);
-          }
-          const float f = ex2_approx(ref[r][c] - m);
-          ref[r][c] = m;
-          l[r][c] = all;
+          const int col = r * 8 + 2 * t + c;
+          if (col >= n_rows) continue;
+          const float inv = l[r][c] == 0.f ? 0.f : 1.0f / l[r][c];
+          __nv_bfloat16* dst = p.o + (size_t)(row_at + col) * D + 4 * g;
 #pragma unroll
-          for (int i = 0; i < NG; ++i) {
-            o[r][i][0][c] *= f;
-            o[r][i][0][c + 2] *= f;
-            o[r][i][1][c] *= f;
-            o[r][i][1][c + 2] *= f;
-          }
+          for (int i = 0; i < NG; ++i)
+            *reinterpret_cast<uint2*>(dst + 32 * i) =
+                make_uint2(pack_bf16(o[r][i][0][c] * inv, o[r][i][0][c + 2] * inv),
+                           pack_bf16(o[r][i][1][c] * inv, o[r][i][1][c + 2] * inv));
+          if (g == 0)
+            p.lse[row_at + col] = l[r][c] == 0.f ? -INFINITY : (ref[r][c] + lg2_approx(l[r][c])) * 0.69314718055994530942f;
         }
-#pragma unroll 1
-      for (int half = W / 2; half >= 1; half >>= 1) {
-        if (busy <= half) continue;
-        // Slots are those of the reading ranks of the first round, which a
-        // rank has read before it writes to one of them.
-        constexpr int kVec = NR * NG * 2;  // float4 of a lane
-        float4* const buf = reinterpret_cast<float4*>(sums);
-        if (rank >= half && rank < 2 * half && rank < busy) {
-          const int slot = half == W / 2 ? rank - half : rank;
+    } else {
+      // A part of a unit: [row][channel / 4], the quads of a row exchanged so
+      // that a store meets no bank twice.
+      float4* const dst = reinterpret_cast<float4*>(starts ? ring : smem + W * C::kRing + warp * C::kSums);
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            const float* x = &o[0][0][0][0] + 4 * i;
-            buf[(slot * kVec + i) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
-          }
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = r * 8 + 2 * t + c;
+#pragma unroll
+          for (int i = 0; i < NG; ++i)
+            dst[col * (D / 4) + ((8 * i + g) ^ (2 * t))] =
+                make_float4(o[r][i][0][c], o[r][i][0][c + 2], o[r][i][1][c], o[r][i][1][c + 2]);
+          if (g == 0) stats[starts ? 1 : 0][warp * C::kRows + col] = make_float2(ref[r][c], l[r][c]);
         }
-        __syncthreads();
-        if (rank < half && rank + half < busy) {
-          const int slot = half == W / 2 ? rank : rank + half;
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            float* x = &o[0][0][0][0] + 4 * i;
-            const float4 y = buf[(slot * kVec + i) * 32 + lane];
-            x[0] += y.x;
-            x[1] += y.y;
-            x[2] += y.z;
-            x[3] += y.w;
-          }
-        }
-      }
-    }
-
-    // ---- results of the unit, or of this CTA's part of it
-    if (rank == 0) {
-      const bool starts = s0 == 0, ends = s1 == now.steps;
-      if (starts && ends) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int col = r * 8 + 2 * t + c;
-            if (col >= n_rows) continue;
-            const float inv = l[r][c] == 0.f ? 0.f : 1.0f / l[r][c];
-            __nv_bfloat16* dst = p.o + (row_at + col) * D + 4 * g;
-#pragma unroll
-            for (int i = 0; i < NG; ++i)
-              *reinterpret_cast<uint2*>(dst + 32 * i) =
-                  make_uint2(pack_bf16(o[r][i][0][c] * inv, o[r][i][0][c + 2] * inv),
-                             pack_bf16(o[r][i][1][c] * inv, o[r][i][1][c + 2] * inv));
-            if (g == 0)
-              p.lse[row_at + col] = l[r][c] == 0.f ? -INFINITY : (ref[r][c] + lg2_approx(l[r][c])) * 0.69314718055994530942f;
-          }
+      if (starts) {
+        mine_left.tail = 1;
+        mine_left.row = row_at;
+        mine_left.rows = n_rows;
+        mine_left.past = my_end - s1 + now.steps;
       } else {
-        const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int col = r * 8 + 2 * t + c;
-            float* dst = p.part_o + ((size_t)slot * C::kRows + col) * D + 4 * g;
-#pragma unroll
-            for (int i = 0; i < NG; ++i)
-              *reinterpret_cast<float4*>(dst + 32 * i) =
-                  make_float4(o[r][i][0][c], o[r][i][0][c + 2], o[r][i][1][c], o[r][i][1][c + 2]);
-            if (g == 0) p.part_ml[(size_t)slot * C::kRows + col] = make_float2(ref[r][c], l[r][c]);
-          }
-        if (starts && lane == 0) {
-          const long long x = end + (now.steps - s1);  // one past the unit's last step, in the list
-          Kv4Cut cut;
-          cut.row = (int)row_at;
-          cut.rows = n_rows;
-          cut.last = (int)((x * active + total - 1) / total) - 1;
-          cut.pad = 0;
-          p.cuts[blockIdx.x] = cut;
-        }
+        mine_left.head = ends ? 2 : 1;
+        mine_left.head_row = row_at;
+        mine_left.head_rows = n_rows;
       }
     }
-    turn += n_steps;
-    advance(now, n_steps);
+  }
+  if (lane == 0) left[warp] = mine_left;
+  __syncthreads();
+
+  // ---- join what the warps have left: chain 0 goes on from the CTA before,
+  // chain k begins with warp k - 1's tail; then the heads of the warps behind
+  // it until the unit's end.  A warp takes a row of a chain at a time.
+  for (int j = warp; j < (W + 1) * C::kRows; j += W) {
+    const int chain = j / C::kRows, col = j % C::kRows;
+    const bool starts = chain > 0;
+    if (starts && !left[chain - 1].tail) continue;
+    int from = chain, row_at = 0, n_rows = 0;  // the first warp whose head belongs to it
+    if (starts) {
+      row_at = left[chain - 1].row;
+      n_rows = left[chain - 1].rows;
+    } else {
+      while (from < W && left[from].head == 0 && !left[from].tail) ++from;  // warps that had no step
+      if (from == W || left[from].head == 0) continue;
+      row_at = left[from].head_row;
+      n_rows = left[from].head_rows;
+    }
+    if (col >= n_rows) continue;
+    bool ends = false;
+    int past = from;
+    float m = starts ? stats[1][(chain - 1) * C::kRows + col].x : -3.402823466e38f;
+    for (; past < W && !ends; ++past) {
+      if (left[past].head == 0) continue;
+      m = fmaxf(m, stats[0][past * C::kRows + col].x);
+      ends = left[past].head == 2;
+    }
+    constexpr int kMany = (D / 4 + 31) / 32;
+    float4 x[kMany];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMany; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const uint8_t* from_, float2 ml) {
+      const float f = ex2_approx(ml.x - m);
+      sum = fmaf(ml.y, f, sum);
+      const float4* const src = reinterpret_cast<const float4*>(from_) + col * (D / 4);
+#pragma unroll
+      for (int i = 0; i < kMany; ++i) {
+        const int quad = 32 * i + lane;
+        if (quad >= D / 4) continue;
+        const float4 y = src[quad ^ (col & 6)];
+        x[i].x = fmaf(y.x, f, x[i].x);
+        x[i].y = fmaf(y.y, f, x[i].y);
+        x[i].z = fmaf(y.z, f, x[i].z);
+        x[i].w = fmaf(y.w, f, x[i].w);
+      }
+    };
+    if (starts) add(smem + (chain - 1) * C::kRing, stats[1][(chain - 1) * C::kRows + col]);
+    for (int w = from; w < past; ++w)
+      if (left[w].head != 0) add(smem + W * C::kRing + w * C::kSums, stats[0][w * C::kRows + col]);
+    if (starts && ends) {
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < kMany; ++i)
+        if (32 * i + lane < D / 4)
+          *reinterpret_cast<uint2*>(p.o + (size_t)(row_at + col) * D + 4 * (32 * i + lane)) =
+              make_uint2(pack_bf16(x[i].x * inv, x[i].y * inv), pack_bf16(x[i].z * inv, x[i].w * inv));
+      if (lane == 0) p.lse[row_at + col] = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * 0.69314718055994530942f;
+    } else {
+      // The unit goes on in another CTA.
+      const size_t slot = (size_t)(2 * blockIdx.x + (starts ? 1 : 0)) * C::kRows + col;
+#pragma unroll
+      for (int i = 0; i < kMany; ++i)
+        if (32 * i + lane < D / 4) reinterpret_cast<float4*>(p.part_o + slot * D)[32 * i + lane] = x[i];
+      if (lane == 0) p.part_ml[slot] = make_float2(m, sum);
+      if (starts && col == 0 && lane == 0) {
+        Kv4Cut cut;
+        cut.row = row_at;
+        cut.rows = n_rows;
+        cut.last = (int)((left[chain - 1].past * active + total - 1) / total) - 1;
+        cut.pad = 0;
+        p.cuts[blockIdx.x] = cut;
+      }
+    }
   }
 
   // After a wait that gave up, copies may still be in flight into this CTA's
@@ -699,7 +738,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, Cfg<D, NR>::kCtas) kv4_f
   if (!ok) {
     const uint64_t t0 = globaltimer_ns();
     for (int s = 0; s < C::kStages; ++s)
-      while (!mbar_try_wait(smem_u32(&my_bars[s]), s < stage ? phase ^ 1 : phase) &&
+      while (!mbar_try_wait(smem_u32(&bar[s]), s < stage ? phase ^ 1 : phase) &&
              globaltimer_ns() - t0 < p.timeout_ns) {
       }
   }
@@ -754,18 +793,12 @@ cudaError_t launch_fwd_t(const Kv4FwdParams& p, int grid, cudaStream_t stream) {
 
 }  // namespace
 
-// Rows of a unit, CTAs an SM and keys a step for head dim d and `rows` query
-// rows a key/value head.  Two row tiles a unit only where one does not hold
-// the rows, and not at d = 256, whose sums take 64 registers a tile.
-void kv4_fwd_shape(int d, int rows, int* unit_rows, int* ctas_per_sm, int* step_keys) {
+// Rows of a unit and keys of a step for head dim d and `rows` query rows a
+// key/value head.  Two row tiles a unit only where one does not hold the rows,
+// and not at d = 256, whose sums take 64 registers a tile.
+void kv4_fwd_shape(int d, int rows, int* unit_rows, int* step_keys) {
   const bool two = rows > kKv4Rows && d != 256;
   *unit_rows = two ? 2 * kKv4Rows : kKv4Rows;
-  switch (d) {
-    case 64: *ctas_per_sm = two ? Cfg<64, 2>::kCtas : Cfg<64, 1>::kCtas; break;
-    case 96: *ctas_per_sm = two ? Cfg<96, 2>::kCtas : Cfg<96, 1>::kCtas; break;
-    case 128: *ctas_per_sm = two ? Cfg<128, 2>::kCtas : Cfg<128, 1>::kCtas; break;
-    default: *ctas_per_sm = Cfg<256, 1>::kCtas; break;
-  }
   *step_keys = Cfg<64, 1>::kKeys;
 }
 
