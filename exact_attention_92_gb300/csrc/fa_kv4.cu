@@ -16,7 +16,7 @@ int internal_device_setup(unsigned int** status, int* sm_count);
 cudaError_t internal_timed_launch(int kernel, cudaStream_t stream, cudaError_t (*launch)(void*), void* ctx);
 cudaError_t launch_kv4_move(int d, bool write, const Kv4Cache& c, const int* start, const int* count, const void* k_in,
                             const void* v_in, void* k_out, void* v_out, int N, cudaStream_t stream);
-void kv4_fwd_shape(int d, int rows, int* unit_rows, int* step_keys);
+void kv4_fwd_shape(int d, int rows, int* unit_rows, int* step_keys, int* unit_cost);
 cudaError_t launch_kv4_fwd(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_kv4_merge(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
 cudaError_t internal_workspace(void** ptr, size_t bytes, cudaStream_t st);
@@ -126,14 +126,17 @@ int check_fwd_sizes(int B, int H, int Hkv, int Nq, int d, int num_pages, int pag
 // How a call is carried out (fa_kv4_plan_t), for sizes that passed
 // check_fwd_sizes.  The lengths are known on the device only, so this goes by
 // what the table can hold.
-void plan_fwd(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages, int sm_count, fa_kv4_plan_t* pl) {
+// FA_ERR_INVALID_ARG where the list of steps might not fit 31 bits.
+int plan_fwd(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages, int sm_count, fa_kv4_plan_t* pl) {
   std::memset(pl, 0, sizeof(*pl));
   pl->rows = (H / Hkv) * Nq;
-  fa::kv4_fwd_shape(d, pl->rows, &pl->unit_rows, &pl->step_keys);
+  int unit_cost = 0;
+  fa::kv4_fwd_shape(d, pl->rows, &pl->unit_rows, &pl->step_keys, &unit_cost);
   pl->row_blocks = (pl->rows + pl->unit_rows - 1) / pl->unit_rows;
   pl->units = B * Hkv * pl->row_blocks;
   const long long held = (long long)max_pages * page_size;
   pl->max_steps = (int)((held + pl->step_keys - 1) / pl->step_keys);
+  if ((long long)pl->units * (pl->max_steps + unit_cost) > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   pl->whole = pl->max_steps <= kWholeSteps ? 1 : 0;
   const long long most = (long long)pl->units * (pl->whole ? 1 : pl->max_steps);
   pl->grid = (int)std::min<long long>(most, sm_count);
@@ -141,6 +144,7 @@ void plan_fwd(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages
   if (!pl->whole)
     pl->workspace_bytes = (uint64_t)pl->grid * (2ull * pl->unit_rows * (d * sizeof(float) + sizeof(float2)) +
                                                 sizeof(fa::Kv4Cut));
+  return FA_OK;
 }
 
 }  // namespace
@@ -182,7 +186,8 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
   e = fa::internal_device_setup(&status, &sm_count);
   if (e) return e;
   fa_kv4_plan_t pl;
-  plan_fwd(B, H, Hkv, Nq, d, page_size, max_pages, sm_count, &pl);
+  e = plan_fwd(B, H, Hkv, Nq, d, page_size, max_pages, sm_count, &pl);
+  if (e) return e;
   Fwd f;
   f.d = d;
   f.unit_rows = pl.unit_rows;
@@ -226,8 +231,10 @@ int fa_kv4_fwd_plan(int B, int H, int Hkv, int Nq, int d, int page_size, int max
   if (plan == nullptr || sm_count < 1) return FA_ERR_INVALID_ARG;
   const int e = check_fwd_sizes(B, H, Hkv, Nq, d, 1, page_size, max_pages, FA_CAUSAL_NONE);
   if (e) return e;
-  plan_fwd(B, H, Hkv, Nq, d, page_size, max_pages, sm_count, plan);
-  return FA_OK;
+  fa_kv4_plan_t pl;
+  const int e2 = plan_fwd(B, H, Hkv, Nq, d, page_size, max_pages, sm_count, &pl);
+  if (e2 == FA_OK) *plan = pl;
+  return e2;
 }
 
 }  // extern "C"

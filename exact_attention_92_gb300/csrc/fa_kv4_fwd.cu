@@ -54,12 +54,10 @@ struct Cfg {
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kBlocks = 2;                             // 16-token blocks a step
   static constexpr int kKeys = kBlocks * kKv4Block;
-  static constexpr int kStages = D == 256 ? 2 : (D == 128 ? 3 : 4);
+  static constexpr int kStages = D == 256 || (D == 128 && NR == 1) ? 2 : 3;
   static constexpr int kStageBytes = kBlocks * Kv4<D>::kBlockBytes;
   static constexpr int kRows = NR * kKv4Rows;
-  static constexpr int kLens = 512;                             // sequence lengths kept in shared memory
-  // What a unit costs a warp besides its steps, in steps.
-  static constexpr int kUnitCost = 1;
+  static constexpr int kLens = 1024;                            // sequence lengths kept in shared memory
   // Shared memory: a ring of steps and the sums of a unit's head for each
   // warp (the sums of a tail go to the ring, which is empty by then).
   static constexpr int kRing = kStages * kStageBytes;
@@ -67,6 +65,10 @@ struct Cfg {
   static constexpr int kSmem = kWarps * (kRing + kSums);
   static_assert(kRing >= kSums, "a tail's sums go where the ring was");
 };
+
+// Places of the list that a unit takes besides one for each of its steps: what
+// it costs a warp, its query rows among it.
+constexpr int kUnitCost = 2;
 
 // A unit, or a stretch of its steps, that a warp has to do.
 struct Piece {
@@ -81,7 +83,7 @@ struct Left {
   int tail;        // 1: the beginning of a unit that goes on
   int row, rows;   // rows of the tail's unit, or of the head's where there is no tail
   int head_row, head_rows;
-  long long past;  // one past the last step of the tail's unit, in the list
+  int past;        // one past the last step of the tail's unit, in the list
 };
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -194,8 +196,15 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
   __shared__ float2 stats[2][W * C::kRows];  // reference and sum of heads, of tails
   __shared__ int lims[W * C::kRows];
   __shared__ int lens[C::kLens];
-  __shared__ long long warp_sum[W];
+  __shared__ int warp_sum[W];
   __shared__ int found[2][4];
+  // Chains of results to be joined: the warps [from, past) whose heads belong
+  // to it, the tail that begins it (or -1), and where its rows are.
+  struct Chain {
+    int tail, from, past, ends, row, rows;
+  };
+  __shared__ Chain chains[W + 1];
+  __shared__ int n_chains;
 
   // Through a shuffle, so that what follows from it stays in uniform registers.
   auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
@@ -217,45 +226,55 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     return n == 0 ? 1 : (n + C::kKeys - 1) / C::kKeys;
   };
 
-  // ---- this CTA's stretch [first, end) of the list.  A unit takes kUnitCost
-  // places and then one for each step.  Each thread adds up a run of sequences.
+  // ---- this CTA's stretch [first, end) of the list (the host has checked
+  // that its places fit 31 bits).  Each thread adds up a run of sequences.
   const int run = (p.c.B + C::kThreads - 1) / C::kThreads;
   const int b0 = min(p.c.B, tid * run), b1 = min(p.c.B, b0 + run);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += C::kUnitCost + steps_of(kv4_length(p.c, p.lens, b));
-  long long upto = mine;
+  const bool keep = p.c.B <= C::kLens;
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = kv4_length(p.c, p.lens, b);
+    if (keep) lens[b] = n;
+    mine += kUnitCost + steps_of(n);
+  }
+  int upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += x;
   }
   if (lane == 31) warp_sum[warp] = upto;
+  if (tid == 0) n_chains = 0;
+  if (tid == 0 && !p.whole) p.cuts[blockIdx.x].row = -1;
   __syncthreads();
-  long long total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < W; ++w) {
-    if (w < warp) upto += warp_sum[w];
-    total += warp_sum[w];
+    const int x = warp_sum[w];
+    if (w < warp) upto += x;
+    total += x;
   }
-  // CTAs that take part: two places for every warp, or a unit each.
-  const long long want = max(total * units / (2 * W), (long long)p.c.B * units);
-  const int active = (int)min((long long)gridDim.x, want);
   total *= units;
-  if (tid == 0 && !p.whole) p.cuts[blockIdx.x].row = -1;
+  // CTAs that take part: two places for every warp, or a unit each.
+  const int active = min((int)gridDim.x, max(total / (2 * W), p.c.B * units));
   if ((int)blockIdx.x >= active) return;
-  long long first = total * blockIdx.x / active, end = total * (blockIdx.x + 1) / active;
+  // The first `more` CTAs have a place more than the others.
+  const int each = total / active, more = total - each * active;
+  int first = (int)blockIdx.x * each + min((int)blockIdx.x, more);
+  int end = first + each + ((int)blockIdx.x < more ? 1 : 0);
   // Sequence, unit, place within it and places of the unit at list place x.
-  auto find = [&](long long x, int* f) {
+  auto find = [&](int x, int* f) {
     if (mine > 0 && (upto - mine) * units <= x && x < upto * units) {
-      long long rest = x - (upto - mine) * units;
-      int b = b0, n = C::kUnitCost + steps_of(kv4_length(p.c, p.lens, b));
-      while (rest >= (long long)n * units && b + 1 < b1) {
-        rest -= (long long)n * units;
-        n = C::kUnitCost + steps_of(kv4_length(p.c, p.lens, ++b));
+      int rest = x - (upto - mine) * units, b = b0;
+      int n = kUnitCost + steps_of(keep ? lens[b] : kv4_length(p.c, p.lens, b));
+      while (rest >= n * units && b + 1 < b1) {
+        rest -= n * units;
+        ++b;
+        n = kUnitCost + steps_of(keep ? lens[b] : kv4_length(p.c, p.lens, b));
       }
       f[0] = b;
-      f[1] = (int)(rest / n);
-      f[2] = (int)(rest % n);
+      f[1] = rest / n;
+      f[2] = rest - f[1] * n;
       f[3] = n;
     }
   };
@@ -272,18 +291,22 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
         ++at_b;
       }
     }
-    if (end < total && found[1][2] > 0) end += found[1][3] - found[1][2];
+    if (end < total && found[1][2] > 0) end += uniform(found[1][3] - found[1][2]);
   }
   if (first >= end) return;
-  const int base_b = at_b;
-  for (int i = tid; i < C::kLens && base_b + i < p.c.B; i += C::kThreads) lens[i] = kv4_length(p.c, p.lens, base_b + i);
-  __syncthreads();
+  const int base_b = keep ? 0 : at_b;
+  if (!keep) {
+    for (int i = tid; i < C::kLens && base_b + i < p.c.B; i += C::kThreads)
+      lens[i] = kv4_length(p.c, p.lens, base_b + i);
+    __syncthreads();
+  }
   auto length = [&](int b) { return uniform(b - base_b < C::kLens ? lens[b - base_b] : kv4_length(p.c, p.lens, b)); };
 
   // ---- this warp's stretch of it, walked by the copies
-  const long long my_end = first + (end - first) * (warp + 1) / W;
-  long long at = first + (end - first) * warp / W;
-  long long skip = at - first + at_off;  // places from the beginning of unit at_u
+  const int warp_each = (end - first) / W, warp_more = (end - first) - warp_each * W;
+  int at = first + warp * warp_each + min(warp, warp_more);
+  const int my_end = at + warp_each + (warp < warp_more ? 1 : 0);
+  int skip = at - first + at_off;  // places from the beginning of unit at_u
   Piece ahead;
   ahead.b = at_b;
   ahead.u = at_u;
@@ -294,20 +317,20 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     row = p.c.table + (size_t)ahead.b * p.c.max_pages;
   };
   sequence();
-  while (skip >= (long long)(units - ahead.u) * (C::kUnitCost + ahead.steps) && ahead.b + 1 < p.c.B) {
-    skip -= (long long)(units - ahead.u) * (C::kUnitCost + ahead.steps);
+  while (skip >= (units - ahead.u) * (kUnitCost + ahead.steps) && ahead.b + 1 < p.c.B) {
+    skip -= (units - ahead.u) * (kUnitCost + ahead.steps);
     ahead.u = 0;
     ++ahead.b;
     sequence();
   }
-  const int jump = (int)(skip / (C::kUnitCost + ahead.steps));
+  const int jump = skip / (kUnitCost + ahead.steps);
   ahead.u += jump;
   int made = 0, taken = 0;  // pieces put into the queue, and taken out
   auto enter = [&](int off) {
     ahead.head = p.row_blocks == 1 ? ahead.u : ahead.u / p.row_blocks;
-    const int upto_off = (int)min((long long)ahead.steps + C::kUnitCost, off + my_end - at);
-    ahead.lo = max(0, off - C::kUnitCost);
-    ahead.hi = max(ahead.lo, upto_off - C::kUnitCost);
+    const int upto_off = min(ahead.steps + kUnitCost, off + my_end - at);
+    ahead.lo = max(0, off - kUnitCost);
+    ahead.hi = max(ahead.lo, upto_off - kUnitCost);
     at += upto_off - off;
     if (ahead.lo < ahead.hi) {
       if (lane == 0) queue[warp * kQueue + made % kQueue] = ahead;
@@ -329,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     enter(0);
   };
   ahead.lo = ahead.hi = 0;
-  if (at < my_end) enter((int)(skip - (long long)jump * (C::kUnitCost + ahead.steps)));
+  if (at < my_end) enter(skip - jump * (kUnitCost + ahead.steps));
 
   // A copy takes the blocks of a step that lie in one page, all of them where
   // pages are long enough; lane i issues the step's copy i, whose page it has
@@ -658,63 +681,81 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
   if (lane == 0) left[warp] = mine_left;
   __syncthreads();
 
-  // ---- join what the warps have left: chain 0 goes on from the CTA before,
-  // chain k begins with warp k - 1's tail; then the heads of the warps behind
-  // it until the unit's end.  A warp takes a row of a chain at a time.
-  for (int j = warp; j < (W + 1) * C::kRows; j += W) {
-    const int chain = j / C::kRows, col = j % C::kRows;
-    const bool starts = chain > 0;
-    if (starts && !left[chain - 1].tail) continue;
-    int from = chain, row_at = 0, n_rows = 0;  // the first warp whose head belongs to it
-    if (starts) {
-      row_at = left[chain - 1].row;
-      n_rows = left[chain - 1].rows;
+  // ---- join what the warps have left: a chain begins with a warp's tail, or
+  // goes on from the CTA before, and takes the heads of the warps behind it
+  // until the unit's end.
+  if (warp == 0 && lane <= W) {
+    Chain c;
+    c.tail = lane - 1;
+    c.from = lane;
+    c.ends = 0;
+    bool is = false;
+    if (lane > 0) {
+      is = left[lane - 1].tail != 0;
+      c.row = left[lane - 1].row;
+      c.rows = left[lane - 1].rows;
     } else {
-      while (from < W && left[from].head == 0 && !left[from].tail) ++from;  // warps that had no step
-      if (from == W || left[from].head == 0) continue;
-      row_at = left[from].head_row;
-      n_rows = left[from].head_rows;
+      while (c.from < W && left[c.from].head == 0 && left[c.from].tail == 0) ++c.from;  // no step, or whole units
+      if (c.from < W && left[c.from].head != 0) {
+        is = true;
+        c.row = left[c.from].head_row;
+        c.rows = left[c.from].head_rows;
+      }
     }
-    if (col >= n_rows) continue;
-    bool ends = false;
-    int past = from;
-    float m = starts ? stats[1][(chain - 1) * C::kRows + col].x : -3.402823466e38f;
-    for (; past < W && !ends; ++past) {
-      if (left[past].head == 0) continue;
-      m = fmaxf(m, stats[0][past * C::kRows + col].x);
-      ends = left[past].head == 2;
+    if (is) {
+      c.past = c.from;
+      while (c.past < W && !c.ends) c.ends = left[c.past++].head == 2;
     }
+    const uint32_t who = __ballot_sync((1u << (W + 1)) - 1, is);
+    if (is) chains[__popc(who & ((1u << lane) - 1))] = c;
+    if (lane == 0) n_chains = __popc(who);
+  }
+  __syncthreads();
+  // A warp takes a row of a chain at a time.
+  for (int j = warp; j < n_chains * C::kRows; j += W) {
+    const Chain c = chains[j / C::kRows];
+    const int col = j % C::kRows;
+    if (col >= c.rows) continue;
+    const bool starts = c.tail >= 0;
+    // Lane w has warp w's reference, sum and factor; lane 31 the tail's.
+    float2 ml = make_float2(-3.402823466e38f, 0.f);
+    if (lane >= c.from && lane < c.past && left[lane].head != 0) ml = stats[0][lane * C::kRows + col];
+    if (lane == 31 && starts) ml = stats[1][c.tail * C::kRows + col];
+    float m = ml.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float f = ex2_approx(ml.x - m);
+    float sum = ml.y * f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     constexpr int kMany = (D / 4 + 31) / 32;
     float4 x[kMany];
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kMany; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const uint8_t* from_, float2 ml) {
-      const float f = ex2_approx(ml.x - m);
-      sum = fmaf(ml.y, f, sum);
-      const float4* const src = reinterpret_cast<const float4*>(from_) + col * (D / 4);
+    auto add = [&](const uint8_t* part, float by, bool there) {
+      const float4* const src = reinterpret_cast<const float4*>(part) + col * (D / 4);
 #pragma unroll
       for (int i = 0; i < kMany; ++i) {
-        const int quad = 32 * i + lane;
-        if (quad >= D / 4) continue;
+        const int quad = min(32 * i + lane, D / 4 - 1);
         const float4 y = src[quad ^ (col & 6)];
-        x[i].x = fmaf(y.x, f, x[i].x);
-        x[i].y = fmaf(y.y, f, x[i].y);
-        x[i].z = fmaf(y.z, f, x[i].z);
-        x[i].w = fmaf(y.w, f, x[i].w);
+        x[i].x = there ? fmaf(y.x, by, x[i].x) : x[i].x;
+        x[i].y = there ? fmaf(y.y, by, x[i].y) : x[i].y;
+        x[i].z = there ? fmaf(y.z, by, x[i].z) : x[i].z;
+        x[i].w = there ? fmaf(y.w, by, x[i].w) : x[i].w;
       }
     };
-    if (starts) add(smem + (chain - 1) * C::kRing, stats[1][(chain - 1) * C::kRows + col]);
-    for (int w = from; w < past; ++w)
-      if (left[w].head != 0) add(smem + W * C::kRing + w * C::kSums, stats[0][w * C::kRows + col]);
-    if (starts && ends) {
+#pragma unroll
+    for (int i = 0; i < kMany; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (starts) add(smem + c.tail * C::kRing, __shfl_sync(0xffffffffu, f, 31), true);
+#pragma unroll 4
+    for (int w = c.from; w < c.past; ++w)
+      add(smem + W * C::kRing + w * C::kSums, __shfl_sync(0xffffffffu, f, w), left[w].head != 0);
+    if (starts && c.ends) {
       const float inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
       for (int i = 0; i < kMany; ++i)
         if (32 * i + lane < D / 4)
-          *reinterpret_cast<uint2*>(p.o + (size_t)(row_at + col) * D + 4 * (32 * i + lane)) =
+          *reinterpret_cast<uint2*>(p.o + (size_t)(c.row + col) * D + 4 * (32 * i + lane)) =
               make_uint2(pack_bf16(x[i].x * inv, x[i].y * inv), pack_bf16(x[i].z * inv, x[i].w * inv));
-      if (lane == 0) p.lse[row_at + col] = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * 0.69314718055994530942f;
+      if (lane == 0) p.lse[c.row + col] = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * 0.69314718055994530942f;
     } else {
       // The unit goes on in another CTA.
       const size_t slot = (size_t)(2 * blockIdx.x + (starts ? 1 : 0)) * C::kRows + col;
@@ -723,10 +764,11 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
         if (32 * i + lane < D / 4) reinterpret_cast<float4*>(p.part_o + slot * D)[32 * i + lane] = x[i];
       if (lane == 0) p.part_ml[slot] = make_float2(m, sum);
       if (starts && col == 0 && lane == 0) {
+        const int last = left[c.tail].past - 1;  // place of the unit's last step
         Kv4Cut cut;
-        cut.row = row_at;
-        cut.rows = n_rows;
-        cut.last = (int)((left[chain - 1].past * active + total - 1) / total) - 1;
+        cut.row = c.row;
+        cut.rows = c.rows;
+        cut.last = last < more * (each + 1) ? last / (each + 1) : more + (last - more * (each + 1)) / each;
         cut.pad = 0;
         p.cuts[blockIdx.x] = cut;
       }
@@ -749,7 +791,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
 // parts in the order of the CTAs.
 template <int D, int NR>
 __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4FwdParams p) {
-  constexpr int kRows = NR * kKv4Rows, kPer = D / 32;
+  constexpr int kRows = NR * kKv4Rows;
+  constexpr int kMany = (D / 4 + 31) / 32, kBatch = 8 / kMany;
   pdl_wait();
   const Kv4Cut cut = p.cuts[blockIdx.x];
   if (cut.row < 0) return;
@@ -758,24 +801,65 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4FwdParams p) {
   for (int row = threadIdx.x / 32; row < cut.rows; row += 8) {
     // Part k: the tail of this CTA, then the heads of those behind it.
     auto at = [&](int k) { return (size_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * kRows + row; };
-    float m = -3.402823466e38f;
-    for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.part_ml[at(k)].x);
+    float4 acc[kMany], next[kBatch][kMany];
+    auto fetch = [&](int k0) {
 #pragma unroll
-    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    float acc[kPer] = {}, l = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float2 ml = p.part_ml[at(k)];
-      const float f = ex2_approx(ml.x - m);
-      l = fmaf(ml.y, f, l);
-      const float* src = p.part_o + at(k) * D + lane;
+      for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(src[32 * i], f, acc[i]);
+        for (int i = 0; i < kMany; ++i)
+          if (k0 + k < parts && 32 * i + lane < D / 4)
+            next[k][i] = reinterpret_cast<const float4*>(p.part_o + at(k0 + k) * D)[32 * i + lane];
+    };
+    fetch(0);
+    float m = -3.402823466e38f, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMany; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < parts; k0 += 32) {  // references of 32 parts at a time
+      const float2 ml = k0 + lane < parts ? p.part_ml[at(k0 + lane)] : make_float2(-3.402823466e38f, 0.f);
+      float top = fmaxf(m, ml.x);
+#pragma unroll
+      for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float back = ex2_approx(m - top), f = ex2_approx(ml.x - top);
+      m = top;
+      float sum = ml.y * f;
+#pragma unroll
+      for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      l = fmaf(l, back, sum);
+#pragma unroll
+      for (int i = 0; i < kMany; ++i) {
+        acc[i].x *= back;
+        acc[i].y *= back;
+        acc[i].z *= back;
+        acc[i].w *= back;
+      }
+      for (int k = k0; k < min(k0 + 32, parts); k += kBatch) {
+        float4 now[kBatch][kMany];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+          for (int i = 0; i < kMany; ++i) now[x][i] = next[x][i];
+        fetch(k + kBatch);
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const float by = __shfl_sync(0xffffffffu, f, k - k0 + x);
+          if (k + x < parts) {
+#pragma unroll
+            for (int i = 0; i < kMany; ++i) {
+              acc[i].x = fmaf(now[x][i].x, by, acc[i].x);
+              acc[i].y = fmaf(now[x][i].y, by, acc[i].y);
+              acc[i].z = fmaf(now[x][i].z, by, acc[i].z);
+              acc[i].w = fmaf(now[x][i].w, by, acc[i].w);
+            }
+          }
+        }
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      p.o[((size_t)cut.row + row) * D + lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv);
+    for (int i = 0; i < kMany; ++i)
+      if (32 * i + lane < D / 4)
+        *reinterpret_cast<uint2*>(p.o + ((size_t)cut.row + row) * D + 4 * (32 * i + lane)) =
+            make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
     if (lane == 0) p.lse[cut.row + row] = l == 0.f ? -INFINITY : (m + lg2_approx(l)) * 0.69314718055994530942f;
   }
 }
@@ -796,10 +880,11 @@ cudaError_t launch_fwd_t(const Kv4FwdParams& p, int grid, cudaStream_t stream) {
 // Rows of a unit and keys of a step for head dim d and `rows` query rows a
 // key/value head.  Two row tiles a unit only where one does not hold the rows,
 // and not at d = 256, whose sums take 64 registers a tile.
-void kv4_fwd_shape(int d, int rows, int* unit_rows, int* step_keys) {
+void kv4_fwd_shape(int d, int rows, int* unit_rows, int* step_keys, int* unit_cost) {
   const bool two = rows > kKv4Rows && d != 256;
   *unit_rows = two ? 2 * kKv4Rows : kKv4Rows;
   *step_keys = Cfg<64, 1>::kKeys;
+  *unit_cost = kUnitCost;
 }
 
 cudaError_t launch_kv4_fwd(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream) {

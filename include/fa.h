@@ -387,6 +387,8 @@ int fa_kv4_read(const void* cache, const int* block_table, const int* start, con
  *   causal : with Nk = lens[b] for sequence b: FA_CAUSAL_NONE, _TOP_LEFT or
  *            _BOTTOM_RIGHT.  A row that sees no key gets O = 0, L = -inf
  *            (all rows of a sequence of length 0).
+ * FA_ERR_INVALID_ARG also where the table could hold more work than a 31-bit
+ * list of steps: units * (max_steps + 2) of fa_kv4_fwd_plan above 2^31 - 1.
  * Scores, softmax and sums are fp32 on the exact held values.
  */
 int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const int* lens, void* o, float* lse,
