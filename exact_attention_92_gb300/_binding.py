@@ -309,36 +309,54 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, causal=False, scale=None, 
     _check(st, "fa_bwd_noalloc")
 
 
-def _check_on_device(name, t):
-    import torch
+# The calls over the 4-bit cache are made once a layer and decoding step, where
+# the time of their checks shows (18 us a call when each was checked by
+# itself, 8 us so): all are looked at in one expression, what is wrong is worked
+# out after that, and the device and the stream are asked for without building
+# objects.
 
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-
-
-def _check_int32(name, t, shape):
-    import torch
-
-    _check_on_device(name, t)
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or any(
-            w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must be a contiguous int32 tensor {shape}, got {t.dtype} {tuple(t.shape)}")
+_torch = None
 
 
-def _check_cache(cache, d):
-    """(num_pages, Hkv, page_size) of a cache tensor for head dim d."""
-    import torch
+def _torch_cuda():
+    """(torch, current CUDA device)."""
+    global _torch
+    if _torch is None:
+        import torch
 
-    _check_on_device("cache", cache)
-    if cache.dtype != torch.uint8 or cache.dim() != 3 or not cache.is_contiguous():
-        raise ValueError("cache must be a contiguous uint8 [num_pages, Hkv, page_size * 9 d / 8] tensor")
-    num_pages, Hkv, page_bytes = cache.shape
-    page_size, rest = divmod(page_bytes * 8, 9 * d)
+        _torch = torch
+    if not _torch.cuda.is_initialized():
+        # No CUDA tensor exists yet, so that any argument is refused.
+        return _torch, None
+    return _torch, _torch._C._cuda_getDevice()
+
+
+def _refuse(tensors, device):
+    """Raises for the first of (name, tensor, type, shape) that is not a
+    contiguous tensor of that type and shape on the current device."""
+    for name, t, dtype, shape in tensors:
+        if not isinstance(t, _torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not dtype or t.dim() != len(shape) or any(
+                w is not None and n != w for n, w in zip(t.shape, shape)) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, "
+                             f"got {t.dtype} {tuple(t.shape)}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, not on the current CUDA device (use torch.cuda.device)")
+    raise ValueError("the arguments do not fit together")
+
+
+def _page_size(page_bytes, d):
+    page_size, rest = divmod(page_bytes * 8, 9 * d) if d > 0 else (0, 1)
     if rest or page_size < 1:
         raise ValueError(f"cache has {page_bytes} bytes a page and head, not a multiple of 9 * {d} / 8")
-    return num_pages, Hkv, page_size
+    return page_size
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(device)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def fa_kv4_cache_bytes(num_pages, Hkv, page_size, d) -> int:
@@ -349,52 +367,82 @@ def fa_kv4_cache_bytes(num_pages, Hkv, page_size, d) -> int:
     return n.value
 
 
-def _kv4_move(what, k, v, cache, block_table, start, count):
-    _check_bhnd("k", k)
-    B, Hkv, N, d = k.shape
-    _check_bhnd("v", v, k.shape)
-    num_pages, heads, page_size = _check_cache(cache, d)
+def _kv4_move(k, v, cache, block_table, start, count):
+    torch, device = _torch_cuda()
+    bf16, i32 = torch.bfloat16, torch.int32
+    try:
+        B, Hkv, N, d = k.shape
+        num_pages, heads, page_bytes = cache.shape
+        rows, max_pages = block_table.shape
+        good = (k.dtype is bf16 and k.get_device() == device and k.is_contiguous()
+                and v.dtype is bf16 and v.get_device() == device and v.is_contiguous() and v.shape == k.shape
+                and cache.dtype is torch.uint8 and cache.get_device() == device and cache.is_contiguous()
+                and block_table.dtype is i32 and block_table.get_device() == device and block_table.is_contiguous()
+                and start.dtype is i32 and start.get_device() == device and start.is_contiguous()
+                and start.shape == (B,) and rows == B
+                and (count is None or count.dtype is i32 and count.get_device() == device and count.is_contiguous()
+                     and count.shape == (B,)))
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        first = tuple(getattr(k, "shape", ()))
+        B, Hkv, N, d = first if len(first) == 4 else (None,) * 4
+        args = [("k", k, bf16, (B, Hkv, N, d)), ("v", v, bf16, (B, Hkv, N, d)),
+                ("cache", cache, torch.uint8, (None, None, None)), ("block_table", block_table, i32, (B, None)),
+                ("start", start, i32, (B,))]
+        _refuse(args if count is None else args + [("count", count, i32, (B,))], device)
     if heads != Hkv:
         raise ValueError(f"cache has {heads} heads, k has {Hkv}")
-    _check_int32("block_table", block_table, (B, None))
-    _check_int32("start", start, (B,))
-    if count is not None:
-        _check_int32("count", count, (B,))
-    return B, Hkv, N, d, num_pages, page_size, block_table.shape[1]
+    return device, (B, Hkv, N, d, num_pages, _page_size(page_bytes, d), max_pages)
 
 
 def fa_kv4_write(k, v, cache, block_table, start, count=None, stream=None):
     """C fa_kv4_write: quantise tokens k, v [B, Hkv, N, d] into the 4-bit
     cache [num_pages, Hkv, page_size * 9 d / 8] (uint8), token i < count[b]
     (all N without count) of sequence b to position start[b] + i."""
-    sizes = _kv4_move("fa_kv4_write", k, v, cache, block_table, start, count)
-    _check(load().fa_kv4_write(_ptr(k), _ptr(v), _ptr(cache), _ptr(block_table), _ptr(start),
-                               None if count is None else _ptr(count), *sizes, _stream_ptr(stream, k.device)),
+    device, sizes = _kv4_move(k, v, cache, block_table, start, count)
+    _check(load().fa_kv4_write(k.data_ptr(), v.data_ptr(), cache.data_ptr(), block_table.data_ptr(), start.data_ptr(),
+                               None if count is None else count.data_ptr(), *sizes, _raw_stream(stream, device)),
            "fa_kv4_write")
 
 
 def fa_kv4_read(cache, block_table, start, k, v, count=None, stream=None):
     """C fa_kv4_read: the held values of positions start[b] + i to rows
     i < count[b] of k, v [B, Hkv, N, d]; other rows are left as they were."""
-    sizes = _kv4_move("fa_kv4_read", k, v, cache, block_table, start, count)
-    _check(load().fa_kv4_read(_ptr(cache), _ptr(block_table), _ptr(start), None if count is None else _ptr(count),
-                              _ptr(k), _ptr(v), *sizes, _stream_ptr(stream, k.device)), "fa_kv4_read")
+    device, sizes = _kv4_move(k, v, cache, block_table, start, count)
+    _check(load().fa_kv4_read(cache.data_ptr(), block_table.data_ptr(), start.data_ptr(),
+                              None if count is None else count.data_ptr(), k.data_ptr(), v.data_ptr(), *sizes,
+                              _raw_stream(stream, device)), "fa_kv4_read")
 
 
 def fa_kv4_fwd(q, cache, block_table, lens, o, lse, causal=False, scale=None, stream=None):
     """C fa_kv4_fwd: attention of q [B, H, Nq, d] over the first lens[b]
     tokens of each sequence in the 4-bit cache; causal as fa_fwd_general."""
-    _check_bhnd("q", q)
-    B, H, Nq, d = q.shape
-    num_pages, Hkv, page_size = _check_cache(cache, d)
-    _check_int32("block_table", block_table, (B, None))
-    _check_int32("lens", lens, (B,))
-    _check_bhnd("o", o, q.shape)
-    _check_lse(lse, (B, H, Nq))
-    _check_on_device("lse", lse)
-    _check(load().fa_kv4_fwd(_ptr(q), _ptr(cache), _ptr(block_table), _ptr(lens), _ptr(o), _ptr(lse), B, H, Hkv, Nq,
-                             d, num_pages, page_size, block_table.shape[1], _causal_code(causal), _scale(scale, d),
-                             _stream_ptr(stream, q.device)), "fa_kv4_fwd")
+    torch, device = _torch_cuda()
+    bf16, i32 = torch.bfloat16, torch.int32
+    try:
+        B, H, Nq, d = q.shape
+        num_pages, Hkv, page_bytes = cache.shape
+        rows, max_pages = block_table.shape
+        good = (q.dtype is bf16 and q.get_device() == device and q.is_contiguous()
+                and o.dtype is bf16 and o.get_device() == device and o.is_contiguous() and o.shape == q.shape
+                and cache.dtype is torch.uint8 and cache.get_device() == device and cache.is_contiguous()
+                and block_table.dtype is i32 and block_table.get_device() == device and block_table.is_contiguous()
+                and lens.dtype is i32 and lens.get_device() == device and lens.is_contiguous() and lens.shape == (B,)
+                and rows == B and lse.dtype is torch.float32 and lse.get_device() == device
+                and lse.is_contiguous() and lse.shape == (B, H, Nq))
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        first = tuple(getattr(q, "shape", ()))
+        B, H, Nq, d = first if len(first) == 4 else (None,) * 4
+        _refuse([("q", q, bf16, (B, H, Nq, d)), ("cache", cache, torch.uint8, (None, None, None)),
+                 ("block_table", block_table, i32, (B, None)), ("lens", lens, i32, (B,)),
+                 ("o", o, bf16, (B, H, Nq, d)), ("lse", lse, torch.float32, (B, H, Nq))], device)
+    page_size = _page_size(page_bytes, d)
+    _check(load().fa_kv4_fwd(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lens.data_ptr(), o.data_ptr(),
+                             lse.data_ptr(), B, H, Hkv, Nq, d, num_pages, page_size, max_pages, _causal_code(causal),
+                             _scale(scale, d), _raw_stream(stream, device)), "fa_kv4_fwd")
 
 
 def fa_poll_status(stream=None):

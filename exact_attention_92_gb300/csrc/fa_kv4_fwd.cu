@@ -30,6 +30,7 @@
 // falls below 2^-14 of that loses relative, not absolute, precision.  The sum
 // of p is fp32.  log2(scale) is taken at 2^-80 at least, which keeps the sum
 // of p below 2^121.
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -869,9 +870,17 @@ namespace {
 template <int D, int NR>
 cudaError_t launch_fwd_t(const Kv4FwdParams& p, int grid, cudaStream_t stream) {
   using C = Cfg<D, NR>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kv4_fwd_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  // The kernel's shared memory is allowed once on each device.
+  static std::atomic<unsigned long long> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kv4_fwd_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
   return launch_pdl(kv4_fwd_kernel<D, NR>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, p);
 }
 

@@ -92,14 +92,14 @@ __device__ __forceinline__ void kv4_decode8(uint32_t w, uint32_t* h) {
 }
 
 // Eight fp32 to e2m1 codes (nearest, ties to even, saturating), x[0] lowest.
-__device__ __forceinline__ uint32_t kv4_encode8(const float* x) {
+__device__ __forceinline__ uint32_t kv4_encode8(const float2* x) {
   uint32_t w;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
       "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(w)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+      : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y));
   return w;
 }
 
