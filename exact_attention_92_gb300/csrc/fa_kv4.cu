@@ -15,7 +15,7 @@ namespace fa {
 int internal_device_setup(unsigned int** status, int* sm_count);
 cudaError_t internal_timed_launch(int kernel, cudaStream_t stream, cudaError_t (*launch)(void*), void* ctx);
 cudaError_t launch_kv4_move(int d, bool write, const Kv4Cache& c, const int* start, const int* count, const void* k_in,
-                            const void* v_in, void* k_out, void* v_out, int N, cudaStream_t stream);
+                            const void* v_in, void* k_out, void* v_out, int N, int sm_count, cudaStream_t stream);
 void kv4_fwd_shape(int d, int rows, int* unit_rows, int* step_keys, int* unit_cost);
 cudaError_t launch_kv4_fwd(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_kv4_merge(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
@@ -41,7 +41,7 @@ int check_sizes(int B, int heads, int Hkv, int rows, int d, int num_pages, int p
   if (page_size < kMinPage || page_size > kMaxPage || (page_size & (page_size - 1)) != 0) return FA_ERR_INVALID_ARG;
   if (!head_dim(d)) return FA_ERR_UNSUPPORTED;
   const long long most = 0x7fffffffLL;
-  if ((long long)max_pages * page_size > most) return FA_ERR_INVALID_ARG;
+  if ((long long)max_pages * page_size > most || rows > (1 << 30)) return FA_ERR_INVALID_ARG;
   if ((long long)B * heads > most || (long long)B * heads * rows > most) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
@@ -69,12 +69,13 @@ struct Move {
   const void *k_in, *v_in;
   void *k_out, *v_out;
   int N;
+  int sm_count;
   cudaStream_t st;
 };
 
 cudaError_t run_move(void* ctx) {
   const Move& m = *static_cast<const Move*>(ctx);
-  return fa::launch_kv4_move(m.d, m.write, m.c, m.start, m.count, m.k_in, m.v_in, m.k_out, m.v_out, m.N, m.st);
+  return fa::launch_kv4_move(m.d, m.write, m.c, m.start, m.count, m.k_in, m.v_in, m.k_out, m.v_out, m.N, m.sm_count, m.st);
 }
 
 int move(bool write, const void* k_in, const void* v_in, void* k_out, void* v_out, const void* cache,
@@ -92,7 +93,7 @@ int move(bool write, const void* k_in, const void* v_in, void* k_out, void* v_ou
   e = fa::internal_device_setup(&status, &sm_count);
   if (e) return e;
   Move m{d, write, view(cache, block_table, B, Hkv, num_pages, page_size, max_pages, status), start, count, k_in, v_in,
-         k_out, v_out, N, static_cast<cudaStream_t>(stream)};
+         k_out, v_out, N, sm_count, static_cast<cudaStream_t>(stream)};
   const int id = write ? FA_KERNEL_KV4_WRITE : FA_KERNEL_KV4_READ;
   return fa::internal_timed_launch(id, m.st, run_move, &m) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -342,7 +342,8 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  *                 the entries of pages that hold a position in use are read
  *                 or used; they must lie in [0, num_pages).
  *   start, count, lens : int32 [B], device memory, 4-byte aligned
- *   B * Hkv * N (B * H * Nq) and max_pages * page_size at most 2^31 - 1
+ *   B * Hkv * N (B * H * Nq) and max_pages * page_size at most 2^31 - 1,
+ *   N at most 2^30
  * These arrays are read on the device, so the host cannot refuse a bad entry:
  * the kernels check each one, skip what it points to (a token is not written,
  * a row not read, the keys of that page not attended to; lengths are clamped
