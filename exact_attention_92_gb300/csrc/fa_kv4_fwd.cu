@@ -3,9 +3,10 @@
 // A unit is a (sequence, key/value head, block of 8 or 16 of the group's query
 // rows); its keys are walked in steps of 32.  The steps of all units form one
 // list, in the order of the units, of which every CTA takes an equal stretch
-// whatever the sequences' lengths; the warps of a CTA take its steps in turn.
-// A unit that a border between two CTAs cuts leaves fp32 partial results, which
-// a second kernel merges in a fixed order.
+// whatever the sequences' lengths, and every warp of it an equal stretch of
+// that.  Where a border cuts a unit, the warps of a CTA join their fp32 results
+// at the CTA's end, and a second kernel merges those of the CTAs, both in the
+// order of the list.
 //
 // Each warp fetches its own steps: bulk copies of whole 16-token blocks into a
 // ring in shared memory, ahead of use, so no warp waits for another within a
@@ -76,15 +77,18 @@ struct Piece {
   int b, u, head;  // sequence; unit within it; key/value head
   int len, steps;  // of the sequence, of each of its units
   int lo, hi;      // steps to do
+  int place;       // of the unit in the list
 };
 
-// What a warp leaves to be joined with its neighbours' results.
+// A part of a unit that a warp leaves to be joined with its neighbours'.
+struct Part {
+  int row, rows;   // the unit's rows in [B, H, Nq]
+  int place;       // of the unit in the list
+  int steps;       // of the unit
+};
 struct Left {
-  int head;        // 1: the end or the middle of a unit that began before; 2: the end
-  int tail;        // 1: the beginning of a unit that goes on
-  int row, rows;   // rows of the tail's unit, or of the head's where there is no tail
-  int head_row, head_rows;
-  int past;        // one past the last step of the tail's unit, in the list
+  int kinds;       // bit 0: a unit's beginning (tail); bits 1, 2: a middle or an end (head), an end
+  Part head, tail;
 };
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -181,6 +185,12 @@ __device__ __forceinline__ float largest_scale(const uint32_t* w) {
 }
 __device__ __forceinline__ float scale_of(const uint32_t* w, int i) { return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]); }
 
+// Place of the n-th bit that is set (n from 0).
+__device__ __forceinline__ int nth_bit(uint32_t x, int n) {
+  for (; n > 0; --n) x &= x - 1;
+  return __ffs(x) - 1;
+}
+
 }  // namespace
 
 template <int D, int NR>
@@ -198,14 +208,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
   __shared__ int lims[W * C::kRows];
   __shared__ int lens[C::kLens];
   __shared__ int warp_sum[W];
-  __shared__ int found[2][4];
-  // Chains of results to be joined: the warps [from, past) whose heads belong
-  // to it, the tail that begins it (or -1), and where its rows are.
-  struct Chain {
-    int tail, from, past, ends, row, rows;
-  };
-  __shared__ Chain chains[W + 1];
-  __shared__ int n_chains;
+  __shared__ int run_end[C::kThreads];
 
   // Through a shuffle, so that what follows from it stays in uniform registers.
   auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
@@ -213,8 +216,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
   const int units = p.c.Hkv * p.row_blocks;  // of a sequence
   const WaitCtl ctl{p.c.status, p.timeout_ns};
 
-  if (tid < W * C::kStages) {
-    mbar_init(&bars[tid], 1);
+  if (lane < C::kStages) {  // each warp its own
+    mbar_init(&bars[warp * C::kStages + lane], 1);
     fence_barrier_init();
   }
   pdl_wait();
@@ -227,111 +230,104 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     return n == 0 ? 1 : (n + C::kKeys - 1) / C::kKeys;
   };
 
-  // ---- this CTA's stretch [first, end) of the list (the host has checked
-  // that its places fit 31 bits).  Each thread adds up a run of sequences.
+  // ---- the list (the host has checked that its places fit 31 bits): each
+  // thread adds up a run of sequences, and each warp looks up what it needs.
   const int run = (p.c.B + C::kThreads - 1) / C::kThreads;
-  const int b0 = min(p.c.B, tid * run), b1 = min(p.c.B, b0 + run);
   const bool keep = p.c.B <= C::kLens;
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) {
+  int upto = 0;
+  for (int b = tid * run; b < min(p.c.B, tid * run + run); ++b) {
     const int n = kv4_length(p.c, p.lens, b);
     if (keep) lens[b] = n;
-    mine += kUnitCost + steps_of(n);
+    upto += kUnitCost + steps_of(n);
   }
-  int upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += x;
   }
-  if (lane == 31) warp_sum[warp] = upto;
-  if (tid == 0) n_chains = 0;
   if (tid == 0 && !p.whole) p.cuts[blockIdx.x].row = -1;
+  run_end[tid] = upto;
+  if (lane == 31) warp_sum[warp] = upto;
   __syncthreads();
-  int total = 0;
+  int sums = lane < W ? warp_sum[lane] : 0;  // lane w: up to warp w's end
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    const int x = warp_sum[w];
-    if (w < warp) upto += x;
-    total += x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += x;
   }
-  total *= units;
-  // CTAs that take part: two places for every warp, or a unit each.
+  const int total = __shfl_sync(0xffffffffu, sums, 31) * units;
+  int base_b = 0;
+  auto length = [&](int b) {
+    return uniform((unsigned)(b - base_b) < (unsigned)C::kLens && (keep || base_b > 0) ? lens[b - base_b]
+                                                                                      : kv4_length(p.c, p.lens, b));
+  };
+  // Sequence, unit, place within it and places of the unit at list place x.
+  struct Found {
+    int b, u, off, places;
+  };
+  auto find = [&](int x) {
+    Found f;
+    const int w = min(__ffs(__ballot_sync(0xffffffffu, sums * units > x)) - 1, W - 1);
+    const int before_w = w > 0 ? __shfl_sync(0xffffffffu, sums, w - 1) : 0;
+    const int in_w = run_end[w * 32 + lane];
+    const int r = __ffs(__ballot_sync(0xffffffffu, (before_w + in_w) * units > x)) - 1;
+    const int before = before_w + (r > 0 ? __shfl_sync(0xffffffffu, in_w, r - 1) : 0);
+    int rest = x - before * units;
+    f.b = (w * 32 + r) * run;
+    f.places = kUnitCost + steps_of(length(f.b));
+    while (rest >= f.places * units && f.b + 1 < p.c.B) {
+      rest -= f.places * units;
+      f.places = kUnitCost + steps_of(length(++f.b));
+    }
+    f.u = rest / f.places;
+    f.off = rest - f.u * f.places;
+    return f;
+  };
+  // CTAs that take part: two places for every warp, or a unit each.  The first
+  // `more` have a place more than the others.
   const int active = min((int)gridDim.x, max(total / (2 * W), p.c.B * units));
   if ((int)blockIdx.x >= active) return;
-  // The first `more` CTAs have a place more than the others.
   const int each = total / active, more = total - each * active;
+  auto cta_of = [&](int place) {
+    return place < more * (each + 1) ? place / (each + 1) : more + (place - more * (each + 1)) / each;
+  };
   int first = (int)blockIdx.x * each + min((int)blockIdx.x, more);
   int end = first + each + ((int)blockIdx.x < more ? 1 : 0);
-  // Sequence, unit, place within it and places of the unit at list place x.
-  auto find = [&](int x, int* f) {
-    if (mine > 0 && (upto - mine) * units <= x && x < upto * units) {
-      int rest = x - (upto - mine) * units, b = b0;
-      int n = kUnitCost + steps_of(keep ? lens[b] : kv4_length(p.c, p.lens, b));
-      while (rest >= n * units && b + 1 < b1) {
-        rest -= n * units;
-        ++b;
-        n = kUnitCost + steps_of(keep ? lens[b] : kv4_length(p.c, p.lens, b));
-      }
-      f[0] = b;
-      f[1] = rest / n;
-      f[2] = rest - f[1] * n;
-      f[3] = n;
+  if (p.whole) {  // the units that begin in the stretch
+    const Found f = find(first);
+    if (f.off > 0) first += f.places - f.off;
+    if (end < total) {
+      const Found e = find(end);
+      if (e.off > 0) end += e.places - e.off;
     }
-  };
-  find(first, found[0]);
-  if (p.whole && end < total) find(end, found[1]);
-  __syncthreads();
-  int at_b = uniform(found[0][0]), at_u = uniform(found[0][1]), at_off = uniform(found[0][2]);
-  if (p.whole) {  // units that begin in the stretch
-    if (at_off > 0) {
-      first += uniform(found[0][3]) - at_off;
-      at_off = 0;
-      if (++at_u == units) {
-        at_u = 0;
-        ++at_b;
-      }
-    }
-    if (end < total && found[1][2] > 0) end += uniform(found[1][3] - found[1][2]);
   }
   if (first >= end) return;
-  const int base_b = keep ? 0 : at_b;
   if (!keep) {
-    for (int i = tid; i < C::kLens && base_b + i < p.c.B; i += C::kThreads)
-      lens[i] = kv4_length(p.c, p.lens, base_b + i);
+    const int b0 = find(first).b;
+    for (int i = tid; i < C::kLens && b0 + i < p.c.B; i += C::kThreads) lens[i] = kv4_length(p.c, p.lens, b0 + i);
     __syncthreads();
+    base_b = b0;
   }
-  auto length = [&](int b) { return uniform(b - base_b < C::kLens ? lens[b - base_b] : kv4_length(p.c, p.lens, b)); };
 
   // ---- this warp's stretch of it, walked by the copies
   const int warp_each = (end - first) / W, warp_more = (end - first) - warp_each * W;
   int at = first + warp * warp_each + min(warp, warp_more);
   const int my_end = at + warp_each + (warp < warp_more ? 1 : 0);
-  int skip = at - first + at_off;  // places from the beginning of unit at_u
   Piece ahead;
-  ahead.b = at_b;
-  ahead.u = at_u;
+  ahead.lo = ahead.hi = 0;
   const int* row = nullptr;  // of the block table
   auto sequence = [&] {
     ahead.len = length(ahead.b);
     ahead.steps = steps_of(ahead.len);
     row = p.c.table + (size_t)ahead.b * p.c.max_pages;
   };
-  sequence();
-  while (skip >= (units - ahead.u) * (kUnitCost + ahead.steps) && ahead.b + 1 < p.c.B) {
-    skip -= (units - ahead.u) * (kUnitCost + ahead.steps);
-    ahead.u = 0;
-    ++ahead.b;
-    sequence();
-  }
-  const int jump = skip / (kUnitCost + ahead.steps);
-  ahead.u += jump;
   int made = 0, taken = 0;  // pieces put into the queue, and taken out
   auto enter = [&](int off) {
     ahead.head = p.row_blocks == 1 ? ahead.u : ahead.u / p.row_blocks;
     const int upto_off = min(ahead.steps + kUnitCost, off + my_end - at);
     ahead.lo = max(0, off - kUnitCost);
     ahead.hi = max(ahead.lo, upto_off - kUnitCost);
+    ahead.place = at - off;
     at += upto_off - off;
     if (ahead.lo < ahead.hi) {
       if (lane == 0) queue[warp * kQueue + made % kQueue] = ahead;
@@ -352,8 +348,13 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     }
     enter(0);
   };
-  ahead.lo = ahead.hi = 0;
-  if (at < my_end) enter(skip - jump * (kUnitCost + ahead.steps));
+  if (at < my_end) {
+    const Found f = find(at);
+    ahead.b = f.b;
+    ahead.u = f.u;
+    sequence();
+    enter(f.off);
+  }
 
   // A copy takes the blocks of a step that lie in one page, all of them where
   // pages are long enough; lane i issues the step's copy i, whose page it has
@@ -386,7 +387,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     if (++ahead.lo == ahead.hi) next_unit();
     look_up();
   };
-  if (ahead.lo == ahead.hi) next_unit();  // only the cost of a unit's beginning was left of it
   look_up();
 #pragma unroll 1
   for (int s = 0; s < C::kStages; ++s) issue(s);
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
   bool ok = true;
   int stage = 0;
   uint32_t phase = 0;
-  Left mine_left = {};
+  Left mine = {};
 
   // ---- units
   while (taken < made) {
@@ -667,61 +667,50 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
                 make_float4(o[r][i][0][c], o[r][i][0][c + 2], o[r][i][1][c], o[r][i][1][c + 2]);
           if (g == 0) stats[starts ? 1 : 0][warp * C::kRows + col] = make_float2(ref[r][c], l[r][c]);
         }
+      const Part part{row_at, n_rows, uniform(now.place), uniform(now.steps)};
       if (starts) {
-        mine_left.tail = 1;
-        mine_left.row = row_at;
-        mine_left.rows = n_rows;
-        mine_left.past = my_end - s1 + now.steps;
+        mine.kinds |= 1;
+        mine.tail = part;
       } else {
-        mine_left.head = ends ? 2 : 1;
-        mine_left.head_row = row_at;
-        mine_left.head_rows = n_rows;
+        mine.kinds |= ends ? 6 : 2;
+        mine.head = part;
       }
     }
   }
-  if (lane == 0) left[warp] = mine_left;
+  if (lane == 0) left[warp] = mine;
   __syncthreads();
 
-  // ---- join what the warps have left: a chain begins with a warp's tail, or
+  // ---- join what the warps have left.  A chain begins with a warp's tail, or
   // goes on from the CTA before, and takes the heads of the warps behind it
-  // until the unit's end.
-  if (warp == 0 && lane <= W) {
-    Chain c;
-    c.tail = lane - 1;
-    c.from = lane;
-    c.ends = 0;
-    bool is = false;
-    if (lane > 0) {
-      is = left[lane - 1].tail != 0;
-      c.row = left[lane - 1].row;
-      c.rows = left[lane - 1].rows;
-    } else {
-      while (c.from < W && left[c.from].head == 0 && left[c.from].tail == 0) ++c.from;  // no step, or whole units
-      if (c.from < W && left[c.from].head != 0) {
-        is = true;
-        c.row = left[c.from].head_row;
-        c.rows = left[c.from].head_rows;
-      }
-    }
-    if (is) {
-      c.past = c.from;
-      while (c.past < W && !c.ends) c.ends = left[c.past++].head == 2;
-    }
-    const uint32_t who = __ballot_sync((1u << (W + 1)) - 1, is);
-    if (is) chains[__popc(who & ((1u << lane) - 1))] = c;
-    if (lane == 0) n_chains = __popc(who);
-  }
-  __syncthreads();
+  // until the unit's end.  Lane c of every warp works out chain c: that from
+  // warp c - 1's tail, or for lane 0 the one from the CTA before.
+  const int kinds = lane < W ? left[lane].kinds : 0;
+  const uint32_t tails = __ballot_sync(0xffffffffu, kinds & 1), heads = __ballot_sync(0xffffffffu, kinds & 2),
+                 stops = __ballot_sync(0xffffffffu, kinds & 4);
+  const int first_left = __ffs(heads | tails) - 1;
+  bool is = lane > 0 ? lane <= W && ((tails >> (lane - 1)) & 1) : first_left >= 0 && ((heads >> first_left) & 1);
+  const int from = lane;                                     // warps [from, past): their heads belong to it
+  const uint32_t ahead_stops = from < W ? stops >> from : 0u;
+  const bool stopped = ahead_stops != 0;
+  const int past = stopped ? from + __ffs(ahead_stops) : W;
+  Part whose{};
+  if (is) whose = lane > 0 ? left[lane - 1].tail : left[first_left].head;
+  const uint32_t chains = __ballot_sync(0xffffffffu, is);
+  // The chains that other CTAs have parts of: from the one before, into the next.
+  const uint32_t open = __ballot_sync(0xffffffffu, is && (lane == 0 || !stopped));
+
   // A warp takes a row of a chain at a time.
-  for (int j = warp; j < n_chains * C::kRows; j += W) {
-    const Chain c = chains[j / C::kRows];
-    const int col = j % C::kRows;
-    if (col >= c.rows) continue;
-    const bool starts = c.tail >= 0;
+  for (int j = warp; j < __popc(chains) * C::kRows; j += W) {
+    const int chain = nth_bit(chains, j / C::kRows), col = j % C::kRows;
+    const int c_rows = __shfl_sync(0xffffffffu, whose.rows, chain);
+    if (col >= c_rows) continue;
+    const int c_row = __shfl_sync(0xffffffffu, whose.row, chain);
+    const int c_past = __shfl_sync(0xffffffffu, past, chain);
+    const uint32_t parts = heads & ((1u << c_past) - 1) & ~((1u << chain) - 1);
     // Lane w has warp w's reference, sum and factor; lane 31 the tail's.
     float2 ml = make_float2(-3.402823466e38f, 0.f);
-    if (lane >= c.from && lane < c.past && left[lane].head != 0) ml = stats[0][lane * C::kRows + col];
-    if (lane == 31 && starts) ml = stats[1][c.tail * C::kRows + col];
+    if ((parts >> lane) & 1) ml = stats[0][lane * C::kRows + col];
+    if (lane == 31 && chain > 0) ml = stats[1][(chain - 1) * C::kRows + col];
     float m = ml.x;
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -731,47 +720,41 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     constexpr int kMany = (D / 4 + 31) / 32;
     float4 x[kMany];
-    auto add = [&](const uint8_t* part, float by, bool there) {
+    auto add = [&](const uint8_t* part, float by) {
       const float4* const src = reinterpret_cast<const float4*>(part) + col * (D / 4);
 #pragma unroll
       for (int i = 0; i < kMany; ++i) {
-        const int quad = min(32 * i + lane, D / 4 - 1);
-        const float4 y = src[quad ^ (col & 6)];
-        x[i].x = there ? fmaf(y.x, by, x[i].x) : x[i].x;
-        x[i].y = there ? fmaf(y.y, by, x[i].y) : x[i].y;
-        x[i].z = there ? fmaf(y.z, by, x[i].z) : x[i].z;
-        x[i].w = there ? fmaf(y.w, by, x[i].w) : x[i].w;
+        const float4 y = src[min(32 * i + lane, D / 4 - 1) ^ (col & 6)];
+        x[i].x = fmaf(y.x, by, x[i].x);
+        x[i].y = fmaf(y.y, by, x[i].y);
+        x[i].z = fmaf(y.z, by, x[i].z);
+        x[i].w = fmaf(y.w, by, x[i].w);
       }
     };
 #pragma unroll
     for (int i = 0; i < kMany; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (starts) add(smem + c.tail * C::kRing, __shfl_sync(0xffffffffu, f, 31), true);
-#pragma unroll 4
-    for (int w = c.from; w < c.past; ++w)
-      add(smem + W * C::kRing + w * C::kSums, __shfl_sync(0xffffffffu, f, w), left[w].head != 0);
-    if (starts && c.ends) {
+    if (chain > 0) add(smem + (chain - 1) * C::kRing, __shfl_sync(0xffffffffu, f, 31));
+    for (uint32_t todo = parts; todo != 0; todo &= todo - 1) {
+      const int w = __ffs(todo) - 1;
+      add(smem + W * C::kRing + w * C::kSums, __shfl_sync(0xffffffffu, f, w));
+    }
+    if (!((open >> chain) & 1)) {
       const float inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
       for (int i = 0; i < kMany; ++i)
         if (32 * i + lane < D / 4)
-          *reinterpret_cast<uint2*>(p.o + (size_t)(c.row + col) * D + 4 * (32 * i + lane)) =
+          *reinterpret_cast<uint2*>(p.o + (size_t)(c_row + col) * D + 4 * (32 * i + lane)) =
               make_uint2(pack_bf16(x[i].x * inv, x[i].y * inv), pack_bf16(x[i].z * inv, x[i].w * inv));
-      if (lane == 0) p.lse[c.row + col] = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * 0.69314718055994530942f;
+      if (lane == 0) p.lse[c_row + col] = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * 0.69314718055994530942f;
     } else {
-      // The unit goes on in another CTA.
-      const size_t slot = (size_t)(2 * blockIdx.x + (starts ? 1 : 0)) * C::kRows + col;
+      const size_t slot = (size_t)(2 * blockIdx.x + (chain > 0 ? 1 : 0)) * C::kRows + col;
 #pragma unroll
       for (int i = 0; i < kMany; ++i)
         if (32 * i + lane < D / 4) reinterpret_cast<float4*>(p.part_o + slot * D)[32 * i + lane] = x[i];
       if (lane == 0) p.part_ml[slot] = make_float2(m, sum);
-      if (starts && col == 0 && lane == 0) {
-        const int last = left[c.tail].past - 1;  // place of the unit's last step
-        Kv4Cut cut;
-        cut.row = c.row;
-        cut.rows = c.rows;
-        cut.last = last < more * (each + 1) ? last / (each + 1) : more + (last - more * (each + 1)) / each;
-        cut.pad = 0;
-        p.cuts[blockIdx.x] = cut;
+      if (chain > 0 && col == 0) {
+        const int place = __shfl_sync(0xffffffffu, whose.place, chain), steps = __shfl_sync(0xffffffffu, whose.steps, chain);
+        if (lane == 0) p.cuts[blockIdx.x] = Kv4Cut{c_row, c_rows, cta_of(place + kUnitCost + steps - 1), 0};
       }
     }
   }
