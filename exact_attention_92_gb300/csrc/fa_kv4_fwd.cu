@@ -59,7 +59,6 @@ struct Cfg {
   static constexpr int kStages = D == 256 || (D == 128 && NR == 1) ? 2 : 3;
   static constexpr int kStageBytes = kBlocks * Kv4<D>::kBlockBytes;
   static constexpr int kRows = NR * kKv4Rows;
-  static constexpr int kLens = 1024;                            // sequence lengths kept in shared memory
   // Shared memory: a ring of steps and the sums of a unit's head for each
   // warp (the sums of a tail go to the ring, which is empty by then).
   static constexpr int kRing = kStages * kStageBytes;
@@ -206,9 +205,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
   __shared__ Left left[W];
   __shared__ float2 stats[2][W * C::kRows];  // reference and sum of heads, of tails
   __shared__ int lims[W * C::kRows];
-  __shared__ int lens[C::kLens];
-  __shared__ int warp_sum[W];
-  __shared__ int run_end[C::kThreads];
 
   // Through a shuffle, so that what follows from it stays in uniform registers.
   auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
@@ -230,50 +226,29 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     return n == 0 ? 1 : (n + C::kKeys - 1) / C::kKeys;
   };
 
-  // ---- the list (the host has checked that its places fit 31 bits): each
-  // thread adds up a run of sequences, and each warp looks up what it needs.
-  const int run = (p.c.B + C::kThreads - 1) / C::kThreads;
-  const bool keep = p.c.B <= C::kLens;
+  // ---- the list (the host has checked that its places fit 31 bits).  Every
+  // warp works it out for itself, each lane adding up a run of sequences: the
+  // warps need not wait for each other before their copies are on the way.
+  auto length = [&](int b) { return kv4_length(p.c, p.lens, b); };
+  const int run = (p.c.B + 31) / 32;
   int upto = 0;
-  for (int b = tid * run; b < min(p.c.B, tid * run + run); ++b) {
-    const int n = kv4_length(p.c, p.lens, b);
-    if (keep) lens[b] = n;
-    upto += kUnitCost + steps_of(n);
-  }
+  for (int b = lane * run; b < min(p.c.B, lane * run + run); ++b) upto += kUnitCost + steps_of(length(b));
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += x;
   }
+  const int total = __shfl_sync(0xffffffffu, upto, 31) * units;
   if (tid == 0 && !p.whole) p.cuts[blockIdx.x].row = -1;
-  run_end[tid] = upto;
-  if (lane == 31) warp_sum[warp] = upto;
-  __syncthreads();
-  int sums = lane < W ? warp_sum[lane] : 0;  // lane w: up to warp w's end
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, sums, o);
-    if (lane >= o) sums += x;
-  }
-  const int total = __shfl_sync(0xffffffffu, sums, 31) * units;
-  int base_b = 0;
-  auto length = [&](int b) {
-    return uniform((unsigned)(b - base_b) < (unsigned)C::kLens && (keep || base_b > 0) ? lens[b - base_b]
-                                                                                      : kv4_length(p.c, p.lens, b));
-  };
   // Sequence, unit, place within it and places of the unit at list place x.
   struct Found {
     int b, u, off, places;
   };
   auto find = [&](int x) {
     Found f;
-    const int w = min(__ffs(__ballot_sync(0xffffffffu, sums * units > x)) - 1, W - 1);
-    const int before_w = w > 0 ? __shfl_sync(0xffffffffu, sums, w - 1) : 0;
-    const int in_w = run_end[w * 32 + lane];
-    const int r = __ffs(__ballot_sync(0xffffffffu, (before_w + in_w) * units > x)) - 1;
-    const int before = before_w + (r > 0 ? __shfl_sync(0xffffffffu, in_w, r - 1) : 0);
-    int rest = x - before * units;
-    f.b = (w * 32 + r) * run;
+    const int r = __ffs(__ballot_sync(0xffffffffu, upto * units > x)) - 1;
+    int rest = x - (r > 0 ? __shfl_sync(0xffffffffu, upto, r - 1) * units : 0);
+    f.b = r * run;
     f.places = kUnitCost + steps_of(length(f.b));
     while (rest >= f.places * units && f.b + 1 < p.c.B) {
       rest -= f.places * units;
@@ -302,13 +277,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     }
   }
   if (first >= end) return;
-  if (!keep) {
-    const int b0 = find(first).b;
-    for (int i = tid; i < C::kLens && b0 + i < p.c.B; i += C::kThreads) lens[i] = kv4_length(p.c, p.lens, b0 + i);
-    __syncthreads();
-    base_b = b0;
-  }
-
   // ---- this warp's stretch of it, walked by the copies
   const int warp_each = (end - first) / W, warp_more = (end - first) - warp_each * W;
   int at = first + warp * warp_each + min(warp, warp_more);
@@ -317,7 +285,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
   ahead.lo = ahead.hi = 0;
   const int* row = nullptr;  // of the block table
   auto sequence = [&] {
-    ahead.len = length(ahead.b);
+    ahead.len = uniform(length(ahead.b));
     ahead.steps = steps_of(ahead.len);
     row = p.c.table + (size_t)ahead.b * p.c.max_pages;
   };
@@ -362,34 +330,42 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
   uint8_t* const ring = smem + warp * C::kRing;
   uint64_t* const bar = bars + warp * C::kStages;
   const int copy_blocks = min(C::kBlocks, 1 << (p.c.page_shift - 4));
-  const bool copies = lane * copy_blocks < C::kBlocks;
+  const uint32_t copy_bytes = copy_blocks * F::kBlockBytes;
+  const int my_key = lane * copy_blocks * kKv4Block;  // of this lane's copy in a step; past the step: no copy
   const uint32_t have_all = (1u << (C::kBlocks / copy_blocks)) - 1;
-  uint32_t have = 0;  // copies that were made, four bits a stage
-  int page = -1;
+  const int page_mask = (1 << p.c.page_shift) - 1;
+  const uint32_t page_bytes = (uint32_t)F::kBlockBytes << (p.c.page_shift - 4);
+  uint32_t have = 0;  // copies that were made, kBlocks bits a stage, the newest stage in the lowest
+  int page = -1;      // of this lane's copy of the step at ahead.lo, -1: none
   auto look_up = [&] {
-    const int pos = ahead.lo * C::kKeys + lane * copy_blocks * kKv4Block;
+    const int pos = ahead.lo * C::kKeys + my_key;
     page = -1;
-    if (copies && ahead.lo < ahead.hi && pos < ahead.len) page = row[pos >> p.c.page_shift];
+    if (my_key < C::kKeys && pos < ahead.len && ahead.lo < ahead.hi) page = row[pos >> p.c.page_shift];
   };
   auto issue = [&](int stage) {
     if (ahead.lo == ahead.hi) return;
-    const int pos = ahead.lo * C::kKeys + lane * copy_blocks * kKv4Block;
-    const bool want = copies && pos < ahead.len;
-    const bool good = want && (unsigned)page < (unsigned)p.c.num_pages;
-    if (want && !good) kv4_bad_index(p.c);
+    const int pos = ahead.lo * C::kKeys + my_key;
+    bool good = (unsigned)page < (unsigned)p.c.num_pages;
+    if (!good && my_key < C::kKeys && pos < ahead.len) kv4_bad_index(p.c);
     const uint32_t ones = __ballot_sync(0xffffffffu, good);
-    have = (have & ~(15u << (4 * stage))) | (ones << (4 * stage));
-    if (lane == 0) mbar_arrive_expect_tx(&bar[stage], __popc(ones) * copy_blocks * F::kBlockBytes);
+    have = (have << C::kBlocks) | ones;
+    if (lane == 0) mbar_arrive_expect_tx(&bar[stage], __popc(ones) * copy_bytes);
     __syncwarp();
     if (good)
-      bulk_load(ring + stage * C::kStageBytes + lane * copy_blocks * F::kBlockBytes,
-                kv4_block<D>(p.c, page, ahead.head, pos), copy_blocks * F::kBlockBytes, &bar[stage]);
+      bulk_load(ring + stage * C::kStageBytes + lane * copy_bytes,
+                p.c.pages + ((size_t)page * p.c.Hkv + ahead.head) * page_bytes +
+                    ((pos & page_mask) / kKv4Block) * F::kBlockBytes,
+                copy_bytes, &bar[stage]);
     if (++ahead.lo == ahead.hi) next_unit();
     look_up();
   };
   look_up();
+  int in_flight = 0;  // stages issued and not yet waited for
 #pragma unroll 1
-  for (int s = 0; s < C::kStages; ++s) issue(s);
+  for (int s = 0; s < C::kStages; ++s) {
+    in_flight += ahead.lo < ahead.hi ? 1 : 0;
+    issue(s);
+  }
 
   bool ok = true;
   int stage = 0;
@@ -612,13 +588,14 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
       ok = __all_sync(0xffffffffu, mbar_wait(&bar[stage], phase, ctl, kWaitKvFull));
       if (!ok) break;
       const uint8_t* const st = ring + stage * C::kStageBytes;
-      const uint32_t there = (have >> (4 * stage)) & 15u;
+      const uint32_t there = (have >> (C::kBlocks * --in_flight)) & ((1u << C::kBlocks) - 1);
       const int key0 = s * C::kKeys;
       if (key0 + C::kKeys <= low && there == have_all)
         step(std::false_type{}, st, key0, there);
       else
         step(std::true_type{}, st, key0, there);
       __syncwarp();  // every lane has read the stage
+      in_flight += ahead.lo < ahead.hi ? 1 : 0;
       issue(stage);
       if (++stage == C::kStages) {
         stage = 0;
