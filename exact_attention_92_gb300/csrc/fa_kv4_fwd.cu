@@ -49,7 +49,7 @@ using namespace dev;
 
 namespace {
 
-template <int D, int NR>
+template <int D, int NR, bool PACK>
 struct Cfg {
   // One CTA an SM; its warps as many as their registers allow.
   static constexpr int kWarps = NR == 1 && D < 256 ? (D == 64 ? 16 : 12) : 8;
@@ -58,7 +58,8 @@ struct Cfg {
   static constexpr int kKeys = kBlocks * kKv4Block;
   static constexpr int kStages = D == 256 || (D == 128 && NR == 1) ? 2 : 3;
   static constexpr int kStageBytes = kBlocks * Kv4<D>::kBlockBytes;
-  static constexpr int kRows = NR * kKv4Rows;
+  static constexpr int kRows = PACK ? kKv4Rows / 2 : NR * kKv4Rows;  // query rows of a unit
+  static_assert(!PACK || (NR == 1 && kBlocks == 2), "two blocks share the columns of a tile");
   // Shared memory: a ring of steps and the sums of a unit's head for each
   // warp (the sums of a tail go to the ring, which is empty by then).
   static constexpr int kRing = kStages * kStageBytes;
@@ -192,10 +193,10 @@ __device__ __forceinline__ int nth_bit(uint32_t x, int n) {
 
 }  // namespace
 
-template <int D, int NR>
-__global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const Kv4FwdParams p) {
+template <int D, int NR, bool PACK>
+__global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(const Kv4FwdParams p) {
   using F = Kv4<D>;
-  using C = Cfg<D, NR>;
+  using C = Cfg<D, NR, PACK>;
   constexpr int NG = F::kGroups, W = C::kWarps;
   constexpr int kQueue = 8;  // pieces between the copies and the products
   static_assert(kQueue >= C::kStages + 2, "a piece has a step at least");
@@ -209,6 +210,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
   // Through a shuffle, so that what follows from it stays in uniform registers.
   auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
   const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32, g = lane / 4, t = lane % 4;
+  // Columns col0, col0 + 1 of a tile are this lane's query rows; where two blocks
+  // share a tile, they are those of block my_blk.
+  const int col0 = PACK ? 2 * (t & 1) : 2 * t, my_blk = PACK ? t >> 1 : 0;
   const int units = p.c.Hkv * p.row_blocks;  // of a sequence
   const WaitCtl ctl{p.c.status, p.timeout_ns};
 
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     const int row_at = uniform((now.b * p.c.Hkv + now.head) * p.rows + row0);  // in [B, H, Nq]
     ++taken;
 
-    uint32_t q[NR][NG][4];  // as the column operand
+    uint32_t q[PACK ? 2 : NR][NG][4];  // as the column operand (PACK: for each block, in its half of the columns)
     float cc[NR][2];        // what turns the sums of columns 2 t, 2 t + 1 into base-2 scores
     int low = len;          // keys that all rows see
 #pragma unroll
@@ -393,8 +397,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         raw[i] = make_uint4(0, 0, 0, 0);
-        if (r * 8 + g < n_rows)
-          raw[i] = *reinterpret_cast<const uint4*>(p.q + (size_t)(row_at + r * 8 + g) * D + 32 * i + 8 * t);
+        const int row = PACK ? g & 3 : r * 8 + g;
+        if (row < n_rows) raw[i] = *reinterpret_cast<const uint4*>(p.q + (size_t)(row_at + row) * D + 32 * i + 8 * t);
       }
       float top = 0.f;
 #pragma unroll
@@ -413,11 +417,19 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
       for (int i = 0; i < NG; ++i) {
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q[r][i][k] = pack_f16(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = pack_f16(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
+          if constexpr (PACK) {
+            q[0][i][k] = g < 4 ? x : 0u;
+            q[1][i][k] = g < 4 ? 0u : x;
+          } else {
+            q[r][i][k] = x;
+          }
+        }
       }
       const float back = p.scale_log2 / up;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) cc[r][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c));
+      for (int c = 0; c < 2; ++c) cc[r][c] = __shfl_sync(0xffffffffu, back, 4 * (col0 + c));
     }
     // Keys that each row sees; padding rows see all.
     if (p.causal != FA_CAUSAL_NONE) {
@@ -449,42 +461,61 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
     // One step: MASK where some row does not see some of the keys.
     auto step = [&](auto mask, const uint8_t* const st, int key0, uint32_t there) {
       constexpr bool MASK = decltype(mask)::value;
-      // Keys g and g + 8 of each block, columns 2 t and 2 t + 1: scores as the
-      // matrix products have them (to be multiplied by cc).
-      float sc[C::kBlocks][NR][4];
+      // Keys g and g + 8 of a block, this lane's columns: scores as the matrix
+      // products have them (to be multiplied by cc).  PACK: tile 0 holds both
+      // blocks, the query rows once in its columns 0-3 for block 0 and once in
+      // 4-7 for block 1, so that a lane has scores of one block only.
+      constexpr int NS = PACK ? 1 : C::kBlocks;
+      float sc[NS][NR][4];
       float top[NR][2];  // largest score + log2(largest scale of the value)
 #pragma unroll
       for (int r = 0; r < NR; ++r) top[r][0] = top[r][1] = -INFINITY;
-      auto seen = [&](int k, int r, int x) {
-        return key0 + k * kKv4Block + g + (x & 2) * 4 < lims[warp * C::kRows + r * 8 + 2 * t + (x & 1)] && ((there >> (k / copy_blocks)) & 1) != 0;
+      auto seen = [&](int s, int r, int x) {
+        const int k = PACK ? my_blk : s;
+        return key0 + k * kKv4Block + g + (x & 2) * 4 < lims[warp * C::kRows + r * 8 + col0 + (x & 1)] &&
+               ((there >> (k / copy_blocks)) & 1) != 0;
       };
 #pragma unroll
-      for (int k = 0; k < C::kBlocks; ++k) {
-        const uint8_t* const blk = st + k * F::kBlockBytes;
-        uint32_t ka[NG], kb[NG], wa[NG], wb[NG];
-        load_key<D>(blk, g, t, ka);
-        load_key<D>(blk, g + 8, t, kb);
+      for (int s = 0; s < NS; ++s) {
+        const uint8_t* const blk = st + (PACK ? my_blk : s) * F::kBlockBytes;
+        uint32_t wa[NG], wb[NG];
         load_scales<D>(blk, g, wa);
         load_scales<D>(blk, g + 8, wb);
+        constexpr int NK = PACK ? C::kBlocks : 1;  // blocks of the tile
+        uint32_t ka[NK][NG], kb[NK][NG];
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          load_key<D>(st + (PACK ? k : s) * F::kBlockBytes, g, t, ka[k]);
+          load_key<D>(st + (PACK ? k : s) * F::kBlockBytes, g + 8, t, kb[k]);
+        }
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) sc[k][r][x] = 0.f;
+          for (int x = 0; x < 4; ++x) sc[s][r][x] = 0.f;
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          uint32_t ha[4], hb[4];
-          kv4_decode8(ka[i], ha);
-          kv4_decode8(kb[i], hb);
+          float c[NR][4];
+#pragma unroll
+          for (int r = 0; r < NR; ++r) c[r][0] = c[r][1] = c[r][2] = c[r][3] = 0.f;
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            uint32_t ha[4], hb[4];
+            kv4_decode8(ka[k][i], ha);
+            kv4_decode8(kb[k][i], hb);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const uint32_t* const b = q[PACK ? k : r][i];
+              mma16816(c[r], ha[0], hb[0], ha[1], hb[1], b[0], b[1]);
+              mma16816(c[r], ha[2], hb[2], ha[3], hb[3], b[2], b[3]);
+            }
+          }
           const float fa_ = scale_of(wa, i), fb_ = scale_of(wb, i);
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(c, ha[0], hb[0], ha[1], hb[1], q[r][i][0], q[r][i][1]);
-            mma16816(c, ha[2], hb[2], ha[3], hb[3], q[r][i][2], q[r][i][3]);
-            sc[k][r][0] = fmaf(fa_, c[0], sc[k][r][0]);
-            sc[k][r][1] = fmaf(fa_, c[1], sc[k][r][1]);
-            sc[k][r][2] = fmaf(fb_, c[2], sc[k][r][2]);
-            sc[k][r][3] = fmaf(fb_, c[3], sc[k][r][3]);
+            sc[s][r][0] = fmaf(fa_, c[r][0], sc[s][r][0]);
+            sc[s][r][1] = fmaf(fa_, c[r][1], sc[s][r][1]);
+            sc[s][r][2] = fmaf(fb_, c[r][2], sc[s][r][2]);
+            sc[s][r][3] = fmaf(fb_, c[r][3], sc[s][r][3]);
           }
         }
         const float va = lg2_approx(largest_scale<NG>(wa)), vb = lg2_approx(largest_scale<NG>(wb));
@@ -492,10 +523,10 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
         for (int r = 0; r < NR; ++r)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float x = fmaf(sc[k][r][c], cc[r][c], va), y = fmaf(sc[k][r][c + 2], cc[r][c], vb);
+            float x = fmaf(sc[s][r][c], cc[r][c], va), y = fmaf(sc[s][r][c + 2], cc[r][c], vb);
             if constexpr (MASK) {
-              x = seen(k, r, c) ? x : -INFINITY;
-              y = seen(k, r, c + 2) ? y : -INFINITY;
+              x = seen(s, r, c) ? x : -INFINITY;
+              y = seen(s, r, c + 2) ? y : -INFINITY;
             }
             top[r][c] = fmax3(top[r][c], x, y);
           }
@@ -529,54 +560,74 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
         }
       }
 
-      // Weights, and O^T += V^T P^T.
+      // Weights, and O^T += V^T P^T.  PACK: columns 4-7 of O gather what block 1
+      // gives the same rows, and are added at the end.
 #pragma unroll
-      for (int k = 0; k < C::kBlocks; ++k) {
-        const uint8_t* const blk = st + k * F::kBlockBytes;
+      for (int s = 0; s < NS; ++s) {
+        const uint8_t* const blk = st + (PACK ? my_blk : s) * F::kBlockBytes;
         uint32_t wa[NG], wb[NG];
         load_scales<D>(blk, g, wa);
         load_scales<D>(blk, g + 8, wb);
-        constexpr int NW = (NG + 1) / 2;
-        uint32_t v0[NW], v1[NW], v2[NW], v3[NW];  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-        load_value<D>(blk, t, g, v0);
-        load_value<D>(blk, 4 + t, g, v1);
-        load_value<D>(blk, 8 + t, g, v2);
-        load_value<D>(blk, 12 + t, g, v3);
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            float y = ex2_approx(fmaf(sc[k][r][x], cc[r][x & 1], -ref[r][x & 1]));
-            if constexpr (MASK) y = seen(k, r, x) ? y : 0.f;
-            sc[k][r][x] = y;
+            float y = ex2_approx(fmaf(sc[s][r][x], cc[r][x & 1], -ref[r][x & 1]));
+            if constexpr (MASK) y = seen(s, r, x) ? y : 0.f;
+            sc[s][r][x] = y;
             l[r][x & 1] += y;
           }
+        constexpr int NW = (NG + 1) / 2, NK = PACK ? C::kBlocks : 1;
+        uint32_t v[NK][4][NW];  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) load_value<D>(st + (PACK ? k : s) * F::kBlockBytes, 4 * x + t, g, v[k][x]);
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
-          // Bytes of two tokens' codes for one channel: even channels, odd channels.
-          const uint32_t lo01 = (v0[j] & 0x0f0f0f0fu) | ((v1[j] << 4) & 0xf0f0f0f0u);
-          const uint32_t hi01 = ((v0[j] >> 4) & 0x0f0f0f0fu) | (v1[j] & 0xf0f0f0f0u);
-          const uint32_t lo23 = (v2[j] & 0x0f0f0f0fu) | ((v3[j] << 4) & 0xf0f0f0f0u);
-          const uint32_t hi23 = ((v2[j] >> 4) & 0x0f0f0f0fu) | (v3[j] & 0xf0f0f0f0u);
-          uint32_t a0[4], a1[4], a2[4], a3[4];
-          kv4_decode8(lo01, a0);
-          kv4_decode8(hi01, a1);
-          kv4_decode8(lo23, a2);
-          kv4_decode8(hi23, a3);
+          // Weights times the scales of this word's groups, as the column operand.
+          uint32_t b0[2][NR], b1[2][NR];
 #pragma unroll
-          for (int i = 2 * j; i < 2 * j + 2 && i < NG; ++i) {
+          for (int h = 0; h < 2; ++h) {
+            const int i = 2 * j + h;
+            if (i >= NG) continue;
             const float fa_ = scale_of(wa, NG + i), fb_ = scale_of(wb, NG + i);
-            const int y = 2 * (i & 1);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-              float x[4] = {sc[k][r][0] * fa_, sc[k][r][1] * fa_, sc[k][r][2] * fb_, sc[k][r][3] * fb_};
+              float x[4] = {sc[s][r][0] * fa_, sc[s][r][1] * fa_, sc[s][r][2] * fb_, sc[s][r][3] * fb_};
               if constexpr (MASK) {  // whatever the scale is
 #pragma unroll
-                for (int z = 0; z < 4; ++z) x[z] = seen(k, r, z) ? x[z] : 0.f;
+                for (int z = 0; z < 4; ++z) x[z] = seen(s, r, z) ? x[z] : 0.f;
               }
-              const uint32_t b0 = transpose8(pack_f16(x[0], x[1])), b1 = transpose8(pack_f16(x[2], x[3]));
-              mma16816(o[r][i][0], a0[y], a1[y], a2[y], a3[y], b0, b1);
-              mma16816(o[r][i][1], a0[y + 1], a1[y + 1], a2[y + 1], a3[y + 1], b0, b1);
+              b0[h][r] = transpose8(pack_f16(x[0], x[1]));
+              b1[h][r] = transpose8(pack_f16(x[2], x[3]));
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            // Bytes of two tokens' codes for one channel: even channels, odd channels.
+            const uint32_t w0 = v[k][0][j], w1 = v[k][1][j], w2 = v[k][2][j], w3 = v[k][3][j];
+            const uint32_t lo01 = (w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u);
+            const uint32_t hi01 = ((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u);
+            const uint32_t lo23 = (w2 & 0x0f0f0f0fu) | ((w3 << 4) & 0xf0f0f0f0u);
+            const uint32_t hi23 = ((w2 >> 4) & 0x0f0f0f0fu) | (w3 & 0xf0f0f0f0u);
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            kv4_decode8(lo01, a0);
+            kv4_decode8(hi01, a1);
+            kv4_decode8(lo23, a2);
+            kv4_decode8(hi23, a3);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int i = 2 * j + h;
+              if (i >= NG) continue;
+              const int y = 2 * h;
+#pragma unroll
+              for (int r = 0; r < NR; ++r) {
+                const bool its = !PACK || g / 4 == k;  // column g is of this block
+                const uint32_t c0 = its ? b0[h][r] : 0u, c1 = its ? b1[h][r] : 0u;
+                mma16816(o[r][i][0], a0[y], a1[y], a2[y], a3[y], c0, c1);
+                mma16816(o[r][i][1], a0[y + 1], a1[y + 1], a2[y + 1], a3[y + 1], c0, c1);
+              }
             }
           }
         }
@@ -612,13 +663,32 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
         l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], 8);
         l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], 16);
       }
+    if constexpr (PACK) {  // columns 4-7 to 0-3
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float m = fmaxf(ref[0][c], __shfl_xor_sync(0xffffffffu, ref[0][c], 2));
+        const float f = ex2_approx(ref[0][c] - m);
+        ref[0][c] = m;
+        l[0][c] *= f;
+        l[0][c] += __shfl_xor_sync(0xffffffffu, l[0][c], 2);
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = c; k < 4; k += 2) {
+              o[0][i][h][k] *= f;
+              o[0][i][h][k] += __shfl_xor_sync(0xffffffffu, o[0][i][h][k], 2);
+            }
+      }
+    }
     if (starts && ends) {
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int col = r * 8 + 2 * t + c;
-          if (col >= n_rows) continue;
+          const int col = r * 8 + col0 + c;
+          if (col >= n_rows || (PACK && t >= 2)) continue;
           const float inv = l[r][c] == 0.f ? 0.f : 1.0f / l[r][c];
           __nv_bfloat16* dst = p.o + (size_t)(row_at + col) * D + 4 * g;
 #pragma unroll
@@ -637,10 +707,11 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
       for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int col = r * 8 + 2 * t + c;
+          const int col = r * 8 + col0 + c;
+          if (PACK && t >= 2) continue;
 #pragma unroll
           for (int i = 0; i < NG; ++i)
-            dst[col * (D / 4) + ((8 * i + g) ^ (2 * t))] =
+            dst[col * (D / 4) + ((8 * i + g) ^ col0)] =
                 make_float4(o[r][i][0][c], o[r][i][0][c + 2], o[r][i][1][c], o[r][i][1][c + 2]);
           if (g == 0) stats[starts ? 1 : 0][warp * C::kRows + col] = make_float2(ref[r][c], l[r][c]);
         }
@@ -750,9 +821,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) kv4_fwd_kernel(const 
 // Merge of the parts of the units that CTA borders cut: a CTA per main CTA, a
 // warp per row.  O = sum_k 2^(ref_k - m) O_k / sum_k 2^(ref_k - m) l_k, the
 // parts in the order of the CTAs.
-template <int D, int NR>
+template <int D, int kRows>
 __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4FwdParams p) {
-  constexpr int kRows = NR * kKv4Rows;
   constexpr int kMany = (D / 4 + 31) / 32, kBatch = 8 / kMany;
   pdl_wait();
   const Kv4Cut cut = p.cuts[blockIdx.x];
@@ -827,9 +897,9 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4FwdParams p) {
 
 namespace {
 
-template <int D, int NR>
+template <int D, int NR, bool PACK>
 cudaError_t launch_fwd_t(const Kv4FwdParams& p, int grid, cudaStream_t stream) {
-  using C = Cfg<D, NR>;
+  using C = Cfg<D, NR, PACK>;
   // The kernel's shared memory is allowed once on each device.
   static std::atomic<unsigned long long> allowed{0};
   int dev = 0;
@@ -837,44 +907,64 @@ cudaError_t launch_fwd_t(const Kv4FwdParams& p, int grid, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kv4_fwd_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(kv4_fwd_kernel<D, NR, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_pdl(kv4_fwd_kernel<D, NR>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, p);
+  return launch_pdl(kv4_fwd_kernel<D, NR, PACK>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, p);
+}
+
+template <int D>
+cudaError_t launch_fwd_d(int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream) {
+  if (unit_rows == kKv4Rows / 2) return launch_fwd_t<D, 1, true>(p, grid, stream);
+  if (unit_rows == kKv4Rows) return launch_fwd_t<D, 1, false>(p, grid, stream);
+  if constexpr (D != 256) {
+    if (unit_rows == 2 * kKv4Rows) return launch_fwd_t<D, 2, false>(p, grid, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t launch_merge_d(int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream) {
+  const dim3 g(grid), b(256);
+  if (unit_rows == kKv4Rows / 2) return launch_pdl(kv4_merge_kernel<D, kKv4Rows / 2>, g, b, 0, stream, p);
+  if (unit_rows == kKv4Rows) return launch_pdl(kv4_merge_kernel<D, kKv4Rows>, g, b, 0, stream, p);
+  if constexpr (D != 256) {
+    if (unit_rows == 2 * kKv4Rows) return launch_pdl(kv4_merge_kernel<D, 2 * kKv4Rows>, g, b, 0, stream, p);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 // Rows of a unit and keys of a step for head dim d and `rows` query rows a
-// key/value head.  Two row tiles a unit only where one does not hold the rows,
-// and not at d = 256, whose sums take 64 registers a tile.
+// key/value head.  Up to four rows leave half of a tile's columns free for a
+// second block of keys, which halves what a step spends on softmax (PACK).  Two
+// row tiles a unit only where one does not hold the rows, and not at d = 256,
+// whose sums take 64 registers a tile.
 void kv4_fwd_shape(int d, int rows, int* unit_rows, int* step_keys, int* unit_cost) {
   const bool two = rows > kKv4Rows && d != 256;
-  *unit_rows = two ? 2 * kKv4Rows : kKv4Rows;
-  *step_keys = Cfg<64, 1>::kKeys;
+  *unit_rows = rows <= kKv4Rows / 2 ? kKv4Rows / 2 : (two ? 2 * kKv4Rows : kKv4Rows);
+  *step_keys = Cfg<64, 1, false>::kKeys;
   *unit_cost = kUnitCost;
 }
 
 cudaError_t launch_kv4_fwd(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream) {
-  const bool two = unit_rows == 2 * kKv4Rows;
   switch (d) {
-    case 64: return two ? launch_fwd_t<64, 2>(p, grid, stream) : launch_fwd_t<64, 1>(p, grid, stream);
-    case 96: return two ? launch_fwd_t<96, 2>(p, grid, stream) : launch_fwd_t<96, 1>(p, grid, stream);
-    case 128: return two ? launch_fwd_t<128, 2>(p, grid, stream) : launch_fwd_t<128, 1>(p, grid, stream);
-    case 256: return two ? cudaErrorInvalidValue : launch_fwd_t<256, 1>(p, grid, stream);
+    case 64: return launch_fwd_d<64>(unit_rows, p, grid, stream);
+    case 96: return launch_fwd_d<96>(unit_rows, p, grid, stream);
+    case 128: return launch_fwd_d<128>(unit_rows, p, grid, stream);
+    case 256: return launch_fwd_d<256>(unit_rows, p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 cudaError_t launch_kv4_merge(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream) {
-  const bool two = unit_rows == 2 * kKv4Rows;
-  const dim3 g(grid), b(256);
   switch (d) {
-    case 64: return launch_pdl(two ? kv4_merge_kernel<64, 2> : kv4_merge_kernel<64, 1>, g, b, 0, stream, p);
-    case 96: return launch_pdl(two ? kv4_merge_kernel<96, 2> : kv4_merge_kernel<96, 1>, g, b, 0, stream, p);
-    case 128: return launch_pdl(two ? kv4_merge_kernel<128, 2> : kv4_merge_kernel<128, 1>, g, b, 0, stream, p);
-    case 256: return launch_pdl(kv4_merge_kernel<256, 1>, g, b, 0, stream, p);
+    case 64: return launch_merge_d<64>(unit_rows, p, grid, stream);
+    case 96: return launch_merge_d<96>(unit_rows, p, grid, stream);
+    case 128: return launch_merge_d<128>(unit_rows, p, grid, stream);
+    case 256: return launch_merge_d<256>(unit_rows, p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }
