@@ -39,9 +39,9 @@ template <int D, int U>
 struct Kv4Tokens {
   size_t row;         // of the token in block 0, in [B, Hkv, N] (block u: 16 u rows on)
   int place;          // in the block
-  uint32_t has;       // bit u: block u holds a token of this thread's
-  bool all;           // of the CTA: every thread has one in every block
-  int page[U];
+  uint32_t has;       // bit u: this thread has a row for block u
+  bool all;           // of the CTA: every thread has one for every block
+  int page[U];        // of block u; -1: none, or out of range
   int in_page;        // 16-token blocks of a page before block 0
   int head;
 };
@@ -81,14 +81,20 @@ __device__ __forceinline__ Kv4Tokens<D, U> kv4_tokens(const Kv4MoveParams& p) {
     w.page[u] = -1;
     if (i0 + 16 * u < n && i0 + 16 * u > -16) {  // for the whole CTA: some row is a token
       if ((unsigned)(block0 + u) < (unsigned)blocks) w.page[u] = table[(block0 + u) >> shift];
-      if ((unsigned)w.page[u] >= (unsigned)p.c.num_pages) w.page[u] = -1;
     }
-    const bool mine = i >= 0 && i < n;
-    if (mine && w.page[u] < 0) kv4_bad_index(p.c);
-    w.has |= (mine && w.page[u] >= 0 ? 1u : 0u) << u;
-    w.all = w.all && i0 + 16 * u >= 0 && i0 + 16 * u + 16 <= n && w.page[u] >= 0;
+    w.has |= (i >= 0 && i < n ? 1u : 0u) << u;
+    w.all = w.all && i0 + 16 * u >= 0 && i0 + 16 * u + 16 <= n;
   }
   return w;
+}
+
+// Whether block u's page is in range; a thread with a row for it records that
+// it is not.
+template <int D, int U>
+__device__ __forceinline__ bool kv4_there(const Kv4MoveParams& p, const Kv4Tokens<D, U>& w, int u) {
+  if ((unsigned)w.page[u] < (unsigned)p.c.num_pages) return true;
+  if ((w.has >> u) & 1) kv4_bad_index(p.c);
+  return false;
 }
 
 // Block u of the CTA's tokens.
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(2 * D) kv4_write_kernel(const Kv4MoveParams p)
       kw = rk == 0.f ? 0u : kw;
       vw = rv == 0.f ? 0u : vw;
       if constexpr (F::kGroups % 2 == 0) vw = exchange_units(vw, g & 1);
-      if (!ALL && !((w.has >> u) & 1)) continue;
+      if ((!ALL && !((w.has >> u) & 1)) || !kv4_there<D, U>(p, w, u)) continue;
       uint8_t* const block = kv4_block_of<D, U>(p, w, u);
       *reinterpret_cast<uint32_t*>(block + at_key) = kw;
       if constexpr (F::kGroups % 2 == 0) {
@@ -235,7 +241,13 @@ __global__ void __launch_bounds__(2 * D) kv4_read_kernel(const Kv4MoveParams p) 
   using F = Kv4<D>;
   constexpr int kPer = D / 8;
   const int c8 = threadIdx.x % kPer, g = c8 / 4, t = c8 % 4;
-  const Kv4Tokens<D, U> w = kv4_tokens<D, U>(p);
+  Kv4Tokens<D, U> w = kv4_tokens<D, U>(p);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (!kv4_there<D, U>(p, w, u)) {
+      w.has &= ~(1u << u);
+      w.all = false;
+    }
   uint4* const k_out = p.k_out + (ptrdiff_t)w.row * kPer + c8;
   uint4* const v_out = p.v_out + (ptrdiff_t)w.row * kPer + c8;
   auto body = [&](auto all) {
