@@ -325,10 +325,16 @@ def _torch_cuda():
         import torch
 
         _torch = torch
-    if not _torch.cuda.is_initialized():
-        # No CUDA tensor exists yet, so that any argument is refused.
-        return _torch, None
-    return _torch, _torch._C._cuda_getDevice()
+    try:
+        return _torch, _torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):
+        return _torch, None  # no CUDA device: any argument is refused
+
+
+# What causal and scale are usually given as.
+_CAUSAL_CODES = {False: FA_CAUSAL_NONE, True: FA_CAUSAL_TOP_LEFT, FA_CAUSAL_BOTTOM_RIGHT: FA_CAUSAL_BOTTOM_RIGHT,
+                 **_CAUSAL_NAMES}
+_DEFAULT_SCALES = {d: _scale(None, d) for d in (64, 96, 128, 256)}
 
 
 def _refuse(tensors, device):
@@ -401,18 +407,22 @@ def fa_kv4_write(k, v, cache, block_table, start, count=None, stream=None):
     cache [num_pages, Hkv, page_size * 9 d / 8] (uint8), token i < count[b]
     (all N without count) of sequence b to position start[b] + i."""
     device, sizes = _kv4_move(k, v, cache, block_table, start, count)
-    _check(load().fa_kv4_write(k.data_ptr(), v.data_ptr(), cache.data_ptr(), block_table.data_ptr(), start.data_ptr(),
-                               None if count is None else count.data_ptr(), *sizes, _raw_stream(stream, device)),
-           "fa_kv4_write")
+    status = (_lib or load()).fa_kv4_write(
+        k.data_ptr(), v.data_ptr(), cache.data_ptr(), block_table.data_ptr(), start.data_ptr(),
+        None if count is None else count.data_ptr(), *sizes, _raw_stream(stream, device))
+    if status != FA_OK:
+        raise FaError(status, "fa_kv4_write")
 
 
 def fa_kv4_read(cache, block_table, start, k, v, count=None, stream=None):
     """C fa_kv4_read: the held values of positions start[b] + i to rows
     i < count[b] of k, v [B, Hkv, N, d]; other rows are left as they were."""
     device, sizes = _kv4_move(k, v, cache, block_table, start, count)
-    _check(load().fa_kv4_read(cache.data_ptr(), block_table.data_ptr(), start.data_ptr(),
-                              None if count is None else count.data_ptr(), k.data_ptr(), v.data_ptr(), *sizes,
-                              _raw_stream(stream, device)), "fa_kv4_read")
+    status = (_lib or load()).fa_kv4_read(
+        cache.data_ptr(), block_table.data_ptr(), start.data_ptr(), None if count is None else count.data_ptr(),
+        k.data_ptr(), v.data_ptr(), *sizes, _raw_stream(stream, device))
+    if status != FA_OK:
+        raise FaError(status, "fa_kv4_read")
 
 
 def fa_kv4_fwd(q, cache, block_table, lens, o, lse, causal=False, scale=None, stream=None):
@@ -440,9 +450,15 @@ def fa_kv4_fwd(q, cache, block_table, lens, o, lse, causal=False, scale=None, st
                  ("block_table", block_table, i32, (B, None)), ("lens", lens, i32, (B,)),
                  ("o", o, bf16, (B, H, Nq, d)), ("lse", lse, torch.float32, (B, H, Nq))], device)
     page_size = _page_size(page_bytes, d)
-    _check(load().fa_kv4_fwd(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lens.data_ptr(), o.data_ptr(),
-                             lse.data_ptr(), B, H, Hkv, Nq, d, num_pages, page_size, max_pages, _causal_code(causal),
-                             _scale(scale, d), _raw_stream(stream, device)), "fa_kv4_fwd")
+    code = _CAUSAL_CODES.get(causal)
+    if code is None:
+        code = _causal_code(causal)
+    scale = _DEFAULT_SCALES.get(d, 1.0) if scale is None else float(scale)
+    status = (_lib or load()).fa_kv4_fwd(
+        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv,
+        Nq, d, num_pages, page_size, max_pages, code, scale, _raw_stream(stream, device))
+    if status != FA_OK:
+        raise FaError(status, "fa_kv4_fwd")
 
 
 def fa_poll_status(stream=None):
