@@ -116,19 +116,16 @@ cudaError_t run_merge(void* ctx) {
   return fa::launch_kv4_merge(f.d, f.unit_rows, f.p, f.grid, f.st);
 }
 
-int check_fwd_sizes(int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size, int max_pages, int causal) {
+// How a call is carried out (fa_kv4_plan_t), but for what depends on the
+// device.  The lengths are known on the device only, so this goes by what the
+// table can hold; FA_ERR_INVALID_ARG where the list of steps might then not fit
+// 31 bits.
+int plan_units(int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size, int max_pages, int causal,
+               fa_kv4_plan_t* pl) {
   const int e = check_sizes(B, H, Hkv, Nq, d, num_pages, page_size, max_pages);
   if (e) return e;
   if (H % Hkv != 0 || causal < FA_CAUSAL_NONE || causal > FA_CAUSAL_BOTTOM_RIGHT) return FA_ERR_INVALID_ARG;
   if ((long long)(H / Hkv) * Nq > kMaxRows) return FA_ERR_UNSUPPORTED;
-  return FA_OK;
-}
-
-// How a call is carried out (fa_kv4_plan_t), for sizes that passed
-// check_fwd_sizes.  The lengths are known on the device only, so this goes by
-// what the table can hold.
-// FA_ERR_INVALID_ARG where the list of steps might not fit 31 bits.
-int plan_fwd(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages, int sm_count, fa_kv4_plan_t* pl) {
   std::memset(pl, 0, sizeof(*pl));
   pl->rows = (H / Hkv) * Nq;
   int unit_cost = 0;
@@ -139,13 +136,16 @@ int plan_fwd(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages,
   pl->max_steps = (int)((held + pl->step_keys - 1) / pl->step_keys);
   if ((long long)pl->units * (pl->max_steps + unit_cost) > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   pl->whole = pl->max_steps <= kWholeSteps ? 1 : 0;
+  pl->launches = pl->whole ? 1 : 2;
+  return FA_OK;
+}
+
+void plan_grid(int d, int sm_count, fa_kv4_plan_t* pl) {
   const long long most = (long long)pl->units * (pl->whole ? 1 : pl->max_steps);
   pl->grid = (int)std::min<long long>(most, sm_count);
-  pl->launches = pl->whole ? 1 : 2;
   if (!pl->whole)
     pl->workspace_bytes = (uint64_t)pl->grid * (2ull * pl->unit_rows * (d * sizeof(float) + sizeof(float2)) +
                                                 sizeof(fa::Kv4Cut));
-  return FA_OK;
 }
 
 }  // namespace
@@ -180,15 +180,14 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
       !aligned(lens, 4))
     return FA_ERR_INVALID_ARG;
   if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
-  int e = check_fwd_sizes(B, H, Hkv, Nq, d, num_pages, page_size, max_pages, causal);
+  fa_kv4_plan_t pl;
+  int e = plan_units(B, H, Hkv, Nq, d, num_pages, page_size, max_pages, causal, &pl);
   if (e) return e;
   unsigned int* status = nullptr;
   int sm_count = 0;
   e = fa::internal_device_setup(&status, &sm_count);
   if (e) return e;
-  fa_kv4_plan_t pl;
-  e = plan_fwd(B, H, Hkv, Nq, d, page_size, max_pages, sm_count, &pl);
-  if (e) return e;
+  plan_grid(d, sm_count, &pl);
   Fwd f;
   f.d = d;
   f.unit_rows = pl.unit_rows;
@@ -230,12 +229,12 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
 int fa_kv4_fwd_plan(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages, int sm_count,
                     fa_kv4_plan_t* plan) {
   if (plan == nullptr || sm_count < 1) return FA_ERR_INVALID_ARG;
-  const int e = check_fwd_sizes(B, H, Hkv, Nq, d, 1, page_size, max_pages, FA_CAUSAL_NONE);
-  if (e) return e;
   fa_kv4_plan_t pl;
-  const int e2 = plan_fwd(B, H, Hkv, Nq, d, page_size, max_pages, sm_count, &pl);
-  if (e2 == FA_OK) *plan = pl;
-  return e2;
+  const int e = plan_units(B, H, Hkv, Nq, d, 1, page_size, max_pages, FA_CAUSAL_NONE, &pl);
+  if (e) return e;
+  plan_grid(d, sm_count, &pl);
+  *plan = pl;
+  return FA_OK;
 }
 
 }  // extern "C"

@@ -65,7 +65,9 @@ struct Cfg {
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kSums = kRows * D * 4;
   static constexpr int kSmem = kWarps * (kRing + kSums);
+  static_assert(kSmem + 8 * 1024 <= 227 * 1024, "shared memory of an SM, 8 KB of it static");
   static_assert(kRing >= kSums, "a tail's sums go where the ring was");
+  static_assert(kWarps <= 30, "a lane for each warp's results, and one for a tail's");
 };
 
 // Places of the list that a unit takes besides one for each of its steps: what
@@ -807,14 +809,19 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     }
   }
 
-  // After a wait that gave up, copies may still be in flight into this CTA's
-  // shared memory: wait for them (bounded) before it is given back.
+  // After a wait that gave up, copies may still be on their way into this CTA's
+  // shared memory: wait for them, bounded, before it is given back.
   if (!ok) {
+    const unsigned long long limit = max(p.timeout_ns, 100000000ull);  // however short the waits' limit is
     const uint64_t t0 = globaltimer_ns();
-    for (int s = 0; s < C::kStages; ++s)
-      while (!mbar_try_wait(smem_u32(&bar[s]), s < stage ? phase ^ 1 : phase) &&
-             globaltimer_ns() - t0 < p.timeout_ns) {
+    for (; in_flight > 0; --in_flight) {
+      while (!mbar_try_wait(smem_u32(&bar[stage]), phase) && globaltimer_ns() - t0 < limit) {
       }
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
   }
 }
 

@@ -349,6 +349,10 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * a row not read, the keys of that page not attended to; lengths are clamped
  * to [0, max_pages * page_size]) and record FA_ERR_BAD_INDEX, which
  * fa_poll_status reports.
+ * The arrays (and the cache) must not be written while a call reads them.
+ * The calls may be captured into a CUDA graph, but not as the first call of
+ * the library on a device.  Their kernels are launched with programmatic
+ * stream serialization like those of the backward.
  */
 
 /* Bytes of a cache: num_pages * Hkv * page_size * 9 d / 8 in *bytes. */
@@ -390,7 +394,11 @@ int fa_kv4_read(const void* cache, const int* block_table, const int* start, con
  *            (all rows of a sequence of length 0).
  * FA_ERR_INVALID_ARG also where the table could hold more work than a 31-bit
  * list of steps: units * (max_steps + 2) of fa_kv4_fwd_plan above 2^31 - 1.
- * Scores, softmax and sums are fp32 on the exact held values.
+ * Scores, softmax and sums are fp32 on the exact held values.  The weights
+ * enter the product with the values in 16 bits (11 significant ones, relative
+ * to the largest weight times scale of the row down to 2^-18 of it, absolute
+ * below that); values above 2^100 or groups whose scale is below 2^-80 keep
+ * less.
  */
 int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const int* lens, void* o, float* lse,
                int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size, int max_pages, int causal,

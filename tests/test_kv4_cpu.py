@@ -201,6 +201,52 @@ def test_fwd_refusals(lib):
         assert _fwd(lib, ptrs) == fa.FA_ERR_INVALID_ARG
 
 
+PLANS = [
+    # B, H, Hkv, Nq, d, page_size, max_pages
+    (1, 1, 1, 1, 64, 16, 1), (1, 32, 8, 1, 128, 16, 3), (8, 32, 8, 1, 128, 64, 128), (64, 32, 8, 1, 128, 64, 256),
+    (9, 12, 4, 5, 96, 32, 188), (16, 64, 4, 1, 256, 64, 128), (3, 8, 1, 16, 128, 1024, 7), (1500, 2, 1, 1, 64, 16, 3),
+    (2, 5, 1, 1, 128, 16, 17), (2, 4, 1, 1, 256, 16, 16), (1, 16, 2, 1, 256, 256, 4096),
+]
+
+
+@pytest.mark.parametrize("sizes", PLANS)
+@pytest.mark.parametrize("sm_count", (1, 152))
+def test_plan(lib, sizes, sm_count):
+    B, H, Hkv, Nq, d, page, pages = sizes
+    pl = fa.fa_kv4_fwd_plan(*sizes, sm_count)
+    assert pl["rows"] == H // Hkv * Nq
+    assert pl["unit_rows"] == (4 if pl["rows"] <= 4 else 16 if pl["rows"] > 8 and d < 256 else 8)
+    assert pl["row_blocks"] * pl["unit_rows"] >= pl["rows"] > (pl["row_blocks"] - 1) * pl["unit_rows"]
+    assert pl["units"] == B * Hkv * pl["row_blocks"]
+    assert pl["max_steps"] * pl["step_keys"] >= page * pages > (pl["max_steps"] - 1) * pl["step_keys"]
+    assert 1 <= pl["grid"] <= sm_count
+    assert pl["grid"] == min(sm_count, pl["units"] * (1 if pl["whole"] else pl["max_steps"]))
+    assert pl["launches"] == (1 if pl["whole"] else 2)
+    part = pl["unit_rows"] * (4 * d + 8)
+    if pl["whole"]:
+        assert pl["workspace_bytes"] == 0
+    else:
+        assert 2 * pl["grid"] * part < pl["workspace_bytes"] <= pl["grid"] * (2 * part + 64)
+
+
+def test_plan_refusals(lib):
+    good = (2, 32, 4, 2, 128, 64, 10, 152)
+    fa.fa_kv4_fwd_plan(*good)
+    for i, bad, want in ((0, 0, 1), (1, 0, 1), (2, 3, 1), (3, 0, 1), (3, 17, 2), (4, 80, 2), (5, 20, 1), (6, 0, 1), (7, 0, 1)):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(fa.FaError) as e:
+            fa.fa_kv4_fwd_plan(*args)
+        assert e.value.status == want, (i, bad)
+    # Units times steps beyond 31 bits.
+    with pytest.raises(fa.FaError) as e:
+        fa.fa_kv4_fwd_plan(1 << 12, 32, 32, 1, 128, 1024, 1 << 10, 152)
+    assert e.value.status == fa.FA_ERR_INVALID_ARG
+    assert _fwd(lib, B=1 << 12, H=32, Hkv=32, Nq=1, page_size=1024, max_pages=1 << 10) == fa.FA_ERR_INVALID_ARG
+    args = [*good, None]
+    assert lib.fa_kv4_fwd_plan(*args) == fa.FA_ERR_INVALID_ARG
+
+
 def test_launch_count_and_status_name(lib):
     assert fa.fa_strerror(fa.FA_ERR_BAD_INDEX).startswith("FA_ERR_BAD_INDEX")
     n = ctypes.c_uint64(7)

@@ -470,6 +470,73 @@ def test_binding_refusals(fa):
     assert fa.fa_poll_status() == fa.FA_OK
 
 
+def test_misaligned_storage_is_refused(fa):
+    torch = torch_cuda()
+    raw = torch.zeros(4 * 2 * 16 * 72 + 16, dtype=torch.uint8, device="cuda")
+    q = torch.zeros((1, 4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    qq = torch.zeros(1 + q.numel(), dtype=torch.bfloat16, device="cuda")[1:].view(q.shape)
+    table, lens = ints([[0, 1]]), ints([20])
+    cache = raw[:4 * 2 * 16 * 72].view(4, 2, -1)
+    fa.kv4_forward(q, cache, table, lens)
+    for a, c in ((qq, cache), (q, raw[8:8 + 4 * 2 * 16 * 72].view(4, 2, -1))):
+        with pytest.raises(fa.FaError) as e:
+            fa.kv4_forward(a, c, table, lens)
+        assert e.value.status == fa.FA_ERR_INVALID_ARG
+    # int32 arrays that start anywhere in another one are fine.
+    many = ints([7, 0, 1, 20])
+    o, lse = fa.kv4_forward(q, cache, many[1:3].view(1, 2), many[3:])
+    assert fa.fa_poll_status() == fa.FA_OK and (host(o) == 0).all()
+
+
+def test_workspace_allocation_failure_is_reported(fa, monkeypatch):
+    rng = np.random.default_rng(10)
+    f = Filled(fa, rng, [900], 1, 64, 16)
+    qd, q = normal(rng, (1, 2, 1, 64))
+    monkeypatch.setenv("FA_TEST_FAIL_ALLOC", "1")
+    with pytest.raises(fa.FaError) as e:
+        fa.kv4_forward(qd, f.cache, f.td, f.ld)
+    assert e.value.status == fa.FA_ERR_NO_MEMORY
+    monkeypatch.delenv("FA_TEST_FAIL_ALLOC")
+    o, lse = fa.kv4_forward(qd, f.cache, f.td, f.ld)
+    assert fa.fa_poll_status() == fa.FA_OK
+    check_attend(o, lse, q, f.k, f.v, [900], 64 ** -0.5, "none")
+
+
+@pytest.mark.parametrize("rows", (1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 33))
+@pytest.mark.parametrize("d", DIMS)
+def test_every_count_of_query_rows(fa, d, rows):
+    """Rows per key/value head about the borders between the tilings, over a
+    table that makes units cut between CTAs and one that does not."""
+    rng = np.random.default_rng(100 * d + rows)
+    lens = [47, 600, 5]
+    f = Filled(fa, rng, lens, 2, d, 32)
+    qd, q = normal(rng, (3, 2 * rows, 1, d))
+    wide = np.full((3, 64), -1, np.int32)
+    wide[:, :f.table.shape[1]] = f.table
+    short = Filled(fa, rng, [47, 33, 0], 2, d, 16)
+    for g, table, n in ((f, ints(wide), lens), (short, short.td, [47, 33, 0])):
+        o, lse = fa.kv4_forward(qd, g.cache, table, g.ld)
+        assert fa.fa_poll_status() == fa.FA_OK
+        check_attend(o, lse, q, g.k, g.v, n, d ** -0.5, "none", f"rows={rows}")
+
+
+def test_waits_that_give_up_are_reported(fa):
+    """With no time to wait, the kernel may give up on its copies: it records
+    FA_ERR_TIMEOUT, returns, and the next call is correct."""
+    rng = np.random.default_rng(12)
+    f = Filled(fa, rng, [5000, 3000], 2, 128, 64)
+    qd, q = normal(rng, (2, 4, 1, 128))
+    before = fa.fa_set_wait_timeout_ns(0)
+    try:
+        fa.kv4_forward(qd, f.cache, f.td, f.ld)
+        assert fa.fa_poll_status() in (fa.FA_OK, fa.FA_ERR_TIMEOUT)
+    finally:
+        fa.fa_set_wait_timeout_ns(before)
+    o, lse = fa.kv4_forward(qd, f.cache, f.td, f.ld)
+    assert fa.fa_poll_status() == fa.FA_OK
+    check_attend(o, lse, q, f.k, f.v, [5000, 3000], 128 ** -0.5, "none")
+
+
 # --------------------------------------------------------- used together
 
 @pytest.mark.parametrize("d", (64, 128, 256))
