@@ -51,8 +51,12 @@ namespace {
 
 template <int D, int NR, bool PACK>
 struct Cfg {
-  // One CTA an SM; its warps as many as their registers allow.
-  static constexpr int kWarps = NR == 1 && D < 256 ? (D == 64 ? 16 : 12) : 8;
+  // One CTA an SM, its warps a multiple of the four schedulers and as many as
+  // their registers allow without spills (65536 over 16, 12 or 8 warps: 128, 168
+  // or 255 each).
+  static constexpr int kWarps = D == 256 || (NR == 2 && D > 64)       ? 8
+                                : NR == 1 && (D == 64 || (D == 96 && !PACK)) ? 16
+                                                                       : 12;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kBlocks = 2;                             // 16-token blocks a step
   static constexpr int kKeys = kBlocks * kKv4Block;
@@ -264,9 +268,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     f.off = rest - f.u * f.places;
     return f;
   };
-  // CTAs that take part: two places for every warp, or a unit each.  The first
+  // CTAs that take part: a place for every warp, or a unit each.  The first
   // `more` have a place more than the others.
-  const int active = min((int)gridDim.x, max(total / (2 * W), p.c.B * units));
+  const int active = min((int)gridDim.x, max(total / W, p.c.B * units));
   if ((int)blockIdx.x >= active) return;
   const int each = total / active, more = total - each * active;
   auto cta_of = [&](int place) {
