@@ -239,10 +239,18 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
   // ---- the list (the host has checked that its places fit 31 bits).  Every
   // warp works it out for itself, each lane adding up a run of sequences: the
   // warps need not wait for each other before their copies are on the way.
-  auto length = [&](int b) { return kv4_length(p.c, p.lens, b); };
+  auto length = [&](int b) { return kv4_length(p.c, p.lens[b]); };
   const int run = (p.c.B + 31) / 32;
   int upto = 0;
-  for (int b = lane * run; b < min(p.c.B, lane * run + run); ++b) upto += kUnitCost + steps_of(length(b));
+  const int b_end = min(p.c.B, lane * run + run);
+  for (int b = lane * run; b < b_end; b += 4) {
+    int n[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = b + i < b_end ? p.lens[b + i] : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (b + i < b_end) upto += kUnitCost + steps_of(kv4_length(p.c, n[i]));
+  }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, upto, o);

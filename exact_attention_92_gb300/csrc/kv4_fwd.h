@@ -41,9 +41,9 @@ struct Kv4FwdParams {
 
 namespace dev {
 
-// Length of sequence b, clamped to what the table can hold.
-__device__ __forceinline__ int kv4_length(const Kv4Cache& c, const int* lens, int b) {
-  const int most = c.max_pages << c.page_shift, n = lens[b];
+// A length, clamped to what the table can hold.
+__device__ __forceinline__ int kv4_length(const Kv4Cache& c, int n) {
+  const int most = c.max_pages << c.page_shift;
   if (n >= 0 && n <= most) return n;
   kv4_bad_index(c);
   return n < 0 ? 0 : most;
