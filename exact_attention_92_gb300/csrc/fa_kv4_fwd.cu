@@ -1,12 +1,14 @@
 // Attention over the 4-bit key/value cache (fa_kv4_fwd).
 //
-// A unit is a (sequence, key/value head, block of 8 or 16 of the group's query
-// rows); its keys are walked in steps of 32.  The steps of all units form one
-// list, in the order of the units, of which every CTA takes an equal stretch
+// A unit is a (sequence, key/value head, block of 4, 8 or 16 of the group's
+// query rows); its keys are walked in steps of 32.  The steps of all units form
+// one list, in the order of the units, of which every CTA takes an equal stretch
 // whatever the sequences' lengths, and every warp of it an equal stretch of
 // that.  Where a border cuts a unit, the warps of a CTA join their fp32 results
 // at the CTA's end, and a second kernel merges those of the CTAs, both in the
-// order of the list.
+// order of the list, so the results do not change from run to run.  (Warps that
+// took a CTA's steps in turn and joined at each unit's end: 64 ragged sequences
+// 127 us in place of 109.)
 //
 // Each warp fetches its own steps: bulk copies of whole 16-token blocks into a
 // ring in shared memory, ahead of use, so no warp waits for another within a
@@ -14,9 +16,21 @@
 // instructions on fp16 (16 keys, or 16 channels, by 8 query rows): the keys and
 // values are the row operand, so the decoding of 8 query rows wastes nothing,
 // and their codes go from shared memory through one conversion instruction per
-// two values into the operand's registers.  (A tcgen05 product would want the
-// 128-row operand in shared memory, decoded: 512 bytes written and read back a
-// token for 144 bytes of cache.)
+// two values into the operand's registers.  With up to 4 query rows (PACK) the
+// two 16-key blocks of a step share the 8 columns, which halves the softmax's
+// share of the instructions: 520 a step and warp in place of 583 at d = 128.
+// (A tcgen05 product would want the 128-row operand in shared memory, decoded:
+// 512 bytes written and read back a token for 144 bytes of cache.)
+//
+// What bounds it (d = 128, 64 sequences of up to 16384 tokens, 8 heads, 4 rows,
+// 552 MB): 96.5 us, 5.7 TB/s of DRAM reads, 84% of what a copy moves; while SMs
+// are busy (92 us) 6.0 TB/s with 57% of the issue slots taken.  A step costs
+// 128 conversions from e2m1 and about 100 other instructions of the same
+// half-rate pipe, which so is in use 55% of the time; the matrix pipe 28%.  Of a
+// call of 8 sequences of 8192 tokens (22.5 us, 11.2 us of traffic) about 3 us
+// go before the first copies (lengths, place in the list, page: three dependent
+// loads), 1.5 us for the last warps to finish (9 or 10 steps each), 1 us to join
+// and 2.5 us to merge.
 //
 // Numbers.  Codes are exact in fp16.  A query row is scaled by a power of two
 // to lie just below 2^16, where fp16 holds its bf16 values exactly down to
@@ -24,10 +38,11 @@
 // summed by the matrix instruction in fp32, multiplied by the group's scale in
 // fp32 and added, so scores are those of the exact held values.  The weights
 // p = 2^(s - ref) are multiplied by the values' scale in fp32 and rounded once
-// to fp16 (11 bits) for the P V product.  To keep p * scale within fp16 the
-// running reference is that of s + log2(the largest scale of the token's
-// value), not of s: p * scale starts at 2^4 for the largest key seen and may
-// grow to 2^14 before the reference is moved (and the sums rescaled); what
+// to fp16 (11 bits) for the P V product: bf16 would lose three bits, and 8 bits
+// of weight are what the output's own rounding costs.  To keep p * scale within
+// fp16 the running reference is that of s + log2(the largest scale of the
+// token's value), not of s: p * scale starts at 2^4 for the largest key seen and
+// may grow to 2^14 before the reference is moved (and the sums rescaled); what
 // falls below 2^-14 of that loses relative, not absolute, precision.  The sum
 // of p is fp32.  log2(scale) is taken at 2^-80 at least, which keeps the sum
 // of p below 2^121.
@@ -318,6 +333,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     if (ahead.lo < ahead.hi) {
       if (lane == 0) queue[warp * kQueue + made % kQueue] = ahead;
       ++made;
+      // Its query rows, nearer before they are wanted (1% of a decoding step).
+      const int row0 = (ahead.u - ahead.head * p.row_blocks) * C::kRows;
+      const int n_rows = min(C::kRows, p.rows - row0);
+      const size_t row_at = ((size_t)ahead.b * p.c.Hkv + ahead.head) * p.rows + row0;
+      if (lane * 64 < n_rows * D)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + row_at * D + lane * 64) : "memory");
     }
   };
   // To the next unit; where the stretch is at its end, lo = hi.
@@ -838,7 +859,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
 }
 
 // Merge of the parts of the units that CTA borders cut: a CTA per main CTA, a
-// warp per row.  O = sum_k 2^(ref_k - m) O_k / sum_k 2^(ref_k - m) l_k, the
+// warp per row.  Bound by its chain of loads (which CTAs, their references and
+// sums): about 2.5 us with its launch.  Merging in the main kernel instead, by
+// the CTA that brings a unit's last part, cost more (two barriers, fences and an
+// atomic in every CTA: 8 sequences of 8192 tokens 24.9 us in place of 22.6).  O = sum_k 2^(ref_k - m) O_k / sum_k 2^(ref_k - m) l_k, the
 // parts in the order of the CTAs.
 template <int D, int kRows>
 __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4FwdParams p) {
