@@ -43,7 +43,8 @@ int check_sizes(int B, int heads, int Hkv, int rows, int d, int num_pages, int p
   if (page_size < kMinPage || page_size > kMaxPage || (page_size & (page_size - 1)) != 0) return FA_ERR_INVALID_ARG;
   if (!head_dim(d)) return FA_ERR_UNSUPPORTED;
   const long long most = 0x7fffffffLL;
-  if ((long long)max_pages * page_size > most || rows > (1 << 30)) return FA_ERR_INVALID_ARG;
+  // Positions and rows stay below 2^30, so that a step past one fits an int.
+  if ((long long)max_pages * page_size > (1 << 30) || rows > (1 << 30)) return FA_ERR_INVALID_ARG;
   if ((long long)B * heads > most || (long long)B * heads * rows > most) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }

@@ -342,8 +342,8 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  *                 the entries of pages that hold a position in use are read
  *                 or used; they must lie in [0, num_pages).
  *   start, count, lens : int32 [B], device memory, 4-byte aligned
- *   B * Hkv * N (B * H * Nq) and max_pages * page_size at most 2^31 - 1,
- *   N at most 2^30
+ *   B * Hkv * N (B * H * Nq) at most 2^31 - 1; N and max_pages * page_size at
+ *   most 2^30
  * These arrays are read on the device, so the host cannot refuse a bad entry:
  * the kernels check each one, skip what it points to (a token is not written,
  * a row not read, the keys of that page not attended to; lengths are clamped
@@ -458,7 +458,9 @@ int fa_selftest_wait_timeout(uint64_t timeout_ns, void* stream);
  * Kernel ids: FA_KERNEL_FWD (forward main kernel), FA_KERNEL_COMBINE
  * (split-KV merge), FA_KERNEL_BWD_PRE (D preprocess), FA_KERNEL_BWD
  * (backward dK/dV kernel; at head dim 128 the CTA-pair kernel),
- * FA_KERNEL_BWD_DQ (backward dQ kernel).
+ * FA_KERNEL_BWD_DQ (backward dQ kernel); FA_KERNEL_KV4_WRITE, _READ, _FWD and
+ * _MERGE (the 4-bit cache's writing, reading, attention and the merge of what
+ * its CTAs leave in parts).
  *   fa_timing_enable(on) : 1 starts recording (and drops old records), 0 stops.
  *   fa_timing_read(kernel, launches, total_ms) : waits for the recorded
  *       events of that kernel, returns how many launches were recorded and

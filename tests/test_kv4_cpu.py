@@ -147,6 +147,8 @@ def _bad_sizes():
     for x in (0, 32, 80, 512, -128):
         yield {"d": x}, "FA_ERR_UNSUPPORTED"
     yield {"max_pages": 1 << 26, "page_size": 32}, "FA_ERR_INVALID_ARG"   # 2^31 positions
+    yield {"max_pages": (1 << 25) + 1, "page_size": 32}, "FA_ERR_INVALID_ARG"
+    yield {"B": 1, "Hkv": 1, "N": (1 << 30) + 1}, "FA_ERR_INVALID_ARG"
     yield {"B": 1 << 16, "Hkv": 1 << 10, "N": 1 << 10}, "FA_ERR_INVALID_ARG"  # 2^36 rows
 
 

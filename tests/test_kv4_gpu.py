@@ -330,6 +330,21 @@ def test_held_nan_reaches_the_rows_that_see_it(fa, d):
     assert np.abs(O[0] - want[0, 0]).max() < 0.02
 
 
+def test_held_nan_of_a_key_reaches_all_channels(fa):
+    rng = np.random.default_rng(3)
+    N, d = 300, 128
+    keys = kv4.to_bf16(rng.standard_normal((1, 1, N, d)))
+    keys[0, 0, N - 1, 5] = np.nan
+    f = Filled(fa, rng, [N], 1, d, 16, keys=keys)
+    for H in (2, 6, 12):
+        qd, q = normal(rng, (1, H, 2, d))
+        o, lse = fa.kv4_forward(qd, f.cache, f.td, f.ld, causal="bottom_right")
+        O, L = host(o)[0], lse.cpu().numpy()[0]
+        assert np.isfinite(O[:, 0]).all() and np.isfinite(L[:, 0]).all()
+        assert np.isnan(O[:, 1]).all() and np.isnan(L[:, 1]).all()
+    assert fa.fa_poll_status() == fa.FA_OK
+
+
 def test_pages_far_apart(fa):
     """A cache beyond 2^32 bytes, its pages in use at both ends."""
     torch = torch_cuda()
@@ -418,7 +433,7 @@ def test_bad_lengths_and_positions_are_clamped_and_reported(fa):
     check_attend(o, lse, q, f.k, f.v, [0, 32], d ** -0.5, "none")
     before = f.cache.clone()
     x = torch.ones((2, 1, 4, d), dtype=torch.bfloat16, device="cuda")
-    for start, count in (([-4, 32], None), ([2 ** 31 - 1, -2 ** 31], None), ([0, 0], [-1, 0])):
+    for start, count in (([-4, 32], None), ([2 ** 31 - 1, -2 ** 31], None), ([0, 0], [-1, 0]), ([32, 40], [5, 0])):
         fa.fa_kv4_write(x, x, f.cache, table, ints(start), None if count is None else ints(count))
         assert fa.fa_poll_status() == fa.FA_ERR_BAD_INDEX
         assert torch.equal(before, f.cache)
@@ -653,11 +668,20 @@ def test_calls_at_once_on_two_streams(fa):
 def test_launches_are_counted(fa):
     torch = torch_cuda()
     rng = np.random.default_rng(22)
-    ids = (fa.FA_KERNEL_KV4_WRITE, fa.FA_KERNEL_KV4_READ, fa.FA_KERNEL_KV4_FWD)
+    ids = (fa.FA_KERNEL_KV4_WRITE, fa.FA_KERNEL_KV4_READ, fa.FA_KERNEL_KV4_FWD, fa.FA_KERNEL_KV4_MERGE)
     before = [fa.fa_launch_count(i) for i in ids]
     f = Filled(fa, rng, [40], 1, 64, 16)
     out = torch.empty((1, 1, 40, 64), dtype=torch.bfloat16, device="cuda")
     fa.fa_kv4_read(f.cache, f.td, ints([0]), out, out.clone())
     fa.kv4_forward(out[:, :, :1].contiguous(), f.cache, f.td, f.ld)
     torch.cuda.synchronize()
-    assert [fa.fa_launch_count(i) - n for i, n in zip(ids, before)] == [1, 1, 1]
+    assert [fa.fa_launch_count(i) - n for i, n in zip(ids, before)] == [1, 1, 1, 0]
+    # The call follows its plan: a table for many tokens means a merge.
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    wide = ints(np.repeat(f.table, 20, 1))
+    for table in (f.td, wide):
+        plan = fa.fa_kv4_fwd_plan(1, 1, 1, 1, 64, 16, table.shape[1], sms)
+        before = [fa.fa_launch_count(i) for i in ids[2:]]
+        fa.kv4_forward(out[:, :, :1].contiguous(), f.cache, table, f.ld)
+        assert [fa.fa_launch_count(i) - n for i, n in zip(ids[2:], before)] == [1, plan["launches"] - 1]
+    assert plan["launches"] == 2
