@@ -16,7 +16,9 @@ int internal_device_setup(unsigned int** status, int* sm_count);
 cudaError_t internal_timed_launch(int kernel, cudaStream_t stream, cudaError_t (*launch)(void*), void* ctx);
 cudaError_t launch_kv4_move(int d, bool write, const Kv4Cache& c, const int* start, const int* count, const void* k_in,
                             const void* v_in, void* k_out, void* v_out, int N, int sm_count, cudaStream_t stream);
-void kv4_fwd_shape(int d, int rows, int* unit_rows, int* step_keys, int* unit_cost);
+int kv4_fwd_unit_rows(int d, int rows, long long sm_steps);
+int kv4_fwd_step_keys();
+int kv4_fwd_unit_cost();
 cudaError_t launch_kv4_fwd(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_kv4_merge(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
 cudaError_t internal_workspace(void** ptr, size_t bytes, cudaStream_t st);
@@ -119,6 +121,8 @@ cudaError_t run_merge(void* ctx) {
   return fa::launch_kv4_merge(f.d, f.unit_rows, f.p, f.grid, f.st);
 }
 
+int units_of(int rows, int unit_rows) { return (rows + unit_rows - 1) / unit_rows; }
+
 // How a call is carried out (fa_kv4_plan_t), but for what depends on the
 // device.  The lengths are known on the device only, so this goes by what the
 // table can hold; FA_ERR_INVALID_ARG where the list of steps might then not fit
@@ -131,19 +135,22 @@ int plan_units(int B, int H, int Hkv, int Nq, int d, int num_pages, int page_siz
   if ((long long)(H / Hkv) * Nq > kMaxRows) return FA_ERR_UNSUPPORTED;
   std::memset(pl, 0, sizeof(*pl));
   pl->rows = (H / Hkv) * Nq;
-  int unit_cost = 0;
-  fa::kv4_fwd_shape(d, pl->rows, &pl->unit_rows, &pl->step_keys, &unit_cost);
-  pl->row_blocks = (pl->rows + pl->unit_rows - 1) / pl->unit_rows;
-  pl->units = B * Hkv * pl->row_blocks;
+  pl->step_keys = fa::kv4_fwd_step_keys();
   const long long held = (long long)max_pages * page_size;
   pl->max_steps = (int)((held + pl->step_keys - 1) / pl->step_keys);
-  if ((long long)pl->units * (pl->max_steps + unit_cost) > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   pl->whole = pl->max_steps <= kWholeSteps ? 1 : 0;
   pl->launches = pl->whole ? 1 : 2;
-  return FA_OK;
+  // With the fewest rows a unit may have.
+  const long long places = (long long)B * Hkv * units_of(pl->rows, fa::kv4_fwd_unit_rows(d, pl->rows, 0)) *
+                           (pl->max_steps + fa::kv4_fwd_unit_cost());
+  return places > 0x7fffffffLL ? FA_ERR_INVALID_ARG : FA_OK;
 }
 
-void plan_grid(int d, int sm_count, fa_kv4_plan_t* pl) {
+void plan_grid(int B, int Hkv, int d, int sm_count, fa_kv4_plan_t* pl) {
+  const long long steps = (long long)B * Hkv * units_of(pl->rows, fa::kv4_fwd_unit_rows(d, pl->rows, 0)) * pl->max_steps;
+  pl->unit_rows = fa::kv4_fwd_unit_rows(d, pl->rows, steps / sm_count);
+  pl->row_blocks = units_of(pl->rows, pl->unit_rows);
+  pl->units = B * Hkv * pl->row_blocks;
   const long long most = (long long)pl->units * (pl->whole ? 1 : pl->max_steps);
   pl->grid = (int)std::min<long long>(most, sm_count);
   if (!pl->whole)
@@ -190,7 +197,7 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
   int sm_count = 0;
   e = fa::internal_device_setup(&status, &sm_count);
   if (e) return e;
-  plan_grid(d, sm_count, &pl);
+  plan_grid(B, Hkv, d, sm_count, &pl);
   Fwd f;
   f.d = d;
   f.unit_rows = pl.unit_rows;
@@ -235,7 +242,7 @@ int fa_kv4_fwd_plan(int B, int H, int Hkv, int Nq, int d, int page_size, int max
   fa_kv4_plan_t pl;
   const int e = plan_units(B, H, Hkv, Nq, d, 1, page_size, max_pages, FA_CAUSAL_NONE, &pl);
   if (e) return e;
-  plan_grid(d, sm_count, &pl);
+  plan_grid(B, Hkv, d, sm_count, &pl);
   *plan = pl;
   return FA_OK;
 }

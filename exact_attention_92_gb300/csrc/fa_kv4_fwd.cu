@@ -980,17 +980,22 @@ cudaError_t launch_merge_d(int unit_rows, const Kv4FwdParams& p, int grid, cudaS
 
 }  // namespace
 
-// Rows of a unit and keys of a step for head dim d and `rows` query rows a
-// key/value head.  Up to four rows leave half of a tile's columns free for a
-// second block of keys, which halves what a step spends on softmax (PACK).  Two
-// row tiles a unit only where one does not hold the rows, and not at d = 256,
-// whose sums take 64 registers a tile.
-void kv4_fwd_shape(int d, int rows, int* unit_rows, int* step_keys, int* unit_cost) {
-  const bool two = rows > kKv4Rows && d != 256;
-  *unit_rows = rows <= kKv4Rows / 2 ? kKv4Rows / 2 : (two ? 2 * kKv4Rows : kKv4Rows);
-  *step_keys = Cfg<64, 1, false>::kKeys;
-  *unit_cost = kUnitCost;
+// Query rows of a unit for head dim d and `rows` query rows a key/value head.
+// Up to four rows leave half of a tile's columns free for a second block of
+// keys, which halves what a step spends on softmax (PACK).  Above eight, two row
+// tiles a unit read and decode each key once for 16 rows, but leave room for
+// fewer warps: where there are few steps to an SM (`sm_steps`, with one tile a
+// unit), one tile is sooner done (d = 128, 16 rows, 8 heads: 4 sequences of 1000
+// tokens, 26 steps an SM, 10.7 us and 12.6 with two; 8 of 4000, 105 steps, 21.9
+// and 23.1; 16 of 4000, 210 steps, 35.5 and 33.0; d = 64 and 96 alike).  Not at
+// d = 256, whose sums take 64 registers a tile.
+int kv4_fwd_unit_rows(int d, int rows, long long sm_steps) {
+  if (rows <= kKv4Rows / 2) return kKv4Rows / 2;
+  return rows > kKv4Rows && d != 256 && sm_steps >= 160 ? 2 * kKv4Rows : kKv4Rows;
 }
+
+int kv4_fwd_step_keys() { return Cfg<64, 1, false>::kKeys; }
+int kv4_fwd_unit_cost() { return kUnitCost; }
 
 cudaError_t launch_kv4_fwd(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream) {
   switch (d) {

@@ -526,10 +526,11 @@ def test_every_count_of_query_rows(fa, d, rows):
     lens = [47, 600, 5]
     f = Filled(fa, rng, lens, 2, d, 32)
     qd, q = normal(rng, (3, 2 * rows, 1, d))
-    wide = np.full((3, 64), -1, np.int32)
+    # 6 heads' units, room for 6144 steps each: two row tiles a unit above 8 rows.
+    wide = np.full((3, 6144), -1, np.int32)
     wide[:, :f.table.shape[1]] = f.table
     short = Filled(fa, rng, [47, 33, 0], 2, d, 16)
-    for g, table, n in ((f, ints(wide), lens), (short, short.td, [47, 33, 0])):
+    for g, table, n in ((f, ints(wide), lens), (f, f.td, lens), (short, short.td, [47, 33, 0])):
         o, lse = fa.kv4_forward(qd, g.cache, table, g.ld)
         assert fa.fa_poll_status() == fa.FA_OK
         check_attend(o, lse, q, g.k, g.v, n, d ** -0.5, "none", f"rows={rows}")
