@@ -310,36 +310,107 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, causal=False, scale=None, 
 
 
 # The calls over the 4-bit cache are made once a layer and decoding step, where
-# the time of their checks shows (18 us a call when each was checked by
-# itself, 8 us so): all are looked at in one expression, what is wrong is worked
-# out after that, and the device and the stream are asked for without building
-# objects.
+# the time of marshalling shows: they go through a native caller (_kv4_call.so,
+# csrc/kv4_call.cpp) that looks at the tensors and calls libfa.so, some 4 us a
+# call on a GB300's host in place of 7 through ctypes and 18 with each tensor
+# checked by itself.  It says only that something is wrong; what, is worked out
+# after that.
 
 _torch = None
+_kv4 = None
 
 
-def _torch_cuda():
-    """(torch, current CUDA device)."""
-    global _torch
-    if _torch is None:
+class _Kv4Ctypes:
+    """What the native caller does, through ctypes: for a package that was
+    built without torch's headers."""
+
+    def __init__(self, lib):
+        self.lib = lib
+
+    @staticmethod
+    def _good(tensors, device):
+        return all(isinstance(t, _torch.Tensor) and t.dtype is dtype and t.dim() == len(shape) and t.is_contiguous()
+                   and t.is_cuda and t.get_device() == device
+                   and all(w is None or n == w for n, w in zip(t.shape, shape)) for t, dtype, shape in tensors)
+
+    def move(self, write, k, v, cache, block_table, start, count, device, stream):
+        bf16, i32 = _torch.bfloat16, _torch.int32
+        shape = getattr(k, "shape", ())
+        if len(shape) != 4:
+            return -1
+        B, Hkv, N, d = shape
+        args = [(k, bf16, shape), (v, bf16, shape), (cache, _torch.uint8, (None, Hkv, None)),
+                (block_table, i32, (B, None)), (start, i32, (B,))]
+        if not self._good(args if count is None else args + [(count, i32, (B,))], device):
+            return -1
+        page_size, rest = divmod(cache.shape[2] * 8, 9 * d) if d else (0, 0)
+        if rest or not page_size:
+            return -1
+        kv = (k.data_ptr(), v.data_ptr())
+        arrays = (block_table.data_ptr(), start.data_ptr(), None if count is None else count.data_ptr())
+        sizes = (B, Hkv, N, d, cache.shape[0], page_size, block_table.shape[1], stream)
+        if write:
+            return self.lib.fa_kv4_write(*kv, cache.data_ptr(), *arrays, *sizes)
+        return self.lib.fa_kv4_read(cache.data_ptr(), *arrays, *kv, *sizes)
+
+    def fwd(self, q, cache, block_table, lens, o, lse, causal, scale, device, stream):
+        shape = getattr(q, "shape", ())
+        if len(shape) != 4:
+            return -1
+        B, H, Nq, d = shape
+        if not self._good([(q, _torch.bfloat16, shape), (o, _torch.bfloat16, shape), (lens, _torch.int32, (B,)),
+                           (cache, _torch.uint8, (None,) * 3), (block_table, _torch.int32, (B, None)),
+                           (lse, _torch.float32, (B, H, Nq))], device):
+            return -1
+        page_size, rest = divmod(cache.shape[2] * 8, 9 * d) if d else (0, 0)
+        if rest or not page_size:
+            return -1
+        return self.lib.fa_kv4_fwd(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+                                   o.data_ptr(), lse.data_ptr(), B, H, cache.shape[1], Nq, d, cache.shape[0], page_size,
+                                   block_table.shape[1], causal, 1.0 / math.sqrt(d) if scale is None else scale, stream)
+
+
+def _kv4_caller():
+    """The caller, and with it torch; made at the first call."""
+    global _torch, _kv4
+    if _kv4 is None:
         import torch
 
+        lib = load()
         _torch = torch
+        try:
+            from . import _kv4_call as native
+        except ImportError:
+            _kv4 = _Kv4Ctypes(lib)
+        else:
+            native.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                          for name in ("fa_kv4_write", "fa_kv4_read", "fa_kv4_fwd")))
+            _kv4 = native
+    return _kv4
+
+
+def _device_and_stream(stream):
+    """The current CUDA device, and the stream's handle on it."""
     try:
-        return _torch, _torch._C._cuda_getDevice()
+        device = _torch._C._cuda_getDevice()
     except (AttributeError, RuntimeError):
-        return _torch, None  # no CUDA device: any argument is refused
+        return -1, 0  # no CUDA device: any tensor is refused
+    if stream is None:
+        return device, _torch._C._cuda_getCurrentRawStream(device)
+    return device, int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-# What causal and scale are usually given as.
+# What causal is usually given as.
 _CAUSAL_CODES = {False: FA_CAUSAL_NONE, True: FA_CAUSAL_TOP_LEFT, FA_CAUSAL_BOTTOM_RIGHT: FA_CAUSAL_BOTTOM_RIGHT,
                  **_CAUSAL_NAMES}
-_DEFAULT_SCALES = {d: _scale(None, d) for d in (64, 96, 128, 256)}
 
 
-def _refuse(tensors, device):
-    """Raises for the first of (name, tensor, type, shape) that is not a
-    contiguous tensor of that type and shape on the current device."""
+def _kv4_refuse(what, status, tensors, device, heads, d):
+    """Raises for a status that is not FA_OK.  -1: for the first of (name,
+    tensor, type, shape) that is not a contiguous tensor of that type and shape
+    on the current device, or for a cache of other heads or page bytes."""
+    if status > 0:
+        raise FaError(status, what)
     for name, t, dtype, shape in tensors:
         if not isinstance(t, _torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -349,20 +420,12 @@ def _refuse(tensors, device):
                              f"got {t.dtype} {tuple(t.shape)}")
         if t.get_device() != device:
             raise ValueError(f"{name} is on {t.device}, not on the current CUDA device (use torch.cuda.device)")
-    raise ValueError("the arguments do not fit together")
-
-
-def _page_size(page_bytes, d):
-    page_size, rest = divmod(page_bytes * 8, 9 * d) if d > 0 else (0, 1)
-    if rest or page_size < 1:
-        raise ValueError(f"cache has {page_bytes} bytes a page and head, not a multiple of 9 * {d} / 8")
-    return page_size
-
-
-def _raw_stream(stream, device):
-    if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(device)
-    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    cache = next(t for name, t, _, _ in tensors if name == "cache")
+    if heads is not None and cache.shape[1] != heads:
+        raise ValueError(f"cache has {cache.shape[1]} heads, k has {heads}")
+    if d == 0 or cache.shape[2] * 8 % (9 * d) or cache.shape[2] == 0:
+        raise ValueError(f"cache has {cache.shape[2]} bytes a page and head, not a multiple of 9 * {d} / 8")
+    raise ValueError(f"{what}: a size is out of range")
 
 
 def fa_kv4_cache_bytes(num_pages, Hkv, page_size, d) -> int:
@@ -373,92 +436,50 @@ def fa_kv4_cache_bytes(num_pages, Hkv, page_size, d) -> int:
     return n.value
 
 
-def _kv4_move(k, v, cache, block_table, start, count):
-    torch, device = _torch_cuda()
-    bf16, i32 = torch.bfloat16, torch.int32
-    try:
-        B, Hkv, N, d = k.shape
-        num_pages, heads, page_bytes = cache.shape
-        rows, max_pages = block_table.shape
-        good = (k.dtype is bf16 and k.get_device() == device and k.is_contiguous()
-                and v.dtype is bf16 and v.get_device() == device and v.is_contiguous() and v.shape == k.shape
-                and cache.dtype is torch.uint8 and cache.get_device() == device and cache.is_contiguous()
-                and block_table.dtype is i32 and block_table.get_device() == device and block_table.is_contiguous()
-                and start.dtype is i32 and start.get_device() == device and start.is_contiguous()
-                and start.shape == (B,) and rows == B
-                and (count is None or count.dtype is i32 and count.get_device() == device and count.is_contiguous()
-                     and count.shape == (B,)))
-    except (AttributeError, ValueError):
-        good = False
-    if not good:
-        first = tuple(getattr(k, "shape", ()))
-        B, Hkv, N, d = first if len(first) == 4 else (None,) * 4
-        args = [("k", k, bf16, (B, Hkv, N, d)), ("v", v, bf16, (B, Hkv, N, d)),
-                ("cache", cache, torch.uint8, (None, None, None)), ("block_table", block_table, i32, (B, None)),
-                ("start", start, i32, (B,))]
-        _refuse(args if count is None else args + [("count", count, i32, (B,))], device)
-    if heads != Hkv:
-        raise ValueError(f"cache has {heads} heads, k has {Hkv}")
-    return device, (B, Hkv, N, d, num_pages, _page_size(page_bytes, d), max_pages)
+def _kv4_move(what, write, k, v, cache, block_table, start, count, stream):
+    caller = _kv4 or _kv4_caller()
+    device, raw = _device_and_stream(stream)
+    status = caller.move(write, k, v, cache, block_table, start, count, device, raw)
+    if status != FA_OK:
+        bf16, i32 = _torch.bfloat16, _torch.int32
+        shape = tuple(getattr(k, "shape", ()))
+        B, Hkv, N, d = shape if len(shape) == 4 else (None,) * 4
+        tensors = [("k", k, bf16, (B, Hkv, N, d)), ("v", v, bf16, (B, Hkv, N, d)),
+                   ("cache", cache, _torch.uint8, (None, None, None)), ("block_table", block_table, i32, (B, None)),
+                   ("start", start, i32, (B,))]
+        _kv4_refuse(what, status, tensors if count is None else tensors + [("count", count, i32, (B,))], device, Hkv, d)
 
 
 def fa_kv4_write(k, v, cache, block_table, start, count=None, stream=None):
     """C fa_kv4_write: quantise tokens k, v [B, Hkv, N, d] into the 4-bit
     cache [num_pages, Hkv, page_size * 9 d / 8] (uint8), token i < count[b]
     (all N without count) of sequence b to position start[b] + i."""
-    device, sizes = _kv4_move(k, v, cache, block_table, start, count)
-    status = (_lib or load()).fa_kv4_write(
-        k.data_ptr(), v.data_ptr(), cache.data_ptr(), block_table.data_ptr(), start.data_ptr(),
-        None if count is None else count.data_ptr(), *sizes, _raw_stream(stream, device))
-    if status != FA_OK:
-        raise FaError(status, "fa_kv4_write")
+    _kv4_move("fa_kv4_write", True, k, v, cache, block_table, start, count, stream)
 
 
 def fa_kv4_read(cache, block_table, start, k, v, count=None, stream=None):
     """C fa_kv4_read: the held values of positions start[b] + i to rows
     i < count[b] of k, v [B, Hkv, N, d]; other rows are left as they were."""
-    device, sizes = _kv4_move(k, v, cache, block_table, start, count)
-    status = (_lib or load()).fa_kv4_read(
-        cache.data_ptr(), block_table.data_ptr(), start.data_ptr(), None if count is None else count.data_ptr(),
-        k.data_ptr(), v.data_ptr(), *sizes, _raw_stream(stream, device))
-    if status != FA_OK:
-        raise FaError(status, "fa_kv4_read")
+    _kv4_move("fa_kv4_read", False, k, v, cache, block_table, start, count, stream)
 
 
 def fa_kv4_fwd(q, cache, block_table, lens, o, lse, causal=False, scale=None, stream=None):
     """C fa_kv4_fwd: attention of q [B, H, Nq, d] over the first lens[b]
     tokens of each sequence in the 4-bit cache; causal as fa_fwd_general."""
-    torch, device = _torch_cuda()
-    bf16, i32 = torch.bfloat16, torch.int32
-    try:
-        B, H, Nq, d = q.shape
-        num_pages, Hkv, page_bytes = cache.shape
-        rows, max_pages = block_table.shape
-        good = (q.dtype is bf16 and q.get_device() == device and q.is_contiguous()
-                and o.dtype is bf16 and o.get_device() == device and o.is_contiguous() and o.shape == q.shape
-                and cache.dtype is torch.uint8 and cache.get_device() == device and cache.is_contiguous()
-                and block_table.dtype is i32 and block_table.get_device() == device and block_table.is_contiguous()
-                and lens.dtype is i32 and lens.get_device() == device and lens.is_contiguous() and lens.shape == (B,)
-                and rows == B and lse.dtype is torch.float32 and lse.get_device() == device
-                and lse.is_contiguous() and lse.shape == (B, H, Nq))
-    except (AttributeError, ValueError):
-        good = False
-    if not good:
-        first = tuple(getattr(q, "shape", ()))
-        B, H, Nq, d = first if len(first) == 4 else (None,) * 4
-        _refuse([("q", q, bf16, (B, H, Nq, d)), ("cache", cache, torch.uint8, (None, None, None)),
-                 ("block_table", block_table, i32, (B, None)), ("lens", lens, i32, (B,)),
-                 ("o", o, bf16, (B, H, Nq, d)), ("lse", lse, torch.float32, (B, H, Nq))], device)
-    page_size = _page_size(page_bytes, d)
+    caller = _kv4 or _kv4_caller()
+    device, raw = _device_and_stream(stream)
     code = _CAUSAL_CODES.get(causal)
     if code is None:
         code = _causal_code(causal)
-    scale = _DEFAULT_SCALES.get(d, 1.0) if scale is None else float(scale)
-    status = (_lib or load()).fa_kv4_fwd(
-        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv,
-        Nq, d, num_pages, page_size, max_pages, code, scale, _raw_stream(stream, device))
+    status = caller.fwd(q, cache, block_table, lens, o, lse, code, scale, device, raw)
     if status != FA_OK:
-        raise FaError(status, "fa_kv4_fwd")
+        shape = tuple(getattr(q, "shape", ()))
+        B, H, Nq, d = shape if len(shape) == 4 else (None,) * 4
+        _kv4_refuse("fa_kv4_fwd", status,
+                    [("q", q, _torch.bfloat16, (B, H, Nq, d)), ("cache", cache, _torch.uint8, (None, None, None)),
+                     ("block_table", block_table, _torch.int32, (B, None)), ("lens", lens, _torch.int32, (B,)),
+                     ("o", o, _torch.bfloat16, (B, H, Nq, d)), ("lse", lse, _torch.float32, (B, H, Nq))],
+                    device, None, d)
 
 
 def fa_poll_status(stream=None):

@@ -22,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
+CALL_SOURCE = os.path.join(CSRC, "kv4_call.cpp")
+CALL = os.path.join(PKG, "_kv4_call.so")
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd256.cu", "fa_bwd.cu", "fa_bwd_pair.cu", "fa_bwd256.cu", "fa_noalloc.cu",
            "fa_kv4.cu", "fa_kv4_move.cu", "fa_kv4_fwd.cu"]
@@ -78,8 +80,45 @@ def check_spills(ptxas_log: str) -> None:
                     raise RuntimeError(f"{entry} starts with {m.group(1)} registers, its register split needs {regs}")
 
 
+def build_call(force: bool = False) -> str | None:
+    """Compile the native caller of the 4-bit cache's entry points (_kv4_call.so,
+    against torch's and Python's headers); None where torch is not installed.
+    It holds no device code: without it the binding makes the same calls through
+    ctypes."""
+    import importlib.util
+    import sysconfig
+
+    spec = importlib.util.find_spec("torch")  # found, not imported
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    if not force and os.path.exists(CALL) and os.path.getmtime(CALL) >= max(
+            os.path.getmtime(CALL_SOURCE), os.path.getmtime(__file__)):
+        return CALL
+    torch_dir = list(spec.submodule_search_locations)[0]
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    tmp = CALL + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+           CALL_SOURCE, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed on {CALL_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
+    return CALL
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile and link libfa.so if any source is newer than it; return its path."""
+    """Compile and link libfa.so if any source is newer than it, and the native
+    caller (build_call); return libfa.so's path."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        call = ex.submit(build_call, force)
+        path = _build_lib(force, verbose, ptxas_verbose)
+        call.result()
+    return path
+
+
+def _build_lib(force: bool, verbose: bool, ptxas_verbose: bool) -> str:
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps() and not ptxas_verbose:
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -259,7 +259,45 @@ def test_launch_count_and_status_name(lib):
         assert lib.fa_launch_count(kid, ctypes.byref(n)) == fa.FA_ERR_INVALID_ARG
 
 
-def test_binding_refuses_host_tensors(lib):
+@pytest.fixture(params=["native", "ctypes"])
+def caller(lib, request, monkeypatch):
+    """The binding with its native caller, and with the one that does without."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(_binding, "_torch", torch)
+    made = _binding._kv4_caller()
+    if request.param == "native":
+        assert made.__name__.endswith("_kv4_call"), "the native caller is built where torch is installed"
+    else:
+        made = _binding._Kv4Ctypes(lib)
+    monkeypatch.setattr(_binding, "_kv4", made)
+    return made
+
+
+def test_callers_refuse_what_is_no_tensor(caller):
+    for bad in (None, 3, "x", [1]):
+        assert caller.move(True, bad, bad, bad, bad, bad, None, 0, 0) == -1
+        assert caller.fwd(bad, bad, bad, bad, bad, bad, 0, None, 0, 0) == -1
+        with pytest.raises(TypeError):
+            fa.fa_kv4_write(bad, bad, bad, bad, bad)
+        with pytest.raises(TypeError):
+            fa.fa_kv4_fwd(bad, bad, bad, bad, bad, bad)
+    with pytest.raises(ValueError):
+        fa.fa_kv4_fwd(None, None, None, None, None, None, causal="sideways")
+
+
+def test_native_caller_checks_its_numbers(lib):
+    pytest.importorskip("torch")
+    native = _binding._kv4_caller()
+    for args in ((), (1, 2), (None,) * 10):
+        with pytest.raises(TypeError):
+            native.fwd(*args)
+        with pytest.raises(TypeError):
+            native.move(*args)
+        with pytest.raises(TypeError):
+            native.bind(*args)
+
+
+def test_binding_refuses_host_tensors(caller):
     torch = pytest.importorskip("torch")
     k = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
     cache = torch.zeros(3, 2, 16 * 72, dtype=torch.uint8)

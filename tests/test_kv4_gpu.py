@@ -45,6 +45,18 @@ def fa():
     return ensure_built()
 
 
+@pytest.fixture(params=["native", "ctypes"])
+def caller(fa, request, monkeypatch):
+    """The binding with its native caller, and with the one that does without."""
+    from exact_attention_92_gb300 import _binding
+
+    made = _binding._kv4_caller()
+    assert made.__name__.endswith("_kv4_call")
+    if request.param == "ctypes":
+        monkeypatch.setattr(_binding, "_kv4", _binding._Kv4Ctypes(fa.load()))
+    return request.param
+
+
 def ints(x):
     return torch_cuda().tensor(x, dtype=torch_cuda().int32, device="cuda")
 
@@ -454,7 +466,7 @@ def test_bad_lengths_and_positions_are_clamped_and_reported(fa):
     check_attend(o, lse, q, f.k, f.v, [32, 32], d ** -0.5, "none")
 
 
-def test_binding_refusals(fa):
+def test_binding_refusals(fa, caller):
     torch = torch_cuda()
     rng = np.random.default_rng(9)
     f = Filled(fa, rng, [32], 2, 64, 16)
@@ -470,6 +482,14 @@ def test_binding_refusals(fa):
         args[i] = bad
         with pytest.raises((ValueError, TypeError, fa.FaError)):
             fa.kv4_forward(*args)
+    o, lse = torch.empty_like(q), torch.empty((1, 4, 1), device="cuda")
+    for bad_o, bad_lse in ((o[:, :2], lse), (o.half(), lse), (o, lse.half()), (o, lse[:, :, 0]), (o.cpu(), lse),
+                           (o, lse.cpu())):
+        with pytest.raises(ValueError):
+            fa.fa_kv4_fwd(q, f.cache, f.td, f.ld, bad_o, bad_lse)
+    with pytest.raises(fa.FaError):
+        fa.fa_kv4_fwd(q, f.cache, f.td, f.ld, o, lse, scale=-1.0)
+    fa.fa_kv4_fwd(q, f.cache, f.td, f.ld, o, lse, causal=fa.FA_CAUSAL_BOTTOM_RIGHT, scale=1, stream=0)
     with pytest.raises(fa.FaError) as e:  # 24-token pages
         fa.kv4_forward(q, torch.zeros((4, 2, 24 * 72), dtype=torch.uint8, device="cuda"), f.td, f.ld)
     assert e.value.status == fa.FA_ERR_INVALID_ARG
@@ -485,7 +505,7 @@ def test_binding_refusals(fa):
     assert fa.fa_poll_status() == fa.FA_OK
 
 
-def test_misaligned_storage_is_refused(fa):
+def test_misaligned_storage_is_refused(fa, caller):
     torch = torch_cuda()
     raw = torch.zeros(4 * 2 * 16 * 72 + 16, dtype=torch.uint8, device="cuda")
     q = torch.zeros((1, 4, 1, 64), dtype=torch.bfloat16, device="cuda")
@@ -556,7 +576,7 @@ def test_waits_that_give_up_are_reported(fa):
 # --------------------------------------------------------- used together
 
 @pytest.mark.parametrize("d", (64, 128, 256))
-def test_prompt_chunk_and_steps(fa, d):
+def test_prompt_chunk_and_steps(fa, caller, d):
     """A prompt is written, a second chunk attends over the history read back
     (the bf16 kernels) and is written too, then single tokens are appended and
     attended to: every result is that of the held values."""
