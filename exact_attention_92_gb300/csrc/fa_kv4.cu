@@ -214,6 +214,7 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
   f.p.causal = causal;
   f.p.scale_log2 = scale * 1.4426950408889634f;
   f.p.whole = pl.whole;
+  f.p.single = pl.whole && pl.grid == pl.units ? 1 : 0;
   f.p.part_o = nullptr;
   f.p.part_ml = nullptr;
   f.p.cuts = nullptr;

@@ -251,27 +251,38 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     return n == 0 ? 1 : (n + C::kKeys - 1) / C::kKeys;
   };
 
+  auto length = [&](int b) { return kv4_length(p.c, p.lens[b]); };
+  Piece ahead;
+  ahead.lo = ahead.hi = 0;
+  const int* row = nullptr;  // of the block table
+  auto sequence = [&] {
+    ahead.len = uniform(length(ahead.b));
+    ahead.steps = steps_of(ahead.len);
+    row = p.c.table + (size_t)ahead.b * p.c.max_pages;
+  };
+
   // ---- the list (the host has checked that its places fit 31 bits).  Every
   // warp works it out for itself, each lane adding up a run of sequences: the
   // warps need not wait for each other before their copies are on the way.
-  auto length = [&](int b) { return kv4_length(p.c, p.lens[b]); };
   const int run = (p.c.B + 31) / 32;
-  int upto = 0;
-  const int b_end = min(p.c.B, lane * run + run);
-  for (int b = lane * run; b < b_end; b += 4) {
-    int n[4];
+  int upto = 0, total = 0;
+  if (!p.single) {
+    const int b_end = min(p.c.B, lane * run + run);
+    for (int b = lane * run; b < b_end; b += 4) {
+      int n[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n[i] = b + i < b_end ? p.lens[b + i] : 0;
+      for (int i = 0; i < 4; ++i) n[i] = b + i < b_end ? p.lens[b + i] : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (b + i < b_end) upto += kUnitCost + steps_of(kv4_length(p.c, n[i]));
+      for (int i = 0; i < 4; ++i)
+        if (b + i < b_end) upto += kUnitCost + steps_of(kv4_length(p.c, n[i]));
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    total = __shfl_sync(0xffffffffu, upto, 31) * units;
   }
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += x;
-  }
-  const int total = __shfl_sync(0xffffffffu, upto, 31) * units;
   if (tid == 0 && !p.whole) p.cuts[blockIdx.x].row = -1;
   // Sequence, unit, place within it and places of the unit at list place x.
   struct Found {
@@ -291,37 +302,39 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     f.off = rest - f.u * f.places;
     return f;
   };
-  // CTAs that take part: a place for every warp, or a unit each.  The first
-  // `more` have a place more than the others.
-  const int active = min((int)gridDim.x, max(total / W, p.c.B * units));
-  if ((int)blockIdx.x >= active) return;
-  const int each = total / active, more = total - each * active;
+  // This CTA's stretch of the list: [first, end).  CTAs that take part: a place
+  // for every warp, or a unit each; the first `more` have a place more than the
+  // others.  Where every unit has a CTA of its own, the list need not be known.
+  int each = 1, more = 0, first = 0, end = 0;
+  if (p.single) {
+    ahead.b = (int)blockIdx.x / units;
+    ahead.u = (int)blockIdx.x - ahead.b * units;
+    sequence();
+    end = kUnitCost + ahead.steps;
+  } else {
+    const int active = min((int)gridDim.x, max(total / W, p.c.B * units));
+    if ((int)blockIdx.x >= active) return;
+    each = total / active;
+    more = total - each * active;
+    first = (int)blockIdx.x * each + min((int)blockIdx.x, more);
+    end = first + each + ((int)blockIdx.x < more ? 1 : 0);
+    if (p.whole) {  // the units that begin in the stretch
+      const Found f = find(first);
+      if (f.off > 0) first += f.places - f.off;
+      if (end < total) {
+        const Found e = find(end);
+        if (e.off > 0) end += e.places - e.off;
+      }
+    }
+    if (first >= end) return;
+  }
   auto cta_of = [&](int place) {
     return place < more * (each + 1) ? place / (each + 1) : more + (place - more * (each + 1)) / each;
   };
-  int first = (int)blockIdx.x * each + min((int)blockIdx.x, more);
-  int end = first + each + ((int)blockIdx.x < more ? 1 : 0);
-  if (p.whole) {  // the units that begin in the stretch
-    const Found f = find(first);
-    if (f.off > 0) first += f.places - f.off;
-    if (end < total) {
-      const Found e = find(end);
-      if (e.off > 0) end += e.places - e.off;
-    }
-  }
-  if (first >= end) return;
   // ---- this warp's stretch of it, walked by the copies
   const int warp_each = (end - first) / W, warp_more = (end - first) - warp_each * W;
   int at = first + warp * warp_each + min(warp, warp_more);
   const int my_end = at + warp_each + (warp < warp_more ? 1 : 0);
-  Piece ahead;
-  ahead.lo = ahead.hi = 0;
-  const int* row = nullptr;  // of the block table
-  auto sequence = [&] {
-    ahead.len = uniform(length(ahead.b));
-    ahead.steps = steps_of(ahead.len);
-    row = p.c.table + (size_t)ahead.b * p.c.max_pages;
-  };
   int made = 0, taken = 0;  // pieces put into the queue, and taken out
   auto enter = [&](int off) {
     ahead.head = p.row_blocks == 1 ? ahead.u : ahead.u / p.row_blocks;
@@ -356,11 +369,15 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     enter(0);
   };
   if (at < my_end) {
-    const Found f = find(at);
-    ahead.b = f.b;
-    ahead.u = f.u;
-    sequence();
-    enter(f.off);
+    if (p.single) {
+      enter(at);
+    } else {
+      const Found f = find(at);
+      ahead.b = f.b;
+      ahead.u = f.u;
+      sequence();
+      enter(f.off);
+    }
   }
 
   // A copy takes the blocks of a step that lie in one page, all of them where

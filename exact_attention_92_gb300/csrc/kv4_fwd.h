@@ -33,6 +33,7 @@ struct Kv4FwdParams {
   int causal;              // FA_CAUSAL_*
   float scale_log2;        // scale * log2(e)
   int whole;               // 1: units are not cut
+  int single;              // 1: nor does a CTA have more than one
   float* part_o;           // [2 * grid][rows of a unit][d]: partial sums (not whole)
   float2* part_ml;         // [2 * grid][rows of a unit]: reference and sum
   Kv4Cut* cuts;            // [grid]
