@@ -18,6 +18,7 @@ cudaError_t launch_kv4_move(int d, bool write, const Kv4Cache& c, const int* sta
                             const void* v_in, void* k_out, void* v_out, int N, int sm_count, cudaStream_t stream);
 int kv4_fwd_unit_rows(int d, int rows, long long sm_steps);
 int kv4_fwd_step_keys();
+int kv4_fwd_warps(int d, int unit_rows);
 int kv4_fwd_unit_cost();
 cudaError_t launch_kv4_fwd(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_kv4_merge(int d, int unit_rows, const Kv4FwdParams& p, int grid, cudaStream_t stream);
@@ -138,8 +139,6 @@ int plan_units(int B, int H, int Hkv, int Nq, int d, int num_pages, int page_siz
   pl->step_keys = fa::kv4_fwd_step_keys();
   const long long held = (long long)max_pages * page_size;
   pl->max_steps = (int)((held + pl->step_keys - 1) / pl->step_keys);
-  pl->whole = pl->max_steps <= kWholeSteps ? 1 : 0;
-  pl->launches = pl->whole ? 1 : 2;
   // With the fewest rows a unit may have.
   const long long places = (long long)B * Hkv * units_of(pl->rows, fa::kv4_fwd_unit_rows(d, pl->rows, 0)) *
                            (pl->max_steps + fa::kv4_fwd_unit_cost());
@@ -151,6 +150,14 @@ void plan_grid(int B, int Hkv, int d, int sm_count, fa_kv4_plan_t* pl) {
   pl->unit_rows = fa::kv4_fwd_unit_rows(d, pl->rows, steps / sm_count);
   pl->row_blocks = units_of(pl->rows, pl->unit_rows);
   pl->units = B * Hkv * pl->row_blocks;
+  // Where every unit has a CTA of its own, up to three steps a warp, and four if
+  // that keeps half the SMs busy (8 heads of d = 128: one sequence of 1000 tokens
+  // 8.3 us, cut 9.2, of 1500 9.8 and 9.2; 16 of 1500 10.5 and 13.3; alike at
+  // d = 64 and 256 with their 16 and 8 warps).
+  const int warps = fa::kv4_fwd_warps(d, pl->unit_rows);
+  const int single = pl->units > sm_count ? 0 : (2 * pl->units >= sm_count ? 4 : 3) * warps;
+  pl->whole = pl->max_steps <= std::max(kWholeSteps, single) ? 1 : 0;
+  pl->launches = pl->whole ? 1 : 2;
   const long long most = (long long)pl->units * (pl->whole ? 1 : pl->max_steps);
   pl->grid = (int)std::min<long long>(most, sm_count);
   if (!pl->whole)

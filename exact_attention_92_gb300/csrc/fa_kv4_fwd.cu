@@ -1011,6 +1011,25 @@ int kv4_fwd_unit_rows(int d, int rows, long long sm_steps) {
   return rows > kKv4Rows && d != 256 && sm_steps >= 160 ? 2 * kKv4Rows : kKv4Rows;
 }
 
+template <int D>
+static int warps_d(int unit_rows) {
+  if (unit_rows == kKv4Rows / 2) return Cfg<D, 1, true>::kWarps;
+  if constexpr (D != 256) {
+    if (unit_rows == 2 * kKv4Rows) return Cfg<D, 2, false>::kWarps;
+  }
+  return Cfg<D, 1, false>::kWarps;
+}
+
+// Warps of a CTA.
+int kv4_fwd_warps(int d, int unit_rows) {
+  switch (d) {
+    case 64: return warps_d<64>(unit_rows);
+    case 96: return warps_d<96>(unit_rows);
+    case 128: return warps_d<128>(unit_rows);
+    default: return warps_d<256>(unit_rows);
+  }
+}
+
 int kv4_fwd_step_keys() { return Cfg<64, 1, false>::kKeys; }
 int kv4_fwd_unit_cost() { return kUnitCost; }
 

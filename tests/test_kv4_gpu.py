@@ -525,7 +525,7 @@ def test_misaligned_storage_is_refused(fa, caller):
 
 def test_workspace_allocation_failure_is_reported(fa, monkeypatch):
     rng = np.random.default_rng(10)
-    f = Filled(fa, rng, [900], 1, 64, 16)
+    f = Filled(fa, rng, [9000], 1, 64, 16)  # cut between CTAs, so that partial results need workspace
     qd, q = normal(rng, (1, 2, 1, 64))
     monkeypatch.setenv("FA_TEST_FAIL_ALLOC", "1")
     with pytest.raises(fa.FaError) as e:
@@ -534,7 +534,7 @@ def test_workspace_allocation_failure_is_reported(fa, monkeypatch):
     monkeypatch.delenv("FA_TEST_FAIL_ALLOC")
     o, lse = fa.kv4_forward(qd, f.cache, f.td, f.ld)
     assert fa.fa_poll_status() == fa.FA_OK
-    check_attend(o, lse, q, f.k, f.v, [900], 64 ** -0.5, "none")
+    check_attend(o, lse, q, f.k, f.v, [9000], 64 ** -0.5, "none")
 
 
 @pytest.mark.parametrize("rows", (1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 33))
@@ -699,7 +699,7 @@ def test_launches_are_counted(fa):
     assert [fa.fa_launch_count(i) - n for i, n in zip(ids, before)] == [1, 1, 1, 0]
     # The call follows its plan: a table for many tokens means a merge.
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    wide = ints(np.repeat(f.table, 20, 1))
+    wide = ints(np.repeat(f.table, 200, 1))
     for table in (f.td, wide):
         plan = fa.fa_kv4_fwd_plan(1, 1, 1, 1, 64, 16, table.shape[1], sms)
         before = [fa.fa_launch_count(i) for i in ids[2:]]
