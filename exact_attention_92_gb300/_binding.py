@@ -311,8 +311,8 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, causal=False, scale=None, 
 
 # The calls over the 4-bit cache are made once a layer and decoding step, where
 # the time of marshalling shows: they go through a native caller (_kv4_call.so,
-# csrc/kv4_call.cpp) that looks at the tensors and calls libfa.so, some 4 us a
-# call on a GB300's host in place of 7 through ctypes and 18 with each tensor
+# csrc/kv4_call.cpp) that looks at the tensors and calls libfa.so, 2.5 us
+# a call on a GB300's host in place of 7 through ctypes and 18 with each tensor
 # checked by itself.  It says only that something is wrong; what, is worked out
 # after that.
 
@@ -367,7 +367,8 @@ class _Kv4Ctypes:
             return -1
         return self.lib.fa_kv4_fwd(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
                                    o.data_ptr(), lse.data_ptr(), B, H, cache.shape[1], Nq, d, cache.shape[0], page_size,
-                                   block_table.shape[1], causal, 1.0 / math.sqrt(d) if scale is None else scale, stream)
+                                   block_table.shape[1], causal if 0 <= causal < 2 ** 31 else -1,
+                                   1.0 / math.sqrt(d) if scale is None else scale, stream)
 
 
 def _kv4_caller():

@@ -115,6 +115,7 @@ int do_fwd(PyObject* const* a) {
       lens->size(0) != B || page == 0 || !fits(*q) || !fits(*cache) || !fits(*table))
     return -1;
   const float s = (float)(a[7] == Py_None ? 1.0 / std::sqrt((double)d) : scale);
+  const int mask = causal >= 0 && causal <= INT32_MAX ? (int)causal : -1;  // not cut to a code that it is not
   const void* const qp = q->data_ptr();
   const void* const cp = cache->data_ptr();
   const int* const tp = static_cast<const int*>(table->data_ptr());
@@ -124,8 +125,7 @@ int do_fwd(PyObject* const* a) {
   const int pages = (int)cache->size(0), heads = (int)cache->size(1), max_pages = (int)table->size(1);
   int status;
   Py_BEGIN_ALLOW_THREADS;
-  status = g_fwd(qp, cp, tp, np, op, lp, (int)B, (int)H, heads, (int)Nq, (int)d, pages, page, max_pages, (int)causal, s,
-                 stream);
+  status = g_fwd(qp, cp, tp, np, op, lp, (int)B, (int)H, heads, (int)Nq, (int)d, pages, page, max_pages, mask, s, stream);
   Py_END_ALLOW_THREADS;
   return status;
 }

@@ -89,6 +89,9 @@ MOVES = [
     (1, 4, 70, 64, [63], None),
     (2, 2, 33, 256, [200, 255], [33, 1]),
     (5, 1, 3, 128, [0, 1, 2, 126, 127], [3, 2, 1, 3, 0]),
+    # Enough tokens that a CTA takes four blocks.
+    (16, 8, 200, 32, list(range(0, 80, 5)), [200, 0, 1, 15, 16, 17, 63, 64, 65, 128, 150, 191, 192, 193, 199, 200]),
+    (8, 13, 223, 64, [0, 1, 15, 16, 17, 48, 63, 64], None),
 ]
 
 
@@ -433,6 +436,35 @@ def test_bad_pages_are_skipped_and_reported(fa, d):
     assert torch.equal(before, f.cache)
 
 
+def test_bad_pages_among_many_tokens(fa):
+    """Where a CTA takes four blocks of tokens, those of a bad page are left
+    out and the others are not."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(24)
+    B, Hkv, N, d, page = 8, 10, 256, 64, 16
+    kd, k = normal(rng, (B, Hkv, N, d))
+    vd, v = normal(rng, (B, Hkv, N, d))
+    table, n = make_table(rng, B, N // page)
+    bad = table.copy()
+    bad[rng.random(bad.shape) < 0.2] = n
+    assert (bad == n).any()
+    cache = fa.kv4_cache(n, Hkv, page, d)
+    fa.fa_kv4_write(kd, vd, cache, ints(bad), ints([0] * B))
+    assert fa.fa_poll_status() == fa.FA_ERR_BAD_INDEX
+    there = np.repeat(bad != n, page, 1)[:, None, :, None]
+    ko, vo = torch.empty_like(kd), torch.empty_like(vd)
+    fa.fa_kv4_read(cache, ints(table), ints([0] * B), ko, vo)  # pages that were not written hold zeros
+    assert fa.fa_poll_status() == fa.FA_OK
+    for out, x in ((ko, k), (vo, v)):
+        assert np.array_equal(host(out), np.where(there, kv4.to_bf16(kv4.held(x)), 0))
+    fa.fa_kv4_write(kd, vd, cache, ints(table), ints([0] * B))
+    ko.fill_(7.0), vo.fill_(7.0)
+    fa.fa_kv4_read(cache, ints(bad), ints([0] * B), ko, vo)
+    assert fa.fa_poll_status() == fa.FA_ERR_BAD_INDEX
+    for out, x in ((ko, k), (vo, v)):
+        assert np.array_equal(host(out), np.where(there, kv4.to_bf16(kv4.held(x)), 7))
+
+
 def test_bad_lengths_and_positions_are_clamped_and_reported(fa):
     torch = torch_cuda()
     rng = np.random.default_rng(7)
@@ -489,6 +521,9 @@ def test_binding_refusals(fa, caller):
             fa.fa_kv4_fwd(q, f.cache, f.td, f.ld, bad_o, bad_lse)
     with pytest.raises(fa.FaError):
         fa.fa_kv4_fwd(q, f.cache, f.td, f.ld, o, lse, scale=-1.0)
+    for causal in (3, -1, 2 ** 32, 2 ** 32 + 1):
+        with pytest.raises(fa.FaError):
+            fa.fa_kv4_fwd(q, f.cache, f.td, f.ld, o, lse, causal=causal)
     fa.fa_kv4_fwd(q, f.cache, f.td, f.ld, o, lse, causal=fa.FA_CAUSAL_BOTTOM_RIGHT, scale=1, stream=0)
     with pytest.raises(fa.FaError) as e:  # 24-token pages
         fa.kv4_forward(q, torch.zeros((4, 2, 24 * 72), dtype=torch.uint8, device="cuda"), f.td, f.ld)
@@ -663,6 +698,73 @@ def test_captured_steps_and_two_graphs(fa):
                 o, lse = got[i][s]
                 check_attend(o[b:b + 1], lse[b:b + 1], j["q"][s, b:b + 1], k[None], v[None], [n0 + s + 1], d ** -0.5,
                              "bottom_right", f"graph {i} step {s}")
+
+
+def test_sequences_that_share_pages(fa):
+    """A prompt's pages stand in several sequences' tables, a page twice in
+    one of them."""
+    rng = np.random.default_rng(23)
+    d, page, n = 128, 32, 150
+    f = Filled(fa, rng, [n], 2, d, page)
+    full = f.table[0, :4]
+    table = np.stack([full, full[[0, 1, 1, 0]], full[[3, 2, 1, 0]]])
+    lens = [128, 100, 128]
+    at = np.concatenate([np.arange(128)[None], np.r_[0:64, 32:64, 0:32][None], np.r_[96:128, 64:96, 32:64, 0:32][None]])
+    k, v = (np.stack([x[0][:, i] for i in at]) for x in (f.k, f.v))
+    qd, q = normal(rng, (3, 8, 2, d))
+    o, lse = fa.kv4_forward(qd, f.cache, ints(table), ints(lens), causal="bottom_right")
+    assert fa.fa_poll_status() == fa.FA_OK
+    check_attend(o, lse, q, k, v, lens, d ** -0.5, "bottom_right")
+    torch = torch_cuda()
+    ko, vo = (torch.empty((3, 2, 128, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    fa.fa_kv4_read(f.cache, ints(table), ints([0] * 3), ko, vo)
+    assert np.array_equal(host(ko), kv4.to_bf16(k)) and np.array_equal(host(vo), kv4.to_bf16(v))
+
+
+CAPTURED_FIRST = """
+import torch
+import exact_attention_92_gb300 as fa
+x = torch.randn((1, 1, 64, 64), device="cuda").to(torch.bfloat16)
+fa.forward(x, x, x)  # the library's first call on the device may not be captured
+torch.cuda.synchronize()
+for d, rows, pages in ((128, 1, 200), (64, 16, 9000), (96, 6, 3)):
+    cache = fa.kv4_cache(4, 1, 16, d)
+    table = torch.full((1, pages), -1, dtype=torch.int32, device="cuda")
+    table[0, :3] = torch.tensor([2, 0, 3], device="cuda")
+    zero, n = (torch.full((1,), i, dtype=torch.int32, device="cuda") for i in (0, 40))
+    k, v = (torch.randn((1, 1, 40, d), device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((1, rows, 1, d), device="cuda").to(torch.bfloat16)
+    ko, vo, o = torch.empty_like(k), torch.empty_like(v), torch.empty_like(q)
+    lse = torch.empty((1, rows, 1), device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fa.fa_kv4_write(k, v, cache, table, zero)
+        fa.fa_kv4_read(cache, table, zero, ko, vo)
+        fa.fa_kv4_fwd(q, cache, table, n, o, lse)
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+    got, got_ko = o.clone(), ko.clone()
+    fa.fa_kv4_read(cache, table, zero, ko, vo)
+    fa.fa_kv4_fwd(q, cache, table, n, o, lse)
+    assert fa.fa_poll_status() == fa.FA_OK
+    assert torch.equal(o, got) and torch.equal(ko, got_ko) and bool((ko != 0).any())
+    s = torch.softmax(q[0, :, 0].float() @ ko[0, 0].float().T / d ** 0.5, -1)
+    assert (s @ vo[0, 0].float() - o[0, :, 0].float()).abs().max() < 0.05
+print("done")
+"""
+
+
+def test_first_calls_may_be_captured(fa):
+    """Kernels that no call has launched before, captured in a new process."""
+    import os
+    import subprocess
+    import sys
+
+    r = subprocess.run([sys.executable, "-c", CAPTURED_FIRST], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "done", r.stdout + r.stderr
 
 
 def test_calls_at_once_on_two_streams(fa):
