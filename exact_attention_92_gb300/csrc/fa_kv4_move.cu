@@ -9,7 +9,9 @@
 // cache) as long as a value costs few enough instructions: writing takes 163 for
 // 16 values a lane (issue slots 70% taken).  Writing 4 x 8192 tokens of 8 heads
 // at d = 128 and reading them back takes 56 us, 90% of what a copy moves;
-// reading 2 x 32768 tokens 54 us, 93%.
+// reading 2 x 32768 tokens 54 us, 94%.  CTAs past a sequence's tokens end at once:
+// 24 pieces of up to 1000 tokens, half of that on average, at d = 64 take 13.3 us to
+// write (16.6 with the work done on no tokens), 11.9 without such CTAs.
 #include <cstdint>
 #include <type_traits>
 
@@ -44,6 +46,7 @@ struct Kv4Tokens {
   int place;          // in the block
   uint32_t has;       // bit u: this thread has a row for block u
   bool all;           // of the CTA: every thread has one for every block
+  int blocks;         // of the CTA: those before the tokens' end, 0 or less: none
   int page[U];        // of block u; -1: none, or out of range
   int in_page;        // 16-token blocks of a page before block 0
   int head;
@@ -77,6 +80,7 @@ __device__ __forceinline__ Kv4Tokens<D, U> kv4_tokens(const Kv4MoveParams& p) {
   w.row = (size_t)bh * p.N + (ptrdiff_t)(i0 + w.place);
   w.has = 0;
   w.all = true;
+  w.blocks = (n - i0 + 15) >> 4;
   w.in_page = block0;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -177,6 +181,7 @@ __global__ void __launch_bounds__(2 * D) kv4_write_kernel(const Kv4MoveParams p)
   constexpr int kPer = D / 8;
   const int c8 = threadIdx.x % kPer, g = c8 / 4, t = c8 % 4;
   const Kv4Tokens<D, U> w = kv4_tokens<D, U>(p);
+  if (w.blocks <= 0) return;
   const uint4* const k_in = p.k_in + (ptrdiff_t)w.row * kPer + c8;
   const uint4* const v_in = p.v_in + (ptrdiff_t)w.row * kPer + c8;
   const int at_key = F::key_word(w.place, g, t), at_scale = F::scale(w.place, t & 1, g);
@@ -196,6 +201,7 @@ __global__ void __launch_bounds__(2 * D) kv4_write_kernel(const Kv4MoveParams p)
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (!ALL && u >= w.blocks) break;
       // A group's 32 channels are a quad of lanes: key and value in one word.
       const uint32_t km = max_abs(max_abs(kr[u].x, kr[u].y), max_abs(kr[u].z, kr[u].w));
       const uint32_t vm = max_abs(max_abs(vr[u].x, vr[u].y), max_abs(vr[u].z, vr[u].w));
@@ -245,6 +251,7 @@ __global__ void __launch_bounds__(2 * D) kv4_read_kernel(const Kv4MoveParams p) 
   constexpr int kPer = D / 8;
   const int c8 = threadIdx.x % kPer, g = c8 / 4, t = c8 % 4;
   Kv4Tokens<D, U> w = kv4_tokens<D, U>(p);
+  if (w.blocks <= 0) return;
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (!kv4_there<D, U>(p, w, u)) {
@@ -286,21 +293,30 @@ __global__ void __launch_bounds__(2 * D) kv4_read_kernel(const Kv4MoveParams p) 
 }
 
 template <int D, int U>
-static cudaError_t launch_move_u(bool write, Kv4MoveParams& p, cudaStream_t stream) {
+static cudaError_t launch_move_u(void (*kernel)(Kv4MoveParams), Kv4MoveParams& p, cudaStream_t stream) {
   // N tokens touch (N + 30) / 16 blocks at most, wherever they begin.
   p.groups = (int)((((long long)p.N + 30) / 16 + U - 1) / U);
   const unsigned grid = (unsigned)p.c.B * p.c.Hkv * p.groups;
-  return launch_pdl(write ? kv4_write_kernel<D, U> : kv4_read_kernel<D, U>, dim3(grid), dim3(2 * D), 0, stream, p);
+  return launch_pdl(kernel, dim3(grid), dim3(2 * D), 0, stream, p);
 }
 
 template <int D>
 static cudaError_t launch_move_t(bool write, Kv4MoveParams& p, int sm_count, cudaStream_t stream) {
-  // Four blocks a CTA keep enough loads in flight (writing and reading 4 x 8192
+  // Several blocks a CTA keep enough loads in flight (writing and reading 4 x 8192
   // tokens of 8 heads at d = 128: 63 us, with one block 75 us); where that leaves
   // SMs without a CTA, one block each is sooner done (100 tokens of 12 heads at
-  // d = 96: 1.8 us, with four blocks 2.6 us).
-  if ((long long)p.c.B * p.c.Hkv * (p.N / 64) >= 2ll * sm_count) return launch_move_u<D, 4>(write, p, stream);
-  return launch_move_u<D, 1>(write, p, stream);
+  // d = 96: 1.8 us, with four blocks 2.6 us).  Writing takes four (4 x 8192 tokens
+  // 27.7 us, with two 28.8).  Reading takes two (28.1 us, with four 28.8; 24 pieces
+  // of up to 1000 tokens at d = 96 20.3 and 21.0), but four at d = 64, whose CTAs
+  // have half the threads (such pieces written and read back 28.7 us, with two 30.6;
+  // read alone 14.2 and 14.6, all of them full 22.4 and 21.7).
+  constexpr int R = D == 64 ? 4 : 2;
+  const bool many = (long long)p.c.B * p.c.Hkv * (p.N / 64) >= 2ll * sm_count;
+  if (write)
+    return many ? launch_move_u<D, 4>(kv4_write_kernel<D, 4>, p, stream)
+                : launch_move_u<D, 1>(kv4_write_kernel<D, 1>, p, stream);
+  return many ? launch_move_u<D, R>(kv4_read_kernel<D, R>, p, stream)
+              : launch_move_u<D, 1>(kv4_read_kernel<D, 1>, p, stream);
 }
 
 cudaError_t launch_kv4_move(int d, bool write, const Kv4Cache& c, const int* start, const int* count, const void* k_in,
