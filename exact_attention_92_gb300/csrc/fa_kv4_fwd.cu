@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     ++taken;
 
     uint32_t q[PACK ? 2 : NR][NG][4];  // as the column operand (PACK: for each block, in its half of the columns)
-    float cc[NR][2];        // what turns the sums of columns 2 t, 2 t + 1 into base-2 scores
+    float2 cc[NR];          // what turns the sums of columns 2 t, 2 t + 1 into base-2 scores
     int low = len;          // keys that all rows see
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -480,8 +480,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
         }
       }
       const float back = p.scale_log2 / up;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) cc[r][c] = __shfl_sync(0xffffffffu, back, 4 * (col0 + c));
+      cc[r].x = __shfl_sync(0xffffffffu, back, 4 * col0);
+      cc[r].y = __shfl_sync(0xffffffffu, back, 4 * col0 + 4);
     }
     // Keys that each row sees; padding rows see all.
     if (p.causal != FA_CAUSAL_NONE) {
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
       // blocks, the query rows once in its columns 0-3 for block 0 and once in
       // 4-7 for block 1, so that a lane has scores of one block only.
       constexpr int NS = PACK ? 1 : C::kBlocks;
-      float sc[NS][NR][4];
+      float2 sc[NS][NR][2];  // keys g, g + 8
       float top[NR][2];  // largest score + log2(largest scale of the value)
 #pragma unroll
       for (int r = 0; r < NR; ++r) top[r][0] = top[r][1] = -INFINITY;
@@ -542,8 +542,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
         }
 #pragma unroll
         for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[s][r][x] = 0.f;
+          for (int x = 0; x < 2; ++x) sc[s][r][x] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
           float c[NR][4];
@@ -564,24 +563,24 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
           const float fa_ = scale_of(wa, i), fb_ = scale_of(wb, i);
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            sc[s][r][0] = fmaf(fa_, c[r][0], sc[s][r][0]);
-            sc[s][r][1] = fmaf(fa_, c[r][1], sc[s][r][1]);
-            sc[s][r][2] = fmaf(fb_, c[r][2], sc[s][r][2]);
-            sc[s][r][3] = fmaf(fb_, c[r][3], sc[s][r][3]);
+            sc[s][r][0] = __ffma2_rn(make_float2(fa_, fa_), make_float2(c[r][0], c[r][1]), sc[s][r][0]);
+            sc[s][r][1] = __ffma2_rn(make_float2(fb_, fb_), make_float2(c[r][2], c[r][3]), sc[s][r][1]);
           }
         }
         const float va = lg2_approx(largest_scale<NG>(wa)), vb = lg2_approx(largest_scale<NG>(wb));
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = fmaf(sc[s][r][c], cc[r][c], va), y = fmaf(sc[s][r][c + 2], cc[r][c], vb);
-            if constexpr (MASK) {
-              x = seen(s, r, c) ? x : -INFINITY;
-              y = seen(s, r, c + 2) ? y : -INFINITY;
-            }
-            top[r][c] = fmax3(top[r][c], x, y);
+        for (int r = 0; r < NR; ++r) {
+          float2 x = __ffma2_rn(sc[s][r][0], cc[r], make_float2(va, va));
+          float2 y = __ffma2_rn(sc[s][r][1], cc[r], make_float2(vb, vb));
+          if constexpr (MASK) {
+            x.x = seen(s, r, 0) ? x.x : -INFINITY;
+            x.y = seen(s, r, 1) ? x.y : -INFINITY;
+            y.x = seen(s, r, 2) ? y.x : -INFINITY;
+            y.y = seen(s, r, 3) ? y.y : -INFINITY;
           }
+          top[r][0] = fmax3(top[r][0], x.x, y.x);
+          top[r][1] = fmax3(top[r][1], x.y, y.y);
+        }
       }
 
       // Move the references of columns that have outgrown them.
@@ -623,11 +622,17 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            float y = ex2_approx(fmaf(sc[s][r][x], cc[r][x & 1], -ref[r][x & 1]));
-            if constexpr (MASK) y = seen(s, r, x) ? y : 0.f;
+          for (int x = 0; x < 2; ++x) {
+            float2 y = __ffma2_rn(sc[s][r][x], cc[r], make_float2(-ref[r][0], -ref[r][1]));
+            y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            if constexpr (MASK) {
+              y.x = seen(s, r, 2 * x) ? y.x : 0.f;
+              y.y = seen(s, r, 2 * x + 1) ? y.y : 0.f;
+            }
             sc[s][r][x] = y;
-            l[r][x & 1] += y;
+            const float2 sum = __fadd2_rn(make_float2(l[r][0], l[r][1]), y);
+            l[r][0] = sum.x;
+            l[r][1] = sum.y;
           }
         constexpr int NW = (NG + 1) / 2, NK = PACK ? C::kBlocks : 1;
         uint32_t v[NK][4][NW];  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
@@ -646,13 +651,15 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
             const float fa_ = scale_of(wa, NG + i), fb_ = scale_of(wb, NG + i);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-              float x[4] = {sc[s][r][0] * fa_, sc[s][r][1] * fa_, sc[s][r][2] * fb_, sc[s][r][3] * fb_};
+              float2 x = __fmul2_rn(sc[s][r][0], make_float2(fa_, fa_)), y = __fmul2_rn(sc[s][r][1], make_float2(fb_, fb_));
               if constexpr (MASK) {  // whatever the scale is
-#pragma unroll
-                for (int z = 0; z < 4; ++z) x[z] = seen(s, r, z) ? x[z] : 0.f;
+                x.x = seen(s, r, 0) ? x.x : 0.f;
+                x.y = seen(s, r, 1) ? x.y : 0.f;
+                y.x = seen(s, r, 2) ? y.x : 0.f;
+                y.y = seen(s, r, 3) ? y.y : 0.f;
               }
-              b0[h][r] = transpose8(pack_f16(x[0], x[1]));
-              b1[h][r] = transpose8(pack_f16(x[2], x[3]));
+              b0[h][r] = transpose8(pack_f16(x.x, x.y));
+              b1[h][r] = transpose8(pack_f16(y.x, y.y));
             }
           }
 #pragma unroll
