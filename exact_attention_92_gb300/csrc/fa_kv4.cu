@@ -30,9 +30,10 @@ namespace {
 
 constexpr int kMinPage = 16, kMaxPage = 1024;
 // Units of at most this many steps are not cut between CTAs: a second launch
-// costs more than it gains (16 sequences of 300 tokens, 8 heads of d = 128, 10
-// steps: 7.4 us whole, 8.2 us cut; one of 1024 tokens, 32 steps: 9.5 and 9.1).
-constexpr int kWholeSteps = 16;
+// costs more than it gains (32 sequences, 8 heads of d = 128: 16 steps 10.0 us
+// whole, 11.5 us cut; 24 steps 12.2 and 13.1; 32 steps, the lengths ragged, 13.3
+// and 12.7).
+constexpr int kWholeSteps = 24;
 constexpr int kMaxRows = 128;  // query rows of a key/value head's group (fa_kv4_fwd)
 
 bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -18,19 +18,21 @@
 // and their codes go from shared memory through one conversion instruction per
 // two values into the operand's registers.  With up to 4 query rows (PACK) the
 // two 16-key blocks of a step share the 8 columns, which halves the softmax's
-// share of the instructions: 520 a step and warp in place of 583 at d = 128.
+// share of the instructions (100.4 -> 96.7 us in the case below).
 // (A tcgen05 product would want the 128-row operand in shared memory, decoded:
 // 512 bytes written and read back a token for 144 bytes of cache.)
 //
 // What bounds it (d = 128, 64 sequences of up to 16384 tokens, 8 heads, 4 rows,
-// 552 MB): 96.5 us, 5.7 TB/s of DRAM reads, 84% of what a copy moves; while SMs
-// are busy (92 us) 6.0 TB/s with 57% of the issue slots taken.  A step costs
-// 128 conversions from e2m1 and about 100 other instructions of the same
-// half-rate pipe, which so is in use 55% of the time; the matrix pipe 28%.  Of a
-// call of 8 sequences of 8192 tokens (22.5 us, 11.2 us of traffic) about 3 us
-// go before the first copies (lengths, place in the list, page: three dependent
-// loads), 1.5 us for the last warps to finish (9 or 10 steps each), 1 us to join
-// and 2.5 us to merge.
+// 552 MB): 94.3 us, 5.9 TB/s of DRAM reads, 86% of what a copy moves.  500
+// instructions a step and warp, 57% of the issue slots while SMs are busy; 128 of
+// them are conversions from e2m1 and about 100 others of the same half-rate pipe,
+// which so is in use 60% of the time; the matrix pipe 28%.  Scores, weights and
+// their sums are packed fp32 (20 instructions a step fewer: 96.7 us without).
+// Of a call of 8 sequences of 8192 tokens (22.3 us, 11.2 us of traffic) 3.4 us
+// go before the first copies are on the way (lengths 0.9, place in the list 1.3,
+// page and issue 1.2) and 2.3 until their bytes are there; the warps end their
+// steps (9 or 10 each) between 14 and 19.6 us, 1.2 us go for the join and about 2
+// for the merge.
 //
 // Numbers.  Codes are exact in fp16.  A query row is scaled by a power of two
 // to lie just below 2^16, where fp16 holds its bf16 values exactly down to
@@ -1009,9 +1011,9 @@ cudaError_t launch_merge_d(int unit_rows, const Kv4FwdParams& p, int grid, cudaS
 // keys, which halves what a step spends on softmax (PACK).  Above eight, two row
 // tiles a unit read and decode each key once for 16 rows, but leave room for
 // fewer warps: where there are few steps to an SM (`sm_steps`, with one tile a
-// unit), one tile is sooner done (d = 128, 16 rows, 8 heads: 4 sequences of 1000
-// tokens, 26 steps an SM, 10.7 us and 12.6 with two; 8 of 4000, 105 steps, 21.9
-// and 23.1; 16 of 4000, 210 steps, 35.5 and 33.0; d = 64 and 96 alike).  Not at
+// unit), one tile is sooner done (d = 128, 16 rows, 8 heads: 4 sequences of 2000
+// tokens, 26 steps an SM, 12.3 us and 13.7 with two; 8 of 4000, 105 steps, 21.9
+// and 22.9; 16 of 4000, 210 steps, 35.2 and 31.9; d = 64 and 96 alike).  Not at
 // d = 256, whose sums take 64 registers a tile.
 int kv4_fwd_unit_rows(int d, int rows, long long sm_steps) {
   if (rows <= kKv4Rows / 2) return kKv4Rows / 2;

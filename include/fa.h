@@ -419,7 +419,7 @@ typedef struct {
   int units;       /* B * Hkv * row_blocks */
   int step_keys;   /* keys that a warp takes at a time */
   int max_steps;   /* ceil(max_pages * page_size / step_keys) */
-  int whole;       /* 1: units are not cut between CTAs (at most 16 steps each, or
+  int whole;       /* 1: units are not cut between CTAs (at most 24 steps each, or
                       three to four for each warp where the units fit the SMs) */
   int grid;        /* CTAs of the main kernel at most */
   int launches;    /* 1, or 2 with the merge of cut units */

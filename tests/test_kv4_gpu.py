@@ -313,9 +313,12 @@ def test_attend_uneven_values(fa, d):
         q = np.abs(kv4.to_bf16(rng.standard_normal((1, 3, 1, d))))
         q[0, 1] = 0
         q[0, 2] = -q[0, 2]
-        o, lse = fa.kv4_forward(given(q), f.cache, f.td, f.ld, scale=0.01)
-        assert fa.fa_poll_status() == fa.FA_OK
-        check_attend(o, lse, q, f.k, f.v, [N], 0.01, "none", f"flip={flip}")
+        wide = np.full((1, 4000), -1, np.int32)  # room for so many steps that CTAs share a sequence
+        wide[:, :f.table.shape[1]] = f.table
+        for table in (f.td, ints(wide)):
+            o, lse = fa.kv4_forward(given(q), f.cache, table, f.ld, scale=0.01)
+            assert fa.fa_poll_status() == fa.FA_OK
+            check_attend(o, lse, q, f.k, f.v, [N], 0.01, "none", f"flip={flip} {tuple(table.shape)}")
 
 
 def test_attend_all_values_zero(fa):
