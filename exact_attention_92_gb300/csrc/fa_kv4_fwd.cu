@@ -69,8 +69,10 @@ namespace {
 template <int D, int NR, bool PACK>
 struct Cfg {
   // One CTA an SM, its warps a multiple of the four schedulers and as many as
-  // their registers allow without spills (65536 over 16, 12 or 8 warps: 128, 168
-  // or 255 each).
+  // their registers allow without spilling more than a few words outside the main
+  // loop's sums (65536 over 16, 12 or 8 warps: 128, 168 or 255 each; 16 warps at
+  // d = 128 spill and take 101 us in place of 96.7 in the case above, two row tiles
+  // at d = 96 with 12 warps 49.2 in place of 47.4).
   static constexpr int kWarps = D == 256 || (NR == 2 && D > 64)       ? 8
                                 : NR == 1 && (D == 64 || (D == 96 && !PACK)) ? 16
                                                                        : 12;
@@ -885,11 +887,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
 }
 
 // Merge of the parts of the units that CTA borders cut: a CTA per main CTA, a
-// warp per row.  Bound by its chain of loads (which CTAs, their references and
-// sums): about 2.5 us with its launch.  Merging in the main kernel instead, by
-// the CTA that brings a unit's last part, cost more (two barriers, fences and an
-// atomic in every CTA: 8 sequences of 8192 tokens 24.9 us in place of 22.6).  O = sum_k 2^(ref_k - m) O_k / sum_k 2^(ref_k - m) l_k, the
-// parts in the order of the CTAs.
+// warp per row.  O = sum_k 2^(ref_k - m) O_k / sum_k 2^(ref_k - m) l_k, the parts in
+// the order of the CTAs.  Bound by its chain of loads (which CTAs, their
+// references and sums): about 2 us with its launch.  Merging in the main kernel
+// instead, by the CTA that brings a unit's last part, cost more (two barriers,
+// fences and an atomic in every CTA: 8 sequences of 8192 tokens 24.9 us in place of
+// 22.6).
 template <int D, int kRows>
 __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4FwdParams p) {
   constexpr int kMany = (D / 4 + 31) / 32, kBatch = 8 / kMany;

@@ -66,22 +66,6 @@ namespace dev {
 // Records that an index out of range was skipped.
 __device__ __forceinline__ void kv4_bad_index(const Kv4Cache& c) { atomicExch(c.status + 1, (unsigned)FA_ERR_BAD_INDEX); }
 
-// Page of sequence b's position pos (0 <= pos < max_pages * page_size), or
-// -1, recorded, if the table's entry is out of range.
-__device__ __forceinline__ int kv4_page(const Kv4Cache& c, int b, int pos) {
-  const int page = c.table[(size_t)b * c.max_pages + (pos >> c.page_shift)];
-  if ((unsigned)page < (unsigned)c.num_pages) return page;
-  kv4_bad_index(c);
-  return -1;
-}
-
-// The 16-token block that holds position pos of a page.
-template <int D>
-__device__ __forceinline__ uint8_t* kv4_block(const Kv4Cache& c, int page, int head, int pos) {
-  const size_t first = ((size_t)page * c.Hkv + head) << (c.page_shift - 4);
-  return c.pages + (first + ((pos & ((1 << c.page_shift) - 1)) >> 4)) * Kv4<D>::kBlockBytes;
-}
-
 // The eight e2m1 codes of a word as four pairs of fp16 (exact).
 __device__ __forceinline__ void kv4_decode8(uint32_t w, uint32_t* h) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
