@@ -311,7 +311,7 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, causal=False, scale=None, 
 
 # The calls over the 4-bit cache are made once a layer and decoding step, where
 # the time of marshalling shows: they go through a native caller (_kv4_call.so,
-# csrc/kv4_call.cpp) that looks at the tensors and calls libfa.so, 2.5 us
+# csrc/kv4_call.cpp) that looks at the tensors and calls libfa.so, 2.1 us
 # a call on a GB300's host in place of 7 through ctypes and 18 with each tensor
 # checked by itself.  It says only that something is wrong; what, is worked out
 # after that.
@@ -333,7 +333,8 @@ class _Kv4Ctypes:
                    and t.is_cuda and t.get_device() == device
                    and all(w is None or n == w for n, w in zip(t.shape, shape)) for t, dtype, shape in tensors)
 
-    def move(self, write, k, v, cache, block_table, start, count, device, stream):
+    def move(self, write, k, v, cache, block_table, start, count, stream):
+        device, stream = _device_and_stream(stream)
         bf16, i32 = _torch.bfloat16, _torch.int32
         shape = getattr(k, "shape", ())
         if len(shape) != 4:
@@ -353,7 +354,8 @@ class _Kv4Ctypes:
             return self.lib.fa_kv4_write(*kv, cache.data_ptr(), *arrays, *sizes)
         return self.lib.fa_kv4_read(cache.data_ptr(), *arrays, *kv, *sizes)
 
-    def fwd(self, q, cache, block_table, lens, o, lse, causal, scale, device, stream):
+    def fwd(self, q, cache, block_table, lens, o, lse, causal, scale, stream):
+        device, stream = _device_and_stream(stream)
         shape = getattr(q, "shape", ())
         if len(shape) != 4:
             return -1
@@ -396,9 +398,12 @@ def _device_and_stream(stream):
         device = _torch._C._cuda_getDevice()
     except (AttributeError, RuntimeError):
         return -1, 0  # no CUDA device: any tensor is refused
-    if stream is None:
-        return device, _torch._C._cuda_getCurrentRawStream(device)
-    return device, int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    return device, _torch._C._cuda_getCurrentRawStream(device) if stream is None else stream
+
+
+def _handle(stream):
+    """The handle (a number) of a stream."""
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 # What causal is usually given as.
@@ -439,8 +444,8 @@ def fa_kv4_cache_bytes(num_pages, Hkv, page_size, d) -> int:
 
 def _kv4_move(what, write, k, v, cache, block_table, start, count, stream):
     caller = _kv4 or _kv4_caller()
-    device, raw = _device_and_stream(stream)
-    status = caller.move(write, k, v, cache, block_table, start, count, device, raw)
+    status = caller.move(write, k, v, cache, block_table, start, count,
+                         stream if stream is None else _handle(stream))
     if status != FA_OK:
         bf16, i32 = _torch.bfloat16, _torch.int32
         shape = tuple(getattr(k, "shape", ()))
@@ -448,7 +453,8 @@ def _kv4_move(what, write, k, v, cache, block_table, start, count, stream):
         tensors = [("k", k, bf16, (B, Hkv, N, d)), ("v", v, bf16, (B, Hkv, N, d)),
                    ("cache", cache, _torch.uint8, (None, None, None)), ("block_table", block_table, i32, (B, None)),
                    ("start", start, i32, (B,))]
-        _kv4_refuse(what, status, tensors if count is None else tensors + [("count", count, i32, (B,))], device, Hkv, d)
+        _kv4_refuse(what, status, tensors if count is None else tensors + [("count", count, i32, (B,))],
+                    _device_and_stream(0)[0], Hkv, d)
 
 
 def fa_kv4_write(k, v, cache, block_table, start, count=None, stream=None):
@@ -468,11 +474,11 @@ def fa_kv4_fwd(q, cache, block_table, lens, o, lse, causal=False, scale=None, st
     """C fa_kv4_fwd: attention of q [B, H, Nq, d] over the first lens[b]
     tokens of each sequence in the 4-bit cache; causal as fa_fwd_general."""
     caller = _kv4 or _kv4_caller()
-    device, raw = _device_and_stream(stream)
     code = _CAUSAL_CODES.get(causal)
     if code is None:
         code = _causal_code(causal)
-    status = caller.fwd(q, cache, block_table, lens, o, lse, code, scale, device, raw)
+    status = caller.fwd(q, cache, block_table, lens, o, lse, code, scale,
+                        stream if stream is None else _handle(stream))
     if status != FA_OK:
         shape = tuple(getattr(q, "shape", ()))
         B, H, Nq, d = shape if len(shape) == 4 else (None,) * 4
@@ -480,7 +486,7 @@ def fa_kv4_fwd(q, cache, block_table, lens, o, lse, causal=False, scale=None, st
                     [("q", q, _torch.bfloat16, (B, H, Nq, d)), ("cache", cache, _torch.uint8, (None, None, None)),
                      ("block_table", block_table, _torch.int32, (B, None)), ("lens", lens, _torch.int32, (B,)),
                      ("o", o, _torch.bfloat16, (B, H, Nq, d)), ("lse", lse, _torch.float32, (B, H, Nq))],
-                    device, None, d)
+                    _device_and_stream(0)[0], None, d)
 
 
 def fa_poll_status(stream=None):

@@ -82,9 +82,9 @@ def check_spills(ptxas_log: str) -> None:
 
 def build_call(force: bool = False) -> str | None:
     """Compile the native caller of the 4-bit cache's entry points (_kv4_call.so,
-    against torch's and Python's headers); None where torch is not installed.
-    It holds no device code: without it the binding makes the same calls through
-    ctypes."""
+    against torch's and Python's headers); None where torch with CUDA is not
+    installed.  It holds no device code: without it the binding makes the same
+    calls through ctypes."""
     import importlib.util
     import sysconfig
 
@@ -96,11 +96,15 @@ def build_call(force: bool = False) -> str | None:
         return CALL
     torch_dir = list(spec.submodule_search_locations)[0]
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    if not os.path.exists(os.path.join(lib, "libc10_cuda.so")):
+        return None
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
     tmp = CALL + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-isystem", inc, "-isystem",
-           os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
-           CALL_SOURCE, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-I",
+           sysconfig.get_paths()["include"], CALL_SOURCE, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cxx} failed on {CALL_SOURCE}:\n{r.stdout}\n{r.stderr}")

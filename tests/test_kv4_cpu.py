@@ -275,14 +275,20 @@ def caller(lib, request, monkeypatch):
 
 def test_callers_refuse_what_is_no_tensor(caller):
     for bad in (None, 3, "x", [1]):
-        assert caller.move(True, bad, bad, bad, bad, bad, None, 0, 0) == -1
-        assert caller.fwd(bad, bad, bad, bad, bad, bad, 0, None, 0, 0) == -1
+        assert caller.move(True, bad, bad, bad, bad, bad, None, 0) == -1
+        assert caller.fwd(bad, bad, bad, bad, bad, bad, 0, None, 0) == -1
         with pytest.raises(TypeError):
             fa.fa_kv4_write(bad, bad, bad, bad, bad)
         with pytest.raises(TypeError):
             fa.fa_kv4_fwd(bad, bad, bad, bad, bad, bad)
     with pytest.raises(ValueError):
         fa.fa_kv4_fwd(None, None, None, None, None, None, causal="sideways")
+
+
+def _cuda():
+    import torch
+
+    return torch.cuda.is_available()
 
 
 def test_native_caller_checks_its_numbers(lib):
@@ -295,6 +301,11 @@ def test_native_caller_checks_its_numbers(lib):
             native.move(*args)
         with pytest.raises(TypeError):
             native.bind(*args)
+    for causal, scale, stream in (("x", None, None), (0, "x", None), (0, None, "x")):
+        if causal == 0 and scale is None and not _cuda():
+            continue  # without a device the stream is not looked at
+        with pytest.raises(TypeError):
+            native.fwd(*(None,) * 6, causal, scale, stream)
 
 
 def test_binding_refuses_host_tensors(caller):
