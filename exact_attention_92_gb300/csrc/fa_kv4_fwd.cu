@@ -1,7 +1,7 @@
 // Attention over the 4-bit key/value cache (fa_kv4_fwd).
 //
-// A unit is a (sequence, key/value head, block of 4, 8 or 16 of the group's
-// query rows); its keys are walked in steps of 32.  The steps of all units form
+// A unit is a (sequence, key/value head, block of 4, 8, 16 or 24 of the
+// group's query rows); its keys are walked in steps of 32.  The steps of all units form
 // one list, in the order of the units, of which every CTA takes an equal stretch
 // whatever the sequences' lengths, and every warp of it an equal stretch of
 // that.  Where a border cuts a unit, the warps of a CTA join their fp32 results
@@ -73,7 +73,7 @@ struct Cfg {
   // loop's sums (65536 over 16, 12 or 8 warps: 128, 168 or 255 each; 16 warps at
   // d = 128 spill and take 101 us in place of 96.7 in the case above, two row tiles
   // at d = 96 with 12 warps 49.2 in place of 47.4).
-  static constexpr int kWarps = D == 256 || (NR == 2 && D > 64)       ? 8
+  static constexpr int kWarps = D == 256 || NR == 3 || (NR == 2 && D > 64) ? 8
                                 : NR == 1 && (D == 64 || (D == 96 && !PACK)) ? 16
                                                                        : 12;
   static constexpr int kThreads = kWarps * 32;
@@ -993,6 +993,9 @@ cudaError_t launch_fwd_d(int unit_rows, const Kv4FwdParams& p, int grid, cudaStr
   if constexpr (D != 256) {
     if (unit_rows == 2 * kKv4Rows) return launch_fwd_t<D, 2, false>(p, grid, stream);
   }
+  if constexpr (D <= 96) {
+    if (unit_rows == 3 * kKv4Rows) return launch_fwd_t<D, 3, false>(p, grid, stream);
+  }
   return cudaErrorInvalidValue;
 }
 
@@ -1003,6 +1006,9 @@ cudaError_t launch_merge_d(int unit_rows, const Kv4FwdParams& p, int grid, cudaS
   if (unit_rows == kKv4Rows) return launch_pdl(kv4_merge_kernel<D, kKv4Rows>, g, b, 0, stream, p);
   if constexpr (D != 256) {
     if (unit_rows == 2 * kKv4Rows) return launch_pdl(kv4_merge_kernel<D, 2 * kKv4Rows>, g, b, 0, stream, p);
+  }
+  if constexpr (D <= 96) {
+    if (unit_rows == 3 * kKv4Rows) return launch_pdl(kv4_merge_kernel<D, 3 * kKv4Rows>, g, b, 0, stream, p);
   }
   return cudaErrorInvalidValue;
 }
@@ -1018,9 +1024,19 @@ cudaError_t launch_merge_d(int unit_rows, const Kv4FwdParams& p, int grid, cudaS
 // tokens, 26 steps an SM, 12.3 us and 13.7 with two; 8 of 4000, 105 steps, 21.9
 // and 22.9; 16 of 4000, 210 steps, 35.2 and 31.9; d = 64 and 96 alike).  Not at
 // d = 256, whose sums take 64 registers a tile.
+// At d = 64 and 96, 17 to 24 rows are one unit of three tiles (24 rows, 16
+// sequences of 8000 tokens: d = 96 57.6 us, with two units of two tiles 76.8;
+// d = 64 46.2 and 53.9), at d = 64 from more steps on (9 of 4000, 178 steps an SM:
+// d = 96 26.7 us and 26.9 with one tile a unit, d = 64 23.2 and 21.1; 14 of 4000,
+// 276 steps: d = 64 28.0 and 27.9).  Four tiles for 32 rows at d = 64 gain nothing
+// (55.8 us, 54.3 with two), nor do three for more rows there (48 rows 77.9 and
+// 75.2).
 int kv4_fwd_unit_rows(int d, int rows, long long sm_steps) {
   if (rows <= kKv4Rows / 2) return kKv4Rows / 2;
-  return rows > kKv4Rows && d != 256 && sm_steps >= 160 ? 2 * kKv4Rows : kKv4Rows;
+  if (rows <= kKv4Rows || d == 256) return kKv4Rows;
+  const bool three = rows > 2 * kKv4Rows && rows <= 3 * kKv4Rows && d <= 96;
+  if (sm_steps < (three && d == 64 ? 280 : 160)) return kKv4Rows;
+  return three ? 3 * kKv4Rows : 2 * kKv4Rows;
 }
 
 template <int D>
@@ -1028,6 +1044,9 @@ static int warps_d(int unit_rows) {
   if (unit_rows == kKv4Rows / 2) return Cfg<D, 1, true>::kWarps;
   if constexpr (D != 256) {
     if (unit_rows == 2 * kKv4Rows) return Cfg<D, 2, false>::kWarps;
+  }
+  if constexpr (D <= 96) {
+    if (unit_rows == 3 * kKv4Rows) return Cfg<D, 3, false>::kWarps;
   }
   return Cfg<D, 1, false>::kWarps;
 }

@@ -413,8 +413,10 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
  */
 typedef struct {
   int rows;        /* query rows that share a key/value head: (H / Hkv) * Nq */
-  int unit_rows;   /* query rows of a unit: 4 when rows <= 4; 16 when rows > 8, d < 256
-                      and an SM has at least 160 steps of 8-row units; else 8 */
+  int unit_rows;   /* query rows of a unit: 4 when rows <= 4; when rows > 8, d < 256
+                      and an SM has at least 160 steps of 8-row units: 24 for 17
+                      to 24 rows at d = 96 and (from 280 steps on) 64, 16
+                      otherwise; else 8 */
   int row_blocks;  /* units per (sequence, key/value head): ceil(rows / unit_rows) */
   int units;       /* B * Hkv * row_blocks */
   int step_keys;   /* keys that a warp takes at a time */

@@ -208,6 +208,7 @@ PLANS = [
     (1, 1, 1, 1, 64, 16, 1), (1, 32, 8, 1, 128, 16, 3), (8, 32, 8, 1, 128, 64, 128), (64, 32, 8, 1, 128, 64, 256),
     (9, 12, 4, 5, 96, 32, 188), (16, 64, 4, 1, 256, 64, 128), (3, 8, 1, 16, 128, 1024, 7), (1500, 2, 1, 1, 64, 16, 3),
     (16, 64, 8, 2, 128, 64, 125), (16, 64, 8, 2, 64, 64, 62), (2, 5, 1, 1, 128, 16, 17), (2, 4, 1, 1, 256, 16, 16), (1, 16, 2, 1, 256, 256, 4096),
+    (16, 24, 1, 1, 64, 64, 500), (16, 20, 1, 1, 96, 64, 500), (16, 24, 1, 1, 128, 64, 500),
 ]
 
 
@@ -218,7 +219,8 @@ def test_plan(lib, sizes, sm_count):
     pl = fa.fa_kv4_fwd_plan(*sizes, sm_count)
     assert pl["rows"] == H // Hkv * Nq
     steps = B * Hkv * -(-pl["rows"] // 8) * pl["max_steps"] // sm_count
-    assert pl["unit_rows"] == (4 if pl["rows"] <= 4 else 16 if pl["rows"] > 8 and d < 256 and steps >= 160 else 8)
+    many, least = (24, 280 if d == 64 else 160) if 16 < pl["rows"] <= 24 and d <= 96 else (16, 160)
+    assert pl["unit_rows"] == (4 if pl["rows"] <= 4 else many if pl["rows"] > 8 and d < 256 and steps >= least else 8)
     assert pl["row_blocks"] * pl["unit_rows"] >= pl["rows"] > (pl["row_blocks"] - 1) * pl["unit_rows"]
     assert pl["units"] == B * Hkv * pl["row_blocks"]
     assert pl["max_steps"] * pl["step_keys"] >= page * pages > (pl["max_steps"] - 1) * pl["step_keys"]

@@ -575,7 +575,7 @@ def test_workspace_allocation_failure_is_reported(fa, monkeypatch):
     check_attend(o, lse, q, f.k, f.v, [9000], 64 ** -0.5, "none")
 
 
-@pytest.mark.parametrize("rows", (1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 33))
+@pytest.mark.parametrize("rows", (1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 24, 25, 33))
 @pytest.mark.parametrize("d", DIMS)
 def test_every_count_of_query_rows(fa, d, rows):
     """Rows per key/value head about the borders between the tilings, over a
