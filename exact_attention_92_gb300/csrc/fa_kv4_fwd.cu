@@ -45,7 +45,10 @@
 // fp16 the running reference is that of s + log2(the largest scale of the
 // token's value), not of s: p * scale starts at 2^4 for the largest key seen and
 // may grow to 2^14 before the reference is moved (and the sums rescaled); what
-// falls below 2^-14 of that loses relative, not absolute, precision.  The sum
+// falls below 2^-14 of that loses relative, not absolute, precision.  A weight is
+// 2^((x - ref) - log2(scale)) of the same rounded x = s + log2(scale) that moves
+// the reference, so it keeps that bound where fp32 holds scores in steps of 4 and
+// more.  The sum
 // of p is fp32.  log2(scale) is taken at 2^-80 at least, which keeps the sum
 // of p below 2^121.
 #include <atomic>
@@ -517,13 +520,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     // One step: MASK where some row does not see some of the keys.
     auto step = [&](auto mask, const uint8_t* const st, int key0, uint32_t there) {
       constexpr bool MASK = decltype(mask)::value;
-      // Keys g and g + 8 of a block, this lane's columns: scores as the matrix
-      // products have them (to be multiplied by cc).  PACK: tile 0 holds both
+      // Keys g and g + 8 of a block, this lane's columns.  PACK: tile 0 holds both
       // blocks, the query rows once in its columns 0-3 for block 0 and once in
       // 4-7 for block 1, so that a lane has scores of one block only.
       constexpr int NS = PACK ? 1 : C::kBlocks;
-      float2 sc[NS][NR][2];  // keys g, g + 8
-      float top[NR][2];  // largest score + log2(largest scale of the value)
+      float2 sc[NS][NR][2];  // keys g, g + 8: q k, then base-2 score + log2(largest scale of the value), then p
+      float vl[NS][2];       // log2(largest scale of the value)
+      float top[NR][2];
 #pragma unroll
       for (int r = 0; r < NR; ++r) top[r][0] = top[r][1] = -INFINITY;
       auto seen = [&](int s, int r, int x) {
@@ -571,11 +574,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
             sc[s][r][1] = __ffma2_rn(make_float2(fb_, fb_), make_float2(c[r][2], c[r][3]), sc[s][r][1]);
           }
         }
-        const float va = lg2_approx(largest_scale<NG>(wa)), vb = lg2_approx(largest_scale<NG>(wb));
+        const float va = vl[s][0] = lg2_approx(largest_scale<NG>(wa)), vb = vl[s][1] = lg2_approx(largest_scale<NG>(wb));
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          float2 x = __ffma2_rn(sc[s][r][0], cc[r], make_float2(va, va));
-          float2 y = __ffma2_rn(sc[s][r][1], cc[r], make_float2(vb, vb));
+          float2 &x = sc[s][r][0], &y = sc[s][r][1];
+          x = __ffma2_rn(x, cc[r], make_float2(va, va));
+          y = __ffma2_rn(y, cc[r], make_float2(vb, vb));
           if constexpr (MASK) {
             x.x = seen(s, r, 0) ? x.x : -INFINITY;
             x.y = seen(s, r, 1) ? x.y : -INFINITY;
@@ -587,10 +591,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
         }
       }
 
-      // Move the references of columns that have outgrown them.
+      // Move the references of columns that have outgrown them.  The same
+      // difference is the weight's exponent below, whatever it was rounded from:
+      // from 2^25 on fp32 holds multiples of 4 only, and ref + 14 may be ref + 16.
       bool grow = false;
 #pragma unroll
-      for (int r = 0; r < NR; ++r) grow |= top[r][0] > ref[r][0] + 14.f || top[r][1] > ref[r][1] + 14.f;
+      for (int r = 0; r < NR; ++r) grow |= top[r][0] - ref[r][0] > 14.f || top[r][1] - ref[r][1] > 14.f;
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float next = x > ref[r][c] + 14.f ? x - 4.f : ref[r][c];
+            const float next = x - ref[r][c] > 14.f ? x - 4.f : ref[r][c];
             const float f = ex2_approx(ref[r][c] - next);
             ref[r][c] = next;
             l[r][c] *= f;
@@ -627,12 +633,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
         for (int r = 0; r < NR; ++r)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float2 y = __ffma2_rn(sc[s][r][x], cc[r], make_float2(-ref[r][0], -ref[r][1]));
-            y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            if constexpr (MASK) {
-              y.x = seen(s, r, 2 * x) ? y.x : 0.f;
-              y.y = seen(s, r, 2 * x + 1) ? y.y : 0.f;
-            }
+            float2 y = __fadd2_rn(sc[s][r][x], make_float2(-ref[r][0], -ref[r][1]));
+            y = __fadd2_rn(y, make_float2(-vl[s][x], -vl[s][x]));
+            y = make_float2(ex2_approx(y.x), ex2_approx(y.y));  // of a key that the row does not see: 0
             sc[s][r][x] = y;
             const float2 sum = __fadd2_rn(make_float2(l[r][0], l[r][1]), y);
             l[r][0] = sum.x;

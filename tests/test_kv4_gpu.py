@@ -321,6 +321,75 @@ def test_attend_uneven_values(fa, d):
             check_attend(o, lse, q, f.k, f.v, [N], 0.01, "none", f"flip={flip} {tuple(table.shape)}")
 
 
+def two_parts(N, d, big, small):
+    """Keys of one head whose channel 0 holds `big` [N] and whose channel 32
+    holds `small` [N], other channels 0."""
+    keys = np.zeros((1, 1, N, d))
+    keys[..., 0], keys[..., 32] = kv4.to_bf16(big), kv4.to_bf16(small)
+    return keys
+
+
+@pytest.mark.parametrize("sign", (1, -1))
+@pytest.mark.parametrize("power", (24, 25, 26, 27, 28, 31, 60))
+@pytest.mark.parametrize("d,H,v_std", [(64, 4, 1.0), (64, 20, 1.0), (96, 6, 1e-3), (96, 20, 1.0), (128, 4, 1e3),
+                                       (128, 16, 1.0), (256, 8, 1.0)])
+def test_attend_scores_beyond_fp32_units(fa, d, H, v_std, power, sign):
+    """Scores of 2^power, where fp32's step is 1 or more, that rise every 32
+    keys by one such step or two: O stays finite and, its weights being at least
+    0, within the values' range.  (O = sum_j w_j v_j / sum_j w_j; the 16-bit
+    weights are off by 2^-11 of themselves, the sums and exponentials by less
+    than another, O by 2^-8.)  Many sequences over the same pages, so that a
+    warp has several steps of each."""
+    rng = np.random.default_rng(power + d)
+    N, B = 2000, 100
+    step = 2.0 ** (power - 23)
+    keys = two_parts(N, d, np.full(N, sign * 2.0 ** (power - 8) * 6), np.arange(N) // 32 * step / 32)
+    f = Filled(fa, rng, [N], 1, d, 16, keys=keys, v_std=v_std)
+    q = np.zeros((1, H, 1, d))
+    q[..., 0] = 2.0 ** 8 / 6
+    q[0, :, 0, 32] = 32 * (1 + np.arange(H) / H)  # base-2 scores of 2^power, and j / 32 steps and more
+    q = kv4.to_bf16(q)
+    scale = float(np.log(2.0))
+    wide = np.full((1, 600), -1, np.int32)  # room for more steps: the unit's rows by the steps of an SM
+    wide[:, :f.table.shape[1]] = f.table
+    top = np.abs(f.v[0, 0]).max(0)
+    for table in (f.table, wide):
+        o, lse = fa.kv4_forward(given(np.repeat(q, B, 0)), f.cache, ints(np.repeat(table, B, 0)), ints([N] * B), scale=scale)
+        assert fa.fa_poll_status() == fa.FA_OK
+        O = host(o)[:, :, 0]
+        assert np.isfinite(O).all() and np.isfinite(lse.cpu().numpy()).all()
+        assert (np.abs(O) <= top * (1 + 2.0 ** -8 + 2.0 ** -10)).all()
+        for b in (0, B - 1):
+            check_attend(o[b:b + 1], lse[b:b + 1], q, f.k, f.v, [N], scale, "none", f"2^{power}")
+
+
+@pytest.mark.parametrize("sign", (1, -1))
+@pytest.mark.parametrize("power", (24, 26, 28, 32, 64, 110))
+@pytest.mark.parametrize("d,H,v_std", [(64, 9, 1.0), (96, 3, 1.0), (128, 1, 1e10), (256, 5, 1e-10)])
+def test_attend_one_key_far_above_the_others(fa, d, H, v_std, power, sign):
+    """Scores of 2^power, each key's 2^-7 of that or more from the next: a
+    score is off by e = 2^-19 of its size at most, so the largest one's key
+    has all the weight (2^(2 e - 2^(power - 7)) of it, nothing, goes to
+    others).  The weight is off by 2^-11 in the product and not in the sum,
+    with less than 2^-12 from the exponentials; O is rounded once."""
+    rng = np.random.default_rng(power + d)
+    N = 60
+    order = rng.permutation(N)
+    keys = two_parts(N, d, sign * 2.0 ** (power // 2) * (1 + order / 32), np.zeros(N))
+    f = Filled(fa, rng, [N], 1, d, 16, keys=keys, v_std=v_std)
+    q = np.zeros((1, H, 1, d))
+    q[..., 0] = 2.0 ** (power - power // 2)
+    best = int(np.argmax(f.k[0, 0, :, 0]))
+    gap = np.sort(f.k[0, 0, :, 0])[-1] - np.sort(f.k[0, 0, :, 0])[-2]
+    assert gap >= 2.0 ** (power // 2 - 7)
+    o, lse = fa.kv4_forward(given(q), f.cache, f.td, f.ld, scale=1.0)
+    assert fa.fa_poll_status() == fa.FA_OK
+    want = f.v[0, 0, best]
+    assert (np.abs(host(o)[0, :, 0] - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12) * np.abs(want)).all()
+    L = q[0, 0, 0, 0] * f.k[0, 0, best, 0]
+    assert (np.abs(lse.cpu().numpy()[0] - L) <= 2.0 ** -19 * abs(L)).all()
+
+
 def test_attend_all_values_zero(fa):
     rng = np.random.default_rng(3)
     f = Filled(fa, rng, [77], 1, 128, 16, vals=np.zeros((1, 1, 77, 128)))
