@@ -390,6 +390,21 @@ def test_attend_one_key_far_above_the_others(fa, d, H, v_std, power, sign):
     assert (np.abs(lse.cpu().numpy()[0] - L) <= 2.0 ** -19 * abs(L)).all()
 
 
+@pytest.mark.parametrize("d", DIMS)
+@pytest.mark.parametrize("q_std,k_std", [(1e-30, 1e31), (1e-33, 1e33), (1e-35, 3e35), (3e-37, 5e36)])
+def test_attend_small_queries_over_large_keys(fa, d, q_std, k_std):
+    """Query rows so small, and keys so large, that neither can be brought to
+    the other's size in fp32: the scores are ordinary ones."""
+    rng = np.random.default_rng(d)
+    lens = [300, 41]
+    f = Filled(fa, rng, lens, 2, d, 32, k_std)
+    for H in (4, 12):
+        qd, q = normal(rng, (2, H, 1, d), q_std)
+        o, lse = fa.kv4_forward(qd, f.cache, f.td, f.ld)
+        assert fa.fa_poll_status() == fa.FA_OK
+        check_attend(o, lse, q, f.k, f.v, lens, d ** -0.5, "none", f"{q_std} {k_std}")
+
+
 def test_attend_all_values_zero(fa):
     rng = np.random.default_rng(3)
     f = Filled(fa, rng, [77], 1, 128, 16, vals=np.zeros((1, 1, 77, 128)))
