@@ -1040,6 +1040,9 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
+    // This grid must not be complete before the dK/dV kernel is, beside which it
+    // runs: a kernel launched programmatically behind it waits for it alone.
+    pdl_wait();
   }
 }
 

@@ -540,6 +540,10 @@ __global__ void __launch_bounds__(b256::kThreads, 1)
   if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+    // The dK pass must not be complete before the dV pass is (nor the dQ kernel
+    // before the dK pass), beside which it runs: a kernel launched
+    // programmatically behind the last of them waits for that one alone.
+    if constexpr (DK) pdl_wait();
   }
 }
 
@@ -811,6 +815,7 @@ __global__ void __launch_bounds__(b256::kThreads, 1)
   if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+    pdl_wait();  // not complete before the dK pass is
   }
 }
 

@@ -895,3 +895,40 @@ def test_launches_are_counted(fa):
         fa.kv4_forward(out[:, :, :1].contiguous(), f.cache, table, f.ld)
         assert [fa.fa_launch_count(i) - n for i, n in zip(ids[2:], before)] == [1, plan["launches"] - 1]
     assert plan["launches"] == 2
+
+
+@pytest.mark.parametrize("d", DIMS)
+def test_cache_calls_behind_a_backward(fa, d):
+    """A call over the cache may start while the kernels of a backward ahead
+    of it are still running: the gradients written into a cache are the final
+    ones, and reading into the backward's own inputs disturbs none of them.
+    Few keys under many query rows: dQ's units are done long before dK's."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(d)
+    Nq, Nk, page = 16384, 100, 16
+    qd, _ = normal(rng, (1, 1, Nq, d))
+    kd, _ = normal(rng, (1, 1, Nk, d))
+    vd, _ = normal(rng, (1, 1, Nk, d))
+    gd, _ = normal(rng, (1, 1, Nq, d))
+    o, lse = fa.forward(qd, kd, vd)
+    want = fa.backward(qd, kd, vd, o, lse, gd)
+    torch.cuda.synchronize()
+    table, n = make_table(rng, 1, -(-Nk // page))
+    cache, other, td, zero = fa.kv4_cache(n, 1, page, d), fa.kv4_cache(n, 1, page, d), ints(table), ints([0])
+    for _ in range(5):
+        k, v = kd.clone(), vd.clone()
+        dq, dk, dv = torch.zeros_like(qd), torch.zeros_like(k), torch.zeros_like(v)
+        torch.cuda.synchronize()
+        fa.fa_bwd_general(qd, k, v, o, lse, gd, dq, dk, dv)
+        fa.fa_kv4_read(other, td, zero, k, v)  # zeros
+        torch.cuda.synchronize()
+        for got, w in zip((dq, dk, dv), want):
+            assert torch.equal(got, w)
+        dk.zero_(), dv.zero_()
+        torch.cuda.synchronize()
+        fa.fa_bwd_general(qd, kd, vd, o, lse, gd, dq, dk, dv)
+        fa.fa_kv4_write(dk, dv, cache, td, zero)
+        fa.fa_kv4_read(cache, td, zero, k, v)
+        for got, w in ((k, want[1]), (v, want[2])):
+            assert np.array_equal(host(got), kv4.to_bf16(kv4.held(host(w))))
+    assert fa.fa_poll_status() == fa.FA_OK
