@@ -40,6 +40,7 @@ from ._binding import (  # noqa: F401
     fa_kv4_read,
     fa_kv4_write,
     fa_poll_status,
+    fa_selftest_kv4_timeout,
     fa_selftest_wait_timeout,
     fa_set_wait_timeout_ns,
     fa_strerror,

@@ -65,6 +65,7 @@ _SIGNATURES = {
     "fa_poll_status": ([_vp], _i),
     "fa_set_wait_timeout_ns": ([_u64], _u64),
     "fa_selftest_wait_timeout": ([_u64, _vp], _i),
+    "fa_selftest_kv4_timeout": ([_vp] * 6 + [_i] * 8 + [_u64, _vp], _i),
     "fa_strerror": ([_i], ctypes.c_char_p),
     "fa_abi_version": ([], _i),
     "fa_trim_workspace": ([], _i),
@@ -354,23 +355,30 @@ class _Kv4Ctypes:
             return self.lib.fa_kv4_write(*kv, cache.data_ptr(), *arrays, *sizes)
         return self.lib.fa_kv4_read(cache.data_ptr(), *arrays, *kv, *sizes)
 
-    def fwd(self, q, cache, block_table, lens, o, lse, causal, scale, stream):
-        device, stream = _device_and_stream(stream)
+    def fwd_args(self, q, cache, block_table, lens, o, lse, device):
+        """Pointers and sizes of fa_kv4_fwd up to max_pages; None if a tensor
+        is not as it should be."""
         shape = getattr(q, "shape", ())
         if len(shape) != 4:
-            return -1
+            return None
         B, H, Nq, d = shape
         if not self._good([(q, _torch.bfloat16, shape), (o, _torch.bfloat16, shape), (lens, _torch.int32, (B,)),
                            (cache, _torch.uint8, (None,) * 3), (block_table, _torch.int32, (B, None)),
                            (lse, _torch.float32, (B, H, Nq))], device):
-            return -1
+            return None
         page_size, rest = divmod(cache.shape[2] * 8, 9 * d) if d else (0, 0)
         if rest or not page_size:
+            return None
+        return (*(t.data_ptr() for t in (q, cache, block_table, lens, o, lse)), B, H, cache.shape[1], Nq, d,
+                cache.shape[0], page_size, block_table.shape[1])
+
+    def fwd(self, q, cache, block_table, lens, o, lse, causal, scale, stream):
+        device, stream = _device_and_stream(stream)
+        args = self.fwd_args(q, cache, block_table, lens, o, lse, device)
+        if args is None:
             return -1
-        return self.lib.fa_kv4_fwd(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
-                                   o.data_ptr(), lse.data_ptr(), B, H, cache.shape[1], Nq, d, cache.shape[0], page_size,
-                                   block_table.shape[1], causal if 0 <= causal < 2 ** 31 else -1,
-                                   1.0 / math.sqrt(d) if scale is None else scale, stream)
+        return self.lib.fa_kv4_fwd(*args, causal if 0 <= causal < 2 ** 31 else -1,
+                                   1.0 / math.sqrt(q.shape[3]) if scale is None else scale, stream)
 
 
 def _kv4_caller():
@@ -480,13 +488,17 @@ def fa_kv4_fwd(q, cache, block_table, lens, o, lse, causal=False, scale=None, st
     status = caller.fwd(q, cache, block_table, lens, o, lse, code, scale,
                         stream if stream is None else _handle(stream))
     if status != FA_OK:
-        shape = tuple(getattr(q, "shape", ()))
-        B, H, Nq, d = shape if len(shape) == 4 else (None,) * 4
-        _kv4_refuse("fa_kv4_fwd", status,
-                    [("q", q, _torch.bfloat16, (B, H, Nq, d)), ("cache", cache, _torch.uint8, (None, None, None)),
-                     ("block_table", block_table, _torch.int32, (B, None)), ("lens", lens, _torch.int32, (B,)),
-                     ("o", o, _torch.bfloat16, (B, H, Nq, d)), ("lse", lse, _torch.float32, (B, H, Nq))],
-                    _device_and_stream(0)[0], None, d)
+        _kv4_refuse_fwd("fa_kv4_fwd", status, q, cache, block_table, lens, o, lse)
+
+
+def _kv4_refuse_fwd(what, status, q, cache, block_table, lens, o, lse):
+    shape = tuple(getattr(q, "shape", ()))
+    B, H, Nq, d = shape if len(shape) == 4 else (None,) * 4
+    _kv4_refuse(what, status,
+                [("q", q, _torch.bfloat16, (B, H, Nq, d)), ("cache", cache, _torch.uint8, (None, None, None)),
+                 ("block_table", block_table, _torch.int32, (B, None)), ("lens", lens, _torch.int32, (B,)),
+                 ("o", o, _torch.bfloat16, (B, H, Nq, d)), ("lse", lse, _torch.float32, (B, H, Nq))],
+                _device_and_stream(0)[0], None, d)
 
 
 def fa_poll_status(stream=None):
@@ -505,6 +517,17 @@ def fa_selftest_wait_timeout(timeout_ns: int, stream=None):
 
     _check(load().fa_selftest_wait_timeout(int(timeout_ns), _stream_ptr(stream, torch.device("cuda"))),
            "fa_selftest_wait_timeout")
+
+
+def fa_selftest_kv4_timeout(q, cache, block_table, lens, o, lse, timeout_ns, stream=None):
+    """C fa_selftest_kv4_timeout: fa_kv4_fwd on these tensors with every wait
+    running out after timeout_ns; fa_poll_status then reports FA_ERR_TIMEOUT."""
+    _kv4_caller()
+    device, stream = _device_and_stream(stream if stream is None else _handle(stream))
+    args = _Kv4Ctypes(load()).fwd_args(q, cache, block_table, lens, o, lse, device)
+    status = -1 if args is None else load().fa_selftest_kv4_timeout(*args, int(timeout_ns), stream)
+    if status != FA_OK:
+        _kv4_refuse_fwd("fa_selftest_kv4_timeout", status, q, cache, block_table, lens, o, lse)
 
 
 def fa_strerror(status: int) -> str:

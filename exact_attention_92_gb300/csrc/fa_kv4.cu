@@ -166,34 +166,10 @@ void plan_grid(int B, int Hkv, int d, int sm_count, fa_kv4_plan_t* pl) {
                                                 sizeof(fa::Kv4Cut));
 }
 
-}  // namespace
-
-extern "C" {
-
-int fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d, uint64_t* bytes) {
-  if (bytes == nullptr) return FA_ERR_INVALID_ARG;
-  const int e = check_sizes(1, 1, Hkv, 1, d, num_pages, page_size, 1);
-  if (e) return e;
-  *bytes = (uint64_t)num_pages * Hkv * page_size * (9 * d / 8);
-  return FA_OK;
-}
-
-int fa_kv4_write(const void* k, const void* v, void* cache, const int* block_table, const int* start,
-                 const int* count, int B, int Hkv, int N, int d, int num_pages, int page_size, int max_pages,
-                 void* stream) {
-  return move(true, k, v, nullptr, nullptr, cache, block_table, start, count, B, Hkv, N, d, num_pages, page_size,
-              max_pages, stream);
-}
-
-int fa_kv4_read(const void* cache, const int* block_table, const int* start, const int* count, void* k, void* v,
-                int B, int Hkv, int N, int d, int num_pages, int page_size, int max_pages, void* stream) {
-  return move(false, nullptr, nullptr, k, v, cache, block_table, start, count, B, Hkv, N, d, num_pages, page_size,
-              max_pages, stream);
-}
-
-int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const int* lens, void* o, float* lse,
-               int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size, int max_pages, int causal,
-               float scale, void* stream) {
+// fa_kv4_fwd, its waits limited to `timeout_ns`; `missing`: see Kv4FwdParams.
+int forward(const void* q, const void* cache, const int* block_table, const int* lens, void* o, float* lse, int B, int H,
+            int Hkv, int Nq, int d, int num_pages, int page_size, int max_pages, int causal, float scale,
+            unsigned long long timeout_ns, uint32_t missing, void* stream) {
   if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(block_table, 4) ||
       !aligned(lens, 4))
     return FA_ERR_INVALID_ARG;
@@ -226,7 +202,8 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
   f.p.part_o = nullptr;
   f.p.part_ml = nullptr;
   f.p.cuts = nullptr;
-  f.p.timeout_ns = fa::internal_wait_timeout_ns();
+  f.p.timeout_ns = timeout_ns;
+  f.p.missing = missing;
   f.st = static_cast<cudaStream_t>(stream);
   void* ws = nullptr;
   if (pl.workspace_bytes > 0) {
@@ -243,6 +220,46 @@ int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const i
   if (ce == cudaSuccess && ws != nullptr) ce = fa::internal_timed_launch(FA_KERNEL_KV4_MERGE, f.st, run_merge, &f);
   if (ws != nullptr) cudaFreeAsync(ws, f.st);
   return ce == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d, uint64_t* bytes) {
+  if (bytes == nullptr) return FA_ERR_INVALID_ARG;
+  const int e = check_sizes(1, 1, Hkv, 1, d, num_pages, page_size, 1);
+  if (e) return e;
+  *bytes = (uint64_t)num_pages * Hkv * page_size * (9 * d / 8);
+  return FA_OK;
+}
+
+int fa_kv4_write(const void* k, const void* v, void* cache, const int* block_table, const int* start,
+                 const int* count, int B, int Hkv, int N, int d, int num_pages, int page_size, int max_pages,
+                 void* stream) {
+  return move(true, k, v, nullptr, nullptr, cache, block_table, start, count, B, Hkv, N, d, num_pages, page_size,
+              max_pages, stream);
+}
+
+int fa_kv4_read(const void* cache, const int* block_table, const int* start, const int* count, void* k, void* v,
+                int B, int Hkv, int N, int d, int num_pages, int page_size, int max_pages, void* stream) {
+  return move(false, nullptr, nullptr, k, v, cache, block_table, start, count, B, Hkv, N, d, num_pages, page_size,
+              max_pages, stream);
+}
+
+int fa_kv4_fwd(const void* q, const void* cache, const int* block_table, const int* lens, void* o, float* lse,
+               int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size, int max_pages, int causal,
+               float scale, void* stream) {
+  return forward(q, cache, block_table, lens, o, lse, B, H, Hkv, Nq, d, num_pages, page_size, max_pages, causal, scale,
+                 fa::internal_wait_timeout_ns(), 0, stream);
+}
+
+int fa_selftest_kv4_timeout(const void* q, const void* cache, const int* block_table, const int* lens, void* o,
+                            float* lse, int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size,
+                            int max_pages, uint64_t timeout_ns, void* stream) {
+  if (timeout_ns > 2000000000ull) return FA_ERR_INVALID_ARG;
+  return forward(q, cache, block_table, lens, o, lse, B, H, Hkv, Nq, d, num_pages, page_size, max_pages,
+                 FA_CAUSAL_NONE, 1.f, timeout_ns, 16, stream);
 }
 
 int fa_kv4_fwd_plan(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages, int sm_count,

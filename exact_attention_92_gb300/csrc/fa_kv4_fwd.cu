@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     if (!good && my_key < C::kKeys && pos < ahead.len) kv4_bad_index(p.c);
     const uint32_t ones = __ballot_sync(0xffffffffu, good);
     have = (have << C::kBlocks) | ones;
-    if (lane == 0) mbar_arrive_expect_tx(&bar[stage], __popc(ones) * copy_bytes);
+    if (lane == 0) mbar_arrive_expect_tx(&bar[stage], __popc(ones) * copy_bytes + p.missing);
     __syncwarp();
     if (good)
       bulk_load(ring + stage * C::kStageBytes + lane * copy_bytes,

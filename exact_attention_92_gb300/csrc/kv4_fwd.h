@@ -38,6 +38,7 @@ struct Kv4FwdParams {
   float2* part_ml;         // [2 * grid][rows of a unit]: reference and sum
   Kv4Cut* cuts;            // [grid]
   unsigned long long timeout_ns;
+  uint32_t missing;        // bytes that every copy is announced with and does not bring (self-test; else 0)
 };
 
 namespace dev {

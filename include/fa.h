@@ -456,6 +456,18 @@ uint64_t fa_set_wait_timeout_ns(uint64_t ns);
 int fa_selftest_wait_timeout(uint64_t timeout_ns, void* stream);
 
 /*
+ * The same for fa_kv4_fwd's kernel, whose waits are for copies: a call
+ * (without a mask, scale 1) that announces each copy with 16 bytes more than
+ * it brings, so that every wait runs out after `timeout_ns`.  The kernel
+ * records FA_ERR_TIMEOUT, waits for the copies in flight for `timeout_ns` or
+ * 0.1 s, whichever is longer, and returns; o and lse are not meaningful.
+ * timeout_ns: at most 2 s (FA_ERR_INVALID_ARG).
+ */
+int fa_selftest_kv4_timeout(const void* q, const void* cache, const int* block_table, const int* lens, void* o,
+                            float* lse, int B, int H, int Hkv, int Nq, int d, int num_pages, int page_size,
+                            int max_pages, uint64_t timeout_ns, void* stream);
+
+/*
  * Per-kernel timing for benchmarks.  While enabled, every launch of a library
  * kernel is bracketed by two CUDA events recorded on the launch's stream.
  * Kernel ids: FA_KERNEL_FWD (forward main kernel), FA_KERNEL_COMBINE

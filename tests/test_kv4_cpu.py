@@ -203,6 +203,15 @@ def test_fwd_refusals(lib):
         assert _fwd(lib, ptrs) == fa.FA_ERR_INVALID_ARG
 
 
+def test_selftest_refuses_what_the_call_refuses(lib):
+    ptrs = [P(0x1000 * (i + 1)) for i in range(6)]
+    s = [FWD[n] for n in ("B", "H", "Hkv", "Nq", "d", "num_pages", "page_size", "max_pages")]
+    assert lib.fa_selftest_kv4_timeout(*ptrs, *s, 2_000_000_001, None) == fa.FA_ERR_INVALID_ARG
+    assert lib.fa_selftest_kv4_timeout(*ptrs, 0, *s[1:], 1000, None) == fa.FA_ERR_INVALID_ARG
+    assert lib.fa_selftest_kv4_timeout(*ptrs[:5], P(0), *s, 1000, None) == fa.FA_ERR_INVALID_ARG
+    assert lib.fa_selftest_kv4_timeout(*ptrs, *s[:3], 17, *s[4:], 1000, None) == fa.FA_ERR_UNSUPPORTED
+
+
 PLANS = [
     # B, H, Hkv, Nq, d, page_size, max_pages
     (1, 1, 1, 1, 64, 16, 1), (1, 32, 8, 1, 128, 16, 3), (8, 32, 8, 1, 128, 64, 128), (64, 32, 8, 1, 128, 64, 256),

@@ -695,6 +695,35 @@ def test_waits_that_give_up_are_reported(fa):
     check_attend(o, lse, q, f.k, f.v, [5000, 3000], 128 ** -0.5, "none")
 
 
+@pytest.mark.parametrize("d,H,lens", [(128, 4, [5000, 3000]), (64, 2, [40, 0]), (96, 40, [900, 4000]), (256, 8, [7, 600])])
+def test_every_wait_runs_out(fa, d, H, lens):
+    """Copies that never arrive in full: every wait gives up after its limit
+    and the drain after its own (0.1 s), the call is reported once and the next
+    one is correct."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(d)
+    f = Filled(fa, rng, lens, 2, d, 64)
+    qd, q = normal(rng, (2, H, 1, d))
+    o, lse = torch.empty_like(qd), torch.empty((2, H, 1), device="cuda")
+    assert fa.fa_poll_status() == fa.FA_OK
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    fa.fa_selftest_kv4_timeout(qd, f.cache, f.td, f.ld, o, lse, 20_000_000)
+    end.record()
+    assert fa.fa_poll_status() == fa.FA_ERR_TIMEOUT
+    assert fa.fa_poll_status() == fa.FA_OK
+    end.synchronize()
+    assert 120 <= start.elapsed_time(end) < 2000  # ms: the wait's limit, then the drain's
+    o, lse = fa.kv4_forward(qd, f.cache, f.td, f.ld)
+    assert fa.fa_poll_status() == fa.FA_OK
+    check_attend(o, lse, q, f.k, f.v, lens, d ** -0.5, "none")
+    with pytest.raises(fa.FaError) as e:
+        fa.fa_selftest_kv4_timeout(qd, f.cache, f.td, f.ld, o, lse, 3_000_000_000)
+    assert e.value.status == fa.FA_ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        fa.fa_selftest_kv4_timeout(qd, f.cache, f.td, f.ld, o, lse[:1], 20_000_000)
+
+
 # --------------------------------------------------------- used together
 
 @pytest.mark.parametrize("d", (64, 128, 256))
