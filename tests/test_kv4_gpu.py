@@ -678,6 +678,52 @@ def test_every_count_of_query_rows(fa, d, rows):
         check_attend(o, lse, q, g.k, g.v, n, d ** -0.5, "none", f"rows={rows}")
 
 
+def attend64(q, k, v, lens, scale):
+    """O, L and the bounds of check_attend, without a mask, for all sequences
+    at once: float64 tensors q [B, Hkv, R, d], k, v [B, Hkv, N, d]."""
+    torch = torch_cuda()
+    n = lens[:, None, None, None].double()
+    seen = torch.arange(k.shape[2], device="cuda")[None, None, None, :] < lens[:, None, None, None]
+    S = (scale * q @ k.transpose(-1, -2)).masked_fill(~seen, -np.inf)
+    L = torch.logsumexp(S, -1)
+    P = torch.where(seen, torch.exp(S - L[..., None]), 0.0)
+    e = 2.0 ** -19 * ((scale * q.abs() @ k.abs().transpose(-1, -2)) * seen).amax(-1)
+    O = P @ v
+    bo = 2.0 ** -8 * O.abs() + (2.0 ** -11 + 2.0 ** -13 + 2.0 ** -20 + 2 * e)[..., None] * (P @ v.abs())
+    bo = bo + n * 2.0 ** -29 * (P * v.abs().amax(-1)[:, :, None]).amax(-1)[..., None]
+    return O, L, bo, e + 2.0 ** -20 * L.abs().clamp(min=1)
+
+
+@pytest.mark.parametrize("rows,B", [(1, 64), (4, 64), (8, 64), (16, 64), (20, 64), (24, 80)])
+@pytest.mark.parametrize("d", DIMS)
+def test_several_whole_units_a_cta(fa, d, rows, B):
+    """More units than SMs, each of at most 24 steps: CTAs take several units
+    whole, and their stretches of the list begin where units do."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(d + rows)
+    Hkv, page, N = 8, 64, 760
+    f = Filled(fa, rng, [N] * 3, Hkv, d, page, room=8)  # three stored sequences, which all others share
+    at = np.arange(B) % 3
+    lens = rng.integers(0, N + 1, B)
+    lens[:5] = (N, 0, 1, 768 - 8, 32)
+    plan = fa.fa_kv4_fwd_plan(B, Hkv * rows, Hkv, 1, d, page, 12, torch.cuda.get_device_properties(0).multi_processor_count)
+    assert plan["whole"] == 1 and plan["launches"] == 1 and plan["grid"] < plan["units"] and plan["max_steps"] == 24
+    if rows in (16, 24):  # the units with two and three tiles of rows
+        assert plan["unit_rows"] == (8 if d == 256 else 24 if rows == 24 and d <= 96 else 16)
+    qd, _ = normal(rng, (B, Hkv * rows, 1, d))
+    o, lse = fa.kv4_forward(qd, f.cache, ints(f.table[at][:, :12]), ints(lens))
+    assert fa.fa_poll_status() == fa.FA_OK
+    k, v = (torch.from_numpy(x).cuda()[torch.from_numpy(at).cuda()] for x in (f.k, f.v))
+    n = torch.from_numpy(lens).cuda()
+    O, L, bo, bl = attend64(qd.double().view(B, Hkv, rows, d), k, v, n, d ** -0.5)
+    o, lse = o.double().view(B, Hkv, rows, d), lse.double().view(B, Hkv, rows)
+    empty = n == 0
+    assert (o[empty] == 0).all() and torch.isneginf(lse[empty]).all() and bool(empty.any())
+    full = ~empty
+    assert ((o - O)[full].abs() <= bo[full] + 1e-38).all(), ((o - O).abs() / bo)[full].max()
+    assert ((lse - L)[full].abs() <= bl[full]).all(), ((lse - L).abs() / bl)[full].max()
+
+
 def test_waits_that_give_up_are_reported(fa):
     """With no time to wait, the kernel may give up on its copies: it records
     FA_ERR_TIMEOUT, returns, and the next call is correct."""
