@@ -571,8 +571,10 @@ int fa_poll_status(void* stream) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return FA_ERR_CUDA;
   unsigned int word[2] = {0u, 0u};
   if (cudaMemcpy(word, s->status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return FA_ERR_CUDA;
-  if ((word[0] | word[1]) != 0u && cudaMemset(s->status, 0, sizeof(word)) != cudaSuccess) return FA_ERR_CUDA;
-  return word[0] != 0u ? (int)(word[0] & 0xffu) : (int)word[1];
+  // Only the word that is reported is cleared: with both set, the next call reports the other.
+  const int which = word[0] != 0u ? 0 : 1;
+  if (word[which] != 0u && cudaMemset(s->status + which, 0, sizeof(word[0])) != cudaSuccess) return FA_ERR_CUDA;
+  return (int)(word[which] & 0xffu);
 }
 
 int fa_selftest_wait_timeout(uint64_t timeout_ns, void* stream) {

@@ -432,10 +432,11 @@ int fa_kv4_fwd_plan(int B, int H, int Hkv, int Nq, int d, int page_size, int max
                     fa_kv4_plan_t* plan);
 
 /*
- * Synchronise `stream`, then return and clear the device status word of the
+ * Synchronise `stream`, then return and clear the device status of the
  * current device: FA_OK, FA_ERR_TIMEOUT if a kernel's bounded wait gave up
  * since the last poll, FA_ERR_BAD_INDEX if a fa_kv4_* kernel skipped an index
- * out of range, or FA_ERR_CUDA if the synchronisation failed.
+ * out of range, or FA_ERR_CUDA if the synchronisation failed.  Where both
+ * happened, one call returns FA_ERR_TIMEOUT and the next FA_ERR_BAD_INDEX.
  */
 int fa_poll_status(void* stream);
 

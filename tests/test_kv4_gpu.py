@@ -585,6 +585,20 @@ def test_bad_lengths_and_positions_are_clamped_and_reported(fa):
     check_attend(o, lse, q, f.k, f.v, [32, 32], d ** -0.5, "none")
 
 
+def test_a_timeout_does_not_hide_a_bad_index(fa):
+    rng = np.random.default_rng(13)
+    f = Filled(fa, rng, [32], 1, 64, 16)
+    qd, _ = normal(rng, (1, 1, 1, 64))
+    for bad_first in (True, False):
+        assert fa.fa_poll_status() == fa.FA_OK
+        if not bad_first:
+            fa.fa_selftest_wait_timeout(10_000_000)
+        fa.kv4_forward(qd, f.cache, f.td, ints([-1]))
+        if bad_first:
+            fa.fa_selftest_wait_timeout(10_000_000)
+        assert [fa.fa_poll_status() for _ in range(3)] == [fa.FA_ERR_TIMEOUT, fa.FA_ERR_BAD_INDEX, fa.FA_OK]
+
+
 def test_binding_refusals(fa, caller):
     torch = torch_cuda()
     rng = np.random.default_rng(9)
