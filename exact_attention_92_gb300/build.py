@@ -15,6 +15,7 @@ import re
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -83,8 +84,8 @@ def check_spills(ptxas_log: str) -> None:
 def build_call(force: bool = False) -> str | None:
     """Compile the native caller of the 4-bit cache's entry points (_kv4_call.so,
     against torch's and Python's headers); None where torch with CUDA is not
-    installed.  It holds no device code: without it the binding makes the same
-    calls through ctypes."""
+    installed, and, with a warning, where it does not compile.  It holds no device
+    code: without it the binding makes the same calls through ctypes."""
     import importlib.util
     import sysconfig
 
@@ -105,9 +106,16 @@ def build_call(force: bool = False) -> str | None:
            os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-I",
            sysconfig.get_paths()["include"], CALL_SOURCE, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}",
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cxx} failed on {CALL_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        said = r.stdout + r.stderr
+    except OSError as e:
+        r, said = None, str(e)
+    if r is None or r.returncode != 0:
+        if os.path.exists(CALL):
+            os.remove(CALL)  # of an older source
+        warnings.warn(f"the 4-bit cache's calls go through ctypes: {cxx} failed on {CALL_SOURCE}:\n{said}")
+        return None
     os.replace(tmp, CALL)
     return CALL
 

@@ -3,6 +3,7 @@ refusals that the host makes before any device work."""
 
 import ctypes
 import itertools
+import os
 
 import numpy as np
 import pytest
@@ -334,3 +335,35 @@ def test_binding_refuses_host_tensors(caller):
     assert fa.kv4_cache(3, 2, 16, 64, device="cpu").shape == cache.shape
     with pytest.raises(fa.FaError):
         fa.kv4_cache(3, 2, 24, 64, device="cpu")
+
+
+# ------------------------------------------------------------ native caller
+
+@pytest.fixture
+def caller_build(lib, monkeypatch, tmp_path):
+    """The build of the native caller with a compiler that only notes that it
+    ran, and its product elsewhere."""
+    pytest.importorskip("torch")
+    runs = tmp_path / "runs"
+    cxx = tmp_path / "cxx"
+    cxx.write_text("#!/bin/sh\n"
+                   f"echo run >> {runs}\n"
+                   'while [ "$1" != -o ]; do shift; done\n'
+                   'echo made > "$2"\n')
+    cxx.chmod(0o755)
+    monkeypatch.setenv("CXX", str(cxx))
+    monkeypatch.setattr(build, "CALL", str(tmp_path / "_kv4_call.so"))
+    return lambda: len(runs.read_text().split()) if runs.exists() else 0
+
+
+@pytest.mark.parametrize("cxx", ("/bin/false", "/nonexistent/c++"))
+def test_build_does_without_a_native_caller(caller_build, monkeypatch, cxx):
+    """A compiler that fails, or is not there, costs the native caller only; one
+    of an older source is not left behind."""
+    assert build.build_call() == build.CALL
+    os.utime(build.CALL, (1, 1))
+    monkeypatch.setenv("CXX", cxx)
+    for _ in range(2):
+        with pytest.warns(UserWarning, match="ctypes"):
+            assert build.build() == build.LIB
+        assert not os.path.exists(build.CALL)
