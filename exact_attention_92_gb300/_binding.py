@@ -10,10 +10,12 @@ raises FaError: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 import re
 import threading
+import warnings
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfa.so")
@@ -311,7 +313,7 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, causal=False, scale=None, 
 
 
 # The calls over the 4-bit cache are made once a layer and decoding step, where
-# the time of marshalling shows: they go through a native caller (_kv4_call.so,
+# the time of marshalling shows: they go through a native caller (_kv4_call,
 # csrc/kv4_call.cpp) that looks at the tensors and calls libfa.so, 2.1 us
 # a call on a GB300's host in place of 7 through ctypes and 18 with each tensor
 # checked by itself.  It says only that something is wrong; what, is worked out
@@ -381,6 +383,26 @@ class _Kv4Ctypes:
                                    1.0 / math.sqrt(q.shape[3]) if scale is None else scale, stream)
 
 
+def _native_caller(torch_version):
+    """The native caller, or None: where it was not built, and, with a warning,
+    where it does not load or was compiled against the headers of another torch
+    (whose tensors it would misread)."""
+    try:
+        native = importlib.import_module("._kv4_call", __package__)
+    except ModuleNotFoundError:
+        return None
+    except ImportError as e:
+        why = str(e)
+    else:
+        built, runs = (re.match(r"[0-9.]*", str(v)).group()
+                       for v in (getattr(native, "torch_version", ""), torch_version))
+        if built == runs:
+            return native
+        why = f"compiled against torch {built or '?'}, this is {runs}"
+    warnings.warn(f"the 4-bit cache's calls go through ctypes ({why}): run the build again")
+    return None
+
+
 def _kv4_caller():
     """The caller, and with it torch; made at the first call."""
     global _torch, _kv4
@@ -389,9 +411,8 @@ def _kv4_caller():
 
         lib = load()
         _torch = torch
-        try:
-            from . import _kv4_call as native
-        except ImportError:
+        native = _native_caller(torch.__version__)
+        if native is None:
             _kv4 = _Kv4Ctypes(lib)
         else:
             native.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value

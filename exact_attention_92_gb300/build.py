@@ -15,6 +15,7 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,7 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 CALL_SOURCE = os.path.join(CSRC, "kv4_call.cpp")
-CALL = os.path.join(PKG, "_kv4_call.so")
+CALL = os.path.join(PKG, "_kv4_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd256.cu", "fa_bwd.cu", "fa_bwd_pair.cu", "fa_bwd256.cu", "fa_noalloc.cu",
            "fa_kv4.cu", "fa_kv4_move.cu", "fa_kv4_fwd.cu"]
@@ -81,24 +82,39 @@ def check_spills(ptxas_log: str) -> None:
                     raise RuntimeError(f"{entry} starts with {m.group(1)} registers, its register split needs {regs}")
 
 
+def _call_key(torch_dir: str) -> str:
+    """What the native caller is compiled against: it holds the layout of
+    torch's and CPython's objects."""
+    import importlib.metadata
+
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    st = os.stat(os.path.join(torch_dir, "lib", "libtorch_python.so"))
+    return "\n".join([version, torch_dir, f"{st.st_size} {st.st_mtime_ns}", sys.version, sysconfig.get_paths()["include"]])
+
+
 def build_call(force: bool = False) -> str | None:
-    """Compile the native caller of the 4-bit cache's entry points (_kv4_call.so,
-    against torch's and Python's headers); None where torch with CUDA is not
+    """Compile the native caller of the 4-bit cache's entry points (CALL, against
+    torch's and Python's headers: again when those are other ones); None where torch with CUDA is not
     installed, and, with a warning, where it does not compile.  It holds no device
     code: without it the binding makes the same calls through ctypes."""
     import importlib.util
-    import sysconfig
 
     spec = importlib.util.find_spec("torch")  # found, not imported
     if spec is None or not spec.submodule_search_locations:
         return None
-    if not force and os.path.exists(CALL) and os.path.getmtime(CALL) >= max(
-            os.path.getmtime(CALL_SOURCE), os.path.getmtime(__file__)):
-        return CALL
     torch_dir = list(spec.submodule_search_locations)[0]
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
-    if not os.path.exists(os.path.join(lib, "libc10_cuda.so")):
+    if not all(os.path.exists(os.path.join(lib, f)) for f in ("libc10_cuda.so", "libtorch_python.so")):
         return None
+    key, key_file = _call_key(torch_dir), CALL + ".key"
+    if not force and os.path.exists(CALL) and os.path.exists(key_file) and os.path.getmtime(CALL) >= max(
+            os.path.getmtime(CALL_SOURCE), os.path.getmtime(__file__)):
+        with open(key_file, encoding="utf-8") as fh:
+            if fh.read() == key:
+                return CALL
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
     tmp = CALL + ".tmp"
@@ -113,10 +129,12 @@ def build_call(force: bool = False) -> str | None:
         r, said = None, str(e)
     if r is None or r.returncode != 0:
         if os.path.exists(CALL):
-            os.remove(CALL)  # of an older source
+            os.remove(CALL)  # of an older source, or against other headers
         warnings.warn(f"the 4-bit cache's calls go through ctypes: {cxx} failed on {CALL_SOURCE}:\n{said}")
         return None
     os.replace(tmp, CALL)
+    with open(key_file, "w", encoding="utf-8") as fh:
+        fh.write(key)
     return CALL
 
 

@@ -14,6 +14,7 @@
 
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 namespace {
 
@@ -175,4 +176,12 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_kv4_call", "Calls over the 4-bi
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__kv4_call() { return PyModule_Create(&g_module); }
+// torch_version: of the headers, for the binding to compare with torch's own.
+PyMODINIT_FUNC PyInit__kv4_call() {
+  PyObject* m = PyModule_Create(&g_module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

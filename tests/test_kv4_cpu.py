@@ -367,3 +367,33 @@ def test_build_does_without_a_native_caller(caller_build, monkeypatch, cxx):
         with pytest.warns(UserWarning, match="ctypes"):
             assert build.build() == build.LIB
         assert not os.path.exists(build.CALL)
+
+
+def test_native_caller_is_compiled_again_for_another_torch(caller_build, monkeypatch):
+    import importlib.metadata
+
+    assert build.build_call() == build.CALL and caller_build() == 1
+    assert build.build_call() == build.CALL and caller_build() == 1
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "1.0")
+    assert build.build_call() == build.CALL and caller_build() == 2
+    assert build.build_call() == build.CALL and caller_build() == 2
+    os.remove(build.CALL + ".key")
+    assert build.build_call() == build.CALL and caller_build() == 3
+
+
+def test_native_caller_is_this_pythons(lib):
+    import sysconfig
+
+    assert build.CALL.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def test_native_caller_of_another_torch_is_not_used(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
+    native = _binding._native_caller(torch.__version__)
+    assert native is not None
+    with pytest.warns(UserWarning, match="1.0.0"):
+        assert _binding._native_caller("1.0.0+cu1") is None
+    monkeypatch.setattr(_binding, "_kv4", None)
+    monkeypatch.setattr(native, "torch_version", "1.0.0")
+    with pytest.warns(UserWarning, match="1.0.0"):
+        assert isinstance(_binding._kv4_caller(), _binding._Kv4Ctypes)
