@@ -321,6 +321,7 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, causal=False, scale=None, 
 
 _torch = None
 _kv4 = None
+_INT_MAX = 2 ** 31 - 1
 
 
 class _Kv4Ctypes:
@@ -334,7 +335,8 @@ class _Kv4Ctypes:
     def _good(tensors, device):
         return all(isinstance(t, _torch.Tensor) and t.dtype is dtype and t.dim() == len(shape) and t.is_contiguous()
                    and t.is_cuda and t.get_device() == device
-                   and all(w is None or n == w for n, w in zip(t.shape, shape)) for t, dtype, shape in tensors)
+                   and all(n <= _INT_MAX and (w is None or n == w) for n, w in zip(t.shape, shape))
+                   for t, dtype, shape in tensors)
 
     def move(self, write, k, v, cache, block_table, start, count, stream):
         device, stream = _device_and_stream(stream)
@@ -455,19 +457,29 @@ def _kv4_refuse(what, status, tensors, device, heads, d):
                              f"got {t.dtype} {tuple(t.shape)}")
         if t.get_device() != device:
             raise ValueError(f"{name} is on {t.device}, not on the current CUDA device (use torch.cuda.device)")
+        if any(n > _INT_MAX for n in t.shape):
+            raise ValueError(f"{name} has a size beyond 2^31 - 1: {tuple(t.shape)}")
     cache = next(t for name, t, _, _ in tensors if name == "cache")
     if heads is not None and cache.shape[1] != heads:
         raise ValueError(f"cache has {cache.shape[1]} heads, k has {heads}")
     if d == 0 or cache.shape[2] * 8 % (9 * d) or cache.shape[2] == 0:
         raise ValueError(f"cache has {cache.shape[2]} bytes a page and head, not a multiple of 9 * {d} / 8")
-    raise ValueError(f"{what}: a size is out of range")
+    raise ValueError(f"{what}: torch gives no memory for one of the tensors")
+
+
+def _c_ints(what, *values):
+    """Numbers as C ints; refused where they are none (ctypes would cut them)."""
+    out = [int(v) for v in values]
+    if any(not -_INT_MAX <= v <= _INT_MAX for v in out):
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    return out
 
 
 def fa_kv4_cache_bytes(num_pages, Hkv, page_size, d) -> int:
     """C fa_kv4_cache_bytes: bytes of a 4-bit key/value cache."""
     n = ctypes.c_uint64(0)
-    _check(load().fa_kv4_cache_bytes(int(num_pages), int(Hkv), int(page_size), int(d), ctypes.byref(n)),
-           "fa_kv4_cache_bytes")
+    sizes = _c_ints("fa_kv4_cache_bytes", num_pages, Hkv, page_size, d)
+    _check(load().fa_kv4_cache_bytes(*sizes, ctypes.byref(n)), "fa_kv4_cache_bytes")
     return n.value
 
 
@@ -611,8 +623,8 @@ def fa_kv4_fwd_plan(B, H, Hkv, Nq, d, page_size, max_pages, sm_count):
     """C fa_kv4_fwd_plan: the launch plan of fa_kv4_fwd, as a dict of the
     fa_kv4_plan_t fields.  Host only; raises FaError on a refused size."""
     plan = Kv4Plan()
-    _check(load().fa_kv4_fwd_plan(int(B), int(H), int(Hkv), int(Nq), int(d), int(page_size), int(max_pages),
-                                  int(sm_count), ctypes.byref(plan)), "fa_kv4_fwd_plan")
+    sizes = _c_ints("fa_kv4_fwd_plan", B, H, Hkv, Nq, d, page_size, max_pages, sm_count)
+    _check(load().fa_kv4_fwd_plan(*sizes, ctypes.byref(plan)), "fa_kv4_fwd_plan")
     return _plan_dict(plan)
 
 

@@ -397,3 +397,58 @@ def test_native_caller_of_another_torch_is_not_used(lib, monkeypatch):
     monkeypatch.setattr(native, "torch_version", "1.0.0")
     with pytest.warns(UserWarning, match="1.0.0"):
         assert isinstance(_binding._kv4_caller(), _binding._Kv4Ctypes)
+
+
+# ------------------------------------------------------- sizes beyond an int
+
+@pytest.mark.parametrize("i", range(4))
+def test_cache_bytes_refuses_sizes_beyond_an_int(lib, i):
+    args = [10, 8, 64, 128]
+    for off in (2 ** 32, -2 ** 32):
+        args[i] += off
+        with pytest.raises(fa.FaError) as e:
+            fa.fa_kv4_cache_bytes(*args)
+        assert e.value.status == fa.FA_ERR_INVALID_ARG
+        args[i] -= off
+
+
+@pytest.mark.parametrize("i", range(8))
+def test_plan_refuses_sizes_beyond_an_int(lib, i):
+    args = [2, 32, 4, 2, 128, 64, 10, 152]
+    args[i] += 2 ** 32
+    with pytest.raises(fa.FaError) as e:
+        fa.fa_kv4_fwd_plan(*args)
+    assert e.value.status == fa.FA_ERR_INVALID_ARG
+
+
+def test_ctypes_caller_refuses_sizes_beyond_an_int(lib, monkeypatch):
+    """A block table of more than 2^31 columns (tensors without memory stand in
+    for it) is refused like the native caller does, not cut to its low bits."""
+    torch = pytest.importorskip("torch")
+
+    class Lib:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} was called")
+
+    class Meta(torch.Tensor):  # a tensor without memory that says it is on the device
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+
+    def meta(*shape, dtype=torch.int32):
+        return torch.empty(shape, dtype=dtype, device="meta").as_subclass(Meta)
+
+    monkeypatch.setattr(_binding, "_torch", torch)
+    monkeypatch.setattr(_binding, "_device_and_stream", lambda stream: (0, 0))
+    made = _binding._Kv4Ctypes(Lib())
+    k = meta(1, 2, 4, 64, dtype=torch.bfloat16)
+    cache, table, one = meta(3, 2, 16 * 72, dtype=torch.uint8), meta(1, 2 ** 32 + 5), meta(1)
+    with pytest.raises(AssertionError):  # the stand-ins are good tensors otherwise
+        made.move(True, k, k, cache, meta(1, 5), one, None, 0)
+    assert made.move(True, k, k, cache, table, one, None, 0) == -1
+    assert made.move(False, k, k, cache, table, one, None, 0) == -1
+    q, lse = meta(1, 4, 1, 64, dtype=torch.bfloat16), meta(1, 4, 1, dtype=torch.float32)
+    assert made.fwd(q, cache, table, one, q, lse, 0, None, 0) == -1
+    with pytest.raises(ValueError, match="block_table has a size"):
+        _binding._kv4_refuse_fwd("fa_kv4_fwd", -1, q, cache, table, one, q, lse)
