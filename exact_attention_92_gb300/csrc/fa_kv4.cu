@@ -230,7 +230,10 @@ int fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d, uint64_t* b
   if (bytes == nullptr) return FA_ERR_INVALID_ARG;
   const int e = check_sizes(1, 1, Hkv, 1, d, num_pages, page_size, 1);
   if (e) return e;
-  *bytes = (uint64_t)num_pages * Hkv * page_size * (9 * d / 8);
+  // A page of a head is below 2^19 bytes; pages and heads are below 2^31 each.
+  const uint64_t page = (uint64_t)page_size * (9 * d / 8), pages = (uint64_t)num_pages * Hkv;
+  if (pages > INT64_MAX / page) return FA_ERR_INVALID_ARG;
+  *bytes = pages * page;
   return FA_OK;
 }
 

@@ -355,7 +355,8 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * stream serialization like those of the backward.
  */
 
-/* Bytes of a cache: num_pages * Hkv * page_size * 9 d / 8 in *bytes. */
+/* Bytes of a cache: num_pages * Hkv * page_size * 9 d / 8 in *bytes
+ * (FA_ERR_INVALID_ARG where that is 2^63 or more). */
 int fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d, uint64_t* bytes);
 
 /*

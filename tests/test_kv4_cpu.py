@@ -452,3 +452,14 @@ def test_ctypes_caller_refuses_sizes_beyond_an_int(lib, monkeypatch):
     assert made.fwd(q, cache, table, one, q, lse, 0, None, 0) == -1
     with pytest.raises(ValueError, match="block_table has a size"):
         _binding._kv4_refuse_fwd("fa_kv4_fwd", -1, q, cache, table, one, q, lse)
+
+
+def test_cache_bytes_beyond_64_bits_are_refused(lib):
+    n = ctypes.c_uint64(5)
+    big = 2 ** 31 - 1
+    for args in ((big, big, 1024, 256), (big, big, 16, 64), (big, 2 ** 14, 1024, 256)):
+        exact = args[0] * args[1] * args[2] * 9 * args[3] // 8
+        want = fa.FA_OK if exact < 2 ** 63 else fa.FA_ERR_INVALID_ARG
+        assert lib.fa_kv4_cache_bytes(*args, ctypes.byref(n)) == want
+        assert n.value == (exact if want == fa.FA_OK else 5)
+        n.value = 5
