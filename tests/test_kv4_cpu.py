@@ -463,3 +463,91 @@ def test_cache_bytes_beyond_64_bits_are_refused(lib):
         assert lib.fa_kv4_cache_bytes(*args, ctypes.byref(n)) == want
         assert n.value == (exact if want == fa.FA_OK else 5)
         n.value = 5
+
+
+# -------------------------------------------- planted mistakes in the oracle
+
+def _pin_of_places(d):
+    """Where include/fa.h puts channels, taken apart from the other end: the
+    channel and token of each nibble of a block, read in the order of bytes."""
+    ng = d // 32
+    for byte in range(16 * d):
+        section, at = divmod(byte, 8 * d)
+        row, col = divmod(at, d // 2)
+        if section == 0:
+            p = row
+            col ^= 64 * (p & 1) if d == 256 else 0
+            word, byte_in = divmod(col, 4)
+            high, rest = divmod(word, 16)
+            t, low = divmod(rest, min(ng, 4))
+            c = 32 * (4 * high + low) + 8 * t + 2 * byte_in
+        else:
+            col ^= {128: 32 * ((row >> 1) & 1), 256: 32 * (row & 3)}.get(d, 0)
+            p = 2 * (row & 3) + ((row >> 2) & 1) + 8 * (row >> 3)
+            unit, byte_in = divmod(col, 2)
+            u, g = divmod(unit, ng)
+            c = 32 * g + 4 * u + 2 * byte_in
+        place = kv4.key_place if section == 0 else kv4.value_place
+        assert place(d, p, c) == (byte, 0) and place(d, p, c + 1) == (byte, 4)
+    at = 16 * d
+    for p, w, g in itertools.product(range(16), range(2), range(ng)):
+        assert kv4.scale_place(d, p, w, g) == at
+        at += 2
+
+
+@pytest.mark.parametrize("d", DIMS)
+def test_places_are_the_headers(d):
+    _pin_of_places(d)
+
+
+def _pins():
+    for d in DIMS:
+        _pin_of_places(d)
+        test_a_block_has_a_place_for_everything(d)
+    test_levels_round_to_nearest_with_ties_to_even()
+    test_scale_is_the_rounded_sixth_of_the_largest()
+    test_a_group_with_a_non_finite_value_reads_as_nan()
+    test_error_of_a_held_value()
+    test_bf16_rounding_of_the_oracle()
+    for d in DIMS:
+        test_write_then_read(d)
+
+
+def test_pins_hold_without_a_mistake():
+    _pins()
+
+
+_KEY, _VALUE, _SCALE, _QUANTISE, _ROUND = (kv4.key_place, kv4.value_place, kv4.scale_place, kv4.quantise, kv4.to_bf16)
+
+
+def _coarse(x):
+    code, bits = _QUANTISE(x)
+    return code & 14, bits
+
+
+def _no_nan(x):
+    code, bits = _QUANTISE(x)
+    return code, np.where(bits == kv4.NAN_BITS, 0, bits).astype(np.uint16)
+
+
+MISTAKES = {
+    "the largest level is 5": ("LEVELS", np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 5.0])),
+    "two levels exchanged": ("LEVELS", np.array([0.0, 0.5, 1.5, 1.0, 2.0, 3.0, 4.0, 6.0])),
+    "tokens 2 and 4 of the values exchanged": ("value_place", lambda d, p, c: _VALUE(d, {2: 4, 4: 2}.get(p, p), c)),
+    "nibbles exchanged": ("key_place", lambda d, p, c: _KEY(d, p, c ^ 1)),
+    "no exchange of halves at d = 256": ("key_place", lambda d, p, c: _KEY(d, p, c) if d != 256 else (
+        p * 128 + _KEY(d, 0, c)[0], _KEY(d, 0, c)[1])),
+    "scales of keys and values exchanged": ("scale_place", lambda d, p, w, g: _SCALE(d, p, 1 - w, g)),
+    "scales of two groups exchanged": ("scale_place", lambda d, p, w, g: _SCALE(d, p, w, g ^ 1 if g < 2 else g)),
+    "three bits of code": ("quantise", _coarse),
+    "non-finite groups held as zeros": ("quantise", _no_nan),
+    "scales cut and not rounded": ("to_bf16", lambda x: _ROUND(np.asarray(x, dtype=np.float64) * (1 - 2.0 ** -9))),
+}
+
+
+@pytest.mark.parametrize("mistake", MISTAKES)
+def test_pins_catch_a_planted_mistake(mistake, monkeypatch):
+    name, wrong = MISTAKES[mistake]
+    monkeypatch.setattr(kv4, name, wrong)
+    with pytest.raises(AssertionError):
+        _pins()
