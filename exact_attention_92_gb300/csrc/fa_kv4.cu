@@ -191,7 +191,6 @@ int forward(const void* q, const void* cache, const int* block_table, const int*
   f.p.lens = lens;
   f.p.o = static_cast<__nv_bfloat16*>(o);
   f.p.lse = lse;
-  f.p.H = H;
   f.p.Nq = Nq;
   f.p.rows = pl.rows;
   f.p.row_blocks = pl.row_blocks;

@@ -26,7 +26,6 @@ struct Kv4FwdParams {
   const int* lens;         // [B]
   __nv_bfloat16* o;        // [B, H, Nq, d]
   float* lse;              // [B, H, Nq]
-  int H;
   int Nq;
   int rows;                // (H / Hkv) * Nq: query rows that share a key/value head
   int row_blocks;          // ceil(rows / rows of a unit)
