@@ -195,7 +195,11 @@ int forward(const void* q, const void* cache, const int* block_table, const int*
   f.p.rows = pl.rows;
   f.p.row_blocks = pl.row_blocks;
   f.p.causal = causal;
-  f.p.scale_log2 = scale * 1.4426950408889634f;
+  int power = 0;
+  const double rest = std::frexp((double)scale * 1.4426950408889634, &power);
+  power = std::min(power - 1, 127);
+  f.p.scale_pow2 = std::ldexp(1.f, power);
+  f.p.scale_rest = (float)(power == 127 ? (double)scale * 1.4426950408889634 / std::ldexp(1.0, 127) : 2 * rest);
   f.p.whole = pl.whole;
   f.p.single = pl.whole && pl.grid == pl.units ? 1 : 0;
   f.p.part_o = nullptr;

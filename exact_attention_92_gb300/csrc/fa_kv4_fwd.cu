@@ -38,7 +38,8 @@
 // to lie just below 2^16, where fp16 holds its bf16 values exactly down to
 // 2^-29 of the row's largest; the products of one group of 32 channels are
 // summed by the matrix instruction in fp32, multiplied by the group's scale over
-// that power of two in fp32 and added, so scores are those of the exact held values.  The weights
+// that power of two (and times that of the softmax's scale) in fp32 and added, so
+// scores are those of the exact held values.  The weights
 // p = 2^(s - ref) are multiplied by the values' scale in fp32 and rounded once
 // to fp16 (11 bits) for the P V product: bf16 would lose three bits, and 8 bits
 // of weight are what the output's own rounding costs.  To keep p * scale within
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     ++taken;
 
     uint32_t q[PACK ? 2 : NR][NG][4];  // as the column operand (PACK: for each block, in its half of the columns)
-    float2 cc[NR];          // what takes the power of two out of the sums of columns 2 t, 2 t + 1
+    float2 cc[NR];          // what takes the power of two out of the sums of columns 2 t, 2 t + 1, and puts the scale's in
     int low = len;          // keys that all rows see
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
           }
         }
       }
-      const float back = __uint_as_float((uint32_t)(top > 0.f ? 254 - f : 127) << 23);  // 1 / up
+      const float back = __uint_as_float((uint32_t)(top > 0.f ? 254 - f : 127) << 23) * p.scale_pow2;  // 1 / up: exact
       cc[r].x = __shfl_sync(0xffffffffu, back, 4 * col0);
       cc[r].y = __shfl_sync(0xffffffffu, back, 4 * col0 + 4);
     }
@@ -524,10 +525,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
       // blocks, the query rows once in its columns 0-3 for block 0 and once in
       // 4-7 for block 1, so that a lane has scores of one block only.
       constexpr int NS = PACK ? 1 : C::kBlocks;
-      float2 sc[NS][NR][2];  // keys g, g + 8: q k, then base-2 score + log2(largest scale of the value), then p
+      float2 sc[NS][NR][2];  // keys g, g + 8: q k, scaled but for `rest`, then base-2 score + log2(largest scale of the value), then p
       float vl[NS][2];       // log2(largest scale of the value)
       float top[NR][2];
-      const float2 to_log2 = make_float2(p.scale_log2, p.scale_log2);
+      const float2 rest = make_float2(p.scale_rest, p.scale_rest);
 #pragma unroll
       for (int r = 0; r < NR; ++r) top[r][0] = top[r][1] = -INFINITY;
       auto seen = [&](int s, int r, int x) {
@@ -571,8 +572,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
           const float fa_ = scale_of(wa, i), fb_ = scale_of(wb, i);
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            // The power of two goes to the scale first (exact): c times a scale
-            // may overflow where the score does not.
+            // The powers of two go to the key's scale first (exact): c times that
+            // scale, or q k, may overflow where the score does not.
             const float2 fa2 = __fmul2_rn(make_float2(fa_, fa_), cc[r]), fb2 = __fmul2_rn(make_float2(fb_, fb_), cc[r]);
             sc[s][r][0] = __ffma2_rn(fa2, make_float2(c[r][0], c[r][1]), sc[s][r][0]);
             sc[s][r][1] = __ffma2_rn(fb2, make_float2(c[r][2], c[r][3]), sc[s][r][1]);
@@ -582,8 +583,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           float2 &x = sc[s][r][0], &y = sc[s][r][1];
-          x = __ffma2_rn(x, to_log2, make_float2(va, va));
-          y = __ffma2_rn(y, to_log2, make_float2(vb, vb));
+          x = __ffma2_rn(x, rest, make_float2(va, va));
+          y = __ffma2_rn(y, rest, make_float2(vb, vb));
           if constexpr (MASK) {
             x.x = seen(s, r, 0) ? x.x : -INFINITY;
             x.y = seen(s, r, 1) ? x.y : -INFINITY;

@@ -30,7 +30,8 @@ struct Kv4FwdParams {
   int rows;                // (H / Hkv) * Nq: query rows that share a key/value head
   int row_blocks;          // ceil(rows / rows of a unit)
   int causal;              // FA_CAUSAL_*
-  float scale_log2;        // scale * log2(e)
+  float scale_pow2;        // scale * log2(e): a power of two,
+  float scale_rest;        // and what is left, 1 to 2 (more if the power is at its largest)
   int whole;               // 1: units are not cut
   int single;              // 1: nor does a CTA have more than one
   float* part_o;           // [2 * grid][rows of a unit][d]: partial sums (not whole)

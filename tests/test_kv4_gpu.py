@@ -405,6 +405,23 @@ def test_attend_small_queries_over_large_keys(fa, d, q_std, k_std):
         check_attend(o, lse, q, f.k, f.v, lens, d ** -0.5, "none", f"{q_std} {k_std}")
 
 
+@pytest.mark.parametrize("d", DIMS)
+@pytest.mark.parametrize("q_std,k_std,scale", [(1e19, 1e19, 1e-39), (1e10, 1e30, 1e-41), (1e-19, 1e-19, 1e37),
+                                               (1e-30, 1e-8, 3e37), (1e-3, 1e-36, 3e38), (1e-30, 1e31, 0.05)])
+def test_attend_scales_far_from_one(fa, d, q_std, k_std, scale):
+    """Scores that only the softmax's scale brings to an ordinary size: q k
+    overflows, or is subnormal, in fp32."""
+    rng = np.random.default_rng(d)
+    scale = float(np.float32(scale))
+    lens = [300, 41]
+    f = Filled(fa, rng, lens, 2, d, 32, k_std)
+    for H in (4, 12):
+        qd, q = normal(rng, (2, H, 1, d), q_std)
+        o, lse = fa.kv4_forward(qd, f.cache, f.td, f.ld, scale=scale)
+        assert fa.fa_poll_status() == fa.FA_OK
+        check_attend(o, lse, q, f.k, f.v, lens, scale, "none", f"{q_std} {k_std} {scale}")
+
+
 def test_attend_all_values_zero(fa):
     rng = np.random.default_rng(3)
     f = Filled(fa, rng, [77], 1, 128, 16, vals=np.zeros((1, 1, 77, 128)))
