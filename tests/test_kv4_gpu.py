@@ -485,6 +485,31 @@ def test_pages_far_apart(fa):
     check_attend(o, lse, q, kv4.held(k), kv4.held(v), [600, 512], d ** -0.5, "none")
 
 
+@pytest.mark.parametrize("d,rows,pages", [(64, 1, 2 ** 20), (128, 9, 2 ** 16)])
+def test_very_long_sequences(fa, d, rows, pages):
+    """2^30 positions, the most there may be, and 2^26: a table whose entries
+    are all one of four pages.  O is that of the pages each seen once, L is
+    larger by the logarithm of how often.  A warp adds up s steps one after the
+    other, in each two products to O (fp32, perhaps cut: 2^-23 of the sum each)
+    and at most four weights to their sum (rounded: 2^-24 each); where all go
+    the same way O is off by s 2^-21 of the largest value, L by s 2^-22."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(d)
+    page, each = 1024, pages // 4
+    f = Filled(fa, rng, [4 * page], 1, d, page)
+    qd, q = normal(rng, (1, rows, 1, d))
+    o, lse = fa.kv4_forward(qd, f.cache, ints(np.tile(f.table[0, :4], each)[None]), ints([pages * page]))
+    assert fa.fa_poll_status() == fa.FA_OK
+    k, v = torch.from_numpy(f.k).cuda(), torch.from_numpy(f.v).cuda()
+    O, L, bo, bl = attend64(qd.double().view(1, 1, rows, d), k, v, ints([4 * page]), d ** -0.5)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    steps = pages * page / 32 * -(-rows // 8) / (sms * 8)  # 8 warps a CTA at least
+    bo = bo + steps * 2.0 ** -21 * v.abs().amax()
+    assert ((o.double().view(O.shape) - O).abs() <= bo).all(), ((o.double().view(O.shape) - O).abs() / bo).max()
+    dl = (lse.double().view(L.shape) - (L + np.log(each))).abs()
+    assert (dl <= bl + steps * 2.0 ** -22 + 2.0 ** -20 * np.log(each)).all(), (dl / bl).max()
+
+
 def test_many_sequences(fa):
     """More sequences than a CTA has threads, most of them short or empty."""
     rng = np.random.default_rng(8)
@@ -979,6 +1004,40 @@ def test_calls_at_once_on_two_streams(fa):
     for i, (o, lse) in enumerate(outs):
         f, d, lens, qd, q, _ = jobs[i % 2]
         check_attend(o, lse, q, f.k, f.v, lens, d ** -0.5, "none")
+
+
+def test_calls_from_several_threads(fa, caller):
+    """Host threads, each with a stream and a cache of its own, call at once."""
+    import threading
+
+    torch = torch_cuda()
+    rng = np.random.default_rng(25)
+    jobs, errors = [], []
+    for d, lens in ((128, [2000, 31]), (64, [700, 900]), (96, [5, 0]), (256, [300, 1500])):
+        f = Filled(fa, rng, lens, 2, d, 32)
+        qd, q = normal(rng, (2, 6, 1, d))
+        jobs.append((f, d, lens, qd, q, torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+
+    def work(f, d, lens, qd, q, st, outs):
+        try:
+            with torch.cuda.stream(st):
+                for _ in range(20):
+                    outs.append(fa.kv4_forward(qd, f.cache, f.td, f.ld))
+        except Exception as e:  # reported by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and fa.fa_poll_status() == fa.FA_OK
+    for f, d, lens, qd, q, st, outs in jobs:
+        assert len(outs) == 20
+        check_attend(*outs[0], q, f.k, f.v, lens, d ** -0.5, "none")
+        assert all(torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1]) for o, l in outs)
 
 
 def test_launches_are_counted(fa):
