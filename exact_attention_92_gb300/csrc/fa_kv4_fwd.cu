@@ -74,12 +74,14 @@ template <int D, int NR, bool PACK>
 struct Cfg {
   // One CTA an SM, its warps a multiple of the four schedulers and as many as
   // their registers allow without spilling more than a few words outside the main
-  // loop's sums (65536 over 16, 12 or 8 warps: 128, 168 or 255 each; 16 warps at
-  // d = 128 spill and take 101 us in place of 96.7 in the case above, two row tiles
-  // at d = 96 with 12 warps 49.2 in place of 47.4).
-  static constexpr int kWarps = D == 256 || NR == 3 || (NR == 2 && D > 64) ? 8
-                                : NR == 1 && (D == 64 || (D == 96 && !PACK)) ? 16
-                                                                       : 12;
+  // loop's sums (65536 over 16, 12 or 8 warps: 128, 168 or 255 each).  16 warps at
+  // d = 128 spill and take 102.4 us in place of 94.7 in the case above.  At d = 96
+  // 12 warps are a little sooner done than 16 (9 ragged sequences, two units of 8
+  // rows 14.4 us and 14.9; 8 rows, 32 sequences of up to 4000 tokens 23.7 and 24.1,
+  // 16 of 8192 33.5 and 33.5), and with two row tiles 12 spill: long calls are 2%
+  // faster (16 rows, 16 sequences of 8192 47.0 and 48.1), short ones 6% slower (15
+  // rows, 9 ragged ones 16.7 and 15.7).
+  static constexpr int kWarps = D == 256 || NR == 3 || (NR == 2 && D > 64) ? 8 : NR == 1 && D == 64 ? 16 : 12;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kBlocks = 2;                             // 16-token blocks a step
   static constexpr int kKeys = kBlocks * kKv4Block;
