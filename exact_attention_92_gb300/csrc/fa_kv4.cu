@@ -31,8 +31,9 @@ namespace {
 constexpr int kMinPage = 16, kMaxPage = 1024;
 // Units of at most this many steps are not cut between CTAs: a second launch
 // costs more than it gains (32 sequences, 8 heads of d = 128: 16 steps 10.0 us
-// whole, 11.5 us cut; 24 steps 12.2 and 13.1; 32 steps, the lengths ragged, 13.3
-// and 12.7).
+// whole, 11.6 us cut; 24 steps 12.2 and 13.1; 32 steps 15.5 and 16.3, but the
+// lengths ragged 13.4 and 12.7).  The host knows the table's width and not the
+// lengths, so this goes by what the table has room for.
 constexpr int kWholeSteps = 24;
 constexpr int kMaxRows = 128;  // query rows of a key/value head's group (fa_kv4_fwd)
 
@@ -153,7 +154,7 @@ void plan_grid(int B, int Hkv, int d, int sm_count, fa_kv4_plan_t* pl) {
   pl->units = B * Hkv * pl->row_blocks;
   // Where every unit has a CTA of its own, up to three steps a warp, and four if
   // that keeps half the SMs busy (8 heads of d = 128: one sequence of 1000 tokens
-  // 8.3 us, cut 9.2, of 1500 9.8 and 9.2; 16 of 1500 10.5 and 13.3; alike at
+  // 8.3 us, cut 9.2, of 1500 9.7 and 9.2; 16 of 1500 10.5 and 13.2; alike at
   // d = 64 and 256 with their 16 and 8 warps).
   const int warps = fa::kv4_fwd_warps(d, pl->unit_rows);
   const int single = pl->units > sm_count ? 0 : (2 * pl->units >= sm_count ? 4 : 3) * warps;

@@ -7,8 +7,8 @@
 // that.  Where a border cuts a unit, the warps of a CTA join their fp32 results
 // at the CTA's end, and a second kernel merges those of the CTAs, both in the
 // order of the list, so the results do not change from run to run.  (Warps that
-// took a CTA's steps in turn and joined at each unit's end: 64 ragged sequences
-// 127 us in place of 109.)
+// took a CTA's steps in turn and joined at each unit's end, in an earlier form of
+// the kernel: 64 ragged sequences 127 us in place of 109.)
 //
 // Each warp fetches its own steps: bulk copies of whole 16-token blocks into a
 // ring in shared memory, ahead of use, so no warp waits for another within a
@@ -18,17 +18,18 @@
 // and their codes go from shared memory through one conversion instruction per
 // two values into the operand's registers.  With up to 4 query rows (PACK) the
 // two 16-key blocks of a step share the 8 columns, which halves the softmax's
-// share of the instructions (100.4 -> 96.7 us in the case below).
+// share of the instructions (100.5 -> 94.6 us in the case below).
 // (A tcgen05 product would want the 128-row operand in shared memory, decoded:
 // 512 bytes written and read back a token for 144 bytes of cache.)
 //
 // What bounds it (d = 128, 64 sequences of up to 16384 tokens, 8 heads, 4 rows,
-// 552 MB): 94.3 us, 5.9 TB/s of DRAM reads, 86% of what a copy moves.  500
-// instructions a step and warp, 57% of the issue slots while SMs are busy; 128 of
+// 552 MB): 94.6 us, 5.8 TB/s of DRAM reads, 86% of what a copy moves.  512
+// instructions a step and warp, 58% of the issue slots while SMs are busy; 128 of
 // them are conversions from e2m1 and about 100 others of the same half-rate pipe,
-// which so is in use 60% of the time; the matrix pipe 28%.  Scores, weights and
-// their sums are packed fp32 (20 instructions a step fewer: 96.7 us without).
-// Of a call of 8 sequences of 8192 tokens (22.3 us, 11.2 us of traffic) 3.4 us
+// which so is in use 61% of the time; the matrix pipe 29%.  Scores, weights and
+// their sums are packed fp32 (20 instructions a step fewer; an earlier form of the
+// step took 94.3 us with them and 96.7 without).
+// Of a call of 8 sequences of 8192 tokens (22.4 us, 11.2 us of traffic) 3.4 us
 // go before the first copies are on the way (lengths 0.9, place in the list 1.3,
 // page and issue 1.2) and 2.3 until their bytes are there; the warps end their
 // steps (9 or 10 each) between 14 and 19.6 us, 1.2 us go for the join and about 2
@@ -50,8 +51,8 @@
 // 2^((x - ref) - log2(scale)) of the same rounded x = s + log2(scale) that moves
 // the reference, so it keeps that bound where fp32 holds scores in steps of 4 and
 // more.  The sum
-// of p is fp32.  log2(scale) is taken at 2^-80 at least, which keeps the sum
-// of p below 2^121.
+// of p is fp32.  The scale is taken at 2^-80 at least: p stays below 2^94, and
+// the sum over the 2^30 positions that a table may have below 2^124.
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -1031,16 +1032,18 @@ cudaError_t launch_merge_d(int unit_rows, const Kv4FwdParams& p, int grid, cudaS
 // tiles a unit read and decode each key once for 16 rows, but leave room for
 // fewer warps: where there are few steps to an SM (`sm_steps`, with one tile a
 // unit), one tile is sooner done (d = 128, 16 rows, 8 heads: 4 sequences of 2000
-// tokens, 26 steps an SM, 12.3 us and 13.7 with two; 8 of 4000, 105 steps, 21.9
-// and 22.9; 16 of 4000, 210 steps, 35.2 and 31.9; d = 64 and 96 alike).  Not at
+// tokens, 26 steps an SM, 12.2 us and 13.7 with two; 8 of 4000, 105 steps, 22.0
+// and 22.6; 16 of 4000, 210 steps, 35.4 and 32.2; d = 64 and 96 24.4 and 23.5, 32.8
+// and 30.1).  The steps are those that the table has room for: a wider one takes
+// the two tiles however short the sequences are.  Not at
 // d = 256, whose sums take 64 registers a tile.
 // At d = 64 and 96, 17 to 24 rows are one unit of three tiles (24 rows, 16
-// sequences of 8000 tokens: d = 96 57.6 us, with two units of two tiles 76.8;
-// d = 64 46.2 and 53.9), at d = 64 from more steps on (9 of 4000, 178 steps an SM:
-// d = 96 26.7 us and 26.9 with one tile a unit, d = 64 23.2 and 21.1; 14 of 4000,
-// 276 steps: d = 64 28.0 and 27.9).  Four tiles for 32 rows at d = 64 gain nothing
-// (55.8 us, 54.3 with two), nor do three for more rows there (48 rows 77.9 and
-// 75.2).
+// sequences of 8000 tokens: d = 96 57.2 us, with three units of one tile 76.9 and
+// two of two tiles 81.4; d = 64 45.6, 54.0 and 55.9), at d = 64 from more steps on
+// (9 of 4000, 178 steps an SM: d = 96 26.8 us and 27.9 with one tile a unit, d = 64
+// 22.7 and 21.5; 14 of 4000, 276 steps: d = 64 28.1 and 28.6).  Three tiles for more
+// rows there gain nothing (48 rows 77.7 us, 77.9 with two), nor did four for 32 rows
+// (an earlier form: 55.8, 54.3 with two).
 int kv4_fwd_unit_rows(int d, int rows, long long sm_steps) {
   if (rows <= kKv4Rows / 2) return kKv4Rows / 2;
   if (rows <= kKv4Rows || d == 256) return kKv4Rows;

@@ -303,9 +303,9 @@ static cudaError_t launch_move_u(void (*kernel)(Kv4MoveParams), Kv4MoveParams& p
 template <int D>
 static cudaError_t launch_move_t(bool write, Kv4MoveParams& p, int sm_count, cudaStream_t stream) {
   // Several blocks a CTA keep enough loads in flight (writing and reading 4 x 8192
-  // tokens of 8 heads at d = 128: 63 us, with one block 75 us); where that leaves
+  // tokens of 8 heads at d = 128: 57.0 us, with one block 67.1); where that leaves
   // SMs without a CTA, one block each is sooner done (100 tokens of 12 heads at
-  // d = 96: 1.8 us, with four blocks 2.6 us).  Writing takes four (4 x 8192 tokens
+  // d = 96, read: 1.66 us, with two blocks 1.86).  Writing takes four (4 x 8192 tokens
   // 27.7 us, with two 28.8).  Reading takes two (28.1 us, with four 28.8; 24 pieces
   // of up to 1000 tokens at d = 96 20.3 and 21.0), but four at d = 64, whose CTAs
   // have half the threads (such pieces written and read back 28.7 us, with two 30.6;
