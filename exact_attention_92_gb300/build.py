@@ -97,9 +97,10 @@ def _call_key(torch_dir: str) -> str:
 
 def build_call(force: bool = False) -> str | None:
     """Compile the native caller of the 4-bit cache's entry points (CALL, against
-    torch's and Python's headers: again when those are other ones); None where torch with CUDA is not
-    installed, and, with a warning, where it does not compile.  It holds no device
-    code: without it the binding makes the same calls through ctypes."""
+    torch's and Python's headers: again when those are other ones); None where
+    torch with CUDA is not installed, and, with a warning, where it does not
+    compile.  It holds no device code: without it the binding makes the same
+    calls through ctypes."""
     import importlib.util
 
     spec = importlib.util.find_spec("torch")  # found, not imported

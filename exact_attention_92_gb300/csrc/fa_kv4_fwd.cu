@@ -50,9 +50,8 @@
 // falls below 2^-14 of that loses relative, not absolute, precision.  A weight is
 // 2^((x - ref) - log2(scale)) of the same rounded x = s + log2(scale) that moves
 // the reference, so it keeps that bound where fp32 holds scores in steps of 4 and
-// more.  The sum
-// of p is fp32.  The scale is taken at 2^-80 at least: p stays below 2^94, and
-// the sum over the 2^30 positions that a table may have below 2^124.
+// more.  The sum of p is fp32.  The scale is taken at 2^-80 at least: p stays below
+// 2^94, and the sum over the 2^30 positions that a table may have below 2^124.
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -451,7 +450,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
     ++taken;
 
     uint32_t q[PACK ? 2 : NR][NG][4];  // as the column operand (PACK: for each block, in its half of the columns)
-    float2 cc[NR];          // what takes the power of two out of the sums of columns 2 t, 2 t + 1, and puts the scale's in
+    float2 cc[NR];          // powers of two that columns 2 t, 2 t + 1 lack: their rows' and the scale's
     int low = len;          // keys that all rows see
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -528,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, PACK>::kThreads, 1) kv4_fwd_kernel(
       // blocks, the query rows once in its columns 0-3 for block 0 and once in
       // 4-7 for block 1, so that a lane has scores of one block only.
       constexpr int NS = PACK ? 1 : C::kBlocks;
-      float2 sc[NS][NR][2];  // keys g, g + 8: q k, scaled but for `rest`, then base-2 score + log2(largest scale of the value), then p
+      float2 sc[NS][NR][2];  // keys g, g + 8: scores but for the factor `rest`, then base-2 ones + vl, then weights
       float vl[NS][2];       // log2(largest scale of the value)
       float top[NR][2];
       const float2 rest = make_float2(p.scale_rest, p.scale_rest);
