@@ -40,6 +40,8 @@ from ._binding import (  # noqa: F401
     fa_kv4_read,
     fa_kv4_write,
     fa_poll_status,
+    fa_rope,
+    fa_rope_phases,
     fa_selftest_kv4_timeout,
     fa_selftest_wait_timeout,
     fa_set_wait_timeout_ns,
@@ -52,6 +54,9 @@ from ._binding import (  # noqa: F401
     kv4_cache,
     kv4_forward,
     load,
+    rope,
+    rope_frequencies,
+    rope_phases,
 )
 
 FA_KERNEL_FWD = 0
@@ -63,3 +68,4 @@ FA_KERNEL_KV4_WRITE = 8
 FA_KERNEL_KV4_READ = 9
 FA_KERNEL_KV4_FWD = 10
 FA_KERNEL_KV4_MERGE = 11
+FA_KERNEL_ROPE = 16

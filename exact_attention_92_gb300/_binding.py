@@ -97,6 +97,15 @@ class Kv4Plan(ctypes.Structure):
                                   "launches")] + [("workspace_bytes", _u64)]
 
 
+class Rows(ctypes.Structure):
+    """fa_rows_t (include/fa.h)."""
+    _fields_ = [("ptr", _vp), ("batch_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+_rows = ctypes.POINTER(Rows)
+_SIGNATURES["fa_rope"] = ([_rows] * 4 + [_vp] * 3 + [_i] * 7 + [_f, _i, _vp], _i)
+_SIGNATURES["fa_rope_phases"] = ([ctypes.POINTER(ctypes.c_double), _i, ctypes.POINTER(_u64)], _i)
 _SIGNATURES["fa_kv4_fwd_plan"] = ([_i] * 8 + [ctypes.POINTER(Kv4Plan)], _i)
 _SIGNATURES["fa_fwd_plan"] = ([_i] * 9 + [_u64, ctypes.POINTER(FwdPlan)], _i)
 _SIGNATURES["fa_bwd_plan"] = ([_i] * 8 + [ctypes.POINTER(BwdPlan)], _i)
@@ -534,6 +543,106 @@ def _kv4_refuse_fwd(what, status, q, cache, block_table, lens, o, lse):
                 _device_and_stream(0)[0], None, d)
 
 
+# ------------------------------------------------------- rows with strides
+
+def _check_rows(name, t, shape, write=False):
+    """A bf16 tensor [tokens, heads, d] or [B, heads, N, d] on the current
+    device, of any strides that fa_rows_t can say."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if any(n > _INT_MAX for n in t.shape):
+        raise ValueError(f"{name} has a size beyond 2^31 - 1: {tuple(t.shape)}")
+    strides = [s for s, n in zip(t.stride()[:-1], t.shape) if n > 1]
+    if (t.shape[-1] > 1 and t.stride(-1) != 1) or any(s % 8 for s in strides):
+        raise ValueError(f"{name} must have contiguous channels and other strides that are multiples of 8, "
+                         f"got {t.stride()}")
+    if write:
+        # Rows of an output do not overlap: each stride spans what the smaller ones reach.
+        reach = t.shape[-1]
+        for s, n in sorted((s, n) for s, n in zip(t.stride()[:-1], t.shape) if n > 1):
+            if s < reach:
+                raise ValueError(f"{name} is written and its rows overlap: strides {t.stride()}")
+            reach += s * (n - 1)
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current CUDA device is "
+                         f"cuda:{torch.cuda.current_device()} (use torch.cuda.device)")
+
+
+def _rows_of(t):
+    """fa_rows_t of a checked tensor; strides that nothing steps by count 0."""
+    st = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
+    if t.dim() == 3:  # [tokens, heads, d]
+        return Rows(t.data_ptr(), 0, st[0], st[1])
+    return Rows(t.data_ptr(), st[0], st[2], st[1])  # [B, heads, N, d]
+
+
+def _check_array(name, t, dtype, shape):
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device (use torch.cuda.device)")
+
+
+def fa_rope_phases(inv_freq):
+    """C fa_rope_phases: frequencies (radians a position, a sequence of
+    floats) as 64-bit fractions of a turn, a list of ints below 2^64."""
+    freq = [float(f) for f in inv_freq]
+    n = len(freq)
+    out = (_u64 * max(1, n))()
+    _check(load().fa_rope_phases((ctypes.c_double * max(1, n))(*freq), n, out), "fa_rope_phases")
+    return list(out)
+
+
+def fa_rope(q, k, q_out, k_out, phases, positions=None, start=None, interleaved=False, mscale=1.0, inverse=False,
+            stream=None):
+    """C fa_rope: q [B, H, N, d] and k [B, Hkv, N, d] (or packed, q [tokens, H,
+    d] and k [tokens, Hkv, d]) turned by their positions into q_out, k_out;
+    any strides with contiguous channels.  phases int64 [rot / 2] from
+    rope_phases; positions int32 [B, N] ([tokens]) or start int32 [B] ([1]).
+    k and k_out may be None; inverse=True turns gradients back."""
+    import torch
+
+    dims = getattr(q, "dim", lambda: 4)()
+    _check_rows("q", q, (None,) * (3 if dims == 3 else 4))
+    if dims == 3:
+        (N, H, d), B = q.shape, 1
+        shape, k_shape, at = (N,), (N, None, d), (N, H, d)
+    else:
+        B, H, N, d = q.shape
+        shape, k_shape, at = (B, N), (B, None, N, d), (B, H, N, d)
+    _check_rows("q_out", q_out, at, write=True)
+    Hkv = 0
+    if k is not None:
+        _check_rows("k", k, k_shape)
+        Hkv = k.shape[1]
+        _check_rows("k_out", k_out, tuple(k.shape), write=True)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _check_array("phases", phases, torch.int64, (getattr(phases, "shape", (0,))[0] if getattr(phases, "ndim", 0) else 0,))
+    if positions is not None:
+        _check_array("positions", positions, torch.int32, shape)
+    if start is not None:
+        _check_array("start", start, torch.int32, (B,))
+    rows = [None if t is None else _rows_of(t) for t in (q, k, q_out, k_out)]
+    st = load().fa_rope(*(None if r is None else ctypes.byref(r) for r in rows), _ptr(phases),
+                        *(None if t is None else _ptr(t) for t in (positions, start)), B, N, H, Hkv, d,
+                        2 * phases.shape[0], 1 if interleaved else 0, float(mscale), 1 if inverse else 0,
+                        _stream_ptr(stream, q.device))
+    _check(st, "fa_rope")
+
+
 def fa_poll_status(stream=None):
     """C fa_poll_status: synchronise the stream, return and clear the device status."""
     import torch
@@ -678,3 +787,56 @@ def kv4_forward(q, cache, block_table, lens, causal=False, scale=None):
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     fa_kv4_fwd(q, cache, block_table, lens, o, lse, causal, scale)
     return o, lse
+
+
+def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=None, slow=1.0, fast=32.0):
+    """Frequencies of rotary positions, radians a position: rot/2 floats
+    base^(-2j/rot), scaled for contexts `factor` times as long as in training:
+      None         not scaled
+      "linear"     every one divided by factor
+      "base"       base times factor^(rot / (rot - 2)): the slowest divided by
+                   factor, the fastest kept
+      "by_parts"   those that turn less than `slow` times over the `original`
+                   positions divided by factor, above `fast` times kept, between
+                   these a mixture in proportion to the turns
+    (some models also scale what is turned: fa_rope's mscale)."""
+    rot, base, factor = int(rot), float(base), float(factor)
+    if rot < 2 or rot % 2 or not base > 0 or not factor > 0:
+        raise ValueError(f"rope_frequencies: rot {rot}, base {base}, factor {factor}")
+    if scaling not in (None, "linear", "base", "by_parts"):
+        raise ValueError(f"scaling must be None, 'linear', 'base' or 'by_parts', got {scaling!r}")
+    if scaling == "base":
+        if rot == 2:
+            raise ValueError("scaling 'base' needs two frequencies at least")
+        base *= factor ** (rot / (rot - 2))
+    freq = [base ** (-2.0 * j / rot) for j in range(rot // 2)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "by_parts":
+        if original is None or not float(original) > 0 or not slow < fast:
+            raise ValueError("scaling 'by_parts' needs the original length, and slow < fast")
+        for j, f in enumerate(freq):
+            keep = min(1.0, max(0.0, (original * f / (2 * math.pi) - slow) / (fast - slow)))
+            freq[j] = f * keep + f / factor * (1.0 - keep)
+    return freq
+
+
+def rope_phases(frequencies, device="cuda"):
+    """fa_rope's `phases` for these frequencies (a sequence or tensor of
+    floats): int64 [rot / 2] on the device."""
+    import torch
+
+    if isinstance(frequencies, torch.Tensor):
+        frequencies = frequencies.double().cpu().tolist()
+    signed = [p - (1 << 64) if p >> 63 else p for p in fa_rope_phases(frequencies)]
+    return torch.tensor(signed, dtype=torch.int64, device=device)
+
+
+def rope(q, k, phases, positions=None, start=None, interleaved=False, mscale=1.0, inverse=False):
+    """Allocate the outputs and run fa_rope; returns (q, k) turned (k may be None)."""
+    import torch
+
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    fa_rope(q, k, q_out, k_out, phases, positions, start, interleaved, mscale, inverse)
+    return q_out, k_out

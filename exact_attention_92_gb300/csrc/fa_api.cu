@@ -417,10 +417,11 @@ struct TimingRec {
 std::mutex g_tmu;
 bool g_timing = false;
 // Launches of each library kernel since the library was loaded (always on).
-std::atomic<unsigned long long> g_launches[FA_KERNEL_KV4_MERGE + 1];
+std::atomic<unsigned long long> g_launches[FA_KERNEL_ROPE + 1];
 
 bool kernel_id(int k) {
-  return (k >= FA_KERNEL_FWD && k <= FA_KERNEL_BWD_DQ) || (k >= FA_KERNEL_KV4_WRITE && k <= FA_KERNEL_KV4_MERGE);
+  return (k >= FA_KERNEL_FWD && k <= FA_KERNEL_BWD_DQ) || (k >= FA_KERNEL_KV4_WRITE && k <= FA_KERNEL_KV4_MERGE) ||
+         k == FA_KERNEL_ROPE;
 }
 
 std::vector<TimingRec> g_recs;

@@ -441,6 +441,56 @@ int fa_kv4_fwd_plan(int B, int H, int Hkv, int Nq, int d, int page_size, int max
                     fa_kv4_plan_t* plan);
 
 /*
+ * Rows of d channels with strides, for the calls below: the row at token i of
+ * head h (of batch b in fa_rope) is at ptr + (b * batch_stride + i * row_stride
+ * + h * head_stride) elements, its channels contiguous.  So tensors [tokens,
+ * heads, d], [heads, tokens, d] and slices of a fused projection's output are
+ * taken as they lie.  ptr must be 16-byte aligned, strides multiples of 8.
+ */
+typedef struct {
+  void* ptr;
+  int64_t batch_stride; /* fa_rope only */
+  int64_t row_stride;
+  int64_t head_stride;
+} fa_rows_t;
+
+/*
+ * Rotary positions: channel pairs of queries and keys turned by an angle that
+ * grows with the position, as models with rotary embeddings do before
+ * attention (the pages have no counterpart).  Pair j < rot/2 of a row at
+ * position t, with theta = t * inv_freq[j]:
+ *   (a, b) -> mscale * (a cos theta - b sin theta, b cos theta + a sin theta)
+ *   q, k         : in, bf16 rows of H and Hkv heads; k may be null (and then
+ *                  k_out and Hkv are not looked at)
+ *   q_out, k_out : out; the same memory with the same strides as q, k, or
+ *                  memory that overlaps no input
+ *   phases       : device, uint64 [rot/2] from fa_rope_phases (8-byte aligned)
+ *   positions    : device, int32 [B,N] (contiguous), or null
+ *   start        : device, int32 [B], or null: without positions, token i of
+ *                  batch b is at position start[b] + i (i without start).  Not
+ *                  both.
+ *   rot          : channels turned, even, 2 <= rot <= d; channels from rot on
+ *                  are passed through
+ *   interleaved  : 0: pair j is channels (j, j + rot/2); else (2j, 2j + 1)
+ *   mscale       : finite; 1 but for frequencies scaled to long contexts in a
+ *                  way that asks for another
+ *   inverse      : nonzero turns by -theta: the gradients of q and k from those
+ *                  of q_out and k_out
+ * B * N <= 2^31 - 1; d as elsewhere.  Angles are exact to 2^-24 of a half turn at
+ * any position; products are fp32, rounded once.
+ */
+int fa_rope(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* q_out, const fa_rows_t* k_out,
+            const uint64_t* phases, const int* positions, const int* start, int B, int N, int H, int Hkv, int d, int rot,
+            int interleaved, float mscale, int inverse, void* stream);
+
+/*
+ * Frequencies (radians a position, finite) as the fraction of a turn a
+ * position in 64-bit fixed point, phases[j] = inv_freq[j] / (2 pi) * 2^64 modulo
+ * 2^64.  Host memory on both sides.
+ */
+int fa_rope_phases(const double* inv_freq, int n, uint64_t* phases);
+
+/*
  * Synchronise `stream`, then return and clear the device status of the
  * current device: FA_OK, FA_ERR_TIMEOUT if a kernel's bounded wait gave up
  * since the last poll, FA_ERR_BAD_INDEX if a fa_kv4_* kernel skipped an index
@@ -503,6 +553,8 @@ int fa_selftest_kv4_timeout(const void* q, const void* cache, const int* block_t
 #define FA_KERNEL_KV4_READ 9
 #define FA_KERNEL_KV4_FWD 10
 #define FA_KERNEL_KV4_MERGE 11
+/* Rotary positions (12 to 15 are not ids). */
+#define FA_KERNEL_ROPE 16
 int fa_timing_enable(int on);
 int fa_timing_read(int kernel, int* launches, double* total_ms);
 
