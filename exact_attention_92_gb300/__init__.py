@@ -39,7 +39,9 @@ from ._binding import (  # noqa: F401
     fa_kv4_fwd_plan,
     fa_kv4_read,
     fa_kv4_write,
+    fa_packed_fwd,
     fa_poll_status,
+    fa_prefix_fwd,
     fa_rope,
     fa_rope_phases,
     fa_selftest_kv4_timeout,
@@ -54,6 +56,8 @@ from ._binding import (  # noqa: F401
     kv4_cache,
     kv4_forward,
     load,
+    packed_forward,
+    prefix_forward,
     rope,
     rope_frequencies,
     rope_phases,
@@ -69,3 +73,6 @@ FA_KERNEL_KV4_READ = 9
 FA_KERNEL_KV4_FWD = 10
 FA_KERNEL_KV4_MERGE = 11
 FA_KERNEL_ROPE = 16
+FA_KERNEL_PACKED_PLAN = 17
+FA_KERNEL_PACKED_FWD = 18
+FA_KERNEL_PACKED_MERGE = 19

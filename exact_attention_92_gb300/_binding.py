@@ -106,6 +106,8 @@ class Rows(ctypes.Structure):
 _rows = ctypes.POINTER(Rows)
 _SIGNATURES["fa_rope"] = ([_rows] * 4 + [_vp] * 3 + [_i] * 7 + [_f, _i, _vp], _i)
 _SIGNATURES["fa_rope_phases"] = ([ctypes.POINTER(ctypes.c_double), _i, ctypes.POINTER(_u64)], _i)
+_SIGNATURES["fa_packed_fwd"] = ([_rows] * 4 + [_vp] * 4 + [_i] * 7 + [_f, _vp], _i)
+_SIGNATURES["fa_prefix_fwd"] = ([_rows] * 6 + [_vp] * 4 + [_i] * 8 + [_f, _vp], _i)
 _SIGNATURES["fa_kv4_fwd_plan"] = ([_i] * 8 + [ctypes.POINTER(Kv4Plan)], _i)
 _SIGNATURES["fa_fwd_plan"] = ([_i] * 9 + [_u64, ctypes.POINTER(FwdPlan)], _i)
 _SIGNATURES["fa_bwd_plan"] = ([_i] * 8 + [ctypes.POINTER(BwdPlan)], _i)
@@ -643,6 +645,50 @@ def fa_rope(q, k, q_out, k_out, phases, positions=None, start=None, interleaved=
     _check(st, "fa_rope")
 
 
+def _packed_fwd(what, q, prefix, k, v, o, lse, cu_q, cu_k, used_k, causal, scale, stream):
+    import torch
+
+    _check_rows("q", q, (None, None, None))
+    Tq, H, d = q.shape
+    _check_rows("k", k, (None, None, d))
+    Tk, Hkv, _ = k.shape
+    _check_rows("v", v, (Tk, Hkv, d))
+    _check_rows("o", o, (Tq, H, d), write=True)
+    _check_array("lse", lse, torch.float32, (H, Tq))
+    B = (cu_q.shape[0] if isinstance(cu_q, torch.Tensor) and cu_q.ndim == 1 else 0) - 1
+    if B < 1:
+        raise ValueError("cu_q must be an int32 CUDA tensor [B + 1] with B >= 1")
+    _check_array("cu_q", cu_q, torch.int32, (B + 1,))
+    _check_array("cu_k", cu_k, torch.int32, (B + 1,))
+    if used_k is not None:
+        _check_array("used_k", used_k, torch.int32, (B,))
+    tensors, P = [q, k, v, o], ()
+    if prefix is not None:
+        _check_rows("k_prefix", prefix[0], (None, Hkv, d))
+        _check_rows("v_prefix", prefix[1], tuple(prefix[0].shape))
+        tensors[1:1] = prefix
+        P = (prefix[0].shape[0],)
+    rows = [ctypes.byref(_rows_of(t)) for t in tensors]
+    st = getattr(load(), what)(*rows, _ptr(lse), _ptr(cu_q), _ptr(cu_k), None if used_k is None else _ptr(used_k), B,
+                               *P, Tq, Tk, H, Hkv, d, _causal_code(causal), _scale(scale, d),
+                               _stream_ptr(stream, q.device))
+    _check(st, what)
+
+
+def fa_packed_fwd(q, k, v, o, lse, cu_q, cu_k, used_k=None, causal=False, scale=None, stream=None):
+    """C fa_packed_fwd: attention over packed sequences, q, o [Tq, H, d] and
+    k, v [Tk, Hkv, d] of any strides with contiguous channels, lse fp32 [H,
+    Tq]; cu_q, cu_k int32 [B + 1], used_k int32 [B] or None; causal as
+    fa_fwd_general, within each sequence."""
+    _packed_fwd("fa_packed_fwd", q, None, k, v, o, lse, cu_q, cu_k, used_k, causal, scale, stream)
+
+
+def fa_prefix_fwd(q, k_prefix, v_prefix, k, v, o, lse, cu_q, cu_k, used_k=None, causal=False, scale=None, stream=None):
+    """C fa_prefix_fwd: fa_packed_fwd where every query row also sees all of
+    k_prefix, v_prefix [P, Hkv, d]."""
+    _packed_fwd("fa_prefix_fwd", q, (k_prefix, v_prefix), k, v, o, lse, cu_q, cu_k, used_k, causal, scale, stream)
+
+
 def fa_poll_status(stream=None):
     """C fa_poll_status: synchronise the stream, return and clear the device status."""
     import torch
@@ -840,3 +886,24 @@ def rope(q, k, phases, positions=None, start=None, interleaved=False, mscale=1.0
     k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
     fa_rope(q, k, q_out, k_out, phases, positions, start, interleaved, mscale, inverse)
     return q_out, k_out
+
+
+def packed_forward(q, k, v, cu_q, cu_k=None, used_k=None, causal=False, scale=None):
+    """Allocate O and LSE and run fa_packed_fwd; returns (o, lse).  cu_k
+    defaults to cu_q.  Rows of no sequence are 0 (and -inf in lse)."""
+    import torch
+
+    o = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.full((q.shape[1], q.shape[0]), -math.inf, dtype=torch.float32, device=q.device)
+    fa_packed_fwd(q, k, v, o, lse, cu_q, cu_q if cu_k is None else cu_k, used_k, causal, scale)
+    return o, lse
+
+
+def prefix_forward(q, k_prefix, v_prefix, k, v, cu_q, cu_k=None, used_k=None, causal=False, scale=None):
+    """Allocate O and LSE and run fa_prefix_fwd; returns (o, lse) as packed_forward."""
+    import torch
+
+    o = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.full((q.shape[1], q.shape[0]), -math.inf, dtype=torch.float32, device=q.device)
+    fa_prefix_fwd(q, k_prefix, v_prefix, k, v, o, lse, cu_q, cu_q if cu_k is None else cu_k, used_k, causal, scale)
+    return o, lse

@@ -28,7 +28,7 @@ CALL_SOURCE = os.path.join(CSRC, "kv4_call.cpp")
 CALL = os.path.join(PKG, "_kv4_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd256.cu", "fa_bwd.cu", "fa_bwd_pair.cu", "fa_bwd256.cu", "fa_noalloc.cu",
-           "fa_kv4.cu", "fa_kv4_move.cu", "fa_kv4_fwd.cu", "fa_rope.cu"]
+           "fa_kv4.cu", "fa_kv4_move.cu", "fa_kv4_fwd.cu", "fa_rope.cu", "fa_packed.cu", "fa_packed_fwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -52,7 +52,7 @@ def _deps():
 # Kernels that read tensor memory with tcgen05.ld: the destination registers
 # of such a load are only valid after tcgen05.wait::ld, so a register spill
 # between the two would store garbage.  The build refuses any spill in them.
-NO_SPILL_KERNELS = ("fa_fwd_kernel", "fa_fwd256_kernel", "fa_bwd_dkdv_kernel", "fa_bwd_dkdv_pair_kernel",
+NO_SPILL_KERNELS = ("fa_fwd_kernel", "fa_packed_fwd_kernel", "fa_fwd256_kernel", "fa_bwd_dkdv_kernel", "fa_bwd_dkdv_pair_kernel",
                     "fa_bwd_dq_kernel", "fa_bwd256_kv_kernel", "fa_bwd256_dq_kernel")
 
 
@@ -61,7 +61,7 @@ NO_SPILL_KERNELS = ("fa_fwd_kernel", "fa_fwd256_kernel", "fa_bwd_dkdv_kernel", "
 # static_asserted against this count in the source; if ptxas gave the entry
 # fewer registers, the warpgroup that asks for more would wait forever.
 REG_SPLIT_KERNELS = {"fa_fwd_kernel": 168, "fa_bwd_dkdv_kernel": 168, "fa_bwd_dkdv_pair_kernel": 168,
-                     "fa_bwd_dq_kernel": 168}
+                     "fa_bwd_dq_kernel": 168, "fa_packed_fwd_kernel": 168}
 
 
 def check_spills(ptxas_log: str) -> None:

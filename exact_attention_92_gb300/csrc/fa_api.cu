@@ -417,11 +417,11 @@ struct TimingRec {
 std::mutex g_tmu;
 bool g_timing = false;
 // Launches of each library kernel since the library was loaded (always on).
-std::atomic<unsigned long long> g_launches[FA_KERNEL_ROPE + 1];
+std::atomic<unsigned long long> g_launches[FA_KERNEL_PACKED_MERGE + 1];
 
 bool kernel_id(int k) {
   return (k >= FA_KERNEL_FWD && k <= FA_KERNEL_BWD_DQ) || (k >= FA_KERNEL_KV4_WRITE && k <= FA_KERNEL_KV4_MERGE) ||
-         k == FA_KERNEL_ROPE;
+         (k >= FA_KERNEL_ROPE && k <= FA_KERNEL_PACKED_MERGE);
 }
 
 std::vector<TimingRec> g_recs;
@@ -476,6 +476,22 @@ int internal_device_setup(unsigned int** status, int* sm_count) {
 int internal_validate(int B, int H, int N, int d, float scale) { return validate(B, H, N, N, d, scale, true); }
 int internal_encode_bhnd(CUtensorMap* m, const void* ptr, int BH, int N, int d, int box_rows) {
   return encode_bhnd(m, ptr, BH, N, d, box_rows);
+}
+// bf16, 128-byte swizzle, zeros outside; sizes and strides (bytes) innermost first.
+int internal_encode_tiled(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
+                          const uint32_t* box) {
+  cuuint64_t d[5], s[5];
+  cuuint32_t b[5], one[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    one[i] = 1;
+    if (i + 1 < rank) s[i] = strides[i];
+  }
+  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), d, s, b, one,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 // Workspace from the library's pool on the current device (set up before).
 cudaError_t internal_workspace(void** ptr, size_t bytes, cudaStream_t st) {

@@ -1,0 +1,104 @@
+// Attention over packed sequences: what the planning kernel, the forward kernel
+// and the merge share.
+//
+// Rows.  Queries are taken in tiles of 128 rows that hold `tile_tokens` tokens
+// of `group_heads` query heads of one key/value head (row = token * group_heads
+// + head), so that K and V are read once for all of these; a block is two tiles.
+// A head group is a (key/value head, run of group_heads of its query heads).
+//
+// Units.  An entry is a block of query tokens with the keys it takes (the shared
+// prefix's, then the sequence's own), a unit is an entry for one head group; all
+// units, head group by head group, make one list of 128-key tiles, each unit
+// followed by kUnitTiles places for its start and end.  Every CTA takes an equal
+// stretch of that list: it depends on nothing but the lengths, so results are
+// the same from run to run.  What a cut leaves in parts is written as fp32
+// partial results, two slots a CTA, and merged.
+//
+// Sequence ends.  A tile of a sequence's last keys must read as zeros where it
+// has no keys: the rows there are another sequence's, or memory of no sequence,
+// and may hold NaN, which a weight of 0 does not silence.  Tensor maps check
+// coordinates, not sequences, so the row is given by two coordinates of the same
+// stride, the tile's first row and the row within the tile.  A tile with n < 128
+// keys left starts at n - 128 in the second: what lies before 0 is outside and
+// reads as zero, and the n keys take the tile's last n places.  (Clipping at the
+// other end would take a map whose base lies ahead of the tensor.  Such a map
+// faults where that address is not mapped, whatever coordinates are loaded.)
+#pragma once
+
+#include <cstdint>
+
+#include "fa_common.h"
+
+namespace fa {
+
+constexpr int kUnitTiles = 2;    // start and end of a unit, in key tiles' time
+constexpr int kSlotRows = 256;   // query rows of a block
+
+struct PackedEntry {
+  int q_row, q_len;  // first token and tokens of the block
+  int k_row, k_len;  // first key row and keys of the sequence
+  int prefix;        // tiles of the prefix, ahead of the sequence's own
+  int tiles;         // tiles in all that the block's last token sees
+  int pos;           // causal: token j of the block sees own keys < pos + j + 1
+  int kind;          // 1: block over the prefix alone (its rows get a second part)
+};
+static_assert(sizeof(PackedEntry) == 32, "read as two 16-byte words");
+
+// Where a CTA's stretch starts: unit and tile.
+struct PackedStart {
+  int unit, tile;
+};
+
+struct PackedSeqs {
+  const int* cu_q;
+  const int* cu_k;
+  const int* used_k;  // or null
+  int B, Tq, Tk;
+  int causal;         // FA_CAUSAL_*
+  unsigned int* status;
+};
+
+struct PackedPlan {
+  PackedSeqs s;
+  int tile_tokens;
+  int prefix_tiles;   // 0: no prefix
+  int shared;         // 1: the prefix has blocks of its own
+  int head_groups;
+  int grid;
+  int min_tiles;      // a cut leaves at least so many on either side
+  int whole;          // 1: no cuts
+  int* seq_base;      // [B + 1] first entry of each sequence
+  PackedEntry* entries;
+  long long* cum;     // [entries + 1] places ahead of each entry
+  PackedStart* starts;  // [grid + 1]
+  int* header;        // entries, of which over the prefix alone
+};
+
+struct PackedFwd {
+  int H, Hkv;
+  int group;          // query heads of a key/value head
+  int group_heads;    // of them in a tile
+  int chunks;         // ceil(group / group_heads)
+  int tile_tokens;
+  int Tq;
+  int prefix_len;
+  int causal;         // 0 or 1
+  int shared;
+  float scale_log2;
+  const PackedEntry* entries;
+  const PackedStart* starts;
+  const int* header;
+  int grid;
+  void* o;
+  long long o_row, o_head;  // strides in elements
+  float* lse;               // [H, Tq]
+  int store32;
+  float* o_slot;      // [2 grid][D / 4][kSlotRows][4]
+  float* lse_slot;    // [2 grid][kSlotRows]
+  float* o_part;      // shared: [2][Tq][H][D], of the prefix and of the own keys
+  float* lse_part;    // shared: [2][H][Tq]
+  unsigned int* status;
+  unsigned long long timeout_ns;
+};
+
+}  // namespace fa

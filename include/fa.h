@@ -491,6 +491,58 @@ int fa_rope(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* q_out, cons
 int fa_rope_phases(const double* inv_freq, int n, uint64_t* phases);
 
 /*
+ * Attention over packed sequences: sequences of different lengths lie one
+ * behind the other without padding, sequence b with the query rows cu_q[b] to
+ * cu_q[b+1] and the key rows cu_k[b] to cu_k[b+1].  Its queries see its own keys
+ * only: the computation of fa_fwd_general for each sequence with Nq and Nk its
+ * lengths ("FlashAttention V2 in depth", section 6.1).
+ *   q, o    : bf16 rows of Tq tokens and H heads;  k, v : of Tk tokens, Hkv heads
+ *             (o: rows that do not overlap; a size-one axis may have any stride,
+ *             others above zero)
+ *   lse     : out, fp32 [H,Tq], contiguous
+ *   cu_q, cu_k : device, int32 [B+1], not decreasing, 0 <= cu_q[b] <= Tq and
+ *             0 <= cu_k[b] <= Tk (4-byte aligned)
+ *   used_k  : device, int32 [B], or null: of the sequence's key rows only the
+ *             first used_k[b] count (a cache with room for more);
+ *             0 <= used_k[b] <= cu_k[b+1] - cu_k[b]
+ *   causal  : FA_CAUSAL_NONE, _TOP_LEFT or _BOTTOM_RIGHT within a sequence (with
+ *             used_k, the keys that count are Nk)
+ *   Hkv     : divides H.  d: 64, 96 or 128 (FA_ERR_UNSUPPORTED otherwise)
+ *   B, Tq >= 1, Tk >= 0 (0: k and v are not looked at); all at most 2^30, and
+ *   (Tq / 256 * H/Hkv + B) * Hkv about at most 2^31 (FA_ERR_INVALID_ARG)
+ * A query row that sees no key gets O = 0, L = -inf.  Lengths of zero are taken.
+ * Rows of o and lse ahead of cu_q[0] and from cu_q[B] on are left as they were.
+ * Nothing that other sequences or the rows between and behind them hold reaches
+ * a sequence's results, NaN included; within a sequence a NaN or an infinity in v
+ * reaches every row, those that the mask hides it from too where they share a
+ * tile of 128 keys with one that sees it, as in the other calls.
+ * The arrays are read on the device: a sequence whose bounds are out of order or
+ * out of range is skipped and FA_ERR_BAD_INDEX recorded (fa_poll_status).  They
+ * must not be written while the call reads them.  The call may be captured into
+ * a CUDA graph, but not as the first call of the library on a device; replays go
+ * by the lengths of their time.  Its kernels are launched with programmatic
+ * stream serialization like those of the backward.  Results are the same from run to
+ * run for the same lengths.
+ */
+int fa_packed_fwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, const fa_rows_t* o, float* lse,
+                  const int* cu_q, const int* cu_k, const int* used_k, int B, int Tq, int Tk, int H, int Hkv, int d,
+                  int causal, float scale, void* stream);
+
+/*
+ * fa_packed_fwd where all sequences share P keys ahead of their own (a common
+ * prompt): every query row sees all of k_prefix, v_prefix [P tokens, Hkv heads],
+ * and its sequence's own keys as in fa_packed_fwd (`causal` is about these).  The
+ * prefix is not walked sequence by sequence where that would take longer: query
+ * rows of many sequences share its tiles, and the two parts of each row are
+ * merged, O = sum exp(L_s - L) O_s, L = log sum exp(L_s).
+ * P >= 1; other arguments as fa_packed_fwd.
+ */
+int fa_prefix_fwd(const fa_rows_t* q, const fa_rows_t* k_prefix, const fa_rows_t* v_prefix, const fa_rows_t* k,
+                  const fa_rows_t* v, const fa_rows_t* o, float* lse, const int* cu_q, const int* cu_k,
+                  const int* used_k, int B, int P, int Tq, int Tk, int H, int Hkv, int d, int causal, float scale,
+                  void* stream);
+
+/*
  * Synchronise `stream`, then return and clear the device status of the
  * current device: FA_OK, FA_ERR_TIMEOUT if a kernel's bounded wait gave up
  * since the last poll, FA_ERR_BAD_INDEX if a fa_kv4_* kernel skipped an index
@@ -553,8 +605,11 @@ int fa_selftest_kv4_timeout(const void* q, const void* cache, const int* block_t
 #define FA_KERNEL_KV4_READ 9
 #define FA_KERNEL_KV4_FWD 10
 #define FA_KERNEL_KV4_MERGE 11
-/* Rotary positions (12 to 15 are not ids). */
+/* Rotary positions and packed sequences (12 to 15 are not ids). */
 #define FA_KERNEL_ROPE 16
+#define FA_KERNEL_PACKED_PLAN 17
+#define FA_KERNEL_PACKED_FWD 18
+#define FA_KERNEL_PACKED_MERGE 19
 int fa_timing_enable(int on);
 int fa_timing_read(int kernel, int* launches, double* total_ms);
 
