@@ -39,6 +39,7 @@ from ._binding import (  # noqa: F401
     fa_kv4_fwd_plan,
     fa_kv4_read,
     fa_kv4_write,
+    fa_packed_bwd,
     fa_packed_fwd,
     fa_poll_status,
     fa_prefix_fwd,
@@ -56,6 +57,7 @@ from ._binding import (  # noqa: F401
     kv4_cache,
     kv4_forward,
     load,
+    packed_backward,
     packed_forward,
     prefix_forward,
     rope,

@@ -107,6 +107,7 @@ _rows = ctypes.POINTER(Rows)
 _SIGNATURES["fa_rope"] = ([_rows] * 4 + [_vp] * 3 + [_i] * 7 + [_f, _i, _vp], _i)
 _SIGNATURES["fa_rope_phases"] = ([ctypes.POINTER(ctypes.c_double), _i, ctypes.POINTER(_u64)], _i)
 _SIGNATURES["fa_packed_fwd"] = ([_rows] * 4 + [_vp] * 4 + [_i] * 7 + [_f, _vp], _i)
+_SIGNATURES["fa_packed_bwd"] = ([_rows] * 4 + [_vp] + [_rows] * 4 + [_vp] * 2 + [_i] * 7 + [_f, _vp], _i)
 _SIGNATURES["fa_prefix_fwd"] = ([_rows] * 6 + [_vp] * 4 + [_i] * 8 + [_f, _vp], _i)
 _SIGNATURES["fa_kv4_fwd_plan"] = ([_i] * 8 + [ctypes.POINTER(Kv4Plan)], _i)
 _SIGNATURES["fa_fwd_plan"] = ([_i] * 9 + [_u64, ctypes.POINTER(FwdPlan)], _i)
@@ -683,6 +684,31 @@ def fa_packed_fwd(q, k, v, o, lse, cu_q, cu_k, used_k=None, causal=False, scale=
     _packed_fwd("fa_packed_fwd", q, None, k, v, o, lse, cu_q, cu_k, used_k, causal, scale, stream)
 
 
+def fa_packed_bwd(q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, causal=False, scale=None, stream=None):
+    """C fa_packed_bwd: gradients of fa_packed_fwd (without used_k); dout, dq
+    have the shape of q, dk, dv that of k."""
+    import torch
+
+    _check_rows("q", q, (None, None, None))
+    Tq, H, d = q.shape
+    _check_rows("k", k, (None, None, d))
+    Tk, Hkv, _ = k.shape
+    for name, t in (("v", v), ("dk", dk), ("dv", dv)):
+        _check_rows(name, t, (Tk, Hkv, d), write=name != "v")
+    for name, t in (("o", o), ("dout", dout), ("dq", dq)):
+        _check_rows(name, t, (Tq, H, d), write=name == "dq")
+    _check_array("lse", lse, torch.float32, (H, Tq))
+    B = (cu_q.shape[0] if isinstance(cu_q, torch.Tensor) and cu_q.ndim == 1 else 0) - 1
+    if B < 1:
+        raise ValueError("cu_q must be an int32 CUDA tensor [B + 1] with B >= 1")
+    _check_array("cu_q", cu_q, torch.int32, (B + 1,))
+    _check_array("cu_k", cu_k, torch.int32, (B + 1,))
+    rows = [ctypes.byref(_rows_of(t)) for t in (q, k, v, o, dout, dq, dk, dv)]
+    st = load().fa_packed_bwd(*rows[:4], _ptr(lse), *rows[4:], _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, H, Hkv, d,
+                              _causal_code(causal), _scale(scale, d), _stream_ptr(stream, q.device))
+    _check(st, "fa_packed_bwd")
+
+
 def fa_prefix_fwd(q, k_prefix, v_prefix, k, v, o, lse, cu_q, cu_k, used_k=None, causal=False, scale=None, stream=None):
     """C fa_prefix_fwd: fa_packed_fwd where every query row also sees all of
     k_prefix, v_prefix [P, Hkv, d]."""
@@ -897,6 +923,16 @@ def packed_forward(q, k, v, cu_q, cu_k=None, used_k=None, causal=False, scale=No
     lse = torch.full((q.shape[1], q.shape[0]), -math.inf, dtype=torch.float32, device=q.device)
     fa_packed_fwd(q, k, v, o, lse, cu_q, cu_q if cu_k is None else cu_k, used_k, causal, scale)
     return o, lse
+
+
+def packed_backward(q, k, v, o, lse, dout, cu_q, cu_k=None, causal=False, scale=None):
+    """Allocate dQ, dK, dV and run fa_packed_bwd; returns (dq, dk, dv).  Rows
+    of no sequence are 0."""
+    import torch
+
+    dq, dk, dv = (torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+    fa_packed_bwd(q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_q if cu_k is None else cu_k, causal, scale)
+    return dq, dk, dv
 
 
 def prefix_forward(q, k_prefix, v_prefix, k, v, cu_q, cu_k=None, used_k=None, causal=False, scale=None):

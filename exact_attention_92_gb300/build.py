@@ -28,7 +28,8 @@ CALL_SOURCE = os.path.join(CSRC, "kv4_call.cpp")
 CALL = os.path.join(PKG, "_kv4_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd256.cu", "fa_bwd.cu", "fa_bwd_pair.cu", "fa_bwd256.cu", "fa_noalloc.cu",
-           "fa_kv4.cu", "fa_kv4_move.cu", "fa_kv4_fwd.cu", "fa_rope.cu", "fa_packed.cu", "fa_packed_fwd.cu"]
+           "fa_kv4.cu", "fa_kv4_move.cu", "fa_kv4_fwd.cu", "fa_rope.cu", "fa_packed.cu", "fa_packed_fwd.cu",
+           "fa_packed_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

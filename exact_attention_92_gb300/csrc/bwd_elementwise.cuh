@@ -63,12 +63,29 @@ __device__ __forceinline__ void p64_colL(uint32_t* s, const float* bl, float sl2
   }
 }
 
+// What a unit of packed sequences has beside its tiles (nothing for tensors
+// [B, H, N, d]).
+template <bool PACKED>
+struct SeqPart {};
+template <>
+struct SeqPart<true> {
+  BwdEntry e;
+};
+
+__device__ __forceinline__ BwdEntry load_entry(const BwdEntry* e) {
+  const int4* w = reinterpret_cast<const int4*>(e);
+  const int4 a = w[0], b = w[1];
+  return BwdEntry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
 // P of 64 key columns [k_first, k_first + 64) of query row q, in place:
 // p = exp2(s * sl2 - L) with one L for the row.  MASK zeroes keys past N and,
 // with the causal mask, keys after q (the caller passes the query row plus
-// the causal offset).
-template <bool MASK>
-__device__ __forceinline__ void p64_rowL(uint32_t* s, float L, float sl2, int q, int k_first, int N, bool causal) {
+// the causal offset).  LOW also zeroes keys before `lowest` (a tile of packed
+// sequences whose keys are its last columns).
+template <bool MASK, bool LOW = false>
+__device__ __forceinline__ void p64_rowL(uint32_t* s, float L, float sl2, int q, int k_first, int N, bool causal,
+                                         int lowest = 0) {
   const float2 sv = make_float2(sl2, sl2);
   const float2 lv = make_float2(-L, -L);
 #pragma unroll
@@ -77,8 +94,8 @@ __device__ __forceinline__ void p64_rowL(uint32_t* s, float L, float sl2, int q,
     float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
     if (MASK) {
       const int k = k_first + e;
-      p0 = (k >= N || (causal && k > q)) ? 0.f : p0;
-      p1 = (k + 1 >= N || (causal && k + 1 > q)) ? 0.f : p1;
+      p0 = (k >= N || (causal && k > q) || (LOW && k < lowest)) ? 0.f : p0;
+      p1 = (k + 1 >= N || (causal && k + 1 > q) || (LOW && k + 1 < lowest)) ? 0.f : p1;
     }
     s[e] = __float_as_uint(p0);
     s[e + 1] = __float_as_uint(p1);

@@ -61,11 +61,13 @@ using namespace dev;
 
 // Register split shared by both kernels: 168 per thread at launch (three
 // warps per SM sub-partition); warpgroup 2 keeps kRegsCtl, the element-wise
-// warpgroups get kRegsMath.
+// warpgroups get kRegsMath.  WIDE: the issuer of the packed units at d = 96 does
+// not fit 72, the element-wise warps fit 208.
+template <bool WIDE>
 struct BwdRegs {
   static constexpr int kRegsAtLaunch = 168;
-  static constexpr int kRegsCtl = 72;
-  static constexpr int kRegsMath = 216;
+  static constexpr int kRegsCtl = WIDE ? 88 : 72;
+  static constexpr int kRegsMath = WIDE ? 208 : 216;
   static_assert(128 * kRegsCtl + 256 * kRegsMath <= 384 * kRegsAtLaunch, "register split exceeds the launch");
 };
 
@@ -107,7 +109,8 @@ struct DkdvCfg {
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
-struct BwdUnit {
+template <bool PACKED>
+struct BwdUnit : SeqPart<PACKED> {
   int bh;     // the head: key/value head (dK/dV kernel), query head (dQ kernel)
   int t;      // the tile this CTA owns (key tile / query tile)
   int first;  // first tile of the other operand
@@ -121,8 +124,18 @@ struct BwdUnit {
 // A dK/dV unit is one key/value tile of one key/value head; its steps walk
 // the visible query tiles of every query head that reads that key/value head
 // (one head, for plain multi-head attention), so dK and dV sum over them.
-__device__ __forceinline__ BwdUnit decode_dkdv(const BwdParams& p, int u) {
-  BwdUnit w;
+template <bool PACKED>
+__device__ __forceinline__ BwdUnit<PACKED> decode_dkdv(const BwdParams& p, int u) {
+  BwdUnit<PACKED> w;
+  if constexpr (PACKED) {
+    w.e = load_entry(p.entries_kv + u / p.Hkv);
+    w.bh = u % p.Hkv;
+    w.t = w.e.tile;
+    w.first = w.e.first;
+    w.per = w.e.count;
+    w.count = w.per * p.group;
+    return w;
+  }
   const int BH = p.B * p.Hkv;
   w.bh = u % BH;
   w.t = u / BH;
@@ -137,8 +150,17 @@ __device__ __forceinline__ BwdUnit decode_dkdv(const BwdParams& p, int u) {
 
 // dQ units: with the causal mask, high query tiles see the most key tiles.
 // Units cover only query tiles [q_tile_first, num_q_tiles), which see keys.
-__device__ __forceinline__ BwdUnit decode_dq(const BwdParams& p, int u) {
-  BwdUnit w;
+template <bool PACKED>
+__device__ __forceinline__ BwdUnit<PACKED> decode_dq(const BwdParams& p, int u) {
+  BwdUnit<PACKED> w;
+  if constexpr (PACKED) {
+    w.e = load_entry(p.entries_q + u / p.H);
+    w.bh = u % p.H;
+    w.t = w.e.tile;
+    w.first = 0;
+    w.count = w.per = w.e.count;
+    return w;
+  }
   const int BH = p.B * p.H;
   w.bh = u % BH;
   w.t = p.causal ? p.num_q_tiles - 1 - u / BH : p.q_tile_first + u / BH;
@@ -155,14 +177,17 @@ __device__ __forceinline__ BwdUnit decode_dq(const BwdParams& p, int u) {
 
 // GQA: key/value heads shared by several query heads (the steps of a unit
 // then run over (query head, query tile) pairs); the multi-head instance
-// keeps the plain per-tile indexing.
-template <int D, bool GQA>
+// keeps the plain per-tile indexing.  PACKED: units of packed sequences
+// (BwdParams::entries_kv): the streamed tiles of a sequence's last rows hold zeros
+// ahead of them (see packed.h), so their first row may lie before the tile's own,
+// or before the sequence; L = +inf there makes the weights 0.
+template <int D, bool GQA, bool PACKED>
 __global__ void __launch_bounds__(384, 1)
     fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                        const BwdParams p) {
   using C = DkdvCfg<D>;
-  using R = BwdRegs;
+  using R = BwdRegs<PACKED && D == 96>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (threadIdx.x == 0) atomicCAS(p.status, 0u, (unsigned int)FA_ERR_CUDA);
@@ -234,6 +259,11 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{p.status, p.timeout_ns};
+  int n_units = p.num_units_kv;
+  if constexpr (PACKED) {
+    pdl_wait();  // the units are on the device
+    n_units = p.entry_counts[0] * p.Hkv;
+  }
 
   if (warp == 9) {
     // ------------------------------------------------------------ producer
@@ -246,16 +276,19 @@ __global__ void __launch_bounds__(384, 1)
     uint32_t kc = 0, qc = 0;
     uint32_t k_issued = 0, v_issued = 0, q_issued = 0, do_issued = 0;  // copies started (for the drain)
     bool ok = true;
-    for (int rnd = 0; ok && rnd * (int)gridDim.x < p.num_units_kv; ++rnd) {
+    for (int rnd = 0; ok && rnd * (int)gridDim.x < n_units; ++rnd) {
       const int u = snake_unit(rnd);
-      if (u >= p.num_units_kv) continue;
-      const BwdUnit w = decode_dkdv(p, u);
+      if (u >= n_units) continue;
+      const BwdUnit<PACKED> w = decode_dkdv<PACKED>(p, u);
+      if (PACKED && w.count == 0) continue;
+      int key0 = w.t * kTileN;
+      if constexpr (PACKED) key0 += w.e.k_row;
       ok = __all_sync(0xffffffffu, mbar_wait(k_empty, (kc & 1) ^ 1, ctl, kWaitBwdLoad));
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(k_full, C::kTileBytes);
         for (int c = 0; c < C::kChunks; ++c)
-          tma_load_3d(smem + C::kOffK + c * C::kChunkBytes, &tm_k, k_full, c * 64, w.t * kTileN, w.bh);
+          tma_load_3d(smem + C::kOffK + c * C::kChunkBytes, &tm_k, k_full, c * 64, key0, w.bh);
       }
       ++k_issued;
       // Step ii: query tile first + ii % per of the (ii / per)-th query head
@@ -271,8 +304,14 @@ __global__ void __launch_bounds__(384, 1)
         } else {
           qt = w.first + ii;
         }
-        const int row = qt * kTileM;
-        const size_t head = (size_t)qh * p.Nq;
+        int row = qt * kTileM;
+        size_t head = (size_t)qh * p.Nq;
+        int skip = 0;  // packed: zero rows ahead of the tile's own
+        if constexpr (PACKED) {
+          skip = max(0, row + kTileM - w.e.q_len);
+          head += w.e.q_row + row - skip;
+          row += w.e.q_row;
+        }
         // L_i and D_i of the step, read from global memory before the waits
         // below so that the reads overlap them instead of delaying the copies.
         float4 l4, d4;
@@ -281,9 +320,15 @@ __global__ void __launch_bounds__(384, 1)
           float* dp = &d4.x;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int qr = row + 4 * lane + e;
-            lp[e] = qr < p.Nq ? p.lse[head + qr] : INFINITY;
-            dp[e] = qr < p.Nq ? p.dvec[head + qr] : 0.f;
+            if constexpr (PACKED) {
+              const int c = 4 * lane + e;
+              lp[e] = c >= skip ? p.lse[head + c] : INFINITY;
+              dp[e] = c >= skip ? p.dvec[head + c] : 0.f;
+            } else {
+              const int qr = row + 4 * lane + e;
+              lp[e] = qr < p.Nq ? p.lse[head + qr] : INFINITY;
+              dp[e] = qr < p.Nq ? p.dvec[head + qr] : 0.f;
+            }
           }
         }
         // Q_i with L_i (log2 units; rows past Nq and rows that see no key
@@ -301,9 +346,13 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive_expect_tx(&q_full[sq], C::kTileBytes);
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d(smem + C::kOffQ + sq * C::kTileBytes + c * C::kChunkBytes, &tm_q, &q_full[sq], c * 64,
-                        row, qh);
+          for (int c = 0; c < C::kChunks; ++c) {
+            uint8_t* dst = smem + C::kOffQ + sq * C::kTileBytes + c * C::kChunkBytes;
+            if constexpr (PACKED)
+              tma_load_4d(dst, &tm_q, &q_full[sq], c * 64, -skip, row, qh);
+            else
+              tma_load_3d(dst, &tm_q, &q_full[sq], c * 64, row, qh);
+          }
         }
         ++q_issued;
         // dO_i with D_i.
@@ -314,9 +363,13 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive_expect_tx(&do_full[sd], C::kTileBytes);
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d(smem + C::kOffDO + sd * C::kTileBytes + c * C::kChunkBytes, &tm_do, &do_full[sd],
-                        c * 64, row, qh);
+          for (int c = 0; c < C::kChunks; ++c) {
+            uint8_t* dst = smem + C::kOffDO + sd * C::kTileBytes + c * C::kChunkBytes;
+            if constexpr (PACKED)
+              tma_load_4d(dst, &tm_do, &do_full[sd], c * 64, -skip, row, qh);
+            else
+              tma_load_3d(dst, &tm_do, &do_full[sd], c * 64, row, qh);
+          }
         }
         ++do_issued;
         if (ii == 0) {
@@ -326,7 +379,7 @@ __global__ void __launch_bounds__(384, 1)
           if (lane == 0) {
             mbar_arrive_expect_tx(v_full, C::kTileBytes);
             for (int c = 0; c < C::kChunks; ++c)
-              tma_load_3d(smem + C::kOffV + c * C::kChunkBytes, &tm_v, v_full, c * 64, w.t * kTileN, w.bh);
+              tma_load_3d(smem + C::kOffV + c * C::kChunkBytes, &tm_v, v_full, c * 64, key0, w.bh);
           }
           ++v_issued;
         }
@@ -369,18 +422,19 @@ __global__ void __launch_bounds__(384, 1)
     // (the `un`-th unit this CTA runs), step `ii` of it.
     struct Cur {
       int rnd, ii, un;
-      BwdUnit w;
+      BwdUnit<PACKED> w;
       bool valid;
     };
     auto seek = [&](Cur& c, int rnd, int un) {
       c.valid = false;
-      for (; rnd * (int)gridDim.x < p.num_units_kv; ++rnd) {
+      for (; rnd * (int)gridDim.x < n_units; ++rnd) {
         const int u = snake_unit(rnd);
-        if (u < p.num_units_kv) {
+        if (u < n_units) {
           c.rnd = rnd;
           c.ii = 0;
           c.un = un;
-          c.w = decode_dkdv(p, u);
+          c.w = decode_dkdv<PACKED>(p, u);
+          if (PACKED && c.w.count == 0) continue;
           c.valid = true;
           return;
         }
@@ -504,6 +558,7 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp < 8) {
     // ------------------------------------------ P^T, dS^T and dK/dV output
     reg_alloc<R::kRegsMath>();
+    using Head = std::conditional_t<PACKED, int, size_t>;  // packed: the head; else its first row
     const int g = warp & 3;    // TMEM lane quarter
     const int hc = warp >> 2;  // query-column half
     const uint32_t lane_off = (uint32_t)(32 * g) << 16;
@@ -517,7 +572,8 @@ __global__ void __launch_bounds__(384, 1)
     // part of the row of dV and of dK is packed to bf16 and released from
     // TMEM before any store is issued, so that the next unit's accumulation
     // does not wait behind the stores.
-    auto write_part = [&](auto nc_tag, int kr, size_t head) {
+    // (Packed: kr is the row of the tensor and `rows` ends the sequence.)
+    auto write_part = [&](auto nc_tag, int kr, Head head, int rows) {
       constexpr int NC = decltype(nc_tag)::value;
       const int c0 = hc ? RowSplit<D>::kLo : 0;
       uint32_t w[2][NC / 2];
@@ -527,32 +583,61 @@ __global__ void __launch_bounds__(384, 1)
       mbar_arrive_warp(dkv_empty);
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(which ? p.dk : p.dv) + (head + kr) * D + c0;
-        store_rows<NC / 16>(reinterpret_cast<uint8_t*>(dst), (size_t)D * 2, kr, p.Nk, w[which], p.store32 != 0);
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(which ? p.dk : p.dv) + c0;
+        size_t stride = (size_t)D * 2;
+        if constexpr (PACKED) {
+          dst += (long long)kr * (which ? p.dk_row : p.dv_row) + (long long)head * (which ? p.dk_head : p.dv_head);
+          stride = (size_t)(which ? p.dk_row : p.dv_row) * 2;
+        } else {
+          dst += (head + kr) * D;
+        }
+        store_rows<NC / 16>(reinterpret_cast<uint8_t*>(dst), stride, kr, PACKED ? rows : p.Nk, w[which], p.store32 != 0);
       }
     };
-    auto write_dkdv = [&](int kr, size_t head) -> bool {
+    auto write_dkdv = [&](int kr, Head head, int rows) -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait(dkv_full, uc & 1, ctl, kWaitBwdSoftmax))) return false;
       ++uc;
       tc_fence_after();
       if constexpr (RowSplit<D>::kLo == RowSplit<D>::kHi) {
-        write_part(std::integral_constant<int, RowSplit<D>::kLo>{}, kr, head);
+        write_part(std::integral_constant<int, RowSplit<D>::kLo>{}, kr, head, rows);
       } else {
         if (hc == 0)
-          write_part(std::integral_constant<int, RowSplit<D>::kLo>{}, kr, head);
+          write_part(std::integral_constant<int, RowSplit<D>::kLo>{}, kr, head, rows);
         else
-          write_part(std::integral_constant<int, RowSplit<D>::kHi>{}, kr, head);
+          write_part(std::integral_constant<int, RowSplit<D>::kHi>{}, kr, head, rows);
       }
       return true;
     };
     int pend_kr = -1;  // the unit whose dK / dV are still in TMEM
-    size_t pend_head = 0;
-    for (int rnd = 0; ok && rnd * (int)gridDim.x < p.num_units_kv; ++rnd) {
+    Head pend_head = 0;
+    int pend_rows = 0;
+    for (int rnd = 0; ok && rnd * (int)gridDim.x < n_units; ++rnd) {
       const int u = snake_unit(rnd);
-      if (u >= p.num_units_kv) continue;
-      const BwdUnit w = decode_dkdv(p, u);
+      if (u >= n_units) continue;
+      const BwdUnit<PACKED> w = decode_dkdv<PACKED>(p, u);
       const int kr = w.t * kTileN + r_key;  // key index
-      const size_t head = (size_t)w.bh * p.Nk;
+      const Head head = PACKED ? (Head)w.bh : (Head)w.bh * p.Nk;
+      int rows = p.Nk, off = p.causal_off, q_len = 0, k_row = 0;
+      if constexpr (PACKED) {
+        rows = w.e.k_len;
+        off = w.e.off;
+        q_len = w.e.q_len;
+        k_row = w.e.k_row;
+        if (w.count == 0) {
+          // No query sees the tile.
+          if (kr < rows) {
+            __nv_bfloat16* dv0 = reinterpret_cast<__nv_bfloat16*>(p.dv) + (long long)(k_row + kr) * p.dv_row + (long long)head * p.dv_head;
+            __nv_bfloat16* dk0 = reinterpret_cast<__nv_bfloat16*>(p.dk) + (long long)(k_row + kr) * p.dk_row + (long long)head * p.dk_head;
+            const int c0 = hc ? RowSplit<D>::kLo : 0, n = hc ? RowSplit<D>::kHi : RowSplit<D>::kLo;
+#pragma unroll 1
+            for (int c = 0; c < n; c += 8) {
+              *reinterpret_cast<uint4*>(dv0 + c0 + c) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(dk0 + c0 + c) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          continue;
+        }
+      }
       int qt = w.first;
       for (int ii = 0; ok && ii < w.count; ++ii, ++qc) {
         if constexpr (GQA) {
@@ -560,7 +645,8 @@ __global__ void __launch_bounds__(384, 1)
         } else {
           qt = w.first + ii;
         }
-        const int q0 = qt * kTileM;
+        int q0 = qt * kTileM;
+        if constexpr (PACKED) q0 -= max(0, q0 + kTileM - q_len);  // the tile's first row, zero rows ahead
         const uint32_t reg = qc & 1;
         const uint32_t tZ = tmem + lane_off + C::col_r(reg) + 64 * hc;
         const uint32_t sq = qc % C::kQStages;
@@ -580,13 +666,13 @@ __global__ void __launch_bounds__(384, 1)
         {
           const float* bl = sLse + sq * 128 + 64 * hc;
           const int qf = q0 + 64 * hc;
-          if ((kr >= p.Nk) || (p.causal && kr > qf + p.causal_off))
-            p64_colL<true>(pv, bl, sl2, kr - p.causal_off, qf, kr >= p.Nk, p.causal != 0);
+          if ((kr >= rows) || (p.causal && kr > qf + off))
+            p64_colL<true>(pv, bl, sl2, kr - off, qf, kr >= rows, p.causal != 0);
           else
             p64_colL<false>(pv, bl, sl2, kr, qf, false, false);
         }
         if (ii == 0 && pend_kr >= 0) {
-          ok = write_dkdv(pend_kr, pend_head);
+          ok = write_dkdv(pend_kr, pend_head, pend_rows);
           if (!ok) break;
         }
         uint32_t pk[32];
@@ -628,10 +714,11 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive_warp(&p_ready[reg]);
       }
       if (!ok) break;
-      pend_kr = kr;
+      pend_kr = PACKED ? k_row + kr : kr;
       pend_head = head;
+      pend_rows = k_row + rows;
     }
-    if (ok && pend_kr >= 0) write_dkdv(pend_kr, pend_head);
+    if (ok && pend_kr >= 0) write_dkdv(pend_kr, pend_head, pend_rows);
   } else {
     reg_dealloc<R::kRegsCtl>();
   }
@@ -670,13 +757,15 @@ struct DqCfg {
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
-template <int D>
+// PACKED: units of packed sequences (BwdParams::entries_q); the last key tile of
+// a sequence holds zeros ahead of its keys (see packed.h).
+template <int D, bool PACKED>
 __global__ void __launch_bounds__(384, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                      const BwdParams p) {
   using C = DqCfg<D>;
-  using R = BwdRegs;
+  using R = BwdRegs<PACKED && D == 96>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (threadIdx.x == 0) atomicCAS(p.status, 0u, (unsigned int)FA_ERR_CUDA);
@@ -744,6 +833,8 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{p.status, p.timeout_ns};
+  // (Packed: the units were there before any dK/dV CTA let this kernel start.)
+  const int n_units = PACKED ? p.entry_counts[1] * p.H : p.num_units;
 
   if (warp == 9) {
     // ------------------------------------------------------------ producer
@@ -752,26 +843,38 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t uc = 0, kc = 0;
       uint32_t q_issued = 0, do_issued = 0, k_issued = 0, v_issued = 0;  // copies started (for the drain)
       bool ok = true;
-      for (int rnd = 0; ok && rnd * (int)gridDim.x < p.num_units; ++rnd) {
+      for (int rnd = 0; ok && rnd * (int)gridDim.x < n_units; ++rnd) {
         const int u = snake_unit(rnd);
-        if (u >= p.num_units) continue;
-        const BwdUnit w = decode_dq(p, u);
+        if (u >= n_units) continue;
+        const BwdUnit<PACKED> w = decode_dq<PACKED>(p, u);
         const int kvbh = p.Hkv == p.H ? w.bh : kv_head_of(w.bh, p.H, p.Hkv);  // K, V head
+        if (PACKED && w.count == 0) continue;
+        int row0 = w.t * kTileM;
+        if constexpr (PACKED) row0 += w.e.q_row;
         ok = mbar_wait(q_empty, (uc & 1) ^ 1, ctl, kWaitBwdLoad);
         if (!ok) break;
         mbar_arrive_expect_tx(q_full, C::kTileBytes);
         for (int c = 0; c < C::kChunks; ++c)
-          tma_load_3d(smem + C::kOffQ + c * C::kChunkBytes, &tm_q, q_full, c * 64, w.t * kTileM, w.bh);
+          tma_load_3d(smem + C::kOffQ + c * C::kChunkBytes, &tm_q, q_full, c * 64, row0, w.bh);
         ++q_issued;
         for (int jj = 0; ok && jj < w.count; ++jj, ++kc) {
-          const int key0 = (w.first + jj) * kTileN;
+          int key0 = (w.first + jj) * kTileN;
+          int skip = 0;  // packed: zero rows ahead of the tile's own
+          if constexpr (PACKED) {
+            skip = max(0, key0 + kTileN - w.e.k_len);
+            key0 += w.e.k_row;
+          }
           const uint32_t sk = kc % C::kKStages;
           ok = mbar_wait(&k_empty[sk], ((kc / C::kKStages) & 1) ^ 1, ctl, kWaitBwdLoad);
           if (!ok) break;
           mbar_arrive_expect_tx(&k_full[sk], C::kTileBytes);
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d(smem + C::kOffK + sk * C::kTileBytes + c * C::kChunkBytes, &tm_k, &k_full[sk], c * 64, key0,
-                        kvbh);
+          for (int c = 0; c < C::kChunks; ++c) {
+            uint8_t* dst = smem + C::kOffK + sk * C::kTileBytes + c * C::kChunkBytes;
+            if constexpr (PACKED)
+              tma_load_4d(dst, &tm_k, &k_full[sk], c * 64, -skip, key0, kvbh);
+            else
+              tma_load_3d(dst, &tm_k, &k_full[sk], c * 64, key0, kvbh);
+          }
           ++k_issued;
           if (jj == 0) {
             // dO_i, needed by the first dP, after the first K.
@@ -779,16 +882,20 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             mbar_arrive_expect_tx(do_full, C::kTileBytes);
             for (int c = 0; c < C::kChunks; ++c)
-              tma_load_3d(smem + C::kOffDO + c * C::kChunkBytes, &tm_do, do_full, c * 64, w.t * kTileM, w.bh);
+              tma_load_3d(smem + C::kOffDO + c * C::kChunkBytes, &tm_do, do_full, c * 64, row0, w.bh);
             ++do_issued;
           }
           const uint32_t sv = kc % C::kVStages;
           ok = mbar_wait(&v_empty[sv], ((kc / C::kVStages) & 1) ^ 1, ctl, kWaitBwdLoad);
           if (!ok) break;
           mbar_arrive_expect_tx(&v_full[sv], C::kTileBytes);
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d(smem + C::kOffV + sv * C::kTileBytes + c * C::kChunkBytes, &tm_v, &v_full[sv], c * 64, key0,
-                        kvbh);
+          for (int c = 0; c < C::kChunks; ++c) {
+            uint8_t* dst = smem + C::kOffV + sv * C::kTileBytes + c * C::kChunkBytes;
+            if constexpr (PACKED)
+              tma_load_4d(dst, &tm_v, &v_full[sv], c * 64, -skip, key0, kvbh);
+            else
+              tma_load_3d(dst, &tm_v, &v_full[sv], c * 64, key0, kvbh);
+          }
           ++v_issued;
         }
         ++uc;
@@ -821,10 +928,11 @@ __global__ void __launch_bounds__(384, 1)
         // dP of every step, once the previous dP was read out; dO_i is
         // released after the unit's last dP.
         uint32_t uc = 0, kc = 0, dn = 0;
-        for (int rnd = 0; ok && rnd * (int)gridDim.x < p.num_units; ++rnd) {
+        for (int rnd = 0; ok && rnd * (int)gridDim.x < n_units; ++rnd) {
           const int u = snake_unit(rnd);
-          if (u >= p.num_units) continue;
-          const BwdUnit w = decode_dq(p, u);
+          if (u >= n_units) continue;
+          const BwdUnit<PACKED> w = decode_dq<PACKED>(p, u);
+          if (PACKED && w.count == 0) continue;
           ok = __all_sync(0xffffffffu, mbar_wait(do_full, uc & 1, ctl, kWaitBwdMma));
           ++uc;
           for (int jj = 0; ok && jj < w.count; ++jj, ++kc) {
@@ -868,10 +976,11 @@ __global__ void __launch_bounds__(384, 1)
           if (last) mma_commit_w(q_empty);
           return true;
         };
-        for (int rnd = 0; ok && rnd * (int)gridDim.x < p.num_units; ++rnd) {
+        for (int rnd = 0; ok && rnd * (int)gridDim.x < n_units; ++rnd) {
           const int u = snake_unit(rnd);
-          if (u >= p.num_units) continue;
-          const BwdUnit w = decode_dq(p, u);
+          if (u >= n_units) continue;
+          const BwdUnit<PACKED> w = decode_dq<PACKED>(p, u);
+          if (PACKED && w.count == 0) continue;
           ok = __all_sync(0xffffffffu, mbar_wait(q_full, uc & 1, ctl, kWaitBwdMma));
           if (!ok) break;
           tc_fence_after();
@@ -914,6 +1023,7 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp < 8) {
     // --------------------------------------------------- P, dS and dQ output
     reg_alloc<R::kRegsMath>();
+    using Head = std::conditional_t<PACKED, int, size_t>;  // packed: the head; else its first row
     const int g = warp & 3;    // TMEM lane quarter: queries [32 g, 32 g + 32)
     const int hc = warp >> 2;  // key-column half
     const uint32_t lane_off = (uint32_t)(32 * g) << 16;
@@ -928,7 +1038,8 @@ __global__ void __launch_bounds__(384, 1)
     // here: the dQ stores follow the TMEM release and overlap the next
     // unit's first steps, and the shuffles of store_rows measured slower
     // than the scattered lines they save.
-    auto write_part = [&](auto nc_tag, int q, size_t head) {
+    // (Packed: q is the row of the tensor and `rows` ends the sequence.)
+    auto write_part = [&](auto nc_tag, int q, Head head, int rows) {
       constexpr int NC = decltype(nc_tag)::value;
       const int c0 = hc ? RowSplit<D>::kLo : 0;
       uint32_t v[NC];
@@ -937,13 +1048,13 @@ __global__ void __launch_bounds__(384, 1)
       tmem_ld_wait<NC>(v);
       tc_fence_before();
       mbar_arrive_warp(dq_empty);
-      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.dq) + (head + q) * D + c0;
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.dq) + (PACKED ? (size_t)q * p.dq_row + head * p.dq_head : (head + q) * D) + c0;
       const float sc = p.scale;
       uint32_t w[NC / 2];
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i)
         w[i] = pack_bf16(__uint_as_float(v[2 * i]) * sc, __uint_as_float(v[2 * i + 1]) * sc);
-      if (q < p.Nq) {
+      if (q < (PACKED ? rows : p.Nq)) {
         if (p.store32) {
 #pragma unroll
           for (int i = 0; i < NC / 16; ++i) st_global_v8(dst + 16 * i, w + 8 * i);
@@ -954,35 +1065,62 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
     };
-    auto write_dq = [&](int q, size_t head) -> bool {
+    auto write_dq = [&](int q, Head head, int rows) -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait(dq_full, uc & 1, ctl, kWaitBwdDq))) return false;
       ++uc;
       tc_fence_after();
       if constexpr (RowSplit<D>::kLo == RowSplit<D>::kHi) {
-        write_part(std::integral_constant<int, RowSplit<D>::kLo>{}, q, head);
+        write_part(std::integral_constant<int, RowSplit<D>::kLo>{}, q, head, rows);
       } else {
         if (hc == 0)
-          write_part(std::integral_constant<int, RowSplit<D>::kLo>{}, q, head);
+          write_part(std::integral_constant<int, RowSplit<D>::kLo>{}, q, head, rows);
         else
-          write_part(std::integral_constant<int, RowSplit<D>::kHi>{}, q, head);
+          write_part(std::integral_constant<int, RowSplit<D>::kHi>{}, q, head, rows);
       }
       return true;
     };
     int pend_q = -1;  // the unit whose dQ is still in TMEM
-    size_t pend_head = 0;
-    for (int rnd = 0; ok && rnd * (int)gridDim.x < p.num_units; ++rnd) {
+    Head pend_head = 0;
+    int pend_rows = 0;
+    for (int rnd = 0; ok && rnd * (int)gridDim.x < n_units; ++rnd) {
       const int u = snake_unit(rnd);
-      if (u >= p.num_units) continue;
-      const BwdUnit w = decode_dq(p, u);
-      const size_t head = (size_t)w.bh * p.Nq;
+      if (u >= n_units) continue;
+      const BwdUnit<PACKED> w = decode_dq<PACKED>(p, u);
+      const Head head = PACKED ? (Head)w.bh : (Head)w.bh * p.Nq;
       const int q = w.t * kTileM + 32 * g + lane;  // query row
-      const float Lraw = q < p.Nq ? p.lse[head + q] : INFINITY;
+      int rows = p.Nq, off = p.causal_off, keys = p.Nk;
+      int q_row = 0;
+      size_t row = (size_t)head + q;
+      if constexpr (PACKED) {
+        rows = w.e.q_len;
+        off = w.e.off;
+        keys = w.e.k_len;
+        q_row = w.e.q_row;
+        row = (size_t)w.bh * p.Nq + q_row + q;
+        if (w.count == 0) {
+          // The tile sees no key.
+          if (q < rows) {
+            __nv_bfloat16* dq0 = reinterpret_cast<__nv_bfloat16*>(p.dq) + (size_t)(q_row + q) * p.dq_row + head * p.dq_head;
+            const int c0 = hc ? RowSplit<D>::kLo : 0, n = hc ? RowSplit<D>::kHi : RowSplit<D>::kLo;
+#pragma unroll 1
+            for (int c = 0; c < n; c += 8)
+              *reinterpret_cast<uint4*>(dq0 + c0 + c) = make_uint4(0, 0, 0, 0);
+          }
+          continue;
+        }
+      }
+      const float Lraw = q < rows ? p.lse[row] : INFINITY;
       const float L = Lraw == -INFINITY ? INFINITY : Lraw * 1.4426950408889634f;  // no key seen: weights 0
-      const float Dq = q < p.Nq ? p.dvec[head + q] : 0.f;
+      const float Dq = q < rows ? p.dvec[row] : 0.f;
       const int q_lo = w.t * kTileM + 32 * g;  // first query of this warp
       for (int jj = 0; ok && jj < w.count; ++jj, ++kc) {
         const uint32_t tS = tmem + lane_off + ((kc & 1) ? C::kColS1 : C::kColS0) + 64 * hc;
-        const int k_first = (w.first + jj) * kTileN + 64 * hc;
+        int k_first = (w.first + jj) * kTileN + 64 * hc;
+        int skip = 0;  // columns of the tile ahead of its keys
+        if constexpr (PACKED) {
+          skip = max(0, (w.first + jj + 1) * kTileN - keys);
+          k_first -= skip;
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[kc & 1], (kc >> 1) & 1, ctl, kWaitBwdSoftmax));
         if (!ok) break;
         tc_fence_after();
@@ -990,12 +1128,12 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld32(tS, pv);
         tmem_ld32(tS + 32, pv + 32);
         tmem_ld_wait<64>(pv);
-        if (k_first + 63 >= p.Nk || (p.causal && k_first + 63 > q_lo + p.causal_off))
-          p64_rowL<true>(pv, L, sl2, q + p.causal_off, k_first, p.Nk, p.causal != 0);
+        if (k_first + 63 >= keys || (PACKED && skip > 0) || (p.causal && k_first + 63 > q_lo + off))
+          p64_rowL<true, PACKED>(pv, L, sl2, q + off, k_first, keys, p.causal != 0, (w.first + jj) * kTileN);
         else
-          p64_rowL<false>(pv, L, sl2, q, k_first, p.Nk, false);
+          p64_rowL<false>(pv, L, sl2, q, k_first, keys, false);
         if (jj == 0 && pend_q >= 0) {
-          ok = write_dq(pend_q, pend_head);
+          ok = write_dq(pend_q, pend_head, pend_rows);
           if (!ok) break;
         }
         ok = __all_sync(0xffffffffu, mbar_wait(dp_full, dc & 1, ctl, kWaitBwdSoftmax));
@@ -1027,10 +1165,11 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive_warp(&p_ready[kc & 1]);
       }
       if (!ok) break;
-      pend_q = q;
+      pend_q = PACKED ? q_row + q : q;
       pend_head = head;
+      pend_rows = q_row + rows;
     }
-    if (ok && pend_q >= 0) write_dq(pend_q, pend_head);
+    if (ok && pend_q >= 0) write_dq(pend_q, pend_head, pend_rows);
   } else {
     reg_dealloc<R::kRegsCtl>();
   }
@@ -1115,28 +1254,28 @@ __global__ void fa_selftest_wait_kernel(unsigned int* status, unsigned long long
 
 // ------------------------------------------------------------------ launch
 
-template <int D, bool GQA>
+template <int D, bool GQA, bool PACKED>
 static cudaError_t launch_dkdv_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                  const CUtensorMap& tdo, const BwdParams& p, int grid, cudaStream_t stream) {
   using C = DkdvCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(fa_bwd_dkdv_kernel<D, GQA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(fa_bwd_dkdv_kernel<D, GQA, PACKED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(fa_bwd_dkdv_kernel<D, GQA>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream, tq, tk, tv, tdo, p);
+  e = launch_pdl(fa_bwd_dkdv_kernel<D, GQA, PACKED>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream, tq, tk, tv, tdo, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool PACKED>
 static cudaError_t launch_dq_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const CUtensorMap& tdo, const BwdParams& p, int grid, cudaStream_t stream) {
   using C = DqCfg<D>;
   cudaError_t e =
-      cudaFuncSetAttribute(fa_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+      cudaFuncSetAttribute(fa_bwd_dq_kernel<D, PACKED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   // May start as the dK/dV kernel's CTAs finish: it reads only the inputs,
   // L and D, and D was complete before any dK/dV CTA let it start.
-  e = launch_pdl(fa_bwd_dq_kernel<D>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream, tq, tk, tv, tdo, p);
+  e = launch_pdl(fa_bwd_dq_kernel<D, PACKED>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream, tq, tk, tv, tdo, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -1146,14 +1285,14 @@ cudaError_t launch_bwd_dkdv(int d, const CUtensorMap& tq, const CUtensorMap& tk,
   const bool gqa = p.Hkv != p.H;
   switch (d) {
     case 64:
-      return gqa ? launch_dkdv_t<64, true>(tq, tk, tv, tdo, p, grid, stream)
-                 : launch_dkdv_t<64, false>(tq, tk, tv, tdo, p, grid, stream);
+      return gqa ? launch_dkdv_t<64, true, false>(tq, tk, tv, tdo, p, grid, stream)
+                 : launch_dkdv_t<64, false, false>(tq, tk, tv, tdo, p, grid, stream);
     case 96:
-      return gqa ? launch_dkdv_t<96, true>(tq, tk, tv, tdo, p, grid, stream)
-                 : launch_dkdv_t<96, false>(tq, tk, tv, tdo, p, grid, stream);
+      return gqa ? launch_dkdv_t<96, true, false>(tq, tk, tv, tdo, p, grid, stream)
+                 : launch_dkdv_t<96, false, false>(tq, tk, tv, tdo, p, grid, stream);
     case 128:
-      return gqa ? launch_dkdv_t<128, true>(tq, tk, tv, tdo, p, grid, stream)
-                 : launch_dkdv_t<128, false>(tq, tk, tv, tdo, p, grid, stream);
+      return gqa ? launch_dkdv_t<128, true, false>(tq, tk, tv, tdo, p, grid, stream)
+                 : launch_dkdv_t<128, false, false>(tq, tk, tv, tdo, p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1161,9 +1300,35 @@ cudaError_t launch_bwd_dkdv(int d, const CUtensorMap& tq, const CUtensorMap& tk,
 cudaError_t launch_bwd_dq(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& tdo, const BwdParams& p, int grid, cudaStream_t stream) {
   switch (d) {
-    case 64: return launch_dq_t<64>(tq, tk, tv, tdo, p, grid, stream);
-    case 96: return launch_dq_t<96>(tq, tk, tv, tdo, p, grid, stream);
-    case 128: return launch_dq_t<128>(tq, tk, tv, tdo, p, grid, stream);
+    case 64: return launch_dq_t<64, false>(tq, tk, tv, tdo, p, grid, stream);
+    case 96: return launch_dq_t<96, false>(tq, tk, tv, tdo, p, grid, stream);
+    case 128: return launch_dq_t<128, false>(tq, tk, tv, tdo, p, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+// The same over packed sequences: streamed operands by maps of [channel, row of
+// the tile, first row, head].  dK/dV of d = 64 and 96 (128 runs on CTA pairs).
+cudaError_t launch_bwd_packed_dkdv(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const CUtensorMap& tdo, const BwdParams& p, int grid, cudaStream_t stream) {
+  const bool gqa = p.Hkv != p.H;
+  switch (d) {
+    case 64:
+      return gqa ? launch_dkdv_t<64, true, true>(tq, tk, tv, tdo, p, grid, stream)
+                 : launch_dkdv_t<64, false, true>(tq, tk, tv, tdo, p, grid, stream);
+    case 96:
+      return gqa ? launch_dkdv_t<96, true, true>(tq, tk, tv, tdo, p, grid, stream)
+                 : launch_dkdv_t<96, false, true>(tq, tk, tv, tdo, p, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_bwd_packed_dq(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const CUtensorMap& tdo, const BwdParams& p, int grid, cudaStream_t stream) {
+  switch (d) {
+    case 64: return launch_dq_t<64, true>(tq, tk, tv, tdo, p, grid, stream);
+    case 96: return launch_dq_t<96, true>(tq, tk, tv, tdo, p, grid, stream);
+    case 128: return launch_dq_t<128, true>(tq, tk, tv, tdo, p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }

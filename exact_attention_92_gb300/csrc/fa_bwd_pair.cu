@@ -43,6 +43,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "bwd_elementwise.cuh"
 #include "sm103_pair.cuh"
@@ -85,7 +86,8 @@ struct BwdRegs {
   static_assert(128 * kRegsCtl + 256 * kRegsMath <= 384 * 168, "register split exceeds the launch");
 };
 
-struct PairUnit {
+template <bool PACKED>
+struct PairUnit : SeqPart<PACKED> {
   int kvbh;   // key/value head
   int tp;     // key tiles 2 tp (rank 0) and 2 tp + 1 (rank 1)
   int first;  // first query tile that sees key tile 2 tp
@@ -95,8 +97,18 @@ struct PairUnit {
 
 // Pair units, low key tiles first (with the causal mask they are seen by
 // the most query rows).
-__device__ __forceinline__ PairUnit decode(const BwdParams& p, int u) {
-  PairUnit w;
+template <bool PACKED>
+__device__ __forceinline__ PairUnit<PACKED> decode(const BwdParams& p, int u) {
+  PairUnit<PACKED> w;
+  if constexpr (PACKED) {
+    w.e = load_entry(p.entries_kv + u / p.Hkv);
+    w.kvbh = u % p.Hkv;
+    w.tp = w.e.tile;
+    w.first = w.e.first;
+    w.per = w.e.count;
+    w.count = w.per * p.group;
+    return w;
+  }
   const int BH = p.B * p.Hkv;
   w.kvbh = u % BH;
   w.tp = u / BH;
@@ -110,7 +122,8 @@ __device__ __forceinline__ int num_pair_units(const BwdParams& p) { return p.B *
 
 }  // namespace pr
 
-template <bool GQA>
+// PACKED: units of packed sequences, as in fa_bwd_dkdv_kernel.
+template <bool GQA, bool PACKED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     fa_bwd_dkdv_pair_kernel(const __grid_constant__ CUtensorMap tm_q64, const __grid_constant__ CUtensorMap tm_q,
                             const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -196,7 +209,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{p.status, p.timeout_ns};
   if (!aligned && threadIdx.x == 0) atomicCAS(p.status, 0u, (unsigned int)FA_ERR_CUDA);
-  const int n_units = aligned ? num_pair_units(p) : 0;
+  int n_units = aligned ? num_pair_units(p) : 0;
+  if constexpr (PACKED) {
+    pdl_wait();  // the units are on the device
+    n_units = aligned ? p.entry_counts[0] * p.Hkv : 0;
+  }
   const int G = (int)gridDim.x >> 1;
 
   if (warp == 9) {
@@ -214,8 +231,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     for (int rnd = 0; ok && rnd * G < n_units; ++rnd) {
       const int u = pair_unit(rnd);
       if (u >= n_units) continue;
-      const PairUnit w = decode(p, u);
-      const int key0 = (2 * w.tp + (int)rank) * kTileN;
+      const PairUnit<PACKED> w = decode<PACKED>(p, u);
+      if (PACKED && w.count == 0) continue;
+      int key0 = (2 * w.tp + (int)rank) * kTileN;
+      if constexpr (PACKED) key0 += w.e.k_row;
       ok = __all_sync(0xffffffffu, mbar_wait(k_empty, (kc & 1) ^ 1, ctl, kWaitBwdLoad));
       if (!ok) break;
       if (lane == 0) {
@@ -234,8 +253,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         } else {
           qt = w.first + ii;
         }
-        const int row = qt * kTileM;
-        const size_t head = (size_t)qh * p.Nq;
+        int row = qt * kTileM;
+        size_t head = (size_t)qh * p.Nq;
+        int skip = 0;  // packed: zero rows ahead of the tile's own
+        if constexpr (PACKED) {
+          skip = max(0, row + kTileM - w.e.q_len);
+          head += w.e.q_row + row - skip;
+          row += w.e.q_row;
+        }
         // L and D of the step's 128 query rows, read before the waits below.
         float4 l4, d4;
         {
@@ -243,9 +268,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           float* dp = &d4.x;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int qr = row + 4 * lane + e;
-            lp[e] = qr < p.Nq ? p.lse[head + qr] : INFINITY;
-            dp[e] = qr < p.Nq ? p.dvec[head + qr] : 0.f;
+            if constexpr (PACKED) {
+              const int c = 4 * lane + e;
+              lp[e] = c >= skip ? p.lse[head + c] : INFINITY;
+              dp[e] = c >= skip ? p.dvec[head + c] : 0.f;
+            } else {
+              const int qr = row + 4 * lane + e;
+              lp[e] = qr < p.Nq ? p.lse[head + qr] : INFINITY;
+              dp[e] = qr < p.Nq ? p.dvec[head + qr] : 0.f;
+            }
           }
         }
         // This CTA's part of Q_i: rows [64 r, 64 r + 64) of both chunks
@@ -257,9 +288,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           uint8_t* st = smem + kOffQ + sq * kStage;
           const uint32_t bar = at_leader(&q_full[sq]);
           if (leader) mbar_arrive_expect_tx(&q_full[sq], 2 * kStage);
-          for (int c = 0; c < 2; ++c)
-            tma_load_3d_pair(st + kStageRows + c * kHalf, &tm_q64, bar, c * 64, row + 64 * (int)rank, qh);
-          tma_load_3d_pair(st + kStageCols, &tm_q, bar, 64 * (int)rank, row, qh);
+          for (int c = 0; c < 2; ++c) {
+            if constexpr (PACKED)
+              tma_load_4d_pair(st + kStageRows + c * kHalf, &tm_q64, bar, c * 64, 64 * (int)rank - skip, row, qh);
+            else
+              tma_load_3d_pair(st + kStageRows + c * kHalf, &tm_q64, bar, c * 64, row + 64 * (int)rank, qh);
+          }
+          if constexpr (PACKED)
+            tma_load_4d_pair(st + kStageCols, &tm_q, bar, 64 * (int)rank, -skip, row, qh);
+          else
+            tma_load_3d_pair(st + kStageCols, &tm_q, bar, 64 * (int)rank, row, qh);
         }
         ++q_issued;
         const uint32_t sd = qc % kDoStages;
@@ -269,9 +307,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           uint8_t* st = smem + kOffDO + sd * kStage;
           const uint32_t bar = at_leader(&do_full[sd]);
           if (leader) mbar_arrive_expect_tx(&do_full[sd], 2 * kStage);
-          for (int c = 0; c < 2; ++c)
-            tma_load_3d_pair(st + kStageRows + c * kHalf, &tm_do64, bar, c * 64, row + 64 * (int)rank, qh);
-          tma_load_3d_pair(st + kStageCols, &tm_do, bar, 64 * (int)rank, row, qh);
+          for (int c = 0; c < 2; ++c) {
+            if constexpr (PACKED)
+              tma_load_4d_pair(st + kStageRows + c * kHalf, &tm_do64, bar, c * 64, 64 * (int)rank - skip, row, qh);
+            else
+              tma_load_3d_pair(st + kStageRows + c * kHalf, &tm_do64, bar, c * 64, row + 64 * (int)rank, qh);
+          }
+          if constexpr (PACKED)
+            tma_load_4d_pair(st + kStageCols, &tm_do, bar, 64 * (int)rank, -skip, row, qh);
+          else
+            tma_load_3d_pair(st + kStageCols, &tm_do, bar, 64 * (int)rank, row, qh);
         }
         ++do_issued;
         if (ii == 0) {
@@ -335,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       };
       struct Cur {
         int rnd, ii, un;
-        PairUnit w;
+        PairUnit<PACKED> w;
         bool valid;
       };
       auto seek = [&](Cur& c, int rnd, int un) {
@@ -346,7 +391,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
             c.rnd = rnd;
             c.ii = 0;
             c.un = un;
-            c.w = decode(p, u);
+            c.w = decode<PACKED>(p, u);
+            if (PACKED && c.w.count == 0) continue;
             c.valid = true;
             return;
           }
@@ -463,6 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   } else if (warp < 8) {
     // ------------------------------------------ P^T, dS^T and dK/dV output
     reg_alloc<R::kRegsMath>();
+    using Head = std::conditional_t<PACKED, int, size_t>;  // packed: the head; else its first row
     const int gq = warp & 3;   // TMEM lane quarter
     const int hc = warp >> 2;  // query-column half
     const uint32_t lane_off = (uint32_t)(32 * gq) << 16;
@@ -476,7 +523,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     // dK_j = scale * sum dS^T Q and dV_j = sum P^T dO of this CTA's key
     // tile; this warp writes head-dim columns [64 hc, 64 hc + 64), packed
     // and released from TMEM before the stores.
-    auto write_dkdv = [&](int kr, size_t head) -> bool {
+    // (Packed: kr is the row of the tensor and `rows` ends the sequence.)
+    auto write_dkdv = [&](int kr, Head head, int rows) -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait(dkv_full, uc & 1, ctl, kWaitBwdSoftmax))) return false;
       ++uc;
       tc_fence_after();
@@ -488,19 +536,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       arrive_leader_warp(dkv_empty_l);
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(which ? p.dk : p.dv) + (head + kr) * kD + c0;
-        store_rows<4>(reinterpret_cast<uint8_t*>(dst), (size_t)kD * 2, kr, p.Nk, wv[which], p.store32 != 0);
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(which ? p.dk : p.dv) + c0;
+        size_t stride = (size_t)kD * 2;
+        if constexpr (PACKED) {
+          dst += (long long)kr * (which ? p.dk_row : p.dv_row) + (long long)head * (which ? p.dk_head : p.dv_head);
+          stride = (size_t)(which ? p.dk_row : p.dv_row) * 2;
+        } else {
+          dst += (head + kr) * kD;
+        }
+        store_rows<4>(reinterpret_cast<uint8_t*>(dst), stride, kr, PACKED ? rows : p.Nk, wv[which], p.store32 != 0);
       }
       return true;
     };
     int pend_kr = -1;
-    size_t pend_head = 0;
+    Head pend_head = 0;
+    int pend_rows = 0;
     for (int rnd = 0; ok && rnd * G < n_units; ++rnd) {
       const int u = pair_unit(rnd);
       if (u >= n_units) continue;
-      const PairUnit w = decode(p, u);
+      const PairUnit<PACKED> w = decode<PACKED>(p, u);
       const int kr = (2 * w.tp + (int)rank) * kTileN + r_key;  // key index
-      const size_t head = (size_t)w.kvbh * p.Nk;
+      const Head head = PACKED ? (Head)w.kvbh : (Head)w.kvbh * p.Nk;
+      int rows = p.Nk, off = p.causal_off, q_len = 0, k_row = 0;
+      if constexpr (PACKED) {
+        rows = w.e.k_len;
+        off = w.e.off;
+        q_len = w.e.q_len;
+        k_row = w.e.k_row;
+        if (w.count == 0) {
+          // No query sees the tiles.
+          if (kr < rows) {
+            __nv_bfloat16* dv0 = reinterpret_cast<__nv_bfloat16*>(p.dv) + (long long)(k_row + kr) * p.dv_row + (long long)head * p.dv_head;
+            __nv_bfloat16* dk0 = reinterpret_cast<__nv_bfloat16*>(p.dk) + (long long)(k_row + kr) * p.dk_row + (long long)head * p.dk_head;
+            for (int c = 64 * hc; c < 64 * hc + 64; c += 8) {
+              *reinterpret_cast<uint4*>(dv0 + c) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(dk0 + c) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          continue;
+        }
+      }
       int qt = w.first;
       for (int ii = 0; ok && ii < w.count; ++ii, ++qc) {
         if constexpr (GQA) {
@@ -508,7 +583,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         } else {
           qt = w.first + ii;
         }
-        const int q0 = qt * kTileM;
+        int q0 = qt * kTileM;
+        if constexpr (PACKED) q0 -= max(0, q0 + kTileM - q_len);  // the tile's first row, zero rows ahead
         const uint32_t reg = qc & 1;
         const uint32_t tZ = tmem + lane_off + 128u * reg + 64 * hc;
         const uint32_t sr = qc % kRvStages;
@@ -527,13 +603,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         {
           const float* bl = sRv + sr * 256 + 64 * hc;
           const int qf = q0 + 64 * hc;
-          if ((kr >= p.Nk) || (p.causal && kr > qf + p.causal_off))
-            p64_colL<true>(pv, bl, sl2, kr - p.causal_off, qf, kr >= p.Nk, p.causal != 0);
+          if ((kr >= rows) || (p.causal && kr > qf + off))
+            p64_colL<true>(pv, bl, sl2, kr - off, qf, kr >= rows, p.causal != 0);
           else
             p64_colL<false>(pv, bl, sl2, kr, qf, false, false);
         }
         if (ii == 0 && pend_kr >= 0) {
-          ok = write_dkdv(pend_kr, pend_head);
+          ok = write_dkdv(pend_kr, pend_head, pend_rows);
           if (!ok) break;
         }
         uint32_t pk[32];
@@ -575,10 +651,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         mbar_arrive_warp(&rv_empty[sr]);  // the step's L and D were read
       }
       if (!ok) break;
-      pend_kr = kr;
+      pend_kr = PACKED ? k_row + kr : kr;
       pend_head = head;
+      pend_rows = k_row + rows;
     }
-    if (ok && pend_kr >= 0) write_dkdv(pend_kr, pend_head);
+    if (ok && pend_kr >= 0) write_dkdv(pend_kr, pend_head, pend_rows);
   } else {
     reg_dealloc<R::kRegsCtl>();
   }
@@ -594,11 +671,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
 
 // ------------------------------------------------------------------ launch
 
-template <bool GQA>
+template <bool GQA, bool PACKED>
 static cudaError_t launch_pair_t(const CUtensorMap& tq64, const CUtensorMap& tq, const CUtensorMap& tk,
                                  const CUtensorMap& tv, const CUtensorMap& tdo64, const CUtensorMap& tdo,
-                                 const BwdParams& p, int sm_count, cudaStream_t stream) {
-  auto* kern = fa_bwd_dkdv_pair_kernel<GQA>;
+                                 const BwdParams& p, long long units, int sm_count, cudaStream_t stream) {
+  auto* kern = fa_bwd_dkdv_pair_kernel<GQA, PACKED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pr::kSmemBytes);
   if (e != cudaSuccess) return e;
   // Pairs resident at once (a pair needs two SMs of one cluster group),
@@ -623,7 +700,6 @@ static cudaError_t launch_pair_t(const CUtensorMap& tq64, const CUtensorMap& tq,
     mp = n;
     max_pairs[dev].store(n, std::memory_order_relaxed);
   }
-  const long long units = (long long)p.B * p.Hkv * ((p.kv_tiles_used + 1) / 2);
   const int pairs = (int)(units < mp ? units : mp);
   e = launch_pdl(kern, dim3(2 * pairs), dim3(pr::kThreads), pr::kSmemBytes, stream, tq64, tq, tk, tv, tdo64, tdo, p);
   if (e != cudaSuccess) return e;
@@ -635,8 +711,18 @@ static cudaError_t launch_pair_t(const CUtensorMap& tq64, const CUtensorMap& tq,
 cudaError_t launch_bwd_dkdv_pair(const CUtensorMap& tq64, const CUtensorMap& tq, const CUtensorMap& tk,
                                  const CUtensorMap& tv, const CUtensorMap& tdo64, const CUtensorMap& tdo,
                                  const BwdParams& p, int sm_count, cudaStream_t stream) {
-  return p.Hkv != p.H ? launch_pair_t<true>(tq64, tq, tk, tv, tdo64, tdo, p, sm_count, stream)
-                      : launch_pair_t<false>(tq64, tq, tk, tv, tdo64, tdo, p, sm_count, stream);
+  const long long units = (long long)p.B * p.Hkv * ((p.kv_tiles_used + 1) / 2);
+  return p.Hkv != p.H ? launch_pair_t<true, false>(tq64, tq, tk, tv, tdo64, tdo, p, units, sm_count, stream)
+                      : launch_pair_t<false, false>(tq64, tq, tk, tv, tdo64, tdo, p, units, sm_count, stream);
+}
+
+// The same over packed sequences, of at most `units` units: the maps of Q and dO
+// are of [channel, row of the tile, first row, head].
+cudaError_t launch_bwd_packed_pair(const CUtensorMap& tq64, const CUtensorMap& tq, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, const CUtensorMap& tdo64, const CUtensorMap& tdo,
+                                   const BwdParams& p, long long units, int sm_count, cudaStream_t stream) {
+  return p.Hkv != p.H ? launch_pair_t<true, true>(tq64, tq, tk, tv, tdo64, tdo, p, units, sm_count, stream)
+                      : launch_pair_t<false, true>(tq64, tq, tk, tv, tdo64, tdo, p, units, sm_count, stream);
 }
 
 }  // namespace fa

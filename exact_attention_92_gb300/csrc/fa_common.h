@@ -101,6 +101,18 @@ struct CombineParams {
   float* lse;
 };
 
+// A unit of the backward pass over packed sequences, for one head: a tile of a
+// sequence and the tiles of the other operand that it meets.
+struct BwdEntry {
+  int q_row, q_len;  // the sequence's first query row and its number
+  int k_row, k_len;  // ... and keys
+  int tile;          // dK/dV: key tile (at d = 128 the pair 2 tile, 2 tile + 1); dQ: query tile
+  int first;         // dK/dV: first query tile that sees it
+  int count;         // tiles of the other operand (dK/dV: for each query head); 0: the gradient rows are 0
+  int off;           // causal: query row i of the sequence sees its keys j <= i + off
+};
+static_assert(sizeof(BwdEntry) == 32, "read as two 16-byte words");
+
 struct BwdParams {
   int B, H;
   int Nq, Nk;                  // query / key rows per head
@@ -127,6 +139,13 @@ struct BwdParams {
   int group;                   // H / Hkv: query heads per key/value head
   unsigned int* status;
   unsigned long long timeout_ns;
+  // Packed sequences (B = 1; Nq and Nk are the rows of the tensors, lse and
+  // dvec [H, Nq]): the units, heaviest first, and their numbers (dK/dV, dQ), on the
+  // device; strides of the gradients' rows and heads in elements.
+  const BwdEntry* entries_kv;
+  const BwdEntry* entries_q;
+  const int* entry_counts;
+  long long dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
 };
 
 }  // namespace fa

@@ -16,71 +16,17 @@
 #include <cstring>
 
 #include "packed.h"
+#include "packed_host.h"
+#include "packed_seq.cuh"
 #include "sm103_primitives.cuh"
 
 namespace fa {
 
 using namespace dev;
 
-int internal_device_setup(unsigned int** status, int* sm_count);
-int internal_encode_tiled(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
-                          const uint32_t* box);
-cudaError_t internal_workspace(void** ptr, size_t bytes, cudaStream_t st);
-cudaError_t internal_timed_launch(int kernel, cudaStream_t stream, cudaError_t (*launch)(void*), void* ctx);
-unsigned long long internal_wait_timeout_ns();
 cudaError_t launch_packed_fwd(int d, const CUtensorMap* tm, const PackedFwd& p, cudaStream_t stream);
 
 namespace {
-
-constexpr int kPlanThreads = 1024;
-
-struct Seq {
-  int q, q_len, k, k_len;
-};
-
-// Sequence b; one whose bounds are out of order or out of the tensors is empty
-// (and reported).
-__device__ __forceinline__ Seq load_seq(const PackedSeqs& s, int b) {
-  const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1], k0 = s.cu_k[b], k1 = s.cu_k[b + 1];
-  bool bad = q0 < 0 || q1 < q0 || q1 > s.Tq || k0 < 0 || k1 < k0 || k1 > s.Tk;
-  int n = k1 - k0;
-  if (!bad && s.used_k != nullptr) {
-    const int used = s.used_k[b];
-    bad = used < 0 || used > n;
-    n = used;
-  }
-  if (bad) {
-    atomicCAS(s.status + 1, 0u, (unsigned int)FA_ERR_BAD_INDEX);
-    return Seq{0, 0, 0, 0};
-  }
-  return Seq{q0, q1 - q0, k0, n};
-}
-
-// Inclusive sum over the CTA; `warps` holds one value a warp.
-template <typename T>
-__device__ T scan_block(T v, T* warps) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
-  }
-  if (lane == 31) warps[w] = v;
-  __syncthreads();
-  if (w == 0) {
-    T x = warps[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const T y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    warps[lane] = x;
-  }
-  __syncthreads();
-  const T out = v + (w > 0 ? warps[w - 1] : T(0));
-  __syncthreads();
-  return out;
-}
 
 __device__ __forceinline__ bool before(const PackedStart& a, const PackedStart& b) {
   return a.unit < b.unit || (a.unit == b.unit && a.tile < b.tile);
@@ -127,13 +73,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
       if (e < over) {
         x = PackedEntry{first + e * block, min(block, rows - e * block), 0, 0, p.prefix_tiles, p.prefix_tiles, 0, 1};
       } else {
-        // The sequence: the last one that starts at or before this entry.
         const int i = e - over;
-        int lo = 0, hi = p.s.B;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) / 2;
-          if (p.seq_base[mid] <= i) lo = mid; else hi = mid;
-        }
+        const int lo = seq_of(p.seq_base, p.s.B, i);
         const Seq s = load_seq(p.s, lo);
         const int t0 = (i - p.seq_base[lo]) * block;
         x.q_row = s.q + t0;
@@ -340,8 +281,7 @@ namespace {
 
 using fa::PackedFwd;
 using fa::PackedPlan;
-
-bool head_dim(int d) { return d == 64 || d == 96 || d == 128; }
+using namespace fa::packed_host;
 
 struct Call {
   int d;
@@ -375,25 +315,6 @@ cudaError_t run_merge(void* ctx) {
   return c.d == 64 ? merge_t<64>(c) : c.d == 96 ? merge_t<96>(c) : merge_t<128>(c);
 }
 
-// Rows that a tensor map can say: strides above zero (but where there is only
-// one), multiples of 16 bytes, below 2^40.
-bool rows_ok(const fa_rows_t* r, long long rows, int heads) {
-  if (r == nullptr || r->ptr == nullptr || (reinterpret_cast<uintptr_t>(r->ptr) & 15u) != 0) return false;
-  const long long most = 1LL << 38;
-  if (rows > 1 && (r->row_stride <= 0 || r->row_stride % 8 != 0 || r->row_stride >= most)) return false;
-  if (heads > 1 && (r->head_stride <= 0 || r->head_stride % 8 != 0 || r->head_stride >= most)) return false;
-  return true;
-}
-// ... and that do not overlap, for outputs.
-bool rows_apart(const fa_rows_t* r, long long rows, int heads, int d) {
-  const long long rs = rows > 1 ? r->row_stride : 0, hs = heads > 1 ? r->head_stride : 0;
-  if (rows == 1) return heads == 1 || hs >= d;
-  if (heads == 1) return rs >= d;
-  return (hs >= d && rs >= (long double)(heads - 1) * hs + d) || (rs >= d && hs >= (long double)(rows - 1) * rs + d);
-}
-
-uint64_t step_bytes(int64_t stride, long long n) { return n > 1 ? (uint64_t)stride * 2 : 16; }
-
 // Queries: [channel, head of the group, token, key/value head].
 int encode_queries(CUtensorMap* m, const fa_rows_t* r, int rows, int heads, int group, int d, int box_heads, int box_rows) {
   const uint64_t rs = step_bytes(r->row_stride, rows), hs = step_bytes(r->head_stride, heads);
@@ -401,23 +322,6 @@ int encode_queries(CUtensorMap* m, const fa_rows_t* r, int rows, int heads, int 
   const uint64_t strides[3] = {hs, rs, hs * group};
   const uint32_t box[4] = {64, (uint32_t)box_heads, (uint32_t)box_rows, 1};
   return fa::internal_encode_tiled(m, r->ptr, 4, dims, strides, box);
-}
-
-// Keys and values of sequences: [channel, row of the tile, first row, head] (see packed.h).
-int encode_keys(CUtensorMap* m, const fa_rows_t* r, int rows, int heads, int d) {
-  const uint64_t rs = step_bytes(r->row_stride, rows), hs = step_bytes(r->head_stride, heads);
-  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)fa::kTileN, (uint64_t)rows, (uint64_t)heads};
-  const uint64_t strides[3] = {rs, rs, hs};
-  const uint32_t box[4] = {64, (uint32_t)fa::kTileN, 1, 1};
-  return fa::internal_encode_tiled(m, r->ptr, 4, dims, strides, box);
-}
-
-// The prefix: one sequence.
-int encode_prefix(CUtensorMap* m, const fa_rows_t* r, int rows, int heads, int d) {
-  const uint64_t dims[3] = {(uint64_t)d, (uint64_t)rows, (uint64_t)heads};
-  const uint64_t strides[2] = {step_bytes(r->row_stride, rows), step_bytes(r->head_stride, heads)};
-  const uint32_t box[3] = {64, 128, 1};
-  return fa::internal_encode_tiled(m, r->ptr, 3, dims, strides, box);
 }
 
 // Kernels are loaded at their first use; those of a head dim all before the
@@ -443,14 +347,11 @@ cudaError_t load(int d) {
   return e;
 }
 
-size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
-
 int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const fa_rows_t* k, const fa_rows_t* v,
             const fa_rows_t* o, float* lse, const int* cu_q, const int* cu_k, const int* used_k, int B, int P, int Tq,
             int Tk, int H, int Hkv, int d, int causal, float scale, void* stream) {
-  const long long most = 1 << 30;
-  if (B < 1 || Tq < 1 || Tk < 0 || P < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || B > most || Tq > most || Tk > most ||
-      P > most)
+  if (B < 1 || Tq < 1 || Tk < 0 || P < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || B > kMost || Tq > kMost || Tk > kMost ||
+      P > kMost)
     return FA_ERR_INVALID_ARG;
   if (!head_dim(d)) return FA_ERR_UNSUPPORTED;
   if (causal < FA_CAUSAL_NONE || causal > FA_CAUSAL_BOTTOM_RIGHT) return FA_ERR_INVALID_ARG;
@@ -458,9 +359,7 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   if (!rows_ok(q, Tq, H) || !rows_ok(o, Tq, H) || !rows_apart(o, Tq, H, d)) return FA_ERR_INVALID_ARG;
   if (Tk > 0 && (!rows_ok(k, Tk, Hkv) || !rows_ok(v, Tk, Hkv))) return FA_ERR_INVALID_ARG;
   if (P > 0 && (!rows_ok(kp, P, Hkv) || !rows_ok(vp, P, Hkv))) return FA_ERR_INVALID_ARG;
-  if (lse == nullptr || (reinterpret_cast<uintptr_t>(lse) & 15u) != 0) return FA_ERR_INVALID_ARG;
-  if (cu_q == nullptr || cu_k == nullptr ||
-      ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k) | reinterpret_cast<uintptr_t>(used_k)) & 3u))
+  if (!array_ok(lse, 16) || !array_ok(cu_q, 4) || !array_ok(cu_k, 4) || (used_k != nullptr && !array_ok(used_k, 4)))
     return FA_ERR_INVALID_ARG;
 
   Call c;
@@ -516,11 +415,11 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   const fa_rows_t* vv = Tk > 0 ? v : q;
   const int own_rows = Tk > 0 ? Tk : 1;
   if (encode_queries(&c.tm[0], q, Tq, H, p.group, d, p.group_heads, p.tile_tokens) ||
-      encode_keys(&c.tm[1], kk, own_rows, Hkv, d) || encode_keys(&c.tm[2], vv, own_rows, Hkv, d))
+      encode_tile(&c.tm[1], kk, own_rows, Hkv, d, 128) || encode_tile(&c.tm[2], vv, own_rows, Hkv, d, 128))
     return FA_ERR_CUDA;
   c.tm[3] = c.tm[1];
   c.tm[4] = c.tm[2];
-  if (P > 0 && (encode_prefix(&c.tm[3], kp, P, Hkv, d) || encode_prefix(&c.tm[4], vp, P, Hkv, d))) return FA_ERR_CUDA;
+  if (P > 0 && (encode_plain(&c.tm[3], kp, P, Hkv, d) || encode_plain(&c.tm[4], vp, P, Hkv, d))) return FA_ERR_CUDA;
 
   if (load(d) != cudaSuccess) {
     cudaGetLastError();
@@ -564,7 +463,7 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   p.o_row = Tq > 1 ? o->row_stride : 0;
   p.o_head = H > 1 ? o->head_stride : 0;
   p.lse = lse;
-  p.store32 = (reinterpret_cast<uintptr_t>(o->ptr) & 31u) == 0 && p.o_row % 16 == 0 && p.o_head % 16 == 0 ? 1 : 0;
+  p.store32 = aligned32(o->ptr, p.o_row, p.o_head) ? 1 : 0;
   p.status = status;
   p.timeout_ns = fa::internal_wait_timeout_ns();
   c.join_grid = (int)std::min<long long>(own_most * hgs * (d / 16), 8LL * sm_count);

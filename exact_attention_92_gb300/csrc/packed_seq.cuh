@@ -1,0 +1,73 @@
+// What the planning kernels of packed sequences share: a sequence's bounds, sums
+// over a CTA, and which sequence the i-th block is of.
+#pragma once
+
+#include "packed.h"
+#include "sm103_primitives.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+struct Seq {
+  int q, q_len, k, k_len;
+};
+
+// Sequence b; one whose bounds are out of order or out of the tensors is empty
+// (and reported).
+__device__ __forceinline__ Seq load_seq(const PackedSeqs& s, int b) {
+  const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1], k0 = s.cu_k[b], k1 = s.cu_k[b + 1];
+  bool bad = q0 < 0 || q1 < q0 || q1 > s.Tq || k0 < 0 || k1 < k0 || k1 > s.Tk;
+  int n = k1 - k0;
+  if (!bad && s.used_k != nullptr) {
+    const int used = s.used_k[b];
+    bad = used < 0 || used > n;
+    n = used;
+  }
+  if (bad) {
+    atomicCAS(s.status + 1, 0u, (unsigned int)FA_ERR_BAD_INDEX);
+    return Seq{0, 0, 0, 0};
+  }
+  return Seq{q0, q1 - q0, k0, n};
+}
+
+// Inclusive sum over the CTA; `warps` holds one value a warp.
+template <typename T>
+__device__ T scan_block(T v, T* warps) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) warps[w] = v;
+  __syncthreads();
+  if (w == 0) {
+    T x = warps[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    warps[lane] = x;
+  }
+  __syncthreads();
+  const T out = v + (w > 0 ? warps[w - 1] : T(0));
+  __syncthreads();
+  return out;
+}
+
+// The sequence of block i, with base[b] the first block of sequence b: the last
+// that starts at or before it.
+__device__ __forceinline__ int seq_of(const int* base, int B, int i) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (base[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace
+}  // namespace fa

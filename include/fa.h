@@ -529,6 +529,23 @@ int fa_packed_fwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, co
                   int causal, float scale, void* stream);
 
 /*
+ * Backward pass over packed sequences: the gradients of fa_packed_fwd (without
+ * used_k), by the kernels of fa_bwd_general ("FlashAttention V2 in depth",
+ * section 7).
+ *   q, k, v, o, lse : the forward's inputs and results;  dout : rows like o
+ *   dq : out, rows of Tq tokens and H heads;  dk, dv : out, of Tk and Hkv (rows
+ *        that do not overlap).  Every gradient row of a sequence is written, 0
+ *        where no key is seen or no query sees it; other rows are left as they
+ *        were.
+ * Other arguments as fa_packed_fwd, with Tk >= 1 and H <= 65535.  Workspace: D,
+ * H*Tq*4 bytes, and the list of units.  Bitwise reproducible from run to run; what
+ * is said there of NaN, bad bounds and graphs holds here too.
+ */
+int fa_packed_bwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, const fa_rows_t* o, const float* lse,
+                  const fa_rows_t* dout, const fa_rows_t* dq, const fa_rows_t* dk, const fa_rows_t* dv, const int* cu_q,
+                  const int* cu_k, int B, int Tq, int Tk, int H, int Hkv, int d, int causal, float scale, void* stream);
+
+/*
  * fa_packed_fwd where all sequences share P keys ahead of their own (a common
  * prompt): every query row sees all of k_prefix, v_prefix [P tokens, Hkv heads],
  * and its sequence's own keys as in fa_packed_fwd (`causal` is about these).  The

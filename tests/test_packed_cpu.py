@@ -46,6 +46,23 @@ def test_oracle_forward():
                         assert np.allclose(got["o"][cu_q[b] + i, h], want, atol=1e-13)
 
 
+def test_oracle_gradients_against_differences():
+    """Central differences of sum(dO * O)."""
+    r = np.random.default_rng(0)
+    q, k, v, do = (r.standard_normal((7, h, 5)) for h in (4, 2, 2, 4))
+    cu_q, cu_k = [0, 3, 7], [0, 2, 7]
+    for causal in ("none", "top_left", "bottom_right"):
+        want = oracle.backward(q, k, v, do, cu_q, cu_k, 0.4, causal)
+        for name, x in (("dq", q), ("dk", k), ("dv", v)):
+            for at in ((0, 0, 0), (2, 1, 3), (6, 1, 4), (4, 0, 2)):
+                keep, vals = x[at], []
+                for h in (1e-5, -1e-5):
+                    x[at] = keep + h
+                    vals.append((do * oracle.forward(q, k, v, cu_q, cu_k, 0.4, causal)["o"]).sum())
+                x[at] = keep
+                assert abs((vals[0] - vals[1]) / 2e-5 - want[name][at]) <= 1e-7 * (1 + abs(want[name][at]))
+
+
 def _rows(ptr, row=256, head=64):
     return ctypes.byref(_binding.Rows(ptr, 0, row, head))
 
@@ -88,6 +105,29 @@ def test_argument_errors_without_a_device(lib):
         for kw in ({}, dict(Tk=0, k=None, v=None), dict(o=_rows(0x40000, row=64, head=640)),
                    dict(H=1, Hkv=1, q=_rows(0x10000, 64, 0), o=_rows(0x40000, 64, 1)), dict(Tq=1, q=_rows(0x10000, 0, 64))):
             assert _fwd(lib, **kw) in (fa.FA_ERR_CUDA, uns), kw
+
+
+def _bwd(lib, **kw):
+    a = dict(q=_rows(0x10000), k=_rows(0x20000), v=_rows(0x30000), o=_rows(0x40000), lse=0x50000, dout=_rows(0x80000),
+             dq=_rows(0x90000), dk=_rows(0xa0000), dv=_rows(0xb0000), cu_q=0x60000, cu_k=0x70000, B=2, Tq=10, Tk=12, H=4,
+             Hkv=4, d=64, causal=0, scale=0.125)
+    a.update(kw)
+    return lib.fa_packed_bwd(*a.values(), None)
+
+
+def test_backward_argument_errors_without_a_device(lib):
+    inv, uns = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED
+    for kw in (dict(q=None), dict(k=_rows(0)), dict(v=None), dict(o=None), dict(lse=0), dict(dout=_rows(0x80001)),
+               dict(dq=None), dict(dk=_rows(0xa0008)), dict(dv=None), dict(cu_q=0), dict(cu_k=0x70001), dict(B=0), dict(Tq=0),
+               dict(Tk=0), dict(H=0), dict(Hkv=3), dict(H=65536, Hkv=65536), dict(causal=4), dict(scale=-1.0),
+               dict(dq=_rows(0x90000, row=128)), dict(dk=_rows(0xa0000, row=64)), dict(dv=_rows(0xb0000, row=0)),
+               dict(dout=_rows(0x80000, head=12)), dict(Tk=(1 << 30) + 1)):
+        assert _bwd(lib, **kw) == inv, kw
+    for d in (32, 256):
+        assert _bwd(lib, d=d) == uns
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        assert _bwd(lib) in (fa.FA_ERR_CUDA, uns)
 
 
 def test_binding_refuses_what_is_no_tensor(lib):
