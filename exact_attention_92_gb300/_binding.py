@@ -397,12 +397,12 @@ class _Kv4Ctypes:
                                    1.0 / math.sqrt(q.shape[3]) if scale is None else scale, stream)
 
 
-def _native_caller(torch_version):
-    """The native caller, or None: where it was not built, and, with a warning,
+def _native_caller(torch_version, module="._kv4_call", what="the 4-bit cache's calls"):
+    """A native caller, or None: where it was not built, and, with a warning,
     where it does not load or was compiled against the headers of another torch
     (whose tensors it would misread)."""
     try:
-        native = importlib.import_module("._kv4_call", __package__)
+        native = importlib.import_module(module, __package__)
     except ModuleNotFoundError:
         return None
     except ImportError as e:
@@ -413,7 +413,7 @@ def _native_caller(torch_version):
         if built == runs:
             return native
         why = f"compiled against torch {built or '?'}, this is {runs}"
-    warnings.warn(f"the 4-bit cache's calls go through ctypes ({why}): run the build again")
+    warnings.warn(f"{what} go through ctypes ({why}): run the build again")
     return None
 
 
@@ -598,6 +598,41 @@ def _check_array(name, t, dtype, shape):
         raise ValueError(f"{name} is on {t.device}, not on the current CUDA device (use torch.cuda.device)")
 
 
+# Rotary positions and packed sequences are called once a layer, in decoding
+# too: their calls go through a native caller (_packed_call,
+# csrc/packed_call.cpp).  Where it is not there, or a tensor is not as it
+# should be (-1), the checks here say what is wrong, and ctypes makes the call.
+
+_packed = None
+
+
+def _packed_caller():
+    """The native caller, or False; looked for at the first call."""
+    global _packed
+    if _packed is None:
+        import torch
+
+        lib = load()
+        native = _native_caller(torch.__version__, "._packed_call", "the calls on packed sequences") or False
+        if native:
+            native.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                          for name in ("fa_rope", "fa_packed_fwd", "fa_prefix_fwd", "fa_packed_bwd")))
+        _packed = native
+    return _packed
+
+
+def _done(status, what):
+    """Whether the native caller made the call; raises for the library's refusals."""
+    if status > 0:
+        raise FaError(status, what)
+    return status == FA_OK
+
+
+def _code_of(causal):
+    code = _CAUSAL_CODES.get(causal) if isinstance(causal, (str, bool, int)) else None
+    return _causal_code(causal) if code is None else code
+
+
 def fa_rope_phases(inv_freq):
     """C fa_rope_phases: frequencies (radians a position, a sequence of
     floats) as 64-bit fractions of a turn, a list of ints below 2^64."""
@@ -615,6 +650,10 @@ def fa_rope(q, k, q_out, k_out, phases, positions=None, start=None, interleaved=
     any strides with contiguous channels.  phases int64 [rot / 2] from
     rope_phases; positions int32 [B, N] ([tokens]) or start int32 [B] ([1]).
     k and k_out may be None; inverse=True turns gradients back."""
+    native = _packed_caller() if _packed is None else _packed
+    if native and _done(native.rope(q, k, q_out, k_out, phases, positions, start, interleaved, mscale, inverse,
+                                    stream if stream is None else _handle(stream)), "fa_rope"):
+        return
     import torch
 
     dims = getattr(q, "dim", lambda: 4)()
@@ -646,7 +685,12 @@ def fa_rope(q, k, q_out, k_out, phases, positions=None, start=None, interleaved=
     _check(st, "fa_rope")
 
 
-def _packed_fwd(what, q, prefix, k, v, o, lse, cu_q, cu_k, used_k, causal, scale, stream):
+def _packed_fwd(what, q, k_prefix, v_prefix, k, v, o, lse, cu_q, cu_k, used_k, causal, scale, stream):
+    native = _packed_caller() if _packed is None else _packed
+    if native and (k_prefix is not None or what == "fa_packed_fwd") and _done(
+            native.forward(q, k_prefix, v_prefix, k, v, o, lse, cu_q, cu_k, used_k, _code_of(causal), scale,
+                           stream if stream is None else _handle(stream)), what):
+        return
     import torch
 
     _check_rows("q", q, (None, None, None))
@@ -664,11 +708,11 @@ def _packed_fwd(what, q, prefix, k, v, o, lse, cu_q, cu_k, used_k, causal, scale
     if used_k is not None:
         _check_array("used_k", used_k, torch.int32, (B,))
     tensors, P = [q, k, v, o], ()
-    if prefix is not None:
-        _check_rows("k_prefix", prefix[0], (None, Hkv, d))
-        _check_rows("v_prefix", prefix[1], tuple(prefix[0].shape))
-        tensors[1:1] = prefix
-        P = (prefix[0].shape[0],)
+    if what == "fa_prefix_fwd":
+        _check_rows("k_prefix", k_prefix, (None, Hkv, d))
+        _check_rows("v_prefix", v_prefix, tuple(k_prefix.shape))
+        tensors[1:1] = [k_prefix, v_prefix]
+        P = (k_prefix.shape[0],)
     rows = [ctypes.byref(_rows_of(t)) for t in tensors]
     st = getattr(load(), what)(*rows, _ptr(lse), _ptr(cu_q), _ptr(cu_k), None if used_k is None else _ptr(used_k), B,
                                *P, Tq, Tk, H, Hkv, d, _causal_code(causal), _scale(scale, d),
@@ -681,12 +725,16 @@ def fa_packed_fwd(q, k, v, o, lse, cu_q, cu_k, used_k=None, causal=False, scale=
     k, v [Tk, Hkv, d] of any strides with contiguous channels, lse fp32 [H,
     Tq]; cu_q, cu_k int32 [B + 1], used_k int32 [B] or None; causal as
     fa_fwd_general, within each sequence."""
-    _packed_fwd("fa_packed_fwd", q, None, k, v, o, lse, cu_q, cu_k, used_k, causal, scale, stream)
+    _packed_fwd("fa_packed_fwd", q, None, None, k, v, o, lse, cu_q, cu_k, used_k, causal, scale, stream)
 
 
 def fa_packed_bwd(q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, causal=False, scale=None, stream=None):
     """C fa_packed_bwd: gradients of fa_packed_fwd (without used_k); dout, dq
     have the shape of q, dk, dv that of k."""
+    native = _packed_caller() if _packed is None else _packed
+    if native and _done(native.backward(q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, _code_of(causal), scale,
+                                        stream if stream is None else _handle(stream)), "fa_packed_bwd"):
+        return
     import torch
 
     _check_rows("q", q, (None, None, None))
@@ -712,7 +760,7 @@ def fa_packed_bwd(q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, causal=False, s
 def fa_prefix_fwd(q, k_prefix, v_prefix, k, v, o, lse, cu_q, cu_k, used_k=None, causal=False, scale=None, stream=None):
     """C fa_prefix_fwd: fa_packed_fwd where every query row also sees all of
     k_prefix, v_prefix [P, Hkv, d]."""
-    _packed_fwd("fa_prefix_fwd", q, (k_prefix, v_prefix), k, v, o, lse, cu_q, cu_k, used_k, causal, scale, stream)
+    _packed_fwd("fa_prefix_fwd", q, k_prefix, v_prefix, k, v, o, lse, cu_q, cu_k, used_k, causal, scale, stream)
 
 
 def fa_poll_status(stream=None):

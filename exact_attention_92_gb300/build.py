@@ -26,6 +26,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 CALL_SOURCE = os.path.join(CSRC, "kv4_call.cpp")
 CALL = os.path.join(PKG, "_kv4_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+PACKED_CALL_SOURCE = os.path.join(CSRC, "packed_call.cpp")
+PACKED_CALL = os.path.join(PKG, "_packed_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd256.cu", "fa_bwd.cu", "fa_bwd_pair.cu", "fa_bwd256.cu", "fa_noalloc.cu",
            "fa_kv4.cu", "fa_kv4_move.cu", "fa_kv4_fwd.cu", "fa_rope.cu", "fa_packed.cu", "fa_packed_fwd.cu",
@@ -97,11 +99,20 @@ def _call_key(torch_dir: str) -> str:
 
 
 def build_call(force: bool = False) -> str | None:
-    """Compile the native caller of the 4-bit cache's entry points (CALL, against
-    torch's and Python's headers: again when those are other ones); None where
-    torch with CUDA is not installed, and, with a warning, where it does not
-    compile.  It holds no device code: without it the binding makes the same
-    calls through ctypes."""
+    """Compile the native caller of the 4-bit cache's entry points (CALL)."""
+    return _build_caller(CALL_SOURCE, CALL, "the 4-bit cache's calls", force)
+
+
+def build_packed_call(force: bool = False) -> str | None:
+    """Compile the native caller of rotary positions and packed sequences (PACKED_CALL)."""
+    return _build_caller(PACKED_CALL_SOURCE, PACKED_CALL, "the calls on packed sequences", force)
+
+
+def _build_caller(source: str, target: str, what: str, force: bool) -> str | None:
+    """Compile a native caller (against torch's and Python's headers: again when
+    those are other ones); None where torch with CUDA is not installed, and,
+    with a warning, where it does not compile.  It holds no device code: without
+    it the binding makes the same calls through ctypes."""
     import importlib.util
 
     spec = importlib.util.find_spec("torch")  # found, not imported
@@ -111,18 +122,18 @@ def build_call(force: bool = False) -> str | None:
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     if not all(os.path.exists(os.path.join(lib, f)) for f in ("libc10_cuda.so", "libtorch_python.so")):
         return None
-    key, key_file = _call_key(torch_dir), CALL + ".key"
-    if not force and os.path.exists(CALL) and os.path.exists(key_file) and os.path.getmtime(CALL) >= max(
-            os.path.getmtime(CALL_SOURCE), os.path.getmtime(__file__)):
+    key, key_file = _call_key(torch_dir), target + ".key"
+    if not force and os.path.exists(target) and os.path.exists(key_file) and os.path.getmtime(target) >= max(
+            os.path.getmtime(source), os.path.getmtime(os.path.join(INCLUDE, "fa.h")), os.path.getmtime(__file__)):
         with open(key_file, encoding="utf-8") as fh:
             if fh.read() == key:
-                return CALL
+                return target
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
-    tmp = CALL + ".tmp"
+    tmp = target + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-isystem", inc, "-isystem",
-           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-I",
-           sysconfig.get_paths()["include"], CALL_SOURCE, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"], source, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}",
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -130,23 +141,24 @@ def build_call(force: bool = False) -> str | None:
     except OSError as e:
         r, said = None, str(e)
     if r is None or r.returncode != 0:
-        if os.path.exists(CALL):
-            os.remove(CALL)  # of an older source, or against other headers
-        warnings.warn(f"the 4-bit cache's calls go through ctypes: {cxx} failed on {CALL_SOURCE}:\n{said}")
+        if os.path.exists(target):
+            os.remove(target)  # of an older source, or against other headers
+        warnings.warn(f"{what} go through ctypes: {cxx} failed on {source}:\n{said}")
         return None
-    os.replace(tmp, CALL)
+    os.replace(tmp, target)
     with open(key_file, "w", encoding="utf-8") as fh:
         fh.write(key)
-    return CALL
+    return target
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile and link libfa.so if any source is newer than it, and the native
-    caller (build_call); return libfa.so's path."""
-    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
-        call = ex.submit(build_call, force)
+    callers (build_call, build_packed_call); return libfa.so's path."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=2) as ex:
+        calls = [ex.submit(build_call, force), ex.submit(build_packed_call, force)]
         path = _build_lib(force, verbose, ptxas_verbose)
-        call.result()
+        for call in calls:
+            call.result()
     return path
 
 
