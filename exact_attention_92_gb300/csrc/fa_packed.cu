@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
   __shared__ long long s_carry;
   const int tid = threadIdx.x;
   pdl_trigger();
+  pdl_wait();
   const int block = 2 * p.tile_tokens;
   // Entries of the sequences: [seq_base[b], seq_base[b + 1]) after those of the prefix.
   int own = 0;
@@ -167,7 +168,8 @@ struct Merge {
 
 // The parts of `unit` in slots: its first CTA is c (which holds its tile 0).
 template <int D>
-__device__ __forceinline__ void add_slots(const PackedFwd& p, Merge& m, int unit, int c, int row, int c16) {
+__device__ __forceinline__ void add_slots(const PackedFwd& p, const PackedStart* starts, Merge& m, int unit, int c, int row,
+                                          int c16) {
   int slot = 2 * c + 1;
   while (true) {
     const float4* o = reinterpret_cast<const float4*>(p.o_slot) + ((size_t)slot * (D / 4) + 4 * c16) * kSlotRows + row;
@@ -175,8 +177,8 @@ __device__ __forceinline__ void add_slots(const PackedFwd& p, Merge& m, int unit
     // The next CTA that starts within the unit and has some of it.
     do {
       ++c;
-      if (c >= p.grid || p.starts[c].unit != unit || p.starts[c].tile == 0) return;
-    } while (p.starts[c + 1].unit == unit && p.starts[c + 1].tile == p.starts[c].tile);
+      if (c >= p.grid || starts[c].unit != unit || starts[c].tile == 0) return;
+    } while (starts[c + 1].unit == unit && starts[c + 1].tile == starts[c].tile);
     slot = 2 * c;
   }
 }
@@ -222,50 +224,68 @@ __global__ void __launch_bounds__(256) fa_packed_merge_kernel(const PackedFwd p)
     int token, head;
     if (!row_of(p, e, hg, row, &token, &head)) continue;
     Merge m;
-    add_slots<D>(p, m, s.unit, c - 1, row, c16);
+    add_slots<D>(p, p.starts, m, s.unit, c - 1, row, c16);
     write_row<D>(p, m, token, head, c16);
   }
 }
 
+// The last CTA that starts at or before the unit's first tile.
+__device__ __forceinline__ int first_cta(const PackedStart* starts, int grid, int unit) {
+  const PackedStart want{unit, 0};
+  int lo = 0, hi = grid;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (before(want, starts[mid])) hi = mid; else lo = mid;
+  }
+  return lo;
+}
+
 // All rows of the sequences, each from its part over the prefix and its part
-// over the sequence's own keys (one row each where the unit was not cut).
+// over the sequence's own keys (one row each where the unit was not cut).  A
+// thread takes 16 channels of a row; rows are taken token by token, so that the
+// threads of a CTA are of few units and find them in the same places.
+constexpr int kJoinStarts = 320;  // CTAs' starts kept in shared memory
 template <int D>
-__global__ void __launch_bounds__(256) fa_packed_join_kernel(const PackedFwd p, const int* cu_q, int B) {
+__global__ void __launch_bounds__(256) fa_packed_join_kernel(const PackedFwd p) {
+  __shared__ PackedStart s_starts[kJoinStarts];
   pdl_wait();
+  const PackedStart* starts = p.starts;
+  if (p.grid < kJoinStarts) {
+    for (int i = threadIdx.x; i <= p.grid; i += 256) s_starts[i] = p.starts[i];
+    starts = s_starts;
+  }
   const int entries = p.header[0], over = p.header[1];
-  const int hgs = p.Hkv * p.chunks;
+  __syncthreads();
+  if (over == 0 || entries == over) return;
   const int block = 2 * p.tile_tokens;
-  // A task is 16 channels of one row of an own block.
-  constexpr int kPer = kSlotRows * (D / 16) / 256;  // CTAs' passes over a unit
-  const long long units = (long long)(entries - over) * hgs * kPer;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int pass = (int)(u % kPer);
-    const long long v = u / kPer;
-    const int e = over + (int)(v % (entries - over)), hg = (int)(v / (entries - over));
-    const PackedEntry x = p.entries[e];
-    const int i = pass * 256 + threadIdx.x;
-    const int c16 = i % (D / 16), row = i / (D / 16);
-    int token, head;
-    if (!row_of(p, x, hg, row, &token, &head)) continue;
-    // The row's place in the prefix's blocks, which start at the first of them.
-    // (Sequences out of order may have rows that these do not cover.)
-    const PackedEntry last = p.entries[over > 0 ? over - 1 : 0];
-    const int at = token - p.entries[0].q_row;
-    const bool covered = over > 0 && at >= 0 && token < last.q_row + last.q_len;
-    const int pe = covered ? at / block : 0, tok = covered ? at - pe * block : 0;
-    const int prow = tok / p.tile_tokens * kTileM + tok % p.tile_tokens * p.group_heads + row % kTileM % p.group_heads;
+  const int q0 = p.entries[0].q_row;
+  const int rows = p.entries[over - 1].q_row + p.entries[over - 1].q_len - q0;
+  constexpr int kPer = D / 16;
+  const long long tasks = (long long)rows * p.H * kPer;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < tasks; i += 256LL * gridDim.x) {
+    const int c16 = (int)(i % kPer);
+    const long long r = i / kPer;
+    const int at = (int)(r / p.H), head = (int)(r - (long long)at * p.H);
+    const int token = q0 + at;
+    // The own block: the last that starts at or before the token.  (A token of no
+    // sequence is behind that block's last.)
+    int lo = over, hi = entries;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (p.entries[mid].q_row <= token) lo = mid; else hi = mid;
+    }
+    const int tok = token - p.entries[lo].q_row;
+    if (tok < 0 || tok >= p.entries[lo].q_len) continue;
+    const int hk = head / p.group, g = head - hk * p.group;
+    const int hg = hk * p.chunks + g / p.group_heads, gh = g % p.group_heads;
+    const int pe = at / block, ptok = at - pe * block;
     Merge m;
-    for (int part = covered ? 0 : 1; part < 2; ++part) {
-      const int unit = hg * entries + (part ? e : pe);
-      const PackedStart want{unit, 0};
-      int lo = 0, hi = p.grid;  // the last CTA that starts at or before the unit
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (before(want, p.starts[mid])) hi = mid; else lo = mid;
-      }
-      const PackedStart nxt = p.starts[lo + 1];
-      if (nxt.unit == unit && nxt.tile > 0) {
-        add_slots<D>(p, m, unit, lo, part ? row : prow, c16);
+    for (int part = 0; part < 2; ++part) {
+      const int unit = hg * entries + (part ? lo : pe), t = part ? tok : ptok;
+      const int c = first_cta(starts, p.grid, unit);
+      if (starts[c + 1].unit == unit && starts[c + 1].tile > 0) {
+        const int row = t / p.tile_tokens * kTileM + t % p.tile_tokens * p.group_heads + gh;
+        add_slots<D>(p, starts, m, unit, c, row, c16);
       } else {
         const float4* o = reinterpret_cast<const float4*>(p.o_part + (((size_t)part * p.Tq + token) * p.H + head) * D) + 4 * c16;
         m.add(p.lse_part[((size_t)part * p.H + head) * p.Tq + token], o, 1);
@@ -288,17 +308,13 @@ struct Call {
   PackedPlan plan;
   PackedFwd p;
   CUtensorMap tm[5];
-  int B, join_grid;
+  int join_grid;
   cudaStream_t st;
 };
 
-// The first kernel of a call writes workspace as soon as it starts.  It is
-// launched in stream order proper: a programmatic launch would be ordered behind
-// the kernel ahead of it, but not behind the allocation in between.
 cudaError_t run_plan(void* ctx) {
   const Call& c = *static_cast<const Call*>(ctx);
-  fa::fa_packed_plan_kernel<<<1, fa::kPlanThreads, 0, c.st>>>(c.plan);
-  return cudaGetLastError();
+  return fa::launch_pdl(fa::fa_packed_plan_kernel, dim3(1), dim3(fa::kPlanThreads), 0, c.st, c.plan);
 }
 cudaError_t run_fwd(void* ctx) {
   const Call& c = *static_cast<const Call*>(ctx);
@@ -307,7 +323,7 @@ cudaError_t run_fwd(void* ctx) {
 template <int D>
 cudaError_t merge_t(const Call& c) {
   if (c.p.shared)
-    return fa::launch_pdl(fa::fa_packed_join_kernel<D>, dim3(c.join_grid), dim3(256), 0, c.st, c.p, c.plan.s.cu_q, c.B);
+    return fa::launch_pdl(fa::fa_packed_join_kernel<D>, dim3(c.join_grid), dim3(256), 0, c.st, c.p);
   return fa::launch_pdl(fa::fa_packed_merge_kernel<D>, dim3(c.p.grid - 1, D / 16), dim3(256), 0, c.st, c.p);
 }
 cudaError_t run_merge(void* ctx) {
@@ -409,7 +425,6 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   const size_t bytes = n_entries + n_cum + n_base + n_starts + up(slot_rows * (d + 1) * 4) + part_rows * (d + 1) * 4;
   c.st = static_cast<cudaStream_t>(stream);
   c.d = d;
-  c.B = B;
 
   const fa_rows_t* kk = Tk > 0 ? k : q;  // never read without keys
   const fa_rows_t* vv = Tk > 0 ? v : q;
@@ -466,7 +481,7 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   p.store32 = aligned32(o->ptr, p.o_row, p.o_head) ? 1 : 0;
   p.status = status;
   p.timeout_ns = fa::internal_wait_timeout_ns();
-  c.join_grid = (int)std::min<long long>(own_most * hgs * (d / 16), 8LL * sm_count);
+  c.join_grid = (int)std::min<long long>(((long long)Tq * H * (d / 16) + 255) / 256, 8LL * sm_count);
 
   cudaError_t ce = fa::internal_timed_launch(FA_KERNEL_PACKED_PLAN, c.st, run_plan, &c);
   if (ce == cudaSuccess) ce = fa::internal_timed_launch(FA_KERNEL_PACKED_FWD, c.st, run_fwd, &c);

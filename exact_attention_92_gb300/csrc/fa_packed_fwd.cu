@@ -43,7 +43,7 @@ struct Cfg {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTileBytes;
-  // Hand-over of the second warpgroup: 32 columns of 128 rows, [warp][column / 4][lane] float4, and (m, l, l_bf).
+  // Hand-over of the second warpgroup: 16 KB of O, [warp][column / 4][lane] float4, and (m, l, l_bf) of 128 rows.
   static constexpr int kOffEx = kOffKV + kStages * kTileBytes;
   static constexpr int kOffStat = kOffEx + 128 * 32 * 4;
   static constexpr int kOffBar = kOffStat + 3 * 128 * 4;
@@ -73,7 +73,7 @@ struct Walk {
   const PackedFwd& p;
   PackedStart s0, s1;
   int entries;
-  int u, u_last, at, hg;
+  int u, u_last, at, hk, chunk;
   PackedEntry next;
 
   __device__ __forceinline__ static PackedEntry fetch(const PackedEntry* e) {
@@ -88,19 +88,19 @@ struct Walk {
     u = s0.unit;
     u_last = s1.tile > 0 ? s1.unit : s1.unit - 1;
     if (s0.unit == s1.unit && s0.tile == s1.tile) u_last = u - 1;
-    hg = 0;
-    at = 0;
+    hk = chunk = at = 0;
     if (u <= u_last) {
-      hg = u / entries;
+      const int hg = u / entries;
       at = u - hg * entries;
+      hk = hg / p.chunks;
+      chunk = hg - hk * p.chunks;
       next = fetch(p.entries + at);
     }
   }
   __device__ __forceinline__ bool get(Piece& w) {
     if (u > u_last) return false;
     w.e = next;
-    const int chunk = hg % p.chunks;
-    w.hk = hg / p.chunks;
+    w.hk = hk;
     w.g0 = chunk * p.group_heads;
     w.lo = u == s0.unit ? s0.tile : 0;
     w.hi = u == s1.unit ? s1.tile : w.e.tiles;
@@ -109,7 +109,10 @@ struct Walk {
     ++u;
     if (++at == entries) {
       at = 0;
-      ++hg;
+      if (++chunk == p.chunks) {
+        chunk = 0;
+        ++hk;
+      }
     }
     if (u <= u_last) next = fetch(p.entries + at);
     if (w.dual) {
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(384, 1)
     const int gh = r_in_tile - tok * p.group_heads;  // query head within the group's run
     const int warp_tok = 32 * wq / p.group_heads;    // the warp's first token
     const float sl2 = p.scale_log2;
-    float4* ex = reinterpret_cast<float4*>(smem + C::kOffEx) + wq * 8 * 32;
+    float4* const ex0 = reinterpret_cast<float4*>(smem + C::kOffEx);
     float* stat = reinterpret_cast<float*>(smem + C::kOffStat);
     uint32_t sc = 0, oc = 0, xc = 0;
     bool ok = true;
@@ -453,9 +456,17 @@ __global__ void __launch_bounds__(384, 1)
         const int kv0 = row - skip;
         if (skip > 0 || kv0 + kTileN > len || (causal && kv0 + kTileN > w.e.pos + first + warp_tok + 1)) {
           const int lim = (causal ? min(len, w.e.pos + first + tok + 1) : len) - kv0;
+          // A word of bits for 32 columns, then one select a column (compares of
+          // every column took 2500 cycles where this takes 700).
 #pragma unroll
-          for (int c = 0; c < kTileN; ++c)
-            if (c >= lim || c < skip) x[c] = -INFINITY;
+          for (int h = 0; h < kTileN / 32; ++h) {
+            const int n = lim - 32 * h, z = skip - 32 * h;
+            uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+            if (z > 0) see &= z >= 32 ? 0u : ~0u << z;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(see & (1u << c))) x[32 * h + c] = -INFINITY;
+          }
         }
         float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
 #pragma unroll
@@ -530,25 +541,41 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive_warp(&p_full[t]);
       }
       if (!ok) break;
+      // ---- the rows' results.  What does not need O is worked out while the last
+      // product runs; then all of the row is read at once.
+      const bool joined = w.dual && w.n1 > 0;                // the second warpgroup hands over
+      const int live_warps = (here * p.group_heads + 31) / 32;
+      // Groups of columns handed over at a time: the four warps' room is for all who have rows.
+      const int group = live_warps <= 1 ? 4 : live_warps == 2 ? 2 : 1;
+      float4* ex = ex0 + wq * group * 256;
+      const int sl = 2 * (int)blockIdx.x + (w.lo > 0 ? 0 : 1);
+      const int slot_row = (w.dual ? 0 : kTileM * t) + r_in_tile;
+      uint8_t* orow = reinterpret_cast<uint8_t*>(p.o) + ((long long)token * p.o_row + (long long)head * p.o_head) * 2;
       if (steps > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(&o_full[t], oc & 1, ctl, kWaitOFull));
         ++oc;
         if (!ok) break;
         tc_fence_after();
       }
-      if (!live) continue;
-      // ---- both warpgroups on one tile: the second hands over
-      const bool joined = w.dual && w.n1 > 0;
+      if (!live || (!mine && !joined)) continue;
+      uint32_t o[D];
+      if (steps > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) tmem_ld32(tO + 32 * c, o + 32 * c);
+        tmem_ld_wait<D>(o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < D; ++i) o[i] = 0u;
+      }
       if (!mine) {
-        if (!joined) continue;
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * c, o);
-          tmem_ld_wait<32>(o);
-          ok = __all_sync(0xffffffffu, mbar_wait(&ex_free[wq], (xc & 1) ^ 1, ctl, kWaitPFull));
-          if (!ok) break;
-          ++xc;
+          const int place = c & (group - 1);
+          if (place == 0) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&ex_free[wq], (xc & 1) ^ 1, ctl, kWaitPFull));
+            ++xc;
+          }
+          if (!ok) continue;
           if (c == 0) {
             stat[r_in_tile] = m_ref;
             stat[128 + r_in_tile] = l;
@@ -556,40 +583,23 @@ __global__ void __launch_bounds__(384, 1)
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            ex[i * 32 + lane] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                            __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-          mbar_arrive_warp(&ex_full[wq]);
+            ex[(8 * place + i) * 32 + lane] =
+                make_float4(__uint_as_float(o[32 * c + 4 * i]), __uint_as_float(o[32 * c + 4 * i + 1]),
+                            __uint_as_float(o[32 * c + 4 * i + 2]), __uint_as_float(o[32 * c + 4 * i + 3]));
+          if (place == group - 1 || c == D / 32 - 1) mbar_arrive_warp(&ex_full[wq]);
         }
         continue;
       }
-      // ---- write the rows.  A row that saw no key has l = 0: O = 0, L = -inf.
-      float a0 = 1.f, a1 = 0.f;
-      float inv_l = 0.f, lse = -INFINITY;
-      auto finish = [&]() {
-        inv_l = l_bf > 0.f ? 1.0f / l_bf : 0.f;
-        lse = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
-      };
-      if (!joined) finish();
-      const bool slot = w.cut;
-      const int sl = 2 * (int)blockIdx.x + (w.lo > 0 ? 0 : 1);
-      const int slot_row = (w.dual ? 0 : kTileM * t) + r_in_tile;
-      uint8_t* orow = reinterpret_cast<uint8_t*>(p.o) + ((long long)token * p.o_row + (long long)head * p.o_head) * 2;
-      float* prow = p.o_part + (((size_t)(1 - w.e.kind) * p.Tq + token) * p.H + head) * D;
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (steps > 0) {
-          tmem_ld32(tO + 32 * c, o);
-          tmem_ld_wait<32>(o);
-        } else {
+      if (joined) {
+        float a0 = 1.f, a1 = 0.f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0u;
-        }
-        float v[32];
-        if (joined) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&ex_full[wq], xc & 1, ctl, kWaitPFull));
-          if (!ok) break;
-          ++xc;
+        for (int c = 0; c < D / 32; ++c) {
+          const int place = c & (group - 1);
+          if (place == 0) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&ex_full[wq], xc & 1, ctl, kWaitPFull));
+            ++xc;
+          }
+          if (!ok) continue;
           if (c == 0) {
             const float m1 = stat[r_in_tile], l1 = stat[128 + r_in_tile], b1 = stat[256 + r_in_tile];
             const float m = fmaxf(m_ref, m1);
@@ -598,48 +608,67 @@ __global__ void __launch_bounds__(384, 1)
             l = l * a0 + l1 * a1;
             l_bf = l_bf * a0 + b1 * a1;
             m_ref = m;
-            finish();
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float4 y = ex[i * 32 + lane];
-            v[4 * i] = (__uint_as_float(o[4 * i]) * a0 + y.x * a1) * inv_l;
-            v[4 * i + 1] = (__uint_as_float(o[4 * i + 1]) * a0 + y.y * a1) * inv_l;
-            v[4 * i + 2] = (__uint_as_float(o[4 * i + 2]) * a0 + y.z * a1) * inv_l;
-            v[4 * i + 3] = (__uint_as_float(o[4 * i + 3]) * a0 + y.w * a1) * inv_l;
+            const float4 y = ex[(8 * place + i) * 32 + lane];
+            uint32_t* x = o + 32 * c + 4 * i;
+            x[0] = __float_as_uint(__uint_as_float(x[0]) * a0 + y.x * a1);
+            x[1] = __float_as_uint(__uint_as_float(x[1]) * a0 + y.y * a1);
+            x[2] = __float_as_uint(__uint_as_float(x[2]) * a0 + y.z * a1);
+            x[3] = __float_as_uint(__uint_as_float(x[3]) * a0 + y.w * a1);
           }
-          mbar_arrive_warp(&ex_free[wq]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * inv_l;
+          if (place == group - 1 || c == D / 32 - 1) mbar_arrive_warp(&ex_free[wq]);
         }
-        if (slot) {
-          float4* dst = reinterpret_cast<float4*>(p.o_slot) + ((size_t)sl * (D / 4) + 8 * c) * kSlotRows + slot_row;
-          if (row_ok) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i * kSlotRows] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-        } else if (p.shared) {
-          uint32_t wv[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) wv[i] = __float_as_uint(v[i]);
-          store_rows_to<4>(reinterpret_cast<uint8_t*>(prow + 32 * c), row_ok, wv, true);
-        } else {
-          uint32_t wv[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) wv[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-          store_rows_to<2>(orow + 64 * c, row_ok, wv, p.store32 != 0);
-        }
+        if (!ok) break;
       }
-      if (!ok) break;
-      if (row_ok) {
-        if (slot)
-          p.lse_slot[(size_t)sl * kSlotRows + slot_row] = lse;
-        else if (p.shared)
-          p.lse_part[((size_t)(1 - w.e.kind) * p.H + head) * p.Tq + token] = lse;
-        else
+      // A row that saw no key has l = 0: O = 0, L = -inf.
+      const float inv_l = l_bf > 0.f ? 1.0f / l_bf : 0.f;
+      const float lse = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
+      const float2 il = make_float2(inv_l, inv_l);
+      if (!w.cut && !p.shared) {
+        // Each lane stores its own row, whole sectors at a time (an exchange between
+        // lanes first, so that a store takes whole lines, cost 3300 cycles a unit).
+        if (row_ok) {
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i) {
+            const float2 a = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il);
+            o[i] = pack_bf16(a.x, a.y);
+          }
+          if (p.store32) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) st_global_v8(orow + 32 * i, o + 8 * i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+              reinterpret_cast<uint4*>(orow)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
           p.lse[(size_t)head * p.Tq + token] = lse;
+        }
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i) {
+        const float2 a = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il);
+        o[2 * i] = __float_as_uint(a.x);
+        o[2 * i + 1] = __float_as_uint(a.y);
+      }
+      if (w.cut) {
+        float4* dst = reinterpret_cast<float4*>(p.o_slot) + (size_t)sl * (D / 4) * kSlotRows + slot_row;
+        if (row_ok) {
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i)
+            dst[i * kSlotRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                             __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          p.lse_slot[(size_t)sl * kSlotRows + slot_row] = lse;
+        }
+      } else {
+        float* prow = p.o_part + (((size_t)(1 - w.e.kind) * p.Tq + token) * p.H + head) * D;
+        if (row_ok) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) st_global_v8(prow + 8 * i, o + 8 * i);
+          p.lse_part[((size_t)(1 - w.e.kind) * p.H + head) * p.Tq + token] = lse;
+        }
       }
     }
     __syncwarp();

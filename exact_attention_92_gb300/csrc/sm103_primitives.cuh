@@ -385,43 +385,6 @@ __device__ __forceinline__ void store_rows(uint8_t* row_ptr, size_t stride, int 
   }
 }
 
-// The same for rows anywhere: each lane has its row's address and whether the
-// row is written.
-template <int U>
-__device__ __forceinline__ void store_rows_to(uint8_t* row_ptr, bool write, uint32_t* w, bool store32) {
-  const int lane = threadIdx.x & 31, l = lane & (U - 1);
-#pragma unroll
-  for (int b = 1; b < U; b <<= 1) {
-    const bool hi = (l & b) != 0;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u & b) continue;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t lo_v = w[8 * u + k], hi_v = w[8 * (u | b) + k];
-        const uint32_t recv = __shfl_xor_sync(0xffffffffu, hi ? lo_v : hi_v, b);
-        w[8 * u + k] = hi ? recv : lo_v;
-        w[8 * (u | b) + k] = hi ? hi_v : recv;
-      }
-    }
-  }
-  const unsigned rows = __ballot_sync(0xffffffffu, write);
-#pragma unroll
-  for (int s = 0; s < U; ++s) {
-    const int from = lane - l + s;
-    uint8_t* dst = reinterpret_cast<uint8_t*>(
-        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row_ptr), from)) + 32 * l;
-    if ((rows >> from) & 1u) {
-      if (store32) {
-        st_global_v8(dst, w + 8 * s);
-      } else {
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[8 * s], w[8 * s + 1], w[8 * s + 2], w[8 * s + 3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[8 * s + 4], w[8 * s + 5], w[8 * s + 6], w[8 * s + 7]);
-      }
-    }
-  }
-}
-
 // acc + the low / high bf16 half of a packed pair: the half is converted to
 // fp32 exactly and added with round-to-nearest (the mixed-precision add of
 // sm_100 and later).
