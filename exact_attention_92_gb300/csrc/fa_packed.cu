@@ -307,7 +307,7 @@ struct Call {
   int d;
   PackedPlan plan;
   PackedFwd p;
-  CUtensorMap tm[5];
+  CUtensorMap tm[6];
   int join_grid;
   cudaStream_t st;
 };
@@ -439,6 +439,12 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   if (load(d) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_CUDA;
+  }
+  // A warp's 32 rows of O are a box of tokens and heads where the heads divide 32.
+  c.tm[5] = c.tm[0];
+  if (32 % p.group_heads == 0) {
+    p.tile_store = 1;
+    if (encode_queries(&c.tm[5], o, Tq, H, p.group, d, p.group_heads, 32 / p.group_heads)) return FA_ERR_CUDA;
   }
   void* ws = nullptr;
   if (fa::internal_workspace(&ws, bytes, c.st) != cudaSuccess) {

@@ -43,9 +43,13 @@ struct Cfg {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTileBytes;
-  // Hand-over of the second warpgroup: 16 KB of O, [warp][column / 4][lane] float4, and (m, l, l_bf) of 128 rows.
-  static constexpr int kOffEx = kOffKV + kStages * kTileBytes;
-  static constexpr int kOffStat = kOffEx + 128 * 32 * 4;
+  // Room of 4 KB for each element-wise warp, from which its rows of O are stored
+  // (32 rows of 128 bytes, swizzled).  That of the second warpgroup also takes
+  // what it hands over: 16 KB of O, [warp][column / 4][lane] float4; (m, l, l_bf) of
+  // 128 rows lie apart.
+  static constexpr int kOffOut = kOffKV + kStages * kTileBytes;
+  static constexpr int kOffEx = kOffOut + 4 * 4096;
+  static constexpr int kOffStat = kOffEx + 4 * 4096;
   static constexpr int kOffBar = kOffStat + 3 * 128 * 4;
   static constexpr int kNumBars = 2 + 2 + 2 * kStages + 2 + 2 + 2 + 4 + 4 + 1;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
@@ -156,7 +160,8 @@ template <int D>
 __global__ void __launch_bounds__(384, 1)
     fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kp,
-                         const __grid_constant__ CUtensorMap tm_vp, const PackedFwd p) {
+                         const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_o,
+                         const PackedFwd p) {
   using namespace pk;
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -212,6 +217,7 @@ __global__ void __launch_bounds__(384, 1)
     tma_prefetch_desc(&tm_v);
     tma_prefetch_desc(&tm_kp);
     tma_prefetch_desc(&tm_vp);
+    tma_prefetch_desc(&tm_o);
   }
   tc_fence_before();
   __syncthreads();
@@ -413,6 +419,8 @@ __global__ void __launch_bounds__(384, 1)
     const int warp_tok = 32 * wq / p.group_heads;    // the warp's first token
     const float sl2 = p.scale_log2;
     float4* const ex0 = reinterpret_cast<float4*>(smem + C::kOffEx);
+    uint8_t* const out = smem + C::kOffOut + warp * 4096;
+    bool storing = false;  // a store from `out` may still be reading it
     float* stat = reinterpret_cast<float*>(smem + C::kOffStat);
     uint32_t sc = 0, oc = 0, xc = 0;
     bool ok = true;
@@ -434,6 +442,13 @@ __global__ void __launch_bounds__(384, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], sc & 1, ctl, kWaitSFull));
         ++sc;
         if (!ok) break;
+        if (j == 0 && storing) {
+          // Before this warp's first arrival of the unit: so whoever writes `out` after
+          // the unit's products finds it read.
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
+          storing = false;
+        }
         if (!live) {
           mbar_arrive_warp(&p_full[t]);
           continue;
@@ -627,14 +642,39 @@ __global__ void __launch_bounds__(384, 1)
       const float lse = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
       const float2 il = make_float2(inv_l, inv_l);
       if (!w.cut && !p.shared) {
-        // Each lane stores its own row, whole sectors at a time (an exchange between
-        // lanes first, so that a store takes whole lines, cost 3300 cycles a unit).
-        if (row_ok) {
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) {
-            const float2 a = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il);
-            o[i] = pack_bf16(a.x, a.y);
+        for (int i = 0; i < D / 2; ++i) {
+          const float2 a = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il);
+          o[i] = pack_bf16(a.x, a.y);
+        }
+        // (The second warpgroup's room may hold what the first still reads of the unit
+        // before; the first has read it once it has a product in this unit.)
+        if (p.tile_store && warp_tok + 32 / p.group_heads <= here && (t == 0 || w.n0 > 0)) {
+          // All 32 rows: 64 channels at a time through shared memory, stored by the
+          // copy engine.  (Stores from registers, a row a lane, touch 32 lines each: 2800
+          // cycles a unit at d = 128, during which the other warps' barriers queue behind
+          // them; with rows exchanged between lanes first, 3300.)
+#pragma unroll
+          for (int h = 0; h < (D + 63) / 64; ++h) {
+            if (storing) {
+              if (lane == 0) bulk_wait_read();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (64 * h + 8 * i >= D) continue;  // (past d = 96 nothing is stored)
+              const uint32_t* x = o + 32 * h + 4 * i;
+              *reinterpret_cast<uint4*>(out + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_4d(&tm_o, out, 64 * h, w.g0, w.e.q_row + first + warp_tok, w.hk);
+              bulk_commit();
+            }
+            storing = true;
           }
+        } else if (row_ok) {
           if (p.store32) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) st_global_v8(orow + 32 * i, o + 8 * i);
@@ -643,8 +683,8 @@ __global__ void __launch_bounds__(384, 1)
             for (int i = 0; i < D / 8; ++i)
               reinterpret_cast<uint4*>(orow)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
-          p.lse[(size_t)head * p.Tq + token] = lse;
         }
+        if (row_ok) p.lse[(size_t)head * p.Tq + token] = lse;
         continue;
       }
 #pragma unroll
@@ -671,6 +711,8 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
     }
+    // The stores have reached the tensor (and read shared memory) before the CTA ends.
+    if (lane == 0) bulk_wait();
     __syncwarp();
   } else {
     reg_dealloc<C::kRegsCtl>();
@@ -693,10 +735,11 @@ static cudaError_t launch_t(const CUtensorMap* tm, const PackedFwd& p, cudaStrea
       cudaFuncSetAttribute(fa_packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(fa_packed_fwd_kernel<D>, dim3(p.grid), dim3(C::kThreads), C::kSmemBytes, stream, tm[0], tm[1], tm[2],
-                    tm[3], tm[4], p);
+                    tm[3], tm[4], tm[5], p);
 }
 
-// tm: Q, K, V, and K, V of the prefix (any map where there is none).
+// tm: Q, K, V, K and V of the prefix (any map where there is none), O (any map
+// without tile_store).
 cudaError_t launch_packed_fwd(int d, const CUtensorMap* tm, const PackedFwd& p, cudaStream_t stream) {
   switch (d) {
     case 64: return launch_t<64>(tm, p, stream);

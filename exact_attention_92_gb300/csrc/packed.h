@@ -93,6 +93,7 @@ struct PackedFwd {
   long long o_row, o_head;  // strides in elements
   float* lse;               // [H, Tq]
   int store32;
+  int tile_store;     // a warp's 32 rows are a box of o's tensor map (32 / group_heads tokens)
   float* o_slot;      // [2 grid][D / 4][kSlotRows][4]
   float* lse_slot;    // [2 grid][kSlotRows]
   float* o_part;      // shared: [2][Tq][H][D], of the prefix and of the own keys
