@@ -34,103 +34,128 @@ __device__ __forceinline__ bool before(const PackedStart& a, const PackedStart& 
 
 }  // namespace
 
+// Sequences and entries up to this number have their places in shared memory.
+constexpr int kPlanShared = 1024;
+
 __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const PackedPlan p) {
   __shared__ long long s_warps[32];
   __shared__ long long s_carry;
+  __shared__ Seq s_seq[kPlanShared];
+  __shared__ int s_base[2][kPlanShared + 1];
+  __shared__ long long s_cum[2][kPlanShared + 1];
   const int tid = threadIdx.x;
   pdl_trigger();
   pdl_wait();
   const int block = 2 * p.tile_tokens;
-  // Entries of the sequences: [seq_base[b], seq_base[b + 1]) after those of the prefix.
-  int own = 0;
+  const bool few = p.s.B <= kPlanShared;
+  int* const base0 = few ? s_base[0] : p.seq_base[0];
+  int* const base1 = few ? s_base[1] : p.seq_base[1];
+  // Entries of the sequences, by list: [base[b], base[b + 1]).  Both numbers in one sum.
+  long long own = 0;
   for (int b0 = 0; b0 < p.s.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    int n = 0;
-    if (b < p.s.B) n = (load_seq(p.s, b).q_len + block - 1) / block;
-    const int sum = (int)scan_block<long long>(n, s_warps);
-    if (b < p.s.B) p.seq_base[b + 1] = own + sum;
-    if (tid == kPlanThreads - 1) s_carry = own + sum;
+    long long n = 0;
+    if (b < p.s.B) {
+      const Seq s = load_seq(p.s, b);
+      if (few) s_seq[b] = s;
+      const int rest = s.q_len % block;
+      n = ((long long)(rest > 0 && rest <= p.tile_tokens) << 32) + s.q_len / block + (rest > p.tile_tokens);
+    }
+    const long long sum = own + scan_block<long long>(n, s_warps);
+    if (b < p.s.B) {
+      base0[b + 1] = (int)(sum & 0xffffffffLL);
+      base1[b + 1] = (int)(sum >> 32);
+    }
+    if (tid == kPlanThreads - 1) s_carry = sum;
     __syncthreads();
-    own = (int)s_carry;
+    own = s_carry;
     __syncthreads();
   }
-  if (tid == 0) p.seq_base[0] = 0;
+  if (tid == 0) base0[0] = base1[0] = 0;
   // Blocks over the prefix alone: all rows from the first sequence's first to
   // the last one's last, whatever sequence they are of.
-  int first = 0, over = 0, rows = 0;
+  int first = 0, rows = 0;
   if (p.shared) {
     first = min(max(p.s.cu_q[0], 0), p.s.Tq);
     rows = max(0, min(p.s.cu_q[p.s.B], p.s.Tq) - first);
-    over = (rows + block - 1) / block;
   }
-  const int entries = over + own;
-  __syncthreads();  // seq_base
-  long long total = 0;
-  for (int e0 = 0; e0 < entries; e0 += kPlanThreads) {
-    const int e = e0 + tid;
-    long long places = 0;
-    if (e < entries) {
-      PackedEntry x;
-      if (e < over) {
-        x = PackedEntry{first + e * block, min(block, rows - e * block), 0, 0, p.prefix_tiles, p.prefix_tiles, 0, 1};
-      } else {
-        const int i = e - over;
-        const int lo = seq_of(p.seq_base, p.s.B, i);
-        const Seq s = load_seq(p.s, lo);
-        const int t0 = (i - p.seq_base[lo]) * block;
-        x.q_row = s.q + t0;
-        x.q_len = min(block, s.q_len - t0);
-        x.k_row = s.k;
-        x.k_len = s.k_len;
-        x.prefix = p.shared ? 0 : p.prefix_tiles;
-        x.pos = t0 + (p.s.causal == FA_CAUSAL_BOTTOM_RIGHT ? s.k_len - s.q_len : 0);
-        const int seen = p.s.causal == FA_CAUSAL_NONE ? s.k_len : min(s.k_len, max(0, x.pos + x.q_len));
-        x.tiles = x.prefix + (seen + kTileN - 1) / kTileN;
-        x.kind = 0;
+  const int rest = rows % block;
+  int over[2], entries[2];
+  over[kWhole] = rows / block + (rest > p.tile_tokens);
+  over[kSmall] = rest > 0 && rest <= p.tile_tokens;
+  entries[kWhole] = over[kWhole] + (int)(own & 0xffffffffLL);
+  entries[kSmall] = over[kSmall] + (int)(own >> 32);
+  __syncthreads();  // base
+  long long total[2];
+#pragma unroll
+  for (int list = 0; list < 2; ++list) {
+    const int* base = list ? base1 : base0;
+    long long* cum = entries[list] <= kPlanShared ? s_cum[list] : p.cum[list];
+    long long sum_all = 0;
+    for (int e0 = 0; e0 < entries[list]; e0 += kPlanThreads) {
+      const int e = e0 + tid;
+      long long places = 0;
+      if (e < entries[list]) {
+        PackedEntry x;
+        if (e < over[list]) {
+          const int t0 = (list ? over[kWhole] : e) * block;
+          x = PackedEntry{first + t0, min(block, rows - t0), 0, 0, p.prefix_tiles, p.prefix_tiles, 0, 1};
+        } else {
+          const int i = e - over[list];
+          const int b = seq_of(base, p.s.B, i);
+          const Seq s = few ? s_seq[b] : load_seq(p.s, b);
+          const int t0 = (list ? base0[b + 1] - base0[b] : i - base[b]) * block;
+          x.q_row = s.q + t0;
+          x.q_len = min(block, s.q_len - t0);
+          x.k_row = s.k;
+          x.k_len = s.k_len;
+          x.prefix = p.shared ? 0 : p.prefix_tiles;
+          x.pos = t0 + (p.s.causal == FA_CAUSAL_BOTTOM_RIGHT ? s.k_len - s.q_len : 0);
+          const int seen = p.s.causal == FA_CAUSAL_NONE ? s.k_len : min(s.k_len, max(0, x.pos + x.q_len));
+          x.tiles = x.prefix + (seen + kTileN - 1) / kTileN;
+          x.kind = 0;
+        }
+        p.entries[list][e] = x;
+        places = (long long)x.tiles * tile_places(list) + unit_places(list);
       }
-      p.entries[e] = x;
-      places = x.tiles + kUnitTiles;
+      const long long sum = sum_all + scan_block<long long>(places, s_warps);
+      if (e < entries[list]) cum[e + 1] = sum;
+      if (tid == kPlanThreads - 1) s_carry = sum;
+      __syncthreads();
+      sum_all = s_carry;
+      __syncthreads();
     }
-    const long long sum = scan_block<long long>(places, s_warps);
-    if (e < entries) p.cum[e + 1] = total + sum;
-    if (tid == kPlanThreads - 1) s_carry = total + sum;
-    __syncthreads();
-    total = s_carry;
-    __syncthreads();
+    if (tid == 0) cum[0] = 0;
+    total[list] = sum_all;
   }
-  if (tid == 0) {
-    p.cum[0] = 0;
-    p.header[0] = entries;
-    p.header[1] = over;
-  }
+  if (tid == 0) *p.header = PackedHeader{{entries[0], entries[1]}, {over[0], over[1]}, first, rows};
   __syncthreads();
-  for (int c = tid; c <= p.grid; c += kPlanThreads) {
-    PackedStart s{0, 0};
-    if (c == p.grid) {
-      s.unit = p.head_groups * entries;
-    } else if (total > 0) {
-      const long long at = total * p.head_groups / p.grid * c + total * p.head_groups % p.grid * c / p.grid;
-      const int hg = (int)(at / total);
-      const long long r = at - hg * total;
-      int lo = 0, hi = entries;  // cum[lo] <= r < cum[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (p.cum[mid] <= r) lo = mid; else hi = mid;
-      }
-      int x = (int)(r - p.cum[lo]);
-      const int n = (int)(p.cum[lo + 1] - p.cum[lo]) - kUnitTiles;
-      if (p.whole)
-        x = 2 * x < n + kUnitTiles ? 0 : n;
-      else if (x < p.min_tiles)
-        x = 0;
-      if (x > n - (p.whole ? 1 : p.min_tiles) && x > 0) {
-        ++lo;
-        x = 0;
-      }
-      s.unit = hg * entries + lo;
-      s.tile = x;
+  // Place `at` of a list as unit and tile.  A cut near a unit's border moves there.
+  auto locate = [&](int list, long long at) -> PackedStart {
+    const long long all = total[list];
+    if (at >= all * p.head_groups) return PackedStart{p.head_groups * entries[list], 0};
+    const long long* cum = entries[list] <= kPlanShared ? s_cum[list] : p.cum[list];
+    const int hg = (int)(at / all);
+    const long long r = at - hg * all;
+    int lo = 0, hi = entries[list];  // cum[lo] <= r < cum[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (cum[mid] <= r) lo = mid; else hi = mid;
     }
-    p.starts[c] = s;
+    const int size = (int)(cum[lo + 1] - cum[lo]), in = (int)(r - cum[lo]);
+    const int n = (size - unit_places(list)) / tile_places(list);
+    int x = in / tile_places(list);
+    const int least = p.whole ? n + 1 : p.min_tiles;
+    if (x < least && 2 * in < size) x = 0;
+    else if (x < least || x > n - least) x = 0, ++lo;
+    return PackedStart{hg * entries[list] + lo, x};
+  };
+  const long long whole = total[kWhole] * p.head_groups, all = whole + total[kSmall] * p.head_groups;
+  auto edge = [&](int c) { return c >= p.grid ? all : all / p.grid * c + all % p.grid * c / p.grid; };
+  for (int c = tid; c <= p.grid; c += kPlanThreads) p.starts[kWhole][c] = locate(kWhole, min(edge(c), whole));
+  for (int v = tid; v <= 2 * p.grid; v += kPlanThreads) {
+    const long long a = max(0LL, edge(v / 2) - whole), b = max(0LL, edge(v / 2 + 1) - whole);
+    p.starts[kSmall][v] = locate(kSmall, v & 1 ? a + (b - a) / 2 : a);
   }
 }
 
@@ -166,18 +191,23 @@ struct Merge {
   }
 };
 
-// The parts of `unit` in slots: its first CTA is c (which holds its tile 0).
+// Rows of a slot of the list.
+__device__ __forceinline__ int slot_rows(int list) { return list ? kSlotRows / 2 : kSlotRows; }
+__device__ __forceinline__ int stretches(const PackedFwd& p, int list) { return list ? 2 * p.grid : p.grid; }
+
+// The parts of `unit` in slots: its tile 0 is in stretch c.
 template <int D>
-__device__ __forceinline__ void add_slots(const PackedFwd& p, const PackedStart* starts, Merge& m, int unit, int c, int row,
-                                          int c16) {
+__device__ __forceinline__ void add_slots(const PackedFwd& p, int list, const PackedStart* starts, Merge& m, int unit, int c,
+                                          int row, int c16) {
+  const int rows = slot_rows(list), end = stretches(p, list);
   int slot = 2 * c + 1;
   while (true) {
-    const float4* o = reinterpret_cast<const float4*>(p.o_slot) + ((size_t)slot * (D / 4) + 4 * c16) * kSlotRows + row;
-    m.add(p.lse_slot[(size_t)slot * kSlotRows + row], o, kSlotRows);
-    // The next CTA that starts within the unit and has some of it.
+    const float4* o = reinterpret_cast<const float4*>(p.o_slot[list]) + ((size_t)slot * (D / 4) + 4 * c16) * rows + row;
+    m.add(p.lse_slot[list][(size_t)slot * rows + row], o, rows);
+    // The next stretch that starts within the unit and has some of it.
     do {
       ++c;
-      if (c >= p.grid || starts[c].unit != unit || starts[c].tile == 0) return;
+      if (c >= end || starts[c].unit != unit || starts[c].tile == 0) return;
     } while (starts[c + 1].unit == unit && starts[c + 1].tile == starts[c].tile);
     slot = 2 * c;
   }
@@ -208,31 +238,34 @@ __device__ __forceinline__ bool row_of(const PackedFwd& p, const PackedEntry& e,
 
 }  // namespace
 
-// Units that were cut: one for each CTA that starts within a unit that no CTA
-// before it starts within.
+// Units that were cut: one for each stretch that starts within a unit that no
+// stretch before it starts within.
 template <int D>
 __global__ void __launch_bounds__(256) fa_packed_merge_kernel(const PackedFwd p) {
   pdl_wait();
-  const int c = blockIdx.x + 1;
-  const PackedStart s = p.starts[c], before_s = p.starts[c - 1];
+  const int list = (int)blockIdx.x >= p.grid - 1 ? kSmall : kWhole;
+  const int c = (int)blockIdx.x + 1 - (list ? p.grid - 1 : 0);
+  const PackedStart* starts = p.starts[list];
+  const PackedStart s = starts[c], before_s = starts[c - 1];
   if (s.tile == 0 || (before_s.unit == s.unit && before_s.tile > 0)) return;
-  const int entries = p.header[0];
+  const int entries = p.header->entries[list];
   const int hg = s.unit / entries;
-  const PackedEntry e = p.entries[s.unit - hg * entries];
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < kSlotRows * (D / 16); i += 256 * gridDim.y) {
-    const int row = i % kSlotRows, c16 = i / kSlotRows;
+  const PackedEntry e = p.entries[list][s.unit - hg * entries];
+  const int rows = slot_rows(list);
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 16); i += 256 * gridDim.y) {
+    const int row = i % rows, c16 = i / rows;
     int token, head;
     if (!row_of(p, e, hg, row, &token, &head)) continue;
     Merge m;
-    add_slots<D>(p, p.starts, m, s.unit, c - 1, row, c16);
+    add_slots<D>(p, list, starts, m, s.unit, c - 1, row, c16);
     write_row<D>(p, m, token, head, c16);
   }
 }
 
-// The last CTA that starts at or before the unit's first tile.
-__device__ __forceinline__ int first_cta(const PackedStart* starts, int grid, int unit) {
+// The last stretch that starts at or before the unit's first tile.
+__device__ __forceinline__ int stretch_of(const PackedStart* starts, int number, int unit) {
   const PackedStart want{unit, 0};
-  int lo = 0, hi = grid;
+  int lo = 0, hi = number;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (before(want, starts[mid])) hi = mid; else lo = mid;
@@ -240,52 +273,62 @@ __device__ __forceinline__ int first_cta(const PackedStart* starts, int grid, in
   return lo;
 }
 
+// The last entry of [lo, hi) that starts at or before the token; -1 if the token is not in it.
+__device__ __forceinline__ int entry_of(const PackedEntry* e, int lo, int hi, int token) {
+  if (lo >= hi) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (e[mid].q_row <= token) lo = mid; else hi = mid;
+  }
+  const int at = token - e[lo].q_row;
+  return at >= 0 && at < e[lo].q_len ? lo : -1;
+}
+
 // All rows of the sequences, each from its part over the prefix and its part
 // over the sequence's own keys (one row each where the unit was not cut).  A
 // thread takes 16 channels of a row; rows are taken token by token, so that the
 // threads of a CTA are of few units and find them in the same places.
-constexpr int kJoinStarts = 320;  // CTAs' starts kept in shared memory
+constexpr int kJoinStarts = 1024;  // starts kept in shared memory
 template <int D>
 __global__ void __launch_bounds__(256) fa_packed_join_kernel(const PackedFwd p) {
   __shared__ PackedStart s_starts[kJoinStarts];
   pdl_wait();
-  const PackedStart* starts = p.starts;
-  if (p.grid < kJoinStarts) {
-    for (int i = threadIdx.x; i <= p.grid; i += 256) s_starts[i] = p.starts[i];
-    starts = s_starts;
+  const PackedStart* starts[2] = {p.starts[0], p.starts[1]};
+  if (3 * p.grid + 2 <= kJoinStarts) {
+    for (int i = threadIdx.x; i < 3 * p.grid + 2; i += 256)
+      s_starts[i] = i <= p.grid ? p.starts[0][i] : p.starts[1][i - p.grid - 1];
+    starts[0] = s_starts;
+    starts[1] = s_starts + p.grid + 1;
   }
-  const int entries = p.header[0], over = p.header[1];
+  const PackedHeader h = *p.header;
   __syncthreads();
-  if (over == 0 || entries == over) return;
   const int block = 2 * p.tile_tokens;
-  const int q0 = p.entries[0].q_row;
-  const int rows = p.entries[over - 1].q_row + p.entries[over - 1].q_len - q0;
   constexpr int kPer = D / 16;
-  const long long tasks = (long long)rows * p.H * kPer;
+  const long long tasks = (long long)h.rows * p.H * kPer;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < tasks; i += 256LL * gridDim.x) {
     const int c16 = (int)(i % kPer);
     const long long r = i / kPer;
     const int at = (int)(r / p.H), head = (int)(r - (long long)at * p.H);
-    const int token = q0 + at;
-    // The own block: the last that starts at or before the token.  (A token of no
-    // sequence is behind that block's last.)
-    int lo = over, hi = entries;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (p.entries[mid].q_row <= token) lo = mid; else hi = mid;
-    }
-    const int tok = token - p.entries[lo].q_row;
-    if (tok < 0 || tok >= p.entries[lo].q_len) continue;
+    const int token = h.first + at;
+    // The own block (a token of no sequence has none).
+    int own_list = kWhole, own = entry_of(p.entries[kWhole], h.over[kWhole], h.entries[kWhole], token);
+    if (own < 0) own_list = kSmall, own = entry_of(p.entries[kSmall], h.over[kSmall], h.entries[kSmall], token);
+    if (own < 0) continue;
     const int hk = head / p.group, g = head - hk * p.group;
     const int hg = hk * p.chunks + g / p.group_heads, gh = g % p.group_heads;
-    const int pe = at / block, ptok = at - pe * block;
+    const int over = at / block;  // the block over the prefix
     Merge m;
+#pragma unroll
     for (int part = 0; part < 2; ++part) {
-      const int unit = hg * entries + (part ? lo : pe), t = part ? tok : ptok;
-      const int c = first_cta(starts, p.grid, unit);
-      if (starts[c + 1].unit == unit && starts[c + 1].tile > 0) {
+      const int list = part ? own_list : over >= h.over[kWhole];
+      const int e = part ? own : list ? 0 : over;
+      const int t = part ? token - p.entries[list][own].q_row : at - over * block;
+      const int unit = hg * h.entries[list] + e;
+      const int c = stretch_of(starts[list], stretches(p, list), unit);
+      const PackedStart next = starts[list][c + 1];
+      if (next.unit == unit && next.tile > 0) {
         const int row = t / p.tile_tokens * kTileM + t % p.tile_tokens * p.group_heads + gh;
-        add_slots<D>(p, starts, m, unit, c, row, c16);
+        add_slots<D>(p, list, starts[list], m, unit, c, row, c16);
       } else {
         const float4* o = reinterpret_cast<const float4*>(p.o_part + (((size_t)part * p.Tq + token) * p.H + head) * D) + 4 * c16;
         m.add(p.lse_part[((size_t)part * p.H + head) * p.Tq + token], o, 1);
@@ -324,7 +367,7 @@ template <int D>
 cudaError_t merge_t(const Call& c) {
   if (c.p.shared)
     return fa::launch_pdl(fa::fa_packed_join_kernel<D>, dim3(c.join_grid), dim3(256), 0, c.st, c.p);
-  return fa::launch_pdl(fa::fa_packed_merge_kernel<D>, dim3(c.p.grid - 1, D / 16), dim3(256), 0, c.st, c.p);
+  return fa::launch_pdl(fa::fa_packed_merge_kernel<D>, dim3(3 * c.p.grid - 2, D / 16), dim3(256), 0, c.st, c.p);
 }
 cudaError_t run_merge(void* ctx) {
   const Call& c = *static_cast<const Call*>(ctx);
@@ -414,15 +457,24 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   pl.whole = key_tiles <= 4 && !p.shared ? 1 : 0;
   p.grid = (int)std::min<long long>(sm_count, entries * hgs * (pl.whole ? 1 : std::max(1LL, key_tiles / pl.min_tiles)));
 
-  // Workspace: the list, then partial results.
-  const size_t n_entries = up((size_t)entries * sizeof(fa::PackedEntry));
-  const size_t n_cum = up((size_t)(entries + 1) * sizeof(long long));
+  // Workspace: the lists, then partial results.  Small blocks are the last of
+  // their sequences (and one over the prefix).
+  const long long small = (long long)std::min(B, Tq) + 1;
+  const size_t n_entries[2] = {up((size_t)entries * sizeof(fa::PackedEntry)), up((size_t)small * sizeof(fa::PackedEntry))};
+  const size_t n_cum[2] = {up((size_t)(entries + 1) * sizeof(long long)), up((size_t)(small + 1) * sizeof(long long))};
   const size_t n_base = up(((size_t)B + 1) * sizeof(int));
-  const size_t n_starts = up(((size_t)p.grid + 1) * sizeof(fa::PackedStart) + 2 * sizeof(int));
-  const bool cuts = !pl.whole && p.grid > 1;
-  const size_t slot_rows = cuts ? (size_t)2 * p.grid * fa::kSlotRows : 0;
+  const size_t n_starts[2] = {up(((size_t)p.grid + 1) * sizeof(fa::PackedStart)),
+                              up(((size_t)2 * p.grid + 1) * sizeof(fa::PackedStart))};
+  const bool cuts = !pl.whole;
+  size_t slot_rows[2] = {0, 0};
+  if (cuts) {
+    slot_rows[0] = (size_t)2 * p.grid * fa::kSlotRows;
+    slot_rows[1] = (size_t)4 * p.grid * (fa::kSlotRows / 2);
+  }
   const size_t part_rows = p.shared ? (size_t)2 * Tq * H : 0;
-  const size_t bytes = n_entries + n_cum + n_base + n_starts + up(slot_rows * (d + 1) * 4) + part_rows * (d + 1) * 4;
+  const size_t bytes = n_entries[0] + n_entries[1] + n_cum[0] + n_cum[1] + 2 * n_base + n_starts[0] + n_starts[1] +
+                       up(sizeof(fa::PackedHeader)) + up(slot_rows[0] * (d + 1) * 4) + up(slot_rows[1] * (d + 1) * 4) +
+                       part_rows * (d + 1) * 4;
   c.st = static_cast<cudaStream_t>(stream);
   c.d = d;
 
@@ -452,17 +504,23 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
     return FA_ERR_NO_MEMORY;
   }
   char* at = static_cast<char*>(ws);
-  pl.entries = reinterpret_cast<fa::PackedEntry*>(at);
-  pl.cum = reinterpret_cast<long long*>(at += n_entries);
-  pl.seq_base = reinterpret_cast<int*>(at += n_cum);
-  pl.starts = reinterpret_cast<fa::PackedStart*>(at += n_base);
-  pl.header = reinterpret_cast<int*>(pl.starts + p.grid + 1);
-  at += n_starts;
-  if (slot_rows > 0) {
-    p.o_slot = reinterpret_cast<float*>(at);
-    p.lse_slot = p.o_slot + slot_rows * d;
-    at += up(slot_rows * (d + 1) * 4);
+  for (int list = 0; list < 2; ++list) {
+    p.entries[list] = pl.entries[list] = reinterpret_cast<fa::PackedEntry*>(at);
+    at += n_entries[list];
+    pl.cum[list] = reinterpret_cast<long long*>(at);
+    at += n_cum[list];
+    pl.seq_base[list] = reinterpret_cast<int*>(at);
+    at += n_base;
+    p.starts[list] = pl.starts[list] = reinterpret_cast<fa::PackedStart*>(at);
+    at += n_starts[list];
+    if (slot_rows[list] > 0) {
+      p.o_slot[list] = reinterpret_cast<float*>(at);
+      p.lse_slot[list] = p.o_slot[list] + slot_rows[list] * d;
+      at += up(slot_rows[list] * (d + 1) * 4);
+    }
   }
+  p.header = pl.header = reinterpret_cast<fa::PackedHeader*>(at);
+  at += up(sizeof(fa::PackedHeader));
   if (part_rows > 0) {
     p.o_part = reinterpret_cast<float*>(at);
     p.lse_part = p.o_part + part_rows * d;
@@ -477,9 +535,6 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   p.prefix_len = P;
   p.causal = causal != FA_CAUSAL_NONE ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.entries = pl.entries;
-  p.starts = pl.starts;
-  p.header = pl.header;
   p.o = o->ptr;
   p.o_row = Tq > 1 ? o->row_stride : 0;
   p.o_head = H > 1 ? o->head_stride : 0;

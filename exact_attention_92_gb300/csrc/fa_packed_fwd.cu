@@ -2,23 +2,22 @@
 // fa_prefix_fwd): the products, online softmax and roles of fa_fwd.cu over the
 // list of units of packed.h.  What differs:
 //
-//  * A CTA walks a stretch of the list that the planning kernel gave it, and may
-//    start and end within a unit.
+//  * A CTA walks stretches of the two lists of units that the planning kernel gave
+//    it, and may start and end within a unit.  It takes the whole blocks first,
+//    as fa_fwd.cu does; then each element-wise warpgroup takes small blocks on its
+//    own, with its own loading and issuing warp, its Q buffer and half of the ring.
 //  * A unit's key tiles are those of the shared prefix (all visible), then the
 //    sequence's own (causal or not, up to its length).
 //  * Rows of a tile are (token, query head) pairs, so that the query heads of a
 //    key/value head share its K and V.
-//  * A block of at most one tile of rows (decoding, the ends of sequences) is
-//    taken by both warpgroups: both hold the same rows, warpgroup t takes the key
-//    tiles lo + t, lo + t + 2, ..., and at the end the second hands its maximum,
-//    sums and O to the first through shared memory.  One tile a step then keeps
-//    two chains of S, softmax and P V going.
 //  * A warp whose 32 rows lie past the block's skips the element-wise work (its
 //    rows of P stay what they were; they reach only rows of O that are not kept).
 //
 // Both warpgroups, registers, tensor memory columns and the rounding of P are as
 // described there.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "packed.h"
 #include "sm103_primitives.cuh"
@@ -44,14 +43,11 @@ struct Cfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTileBytes;
   // Room of 4 KB for each element-wise warp, from which its rows of O are stored
-  // (32 rows of 128 bytes, swizzled).  That of the second warpgroup also takes
-  // what it hands over: 16 KB of O, [warp][column / 4][lane] float4; (m, l, l_bf) of
-  // 128 rows lie apart.
+  // (32 rows of 128 bytes, swizzled).
   static constexpr int kOffOut = kOffKV + kStages * kTileBytes;
-  static constexpr int kOffEx = kOffOut + 4 * 4096;
-  static constexpr int kOffStat = kOffEx + 4 * 4096;
-  static constexpr int kOffBar = kOffStat + 3 * 128 * 4;
-  static constexpr int kNumBars = 2 + 2 + 2 * kStages + 2 + 2 + 2 + 4 + 4 + 1;
+  static constexpr int kOffBar = kOffOut + 8 * 4096;
+  static constexpr int kPhaseBars = 2 + 2 + 2 * kStages + 2 + 2 + 2;
+  static constexpr int kNumBars = 2 * kPhaseBars + 1 + 2;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
   static_assert(kSmemBytes <= 232448, "shared memory");
   static constexpr float kRescaleThreshold = 24.0f;  // log2 units, as in fa_fwd.cu
@@ -62,20 +58,23 @@ struct Cfg {
   static_assert(kRegsCtl % 8 == 0 && kRegsMath % 8 == 0, "setmaxnreg counts are multiples of 8");
 };
 
-// A CTA's part of one unit.
+// A stretch's part of one unit.
 struct Piece {
   PackedEntry e;
   int hk, g0;    // key/value head, first query head of the group's
   int lo, hi;    // tiles of this part
-  int n0, n1;    // steps of warpgroup 0 and 1
-  bool dual;     // both warpgroups on the block's one tile
+  int n0;        // steps of tile 0 of a whole block (tile 1, and a small block, take all)
   bool cut;      // not the whole unit
 };
 
-// The units of a CTA, in order.  The next entry is fetched a unit ahead.
+// The units of a stretch of a list, in order.  AHEAD: the next entry is fetched a
+// unit ahead (not by the issuing warps, whose registers are few: they come to a
+// unit while the element-wise warps still end the one before).
+template <bool AHEAD>
 struct Walk {
   const PackedFwd& p;
   PackedStart s0, s1;
+  const PackedEntry* list;
   int entries;
   int u, u_last, at, hk, chunk;
   PackedEntry next;
@@ -85,10 +84,13 @@ struct Walk {
     const int4 a = w[0], b = w[1];
     return PackedEntry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   }
-  __device__ __forceinline__ explicit Walk(const PackedFwd& params) : p(params) {
-    s0 = p.starts[blockIdx.x];
-    s1 = p.starts[blockIdx.x + 1];
-    entries = p.header[0];
+  __device__ __forceinline__ Walk(const PackedFwd& params, int which, int stretch) : p(params) { start(which, stretch); }
+  __device__ __forceinline__ void start(int which, int stretch) {
+    const PackedStart* s = p.starts[which] + stretch;
+    s0 = s[0];
+    s1 = s[1];
+    list = p.entries[which];
+    entries = p.header->entries[which];
     u = s0.unit;
     u_last = s1.tile > 0 ? s1.unit : s1.unit - 1;
     if (s0.unit == s1.unit && s0.tile == s1.tile) u_last = u - 1;
@@ -98,18 +100,17 @@ struct Walk {
       at = u - hg * entries;
       hk = hg / p.chunks;
       chunk = hg - hk * p.chunks;
-      next = fetch(p.entries + at);
+      if (AHEAD) next = fetch(list + at);
     }
   }
   __device__ __forceinline__ bool get(Piece& w) {
     if (u > u_last) return false;
-    w.e = next;
+    w.e = AHEAD ? next : fetch(list + at);
     w.hk = hk;
     w.g0 = chunk * p.group_heads;
     w.lo = u == s0.unit ? s0.tile : 0;
     w.hi = u == s1.unit ? s1.tile : w.e.tiles;
     w.cut = w.lo > 0 || w.hi < w.e.tiles;
-    w.dual = w.e.q_len <= p.tile_tokens;
     ++u;
     if (++at == entries) {
       at = 0;
@@ -118,21 +119,59 @@ struct Walk {
         ++hk;
       }
     }
-    if (u <= u_last) next = fetch(p.entries + at);
-    if (w.dual) {
-      const int nk = max(0, w.hi - w.lo);
-      w.n0 = (nk + 1) / 2;
-      w.n1 = nk / 2;
-    } else {
-      // The second tile holds the block's last token; the first may see less.
-      const int own = p.causal ? min(w.e.k_len, max(0, w.e.pos + p.tile_tokens)) : w.e.k_len;
-      const int seen = w.e.kind ? w.e.prefix : w.e.prefix + (own + kTileN - 1) / kTileN;
-      w.n0 = max(0, min(w.hi, seen) - w.lo);
-      w.n1 = max(0, w.hi - w.lo);
-    }
+    if (AHEAD && u <= u_last) next = fetch(list + at);
+    // The second tile holds the block's last token; the first may see less.
+    const int own = p.causal ? min(w.e.k_len, max(0, w.e.pos + p.tile_tokens)) : w.e.k_len;
+    const int seen = w.e.kind ? w.e.prefix : w.e.prefix + (own + kTileN - 1) / kTileN;
+    w.n0 = max(0, min(w.hi, seen) - w.lo);
     return true;
   }
 };
+
+// Barriers of one way of taking units: of whole blocks (list 0), or of small ones.
+template <int D, int LIST>
+struct Bars {
+  static constexpr int kStages = Cfg<D>::kStages;
+  uint64_t* b;
+  __device__ __forceinline__ explicit Bars(uint64_t* all) : b(all + LIST * Cfg<D>::kPhaseBars) {}
+  __device__ __forceinline__ uint64_t* q_full(int t) const { return b + t; }
+  __device__ __forceinline__ uint64_t* q_empty(int t) const { return b + 2 + t; }
+  __device__ __forceinline__ uint64_t* kv_full(int s) const { return b + 4 + s; }
+  __device__ __forceinline__ uint64_t* kv_empty(int s) const { return b + 4 + kStages + s; }
+  __device__ __forceinline__ uint64_t* s_full(int t) const { return b + 4 + 2 * kStages + t; }
+  __device__ __forceinline__ uint64_t* p_full(int t) const { return b + 6 + 2 * kStages + t; }
+  __device__ __forceinline__ uint64_t* o_full(int t) const { return b + 8 + 2 * kStages + t; }
+};
+
+// Key tile x of a unit, K or V, into a ring slot.
+template <int D>
+__device__ __forceinline__ void load_keys(uint8_t* dst, uint64_t* bar, const Piece& w, int x, const CUtensorMap* own,
+                                          const CUtensorMap* prefix) {
+  using C = Cfg<D>;
+  mbar_arrive_expect_tx(bar, C::kTileBytes);
+  if (x < w.e.prefix) {
+#pragma unroll
+    for (int c = 0; c < C::kChunks; ++c) tma_load_3d(dst + c * C::kChunkBytes, prefix, bar, c * 64, x * kTileN, w.hk);
+  } else {
+    const int row = (x - w.e.prefix) * kTileN;
+    const int n = min(kTileN, w.e.k_len - row);  // keys of the sequence in the tile
+#pragma unroll
+    for (int c = 0; c < C::kChunks; ++c)
+      tma_load_4d(dst + c * C::kChunkBytes, own, bar, c * 64, n - kTileN, w.e.k_row + row, w.hk);
+  }
+}
+
+// Tile t of a block's queries.  (Rows past the block's are another one's: they
+// reach no row but their own.)
+template <int D>
+__device__ __forceinline__ void load_queries(uint8_t* dst, uint64_t* bar, const PackedFwd& p, const Piece& w, int t,
+                                             const CUtensorMap* m) {
+  using C = Cfg<D>;
+  mbar_arrive_expect_tx(bar, (uint32_t)(p.group_heads * p.tile_tokens) * 128u * C::kChunks);
+#pragma unroll
+  for (int c = 0; c < C::kChunks; ++c)
+    tma_load_4d(dst + c * C::kChunkBytes, m, bar, c * 64, w.g0, w.e.q_row + t * p.tile_tokens, w.hk);
+}
 
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t tmem_s, uint32_t q_lo, uint32_t k_lo, uint32_t hi) {
@@ -173,38 +212,22 @@ __global__ void __launch_bounds__(384, 1)
   uint8_t* sQ = smem + C::kOffQ;
   uint8_t* sKV = smem + C::kOffKV;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* q_full = bars;
-  uint64_t* q_empty = bars + 2;
-  uint64_t* kv_full = bars + 4;
-  uint64_t* kv_empty = kv_full + C::kStages;
-  uint64_t* s_full = kv_empty + C::kStages;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
-  uint64_t* ex_full = o_full + 2;   // [4]: warp w's columns handed over
-  uint64_t* ex_free = ex_full + 4;  // [4]: ... and read
-  uint64_t* drain = ex_free + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  const Bars<D, kWhole> wb(bars);
+  const Bars<D, kSmall> sb(bars);
+  uint64_t* whole_done = bars + 2 * C::kPhaseBars;    // every product of the whole blocks is complete
+  uint64_t* drain = whole_done + 1;                   // [2]: of each issuing warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  constexpr int kHalf = C::kStages / 2;               // ring slots of a warpgroup with small blocks
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&o_full[i], 1);
+    for (int i = 0; i < C::kNumBars; ++i) {
+      const int k = i % C::kPhaseBars;
+      const bool p_full = i < 2 * C::kPhaseBars && (k == 6 + 2 * C::kStages || k == 7 + 2 * C::kStages);
+      mbar_init(&bars[i], p_full ? 4 : 1);  // p_full: a warpgroup's warps
     }
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&ex_full[i], 1);
-      mbar_init(&ex_free[i], 1);
-    }
-    mbar_init(drain, 1);
     fence_barrier_init();
   }
   if (warp == 8) {
@@ -227,183 +250,217 @@ __global__ void __launch_bounds__(384, 1)
   // The plan, and whatever wrote the tensors, is complete.
   pdl_wait();
   pdl_trigger();
-  if (warp == 9) {
-    reg_dealloc<C::kRegsCtl>();
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint32_t q_bytes = (uint32_t)(p.group_heads * p.tile_tokens) * 128u * C::kChunks;
-      uint32_t rc = 0;
-      uint32_t qc[2] = {0, 0};
-      bool ok = true;
-      Walk walk(p);
+  // What an issuing warp does for the small blocks of warpgroup t.
+  auto issue_small = [&](auto which_t, bool ok) {
+      constexpr uint32_t hi = sdesc_hi(1024);
+      constexpr uint32_t kTileStep = C::kTileBytes >> 4;
+      const uint32_t q_lo0 = sdesc_lo(smem_u32(sQ), 16);
+      const uint32_t k_lo0 = sdesc_lo(smem_u32(sKV), 16);
+      const uint32_t v_lo0 = sdesc_lo(smem_u32(sKV), C::kChunkBytes);
+      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t where) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, where));
+      };
       Piece w;
+      constexpr int t = decltype(which_t)::value;
+      const uint32_t q_lo = q_lo0 + t * kTileStep, t_s = tmem + C::col_s(t), t_o = tmem + C::col_o(t);
+      uint32_t pos = 0, qn = 0, pn = 0;
+      auto key_slot = [&](uint32_t i) { return t * kHalf + i % kHalf; };
+      auto wait_kv = [&](uint32_t i) -> bool { return wait(sb.kv_full(key_slot(i)), (i / kHalf) & 1, kWaitKvFull); };
+      auto issue_s = [&](bool last) -> bool {  // S of the K at `pos`
+        if (!wait_kv(pos)) return false;
+        tc_fence_after();
+        issue_qk<D>(t_s, q_lo, k_lo0 + key_slot(pos) * kTileStep, hi);
+        mma_commit_w(sb.s_full(t));
+        if (last) mma_commit_w(sb.q_empty(t));
+        mma_commit_w(sb.kv_empty(key_slot(pos)));
+        ++pos;
+        return true;
+      };
+      Walk<false> walk(p, kSmall, 2 * blockIdx.x + t);
       while (ok && walk.get(w)) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || (t ? w.dual || w.n1 == 0 : w.n0 == 0)) continue;
-          ok = mbar_wait(&q_empty[t], (qc[t] & 1) ^ 1, ctl, kWaitQEmpty);
-          if (!ok) continue;
-          // (Rows past the block's are another one's: they reach no row but their own.)
-          mbar_arrive_expect_tx(&q_full[t], q_bytes);
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d(sQ + t * C::kTileBytes + c * C::kChunkBytes, &tm_q, &q_full[t], c * 64, w.g0,
-                        w.e.q_row + t * p.tile_tokens, w.hk);
-          ++qc[t];
+        const int n = w.hi - w.lo;
+        if (n == 0) continue;
+        // (The loads wait for the whole blocks' products.)
+        ok = wait(sb.q_full(t), qn & 1, kWaitQFull) && issue_s(n == 1);
+        ++qn;
+        for (int j = 0; ok && j < n; ++j) {
+          ok = wait_kv(pos) && wait(sb.p_full(t), pn & 1, kWaitPFull);
+          ++pn;
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv<D>(t_o, t_s, v_lo0 + key_slot(pos) * kTileStep, hi, j > 0);
+          mma_commit_w(sb.kv_empty(key_slot(pos)));
+          ++pos;
+          if (j + 1 < n)
+            ok = issue_s(j + 2 == n);
+          else
+            mma_commit_w(sb.o_full(t));
         }
+      }
+      // Every MMA this warp issued completes before TMEM is released.
+      mma_commit_w(&drain[t]);
+      (void)wait(&drain[t], 0, kWaitDrain);
+  };
+  // What a producer does for the small blocks of warpgroup t.
+  auto load_small = [&](auto which_t, bool ok) {
+      Piece w;
+      constexpr int t = decltype(which_t)::value;
+      Walk<true> walk(p, kSmall, 2 * blockIdx.x + t);
+      uint32_t pos = 0, qn = 0;
+      bool first = true;
+      while (ok && walk.get(w)) {
+        if (w.hi == w.lo) continue;
+        // The products of the whole blocks have read Q and the ring.
+        if (first) ok = mbar_wait(whole_done, 0, ctl, kWaitKvEmpty);
+        first = false;
+        ok = ok && mbar_wait(sb.q_empty(t), (qn & 1) ^ 1, ctl, kWaitQEmpty);
+        if (!ok) break;
+        load_queries<D>(sQ + t * C::kTileBytes, sb.q_full(t), p, w, 0, &tm_q);
+        ++qn;
         for (int x = w.lo; ok && x < w.hi; ++x) {
-          const bool pre = x < w.e.prefix;
-          const int row = (pre ? x : x - w.e.prefix) * kTileN;
-          const int n = min(kTileN, w.e.k_len - row);  // keys of the sequence in an own tile
+#pragma unroll
           for (int which = 0; which < 2; ++which) {
-            const uint32_t slot = rc % C::kStages;
-            ok = mbar_wait(&kv_empty[slot], ((rc / C::kStages) & 1) ^ 1, ctl, kWaitKvEmpty);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&kv_full[slot], C::kTileBytes);
-            uint8_t* dst = sKV + slot * C::kTileBytes;
-            for (int c = 0; c < C::kChunks; ++c) {
-              if (pre)
-                tma_load_3d(dst + c * C::kChunkBytes, which ? &tm_vp : &tm_kp, &kv_full[slot], c * 64, row, w.hk);
-              else
-                tma_load_4d(dst + c * C::kChunkBytes, which ? &tm_v : &tm_k, &kv_full[slot], c * 64, n - kTileN,
-                            w.e.k_row + row, w.hk);
-            }
-            ++rc;
+            const uint32_t slot = t * kHalf + pos % kHalf;
+            ok = ok && mbar_wait(sb.kv_empty(slot), ((pos / kHalf) & 1) ^ 1, ctl, kWaitKvEmpty);
+            if (!ok) continue;
+            load_keys<D>(sKV + slot * C::kTileBytes, sb.kv_full(slot), w, x, which ? &tm_v : &tm_k,
+                         which ? &tm_vp : &tm_kp);
+            ++pos;
           }
         }
       }
-      // Let every copy this thread started land before the CTA can exit.
-      const uint32_t first = rc > (uint32_t)C::kStages ? rc - C::kStages : 0u;
-      for (uint32_t pos = first; pos < rc; ++pos)
-        mbar_wait(&kv_full[pos % C::kStages], (pos / C::kStages) & 1, ctl, kWaitDrain);
-      for (int t = 0; t < 2; ++t)
-        if (qc[t] > 0) mbar_wait(&q_full[t], (qc[t] - 1) & 1, ctl, kWaitDrain);
+      for (uint32_t i = pos > (uint32_t)kHalf ? pos - kHalf : 0u; i < pos; ++i)
+        mbar_wait(sb.kv_full(t * kHalf + i % kHalf), (i / kHalf) & 1, ctl, kWaitDrain);
+      if (qn > 0) mbar_wait(sb.q_full(t), (qn - 1) & 1, ctl, kWaitDrain);
+  };
+  if (warp == 9) {
+    reg_dealloc<C::kRegsCtl>();
+    // ----------------------------------------------------------- producers
+    if (lane == 0) {
+      bool ok = true;
+      Piece w;
+      uint32_t rc = 0, qc[2] = {0, 0};
+        // Whole blocks.
+        Walk<true> walk(p, kWhole, blockIdx.x);
+        while (ok && walk.get(w)) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || (t ? w.hi == w.lo : w.n0 == 0)) continue;
+            ok = mbar_wait(wb.q_empty(t), (qc[t] & 1) ^ 1, ctl, kWaitQEmpty);
+            if (!ok) continue;
+            load_queries<D>(sQ + t * C::kTileBytes, wb.q_full(t), p, w, t, &tm_q);
+            ++qc[t];
+          }
+          for (int x = w.lo; ok && x < w.hi; ++x) {
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+              const uint32_t slot = rc % C::kStages;
+              ok = ok && mbar_wait(wb.kv_empty(slot), ((rc / C::kStages) & 1) ^ 1, ctl, kWaitKvEmpty);
+              if (!ok) continue;
+              load_keys<D>(sKV + slot * C::kTileBytes, wb.kv_full(slot), w, x, which ? &tm_v : &tm_k,
+                           which ? &tm_vp : &tm_kp);
+              ++rc;
+            }
+          }
+        }
+        // Let every copy this thread started land before the CTA can exit.
+        for (uint32_t pos = rc > (uint32_t)C::kStages ? rc - C::kStages : 0u; pos < rc; ++pos)
+          mbar_wait(wb.kv_full(pos % C::kStages), (pos / C::kStages) & 1, ctl, kWaitDrain);
+        for (int t = 0; t < 2; ++t)
+          if (qc[t] > 0) mbar_wait(wb.q_full(t), (qc[t] - 1) & 1, ctl, kWaitDrain);
+      load_small(std::integral_constant<int, 0>{}, ok);
     }
+    __syncwarp();
+  } else if (warp == 11) {
+    reg_dealloc<C::kRegsCtl>();
+    if (lane == 0) load_small(std::integral_constant<int, 1>{}, true);
+    __syncwarp();
   } else if (warp == 8) {
     reg_dealloc<C::kRegsCtl>();
-    // ---------------------------------------------------------- MMA issuer
+    // --------------------------------------------------------- MMA issuers
+    bool ok = true;
     {
       constexpr uint32_t hi = sdesc_hi(1024);
       constexpr uint32_t kTileStep = C::kTileBytes >> 4;
       const uint32_t q_lo0 = sdesc_lo(smem_u32(sQ), 16);
       const uint32_t k_lo0 = sdesc_lo(smem_u32(sKV), 16);
       const uint32_t v_lo0 = sdesc_lo(smem_u32(sKV), C::kChunkBytes);
-      uint32_t rc = 0;
-      uint32_t qc[2] = {0, 0}, pc[2] = {0, 0};
-      bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t where) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, where));
       };
-      auto wait_kv = [&](uint32_t pos) -> bool {
-        return wait(&kv_full[pos % C::kStages], (pos / C::kStages) & 1, kWaitKvFull);
-      };
-      Walk walk(p);
       Piece w;
-      while (ok && walk.get(w)) {
-        const int nmax = max(w.n0, w.n1);
-        if (nmax == 0) continue;
+        // Whole blocks: the order of fa_fwd.cu.
+        uint32_t rc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+        auto wait_kv = [&](uint32_t pos) -> bool {
+          return wait(wb.kv_full(pos % C::kStages), (pos / C::kStages) & 1, kWaitKvFull);
+        };
+        Walk<false> walk(p, kWhole, blockIdx.x);
+        while (ok && walk.get(w)) {
+          const int n1 = w.hi - w.lo;
+          if (n1 == 0) continue;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || (t ? w.dual || w.n1 == 0 : w.n0 == 0)) continue;
-          ok = wait(&q_full[t], qc[t] & 1, kWaitQFull);
-          ++qc[t];
-        }
-        if (!ok) break;
-        if (w.dual) {
-          // Warpgroup t's step j reads key tile 2j + t (K at position rc + 2
-          // (2j + t), V one after it); each K and V has one reader and is
-          // released after its product.
-          const int nk = w.n0 + w.n1;
-          auto qk = [&](int t, int j) -> bool {
-            const int tile = 2 * j + t;
-            const uint32_t pos_k = rc + 2 * tile;
-            if (!wait_kv(pos_k)) return false;
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || (t ? n1 : w.n0) == 0) continue;
+            ok = wait(wb.q_full(t), qc[t] & 1, kWaitQFull);
+            ++qc[t];
+          }
+          ok = ok && wait_kv(rc);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t ? n1 : w.n0;
+            if (nt == 0) continue;
+            issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + (rc % C::kStages) * kTileStep, hi);
+            mma_commit_w(wb.s_full(t));
+            if (nt == 1) mma_commit_w(wb.q_empty(t));  // Q_t's last product
+          }
+          mma_commit_w(wb.kv_empty(rc % C::kStages));
+          for (int j = 0; ok && j < n1; ++j) {
+            const uint32_t pos_v = rc + 2 * j + 1;
+            const uint32_t pos_k = pos_v + 1;
+            const uint32_t slot_v = pos_v % C::kStages;
+            const uint32_t slot_k = pos_k % C::kStages;
+            ok = wait_kv(pos_v);
+            if (!ok) break;
             tc_fence_after();
-            issue_qk<D>(tmem + C::col_s(t), q_lo0, k_lo0 + (pos_k % C::kStages) * kTileStep, hi);
-            mma_commit_w(&s_full[t]);
-            if (tile + 1 == nk) mma_commit_w(&q_empty[0]);  // the block's last product with Q
-            mma_commit_w(&kv_empty[pos_k % C::kStages]);
-            return true;
-          };
-          ok = qk(0, 0);
-          if (ok && w.n1 > 0) ok = qk(1, 0);
-          for (int j = 0; ok && j < nmax; ++j) {
+            bool k_ready = false;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              const int nt = t ? w.n1 : w.n0;
+              const int nt = t ? n1 : w.n0;
               if (!ok || j >= nt) continue;
-              const uint32_t pos_v = rc + 2 * (2 * j + t) + 1;
-              ok = wait_kv(pos_v) && wait(&p_full[t], pc[t] & 1, kWaitPFull);
+              ok = wait(wb.p_full(t), pc[t] & 1, kWaitPFull);
               ++pc[t];
               if (!ok) continue;
               tc_fence_after();
-              issue_pv<D>(tmem + C::col_o(t), tmem + C::col_s(t), v_lo0 + (pos_v % C::kStages) * kTileStep, hi, j > 0);
-              mma_commit_w(&kv_empty[pos_v % C::kStages]);
-              if (j + 1 < nt)
-                ok = qk(t, j + 1);
-              else
-                mma_commit_w(&o_full[t]);
-            }
-          }
-          rc += 2 * nk;
-          continue;
-        }
-        {
-          const uint32_t slot_k = rc % C::kStages;
-          ok = wait_kv(rc);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int nt = t ? w.n1 : w.n0;
-            if (nt == 0) continue;
-            issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + slot_k * kTileStep, hi);
-            mma_commit_w(&s_full[t]);
-            if (nt == 1) mma_commit_w(&q_empty[t]);  // Q_t's last product
-          }
-          mma_commit_w(&kv_empty[slot_k]);
-        }
-        for (int j = 0; ok && j < nmax; ++j) {
-          const uint32_t pos_v = rc + 2 * j + 1;
-          const uint32_t pos_k = pos_v + 1;
-          const uint32_t slot_v = pos_v % C::kStages;
-          const uint32_t slot_k = pos_k % C::kStages;
-          ok = wait_kv(pos_v);
-          if (!ok) break;
-          tc_fence_after();
-          bool k_ready = false;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int nt = t ? w.n1 : w.n0;
-            if (!ok || j >= nt) continue;
-            ok = wait(&p_full[t], pc[t] & 1, kWaitPFull);
-            ++pc[t];
-            if (!ok) continue;
-            tc_fence_after();
-            issue_pv<D>(tmem + C::col_o(t), tmem + C::col_s(t), v_lo0 + slot_v * kTileStep, hi, j > 0);
-            if (j + 1 < nt) {
-              if (!k_ready) {
-                ok = wait_kv(pos_k);
-                if (!ok) continue;
-                tc_fence_after();
-                k_ready = true;
+              issue_pv<D>(tmem + C::col_o(t), tmem + C::col_s(t), v_lo0 + slot_v * kTileStep, hi, j > 0);
+              if (j + 1 < nt) {
+                if (!k_ready) {
+                  ok = wait_kv(pos_k);
+                  if (!ok) continue;
+                  tc_fence_after();
+                  k_ready = true;
+                }
+                issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + slot_k * kTileStep, hi);
+                mma_commit_w(wb.s_full(t));
+                if (j + 2 == nt) mma_commit_w(wb.q_empty(t));  // Q_t's last product
+              } else {
+                mma_commit_w(wb.o_full(t));
               }
-              issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + slot_k * kTileStep, hi);
-              mma_commit_w(&s_full[t]);
-              if (j + 2 == nt) mma_commit_w(&q_empty[t]);  // Q_t's last product
-            } else {
-              mma_commit_w(&o_full[t]);
             }
+            if (!ok) break;
+            mma_commit_w(wb.kv_empty(slot_v));
+            if (j + 1 < n1) mma_commit_w(wb.kv_empty(slot_k));
           }
-          if (!ok) break;
-          mma_commit_w(&kv_empty[slot_v]);
-          if (j + 1 < nmax) mma_commit_w(&kv_empty[slot_k]);
+          rc += 2 * n1;
         }
-        rc += 2 * nmax;
-      }
-      // Every MMA this warp issued completes before TMEM is released.
-      mma_commit_w(drain);
-      (void)wait(drain, 0, kWaitDrain);
+        mma_commit_w(whole_done);
     }
+    issue_small(std::integral_constant<int, 0>{}, ok);
+    __syncwarp();
+  } else if (warp == 10) {
+    reg_dealloc<C::kRegsCtl>();
+    issue_small(std::integral_constant<int, 1>{}, true);
     __syncwarp();
   } else if (warp < 8) {
     reg_alloc<C::kRegsMath>();
@@ -418,39 +475,35 @@ __global__ void __launch_bounds__(384, 1)
     const int gh = r_in_tile - tok * p.group_heads;  // query head within the group's run
     const int warp_tok = 32 * wq / p.group_heads;    // the warp's first token
     const float sl2 = p.scale_log2;
-    float4* const ex0 = reinterpret_cast<float4*>(smem + C::kOffEx);
     uint8_t* const out = smem + C::kOffOut + warp * 4096;
     bool storing = false;  // a store from `out` may still be reading it
-    float* stat = reinterpret_cast<float*>(smem + C::kOffStat);
-    uint32_t sc = 0, oc = 0, xc = 0;
     bool ok = true;
-    Walk walk(p);
+    // The units of a list: one copy of the code for each.
+    auto take = [&](auto which) {
+    constexpr int kList = decltype(which)::value;
+    constexpr bool small = kList == kSmall;
+    const Bars<D, kList> bar(bars);
+    uint64_t *const s_full = bar.s_full(t), *const p_full = bar.p_full(t), *const o_full = bar.o_full(t);
+    uint32_t sc = 0, oc = 0;
+    Walk<true> walk(p, kList, small ? 2 * blockIdx.x + t : blockIdx.x);
     Piece w;
     while (ok && walk.get(w)) {
-      const int steps = t ? w.n1 : w.n0;
-      const int first = w.dual ? 0 : t * p.tile_tokens;     // the tile's first token in the block
-      const int here = min(p.tile_tokens, w.e.q_len - first);  // its tokens (<= 0: none)
+      const int steps = t || small ? w.hi - w.lo : w.n0;
+      const int first = small ? 0 : t * p.tile_tokens;         // the tile's first token in the block
+      const int here = min(p.tile_tokens, w.e.q_len - first);  // its tokens
       const bool live = warp_tok < here;                       // the warp has rows
       const bool row_ok = tok < here && tok < p.tile_tokens && w.g0 + gh < p.group;
-      const bool mine = !w.dual || t == 0;                     // this warpgroup writes the rows
       const int token = w.e.q_row + first + tok;
       const int head = w.hk * p.group + w.g0 + gh;
       float m_ref = -INFINITY;  // reference max of this row, log2 units
       float l = 0.f;     // sum of the fp32 weights: L = m + log l
       float l_bf = 0.f;  // sum of the bf16-rounded weights the PV MMA takes: O = O~ / l_bf
       for (int j = 0; j < steps; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], sc & 1, ctl, kWaitSFull));
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full, sc & 1, ctl, kWaitSFull));
         ++sc;
         if (!ok) break;
-        if (j == 0 && storing) {
-          // Before this warp's first arrival of the unit: so whoever writes `out` after
-          // the unit's products finds it read.
-          if (lane == 0) bulk_wait_read();
-          __syncwarp();
-          storing = false;
-        }
         if (!live) {
-          mbar_arrive_warp(&p_full[t]);
+          mbar_arrive_warp(p_full);
           continue;
         }
         tc_fence_after();
@@ -461,7 +514,7 @@ __global__ void __launch_bounds__(384, 1)
         float x[kTileN];
 #pragma unroll
         for (int c = 0; c < kTileN; ++c) x[c] = __uint_as_float(s[c]);
-        const int tile = w.lo + (w.dual ? 2 * j + t : j);
+        const int tile = w.lo + j;
         const bool pre = tile < w.e.prefix;
         const int row = (pre ? tile : tile - w.e.prefix) * kTileN;
         const int len = pre ? p.prefix_len : w.e.k_len;
@@ -553,26 +606,22 @@ __global__ void __launch_bounds__(384, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive_warp(&p_full[t]);
+        mbar_arrive_warp(p_full);
       }
       if (!ok) break;
       // ---- the rows' results.  What does not need O is worked out while the last
       // product runs; then all of the row is read at once.
-      const bool joined = w.dual && w.n1 > 0;                // the second warpgroup hands over
-      const int live_warps = (here * p.group_heads + 31) / 32;
-      // Groups of columns handed over at a time: the four warps' room is for all who have rows.
-      const int group = live_warps <= 1 ? 4 : live_warps == 2 ? 2 : 1;
-      float4* ex = ex0 + wq * group * 256;
-      const int sl = 2 * (int)blockIdx.x + (w.lo > 0 ? 0 : 1);
-      const int slot_row = (w.dual ? 0 : kTileM * t) + r_in_tile;
+      const int stretch = small ? 2 * (int)blockIdx.x + t : (int)blockIdx.x;
+      const int sl = 2 * stretch + (w.lo > 0 ? 0 : 1);
+      const int slot_row = (small ? 0 : kTileM * t) + r_in_tile;
       uint8_t* orow = reinterpret_cast<uint8_t*>(p.o) + ((long long)token * p.o_row + (long long)head * p.o_head) * 2;
       if (steps > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[t], oc & 1, ctl, kWaitOFull));
+        ok = __all_sync(0xffffffffu, mbar_wait(o_full, oc & 1, ctl, kWaitOFull));
         ++oc;
         if (!ok) break;
         tc_fence_after();
       }
-      if (!live || (!mine && !joined)) continue;
+      if (!live) continue;
       uint32_t o[D];
       if (steps > 0) {
 #pragma unroll
@@ -581,61 +630,6 @@ __global__ void __launch_bounds__(384, 1)
       } else {
 #pragma unroll
         for (int i = 0; i < D; ++i) o[i] = 0u;
-      }
-      if (!mine) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const int place = c & (group - 1);
-          if (place == 0) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&ex_free[wq], (xc & 1) ^ 1, ctl, kWaitPFull));
-            ++xc;
-          }
-          if (!ok) continue;
-          if (c == 0) {
-            stat[r_in_tile] = m_ref;
-            stat[128 + r_in_tile] = l;
-            stat[256 + r_in_tile] = l_bf;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            ex[(8 * place + i) * 32 + lane] =
-                make_float4(__uint_as_float(o[32 * c + 4 * i]), __uint_as_float(o[32 * c + 4 * i + 1]),
-                            __uint_as_float(o[32 * c + 4 * i + 2]), __uint_as_float(o[32 * c + 4 * i + 3]));
-          if (place == group - 1 || c == D / 32 - 1) mbar_arrive_warp(&ex_full[wq]);
-        }
-        continue;
-      }
-      if (joined) {
-        float a0 = 1.f, a1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const int place = c & (group - 1);
-          if (place == 0) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&ex_full[wq], xc & 1, ctl, kWaitPFull));
-            ++xc;
-          }
-          if (!ok) continue;
-          if (c == 0) {
-            const float m1 = stat[r_in_tile], l1 = stat[128 + r_in_tile], b1 = stat[256 + r_in_tile];
-            const float m = fmaxf(m_ref, m1);
-            a0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
-            a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
-            l = l * a0 + l1 * a1;
-            l_bf = l_bf * a0 + b1 * a1;
-            m_ref = m;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 y = ex[(8 * place + i) * 32 + lane];
-            uint32_t* x = o + 32 * c + 4 * i;
-            x[0] = __float_as_uint(__uint_as_float(x[0]) * a0 + y.x * a1);
-            x[1] = __float_as_uint(__uint_as_float(x[1]) * a0 + y.y * a1);
-            x[2] = __float_as_uint(__uint_as_float(x[2]) * a0 + y.z * a1);
-            x[3] = __float_as_uint(__uint_as_float(x[3]) * a0 + y.w * a1);
-          }
-          if (place == group - 1 || c == D / 32 - 1) mbar_arrive_warp(&ex_free[wq]);
-        }
-        if (!ok) break;
       }
       // A row that saw no key has l = 0: O = 0, L = -inf.
       const float inv_l = l_bf > 0.f ? 1.0f / l_bf : 0.f;
@@ -647,9 +641,7 @@ __global__ void __launch_bounds__(384, 1)
           const float2 a = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il);
           o[i] = pack_bf16(a.x, a.y);
         }
-        // (The second warpgroup's room may hold what the first still reads of the unit
-        // before; the first has read it once it has a product in this unit.)
-        if (p.tile_store && warp_tok + 32 / p.group_heads <= here && (t == 0 || w.n0 > 0)) {
+        if (p.tile_store && warp_tok + 32 / p.group_heads <= here) {
           // All 32 rows: 64 channels at a time through shared memory, stored by the
           // copy engine.  (Stores from registers, a row a lane, touch 32 lines each: 2800
           // cycles a unit at d = 128, during which the other warps' barriers queue behind
@@ -694,13 +686,14 @@ __global__ void __launch_bounds__(384, 1)
         o[2 * i + 1] = __float_as_uint(a.y);
       }
       if (w.cut) {
-        float4* dst = reinterpret_cast<float4*>(p.o_slot) + (size_t)sl * (D / 4) * kSlotRows + slot_row;
+        const int rows = small ? kSlotRows / 2 : kSlotRows;
+        float4* dst = reinterpret_cast<float4*>(p.o_slot[small]) + (size_t)sl * (D / 4) * rows + slot_row;
         if (row_ok) {
 #pragma unroll
           for (int i = 0; i < D / 4; ++i)
-            dst[i * kSlotRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+            dst[i * rows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                              __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-          p.lse_slot[(size_t)sl * kSlotRows + slot_row] = lse;
+          p.lse_slot[small][(size_t)sl * rows + slot_row] = lse;
         }
       } else {
         float* prow = p.o_part + (((size_t)(1 - w.e.kind) * p.Tq + token) * p.H + head) * D;
@@ -711,6 +704,9 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
     }
+    };
+    take(std::integral_constant<int, kWhole>{});
+    take(std::integral_constant<int, kSmall>{});
     // The stores have reached the tensor (and read shared memory) before the CTA ends.
     if (lane == 0) bulk_wait();
     __syncwarp();

@@ -7,12 +7,18 @@
 // A head group is a (key/value head, run of group_heads of its query heads).
 //
 // Units.  An entry is a block of query tokens with the keys it takes (the shared
-// prefix's, then the sequence's own), a unit is an entry for one head group; all
-// units, head group by head group, make one list of 128-key tiles, each unit
-// followed by kUnitTiles places for its start and end.  Every CTA takes an equal
-// stretch of that list: it depends on nothing but the lengths, so results are
-// the same from run to run.  What a cut leaves in parts is written as fp32
-// partial results, two slots a CTA, and merged.
+// prefix's, then the sequence's own), a unit is an entry for one head group.
+// There are two lists of them, each head group by head group:
+//   whole blocks   (more than one tile of rows): both element-wise warpgroups of a
+//                  CTA take a tile of rows each and share the K, V tiles;
+//   small blocks   (at most one tile: decoding, the ends of sequences): each
+//                  warpgroup, with its own loads and products, takes units alone,
+//                  so that one's start and end overlap the other's steps.
+// The lists' 128-key tiles, weighted by what they take, make one line of places,
+// of which every CTA takes an equal stretch (its two warpgroups halve what of it
+// are small blocks).  That depends on nothing but the lengths, so results are the
+// same from run to run.  What a cut leaves in parts is written as fp32 partial
+// results, two slots a stretch, and merged.
 //
 // Sequence ends.  A tile of a sequence's last keys must read as zeros where it
 // has no keys: the rows there are another sequence's, or memory of no sequence,
@@ -31,8 +37,13 @@
 
 namespace fa {
 
-constexpr int kUnitTiles = 2;    // start and end of a unit, in key tiles' time
-constexpr int kSlotRows = 256;   // query rows of a block
+constexpr int kSlotRows = 256;   // query rows of a whole block; half of it of a small one
+
+// Places of a key tile and of a unit's start and end, in a quarter of a tile of a
+// whole block (1.4 us at d = 128; a unit costs 3.5 to 4 us more).  Small blocks
+// run two at a time.
+__host__ __device__ constexpr int tile_places(int list) { return list ? 3 : 4; }
+__host__ __device__ constexpr int unit_places(int list) { return list ? 3 : 11; }
 
 struct PackedEntry {
   int q_row, q_len;  // first token and tokens of the block
@@ -58,6 +69,14 @@ struct PackedSeqs {
   unsigned int* status;
 };
 
+constexpr int kWhole = 0, kSmall = 1;  // the lists
+
+struct PackedHeader {
+  int entries[2];        // of each list
+  int over[2];           // of these, over the prefix alone (the first ones)
+  int first, rows;       // query tokens that those cover
+};
+
 struct PackedPlan {
   PackedSeqs s;
   int tile_tokens;
@@ -67,11 +86,11 @@ struct PackedPlan {
   int grid;
   int min_tiles;      // a cut leaves at least so many on either side
   int whole;          // 1: no cuts
-  int* seq_base;      // [B + 1] first entry of each sequence
-  PackedEntry* entries;
-  long long* cum;     // [entries + 1] places ahead of each entry
-  PackedStart* starts;  // [grid + 1]
-  int* header;        // entries, of which over the prefix alone
+  int* seq_base[2];        // [B + 1] first entry of each sequence (where it does not fit shared memory)
+  PackedEntry* entries[2];
+  long long* cum[2];       // [entries + 1] places ahead of each entry (likewise)
+  PackedStart* starts[2];  // [grid + 1], [2 grid + 1]
+  PackedHeader* header;
 };
 
 struct PackedFwd {
@@ -85,17 +104,17 @@ struct PackedFwd {
   int causal;         // 0 or 1
   int shared;
   float scale_log2;
-  const PackedEntry* entries;
-  const PackedStart* starts;
-  const int* header;
+  const PackedEntry* entries[2];
+  const PackedStart* starts[2];
+  const PackedHeader* header;
   int grid;
   void* o;
   long long o_row, o_head;  // strides in elements
   float* lse;               // [H, Tq]
   int store32;
   int tile_store;     // a warp's 32 rows are a box of o's tensor map (32 / group_heads tokens)
-  float* o_slot;      // [2 grid][D / 4][kSlotRows][4]
-  float* lse_slot;    // [2 grid][kSlotRows]
+  float* o_slot[2];   // [2 stretches][D / 4][rows][4]
+  float* lse_slot[2];  // [2 stretches][rows]
   float* o_part;      // shared: [2][Tq][H][D], of the prefix and of the own keys
   float* lse_part;    // shared: [2][H][Tq]
   unsigned int* status;
