@@ -151,7 +151,19 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
     return PackedStart{hg * entries[list] + lo, x};
   };
   const long long whole = total[kWhole] * p.head_groups, all = whole + total[kSmall] * p.head_groups;
-  auto edge = [&](int c) { return c >= p.grid ? all : all / p.grid * c + all % p.grid * c / p.grid; };
+  // A CTA that takes of both lists fills its pipeline twice (10 to 25 us more at
+  // d = 128), and a pair of SMs that runs both slows down: pairs of CTAs take one
+  // list where that makes no stretch longer by a 16th.
+  const int apart = 2 * (int)((whole * p.grid + all) / max(2 * all, 1LL));
+  const int behind = p.grid - apart;
+  const bool split = whole > 0 && all > whole && apart > 0 && behind > 0 &&
+                     max(whole / apart, (all - whole) / behind) <= all / p.grid + all / p.grid / 16;
+  auto part = [](long long sum, int n, int c) { return sum / n * c + sum % n * c / n; };
+  auto edge = [&](int c) {
+    if (c >= p.grid) return all;
+    if (!split) return part(all, p.grid, c);
+    return c < apart ? part(whole, apart, c) : whole + part(all - whole, behind, c - apart);
+  };
   for (int c = tid; c <= p.grid; c += kPlanThreads) p.starts[kWhole][c] = locate(kWhole, min(edge(c), whole));
   for (int v = tid; v <= 2 * p.grid; v += kPlanThreads) {
     const long long a = max(0LL, edge(v / 2) - whole), b = max(0LL, edge(v / 2 + 1) - whole);
@@ -170,12 +182,9 @@ struct Merge {
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
   }
-  // A part with logsumexp ls whose 16 channels are float4s `step` apart.
-  __device__ __forceinline__ void add(float ls, const float4* o, size_t step) {
+  // A part with logsumexp ls; a row without keys has none, and nothing in v.
+  __device__ __forceinline__ void add(float ls, const float4 (&v)[4]) {
     if (ls == -INFINITY) return;
-    float4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = o[i * step];
     const float m_new = fmaxf(m, ls);
     const float keep = m == -INFINITY ? 0.f : exp2f((m - m_new) * 1.4426950408889634f);
     const float wgt = exp2f((ls - m_new) * 1.4426950408889634f);
@@ -195,26 +204,93 @@ struct Merge {
 __device__ __forceinline__ int slot_rows(int list) { return list ? kSlotRows / 2 : kSlotRows; }
 __device__ __forceinline__ int stretches(const PackedFwd& p, int list) { return list ? 2 * p.grid : p.grid; }
 
-// The parts of `unit` in slots: its tile 0 is in stretch c.
-template <int D>
+__device__ __forceinline__ bool same(const PackedStart& a, const PackedStart& b) {
+  return a.unit == b.unit && a.tile == b.tile;
+}
+
+// Parts first, first + step, ... of `unit` in slots: its tile 0 is in stretch c, and
+// each stretch that starts within the unit and has some of it (starts[0] is that
+// of c) has a part.  kAtOnce of them are read at a time.
+template <int D, int kAtOnce>
 __device__ __forceinline__ void add_slots(const PackedFwd& p, int list, const PackedStart* starts, Merge& m, int unit, int c,
-                                          int row, int c16) {
-  const int rows = slot_rows(list), end = stretches(p, list);
-  int slot = 2 * c + 1;
-  while (true) {
-    const float4* o = reinterpret_cast<const float4*>(p.o_slot[list]) + ((size_t)slot * (D / 4) + 4 * c16) * rows + row;
-    m.add(p.lse_slot[list][(size_t)slot * rows + row], o, rows);
-    // The next stretch that starts within the unit and has some of it.
-    do {
-      ++c;
-      if (c >= end || starts[c].unit != unit || starts[c].tile == 0) return;
-    } while (starts[c + 1].unit == unit && starts[c + 1].tile == starts[c].tile);
-    slot = 2 * c;
+                                          int first, int step, int row, int c16) {
+  const int rows = slot_rows(list), left = stretches(p, list) - c;
+  const float4* o = reinterpret_cast<const float4*>(p.o_slot[list]) + (size_t)4 * c16 * rows + row;
+  const float* lse = p.lse_slot[list] + row;
+  bool more = true;
+  for (int k = first; more;) {
+    int slot[kAtOnce];
+    float ls[kAtOnce];
+    float4 v[kAtOnce][4];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      more = more && k < left && (k == 0 || (starts[k].unit == unit && starts[k].tile > 0));
+      slot[i] = !more || (k > 0 && same(starts[k], starts[k + 1])) ? -1 : k == 0 ? 2 * c + 1 : 2 * (c + k);
+      k += step;
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      ls[i] = -INFINITY;
+      if (slot[i] < 0) continue;
+      ls[i] = lse[(size_t)slot[i] * rows];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[i][x] = o[((size_t)slot[i] * (D / 4) + x) * rows];
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) m.add(ls[i], v[i]);
   }
 }
 
+// Rows of a CTA of the merges: thread tid works on row tid % n_rows (a power of
+// two), and where that leaves threads over, they take a share of the row's parts
+// each: a step of one sequence over 128 Ki keys and 8 heads, cut in 300, took
+// 112 us with one thread for 16 channels of a row, and 12 us so.
+constexpr int kMergeThreads = 256;
+
+struct MergeShared {
+  float m[kMergeThreads], tot[kMergeThreads];
+  float acc[kMergeThreads][17];
+};
+
+// Writes the CTA's rows; `shares` threads have parts of a row.
 template <int D>
-__device__ __forceinline__ void write_row(const PackedFwd& p, const Merge& m, int token, int head, int c16) {
+__device__ __forceinline__ void write_rows(const PackedFwd& p, MergeShared& sh, Merge& m, int n_rows, int shares, bool ok,
+                                           int token, int head, int c16) {
+  const int tid = threadIdx.x;
+  if (shares > 1) {
+    sh.m[tid] = m.m;
+    sh.tot[tid] = m.tot;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sh.acc[tid][i] = m.acc[i];
+    __syncthreads();
+    // A halving of the shares at a time.
+    int width = 1;
+    while (width < shares) width *= 2;
+    const int share = tid / n_rows;
+    for (int half = width / 2; half > 0; half /= 2) {
+      if (share < half && share + half < shares) {
+        const int x = tid + half * n_rows;
+        const float m_x = sh.m[x];
+        if (m_x != -INFINITY) {
+          const float m_new = fmaxf(m.m, m_x);
+          const float keep = m.m == -INFINITY ? 0.f : exp2f((m.m - m_new) * 1.4426950408889634f);
+          const float wgt = exp2f((m_x - m_new) * 1.4426950408889634f);
+          m.m = m_new;
+          m.tot = m.tot * keep + wgt * sh.tot[x];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) m.acc[i] = m.acc[i] * keep + wgt * sh.acc[x][i];
+          sh.m[tid] = m.m;
+          sh.tot[tid] = m.tot;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sh.acc[tid][i] = m.acc[i];
+        }
+      }
+      shares = min(shares, half);
+      __syncthreads();
+    }
+    ok = ok && share == 0;
+  }
+  if (!ok) return;
   const float inv = m.tot > 0.f ? 1.0f / m.tot : 0.f;
   uint32_t w[8];
 #pragma unroll
@@ -239,27 +315,41 @@ __device__ __forceinline__ bool row_of(const PackedFwd& p, const PackedEntry& e,
 }  // namespace
 
 // Units that were cut: one for each stretch that starts within a unit that no
-// stretch before it starts within.
+// stretch before it starts within.  blockIdx.y: 16 channels.
 template <int D>
-__global__ void __launch_bounds__(256) fa_packed_merge_kernel(const PackedFwd p) {
+__global__ void __launch_bounds__(kMergeThreads) fa_packed_merge_kernel(const PackedFwd p) {
+  __shared__ PackedStart s_starts[2 * kMostGrid + 2];
+  __shared__ MergeShared sh;
+  __shared__ int s_parts;
   pdl_wait();
+  const int tid = threadIdx.x;
   const int list = (int)blockIdx.x >= p.grid - 1 ? kSmall : kWhole;
-  const int c = (int)blockIdx.x + 1 - (list ? p.grid - 1 : 0);
+  const int c = (int)blockIdx.x - (list ? p.grid - 1 : 0);  // the unit starts in stretch c
   const PackedStart* starts = p.starts[list];
-  const PackedStart s = starts[c], before_s = starts[c - 1];
+  const PackedStart before_s = starts[c], s = starts[c + 1];
   if (s.tile == 0 || (before_s.unit == s.unit && before_s.tile > 0)) return;
+  const int end = stretches(p, list);
+  if (tid == 0) s_parts = end - c;
+  __syncthreads();
+  for (int i = c + tid; i <= end; i += kMergeThreads) {
+    const PackedStart x = starts[i];
+    s_starts[i - c] = x;
+    if (i > c && (x.unit != s.unit || x.tile == 0)) atomicMin(&s_parts, i - c);
+  }
   const int entries = p.header->entries[list];
   const int hg = s.unit / entries;
   const PackedEntry e = p.entries[list][s.unit - hg * entries];
-  const int rows = slot_rows(list);
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 16); i += 256 * gridDim.y) {
-    const int row = i % rows, c16 = i / rows;
-    int token, head;
-    if (!row_of(p, e, hg, row, &token, &head)) continue;
-    Merge m;
-    add_slots<D>(p, list, starts, m, s.unit, c - 1, row, c16);
-    write_row<D>(p, m, token, head, c16);
-  }
+  const int used = e.q_len > p.tile_tokens ? 2 * kTileM : e.q_len * p.group_heads;
+  int n_rows = 1;
+  while (n_rows < used) n_rows *= 2;
+  const int row = tid & (n_rows - 1), share = tid / n_rows;
+  __syncthreads();
+  const int shares = s_parts > 4 ? min(kMergeThreads / n_rows, s_parts) : 1;
+  int token, head;
+  const bool ok = row_of(p, e, hg, row, &token, &head) && share < shares;
+  Merge m;
+  if (ok) add_slots<D, 2>(p, list, s_starts, m, s.unit, c, share, shares, row, blockIdx.y);
+  write_rows<D>(p, sh, m, n_rows, shares, ok, token, head, blockIdx.y);
 }
 
 // The last stretch that starts at or before the unit's first tile.
@@ -273,68 +363,78 @@ __device__ __forceinline__ int stretch_of(const PackedStart* starts, int number,
   return lo;
 }
 
-// The last entry of [lo, hi) that starts at or before the token; -1 if the token is not in it.
-__device__ __forceinline__ int entry_of(const PackedEntry* e, int lo, int hi, int token) {
-  if (lo >= hi) return -1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (e[mid].q_row <= token) lo = mid; else hi = mid;
-  }
-  const int at = token - e[lo].q_row;
-  return at >= 0 && at < e[lo].q_len ? lo : -1;
-}
-
 // All rows of the sequences, each from its part over the prefix and its part
 // over the sequence's own keys (one row each where the unit was not cut).  A
-// thread takes 16 channels of a row; rows are taken token by token, so that the
-// threads of a CTA are of few units and find them in the same places.
-constexpr int kJoinStarts = 1024;  // starts kept in shared memory
+// CTA takes rows / H tokens at a time (or `rows` heads of one) and 16 channels,
+// blockIdx.y; heads come first, so that a group's rows are read side by side.
 template <int D>
-__global__ void __launch_bounds__(256) fa_packed_join_kernel(const PackedFwd p) {
-  __shared__ PackedStart s_starts[kJoinStarts];
+__global__ void __launch_bounds__(kMergeThreads) fa_packed_join_kernel(const PackedFwd p, int tokens, int n_rows) {
+  __shared__ PackedStart s_starts[3 * kMostGrid + 2];
+  __shared__ MergeShared sh;
+  __shared__ int s_own[kMergeThreads];  // the token's own block: entry and list; -1: of no sequence
+  const int tid = threadIdx.x;
+  const int c16 = blockIdx.y;
+  const int shares = kMergeThreads / n_rows, share = tid / n_rows;
   pdl_wait();
-  const PackedStart* starts[2] = {p.starts[0], p.starts[1]};
-  if (3 * p.grid + 2 <= kJoinStarts) {
-    for (int i = threadIdx.x; i < 3 * p.grid + 2; i += 256)
-      s_starts[i] = i <= p.grid ? p.starts[0][i] : p.starts[1][i - p.grid - 1];
-    starts[0] = s_starts;
-    starts[1] = s_starts + p.grid + 1;
-  }
+  for (int i = tid; i < 3 * p.grid + 2; i += kMergeThreads)
+    s_starts[i] = i <= p.grid ? p.starts[0][i] : p.starts[1][i - p.grid - 1];
   const PackedHeader h = *p.header;
-  __syncthreads();
   const int block = 2 * p.tile_tokens;
-  constexpr int kPer = D / 16;
-  const long long tasks = (long long)h.rows * p.H * kPer;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < tasks; i += 256LL * gridDim.x) {
-    const int c16 = (int)(i % kPer);
-    const long long r = i / kPer;
-    const int at = (int)(r / p.H), head = (int)(r - (long long)at * p.H);
-    const int token = h.first + at;
-    // The own block (a token of no sequence has none).
-    int own_list = kWhole, own = entry_of(p.entries[kWhole], h.over[kWhole], h.entries[kWhole], token);
-    if (own < 0) own_list = kSmall, own = entry_of(p.entries[kSmall], h.over[kSmall], h.entries[kSmall], token);
-    if (own < 0) continue;
-    const int hk = head / p.group, g = head - hk * p.group;
-    const int hg = hk * p.chunks + g / p.group_heads, gh = g % p.group_heads;
-    const int over = at / block;  // the block over the prefix
-    Merge m;
+  for (int at0 = blockIdx.x * tokens; at0 < h.rows; at0 += gridDim.x * tokens) {
+    const int n = min(tokens, h.rows - at0), t0 = h.first + at0;
+    if (tid < n) s_own[tid] = -1;
+    __syncthreads();
+    // Every thread looks whether an entry of its has one of the tokens.
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const int list = part ? own_list : over >= h.over[kWhole];
-      const int e = part ? own : list ? 0 : over;
-      const int t = part ? token - p.entries[list][own].q_row : at - over * block;
-      const int unit = hg * h.entries[list] + e;
-      const int c = stretch_of(starts[list], stretches(p, list), unit);
-      const PackedStart next = starts[list][c + 1];
-      if (next.unit == unit && next.tile > 0) {
-        const int row = t / p.tile_tokens * kTileM + t % p.tile_tokens * p.group_heads + gh;
-        add_slots<D>(p, list, starts[list], m, unit, c, row, c16);
-      } else {
-        const float4* o = reinterpret_cast<const float4*>(p.o_part + (((size_t)part * p.Tq + token) * p.H + head) * D) + 4 * c16;
-        m.add(p.lse_part[((size_t)part * p.H + head) * p.Tq + token], o, 1);
+    for (int list = 0; list < 2; ++list) {
+      const PackedEntry* e = p.entries[list];
+      int lo = h.over[list], hi = h.entries[list];
+      while (hi - lo > 1024) {  // the entry of t0, if there is one, stays within [lo, hi)
+        const int mid = (lo + hi) / 2;
+        if (e[mid].q_row <= t0) lo = mid; else hi = mid;
+      }
+      hi = min(hi + n, h.entries[list]);
+      for (int i = lo + tid; i < hi; i += kMergeThreads) {
+        const int a = max(e[i].q_row - t0, 0), b = min(e[i].q_row + e[i].q_len - t0, n);
+        for (int x = a; x < b; ++x) s_own[x] = 2 * i + list;
       }
     }
-    write_row<D>(p, m, token, head, c16);
+    __syncthreads();
+    for (int r0 = 0; r0 < n * p.H; r0 += n_rows) {
+      const int r = r0 + (tid & (n_rows - 1));
+      const int x = r / p.H, head = r - x * p.H;
+      const int at = at0 + x, token = t0 + x;
+      const bool ok = x < n && s_own[x] >= 0;
+      Merge m;
+      if (ok) {
+        const int own = s_own[x] >> 1, own_list = s_own[x] & 1;
+        const int hk = head / p.group, g = head - hk * p.group;
+        const int hg = hk * p.chunks + g / p.group_heads, gh = g % p.group_heads;
+        const int over = at / block;  // the block over the prefix
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const int list = part ? own_list : over >= h.over[kWhole];
+          const int e = part ? own : list ? 0 : over;
+          const int t = part ? token - p.entries[list][own].q_row : at - over * block;
+          const int unit = hg * h.entries[list] + e;
+          const int turn = part ? shares - 1 - share : share;  // the prefix's parts from the first share on
+          const PackedStart* starts = s_starts + (list ? p.grid + 1 : 0);
+          const int c = stretch_of(starts, stretches(p, list), unit);
+          const PackedStart next = starts[c + 1];
+          if (next.unit == unit && next.tile > 0) {
+            const int row = t / p.tile_tokens * kTileM + t % p.tile_tokens * p.group_heads + gh;
+            add_slots<D, 2>(p, list, starts + c, m, unit, c, turn, shares, row, c16);
+          } else if (turn == 0) {
+            const float4* o = reinterpret_cast<const float4*>(p.o_part + (((size_t)part * p.Tq + token) * p.H + head) * D) + 4 * c16;
+            const float4 v[4] = {o[0], o[1], o[2], o[3]};
+            m.add(p.lse_part[((size_t)part * p.H + head) * p.Tq + token], v);
+          }
+        }
+      }
+      write_rows<D>(p, sh, m, n_rows, shares, ok, token, head, c16);
+      if (shares > 1) __syncthreads();  // sh
+    }
+    __syncthreads();  // s_own
   }
 }
 
@@ -351,7 +451,7 @@ struct Call {
   PackedPlan plan;
   PackedFwd p;
   CUtensorMap tm[6];
-  int join_grid;
+  int join_grid, join_tokens, join_rows;
   cudaStream_t st;
 };
 
@@ -365,9 +465,11 @@ cudaError_t run_fwd(void* ctx) {
 }
 template <int D>
 cudaError_t merge_t(const Call& c) {
+  const dim3 block(fa::kMergeThreads);
   if (c.p.shared)
-    return fa::launch_pdl(fa::fa_packed_join_kernel<D>, dim3(c.join_grid), dim3(256), 0, c.st, c.p);
-  return fa::launch_pdl(fa::fa_packed_merge_kernel<D>, dim3(3 * c.p.grid - 2, D / 16), dim3(256), 0, c.st, c.p);
+    return fa::launch_pdl(fa::fa_packed_join_kernel<D>, dim3(c.join_grid, D / 16), block, 0, c.st, c.p, c.join_tokens,
+                          c.join_rows);
+  return fa::launch_pdl(fa::fa_packed_merge_kernel<D>, dim3(3 * c.p.grid - 2, D / 16), block, 0, c.st, c.p);
 }
 cudaError_t run_merge(void* ctx) {
   const Call& c = *static_cast<const Call*>(ctx);
@@ -455,7 +557,7 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   const long long key_tiles = prefix_tiles + (Tk + fa::kTileN - 1) / fa::kTileN;
   pl.min_tiles = 2;
   pl.whole = key_tiles <= 4 && !p.shared ? 1 : 0;
-  p.grid = (int)std::min<long long>(sm_count, entries * hgs * (pl.whole ? 1 : std::max(1LL, key_tiles / pl.min_tiles)));
+  p.grid = (int)std::min<long long>(std::min(sm_count, fa::kMostGrid), entries * hgs * (pl.whole ? 1 : std::max(1LL, key_tiles / pl.min_tiles)));
 
   // Workspace: the lists, then partial results.  Small blocks are the last of
   // their sequences (and one over the prefix).
@@ -542,7 +644,12 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   p.store32 = aligned32(o->ptr, p.o_row, p.o_head) ? 1 : 0;
   p.status = status;
   p.timeout_ns = fa::internal_wait_timeout_ns();
-  c.join_grid = (int)std::min<long long>(((long long)Tq * H * (d / 16) + 255) / 256, 8LL * sm_count);
+  // Rows of a CTA of the join: all its threads', or fewer where these leave SMs over.
+  c.join_rows = fa::kMergeThreads;
+  while (c.join_rows > 8 && (long long)Tq * H / c.join_rows * (d / 16) < 2 * sm_count) c.join_rows /= 2;
+  c.join_tokens = std::max(1, c.join_rows / H);
+  c.join_grid = (Tq + c.join_tokens - 1) / c.join_tokens;
+  c.join_grid = std::min(c.join_grid, sm_count);
 
   cudaError_t ce = fa::internal_timed_launch(FA_KERNEL_PACKED_PLAN, c.st, run_plan, &c);
   if (ce == cudaSuccess) ce = fa::internal_timed_launch(FA_KERNEL_PACKED_FWD, c.st, run_fwd, &c);

@@ -730,8 +730,11 @@ static cudaError_t launch_t(const CUtensorMap* tm, const PackedFwd& p, cudaStrea
   const cudaError_t e =
       cudaFuncSetAttribute(fa_packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fa_packed_fwd_kernel<D>, dim3(p.grid), dim3(C::kThreads), C::kSmemBytes, stream, tm[0], tm[1], tm[2],
-                    tm[3], tm[4], tm[5], p);
+  // Two CTAs of a cluster run on a pair of SMs.  Where one of a pair takes whole
+  // blocks and the other small ones, each in code of its own, the first takes 5 to
+  // 8 % longer; so pairs stay together, and the plan gives both the same list.
+  return launch_pdl_clusters(p.grid % 2 == 0 ? 2 : 1, fa_packed_fwd_kernel<D>, dim3(p.grid), dim3(C::kThreads),
+                             C::kSmemBytes, stream, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], p);
 }
 
 // tm: Q, K, V, K and V of the prefix (any map where there is none), O (any map

@@ -38,12 +38,13 @@
 namespace fa {
 
 constexpr int kSlotRows = 256;   // query rows of a whole block; half of it of a small one
+constexpr int kMostGrid = 340;   // CTAs of the forward kernel: the merges keep their starts in shared memory
 
 // Places of a key tile and of a unit's start and end, in a quarter of a tile of a
 // whole block (1.4 us at d = 128; a unit costs 3.5 to 4 us more).  Small blocks
 // run two at a time.
-__host__ __device__ constexpr int tile_places(int list) { return list ? 3 : 4; }
-__host__ __device__ constexpr int unit_places(int list) { return list ? 3 : 11; }
+__host__ __device__ constexpr int tile_places(int list) { return list ? 6 : 8; }
+__host__ __device__ constexpr int unit_places(int list) { return list ? 6 : 16; }
 
 struct PackedEntry {
   int q_row, q_len;  // first token and tokens of the block
