@@ -314,42 +314,68 @@ __device__ __forceinline__ bool row_of(const PackedFwd& p, const PackedEntry& e,
 
 }  // namespace
 
+// What the plan wrote may be read ahead of the wait for the forward kernel: that
+// lets its dependents start only once it has seen the plan.  (Past the L1 cache,
+// which no launch has emptied for it.)
+__device__ __forceinline__ PackedStart read_start(const PackedStart* s) {
+  const int2 v = __ldcg(reinterpret_cast<const int2*>(s));
+  return PackedStart{v.x, v.y};
+}
+__device__ __forceinline__ PackedEntry read_entry(const PackedEntry* e) {
+  const int4 a = __ldcg(reinterpret_cast<const int4*>(e)), b = __ldcg(reinterpret_cast<const int4*>(e) + 1);
+  return PackedEntry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
 // Units that were cut: one for each stretch that starts within a unit that no
-// stretch before it starts within.  blockIdx.y: 16 channels.
+// stretch before it starts within.  A CTA takes 16 channels of a unit, or all of
+// a small block in few parts.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) fa_packed_merge_kernel(const PackedFwd p) {
   __shared__ PackedStart s_starts[2 * kMostGrid + 2];
   __shared__ MergeShared sh;
   __shared__ int s_parts;
-  pdl_wait();
+  constexpr int kPer = D / 16;
   const int tid = threadIdx.x;
   const int list = (int)blockIdx.x >= p.grid - 1 ? kSmall : kWhole;
   const int c = (int)blockIdx.x - (list ? p.grid - 1 : 0);  // the unit starts in stretch c
   const PackedStart* starts = p.starts[list];
-  const PackedStart before_s = starts[c], s = starts[c + 1];
-  if (s.tile == 0 || (before_s.unit == s.unit && before_s.tile > 0)) return;
+  const PackedStart before_s = read_start(starts + c), s = read_start(starts + c + 1);
+  if (s.tile == 0 || (before_s.unit == s.unit && before_s.tile > 0)) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();  // one waits, so that this grid does not end ahead of the one before it
+    return;
+  }
   const int end = stretches(p, list);
   if (tid == 0) s_parts = end - c;
   __syncthreads();
   for (int i = c + tid; i <= end; i += kMergeThreads) {
-    const PackedStart x = starts[i];
+    const PackedStart x = read_start(starts + i);
     s_starts[i - c] = x;
     if (i > c && (x.unit != s.unit || x.tile == 0)) atomicMin(&s_parts, i - c);
   }
-  const int entries = p.header->entries[list];
+  const int entries = __ldcg(&p.header->entries[list]);
   const int hg = s.unit / entries;
-  const PackedEntry e = p.entries[list][s.unit - hg * entries];
+  const PackedEntry e = read_entry(p.entries[list] + (s.unit - hg * entries));
   const int used = e.q_len > p.tile_tokens ? 2 * kTileM : e.q_len * p.group_heads;
   int n_rows = 1;
   while (n_rows < used) n_rows *= 2;
-  const int row = tid & (n_rows - 1), share = tid / n_rows;
   __syncthreads();
-  const int shares = s_parts > 4 ? min(kMergeThreads / n_rows, s_parts) : 1;
+  const bool few = s_parts <= 4;
+  const bool all = list && few;
+  if (all && blockIdx.y > 0) return;  // (the first of these waits)
+  const int per = all ? min(kPer, kMergeThreads / n_rows) : 1;  // of 16 channels, at a time
+  const int row = tid & (n_rows - 1), channels = tid / n_rows % per, share = tid / (n_rows * per);
+  const int shares = few ? 1 : min(kMergeThreads / n_rows, s_parts);
   int token, head;
-  const bool ok = row_of(p, e, hg, row, &token, &head) && share < shares;
-  Merge m;
-  if (ok) add_slots<D, 2>(p, list, s_starts, m, s.unit, c, share, shares, row, blockIdx.y);
-  write_rows<D>(p, sh, m, n_rows, shares, ok, token, head, blockIdx.y);
+  const bool row_ok = row_of(p, e, hg, row, &token, &head) && share < shares;
+  pdl_wait();
+  for (int at = blockIdx.y; at < (all ? kPer : (int)blockIdx.y + 1); at += per) {
+    const int c16 = at + channels;
+    const bool ok = row_ok && c16 < kPer;
+    Merge m;
+    if (ok) add_slots<D, 2>(p, list, s_starts, m, s.unit, c, share, shares, row, c16);
+    write_rows<D>(p, sh, m, n_rows * per, shares, ok, token, head, c16);
+    if (shares > 1) __syncthreads();  // sh
+  }
 }
 
 // The last stretch that starts at or before the unit's first tile.
@@ -368,17 +394,20 @@ __device__ __forceinline__ int stretch_of(const PackedStart* starts, int number,
 // CTA takes rows / H tokens at a time (or `rows` heads of one) and 16 channels,
 // blockIdx.y; heads come first, so that a group's rows are read side by side.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) fa_packed_join_kernel(const PackedFwd p, int tokens, int n_rows) {
+__global__ void __launch_bounds__(kMergeThreads, 3) fa_packed_join_kernel(const PackedFwd p, int tokens, int n_rows) {
   __shared__ PackedStart s_starts[3 * kMostGrid + 2];
   __shared__ MergeShared sh;
   __shared__ int s_own[kMergeThreads];  // the token's own block: entry and list; -1: of no sequence
   const int tid = threadIdx.x;
   const int c16 = blockIdx.y;
   const int shares = kMergeThreads / n_rows, share = tid / n_rows;
-  pdl_wait();
   for (int i = tid; i < 3 * p.grid + 2; i += kMergeThreads)
-    s_starts[i] = i <= p.grid ? p.starts[0][i] : p.starts[1][i - p.grid - 1];
-  const PackedHeader h = *p.header;
+    s_starts[i] = read_start(i <= p.grid ? p.starts[0] + i : p.starts[1] + (i - p.grid - 1));
+  __shared__ PackedHeader h;
+  static_assert(sizeof(PackedHeader) == 6 * sizeof(int), "copied as words");
+  if (tid < 6) reinterpret_cast<int*>(&h)[tid] = __ldcg(reinterpret_cast<const int*>(p.header) + tid);
+  __syncthreads();
+  bool waited = false;
   const int block = 2 * p.tile_tokens;
   for (int at0 = blockIdx.x * tokens; at0 < h.rows; at0 += gridDim.x * tokens) {
     const int n = min(tokens, h.rows - at0), t0 = h.first + at0;
@@ -391,15 +420,18 @@ __global__ void __launch_bounds__(kMergeThreads) fa_packed_join_kernel(const Pac
       int lo = h.over[list], hi = h.entries[list];
       while (hi - lo > 1024) {  // the entry of t0, if there is one, stays within [lo, hi)
         const int mid = (lo + hi) / 2;
-        if (e[mid].q_row <= t0) lo = mid; else hi = mid;
+        if (__ldcg(&e[mid].q_row) <= t0) lo = mid; else hi = mid;
       }
       hi = min(hi + n, h.entries[list]);
       for (int i = lo + tid; i < hi; i += kMergeThreads) {
-        const int a = max(e[i].q_row - t0, 0), b = min(e[i].q_row + e[i].q_len - t0, n);
+        const int2 row_len = __ldcg(reinterpret_cast<const int2*>(e + i));
+        const int a = max(row_len.x - t0, 0), b = min(row_len.x + row_len.y - t0, n);
         for (int x = a; x < b; ++x) s_own[x] = 2 * i + list;
       }
     }
     __syncthreads();
+    if (!waited) pdl_wait();
+    waited = true;
     for (int r0 = 0; r0 < n * p.H; r0 += n_rows) {
       const int r = r0 + (tid & (n_rows - 1));
       const int x = r / p.H, head = r - x * p.H;
@@ -411,7 +443,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_packed_join_kernel(const Pac
         const int hk = head / p.group, g = head - hk * p.group;
         const int hg = hk * p.chunks + g / p.group_heads, gh = g % p.group_heads;
         const int over = at / block;  // the block over the prefix
-#pragma unroll
+#pragma unroll 1
         for (int part = 0; part < 2; ++part) {
           const int list = part ? own_list : over >= h.over[kWhole];
           const int e = part ? own : list ? 0 : over;
@@ -436,6 +468,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_packed_join_kernel(const Pac
     }
     __syncthreads();  // s_own
   }
+  if (!waited) pdl_wait();
 }
 
 }  // namespace fa
