@@ -37,12 +37,66 @@ __device__ __forceinline__ bool before(const PackedStart& a, const PackedStart& 
 // Sequences and entries up to this number have their places in shared memory.
 constexpr int kPlanShared = 1024;
 
+// Where the CTAs' stretches start, once the entries' places are summed up: cum[e]
+// is what lies ahead of entry e, the small blocks' behind the whole ones'.  T: an
+// unsigned word where the places of all head groups fit, else 64 bits, whose
+// divisions take 2000 cycles more.
+template <typename T>
+__device__ __forceinline__ void plan_starts(const PackedPlan& p, const long long* cum, const int (&entries)[2]) {
+  const int tid = threadIdx.x;
+  const T total[2] = {(T)cum[entries[0]], (T)(cum[entries[0] + entries[1]] - cum[entries[0]])};
+  // Place `at` of a list as unit and tile.  A cut near a unit's border moves there.
+  auto locate = [&](int list, T at) -> PackedStart {
+    const T all = list ? total[1] : total[0];
+    const int n_entries = list ? entries[1] : entries[0], base = list ? entries[0] : 0;
+    if (at >= all * (T)p.head_groups) return PackedStart{p.head_groups * n_entries, 0};
+    const int hg = (int)(at / all);
+    const long long r = (long long)(at - (T)hg * all) + cum[base];
+    int lo = base, hi = base + n_entries;  // cum[lo] <= r < cum[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (cum[mid] <= r) lo = mid; else hi = mid;
+    }
+    const int size = (int)(cum[lo + 1] - cum[lo]), in = (int)(r - cum[lo]);
+    const int n = (size - unit_places(list)) / tile_places(list);
+    int x = in / tile_places(list);
+    const int least = p.whole ? n + 1 : p.min_tiles;
+    if (x < least && 2 * in < size) x = 0;
+    else if (x < least || x > n - least) x = 0, ++lo;
+    return PackedStart{hg * n_entries + lo - base, x};
+  };
+  const T whole = total[0] * (T)p.head_groups, all = whole + total[1] * (T)p.head_groups;
+  // A CTA that takes of both lists fills its pipeline twice (10 to 25 us more at
+  // d = 128), and a pair of SMs that runs both slows down: pairs of CTAs take one
+  // list where that makes no stretch longer by a 16th.
+  const int apart = all > 0 ? 2 * (int)((float)whole / (float)all * 0.5f * (float)p.grid + 0.5f) : 0;
+  const int behind = p.grid - apart;
+  const T even = all / (T)p.grid;
+  const bool split = whole > 0 && all > whole && apart > 0 && behind > 0 &&
+                     max(whole / (T)apart, (all - whole) / (T)behind) <= even + even / 16;
+  auto part = [](T sum, T n, T c) { return sum / n * c + sum % n * c / n; };
+  auto edge = [&](int c) -> T {
+    if (c >= p.grid) return all;
+    if (!split) return part(all, p.grid, c);
+    return c < apart ? part(whole, apart, c) : whole + part(all - whole, behind, c - apart);
+  };
+  auto behind_whole = [&](T x) { return x > whole ? x - whole : T(0); };
+  for (int i = tid; i < 3 * p.grid + 2; i += kPlanThreads) {
+    if (i <= p.grid) {
+      p.starts[kWhole][i] = locate(kWhole, min(edge(i), whole));
+    } else {
+      const int v = i - p.grid - 1;
+      const T a = behind_whole(edge(v / 2)), b = behind_whole(edge(v / 2 + 1));
+      p.starts[kSmall][v] = locate(kSmall, v & 1 ? a + (b - a) / 2 : a);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const PackedPlan p) {
-  __shared__ long long s_warps[32];
-  __shared__ long long s_carry;
+  __shared__ long long s_warps[2][32];
   __shared__ Seq s_seq[kPlanShared];
   __shared__ int s_base[2][kPlanShared + 1];
-  __shared__ long long s_cum[2][kPlanShared + 1];
+  __shared__ long long s_cum[kPlanShared + 1];
   const int tid = threadIdx.x;
   pdl_trigger();
   pdl_wait();
@@ -50,8 +104,9 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
   const bool few = p.s.B <= kPlanShared;
   int* const base0 = few ? s_base[0] : p.seq_base[0];
   int* const base1 = few ? s_base[1] : p.seq_base[1];
+  Scan<long long> scan(s_warps);
   // Entries of the sequences, by list: [base[b], base[b + 1]).  Both numbers in one sum.
-  long long own = 0;
+  long long own = 0, more;
   for (int b0 = 0; b0 < p.s.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     long long n = 0;
@@ -61,15 +116,12 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
       const int rest = s.q_len % block;
       n = ((long long)(rest > 0 && rest <= p.tile_tokens) << 32) + s.q_len / block + (rest > p.tile_tokens);
     }
-    const long long sum = own + scan_block<long long>(n, s_warps);
+    const long long sum = own + scan(n, &more);
     if (b < p.s.B) {
       base0[b + 1] = (int)(sum & 0xffffffffLL);
       base1[b + 1] = (int)(sum >> 32);
     }
-    if (tid == kPlanThreads - 1) s_carry = sum;
-    __syncthreads();
-    own = s_carry;
-    __syncthreads();
+    own += more;
   }
   if (tid == 0) base0[0] = base1[0] = 0;
   // Blocks over the prefix alone: all rows from the first sequence's first to
@@ -85,90 +137,50 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
   over[kSmall] = rest > 0 && rest <= p.tile_tokens;
   entries[kWhole] = over[kWhole] + (int)(own & 0xffffffffLL);
   entries[kSmall] = over[kSmall] + (int)(own >> 32);
+  const int both = entries[kWhole] + entries[kSmall];
+  long long* const cum = both <= kPlanShared ? s_cum : p.cum;
   __syncthreads();  // base
-  long long total[2];
-#pragma unroll
-  for (int list = 0; list < 2; ++list) {
-    const int* base = list ? base1 : base0;
-    long long* cum = entries[list] <= kPlanShared ? s_cum[list] : p.cum[list];
-    long long sum_all = 0;
-    for (int e0 = 0; e0 < entries[list]; e0 += kPlanThreads) {
-      const int e = e0 + tid;
-      long long places = 0;
-      if (e < entries[list]) {
-        PackedEntry x;
-        if (e < over[list]) {
-          const int t0 = (list ? over[kWhole] : e) * block;
-          x = PackedEntry{first + t0, min(block, rows - t0), 0, 0, p.prefix_tiles, p.prefix_tiles, 0, 1};
-        } else {
-          const int i = e - over[list];
-          const int b = seq_of(base, p.s.B, i);
-          const Seq s = few ? s_seq[b] : load_seq(p.s, b);
-          const int t0 = (list ? base0[b + 1] - base0[b] : i - base[b]) * block;
-          x.q_row = s.q + t0;
-          x.q_len = min(block, s.q_len - t0);
-          x.k_row = s.k;
-          x.k_len = s.k_len;
-          x.prefix = p.shared ? 0 : p.prefix_tiles;
-          x.pos = t0 + (p.s.causal == FA_CAUSAL_BOTTOM_RIGHT ? s.k_len - s.q_len : 0);
-          const int seen = p.s.causal == FA_CAUSAL_NONE ? s.k_len : min(s.k_len, max(0, x.pos + x.q_len));
-          x.tiles = x.prefix + (seen + kTileN - 1) / kTileN;
-          x.kind = 0;
-        }
-        p.entries[list][e] = x;
-        places = (long long)x.tiles * tile_places(list) + unit_places(list);
+  long long places_all = 0;
+  for (int e0 = 0; e0 < both; e0 += kPlanThreads) {
+    const int at = e0 + tid;
+    long long places = 0;
+    if (at < both) {
+      const int list = at >= entries[kWhole];
+      const int e = list ? at - entries[kWhole] : at, n_over = list ? over[kSmall] : over[kWhole];
+      PackedEntry x;
+      if (e < n_over) {
+        const int t0 = (list ? over[kWhole] : e) * block;
+        x = PackedEntry{first + t0, min(block, rows - t0), 0, 0, p.prefix_tiles, p.prefix_tiles, 0, 1};
+      } else {
+        const int* base = list ? base1 : base0;
+        const int i = e - n_over;
+        const int b = seq_of(base, p.s.B, i);
+        const Seq s = few ? s_seq[b] : load_seq(p.s, b);
+        const int t0 = (list ? base0[b + 1] - base0[b] : i - base[b]) * block;
+        x.q_row = s.q + t0;
+        x.q_len = min(block, s.q_len - t0);
+        x.k_row = s.k;
+        x.k_len = s.k_len;
+        x.prefix = p.shared ? 0 : p.prefix_tiles;
+        x.pos = t0 + (p.s.causal == FA_CAUSAL_BOTTOM_RIGHT ? s.k_len - s.q_len : 0);
+        const int seen = p.s.causal == FA_CAUSAL_NONE ? s.k_len : min(s.k_len, max(0, x.pos + x.q_len));
+        x.tiles = x.prefix + (seen + kTileN - 1) / kTileN;
+        x.kind = 0;
       }
-      const long long sum = sum_all + scan_block<long long>(places, s_warps);
-      if (e < entries[list]) cum[e + 1] = sum;
-      if (tid == kPlanThreads - 1) s_carry = sum;
-      __syncthreads();
-      sum_all = s_carry;
-      __syncthreads();
+      (list ? p.entries[kSmall] : p.entries[kWhole])[e] = x;
+      places = (long long)x.tiles * tile_places(list) + unit_places(list);
     }
-    if (tid == 0) cum[0] = 0;
-    total[list] = sum_all;
+    const long long sum = places_all + scan(places, &more);
+    if (at < both) cum[at + 1] = sum;
+    places_all += more;
   }
-  if (tid == 0) *p.header = PackedHeader{{entries[0], entries[1]}, {over[0], over[1]}, first, rows};
-  __syncthreads();
-  // Place `at` of a list as unit and tile.  A cut near a unit's border moves there.
-  auto locate = [&](int list, long long at) -> PackedStart {
-    const long long all = total[list];
-    if (at >= all * p.head_groups) return PackedStart{p.head_groups * entries[list], 0};
-    const long long* cum = entries[list] <= kPlanShared ? s_cum[list] : p.cum[list];
-    const int hg = (int)(at / all);
-    const long long r = at - hg * all;
-    int lo = 0, hi = entries[list];  // cum[lo] <= r < cum[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (cum[mid] <= r) lo = mid; else hi = mid;
-    }
-    const int size = (int)(cum[lo + 1] - cum[lo]), in = (int)(r - cum[lo]);
-    const int n = (size - unit_places(list)) / tile_places(list);
-    int x = in / tile_places(list);
-    const int least = p.whole ? n + 1 : p.min_tiles;
-    if (x < least && 2 * in < size) x = 0;
-    else if (x < least || x > n - least) x = 0, ++lo;
-    return PackedStart{hg * entries[list] + lo, x};
-  };
-  const long long whole = total[kWhole] * p.head_groups, all = whole + total[kSmall] * p.head_groups;
-  // A CTA that takes of both lists fills its pipeline twice (10 to 25 us more at
-  // d = 128), and a pair of SMs that runs both slows down: pairs of CTAs take one
-  // list where that makes no stretch longer by a 16th.
-  const int apart = 2 * (int)((whole * p.grid + all) / max(2 * all, 1LL));
-  const int behind = p.grid - apart;
-  const bool split = whole > 0 && all > whole && apart > 0 && behind > 0 &&
-                     max(whole / apart, (all - whole) / behind) <= all / p.grid + all / p.grid / 16;
-  auto part = [](long long sum, int n, int c) { return sum / n * c + sum % n * c / n; };
-  auto edge = [&](int c) {
-    if (c >= p.grid) return all;
-    if (!split) return part(all, p.grid, c);
-    return c < apart ? part(whole, apart, c) : whole + part(all - whole, behind, c - apart);
-  };
-  for (int c = tid; c <= p.grid; c += kPlanThreads) p.starts[kWhole][c] = locate(kWhole, min(edge(c), whole));
-  for (int v = tid; v <= 2 * p.grid; v += kPlanThreads) {
-    const long long a = max(0LL, edge(v / 2) - whole), b = max(0LL, edge(v / 2 + 1) - whole);
-    p.starts[kSmall][v] = locate(kSmall, v & 1 ? a + (b - a) / 2 : a);
+  if (tid == 0) {
+    cum[0] = 0;
+    *p.header = PackedHeader{{entries[0], entries[1]}, {over[0], over[1]}, first, rows};
   }
+  __syncthreads();  // cum
+  if (places_all * p.head_groups < 0x7fffffffLL) plan_starts<unsigned>(p, cum, entries);
+  else plan_starts<unsigned long long>(p, cum, entries);
 }
 
 // Partial results of a unit, merged for one row and 16 channels at a time:
@@ -596,7 +608,7 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   // their sequences (and one over the prefix).
   const long long small = (long long)std::min(B, Tq) + 1;
   const size_t n_entries[2] = {up((size_t)entries * sizeof(fa::PackedEntry)), up((size_t)small * sizeof(fa::PackedEntry))};
-  const size_t n_cum[2] = {up((size_t)(entries + 1) * sizeof(long long)), up((size_t)(small + 1) * sizeof(long long))};
+  const size_t n_cum = up((size_t)(entries + small + 1) * sizeof(long long));
   const size_t n_base = up(((size_t)B + 1) * sizeof(int));
   const size_t n_starts[2] = {up(((size_t)p.grid + 1) * sizeof(fa::PackedStart)),
                               up(((size_t)2 * p.grid + 1) * sizeof(fa::PackedStart))};
@@ -607,7 +619,7 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
     slot_rows[1] = (size_t)4 * p.grid * (fa::kSlotRows / 2);
   }
   const size_t part_rows = p.shared ? (size_t)2 * Tq * H : 0;
-  const size_t bytes = n_entries[0] + n_entries[1] + n_cum[0] + n_cum[1] + 2 * n_base + n_starts[0] + n_starts[1] +
+  const size_t bytes = n_entries[0] + n_entries[1] + n_cum + 2 * n_base + n_starts[0] + n_starts[1] +
                        up(sizeof(fa::PackedHeader)) + up(slot_rows[0] * (d + 1) * 4) + up(slot_rows[1] * (d + 1) * 4) +
                        part_rows * (d + 1) * 4;
   c.st = static_cast<cudaStream_t>(stream);
@@ -639,11 +651,11 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
     return FA_ERR_NO_MEMORY;
   }
   char* at = static_cast<char*>(ws);
+  pl.cum = reinterpret_cast<long long*>(at);
+  at += n_cum;
   for (int list = 0; list < 2; ++list) {
     p.entries[list] = pl.entries[list] = reinterpret_cast<fa::PackedEntry*>(at);
     at += n_entries[list];
-    pl.cum[list] = reinterpret_cast<long long*>(at);
-    at += n_cum[list];
     pl.seq_base[list] = reinterpret_cast<int*>(at);
     at += n_base;
     p.starts[list] = pl.starts[list] = reinterpret_cast<fa::PackedStart*>(at);

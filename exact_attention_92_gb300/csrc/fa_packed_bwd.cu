@@ -35,7 +35,7 @@ cudaError_t launch_bwd_packed_dq(int d, const CUtensorMap& tq, const CUtensorMap
 struct PackedBwdPlan {
   PackedSeqs s;
   int kv_block;       // keys of a dK/dV unit: 128 or 256
-  int* seq_base;      // [B + 1]
+  int* seq_base[2];   // [B + 1] first entry of each sequence, of either list (where it does not fit shared memory)
   BwdEntry* entries_kv;
   BwdEntry* entries_q;
   int* counts;        // entries of the two lists
@@ -44,13 +44,22 @@ struct PackedBwdPlan {
 namespace {
 
 constexpr int kBuckets = 2048;
+constexpr int kPlanShared = 1024;  // sequences up to this number have their places in shared memory
+
+struct BwdPlanShared {
+  long long warps[2][32];
+  Seq seq[kPlanShared];
+  int base[kPlanShared + 1];
+  int bucket[kBuckets];
+  int most;
+};
 
 // Entry i of a list: KV, the i-th key block, else the i-th query tile.
 template <bool KV>
-__device__ __forceinline__ BwdEntry make_entry(const PackedBwdPlan& p, int i) {
-  const int b = seq_of(p.seq_base, p.s.B, i);
-  const Seq s = load_seq(p.s, b);
-  BwdEntry e{s.q, s.q_len, s.k, s.k_len, i - p.seq_base[b], 0, 0, 0};
+__device__ __forceinline__ BwdEntry make_entry(const PackedBwdPlan& p, const Seq* seq, const int* base, int i) {
+  const int b = seq_of(base, p.s.B, i);
+  const Seq s = seq != nullptr ? seq[b] : load_seq(p.s, b);
+  BwdEntry e{s.q, s.q_len, s.k, s.k_len, i - base[b], 0, 0, 0};
   e.off = p.s.causal == FA_CAUSAL_BOTTOM_RIGHT ? s.k_len - s.q_len : 0;
   const bool causal = p.s.causal != FA_CAUSAL_NONE;
   if (KV) {
@@ -67,65 +76,64 @@ __device__ __forceinline__ BwdEntry make_entry(const PackedBwdPlan& p, int i) {
 
 // One list, heaviest entries first (a counting sort; entries of equal count in any order).
 template <bool KV>
-__device__ void make_list(const PackedBwdPlan& p, BwdEntry* out, int* count, long long* s_warps, long long* s_carry,
-                          int* s_bucket, int* s_most) {
+__device__ void make_list(const PackedBwdPlan& p, int* far_base, BwdEntry* out, int* count, BwdPlanShared& sh) {
   const int tid = threadIdx.x;
   const int block = KV ? p.kv_block : kTileM;
-  int n = 0;
+  const bool few = p.s.B <= kPlanShared;
+  int* const base = few ? sh.base : far_base;
+  const Seq* const seq = few ? sh.seq : nullptr;
+  Scan<long long> scan(sh.warps);
+  if (tid == 0) sh.most = 0;
+  for (int i = tid; i < kBuckets; i += kPlanThreads) sh.bucket[i] = 0;
+  long long n_all = 0, more;
+  int most = 0;  // no entry has more steps: those of a sequence without a mask
   for (int b0 = 0; b0 < p.s.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     int tiles = 0;
     if (b < p.s.B) {
       const Seq s = load_seq(p.s, b);
+      if (few) sh.seq[b] = s;
       tiles = ((KV ? s.k_len : s.q_len) + block - 1) / block;
+      if (tiles > 0) most = max(most, ((KV ? s.q_len : s.k_len) + kTileM - 1) / kTileM);
     }
-    const int sum = (int)scan_block<long long>(tiles, s_warps);
-    if (b < p.s.B) p.seq_base[b + 1] = n + sum;
-    if (tid == kPlanThreads - 1) *s_carry = n + sum;
-    __syncthreads();
-    n = (int)*s_carry;
-    __syncthreads();
+    const long long sum = n_all + scan(tiles, &more);
+    if (b < p.s.B) base[b + 1] = (int)sum;
+    n_all += more;
   }
+  const int n = (int)n_all;
   if (tid == 0) {
-    p.seq_base[0] = 0;
+    base[0] = 0;
     *count = n;
-    *s_most = 0;
   }
-  for (int i = tid; i < kBuckets; i += kPlanThreads) s_bucket[i] = 0;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if ((tid & 31) == 0) atomicMax(&sh.most, most);
   __syncthreads();
-  int most = 0;
-  for (int i = tid; i < n; i += kPlanThreads) most = max(most, make_entry<KV>(p, i).count);
-  atomicMax(s_most, most);
-  __syncthreads();
-  most = *s_most;
+  most = sh.most;
   // Bucket 0 holds the heaviest.
   auto bucket = [&](int c) { return most < kBuckets ? most - c : (int)((long long)(most - c) * (kBuckets - 1) / most); };
-  for (int i = tid; i < n; i += kPlanThreads) atomicAdd(&s_bucket[bucket(make_entry<KV>(p, i).count)], 1);
+  for (int i = tid; i < n; i += kPlanThreads) atomicAdd(&sh.bucket[bucket(make_entry<KV>(p, seq, base, i).count)], 1);
   __syncthreads();
   // Where each bucket starts: two buckets a thread.
-  const int a0 = s_bucket[2 * tid], a1 = s_bucket[2 * tid + 1];
-  const int end = (int)scan_block<long long>(a0 + a1, s_warps);
-  s_bucket[2 * tid] = end - a1 - a0;
-  s_bucket[2 * tid + 1] = end - a1;
+  const int a0 = sh.bucket[2 * tid], a1 = sh.bucket[2 * tid + 1];
+  const int end = (int)scan(a0 + a1, &more);
+  sh.bucket[2 * tid] = end - a1 - a0;
+  sh.bucket[2 * tid + 1] = end - a1;
   __syncthreads();
   for (int i = tid; i < n; i += kPlanThreads) {
-    const BwdEntry e = make_entry<KV>(p, i);
-    out[atomicAdd(&s_bucket[bucket(e.count)], 1)] = e;
+    const BwdEntry e = make_entry<KV>(p, seq, base, i);
+    out[atomicAdd(&sh.bucket[bucket(e.count)], 1)] = e;
   }
-  __syncthreads();
 }
 static_assert(kBuckets == 2 * kPlanThreads, "two buckets a thread");
 
 }  // namespace
 
+// A CTA for each list.
 __global__ void __launch_bounds__(kPlanThreads) fa_packed_bwd_plan_kernel(const PackedBwdPlan p) {
-  __shared__ long long s_warps[32];
-  __shared__ long long s_carry;
-  __shared__ int s_bucket[kBuckets];
-  __shared__ int s_most;
+  __shared__ BwdPlanShared sh;
   pdl_trigger();
-  make_list<true>(p, p.entries_kv, p.counts, s_warps, &s_carry, s_bucket, &s_most);
-  make_list<false>(p, p.entries_q, p.counts + 1, s_warps, &s_carry, s_bucket, &s_most);
+  if (blockIdx.x == 0) make_list<true>(p, p.seq_base[0], p.entries_kv, p.counts, sh);
+  else make_list<false>(p, p.seq_base[1], p.entries_q, p.counts + 1, sh);
 }
 
 // D = rowsum(dO * O) for rows of any strides, [H, Tq]: as fa_bwd_preprocess, the
@@ -202,7 +210,7 @@ struct Call {
 
 cudaError_t run_plan(void* ctx) {
   const Call& c = *static_cast<const Call*>(ctx);
-  fa::fa_packed_bwd_plan_kernel<<<1, fa::kPlanThreads, 0, c.st>>>(c.plan);
+  fa::fa_packed_bwd_plan_kernel<<<2, fa::kPlanThreads, 0, c.st>>>(c.plan);
   return cudaGetLastError();
 }
 template <int D>
@@ -272,7 +280,7 @@ extern "C" int fa_packed_bwd(const fa_rows_t* q, const fa_rows_t* k, const fa_ro
     return FA_ERR_CUDA;
 
   const size_t n_kv = up((size_t)kv_most * sizeof(fa::BwdEntry)), n_q = up((size_t)q_most * sizeof(fa::BwdEntry));
-  const size_t n_base = up(((size_t)B + 3) * sizeof(int)), n_d = (size_t)H * Tq * sizeof(float);
+  const size_t n_base = up((2 * ((size_t)B + 1) + 2) * sizeof(int)), n_d = (size_t)H * Tq * sizeof(float);
   c.st = static_cast<cudaStream_t>(stream);
   void* ws = nullptr;
   if (fa::internal_workspace(&ws, n_kv + n_q + n_base + n_d, c.st) != cudaSuccess) {
@@ -283,7 +291,8 @@ extern "C" int fa_packed_bwd(const fa_rows_t* q, const fa_rows_t* k, const fa_ro
   c.plan.entries_kv = reinterpret_cast<fa::BwdEntry*>(at);
   c.plan.entries_q = reinterpret_cast<fa::BwdEntry*>(at += n_kv);
   c.plan.counts = reinterpret_cast<int*>(at += n_q);
-  c.plan.seq_base = c.plan.counts + 2;
+  c.plan.seq_base[0] = c.plan.counts + 2;
+  c.plan.seq_base[1] = c.plan.seq_base[0] + B + 1;
   c.dvec = reinterpret_cast<float*>(at + n_base);
   c.plan.s = fa::PackedSeqs{cu_q, cu_k, nullptr, B, Tq, Tk, causal, status};
   c.plan.kv_block = kv_block;

@@ -89,7 +89,7 @@ struct PackedPlan {
   int whole;          // 1: no cuts
   int* seq_base[2];        // [B + 1] first entry of each sequence (where it does not fit shared memory)
   PackedEntry* entries[2];
-  long long* cum[2];       // [entries + 1] places ahead of each entry (likewise)
+  long long* cum;          // [entries of both + 1] places ahead of each entry (likewise)
   PackedStart* starts[2];  // [grid + 1], [2 grid + 1]
   PackedHeader* header;
 };

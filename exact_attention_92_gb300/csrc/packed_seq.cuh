@@ -32,31 +32,35 @@ __device__ __forceinline__ Seq load_seq(const PackedSeqs& s, int b) {
   return Seq{q0, q1 - q0, k0, n};
 }
 
-// Inclusive sum over the CTA; `warps` holds one value a warp.
+// Sums over a CTA: of the threads up to this one, and of all.  Two sets of words
+// taken in turn, so that one barrier a scan is enough.
 template <typename T>
-__device__ T scan_block(T v, T* warps) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+struct Scan {
+  T (*warps)[32];
+  int turn;
+  __device__ __forceinline__ explicit Scan(T (*w)[32]) : warps(w), turn(0) {}
+  __device__ __forceinline__ T operator()(T v, T* total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    T* sums = warps[turn];
+    turn ^= 1;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
-  }
-  if (lane == 31) warps[w] = v;
-  __syncthreads();
-  if (w == 0) {
-    T x = warps[lane];
+    for (int o = 1; o < 32; o <<= 1) {
+      const T x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    if (lane == 31) sums[w] = v;
+    __syncthreads();
+    T x = sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const T y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    warps[lane] = x;
+    *total = __shfl_sync(0xffffffffu, x, 31);
+    const T before = __shfl_sync(0xffffffffu, x, w > 0 ? w - 1 : 0);
+    return v + (w > 0 ? before : T(0));
   }
-  __syncthreads();
-  const T out = v + (w > 0 ? warps[w - 1] : T(0));
-  __syncthreads();
-  return out;
-}
+};
 
 // The sequence of block i, with base[b] the first block of sequence b: the last
 // that starts at or before it.
