@@ -222,34 +222,20 @@ __device__ __forceinline__ bool same(const PackedStart& a, const PackedStart& b)
 
 // Parts first, first + step, ... of `unit` in slots: its tile 0 is in stretch c, and
 // each stretch that starts within the unit and has some of it (starts[0] is that
-// of c) has a part.  kAtOnce of them are read at a time.
-template <int D, int kAtOnce>
+// of c) has a part.
+template <int D>
 __device__ __forceinline__ void add_slots(const PackedFwd& p, int list, const PackedStart* starts, Merge& m, int unit, int c,
                                           int first, int step, int row, int c16) {
   const int rows = slot_rows(list), left = stretches(p, list) - c;
   const float4* o = reinterpret_cast<const float4*>(p.o_slot[list]) + (size_t)4 * c16 * rows + row;
   const float* lse = p.lse_slot[list] + row;
-  bool more = true;
-  for (int k = first; more;) {
-    int slot[kAtOnce];
-    float ls[kAtOnce];
-    float4 v[kAtOnce][4];
+  for (int k = first; k < left && (k == 0 || (starts[k].unit == unit && starts[k].tile > 0)); k += step) {
+    if (k > 0 && same(starts[k], starts[k + 1])) continue;
+    const size_t slot = k == 0 ? 2 * c + 1 : 2 * (c + k);
+    float4 v[4];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      more = more && k < left && (k == 0 || (starts[k].unit == unit && starts[k].tile > 0));
-      slot[i] = !more || (k > 0 && same(starts[k], starts[k + 1])) ? -1 : k == 0 ? 2 * c + 1 : 2 * (c + k);
-      k += step;
-    }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      ls[i] = -INFINITY;
-      if (slot[i] < 0) continue;
-      ls[i] = lse[(size_t)slot[i] * rows];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) v[i][x] = o[((size_t)slot[i] * (D / 4) + x) * rows];
-    }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) m.add(ls[i], v[i]);
+    for (int x = 0; x < 4; ++x) v[x] = o[(slot * (D / 4) + x) * rows];
+    m.add(lse[slot * rows], v);
   }
 }
 
@@ -342,7 +328,7 @@ __device__ __forceinline__ PackedEntry read_entry(const PackedEntry* e) {
 // stretch before it starts within.  A CTA takes 16 channels of a unit, or all of
 // a small block in few parts.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) fa_packed_merge_kernel(const PackedFwd p) {
+__global__ void __launch_bounds__(kMergeThreads, 4) fa_packed_merge_kernel(const PackedFwd p) {
   __shared__ PackedStart s_starts[2 * kMostGrid + 2];
   __shared__ MergeShared sh;
   __shared__ int s_parts;
@@ -384,7 +370,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_packed_merge_kernel(const Pa
     const int c16 = at + channels;
     const bool ok = row_ok && c16 < kPer;
     Merge m;
-    if (ok) add_slots<D, 2>(p, list, s_starts, m, s.unit, c, share, shares, row, c16);
+    if (ok) add_slots<D>(p, list, s_starts, m, s.unit, c, share, shares, row, c16);
     write_rows<D>(p, sh, m, n_rows * per, shares, ok, token, head, c16);
     if (shares > 1) __syncthreads();  // sh
   }
@@ -406,7 +392,7 @@ __device__ __forceinline__ int stretch_of(const PackedStart* starts, int number,
 // CTA takes rows / H tokens at a time (or `rows` heads of one) and 16 channels,
 // blockIdx.y; heads come first, so that a group's rows are read side by side.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads, 3) fa_packed_join_kernel(const PackedFwd p, int tokens, int n_rows) {
+__global__ void __launch_bounds__(kMergeThreads, 4) fa_packed_join_kernel(const PackedFwd p, int tokens, int n_rows) {
   __shared__ PackedStart s_starts[3 * kMostGrid + 2];
   __shared__ MergeShared sh;
   __shared__ int s_own[kMergeThreads];  // the token's own block: entry and list; -1: of no sequence
@@ -467,7 +453,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) fa_packed_join_kernel(const 
           const PackedStart next = starts[c + 1];
           if (next.unit == unit && next.tile > 0) {
             const int row = t / p.tile_tokens * kTileM + t % p.tile_tokens * p.group_heads + gh;
-            add_slots<D, 2>(p, list, starts + c, m, unit, c, turn, shares, row, c16);
+            add_slots<D>(p, list, starts + c, m, unit, c, turn, shares, row, c16);
           } else if (turn == 0) {
             const float4* o = reinterpret_cast<const float4*>(p.o_part + (((size_t)part * p.Tq + token) * p.H + head) * D) + 4 * c16;
             const float4 v[4] = {o[0], o[1], o[2], o[3]};
@@ -689,9 +675,10 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   p.store32 = aligned32(o->ptr, p.o_row, p.o_head) ? 1 : 0;
   p.status = status;
   p.timeout_ns = fa::internal_wait_timeout_ns();
-  // Rows of a CTA of the join: all its threads', or fewer where these leave SMs over.
+  // Rows of a CTA of the join: all its threads', or fewer where these leave SMs
+  // over (not many more CTAs than that: twice as many take 3 us longer).
   c.join_rows = fa::kMergeThreads;
-  while (c.join_rows > 8 && (long long)Tq * H / c.join_rows * (d / 16) < 2 * sm_count) c.join_rows /= 2;
+  while (c.join_rows > 8 && (long long)Tq * H / c.join_rows * (d / 16) < sm_count) c.join_rows /= 2;
   c.join_tokens = std::max(1, c.join_rows / H);
   c.join_grid = (Tq + c.join_tokens - 1) / c.join_tokens;
   c.join_grid = std::min(c.join_grid, sm_count);
