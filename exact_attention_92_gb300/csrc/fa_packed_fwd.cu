@@ -84,8 +84,7 @@ struct Walk {
     const int4 a = w[0], b = w[1];
     return PackedEntry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   }
-  __device__ __forceinline__ Walk(const PackedFwd& params, int which, int stretch) : p(params) { start(which, stretch); }
-  __device__ __forceinline__ void start(int which, int stretch) {
+  __device__ __forceinline__ Walk(const PackedFwd& params, int which, int stretch) : p(params) {
     const PackedStart* s = p.starts[which] + stretch;
     s0 = s[0];
     s1 = s[1];
@@ -252,86 +251,86 @@ __global__ void __launch_bounds__(384, 1)
   pdl_trigger();
   // What an issuing warp does for the small blocks of warpgroup t.
   auto issue_small = [&](auto which_t, bool ok) {
-      constexpr uint32_t hi = sdesc_hi(1024);
-      constexpr uint32_t kTileStep = C::kTileBytes >> 4;
-      const uint32_t q_lo0 = sdesc_lo(smem_u32(sQ), 16);
-      const uint32_t k_lo0 = sdesc_lo(smem_u32(sKV), 16);
-      const uint32_t v_lo0 = sdesc_lo(smem_u32(sKV), C::kChunkBytes);
-      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t where) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, where));
-      };
-      Piece w;
-      constexpr int t = decltype(which_t)::value;
-      const uint32_t q_lo = q_lo0 + t * kTileStep, t_s = tmem + C::col_s(t), t_o = tmem + C::col_o(t);
-      uint32_t pos = 0, qn = 0, pn = 0;
-      auto key_slot = [&](uint32_t i) { return t * kHalf + i % kHalf; };
-      auto wait_kv = [&](uint32_t i) -> bool { return wait(sb.kv_full(key_slot(i)), (i / kHalf) & 1, kWaitKvFull); };
-      auto issue_s = [&](bool last) -> bool {  // S of the K at `pos`
-        if (!wait_kv(pos)) return false;
+    constexpr uint32_t hi = sdesc_hi(1024);
+    constexpr uint32_t kTileStep = C::kTileBytes >> 4;
+    const uint32_t q_lo0 = sdesc_lo(smem_u32(sQ), 16);
+    const uint32_t k_lo0 = sdesc_lo(smem_u32(sKV), 16);
+    const uint32_t v_lo0 = sdesc_lo(smem_u32(sKV), C::kChunkBytes);
+    auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t where) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, where));
+    };
+    Piece w;
+    constexpr int t = decltype(which_t)::value;
+    const uint32_t q_lo = q_lo0 + t * kTileStep, t_s = tmem + C::col_s(t), t_o = tmem + C::col_o(t);
+    uint32_t pos = 0, qn = 0, pn = 0;
+    auto key_slot = [&](uint32_t i) { return t * kHalf + i % kHalf; };
+    auto wait_kv = [&](uint32_t i) -> bool { return wait(sb.kv_full(key_slot(i)), (i / kHalf) & 1, kWaitKvFull); };
+    auto issue_s = [&](bool last) -> bool {  // S of the K at `pos`
+      if (!wait_kv(pos)) return false;
+      tc_fence_after();
+      issue_qk<D>(t_s, q_lo, k_lo0 + key_slot(pos) * kTileStep, hi);
+      mma_commit_w(sb.s_full(t));
+      if (last) mma_commit_w(sb.q_empty(t));
+      mma_commit_w(sb.kv_empty(key_slot(pos)));
+      ++pos;
+      return true;
+    };
+    Walk<false> walk(p, kSmall, 2 * blockIdx.x + t);
+    while (ok && walk.get(w)) {
+      const int n = w.hi - w.lo;
+      if (n == 0) continue;
+      // (The loads wait for the whole blocks' products.)
+      ok = wait(sb.q_full(t), qn & 1, kWaitQFull) && issue_s(n == 1);
+      ++qn;
+      for (int j = 0; ok && j < n; ++j) {
+        ok = wait_kv(pos) && wait(sb.p_full(t), pn & 1, kWaitPFull);
+        ++pn;
+        if (!ok) break;
         tc_fence_after();
-        issue_qk<D>(t_s, q_lo, k_lo0 + key_slot(pos) * kTileStep, hi);
-        mma_commit_w(sb.s_full(t));
-        if (last) mma_commit_w(sb.q_empty(t));
+        issue_pv<D>(t_o, t_s, v_lo0 + key_slot(pos) * kTileStep, hi, j > 0);
         mma_commit_w(sb.kv_empty(key_slot(pos)));
         ++pos;
-        return true;
-      };
-      Walk<false> walk(p, kSmall, 2 * blockIdx.x + t);
-      while (ok && walk.get(w)) {
-        const int n = w.hi - w.lo;
-        if (n == 0) continue;
-        // (The loads wait for the whole blocks' products.)
-        ok = wait(sb.q_full(t), qn & 1, kWaitQFull) && issue_s(n == 1);
-        ++qn;
-        for (int j = 0; ok && j < n; ++j) {
-          ok = wait_kv(pos) && wait(sb.p_full(t), pn & 1, kWaitPFull);
-          ++pn;
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv<D>(t_o, t_s, v_lo0 + key_slot(pos) * kTileStep, hi, j > 0);
-          mma_commit_w(sb.kv_empty(key_slot(pos)));
-          ++pos;
-          if (j + 1 < n)
-            ok = issue_s(j + 2 == n);
-          else
-            mma_commit_w(sb.o_full(t));
-        }
+        if (j + 1 < n)
+          ok = issue_s(j + 2 == n);
+        else
+          mma_commit_w(sb.o_full(t));
       }
-      // Every MMA this warp issued completes before TMEM is released.
-      mma_commit_w(&drain[t]);
-      (void)wait(&drain[t], 0, kWaitDrain);
+    }
+    // Every MMA this warp issued completes before TMEM is released.
+    mma_commit_w(&drain[t]);
+    (void)wait(&drain[t], 0, kWaitDrain);
   };
   // What a producer does for the small blocks of warpgroup t.
   auto load_small = [&](auto which_t, bool ok) {
-      Piece w;
-      constexpr int t = decltype(which_t)::value;
-      Walk<true> walk(p, kSmall, 2 * blockIdx.x + t);
-      uint32_t pos = 0, qn = 0;
-      bool first = true;
-      while (ok && walk.get(w)) {
-        if (w.hi == w.lo) continue;
-        // The products of the whole blocks have read Q and the ring.
-        if (first) ok = mbar_wait(whole_done, 0, ctl, kWaitKvEmpty);
-        first = false;
-        ok = ok && mbar_wait(sb.q_empty(t), (qn & 1) ^ 1, ctl, kWaitQEmpty);
-        if (!ok) break;
-        load_queries<D>(sQ + t * C::kTileBytes, sb.q_full(t), p, w, 0, &tm_q);
-        ++qn;
-        for (int x = w.lo; ok && x < w.hi; ++x) {
+    Piece w;
+    constexpr int t = decltype(which_t)::value;
+    Walk<true> walk(p, kSmall, 2 * blockIdx.x + t);
+    uint32_t pos = 0, qn = 0;
+    bool first = true;
+    while (ok && walk.get(w)) {
+      if (w.hi == w.lo) continue;
+      // The products of the whole blocks have read Q and the ring.
+      if (first) ok = mbar_wait(whole_done, 0, ctl, kWaitKvEmpty);
+      first = false;
+      ok = ok && mbar_wait(sb.q_empty(t), (qn & 1) ^ 1, ctl, kWaitQEmpty);
+      if (!ok) break;
+      load_queries<D>(sQ + t * C::kTileBytes, sb.q_full(t), p, w, 0, &tm_q);
+      ++qn;
+      for (int x = w.lo; ok && x < w.hi; ++x) {
 #pragma unroll
-          for (int which = 0; which < 2; ++which) {
-            const uint32_t slot = t * kHalf + pos % kHalf;
-            ok = ok && mbar_wait(sb.kv_empty(slot), ((pos / kHalf) & 1) ^ 1, ctl, kWaitKvEmpty);
-            if (!ok) continue;
-            load_keys<D>(sKV + slot * C::kTileBytes, sb.kv_full(slot), w, x, which ? &tm_v : &tm_k,
-                         which ? &tm_vp : &tm_kp);
-            ++pos;
-          }
+        for (int which = 0; which < 2; ++which) {
+          const uint32_t slot = t * kHalf + pos % kHalf;
+          ok = ok && mbar_wait(sb.kv_empty(slot), ((pos / kHalf) & 1) ^ 1, ctl, kWaitKvEmpty);
+          if (!ok) continue;
+          load_keys<D>(sKV + slot * C::kTileBytes, sb.kv_full(slot), w, x, which ? &tm_v : &tm_k,
+                       which ? &tm_vp : &tm_kp);
+          ++pos;
         }
       }
-      for (uint32_t i = pos > (uint32_t)kHalf ? pos - kHalf : 0u; i < pos; ++i)
-        mbar_wait(sb.kv_full(t * kHalf + i % kHalf), (i / kHalf) & 1, ctl, kWaitDrain);
-      if (qn > 0) mbar_wait(sb.q_full(t), (qn - 1) & 1, ctl, kWaitDrain);
+    }
+    for (uint32_t i = pos > (uint32_t)kHalf ? pos - kHalf : 0u; i < pos; ++i)
+      mbar_wait(sb.kv_full(t * kHalf + i % kHalf), (i / kHalf) & 1, ctl, kWaitDrain);
+    if (qn > 0) mbar_wait(sb.q_full(t), (qn - 1) & 1, ctl, kWaitDrain);
   };
   if (warp == 9) {
     reg_dealloc<C::kRegsCtl>();
@@ -340,34 +339,34 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true;
       Piece w;
       uint32_t rc = 0, qc[2] = {0, 0};
-        // Whole blocks.
-        Walk<true> walk(p, kWhole, blockIdx.x);
-        while (ok && walk.get(w)) {
+      // Whole blocks.
+      Walk<true> walk(p, kWhole, blockIdx.x);
+      while (ok && walk.get(w)) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok || (t ? w.hi == w.lo : w.n0 == 0)) continue;
-            ok = mbar_wait(wb.q_empty(t), (qc[t] & 1) ^ 1, ctl, kWaitQEmpty);
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || (t ? w.hi == w.lo : w.n0 == 0)) continue;
+          ok = mbar_wait(wb.q_empty(t), (qc[t] & 1) ^ 1, ctl, kWaitQEmpty);
+          if (!ok) continue;
+          load_queries<D>(sQ + t * C::kTileBytes, wb.q_full(t), p, w, t, &tm_q);
+          ++qc[t];
+        }
+        for (int x = w.lo; ok && x < w.hi; ++x) {
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            const uint32_t slot = rc % C::kStages;
+            ok = ok && mbar_wait(wb.kv_empty(slot), ((rc / C::kStages) & 1) ^ 1, ctl, kWaitKvEmpty);
             if (!ok) continue;
-            load_queries<D>(sQ + t * C::kTileBytes, wb.q_full(t), p, w, t, &tm_q);
-            ++qc[t];
-          }
-          for (int x = w.lo; ok && x < w.hi; ++x) {
-#pragma unroll
-            for (int which = 0; which < 2; ++which) {
-              const uint32_t slot = rc % C::kStages;
-              ok = ok && mbar_wait(wb.kv_empty(slot), ((rc / C::kStages) & 1) ^ 1, ctl, kWaitKvEmpty);
-              if (!ok) continue;
-              load_keys<D>(sKV + slot * C::kTileBytes, wb.kv_full(slot), w, x, which ? &tm_v : &tm_k,
-                           which ? &tm_vp : &tm_kp);
-              ++rc;
-            }
+            load_keys<D>(sKV + slot * C::kTileBytes, wb.kv_full(slot), w, x, which ? &tm_v : &tm_k,
+                         which ? &tm_vp : &tm_kp);
+            ++rc;
           }
         }
-        // Let every copy this thread started land before the CTA can exit.
-        for (uint32_t pos = rc > (uint32_t)C::kStages ? rc - C::kStages : 0u; pos < rc; ++pos)
-          mbar_wait(wb.kv_full(pos % C::kStages), (pos / C::kStages) & 1, ctl, kWaitDrain);
-        for (int t = 0; t < 2; ++t)
-          if (qc[t] > 0) mbar_wait(wb.q_full(t), (qc[t] - 1) & 1, ctl, kWaitDrain);
+      }
+      // Let every copy this thread started land before the CTA can exit.
+      for (uint32_t pos = rc > (uint32_t)C::kStages ? rc - C::kStages : 0u; pos < rc; ++pos)
+        mbar_wait(wb.kv_full(pos % C::kStages), (pos / C::kStages) & 1, ctl, kWaitDrain);
+      for (int t = 0; t < 2; ++t)
+        if (qc[t] > 0) mbar_wait(wb.q_full(t), (qc[t] - 1) & 1, ctl, kWaitDrain);
       load_small(std::integral_constant<int, 0>{}, ok);
     }
     __syncwarp();
@@ -389,72 +388,72 @@ __global__ void __launch_bounds__(384, 1)
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, where));
       };
       Piece w;
-        // Whole blocks: the order of fa_fwd.cu.
-        uint32_t rc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
-        auto wait_kv = [&](uint32_t pos) -> bool {
-          return wait(wb.kv_full(pos % C::kStages), (pos / C::kStages) & 1, kWaitKvFull);
-        };
-        Walk<false> walk(p, kWhole, blockIdx.x);
-        while (ok && walk.get(w)) {
-          const int n1 = w.hi - w.lo;
-          if (n1 == 0) continue;
+      // Whole blocks: the order of fa_fwd.cu.
+      uint32_t rc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+      auto wait_kv = [&](uint32_t pos) -> bool {
+        return wait(wb.kv_full(pos % C::kStages), (pos / C::kStages) & 1, kWaitKvFull);
+      };
+      Walk<false> walk(p, kWhole, blockIdx.x);
+      while (ok && walk.get(w)) {
+        const int n1 = w.hi - w.lo;
+        if (n1 == 0) continue;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok || (t ? n1 : w.n0) == 0) continue;
-            ok = wait(wb.q_full(t), qc[t] & 1, kWaitQFull);
-            ++qc[t];
-          }
-          ok = ok && wait_kv(rc);
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || (t ? n1 : w.n0) == 0) continue;
+          ok = wait(wb.q_full(t), qc[t] & 1, kWaitQFull);
+          ++qc[t];
+        }
+        ok = ok && wait_kv(rc);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t ? n1 : w.n0;
+          if (nt == 0) continue;
+          issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + (rc % C::kStages) * kTileStep, hi);
+          mma_commit_w(wb.s_full(t));
+          if (nt == 1) mma_commit_w(wb.q_empty(t));  // Q_t's last product
+        }
+        mma_commit_w(wb.kv_empty(rc % C::kStages));
+        for (int j = 0; ok && j < n1; ++j) {
+          const uint32_t pos_v = rc + 2 * j + 1;
+          const uint32_t pos_k = pos_v + 1;
+          const uint32_t slot_v = pos_v % C::kStages;
+          const uint32_t slot_k = pos_k % C::kStages;
+          ok = wait_kv(pos_v);
           if (!ok) break;
           tc_fence_after();
+          bool k_ready = false;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int nt = t ? n1 : w.n0;
-            if (nt == 0) continue;
-            issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + (rc % C::kStages) * kTileStep, hi);
-            mma_commit_w(wb.s_full(t));
-            if (nt == 1) mma_commit_w(wb.q_empty(t));  // Q_t's last product
-          }
-          mma_commit_w(wb.kv_empty(rc % C::kStages));
-          for (int j = 0; ok && j < n1; ++j) {
-            const uint32_t pos_v = rc + 2 * j + 1;
-            const uint32_t pos_k = pos_v + 1;
-            const uint32_t slot_v = pos_v % C::kStages;
-            const uint32_t slot_k = pos_k % C::kStages;
-            ok = wait_kv(pos_v);
-            if (!ok) break;
+            if (!ok || j >= nt) continue;
+            ok = wait(wb.p_full(t), pc[t] & 1, kWaitPFull);
+            ++pc[t];
+            if (!ok) continue;
             tc_fence_after();
-            bool k_ready = false;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int nt = t ? n1 : w.n0;
-              if (!ok || j >= nt) continue;
-              ok = wait(wb.p_full(t), pc[t] & 1, kWaitPFull);
-              ++pc[t];
-              if (!ok) continue;
-              tc_fence_after();
-              issue_pv<D>(tmem + C::col_o(t), tmem + C::col_s(t), v_lo0 + slot_v * kTileStep, hi, j > 0);
-              if (j + 1 < nt) {
-                if (!k_ready) {
-                  ok = wait_kv(pos_k);
-                  if (!ok) continue;
-                  tc_fence_after();
-                  k_ready = true;
-                }
-                issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + slot_k * kTileStep, hi);
-                mma_commit_w(wb.s_full(t));
-                if (j + 2 == nt) mma_commit_w(wb.q_empty(t));  // Q_t's last product
-              } else {
-                mma_commit_w(wb.o_full(t));
+            issue_pv<D>(tmem + C::col_o(t), tmem + C::col_s(t), v_lo0 + slot_v * kTileStep, hi, j > 0);
+            if (j + 1 < nt) {
+              if (!k_ready) {
+                ok = wait_kv(pos_k);
+                if (!ok) continue;
+                tc_fence_after();
+                k_ready = true;
               }
+              issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + slot_k * kTileStep, hi);
+              mma_commit_w(wb.s_full(t));
+              if (j + 2 == nt) mma_commit_w(wb.q_empty(t));  // Q_t's last product
+            } else {
+              mma_commit_w(wb.o_full(t));
             }
-            if (!ok) break;
-            mma_commit_w(wb.kv_empty(slot_v));
-            if (j + 1 < n1) mma_commit_w(wb.kv_empty(slot_k));
           }
-          rc += 2 * n1;
+          if (!ok) break;
+          mma_commit_w(wb.kv_empty(slot_v));
+          if (j + 1 < n1) mma_commit_w(wb.kv_empty(slot_k));
         }
-        mma_commit_w(whole_done);
+        rc += 2 * n1;
+      }
+      mma_commit_w(whole_done);
     }
     issue_small(std::integral_constant<int, 0>{}, ok);
     __syncwarp();
@@ -480,230 +479,230 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
     // The units of a list: one copy of the code for each.
     auto take = [&](auto which) {
-    constexpr int kList = decltype(which)::value;
-    constexpr bool small = kList == kSmall;
-    const Bars<D, kList> bar(bars);
-    uint64_t *const s_full = bar.s_full(t), *const p_full = bar.p_full(t), *const o_full = bar.o_full(t);
-    uint32_t sc = 0, oc = 0;
-    Walk<true> walk(p, kList, small ? 2 * blockIdx.x + t : blockIdx.x);
-    Piece w;
-    while (ok && walk.get(w)) {
-      const int steps = t || small ? w.hi - w.lo : w.n0;
-      const int first = small ? 0 : t * p.tile_tokens;         // the tile's first token in the block
-      const int here = min(p.tile_tokens, w.e.q_len - first);  // its tokens
-      const bool live = warp_tok < here;                       // the warp has rows
-      const bool row_ok = tok < here && tok < p.tile_tokens && w.g0 + gh < p.group;
-      const int token = w.e.q_row + first + tok;
-      const int head = w.hk * p.group + w.g0 + gh;
-      float m_ref = -INFINITY;  // reference max of this row, log2 units
-      float l = 0.f;     // sum of the fp32 weights: L = m + log l
-      float l_bf = 0.f;  // sum of the bf16-rounded weights the PV MMA takes: O = O~ / l_bf
-      for (int j = 0; j < steps; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full, sc & 1, ctl, kWaitSFull));
-        ++sc;
-        if (!ok) break;
-        if (!live) {
-          mbar_arrive_warp(p_full);
-          continue;
-        }
-        tc_fence_after();
-        uint32_t s[kTileN];
+      constexpr int kList = decltype(which)::value;
+      constexpr bool small = kList == kSmall;
+      const Bars<D, kList> bar(bars);
+      uint64_t *const s_full = bar.s_full(t), *const p_full = bar.p_full(t), *const o_full = bar.o_full(t);
+      uint32_t sc = 0, oc = 0;
+      Walk<true> walk(p, kList, small ? 2 * blockIdx.x + t : blockIdx.x);
+      Piece w;
+      while (ok && walk.get(w)) {
+        const int steps = t || small ? w.hi - w.lo : w.n0;
+        const int first = small ? 0 : t * p.tile_tokens;         // the tile's first token in the block
+        const int here = min(p.tile_tokens, w.e.q_len - first);  // its tokens
+        const bool live = warp_tok < here;                       // the warp has rows
+        const bool row_ok = tok < here && tok < p.tile_tokens && w.g0 + gh < p.group;
+        const int token = w.e.q_row + first + tok;
+        const int head = w.hk * p.group + w.g0 + gh;
+        float m_ref = -INFINITY;  // reference max of this row, log2 units
+        float l = 0.f;     // sum of the fp32 weights: L = m + log l
+        float l_bf = 0.f;  // sum of the bf16-rounded weights the PV MMA takes: O = O~ / l_bf
+        for (int j = 0; j < steps; ++j) {
+          ok = __all_sync(0xffffffffu, mbar_wait(s_full, sc & 1, ctl, kWaitSFull));
+          ++sc;
+          if (!ok) break;
+          if (!live) {
+            mbar_arrive_warp(p_full);
+            continue;
+          }
+          tc_fence_after();
+          uint32_t s[kTileN];
 #pragma unroll
-        for (int c = 0; c < kTileN / 32; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
-        tmem_ld_wait<kTileN>(s);
-        float x[kTileN];
+          for (int c = 0; c < kTileN / 32; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
+          tmem_ld_wait<kTileN>(s);
+          float x[kTileN];
 #pragma unroll
-        for (int c = 0; c < kTileN; ++c) x[c] = __uint_as_float(s[c]);
-        const int tile = w.lo + j;
-        const bool pre = tile < w.e.prefix;
-        const int row = (pre ? tile : tile - w.e.prefix) * kTileN;
-        const int len = pre ? p.prefix_len : w.e.k_len;
-        const bool causal = p.causal && !pre;
-        // Column c is key kv0 + c; a sequence's last tile has its keys at the end.
-        const int skip = pre ? 0 : max(0, row + kTileN - len);
-        const int kv0 = row - skip;
-        if (skip > 0 || kv0 + kTileN > len || (causal && kv0 + kTileN > w.e.pos + first + warp_tok + 1)) {
-          const int lim = (causal ? min(len, w.e.pos + first + tok + 1) : len) - kv0;
-          // A word of bits for 32 columns, then one select a column (compares of
-          // every column took 2500 cycles where this takes 700).
+          for (int c = 0; c < kTileN; ++c) x[c] = __uint_as_float(s[c]);
+          const int tile = w.lo + j;
+          const bool pre = tile < w.e.prefix;
+          const int row = (pre ? tile : tile - w.e.prefix) * kTileN;
+          const int len = pre ? p.prefix_len : w.e.k_len;
+          const bool causal = p.causal && !pre;
+          // Column c is key kv0 + c; a sequence's last tile has its keys at the end.
+          const int skip = pre ? 0 : max(0, row + kTileN - len);
+          const int kv0 = row - skip;
+          if (skip > 0 || kv0 + kTileN > len || (causal && kv0 + kTileN > w.e.pos + first + warp_tok + 1)) {
+            const int lim = (causal ? min(len, w.e.pos + first + tok + 1) : len) - kv0;
+            // A word of bits for 32 columns, then one select a column (compares of
+            // every column took 2500 cycles where this takes 700).
+#pragma unroll
+            for (int h = 0; h < kTileN / 32; ++h) {
+              const int n = lim - 32 * h, z = skip - 32 * h;
+              uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+              if (z > 0) see &= z >= 32 ? 0u : ~0u << z;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(see & (1u << c))) x[32 * h + c] = -INFINITY;
+            }
+          }
+          float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+          for (int c = 4; c + 8 <= kTileN; c += 8) {
+            mx0 = fmax3(mx0, x[c], x[c + 1]);
+            mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
+            mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
+            mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
+          }
+          mx0 = fmax3(mx0, x[kTileN - 4], x[kTileN - 3]);
+          mx1 = fmax3(mx1, x[kTileN - 2], x[kTileN - 1]);
+          const float m_tile = fmax3(fmaxf(mx0, mx1), mx2, mx3) * sl2;
+          float f = 1.f;
+          bool rescale = false;
+          if (j == 0) {
+            m_ref = m_tile;
+          } else if (__any_sync(0xffffffffu, m_tile > m_ref + C::kRescaleThreshold)) {
+            const float m_new = fmaxf(m_ref, m_tile);
+            f = (m_new == -INFINITY) ? 1.f : ex2_approx(m_ref - m_new);
+            l *= f;
+            l_bf *= f;
+            m_ref = m_new;
+            rescale = true;
+          }
+          const float m_exp = (m_ref == -INFINITY) ? 0.f : m_ref;
+          const float2 sl2v = make_float2(sl2, sl2);
+          const float2 negv = make_float2(-m_exp, -m_exp);
+          float2 ls0 = make_float2(0.f, 0.f), ls1 = ls0;
+          float lr0 = 0.f, lr1 = 0.f, lr2 = 0.f, lr3 = 0.f;
 #pragma unroll
           for (int h = 0; h < kTileN / 32; ++h) {
-            const int n = lim - 32 * h, z = skip - 32 * h;
-            uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
-            if (z > 0) see &= z >= 32 ? 0u : ~0u << z;
+            uint32_t pk_[16];
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!(see & (1u << c))) x[32 * h + c] = -INFINITY;
-          }
-        }
-        float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
-#pragma unroll
-        for (int c = 4; c + 8 <= kTileN; c += 8) {
-          mx0 = fmax3(mx0, x[c], x[c + 1]);
-          mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
-          mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
-          mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
-        }
-        mx0 = fmax3(mx0, x[kTileN - 4], x[kTileN - 3]);
-        mx1 = fmax3(mx1, x[kTileN - 2], x[kTileN - 1]);
-        const float m_tile = fmax3(fmaxf(mx0, mx1), mx2, mx3) * sl2;
-        float f = 1.f;
-        bool rescale = false;
-        if (j == 0) {
-          m_ref = m_tile;
-        } else if (__any_sync(0xffffffffu, m_tile > m_ref + C::kRescaleThreshold)) {
-          const float m_new = fmaxf(m_ref, m_tile);
-          f = (m_new == -INFINITY) ? 1.f : ex2_approx(m_ref - m_new);
-          l *= f;
-          l_bf *= f;
-          m_ref = m_new;
-          rescale = true;
-        }
-        const float m_exp = (m_ref == -INFINITY) ? 0.f : m_ref;
-        const float2 sl2v = make_float2(sl2, sl2);
-        const float2 negv = make_float2(-m_exp, -m_exp);
-        float2 ls0 = make_float2(0.f, 0.f), ls1 = ls0;
-        float lr0 = 0.f, lr1 = 0.f, lr2 = 0.f, lr3 = 0.f;
-#pragma unroll
-        for (int h = 0; h < kTileN / 32; ++h) {
-          uint32_t pk_[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 a = __ffma2_rn(make_float2(x[32 * h + e], x[32 * h + e + 1]), sl2v, negv);
-            const float p0 = ex2_approx(a.x);
-            const float p1 = ex2_approx(a.y);
-            const uint32_t pp = pack_bf16(p0, p1);
-            if ((e >> 1) & 1) {
-              ls1 = __fadd2_rn(ls1, make_float2(p0, p1));
-              lr2 = add_bf16_lo(lr2, pp);
-              lr3 = add_bf16_hi(lr3, pp);
-            } else {
-              ls0 = __fadd2_rn(ls0, make_float2(p0, p1));
-              lr0 = add_bf16_lo(lr0, pp);
-              lr1 = add_bf16_hi(lr1, pp);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 a = __ffma2_rn(make_float2(x[32 * h + e], x[32 * h + e + 1]), sl2v, negv);
+              const float p0 = ex2_approx(a.x);
+              const float p1 = ex2_approx(a.y);
+              const uint32_t pp = pack_bf16(p0, p1);
+              if ((e >> 1) & 1) {
+                ls1 = __fadd2_rn(ls1, make_float2(p0, p1));
+                lr2 = add_bf16_lo(lr2, pp);
+                lr3 = add_bf16_hi(lr3, pp);
+              } else {
+                ls0 = __fadd2_rn(ls0, make_float2(p0, p1));
+                lr0 = add_bf16_lo(lr0, pp);
+                lr1 = add_bf16_hi(lr1, pp);
+              }
+              pk_[e / 2] = pp;
             }
-            pk_[e / 2] = pp;
+            tmem_st16(tS + 16 * h, pk_);
           }
-          tmem_st16(tS + 16 * h, pk_);
-        }
-        l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
-        l_bf += (lr0 + lr1) + (lr2 + lr3);
-        if (rescale) {
+          l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
+          l_bf += (lr0 + lr1) + (lr2 + lr3);
+          if (rescale) {
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32 * c, o);
-            tmem_ld_wait<32>(o);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * c, o);
+              tmem_ld_wait<32>(o);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
-                                          make_float2(f, f));
-              o[i] = __float_as_uint(v.x);
-              o[i + 1] = __float_as_uint(v.y);
+              for (int i = 0; i < 32; i += 2) {
+                const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                                            make_float2(f, f));
+                o[i] = __float_as_uint(v.x);
+                o[i + 1] = __float_as_uint(v.y);
+              }
+              tmem_st32(tO + 32 * c, o);
             }
-            tmem_st32(tO + 32 * c, o);
           }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive_warp(p_full);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive_warp(p_full);
-      }
-      if (!ok) break;
-      // ---- the rows' results.  What does not need O is worked out while the last
-      // product runs; then all of the row is read at once.
-      const int stretch = small ? 2 * (int)blockIdx.x + t : (int)blockIdx.x;
-      const int sl = 2 * stretch + (w.lo > 0 ? 0 : 1);
-      const int slot_row = (small ? 0 : kTileM * t) + r_in_tile;
-      uint8_t* orow = reinterpret_cast<uint8_t*>(p.o) + ((long long)token * p.o_row + (long long)head * p.o_head) * 2;
-      if (steps > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(o_full, oc & 1, ctl, kWaitOFull));
-        ++oc;
         if (!ok) break;
-        tc_fence_after();
-      }
-      if (!live) continue;
-      uint32_t o[D];
-      if (steps > 0) {
+        // ---- the rows' results.  What does not need O is worked out while the last
+        // product runs; then all of the row is read at once.
+        const int stretch = small ? 2 * (int)blockIdx.x + t : (int)blockIdx.x;
+        const int sl = 2 * stretch + (w.lo > 0 ? 0 : 1);
+        const int slot_row = (small ? 0 : kTileM * t) + r_in_tile;
+        uint8_t* orow = reinterpret_cast<uint8_t*>(p.o) + ((long long)token * p.o_row + (long long)head * p.o_head) * 2;
+        if (steps > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(o_full, oc & 1, ctl, kWaitOFull));
+          ++oc;
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (!live) continue;
+        uint32_t o[D];
+        if (steps > 0) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) tmem_ld32(tO + 32 * c, o + 32 * c);
-        tmem_ld_wait<D>(o);
-      } else {
+          for (int c = 0; c < D / 32; ++c) tmem_ld32(tO + 32 * c, o + 32 * c);
+          tmem_ld_wait<D>(o);
+        } else {
 #pragma unroll
-        for (int i = 0; i < D; ++i) o[i] = 0u;
-      }
-      // A row that saw no key has l = 0: O = 0, L = -inf.
-      const float inv_l = l_bf > 0.f ? 1.0f / l_bf : 0.f;
-      const float lse = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
-      const float2 il = make_float2(inv_l, inv_l);
-      if (!w.cut && !p.shared) {
+          for (int i = 0; i < D; ++i) o[i] = 0u;
+        }
+        // A row that saw no key has l = 0: O = 0, L = -inf.
+        const float inv_l = l_bf > 0.f ? 1.0f / l_bf : 0.f;
+        const float lse = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
+        const float2 il = make_float2(inv_l, inv_l);
+        if (!w.cut && !p.shared) {
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i) {
+            const float2 a = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il);
+            o[i] = pack_bf16(a.x, a.y);
+          }
+          if (p.tile_store && warp_tok + 32 / p.group_heads <= here) {
+            // All 32 rows: 64 channels at a time through shared memory, stored by the
+            // copy engine.  (Stores from registers, a row a lane, touch 32 lines each: 2800
+            // cycles a unit at d = 128, during which the other warps' barriers queue behind
+            // them; with rows exchanged between lanes first, 3300.)
+#pragma unroll
+            for (int h = 0; h < (D + 63) / 64; ++h) {
+              if (storing) {
+                if (lane == 0) bulk_wait_read();
+                __syncwarp();
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (64 * h + 8 * i >= D) continue;  // (past d = 96 nothing is stored)
+                const uint32_t* x = o + 32 * h + 4 * i;
+                *reinterpret_cast<uint4*>(out + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+              }
+              fence_async_shared();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_4d(&tm_o, out, 64 * h, w.g0, w.e.q_row + first + warp_tok, w.hk);
+                bulk_commit();
+              }
+              storing = true;
+            }
+          } else if (row_ok) {
+            if (p.store32) {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) st_global_v8(orow + 32 * i, o + 8 * i);
+            } else {
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i)
+                reinterpret_cast<uint4*>(orow)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+          }
+          if (row_ok) p.lse[(size_t)head * p.Tq + token] = lse;
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < D / 2; ++i) {
           const float2 a = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il);
-          o[i] = pack_bf16(a.x, a.y);
+          o[2 * i] = __float_as_uint(a.x);
+          o[2 * i + 1] = __float_as_uint(a.y);
         }
-        if (p.tile_store && warp_tok + 32 / p.group_heads <= here) {
-          // All 32 rows: 64 channels at a time through shared memory, stored by the
-          // copy engine.  (Stores from registers, a row a lane, touch 32 lines each: 2800
-          // cycles a unit at d = 128, during which the other warps' barriers queue behind
-          // them; with rows exchanged between lanes first, 3300.)
+        if (w.cut) {
+          const int rows = small ? kSlotRows / 2 : kSlotRows;
+          float4* dst = reinterpret_cast<float4*>(p.o_slot[small]) + (size_t)sl * (D / 4) * rows + slot_row;
+          if (row_ok) {
 #pragma unroll
-          for (int h = 0; h < (D + 63) / 64; ++h) {
-            if (storing) {
-              if (lane == 0) bulk_wait_read();
-              __syncwarp();
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (64 * h + 8 * i >= D) continue;  // (past d = 96 nothing is stored)
-              const uint32_t* x = o + 32 * h + 4 * i;
-              *reinterpret_cast<uint4*>(out + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-            }
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_4d(&tm_o, out, 64 * h, w.g0, w.e.q_row + first + warp_tok, w.hk);
-              bulk_commit();
-            }
-            storing = true;
+            for (int i = 0; i < D / 4; ++i)
+              dst[i * rows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                               __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            p.lse_slot[small][(size_t)sl * rows + slot_row] = lse;
           }
-        } else if (row_ok) {
-          if (p.store32) {
+        } else {
+          float* prow = p.o_part + (((size_t)(1 - w.e.kind) * p.Tq + token) * p.H + head) * D;
+          if (row_ok) {
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) st_global_v8(orow + 32 * i, o + 8 * i);
-          } else {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              reinterpret_cast<uint4*>(orow)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < D / 8; ++i) st_global_v8(prow + 8 * i, o + 8 * i);
+            p.lse_part[((size_t)(1 - w.e.kind) * p.H + head) * p.Tq + token] = lse;
           }
         }
-        if (row_ok) p.lse[(size_t)head * p.Tq + token] = lse;
-        continue;
       }
-#pragma unroll
-      for (int i = 0; i < D / 2; ++i) {
-        const float2 a = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il);
-        o[2 * i] = __float_as_uint(a.x);
-        o[2 * i + 1] = __float_as_uint(a.y);
-      }
-      if (w.cut) {
-        const int rows = small ? kSlotRows / 2 : kSlotRows;
-        float4* dst = reinterpret_cast<float4*>(p.o_slot[small]) + (size_t)sl * (D / 4) * rows + slot_row;
-        if (row_ok) {
-#pragma unroll
-          for (int i = 0; i < D / 4; ++i)
-            dst[i * rows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                             __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-          p.lse_slot[small][(size_t)sl * rows + slot_row] = lse;
-        }
-      } else {
-        float* prow = p.o_part + (((size_t)(1 - w.e.kind) * p.Tq + token) * p.H + head) * D;
-        if (row_ok) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) st_global_v8(prow + 8 * i, o + 8 * i);
-          p.lse_part[((size_t)(1 - w.e.kind) * p.H + head) * p.Tq + token] = lse;
-        }
-      }
-    }
     };
     take(std::integral_constant<int, kWhole>{});
     take(std::integral_constant<int, kSmall>{});
