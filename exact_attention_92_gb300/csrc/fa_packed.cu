@@ -587,6 +587,8 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   if (entries * hgs > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   const long long key_tiles = prefix_tiles + (Tk + fa::kTileN - 1) / fa::kTileN;
   pl.min_tiles = 2;
+  // Few keys: no cuts, and no merge behind them (4 x 16 heads of d = 64 over 384 keys
+  // 12.3 us and not 13.4; 16.9 and not 16 over 768 keys of 8 heads of d = 128).
   pl.whole = key_tiles <= 4 && !p.shared ? 1 : 0;
   p.grid = (int)std::min<long long>(std::min(sm_count, fa::kMostGrid), entries * hgs * (pl.whole ? 1 : std::max(1LL, key_tiles / pl.min_tiles)));
 

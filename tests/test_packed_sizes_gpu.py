@@ -1,0 +1,205 @@
+"""Packed sequences where sizes leave the ordinary: more sequences and blocks than a CTA plans in shared memory, one
+sequence over all of the device, offsets past 32 bits; calls side by side, through either caller, and one after another as
+a server makes them.  Bounds are packed_util's."""
+
+import threading
+
+import numpy as np
+import pytest
+
+from gpu_util import ensure_built, host, torch_cuda
+from oracle import packed as oracle
+from oracle import rope as rope_oracle
+from packed_util import check_forward, i32, make, scale_of, starts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fa():
+    torch_cuda()
+    return ensure_built()
+
+
+def _check(fa, lq, lk, H, Hkv, d, causal, seed, used=None, prefix=0):
+    q, k, v = make(lq, lk, H, Hkv, d, seed)
+    cq, ck = starts(lq), starts(lk)
+    args = (i32(cq), i32(ck), None if used is None else i32(used), causal)
+    pre = None
+    if prefix:
+        _, kp, vp = make([1], [prefix], H, Hkv, d, seed + 1)
+        pre = (host(kp), host(vp))
+        o, lse = fa.prefix_forward(q, kp, vp, k, v, *args)
+    else:
+        o, lse = fa.packed_forward(q, k, v, *args)
+    assert fa.fa_poll_status() == fa.FA_OK
+    check_forward(o, lse, oracle.forward(host(q), host(k), host(v), cq, ck, scale_of(d), causal, used, pre), d)
+
+
+@pytest.mark.parametrize("prefix", [0, 400])
+@pytest.mark.parametrize("B,H,most", [(3000, 2, 4), (1100, 128, 4), (700, 128, 6)])
+def test_many_sequences(fa, B, H, most, prefix):
+    """Blocks of two tokens (128 heads) or of many: over 1024 sequences, small blocks, whole blocks, and of both together."""
+    g = np.random.default_rng(B + prefix)
+    lq = g.integers(0, most, B).tolist()
+    lk = [n + int(g.integers(0, 30)) for n in lq]
+    _check(fa, lq, lk, H, 1, 64, "bottom_right", 50, prefix=prefix)
+
+
+def test_many_sequences_backward_is_that_of_each(fa):
+    """Over 1024 sequences: dq, dk, dv of the first, of one in the middle and of the last are those of calls of their own."""
+    torch = torch_cuda()
+    g = np.random.default_rng(5)
+    lens = g.integers(1, 40, 1300).tolist()
+    q, k, v = make(lens, lens, 2, 1, 64, 51)
+    do = torch.randn(q.shape, generator=torch.Generator().manual_seed(52)).to(torch.bfloat16).cuda()
+    cu = starts(lens)
+    o, lse = fa.packed_forward(q, k, v, i32(cu), causal=True)
+    grads = fa.packed_backward(q, k, v, o, lse, do, i32(cu), causal=True)
+    for b in (0, 1, 650, 1299):
+        part = slice(cu[b], cu[b + 1])
+        one = [x[part].contiguous() for x in (q, k, v, o, do)]
+        alone = fa.packed_backward(*one[:4], lse[:, part].contiguous(), one[4], i32([0, lens[b]]), causal=True)
+        assert all(torch.equal(x[part], y) for x, y in zip(grads, alone))
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("H,Hkv,n", [(8, 1, 70000), (3, 3, 20011)])
+def test_one_sequence_over_the_whole_device(fa, d, H, Hkv, n):
+    """Hundreds of parts of one row are merged."""
+    _check(fa, [1], [n], H, Hkv, d, "none", 53)
+    _check(fa, [2], [3], H, Hkv, d, "bottom_right", 54, prefix=n)
+
+
+def test_answers_behind_a_long_prefix(fa):
+    _check(fa, [1] * 24, [(5 * i) % 60 for i in range(24)], 8, 1, 128, "bottom_right", 55, prefix=30000)
+
+
+def test_offsets_past_32_bits(fa):
+    """Keys and queries whose elements lie past 2^31 of them; nothing else of the tensors is read or written."""
+    torch = torch_cuda()
+    room, H, Hkv, d = 9_000_000, 4, 2, 128
+    used, lq = [300, 700], [5, 40]
+    k, v = (torch.empty(room, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert k.numel() > 2 ** 31
+    q, ks, vs = make(lq, used, H, Hkv, d, 56)
+    cu_k = [0, room - 1000, room]
+    for big, small in ((k, ks), (v, vs)):
+        big[:300] = small[:300]
+        big[room - 1000:room - 300] = small[300:]
+    o, lse = fa.packed_forward(q, k, v, i32(starts(lq)), i32(cu_k), i32(used), "bottom_right")
+    assert fa.fa_poll_status() == fa.FA_OK
+    want = oracle.forward(host(q), host(ks), host(vs), starts(lq), starts(used), scale_of(d), "bottom_right")
+    check_forward(o, lse, want, d)
+    del k, v
+    T, H, n = 140_000, 128, 150
+    far_q = torch.empty(T, H, d, dtype=torch.bfloat16, device="cuda")
+    far_o, far_l = torch.zeros_like(far_q), torch.zeros(H, T, device="cuda")
+    assert far_q.numel() > 2 ** 31
+    q, ks, vs = make([n], [n], H, 8, d, 57)
+    far_q[T - n:] = q
+    fa.fa_packed_fwd(far_q, ks, vs, far_o, far_l, i32([T - n, T]), i32([0, n]), causal=True)
+    assert fa.fa_poll_status() == fa.FA_OK
+    o, lse = fa.packed_forward(q, ks, vs, i32([0, n]), causal=True)
+    assert torch.equal(far_o[T - n:], o) and torch.equal(far_l[:, T - n:], lse)
+    assert not bool(far_o[:1000].any()) and not bool(far_o[T - n - 1000:T - n].any())
+
+
+def test_calls_side_by_side(fa):
+    """Threads of the host, each on a stream of its own: the bits of calls one after another."""
+    torch = torch_cuda()
+    cases = []
+    for i, (lens, H, Hkv, d) in enumerate((([700, 33, 900], 8, 2, 128), ([64] * 40, 4, 4, 64), ([1, 1, 2000], 6, 3, 96))):
+        q, k, v = make(lens, lens, H, Hkv, d, 60 + i)
+        cu = i32(starts(lens))
+        do = torch.randn(q.shape, generator=torch.Generator().manual_seed(70 + i)).to(torch.bfloat16).cuda()
+
+        def call(q=q, k=k, v=v, cu=cu, do=do):
+            o, lse = fa.packed_forward(q, k, v, cu, causal=True)
+            return [o, lse, *fa.packed_backward(q, k, v, o, lse, do, cu, causal=True)]
+
+        cases.append((call, call()))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(call, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got = call()
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                        wrong.append("bits")
+        except Exception as e:  # noqa: BLE001 (reported by the test's own thread)
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_either_caller(fa, monkeypatch):
+    """The native caller, and ctypes where it was not built: the same bits, the same refusals."""
+    torch = torch_cuda()
+    from exact_attention_92_gb300 import _binding
+
+    lens, H, Hkv, d = [300, 41], 4, 2, 64
+    q, k, v = make(lens, lens, H, Hkv, d, 80)
+    _, kp, vp = make([1], [200], H, Hkv, d, 81)
+    cu, ph = i32(starts(lens)), fa.rope_phases(fa.rope_frequencies(d))
+    do = torch.randn(q.shape, generator=torch.Generator().manual_seed(82)).to(torch.bfloat16).cuda()
+
+    def everything():
+        qr, kr = fa.rope(q, k, ph)
+        o, lse = fa.packed_forward(qr, kr, v, cu, causal=True)
+        grads = fa.packed_backward(qr, kr, v, o, lse, do, cu, causal=True)
+        refused = []
+        for bad in (lambda: fa.packed_forward(q, k, v, cu, scale=-1.0), lambda: fa.packed_forward(q, k, v, cu.long()),
+                    lambda: fa.packed_forward(q, k[:, :1].expand(341, 2, 64), v, cu), lambda: fa.rope(q.float(), k, ph),
+                    lambda: fa.prefix_forward(q, kp[:0], vp[:0], k, v, cu),
+                    lambda: fa.packed_backward(q, k, v, o, lse[:, :9], do, cu)):
+            with pytest.raises((fa.FaError, ValueError, TypeError)) as e:
+                bad()
+            refused.append((type(e.value), getattr(e.value, "status", None)))
+        return [qr, kr, o, lse, *grads, *fa.prefix_forward(qr, kp, vp, kr, v, cu)], refused
+
+    first = everything()
+    monkeypatch.setattr(_binding, "_packed", False)
+    second = everything()
+    assert all(torch.equal(a, b) for a, b in zip(first[0], second[0]))
+    assert first[1] == second[1]
+
+
+def test_steps_of_a_server(fa):
+    """A prompt behind a shared document and then steps: new rows are turned, put into the cache and answered."""
+    torch = torch_cuda()
+    P, H, Hkv, d, room = 300, 8, 2, 128, 256
+    B = 3
+    prompts = [100, 7, 150]
+    _, kp, vp = make([1], [P], H, Hkv, d, 90)
+    cache_k, cache_v = (torch.full((B * room, Hkv, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    freq = fa.rope_frequencies(d)
+    ph = fa.rope_phases(freq)
+    used = [0] * B
+    for step in range(4):
+        lq = prompts if step == 0 else [1] * B
+        q, k, v = make(lq, lq, H, Hkv, d, 91 + step)
+        pos = [P + used[b] + i for b in range(B) for i in range(lq[b])]
+        qr, kr = fa.rope(q, k, ph, positions=i32(pos))
+        theta = rope_oracle.angles(np.asarray(pos), freq)[:, None]
+        for got, x in ((qr, q), (kr, k)):
+            want = rope_oracle.rotate(host(x), theta, d)
+            assert bool((np.abs(host(got) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -18 * np.abs(host(x)).max()).all())
+        at = [b * room + used[b] + i for b in range(B) for i in range(lq[b])]
+        cache_k[at], cache_v[at] = kr, v
+        used = [u + n for u, n in zip(used, lq)]
+        o, lse = fa.prefix_forward(qr, kp, vp, cache_k, cache_v, i32(starts(lq)), i32(starts([room] * B)), i32(used),
+                                   "bottom_right")
+        assert fa.fa_poll_status() == fa.FA_OK
+        clean = [host(torch.nan_to_num(x)) for x in (cache_k, cache_v)]
+        want = oracle.forward(host(qr), *clean, starts(lq), starts([room] * B), scale_of(d), "bottom_right", used,
+                              (host(kp), host(vp)))
+        check_forward(o, lse, want, d)
