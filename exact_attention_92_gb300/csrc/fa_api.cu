@@ -573,7 +573,7 @@ const char* fa_strerror(int status) {
     case FA_ERR_SCRATCH_TOO_SMALL:
       return "FA_ERR_SCRATCH_TOO_SMALL: problem needs more than the static scratch of fa_bwd_noalloc";
     case FA_ERR_BAD_INDEX:
-      return "FA_ERR_BAD_INDEX: a page, position or length on the device was out of range and was skipped";
+      return "FA_ERR_BAD_INDEX: a page, position, length or bound on the device was out of range and was skipped";
     default: return "unknown fa_status";
   }
 }

@@ -66,8 +66,9 @@ typedef enum {
   FA_ERR_NO_MEMORY = 4,   /* workspace allocation failed                     */
   FA_ERR_TIMEOUT = 5,     /* a device-side wait gave up (fa_poll_status)     */
   FA_ERR_SCRATCH_TOO_SMALL = 6, /* fa_bwd_noalloc: problem exceeds its scratch */
-  FA_ERR_BAD_INDEX = 7 /* fa_kv4_*: a page, position or length on the device was
-                          out of range and was skipped (fa_poll_status) */
+  FA_ERR_BAD_INDEX = 7 /* a page, position, length or bound of a sequence on the device
+                          was out of range and was skipped (fa_kv4_*, fa_packed_*,
+                          fa_prefix_fwd; reported by fa_poll_status) */
 } fa_status;
 
 /*
@@ -562,8 +563,8 @@ int fa_prefix_fwd(const fa_rows_t* q, const fa_rows_t* k_prefix, const fa_rows_t
 /*
  * Synchronise `stream`, then return and clear the device status of the
  * current device: FA_OK, FA_ERR_TIMEOUT if a kernel's bounded wait gave up
- * since the last poll, FA_ERR_BAD_INDEX if a fa_kv4_* kernel skipped an index
- * out of range, or FA_ERR_CUDA if the synchronisation failed.  Where both
+ * since the last poll, FA_ERR_BAD_INDEX if a kernel of the 4-bit cache or of
+ * packed sequences skipped an index out of range, or FA_ERR_CUDA if the synchronisation failed.  Where both
  * happened, one call returns FA_ERR_TIMEOUT and the next FA_ERR_BAD_INDEX.
  */
 int fa_poll_status(void* stream);
@@ -604,7 +605,9 @@ int fa_selftest_kv4_timeout(const void* q, const void* cache, const int* block_t
  * (backward dK/dV kernel; at head dim 128 the CTA-pair kernel),
  * FA_KERNEL_BWD_DQ (backward dQ kernel); FA_KERNEL_KV4_WRITE, _READ, _FWD and
  * _MERGE (the 4-bit cache's writing, reading, attention and the merge of what
- * its CTAs leave in parts).
+ * its CTAs leave in parts); FA_KERNEL_ROPE; FA_KERNEL_PACKED_PLAN, _FWD and
+ * _MERGE (packed sequences' planning, of either pass, their attention and the
+ * merge of its parts; their backward kernels count under the FA_KERNEL_BWD ids).
  *   fa_timing_enable(on) : 1 starts recording (and drops old records), 0 stops.
  *   fa_timing_read(kernel, launches, total_ms) : waits for the recorded
  *       events of that kernel, returns how many launches were recorded and

@@ -2,19 +2,18 @@
 
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
 
 import exact_attention_92_gb300 as fa
-from exact_attention_92_gb300 import _binding
+from exact_attention_92_gb300 import _binding, build
 from oracle import packed as oracle
 
 
 @pytest.fixture(scope="module")
 def lib():
-    from exact_attention_92_gb300 import build
-
     build.build()
     return fa.load()
 
@@ -137,3 +136,48 @@ def test_binding_refuses_what_is_no_tensor(lib):
             fa.fa_packed_fwd(bad, bad, bad, bad, bad, bad, bad)
         with pytest.raises(TypeError):
             fa.fa_prefix_fwd(bad, bad, bad, bad, bad, bad, bad, bad, bad)
+
+
+def _native():
+    torch = pytest.importorskip("torch")
+    native = _binding._native_caller(torch.__version__, "._packed_call", "the calls on packed sequences")
+    assert native is not None, "the native caller is built where torch is installed"
+    return native
+
+
+def test_native_caller_checks_its_numbers(lib):
+    native = _native()
+    for call in (native.bind, native.rope, native.forward, native.backward):
+        for args in ((), (1, 2), (None,) * 30):
+            with pytest.raises(TypeError):
+                call(*args)
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_binding_refuses_host_tensors(lib, native, monkeypatch):
+    torch = pytest.importorskip("torch")
+    if not native:
+        monkeypatch.setattr(_binding, "_packed", False)
+    q = torch.zeros(6, 2, 64, dtype=torch.bfloat16)
+    cu, lse = torch.tensor([0, 2, 6], dtype=torch.int32), torch.zeros(2, 6)
+    for call in (lambda: fa.fa_packed_fwd(q, q, q, q, lse, cu, cu), lambda: fa.fa_prefix_fwd(q, q, q, q, q, q, lse, cu, cu),
+                 lambda: fa.fa_packed_bwd(q, q, q, q, lse, q, q, q, q, cu, cu),
+                 lambda: fa.fa_rope(q, q, q, q, torch.zeros(32, dtype=torch.int64))):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_build_does_without_a_native_caller(lib, monkeypatch, tmp_path):
+    """A compiler that is not there costs the native caller only; one of an older source is not left behind."""
+    pytest.importorskip("torch")
+    cxx = tmp_path / "cxx"
+    cxx.write_text('#!/bin/sh\nwhile [ "$1" != -o ]; do shift; done\necho made > "$2"\n')
+    cxx.chmod(0o755)
+    monkeypatch.setenv("CXX", str(cxx))
+    monkeypatch.setattr(build, "PACKED_CALL", str(tmp_path / "_packed_call.so"))
+    assert build.build_packed_call() == build.PACKED_CALL
+    os.utime(build.PACKED_CALL, (1, 1))
+    monkeypatch.setenv("CXX", "/nonexistent/c++")
+    with pytest.warns(UserWarning, match="ctypes"):
+        assert build.build_packed_call() is None
+    assert not os.path.exists(build.PACKED_CALL)
