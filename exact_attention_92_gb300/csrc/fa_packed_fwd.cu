@@ -496,7 +496,6 @@ __global__ void __launch_bounds__(384, 1)
         const int head = w.hk * p.group + w.g0 + gh;
         float m_ref = -INFINITY;  // reference max of this row, log2 units
         float l = 0.f;     // sum of the fp32 weights: L = m + log l
-        float l_bf = 0.f;  // sum of the bf16-rounded weights the PV MMA takes: O = O~ / l_bf
         for (int j = 0; j < steps; ++j) {
           ok = __all_sync(0xffffffffu, mbar_wait(s_full, sc & 1, ctl, kWaitSFull));
           ++sc;
@@ -554,7 +553,6 @@ __global__ void __launch_bounds__(384, 1)
             const float m_new = fmaxf(m_ref, m_tile);
             f = (m_new == -INFINITY) ? 1.f : ex2_approx(m_ref - m_new);
             l *= f;
-            l_bf *= f;
             m_ref = m_new;
             rescale = true;
           }
@@ -562,7 +560,6 @@ __global__ void __launch_bounds__(384, 1)
           const float2 sl2v = make_float2(sl2, sl2);
           const float2 negv = make_float2(-m_exp, -m_exp);
           float2 ls0 = make_float2(0.f, 0.f), ls1 = ls0;
-          float lr0 = 0.f, lr1 = 0.f, lr2 = 0.f, lr3 = 0.f;
 #pragma unroll
           for (int h = 0; h < kTileN / 32; ++h) {
             uint32_t pk_[16];
@@ -574,19 +571,14 @@ __global__ void __launch_bounds__(384, 1)
               const uint32_t pp = pack_bf16(p0, p1);
               if ((e >> 1) & 1) {
                 ls1 = __fadd2_rn(ls1, make_float2(p0, p1));
-                lr2 = add_bf16_lo(lr2, pp);
-                lr3 = add_bf16_hi(lr3, pp);
               } else {
                 ls0 = __fadd2_rn(ls0, make_float2(p0, p1));
-                lr0 = add_bf16_lo(lr0, pp);
-                lr1 = add_bf16_hi(lr1, pp);
               }
               pk_[e / 2] = pp;
             }
             tmem_st16(tS + 16 * h, pk_);
           }
           l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
-          l_bf += (lr0 + lr1) + (lr2 + lr3);
           if (rescale) {
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -631,7 +623,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int i = 0; i < D; ++i) o[i] = 0u;
         }
         // A row that saw no key has l = 0: O = 0, L = -inf.
-        const float inv_l = l_bf > 0.f ? 1.0f / l_bf : 0.f;
+        const float inv_l = l > 0.f ? 1.0f / l : 0.f;
         const float lse = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
         const float2 il = make_float2(inv_l, inv_l);
         if (!w.cut && !p.shared) {
