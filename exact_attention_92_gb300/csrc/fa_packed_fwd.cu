@@ -39,6 +39,12 @@ struct Cfg {
   static constexpr int kThreads = 384;
   __host__ __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
   __host__ __device__ static constexpr uint32_t col_o(int t) { return 256u + (uint32_t)kOCols * t; }
+  // The weights P take the place of S in tensor memory, or columns of their own where
+  // there is room (d = 64): then S of the next keys is worked out while the
+  // element-wise warps still have this one (64 sequences' steps over 4096 keys 173 ->
+  // 165 us, 4 prompts of 4096 without a mask 533 -> 519).
+  static constexpr bool kOwnP = D == 64;
+  __host__ __device__ static constexpr uint32_t col_p(int t) { return kOwnP ? 256u + 2 * kOCols + 64u * t : col_s(t); }
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTileBytes;
@@ -46,7 +52,7 @@ struct Cfg {
   // (32 rows of 128 bytes, swizzled).
   static constexpr int kOffOut = kOffKV + kStages * kTileBytes;
   static constexpr int kOffBar = kOffOut + 8 * 4096;
-  static constexpr int kPhaseBars = 2 + 2 + 2 * kStages + 2 + 2 + 2;
+  static constexpr int kPhaseBars = 2 + 2 + 2 * kStages + 2 + 2 + 2 + 2;
   static constexpr int kNumBars = 2 * kPhaseBars + 1 + 2;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
   static_assert(kSmemBytes <= 232448, "shared memory");
@@ -139,7 +145,8 @@ struct Bars {
   __device__ __forceinline__ uint64_t* kv_empty(int s) const { return b + 4 + kStages + s; }
   __device__ __forceinline__ uint64_t* s_full(int t) const { return b + 4 + 2 * kStages + t; }
   __device__ __forceinline__ uint64_t* p_full(int t) const { return b + 6 + 2 * kStages + t; }
-  __device__ __forceinline__ uint64_t* o_full(int t) const { return b + 8 + 2 * kStages + t; }
+  __device__ __forceinline__ uint64_t* s_read(int t) const { return b + 8 + 2 * kStages + t; }
+  __device__ __forceinline__ uint64_t* o_full(int t) const { return b + 10 + 2 * kStages + t; }
 };
 
 // Key tile x of a unit, K or V, into a ring slot.
@@ -224,8 +231,8 @@ __global__ void __launch_bounds__(384, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i) {
       const int k = i % C::kPhaseBars;
-      const bool p_full = i < 2 * C::kPhaseBars && (k == 6 + 2 * C::kStages || k == 7 + 2 * C::kStages);
-      mbar_init(&bars[i], p_full ? 4 : 1);  // p_full: a warpgroup's warps
+      const bool of_warps = i < 2 * C::kPhaseBars && k >= 6 + 2 * C::kStages && k < 10 + 2 * C::kStages;
+      mbar_init(&bars[i], of_warps ? 4 : 1);  // p_full, s_read: a warpgroup's warps
     }
     fence_barrier_init();
   }
@@ -262,17 +269,19 @@ __global__ void __launch_bounds__(384, 1)
     Piece w;
     constexpr int t = decltype(which_t)::value;
     const uint32_t q_lo = q_lo0 + t * kTileStep, t_s = tmem + C::col_s(t), t_o = tmem + C::col_o(t);
-    uint32_t pos = 0, qn = 0, pn = 0;
+    const uint32_t t_p = tmem + C::col_p(t);
+    uint32_t pos = 0, qn = 0, pn = 0, sn = 0;  // pos: the unit's first ring place
     auto key_slot = [&](uint32_t i) { return t * kHalf + i % kHalf; };
     auto wait_kv = [&](uint32_t i) -> bool { return wait(sb.kv_full(key_slot(i)), (i / kHalf) & 1, kWaitKvFull); };
-    auto issue_s = [&](bool last) -> bool {  // S of the K at `pos`
-      if (!wait_kv(pos)) return false;
+    auto issue_s = [&](int j, bool last) -> bool {  // S of the unit's key tile j
+      const uint32_t at = pos + 2 * j;
+      if (!wait_kv(at) || (C::kOwnP && sn > 0 && !wait(sb.s_read(t), (sn - 1) & 1, kWaitPFull))) return false;
+      ++sn;
       tc_fence_after();
-      issue_qk<D>(t_s, q_lo, k_lo0 + key_slot(pos) * kTileStep, hi);
+      issue_qk<D>(t_s, q_lo, k_lo0 + key_slot(at) * kTileStep, hi);
       mma_commit_w(sb.s_full(t));
       if (last) mma_commit_w(sb.q_empty(t));
-      mma_commit_w(sb.kv_empty(key_slot(pos)));
-      ++pos;
+      mma_commit_w(sb.kv_empty(key_slot(at)));
       return true;
     };
     Walk<false> walk(p, kSmall, 2 * blockIdx.x + t);
@@ -280,21 +289,21 @@ __global__ void __launch_bounds__(384, 1)
       const int n = w.hi - w.lo;
       if (n == 0) continue;
       // (The loads wait for the whole blocks' products.)
-      ok = wait(sb.q_full(t), qn & 1, kWaitQFull) && issue_s(n == 1);
+      ok = wait(sb.q_full(t), qn & 1, kWaitQFull) && issue_s(0, n == 1);
       ++qn;
       for (int j = 0; ok && j < n; ++j) {
-        ok = wait_kv(pos) && wait(sb.p_full(t), pn & 1, kWaitPFull);
+        const uint32_t at = pos + 2 * j + 1;
+        if (C::kOwnP && j + 1 < n) ok = issue_s(j + 1, j + 2 == n);
+        ok = ok && wait_kv(at) && wait(sb.p_full(t), pn & 1, kWaitPFull);
         ++pn;
         if (!ok) break;
         tc_fence_after();
-        issue_pv<D>(t_o, t_s, v_lo0 + key_slot(pos) * kTileStep, hi, j > 0);
-        mma_commit_w(sb.kv_empty(key_slot(pos)));
-        ++pos;
-        if (j + 1 < n)
-          ok = issue_s(j + 2 == n);
-        else
-          mma_commit_w(sb.o_full(t));
+        issue_pv<D>(t_o, t_p, v_lo0 + key_slot(at) * kTileStep, hi, j > 0);
+        mma_commit_w(sb.kv_empty(key_slot(at)));
+        if (C::kOwnP || j + 1 == n) mma_commit_w(sb.o_full(t));
+        if (!C::kOwnP && j + 1 < n) ok = issue_s(j + 1, j + 2 == n);
       }
+      pos += 2 * n;
     }
     // Every MMA this warp issued completes before TMEM is released.
     mma_commit_w(&drain[t]);
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(384, 1)
       };
       Piece w;
       // Whole blocks: the order of fa_fwd.cu.
-      uint32_t rc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+      uint32_t rc = 0, qc[2] = {0, 0}, pc[2] = {0, 0}, sc[2] = {0, 0};
       auto wait_kv = [&](uint32_t pos) -> bool {
         return wait(wb.kv_full(pos % C::kStages), (pos / C::kStages) & 1, kWaitKvFull);
       };
@@ -403,53 +412,95 @@ __global__ void __launch_bounds__(384, 1)
           ok = wait(wb.q_full(t), qc[t] & 1, kWaitQFull);
           ++qc[t];
         }
-        ok = ok && wait_kv(rc);
-        if (!ok) break;
-        tc_fence_after();
+        if constexpr (C::kOwnP) {
+          // S of the unit's key tile j for one tile of rows.
+          auto issue_s = [&](int t, int j) {
+            const int nt = t ? n1 : w.n0;
+            const uint32_t slot = (rc + 2 * j) % C::kStages;
+            if (sc[t] > 0) ok = wait(wb.s_read(t), (sc[t] - 1) & 1, kWaitPFull);
+            ++sc[t];
+            ok = ok && wait_kv(rc + 2 * j);
+            if (!ok) return;
+            tc_fence_after();
+            issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + slot * kTileStep, hi);
+            mma_commit_w(wb.s_full(t));
+            if (j + 1 == nt) mma_commit_w(wb.q_empty(t));  // Q_t's last product
+          };
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int nt = t ? n1 : w.n0;
-          if (nt == 0) continue;
-          issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + (rc % C::kStages) * kTileStep, hi);
-          mma_commit_w(wb.s_full(t));
-          if (nt == 1) mma_commit_w(wb.q_empty(t));  // Q_t's last product
-        }
-        mma_commit_w(wb.kv_empty(rc % C::kStages));
-        for (int j = 0; ok && j < n1; ++j) {
-          const uint32_t pos_v = rc + 2 * j + 1;
-          const uint32_t pos_k = pos_v + 1;
-          const uint32_t slot_v = pos_v % C::kStages;
-          const uint32_t slot_k = pos_k % C::kStages;
-          ok = wait_kv(pos_v);
+          for (int t = 0; t < 2; ++t)
+            if (ok && (t ? n1 : w.n0) > 0) issue_s(t, 0);
+          if (ok) mma_commit_w(wb.kv_empty(rc % C::kStages));
+          // A tile's next S goes ahead of its product with V, and all of one tile ahead of
+          // the other's: that keeps the warpgroups half a step apart, one in the maxima
+          // while the other is in the exponentials.
+          for (int j = 0; ok && j < n1; ++j) {
+            const uint32_t slot = (rc + 2 * j + 1) % C::kStages;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int nt = t ? n1 : w.n0;
+              if (!ok || j >= nt) continue;
+              if (j + 1 < nt) issue_s(t, j + 1);
+              ok = ok && wait_kv(rc + 2 * j + 1) && wait(wb.p_full(t), pc[t] & 1, kWaitPFull);
+              ++pc[t];
+              if (!ok) continue;
+              tc_fence_after();
+              issue_pv<D>(tmem + C::col_o(t), tmem + C::col_p(t), v_lo0 + slot * kTileStep, hi, j > 0);
+              mma_commit_w(wb.o_full(t));
+            }
+            if (!ok) break;
+            if (j + 1 < n1) mma_commit_w(wb.kv_empty((rc + 2 * j + 2) % C::kStages));
+            mma_commit_w(wb.kv_empty(slot));
+          }
+          if (!ok) break;
+        } else {
+          ok = ok && wait_kv(rc);
           if (!ok) break;
           tc_fence_after();
-          bool k_ready = false;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int nt = t ? n1 : w.n0;
-            if (!ok || j >= nt) continue;
-            ok = wait(wb.p_full(t), pc[t] & 1, kWaitPFull);
-            ++pc[t];
-            if (!ok) continue;
-            tc_fence_after();
-            issue_pv<D>(tmem + C::col_o(t), tmem + C::col_s(t), v_lo0 + slot_v * kTileStep, hi, j > 0);
-            if (j + 1 < nt) {
-              if (!k_ready) {
-                ok = wait_kv(pos_k);
-                if (!ok) continue;
-                tc_fence_after();
-                k_ready = true;
-              }
-              issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + slot_k * kTileStep, hi);
-              mma_commit_w(wb.s_full(t));
-              if (j + 2 == nt) mma_commit_w(wb.q_empty(t));  // Q_t's last product
-            } else {
-              mma_commit_w(wb.o_full(t));
-            }
+            if (nt == 0) continue;
+            issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + (rc % C::kStages) * kTileStep, hi);
+            mma_commit_w(wb.s_full(t));
+            if (nt == 1) mma_commit_w(wb.q_empty(t));  // Q_t's last product
           }
-          if (!ok) break;
-          mma_commit_w(wb.kv_empty(slot_v));
-          if (j + 1 < n1) mma_commit_w(wb.kv_empty(slot_k));
+          mma_commit_w(wb.kv_empty(rc % C::kStages));
+          for (int j = 0; ok && j < n1; ++j) {
+            const uint32_t pos_v = rc + 2 * j + 1;
+            const uint32_t pos_k = pos_v + 1;
+            const uint32_t slot_v = pos_v % C::kStages;
+            const uint32_t slot_k = pos_k % C::kStages;
+            ok = wait_kv(pos_v);
+            if (!ok) break;
+            tc_fence_after();
+            bool k_ready = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int nt = t ? n1 : w.n0;
+              if (!ok || j >= nt) continue;
+              ok = wait(wb.p_full(t), pc[t] & 1, kWaitPFull);
+              ++pc[t];
+              if (!ok) continue;
+              tc_fence_after();
+              issue_pv<D>(tmem + C::col_o(t), tmem + C::col_p(t), v_lo0 + slot_v * kTileStep, hi, j > 0);
+              if (j + 1 < nt) {
+                if (!k_ready) {
+                  ok = wait_kv(pos_k);
+                  if (!ok) continue;
+                  tc_fence_after();
+                  k_ready = true;
+                }
+                issue_qk<D>(tmem + C::col_s(t), q_lo0 + t * kTileStep, k_lo0 + slot_k * kTileStep, hi);
+                mma_commit_w(wb.s_full(t));
+                if (j + 2 == nt) mma_commit_w(wb.q_empty(t));  // Q_t's last product
+              } else {
+                mma_commit_w(wb.o_full(t));
+              }
+            }
+            if (!ok) break;
+            mma_commit_w(wb.kv_empty(slot_v));
+            if (j + 1 < n1) mma_commit_w(wb.kv_empty(slot_k));
+          }
         }
         rc += 2 * n1;
       }
@@ -469,6 +520,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
     const uint32_t tS = tmem + lane_off + C::col_s(t);
     const uint32_t tO = tmem + lane_off + C::col_o(t);
+    const uint32_t tP = tmem + lane_off + C::col_p(t);
     const int r_in_tile = 32 * wq + lane;
     const int tok = r_in_tile / p.group_heads;      // token within the tile
     const int gh = r_in_tile - tok * p.group_heads;  // query head within the group's run
@@ -482,7 +534,8 @@ __global__ void __launch_bounds__(384, 1)
       constexpr int kList = decltype(which)::value;
       constexpr bool small = kList == kSmall;
       const Bars<D, kList> bar(bars);
-      uint64_t *const s_full = bar.s_full(t), *const p_full = bar.p_full(t), *const o_full = bar.o_full(t);
+      uint64_t *const s_full = bar.s_full(t), *const p_full = bar.p_full(t), *const s_read = bar.s_read(t);
+      uint64_t* const o_full = bar.o_full(t);
       uint32_t sc = 0, oc = 0;
       Walk<true> walk(p, kList, small ? 2 * blockIdx.x + t : blockIdx.x);
       Piece w;
@@ -500,7 +553,19 @@ __global__ void __launch_bounds__(384, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(s_full, sc & 1, ctl, kWaitSFull));
           ++sc;
           if (!ok) break;
+          // With columns of its own, P is free (and O complete) once the product before
+          // this one is done.
+          auto wait_pv = [&]() -> bool {
+            if (!C::kOwnP || j == 0) return true;
+            const bool done = __all_sync(0xffffffffu, mbar_wait(o_full, oc & 1, ctl, kWaitOFull));
+            ++oc;
+            tc_fence_after();
+            return done;
+          };
           if (!live) {
+            if (C::kOwnP) mbar_arrive_warp(s_read);
+            ok = wait_pv();
+            if (!ok) break;
             mbar_arrive_warp(p_full);
             continue;
           }
@@ -509,6 +574,10 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int c = 0; c < kTileN / 32; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
           tmem_ld_wait<kTileN>(s);
+          if (C::kOwnP) {
+            tc_fence_before();
+            mbar_arrive_warp(s_read);
+          }
           float x[kTileN];
 #pragma unroll
           for (int c = 0; c < kTileN; ++c) x[c] = __uint_as_float(s[c]);
@@ -556,6 +625,8 @@ __global__ void __launch_bounds__(384, 1)
             m_ref = m_new;
             rescale = true;
           }
+          ok = wait_pv();
+          if (!ok) break;
           const float m_exp = (m_ref == -INFINITY) ? 0.f : m_ref;
           const float2 sl2v = make_float2(sl2, sl2);
           const float2 negv = make_float2(-m_exp, -m_exp);
@@ -576,7 +647,7 @@ __global__ void __launch_bounds__(384, 1)
               }
               pk_[e / 2] = pp;
             }
-            tmem_st16(tS + 16 * h, pk_);
+            tmem_st16(tP + 16 * h, pk_);
           }
           l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
           if (rescale) {
