@@ -24,6 +24,7 @@ namespace fa {
 
 using namespace dev;
 
+cudaError_t load_packed_fwd(int d);
 cudaError_t launch_packed_fwd(int d, const CUtensorMap* tm, const PackedFwd& p, cudaStream_t stream);
 
 namespace {
@@ -113,8 +114,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
     if (b < p.s.B) {
       const Seq s = load_seq(p.s, b);
       if (few) s_seq[b] = s;
-      const int rest = s.q_len % block;
-      n = ((long long)(rest > 0 && rest <= p.tile_tokens) << 32) + s.q_len / block + (rest > p.tile_tokens);
+      const int2 blocks = blocks_of(s, p.tile_tokens);
+      n = ((long long)blocks.y << 32) + blocks.x;
     }
     const long long sum = own + scan(n, &more);
     if (b < p.s.B) {
@@ -157,15 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
         const int b = seq_of(base, p.s.B, i);
         const Seq s = few ? s_seq[b] : load_seq(p.s, b);
         const int t0 = (list ? base0[b + 1] - base0[b] : i - base[b]) * block;
-        x.q_row = s.q + t0;
-        x.q_len = min(block, s.q_len - t0);
-        x.k_row = s.k;
-        x.k_len = s.k_len;
-        x.prefix = p.shared ? 0 : p.prefix_tiles;
-        x.pos = t0 + (p.s.causal == FA_CAUSAL_BOTTOM_RIGHT ? s.k_len - s.q_len : 0);
-        const int seen = p.s.causal == FA_CAUSAL_NONE ? s.k_len : min(s.k_len, max(0, x.pos + x.q_len));
-        x.tiles = x.prefix + (seen + kTileN - 1) / kTileN;
-        x.kind = 0;
+        x = block_at(s, t0, block, p.shared ? 0 : p.prefix_tiles, p.s.causal);
       }
       (list ? p.entries[kSmall] : p.entries[kWhole])[e] = x;
       places = (long long)x.tiles * tile_places(list) + unit_places(list);
@@ -535,6 +528,7 @@ cudaError_t load(int d) {
   const unsigned bit = 1u << (d / 32);
   if (loaded[dev].load(std::memory_order_relaxed) & bit) return cudaSuccess;
   e = d == 64 ? load_t<64>() : d == 96 ? load_t<96>() : load_t<128>();
+  if (e == cudaSuccess) e = fa::load_packed_fwd(d);
   if (e == cudaSuccess) loaded[dev].fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
@@ -586,11 +580,15 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   const long long entries = own_most + (p.shared ? Tq / block + 1 : 0);
   if (entries * hgs > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   const long long key_tiles = prefix_tiles + (Tk + fa::kTileN - 1) / fa::kTileN;
+  // Few keys of few sequences: each CTA finds its units itself, and none is cut, so
+  // that the forward kernel is all there is (one token, 8 heads of d = 128 over 768,
+  // 1024 and 1536 keys: 11.4, 13.7 and 19 us; planned, cut and merged 16.3, 15.3 and
+  // 15.1; 16 heads of d = 64 over 1024 and 1536: 11.1 and 14.4, planned 15.2 and 15.7).
+  const bool direct = B <= fa::kDirectSeqs && key_tiles <= 8 + (128 - d) / 16 && !p.shared && entries * hgs <= 4LL * sm_count;
   pl.min_tiles = 2;
-  // Few keys: no cuts, and no merge behind them (4 x 16 heads of d = 64 over 384 keys
-  // 12.3 us and not 13.4; 16.9 and not 16 over 768 keys of 8 heads of d = 128).
+  // Of many sequences: no cuts (and no merge) where the cuts would be of single tiles.
   pl.whole = key_tiles <= 4 && !p.shared ? 1 : 0;
-  p.grid = (int)std::min<long long>(std::min(sm_count, fa::kMostGrid), entries * hgs * (pl.whole ? 1 : std::max(1LL, key_tiles / pl.min_tiles)));
+  p.grid = (int)std::min<long long>(std::min(sm_count, fa::kMostGrid), entries * hgs * (pl.whole || direct ? 1 : std::max(1LL, key_tiles / pl.min_tiles)));
 
   // Workspace: the lists, then partial results.  Small blocks are the last of
   // their sequences (and one over the prefix).
@@ -600,7 +598,7 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   const size_t n_base = up(((size_t)B + 1) * sizeof(int));
   const size_t n_starts[2] = {up(((size_t)p.grid + 1) * sizeof(fa::PackedStart)),
                               up(((size_t)2 * p.grid + 1) * sizeof(fa::PackedStart))};
-  const bool cuts = !pl.whole;
+  const bool cuts = !pl.whole && !direct;
   size_t slot_rows[2] = {0, 0};
   if (cuts) {
     slot_rows[0] = (size_t)2 * p.grid * fa::kSlotRows;
@@ -634,33 +632,38 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
     if (encode_queries(&c.tm[5], o, Tq, H, p.group, d, p.group_heads, 32 / p.group_heads)) return FA_ERR_CUDA;
   }
   void* ws = nullptr;
-  if (fa::internal_workspace(&ws, bytes, c.st) != cudaSuccess) {
+  if (!direct && fa::internal_workspace(&ws, bytes, c.st) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_NO_MEMORY;
   }
-  char* at = static_cast<char*>(ws);
-  pl.cum = reinterpret_cast<long long*>(at);
-  at += n_cum;
-  for (int list = 0; list < 2; ++list) {
-    p.entries[list] = pl.entries[list] = reinterpret_cast<fa::PackedEntry*>(at);
-    at += n_entries[list];
-    pl.seq_base[list] = reinterpret_cast<int*>(at);
-    at += n_base;
-    p.starts[list] = pl.starts[list] = reinterpret_cast<fa::PackedStart*>(at);
-    at += n_starts[list];
-    if (slot_rows[list] > 0) {
-      p.o_slot[list] = reinterpret_cast<float*>(at);
-      p.lse_slot[list] = p.o_slot[list] + slot_rows[list] * d;
-      at += up(slot_rows[list] * (d + 1) * 4);
+  if (!direct) {
+    char* at = static_cast<char*>(ws);
+    pl.cum = reinterpret_cast<long long*>(at);
+    at += n_cum;
+    for (int list = 0; list < 2; ++list) {
+      p.entries[list] = pl.entries[list] = reinterpret_cast<fa::PackedEntry*>(at);
+      at += n_entries[list];
+      pl.seq_base[list] = reinterpret_cast<int*>(at);
+      at += n_base;
+      p.starts[list] = pl.starts[list] = reinterpret_cast<fa::PackedStart*>(at);
+      at += n_starts[list];
+      if (slot_rows[list] > 0) {
+        p.o_slot[list] = reinterpret_cast<float*>(at);
+        p.lse_slot[list] = p.o_slot[list] + slot_rows[list] * d;
+        at += up(slot_rows[list] * (d + 1) * 4);
+      }
+    }
+    p.header = pl.header = reinterpret_cast<fa::PackedHeader*>(at);
+    at += up(sizeof(fa::PackedHeader));
+    if (part_rows > 0) {
+      p.o_part = reinterpret_cast<float*>(at);
+      p.lse_part = p.o_part + part_rows * d;
     }
   }
-  p.header = pl.header = reinterpret_cast<fa::PackedHeader*>(at);
-  at += up(sizeof(fa::PackedHeader));
-  if (part_rows > 0) {
-    p.o_part = reinterpret_cast<float*>(at);
-    p.lse_part = p.o_part + part_rows * d;
-  }
-  pl.s = fa::PackedSeqs{cu_q, cu_k, used_k, B, Tq, Tk, causal, status};
+  p.s = pl.s = fa::PackedSeqs{cu_q, cu_k, used_k, B, Tq, Tk, causal, status};
+  p.direct = direct ? 1 : 0;
+  p.head_groups = (int)hgs;
+  p.prefix_tiles = prefix_tiles;
   pl.tile_tokens = p.tile_tokens;
   pl.prefix_tiles = prefix_tiles;
   pl.shared = p.shared;
@@ -685,10 +688,11 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   c.join_grid = (Tq + c.join_tokens - 1) / c.join_tokens;
   c.join_grid = std::min(c.join_grid, sm_count);
 
-  cudaError_t ce = fa::internal_timed_launch(FA_KERNEL_PACKED_PLAN, c.st, run_plan, &c);
+  cudaError_t ce = cudaSuccess;
+  if (!direct) ce = fa::internal_timed_launch(FA_KERNEL_PACKED_PLAN, c.st, run_plan, &c);
   if (ce == cudaSuccess) ce = fa::internal_timed_launch(FA_KERNEL_PACKED_FWD, c.st, run_fwd, &c);
   if (ce == cudaSuccess && (cuts || p.shared)) ce = fa::internal_timed_launch(FA_KERNEL_PACKED_MERGE, c.st, run_merge, &c);
-  cudaFreeAsync(ws, c.st);
+  if (ws != nullptr) cudaFreeAsync(ws, c.st);
   return ce == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "packed.h"
+#include "packed_seq.cuh"
 #include "sm103_primitives.cuh"
 
 namespace fa {
@@ -27,6 +28,77 @@ namespace fa {
 using namespace dev;
 
 namespace pk {
+
+// A stretch's part of one unit.
+struct Piece {
+  PackedEntry e;
+  int hk, g0;    // key/value head, first query head of the group's
+  int lo, hi;    // tiles of this part
+  int n0;        // steps of tile 0 of a whole block (tile 1, and a small block, take all)
+  bool cut;      // not the whole unit
+};
+
+// Steps of a whole block's first tile of rows: the second holds the block's last
+// token, the first may see less.
+__device__ __forceinline__ int first_steps(const PackedFwd& p, const Piece& w) {
+  const int own = p.causal ? min(w.e.k_len, max(0, w.e.pos + p.tile_tokens)) : w.e.k_len;
+  const int seen = w.e.kind ? w.e.prefix : w.e.prefix + (own + kTileN - 1) / kTileN;
+  return max(0, min(w.hi, seen) - w.lo);
+}
+
+// A call without a plan: the sequences, and the first unit of each, by list.
+struct DirectSeqs {
+  Seq seq[kDirectSeqs];
+  int base[2][kDirectSeqs + 1];
+  // By the threads of one warp.
+  __device__ __forceinline__ void fill(const PackedFwd& p) {
+    const int lane = threadIdx.x & 31;
+    Seq x{0, 0, 0, 0};
+    if (lane < p.s.B) x = load_seq(p.s, lane);
+    seq[lane] = x;
+    int2 n = blocks_of(x, p.tile_tokens);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, n.x, o), b = __shfl_up_sync(0xffffffffu, n.y, o);
+      if (lane >= o) n.x += a, n.y += b;
+    }
+    base[kWhole][lane + 1] = n.x;
+    base[kSmall][lane + 1] = n.y;
+    if (lane == 0) base[kWhole][0] = base[kSmall][0] = 0;
+  }
+};
+static_assert(kDirectSeqs == 32, "a lane each");
+
+// The units of a CTA (of its warpgroup t, of the small ones) without a plan: every
+// grid-th; the small ones from the CTAs on that have the fewest whole ones.
+struct DirectWalk {
+  const PackedFwd& p;
+  const DirectSeqs* q;
+  int list, entries, u, step;
+  __device__ __forceinline__ DirectWalk(const PackedFwd& params, const DirectSeqs* seqs, int which, int t)
+      : p(params), q(seqs), list(which) {
+    const int grid = gridDim.x, c = blockIdx.x;
+    entries = q->base[list][kDirectSeqs];
+    u = list == kSmall ? t * grid + (grid - 1 - c) : c;
+    step = list == kSmall ? 2 * grid : grid;
+  }
+  __device__ __forceinline__ bool get(Piece& w) {
+    if (u >= entries * p.head_groups) return false;
+    const int hg = u / entries, i = u - hg * entries;
+    const int b = seq_of(q->base[list], kDirectSeqs, i);
+    const int block = 2 * p.tile_tokens;
+    const int t0 = (list == kSmall ? q->base[kWhole][b + 1] - q->base[kWhole][b] : i - q->base[kWhole][b]) * block;
+    w.e = block_at(q->seq[b], t0, block, p.prefix_tiles, p.s.causal);
+    w.hk = hg / p.chunks;
+    w.g0 = (hg - w.hk * p.chunks) * p.group_heads;
+    w.lo = 0;
+    w.hi = w.e.tiles;
+    w.cut = false;
+    w.n0 = first_steps(p, w);
+    u += step;
+    return true;
+  }
+};
 
 template <int D>
 struct Cfg {
@@ -54,7 +126,8 @@ struct Cfg {
   static constexpr int kOffBar = kOffOut + 8 * 4096;
   static constexpr int kPhaseBars = 2 + 2 + 2 * kStages + 2 + 2 + 2 + 2;
   static constexpr int kNumBars = 2 * kPhaseBars + 1 + 2;
-  static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
+  static constexpr int kOffSeqs = (kOffBar + kNumBars * 8 + 16 + 15) / 16 * 16;
+  static constexpr int kSmemBytes = kOffSeqs + (int)sizeof(DirectSeqs);
   static_assert(kSmemBytes <= 232448, "shared memory");
   static constexpr float kRescaleThreshold = 24.0f;  // log2 units, as in fa_fwd.cu
   static constexpr int kRegsAtLaunch = 168;
@@ -64,20 +137,11 @@ struct Cfg {
   static_assert(kRegsCtl % 8 == 0 && kRegsMath % 8 == 0, "setmaxnreg counts are multiples of 8");
 };
 
-// A stretch's part of one unit.
-struct Piece {
-  PackedEntry e;
-  int hk, g0;    // key/value head, first query head of the group's
-  int lo, hi;    // tiles of this part
-  int n0;        // steps of tile 0 of a whole block (tile 1, and a small block, take all)
-  bool cut;      // not the whole unit
-};
-
 // The units of a stretch of a list, in order.  AHEAD: the next entry is fetched a
 // unit ahead (not by the issuing warps, whose registers are few: they come to a
 // unit while the element-wise warps still end the one before).
 template <bool AHEAD>
-struct Walk {
+struct PlannedWalk {
   const PackedFwd& p;
   PackedStart s0, s1;
   const PackedEntry* list;
@@ -90,7 +154,8 @@ struct Walk {
     const int4 a = w[0], b = w[1];
     return PackedEntry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   }
-  __device__ __forceinline__ Walk(const PackedFwd& params, int which, int stretch) : p(params) {
+  __device__ __forceinline__ PlannedWalk(const PackedFwd& params, const DirectSeqs*, int which, int t) : p(params) {
+    const int stretch = which == kSmall ? 2 * (int)blockIdx.x + t : (int)blockIdx.x;
     const PackedStart* s = p.starts[which] + stretch;
     s0 = s[0];
     s1 = s[1];
@@ -125,13 +190,13 @@ struct Walk {
       }
     }
     if (AHEAD && u <= u_last) next = fetch(list + at);
-    // The second tile holds the block's last token; the first may see less.
-    const int own = p.causal ? min(w.e.k_len, max(0, w.e.pos + p.tile_tokens)) : w.e.k_len;
-    const int seen = w.e.kind ? w.e.prefix : w.e.prefix + (own + kTileN - 1) / kTileN;
-    w.n0 = max(0, min(w.hi, seen) - w.lo);
+    w.n0 = first_steps(p, w);
     return true;
   }
 };
+
+template <bool AHEAD, bool DIRECT>
+using Walk = std::conditional_t<DIRECT, DirectWalk, PlannedWalk<AHEAD>>;
 
 // Barriers of one way of taking units: of whole blocks (list 0), or of small ones.
 template <int D, int LIST>
@@ -201,7 +266,7 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint32_t tmem_p, uint3
 
 }  // namespace pk
 
-template <int D>
+template <int D, bool DIRECT>
 __global__ void __launch_bounds__(384, 1)
     fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kp,
@@ -256,6 +321,11 @@ __global__ void __launch_bounds__(384, 1)
   // The plan, and whatever wrote the tensors, is complete.
   pdl_wait();
   pdl_trigger();
+  DirectSeqs* const seqs = reinterpret_cast<DirectSeqs*>(smem + C::kOffSeqs);
+  if constexpr (DIRECT) {
+    if (warp == 0) seqs->fill(p);
+    __syncthreads();
+  }
   // What an issuing warp does for the small blocks of warpgroup t.
   auto issue_small = [&](auto which_t, bool ok) {
     constexpr uint32_t hi = sdesc_hi(1024);
@@ -284,7 +354,7 @@ __global__ void __launch_bounds__(384, 1)
       mma_commit_w(sb.kv_empty(key_slot(at)));
       return true;
     };
-    Walk<false> walk(p, kSmall, 2 * blockIdx.x + t);
+    Walk<false, DIRECT> walk(p, seqs, kSmall, t);
     while (ok && walk.get(w)) {
       const int n = w.hi - w.lo;
       if (n == 0) continue;
@@ -313,7 +383,7 @@ __global__ void __launch_bounds__(384, 1)
   auto load_small = [&](auto which_t, bool ok) {
     Piece w;
     constexpr int t = decltype(which_t)::value;
-    Walk<true> walk(p, kSmall, 2 * blockIdx.x + t);
+    Walk<true, DIRECT> walk(p, seqs, kSmall, t);
     uint32_t pos = 0, qn = 0;
     bool first = true;
     while (ok && walk.get(w)) {
@@ -349,7 +419,7 @@ __global__ void __launch_bounds__(384, 1)
       Piece w;
       uint32_t rc = 0, qc[2] = {0, 0};
       // Whole blocks.
-      Walk<true> walk(p, kWhole, blockIdx.x);
+      Walk<true, DIRECT> walk(p, seqs, kWhole, 0);
       while (ok && walk.get(w)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -402,7 +472,7 @@ __global__ void __launch_bounds__(384, 1)
       auto wait_kv = [&](uint32_t pos) -> bool {
         return wait(wb.kv_full(pos % C::kStages), (pos / C::kStages) & 1, kWaitKvFull);
       };
-      Walk<false> walk(p, kWhole, blockIdx.x);
+      Walk<false, DIRECT> walk(p, seqs, kWhole, 0);
       while (ok && walk.get(w)) {
         const int n1 = w.hi - w.lo;
         if (n1 == 0) continue;
@@ -537,7 +607,7 @@ __global__ void __launch_bounds__(384, 1)
       uint64_t *const s_full = bar.s_full(t), *const p_full = bar.p_full(t), *const s_read = bar.s_read(t);
       uint64_t* const o_full = bar.o_full(t);
       uint32_t sc = 0, oc = 0;
-      Walk<true> walk(p, kList, small ? 2 * blockIdx.x + t : blockIdx.x);
+      Walk<true, DIRECT> walk(p, seqs, kList, t);
       Piece w;
       while (ok && walk.get(w)) {
         const int steps = t || small ? w.hi - w.lo : w.n0;
@@ -787,25 +857,32 @@ __global__ void __launch_bounds__(384, 1)
 // ------------------------------------------------------------------ launch
 
 template <int D>
+static cudaError_t load_t() {
+  constexpr auto kWhat = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  const cudaError_t e = cudaFuncSetAttribute(fa_packed_fwd_kernel<D, true>, kWhat, pk::Cfg<D>::kSmemBytes);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(fa_packed_fwd_kernel<D, false>, kWhat, pk::Cfg<D>::kSmemBytes);
+}
+
+template <int D, bool DIRECT>
 static cudaError_t launch_t(const CUtensorMap* tm, const PackedFwd& p, cudaStream_t stream) {
   using C = pk::Cfg<D>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(fa_packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  if (e != cudaSuccess) return e;
   // Two CTAs of a cluster run on a pair of SMs.  Where one of a pair takes whole
   // blocks and the other small ones, each in code of its own, the first takes 5 to
   // 8 % longer; so pairs stay together, and the plan gives both the same list.
-  return launch_pdl_clusters(p.grid % 2 == 0 ? 2 : 1, fa_packed_fwd_kernel<D>, dim3(p.grid), dim3(C::kThreads),
-                             C::kSmemBytes, stream, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], p);
+  return launch_pdl_clusters(!DIRECT && p.grid % 2 == 0 ? 2 : 1, fa_packed_fwd_kernel<D, DIRECT>, dim3(p.grid),
+                             dim3(C::kThreads), C::kSmemBytes, stream, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], p);
 }
+
+// Loads the kernels of a head dim on the current device; ahead of their launches.
+cudaError_t load_packed_fwd(int d) { return d == 64 ? load_t<64>() : d == 96 ? load_t<96>() : load_t<128>(); }
 
 // tm: Q, K, V, K and V of the prefix (any map where there is none), O (any map
 // without tile_store).
 cudaError_t launch_packed_fwd(int d, const CUtensorMap* tm, const PackedFwd& p, cudaStream_t stream) {
   switch (d) {
-    case 64: return launch_t<64>(tm, p, stream);
-    case 96: return launch_t<96>(tm, p, stream);
-    case 128: return launch_t<128>(tm, p, stream);
+    case 64: return p.direct ? launch_t<64, true>(tm, p, stream) : launch_t<64, false>(tm, p, stream);
+    case 96: return p.direct ? launch_t<96, true>(tm, p, stream) : launch_t<96, false>(tm, p, stream);
+    case 128: return p.direct ? launch_t<128, true>(tm, p, stream) : launch_t<128, false>(tm, p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -38,6 +38,7 @@
 namespace fa {
 
 constexpr int kSlotRows = 256;   // query rows of a whole block; half of it of a small one
+constexpr int kDirectSeqs = 32;  // sequences of a call without a plan
 constexpr int kMostGrid = 340;   // CTAs of the forward kernel: the merges keep their starts in shared memory
 
 // Places of a key tile and of a unit's start and end, in a quarter of a tile of a
@@ -95,6 +96,9 @@ struct PackedPlan {
 };
 
 struct PackedFwd {
+  PackedSeqs s;
+  int direct;         // 1: no plan; CTAs take units in turn
+  int head_groups, prefix_tiles;
   int H, Hkv;
   int group;          // query heads of a key/value head
   int group_heads;    // of them in a tile

@@ -73,5 +73,26 @@ __device__ __forceinline__ int seq_of(const int* base, int B, int i) {
   return lo;
 }
 
+// Blocks of a sequence, by list: whole ones, and at most one small one behind them.
+__device__ __forceinline__ int2 blocks_of(const Seq& s, int tile_tokens) {
+  const int block = 2 * tile_tokens, rest = s.q_len % block;
+  return make_int2(s.q_len / block + (rest > tile_tokens), rest > 0 && rest <= tile_tokens);
+}
+
+// The block of a sequence that starts at its token t0, behind `prefix` tiles.
+__device__ __forceinline__ PackedEntry block_at(const Seq& s, int t0, int block, int prefix, int causal) {
+  PackedEntry x;
+  x.q_row = s.q + t0;
+  x.q_len = min(block, s.q_len - t0);
+  x.k_row = s.k;
+  x.k_len = s.k_len;
+  x.prefix = prefix;
+  x.pos = t0 + (causal == FA_CAUSAL_BOTTOM_RIGHT ? s.k_len - s.q_len : 0);
+  const int seen = causal == FA_CAUSAL_NONE ? s.k_len : min(s.k_len, max(0, x.pos + x.q_len));
+  x.tiles = prefix + (seen + kTileN - 1) / kTileN;
+  x.kind = 0;
+  return x;
+}
+
 }  // namespace
 }  // namespace fa

@@ -242,7 +242,7 @@ def test_bad_bounds_are_skipped_and_reported(fa):
 
 
 def test_failed_workspace_is_reported(fa, monkeypatch):
-    lens = [50, 60]
+    lens = [1500, 600]
     q, k, v = make(lens, lens, 2, 2, 64, 12)
     monkeypatch.setenv("FA_TEST_FAIL_ALLOC", "1")
     with pytest.raises(fa.FaError) as e:
@@ -280,10 +280,10 @@ def test_refusals(fa):
 
 
 def test_launches(fa):
-    """A plan and the forward kernel; the merge where units can be cut."""
+    """The forward kernel alone over few keys; with a plan, and the merge where units can be cut."""
     ids = (fa.FA_KERNEL_PACKED_PLAN, fa.FA_KERNEL_PACKED_FWD, fa.FA_KERNEL_PACKED_MERGE)
-    for lens, merges in (([40, 50], 0), ([900, 300], 1)):
+    for lens, plans, merges in (([40, 50], 0, 0), ([13] * 33, 1, 0), ([900, 800], 1, 1)):
         q, k, v = make(lens, lens, 2, 2, 64, 14)
         before = [fa.fa_launch_count(i) for i in ids]
         fa.packed_forward(q, k, v, i32(starts(lens)))
-        assert [fa.fa_launch_count(i) - n for i, n in zip(ids, before)] == [1, 1, merges]
+        assert [fa.fa_launch_count(i) - n for i, n in zip(ids, before)] == [plans, 1, merges]
