@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) fa_packed_join_kernel(const 
   __shared__ PackedStart s_starts[3 * kMostGrid + 2];
   __shared__ MergeShared sh;
   __shared__ int s_own[kMergeThreads];  // the token's own block: entry and list; -1: of no sequence
+  __shared__ int s_row[kMergeThreads];  // and the block's first token
   const int tid = threadIdx.x;
   const int c16 = blockIdx.y;
   const int shares = kMergeThreads / n_rows, share = tid / n_rows;
@@ -417,36 +418,50 @@ __global__ void __launch_bounds__(kMergeThreads, 4) fa_packed_join_kernel(const 
       for (int i = lo + tid; i < hi; i += kMergeThreads) {
         const int2 row_len = __ldcg(reinterpret_cast<const int2*>(e + i));
         const int a = max(row_len.x - t0, 0), b = min(row_len.x + row_len.y - t0, n);
-        for (int x = a; x < b; ++x) s_own[x] = 2 * i + list;
+        for (int x = a; x < b; ++x) {
+          s_own[x] = 2 * i + list;
+          s_row[x] = row_len.x;
+        }
       }
     }
     __syncthreads();
-    if (!waited) pdl_wait();
-    waited = true;
     for (int r0 = 0; r0 < n * p.H; r0 += n_rows) {
       const int r = r0 + (tid & (n_rows - 1));
       const int x = r / p.H, head = r - x * p.H;
       const int at = at0 + x, token = t0 + x;
       const bool ok = x < n && s_own[x] >= 0;
-      Merge m;
+      // Where the two parts are: in the slots from stretch c on, or as a row of their own (c < 0).
+      int c[2] = {-1, -1}, unit[2], row[2];
+      const int own_list = ok ? s_own[x] & 1 : 0;
+      const int over_list = at / block >= h.over[kWhole];
       if (ok) {
-        const int own = s_own[x] >> 1, own_list = s_own[x] & 1;
+        const int own = s_own[x] >> 1;
         const int hk = head / p.group, g = head - hk * p.group;
         const int hg = hk * p.chunks + g / p.group_heads, gh = g % p.group_heads;
-        const int over = at / block;  // the block over the prefix
-#pragma unroll 1
+#pragma unroll
         for (int part = 0; part < 2; ++part) {
-          const int list = part ? own_list : over >= h.over[kWhole];
-          const int e = part ? own : list ? 0 : over;
-          const int t = part ? token - p.entries[list][own].q_row : at - over * block;
-          const int unit = hg * h.entries[list] + e;
-          const int turn = part ? shares - 1 - share : share;  // the prefix's parts from the first share on
+          const int list = part ? own_list : over_list;
+          const int e = part ? own : list ? 0 : at / block;
+          const int t = part ? token - s_row[x] : at % block;
+          unit[part] = hg * h.entries[list] + e;
+          row[part] = t / p.tile_tokens * kTileM + t % p.tile_tokens * p.group_heads + gh;
           const PackedStart* starts = s_starts + (list ? p.grid + 1 : 0);
-          const int c = stretch_of(starts, stretches(p, list), unit);
-          const PackedStart next = starts[c + 1];
-          if (next.unit == unit && next.tile > 0) {
-            const int row = t / p.tile_tokens * kTileM + t % p.tile_tokens * p.group_heads + gh;
-            add_slots<D>(p, list, starts + c, m, unit, c, turn, shares, row, c16);
+          const int at_c = stretch_of(starts, stretches(p, list), unit[part]);
+          const PackedStart next = starts[at_c + 1];
+          if (next.unit == unit[part] && next.tile > 0) c[part] = at_c;
+        }
+      }
+      if (!waited) pdl_wait();
+      waited = true;
+      Merge m;
+      if (ok) {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const int list = part ? own_list : over_list;
+          const int turn = part ? shares - 1 - share : share;  // the prefix's parts from the first share on
+          if (c[part] >= 0) {
+            const PackedStart* starts = s_starts + (list ? p.grid + 1 : 0);
+            add_slots<D>(p, list, starts + c[part], m, unit[part], c[part], turn, shares, row[part], c16);
           } else if (turn == 0) {
             const float4* o = reinterpret_cast<const float4*>(p.o_part + (((size_t)part * p.Tq + token) * p.H + head) * D) + 4 * c16;
             const float4 v[4] = {o[0], o[1], o[2], o[3]};

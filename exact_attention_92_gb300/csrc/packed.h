@@ -41,11 +41,13 @@ constexpr int kSlotRows = 256;   // query rows of a whole block; half of it of a
 constexpr int kDirectSeqs = 32;  // sequences of a call without a plan
 constexpr int kMostGrid = 340;   // CTAs of the forward kernel: the merges keep their starts in shared memory
 
-// Places of a key tile and of a unit's start and end, in a quarter of a tile of a
-// whole block (1.4 us at d = 128; a unit costs 3.5 to 4 us more).  Small blocks
-// run two at a time.
+// Places of a key tile and of a unit's start and end: an eighth of a tile of a whole
+// block (1.4 us at d = 128; small blocks run two at a time).  16 prompts of 16 Ki
+// tokens, a server's batch and 64 answers behind a prefix take 197, 204 and 54 us;
+// with 16 for a whole unit 200, 204 and 54, with 6 for a small one 197, 212 and 57,
+// with 7 for a small tile 197, 223 and 58.
 __host__ __device__ constexpr int tile_places(int list) { return list ? 6 : 8; }
-__host__ __device__ constexpr int unit_places(int list) { return list ? 6 : 16; }
+__host__ __device__ constexpr int unit_places(int list) { return list ? 4 : 14; }
 
 struct PackedEntry {
   int q_row, q_len;  // first token and tokens of the block
