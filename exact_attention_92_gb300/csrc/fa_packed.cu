@@ -95,6 +95,7 @@ __device__ __forceinline__ void plan_starts(const PackedPlan& p, const long long
 
 __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const PackedPlan p) {
   __shared__ long long s_warps[2][32];
+  __shared__ int s_starts[2][32];
   __shared__ Seq s_seq[kPlanShared];
   __shared__ int s_base[2][kPlanShared + 1];
   __shared__ long long s_cum[kPlanShared + 1];
@@ -106,13 +107,17 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
   int* const base0 = few ? s_base[0] : p.seq_base[0];
   int* const base1 = few ? s_base[1] : p.seq_base[1];
   Scan<long long> scan(s_warps);
+  Scan<int, true> furthest(s_starts);
   // Entries of the sequences, by list: [base[b], base[b + 1]).  Both numbers in one sum.
   long long own = 0, more;
+  int first_q = 0, next_q;
   for (int b0 = 0; b0 < p.s.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     long long n = 0;
+    const int at_q = max(first_q, furthest(b < p.s.B ? start_of(p.s.cu_q, b, p.s.Tq) : 0, &next_q));
+    first_q = max(first_q, next_q);
     if (b < p.s.B) {
-      const Seq s = load_seq(p.s, b);
+      const Seq s = load_seq(p.s, b, at_q);
       if (few) s_seq[b] = s;
       const int2 blocks = blocks_of(s, p.tile_tokens);
       n = ((long long)blocks.y << 32) + blocks.x;
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
         const int* base = list ? base1 : base0;
         const int i = e - n_over;
         const int b = seq_of(base, p.s.B, i);
-        const Seq s = few ? s_seq[b] : load_seq(p.s, b);
+        const Seq s = few ? s_seq[b] : load_seq(p.s, b, 0);  // (one with blocks is in order)
         const int t0 = (list ? base0[b + 1] - base0[b] : i - base[b]) * block;
         x = block_at(s, t0, block, p.shared ? 0 : p.prefix_tiles, p.s.causal);
       }

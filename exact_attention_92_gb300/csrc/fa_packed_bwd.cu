@@ -48,6 +48,7 @@ constexpr int kPlanShared = 1024;  // sequences up to this number have their pla
 
 struct BwdPlanShared {
   long long warps[2][32];
+  int starts[2][2][32];
   Seq seq[kPlanShared];
   int base[kPlanShared + 1];
   int bucket[kBuckets];
@@ -58,7 +59,7 @@ struct BwdPlanShared {
 template <bool KV>
 __device__ __forceinline__ BwdEntry make_entry(const PackedBwdPlan& p, const Seq* seq, const int* base, int i) {
   const int b = seq_of(base, p.s.B, i);
-  const Seq s = seq != nullptr ? seq[b] : load_seq(p.s, b);
+  const Seq s = seq != nullptr ? seq[b] : load_seq(p.s, b, 0);  // (one with entries is in order)
   BwdEntry e{s.q, s.q_len, s.k, s.k_len, i - base[b], 0, 0, 0};
   e.off = p.s.causal == FA_CAUSAL_BOTTOM_RIGHT ? s.k_len - s.q_len : 0;
   const bool causal = p.s.causal != FA_CAUSAL_NONE;
@@ -83,15 +84,21 @@ __device__ void make_list(const PackedBwdPlan& p, int* far_base, BwdEntry* out, 
   int* const base = few ? sh.base : far_base;
   const Seq* const seq = few ? sh.seq : nullptr;
   Scan<long long> scan(sh.warps);
+  Scan<int, true> furthest_q(sh.starts[0]), furthest_k(sh.starts[1]);
   if (tid == 0) sh.most = 0;
   for (int i = tid; i < kBuckets; i += kPlanThreads) sh.bucket[i] = 0;
   long long n_all = 0, more;
   int most = 0;  // no entry has more steps: those of a sequence without a mask
+  int first_q = 0, first_k = 0, next_q, next_k;
   for (int b0 = 0; b0 < p.s.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     int tiles = 0;
+    const int at_q = max(first_q, furthest_q(b < p.s.B ? start_of(p.s.cu_q, b, p.s.Tq) : 0, &next_q));
+    const int at_k = max(first_k, furthest_k(b < p.s.B ? start_of(p.s.cu_k, b, p.s.Tk) : 0, &next_k));
+    first_q = max(first_q, next_q);
+    first_k = max(first_k, next_k);
     if (b < p.s.B) {
-      const Seq s = load_seq(p.s, b);
+      const Seq s = load_seq(p.s, b, at_q, at_k);
       if (few) sh.seq[b] = s;
       tiles = ((KV ? s.k_len : s.q_len) + block - 1) / block;
       if (tiles > 0) most = max(most, ((KV ? s.q_len : s.k_len) + kTileM - 1) / kTileM);

@@ -54,7 +54,13 @@ struct DirectSeqs {
   __device__ __forceinline__ void fill(const PackedFwd& p) {
     const int lane = threadIdx.x & 31;
     Seq x{0, 0, 0, 0};
-    if (lane < p.s.B) x = load_seq(p.s, lane);
+    int first_q = lane < p.s.B ? start_of(p.s.cu_q, lane, p.s.Tq) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, first_q, o);
+      if (lane >= o) first_q = max(first_q, a);
+    }
+    if (lane < p.s.B) x = load_seq(p.s, lane, first_q);
     seq[lane] = x;
     int2 n = blocks_of(x, p.tile_tokens);
 #pragma unroll

@@ -14,11 +14,19 @@ struct Seq {
   int q, q_len, k, k_len;
 };
 
+// Where sequence b starts, as far as it is within the rows (0 otherwise).  A sequence
+// is out of order where one before it starts further on: taken all the same, such
+// sequences would overlap and have more blocks than there is room for.
+__device__ __forceinline__ int start_of(const int* cu, int b, int rows) {
+  const int x = cu[b];
+  return x >= 0 && x <= rows ? x : 0;
+}
+
 // Sequence b; one whose bounds are out of order or out of the tensors is empty
-// (and reported).
-__device__ __forceinline__ Seq load_seq(const PackedSeqs& s, int b) {
+// (and reported).  first_q: the furthest start of the sequences up to this one.
+__device__ __forceinline__ Seq load_seq(const PackedSeqs& s, int b, int first_q, int first_k = 0) {
   const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1], k0 = s.cu_k[b], k1 = s.cu_k[b + 1];
-  bool bad = q0 < 0 || q1 < q0 || q1 > s.Tq || k0 < 0 || k1 < k0 || k1 > s.Tk;
+  bool bad = q0 < first_q || q0 < 0 || q1 < q0 || q1 > s.Tq || k0 < first_k || k0 < 0 || k1 < k0 || k1 > s.Tk;
   int n = k1 - k0;
   if (!bad && s.used_k != nullptr) {
     const int used = s.used_k[b];
@@ -32,13 +40,14 @@ __device__ __forceinline__ Seq load_seq(const PackedSeqs& s, int b) {
   return Seq{q0, q1 - q0, k0, n};
 }
 
-// Sums over a CTA: of the threads up to this one, and of all.  Two sets of words
-// taken in turn, so that one barrier a scan is enough.
-template <typename T>
+// Sums (or, MAX, largest values) over a CTA: of the threads up to this one, and of
+// all.  Two sets of words taken in turn, so that one barrier a scan is enough.
+template <typename T, bool MAX = false>
 struct Scan {
   T (*warps)[32];
   int turn;
   __device__ __forceinline__ explicit Scan(T (*w)[32]) : warps(w), turn(0) {}
+  __device__ __forceinline__ static T join(T a, T b) { return MAX ? (a > b ? a : b) : a + b; }
   __device__ __forceinline__ T operator()(T v, T* total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     T* sums = warps[turn];
@@ -46,7 +55,7 @@ struct Scan {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const T x = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += x;
+      if (lane >= o) v = join(v, x);
     }
     if (lane == 31) sums[w] = v;
     __syncthreads();
@@ -54,11 +63,11 @@ struct Scan {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const T y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      if (lane >= o) x = join(x, y);
     }
     *total = __shfl_sync(0xffffffffu, x, 31);
     const T before = __shfl_sync(0xffffffffu, x, w > 0 ? w - 1 : 0);
-    return v + (w > 0 ? before : T(0));
+    return w > 0 ? join(v, before) : v;
   }
 };
 

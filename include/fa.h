@@ -517,9 +517,11 @@ int fa_rope_phases(const double* inv_freq, int n, uint64_t* phases);
  * a sequence's results, NaN included; within a sequence a NaN or an infinity in v
  * reaches every row, those that the mask hides it from too where they share a
  * tile of 128 keys with one that sees it, as in the other calls.
- * The arrays are read on the device: a sequence whose bounds are out of order or
- * out of range is skipped and FA_ERR_BAD_INDEX recorded (fa_poll_status).  They
- * must not be written while the call reads them.  The call may be captured into
+ * The arrays are read on the device: a sequence whose bounds are out of range or
+ * out of order (its queries', and in fa_packed_bwd its keys', starting ahead of
+ * those of one before it included) is skipped and FA_ERR_BAD_INDEX recorded
+ * (fa_poll_status).  They must not be written while the call reads them.  The
+ * call may be captured into
  * a CUDA graph, but not as the first call of the library on a device; replays go
  * by the lengths of their time.  Its kernels are launched with programmatic
  * stream serialization like those of the backward.  Results are the same from run to

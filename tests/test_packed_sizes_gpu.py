@@ -203,3 +203,65 @@ def test_steps_of_a_server(fa):
         want = oracle.forward(host(qr), *clean, starts(lq), starts([room] * B), scale_of(d), "bottom_right", used,
                               (host(kp), host(vp)))
         check_forward(o, lse, want, d)
+
+
+@pytest.mark.parametrize("causal", ["none", "top_left", "bottom_right"])
+@pytest.mark.parametrize("H,Hkv,d", [(2, 2, 64), (8, 2, 128), (3, 1, 96)])
+def test_ragged_lengths_with_a_plan(fa, causal, H, Hkv, d):
+    lens = [257, 1, 128, 0, 127, 300, 1000, 129, 2]
+    _check(fa, lens, lens, H, Hkv, d, causal, 100)
+    _check(fa, [40, 0, 1, 300, 1], [1700, 5, 0, 130, 900], H, Hkv, d, causal, 101)
+
+
+@pytest.mark.parametrize("prefix", [0, 500])
+def test_nan_stays_in_its_sequence_with_a_plan(fa, prefix):
+    torch = torch_cuda()
+    lens = [700, 70, 1300, 29] + [3] * 40
+    q, k, v = make(lens, lens, 4, 2, 128, 102, pad=5)
+    _, kp, vp = make([1], [500], 4, 2, 128, 103)
+    cu = i32(starts(lens))
+
+    def call():
+        return fa.prefix_forward(q, kp, vp, k, v, cu, causal=True) if prefix else fa.packed_forward(q, k, v, cu, causal=True)
+
+    clean, clean_l = call()
+    for x in (q, k, v):
+        x[700:770] = float("nan")
+        x[720:760] = float("inf")
+        x[sum(lens):] = float("nan")
+    o, lse = call()
+    keep = [*range(700), *range(770, sum(lens))]
+    assert torch.equal(o[keep], clean[keep]) and torch.equal(lse[:, keep], clean_l[:, keep])
+
+
+@pytest.mark.parametrize("B", [7, 41, 1501])
+def test_bounds_that_go_back_are_skipped(fa, B):
+    """0, T, 0, T, ...: the sequences from the second on are out of order and skipped, so that there are never more blocks
+    than rows; the first has what it has alone."""
+    torch = torch_cuda()
+    T, H, Hkv, d = 600, 2, 1, 64
+    q, k, v = make([T], [T], H, Hkv, d, 104)
+    do = torch.randn(q.shape, generator=torch.Generator().manual_seed(105)).to(torch.bfloat16).cuda()
+    good, bad = i32([0, T]), i32([T * (b % 2) for b in range(B + 1)])
+    _, kp, vp = make([1], [300], H, Hkv, d, 106)
+    o, lse = fa.packed_forward(q, k, v, good, causal=True)
+    want = fa.packed_backward(q, k, v, o, lse, do, good, causal=True)
+    behind, _ = fa.prefix_forward(q, kp, vp, k, v, good, causal=True)
+    assert fa.fa_poll_status() == fa.FA_OK
+    got, got_l = fa.packed_forward(q, k, v, bad, causal=True)
+    assert fa.fa_poll_status() == fa.FA_ERR_BAD_INDEX
+    scale = float(o.abs().max())
+    assert float((got.float() - o.float()).abs().max()) <= 2.0 ** -6 * scale  # (cut elsewhere, or not)
+    assert torch.allclose(got_l, lse, rtol=1e-5, atol=1e-5)
+    grads = fa.packed_backward(q, k, v, o, lse, do, bad, causal=True)
+    assert fa.fa_poll_status() == fa.FA_ERR_BAD_INDEX
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))
+    got, _ = fa.prefix_forward(q, kp, vp, k, v, bad, causal=True)
+    assert fa.fa_poll_status() == fa.FA_ERR_BAD_INDEX
+    assert float((got.float() - behind.float()).abs().max()) <= 2.0 ** -6 * float(behind.abs().max())
+    # Only the queries, or only the keys, go back.
+    long_k = i32([0, T] + [T] * (B - 1))
+    fa.packed_backward(q, k, v, o, lse, do, bad, long_k, causal=True)
+    assert fa.fa_poll_status() == fa.FA_ERR_BAD_INDEX
+    fa.packed_backward(q, k, v, o, lse, do, long_k, bad, causal=True)
+    assert fa.fa_poll_status() == fa.FA_ERR_BAD_INDEX
