@@ -601,10 +601,13 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   if (entries * hgs > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   const long long key_tiles = prefix_tiles + (Tk + fa::kTileN - 1) / fa::kTileN;
   // Few keys of few sequences: each CTA finds its units itself, and none is cut, so
-  // that the forward kernel is all there is (one token, 8 heads of d = 128 over 768,
-  // 1024 and 1536 keys: 11.4, 13.7 and 19 us; planned, cut and merged 16.3, 15.3 and
-  // 15.1; 16 heads of d = 64 over 1024 and 1536: 11.1 and 14.4, planned 15.2 and 15.7).
-  const bool direct = B <= fa::kDirectSeqs && key_tiles <= 8 + (128 - d) / 16 && !p.shared && entries * hgs <= 4LL * sm_count;
+  // that the forward kernel is all there is.  One token, 8 key/value heads of d = 128:
+  // 1 sequence of 1024, 1536, 2048 and 4096 keys 10.6, 13.3, 15.7 and 26 us, planned,
+  // cut and merged 15.3, 15.1, 15.6 and 18; 4 of 1024 keys 11.1 and 19.8, 8 of 512 8.5
+  // and 17.6; 4 prompts of 1024, 4 heads, 16.6 and 23.2.  (Of several sequences one may
+  // have all the keys: 26 us in place of 18, at worst.)
+  const bool direct = B <= fa::kDirectSeqs && key_tiles <= (std::min(B, Tq) > 1 ? 40 : 16) && !p.shared &&
+                      entries * hgs <= 4LL * sm_count;
   pl.min_tiles = 2;
   // Of many sequences: no cuts (and no merge) where the cuts would be of single tiles.
   pl.whole = key_tiles <= 4 && !p.shared ? 1 : 0;
@@ -682,6 +685,9 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   }
   p.s = pl.s = fa::PackedSeqs{cu_q, cu_k, used_k, B, Tq, Tk, causal, status};
   p.direct = direct ? 1 : 0;
+  // (One token, 8 heads of d = 128 over 600 and 1024 keys: 10.5 and 13.7 us by one
+  // warpgroup, 9.5 and 10.7 by two; 4 sequences of 150 tokens in all 6.6, and 7.2.)
+  p.halves = key_tiles >= 4 ? 1 : 0;
   p.head_groups = (int)hgs;
   p.prefix_tiles = prefix_tiles;
   pl.tile_tokens = p.tile_tokens;

@@ -76,20 +76,24 @@ struct DirectSeqs {
 static_assert(kDirectSeqs == 32, "a lane each");
 
 // The units of a CTA (of its warpgroup t, of the small ones) without a plan: every
-// grid-th; the small ones from the CTAs on that have the fewest whole ones.
+// grid-th; the small ones from the CTAs on that have the fewest whole ones.  Where
+// there are no more small ones than CTAs (dual), the warpgroups of a CTA halve the
+// keys of one.
 struct DirectWalk {
   const PackedFwd& p;
   const DirectSeqs* q;
-  int list, entries, u, step;
-  __device__ __forceinline__ DirectWalk(const PackedFwd& params, const DirectSeqs* seqs, int which, int t)
-      : p(params), q(seqs), list(which) {
+  int list, t, u;
+  // (Read again at each unit: the issuing warps have few registers.)
+  __device__ __forceinline__ int units() const { return q->base[list][kDirectSeqs] * p.head_groups; }
+  __device__ __forceinline__ bool dual() const { return list == kSmall && p.halves && units() <= (int)gridDim.x; }
+  __device__ __forceinline__ DirectWalk(const PackedFwd& params, const DirectSeqs* seqs, int which, int wg)
+      : p(params), q(seqs), list(which), t(wg) {
     const int grid = gridDim.x, c = blockIdx.x;
-    entries = q->base[list][kDirectSeqs];
-    u = list == kSmall ? t * grid + (grid - 1 - c) : c;
-    step = list == kSmall ? 2 * grid : grid;
+    u = list == kSmall ? (dual() ? 0 : t * grid) + (grid - 1 - c) : c;
   }
   __device__ __forceinline__ bool get(Piece& w) {
-    if (u >= entries * p.head_groups) return false;
+    if (u >= units()) return false;
+    const int entries = q->base[list][kDirectSeqs];
     const int hg = u / entries, i = u - hg * entries;
     const int b = seq_of(q->base[list], kDirectSeqs, i);
     const int block = 2 * p.tile_tokens;
@@ -97,11 +101,13 @@ struct DirectWalk {
     w.e = block_at(q->seq[b], t0, block, p.prefix_tiles, p.s.causal);
     w.hk = hg / p.chunks;
     w.g0 = (hg - w.hk * p.chunks) * p.group_heads;
-    w.lo = 0;
-    w.hi = w.e.tiles;
+    const bool dual = this->dual();
+    const int half = dual ? (w.e.tiles + 1) / 2 : w.e.tiles;
+    w.lo = t > 0 && dual ? half : 0;
+    w.hi = t > 0 && dual ? w.e.tiles : half;
     w.cut = false;
     w.n0 = first_steps(p, w);
-    u += step;
+    u += list == kSmall ? 2 * gridDim.x : gridDim.x;
     return true;
   }
 };
@@ -131,7 +137,7 @@ struct Cfg {
   static constexpr int kOffOut = kOffKV + kStages * kTileBytes;
   static constexpr int kOffBar = kOffOut + 8 * 4096;
   static constexpr int kPhaseBars = 2 + 2 + 2 * kStages + 2 + 2 + 2 + 2;
-  static constexpr int kNumBars = 2 * kPhaseBars + 1 + 2;
+  static constexpr int kNumBars = 2 * kPhaseBars + 1 + 2 + 1;
   static constexpr int kOffSeqs = (kOffBar + kNumBars * 8 + 16 + 15) / 16 * 16;
   static constexpr int kSmemBytes = kOffSeqs + (int)sizeof(DirectSeqs);
   static_assert(kSmemBytes <= 232448, "shared memory");
@@ -293,7 +299,8 @@ __global__ void __launch_bounds__(384, 1)
   const Bars<D, kSmall> sb(bars);
   uint64_t* whole_done = bars + 2 * C::kPhaseBars;    // every product of the whole blocks is complete
   uint64_t* drain = whole_done + 1;                   // [2]: of each issuing warp
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  uint64_t* half_done = drain + 2;                    // a unit's second half is complete (DirectWalk)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(half_done + 1);
   constexpr int kHalf = C::kStages / 2;               // ring slots of a warpgroup with small blocks
 
   const int warp = threadIdx.x / 32;
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < C::kNumBars; ++i) {
       const int k = i % C::kPhaseBars;
       const bool of_warps = i < 2 * C::kPhaseBars && k >= 6 + 2 * C::kStages && k < 10 + 2 * C::kStages;
-      mbar_init(&bars[i], of_warps ? 4 : 1);  // p_full, s_read: a warpgroup's warps
+      mbar_init(&bars[i], of_warps || i == C::kNumBars - 1 ? 4 : 1);  // p_full, s_read, half_done: a warpgroup's warps
     }
     fence_barrier_init();
   }
@@ -620,9 +627,6 @@ __global__ void __launch_bounds__(384, 1)
         const int first = small ? 0 : t * p.tile_tokens;         // the tile's first token in the block
         const int here = min(p.tile_tokens, w.e.q_len - first);  // its tokens
         const bool live = warp_tok < here;                       // the warp has rows
-        const bool row_ok = tok < here && tok < p.tile_tokens && w.g0 + gh < p.group;
-        const int token = w.e.q_row + first + tok;
-        const int head = w.hk * p.group + w.g0 + gh;
         float m_ref = -INFINITY;  // reference max of this row, log2 units
         float l = 0.f;     // sum of the fp32 weights: L = m + log l
         for (int j = 0; j < steps; ++j) {
@@ -749,6 +753,9 @@ __global__ void __launch_bounds__(384, 1)
         if (!ok) break;
         // ---- the rows' results.  What does not need O is worked out while the last
         // product runs; then all of the row is read at once.
+        const bool row_ok = tok < here && tok < p.tile_tokens && w.g0 + gh < p.group;
+        const int token = w.e.q_row + first + tok;
+        const int head = w.hk * p.group + w.g0 + gh;
         const int stretch = small ? 2 * (int)blockIdx.x + t : (int)blockIdx.x;
         const int sl = 2 * stretch + (w.lo > 0 ? 0 : 1);
         const int slot_row = (small ? 0 : kTileM * t) + r_in_tile;
@@ -759,7 +766,52 @@ __global__ void __launch_bounds__(384, 1)
           if (!ok) break;
           tc_fence_after();
         }
-        if (!live) continue;
+        bool dual = false;
+        if constexpr (DIRECT) dual = walk.dual();
+        if (!live) {
+          if (dual && t == 1) mbar_arrive_warp(half_done);
+          continue;
+        }
+        // Halves of a unit: the first one's warps find the second's rows of O in the same
+        // lanes of tensor memory, its maxima and sums in its room for O.
+        if (dual) {
+          uint32_t none;  // keeps the addresses from being worked out ahead of the steps, which have no register over
+          asm volatile("mov.u32 %0, 0;" : "=r"(none));
+          float2* const stats = reinterpret_cast<float2*>(smem + C::kOffOut + (4 + wq) * 4096) + lane + none;
+          if (t == 1) {
+            if (storing) {  // from that room, rows of a whole block
+              if (lane == 0) bulk_wait_read();
+              __syncwarp();
+            }
+            *stats = make_float2(m_ref, l);
+            tc_fence_before();
+            mbar_arrive_warp(half_done);
+            continue;
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait(half_done, 0, ctl, kWaitOFull));
+          if (!ok) break;
+          tc_fence_after();
+          const float2 other = *stats;
+          const float m_new = fmaxf(m_ref, other.x);
+          const float keep = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m_new);
+          const float add = other.x == -INFINITY ? 0.f : ex2_approx(other.x - m_new);
+          m_ref = m_new;
+          l = l * keep + other.y * add;
+          // (Of one tile the second half has nothing, and its columns hold anything.)
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t a[16], b[16];
+            tmem_ld16(tO + 16 * c + none, a);
+            tmem_ld16(tO + (C::col_o(1) - C::col_o(0)) + 16 * c + none, b);
+            tmem_ld_wait<16>(a);
+            tmem_ld_wait<16>(b);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              a[i] = __float_as_uint(__uint_as_float(a[i]) * keep + (add > 0.f ? __uint_as_float(b[i]) * add : 0.f));
+            tmem_st16(tO + 16 * c, a);
+          }
+          tmem_st_wait();
+        }
         uint32_t o[D];
         if (steps > 0) {
 #pragma unroll
@@ -773,7 +825,7 @@ __global__ void __launch_bounds__(384, 1)
         const float inv_l = l > 0.f ? 1.0f / l : 0.f;
         const float lse = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
         const float2 il = make_float2(inv_l, inv_l);
-        if (!w.cut && !p.shared) {
+        if (DIRECT || (!w.cut && !p.shared)) {
 #pragma unroll
           for (int i = 0; i < D / 2; ++i) {
             const float2 a = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il);

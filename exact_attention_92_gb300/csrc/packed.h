@@ -100,6 +100,7 @@ struct PackedPlan {
 struct PackedFwd {
   PackedSeqs s;
   int direct;         // 1: no plan; CTAs take units in turn
+  int halves;         // direct: small blocks may be halved between a CTA's warpgroups
   int head_groups, prefix_tiles;
   int H, Hkv;
   int group;          // query heads of a key/value head

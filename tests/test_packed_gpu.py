@@ -63,7 +63,8 @@ def test_query_heads_of_a_group(fa, H, Hkv):
 
 
 @pytest.mark.parametrize("d", [64, 96, 128])
-@pytest.mark.parametrize("H,Hkv,lens", [(4, 1, [3000, 5, 900]), (1, 1, [5000]), (8, 8, [1500, 700, 2])])
+@pytest.mark.parametrize("H,Hkv,lens", [(4, 1, [3000, 5, 900]), (1, 1, [5000]), (8, 8, [1500, 700, 2]),
+                                        (4, 1, [5000, 5, 900]), (8, 8, [2500, 2700, 2])])
 def test_long_sequences_are_cut_between_ctas(fa, d, H, Hkv, lens):
     _run(fa, lens, lens, H, Hkv, d, "top_left", seed=2)
 
@@ -242,7 +243,7 @@ def test_bad_bounds_are_skipped_and_reported(fa):
 
 
 def test_failed_workspace_is_reported(fa, monkeypatch):
-    lens = [1500, 600]
+    lens = [4500, 900]
     q, k, v = make(lens, lens, 2, 2, 64, 12)
     monkeypatch.setenv("FA_TEST_FAIL_ALLOC", "1")
     with pytest.raises(fa.FaError) as e:
@@ -282,7 +283,7 @@ def test_refusals(fa):
 def test_launches(fa):
     """The forward kernel alone over few keys; with a plan, and the merge where units can be cut."""
     ids = (fa.FA_KERNEL_PACKED_PLAN, fa.FA_KERNEL_PACKED_FWD, fa.FA_KERNEL_PACKED_MERGE)
-    for lens, plans, merges in (([40, 50], 0, 0), ([13] * 33, 1, 0), ([900, 800], 1, 1)):
+    for lens, plans, merges in (([40, 50], 0, 0), ([13] * 33, 1, 0), ([3000, 2400], 1, 1)):
         q, k, v = make(lens, lens, 2, 2, 64, 14)
         before = [fa.fa_launch_count(i) for i in ids]
         fa.packed_forward(q, k, v, i32(starts(lens)))
