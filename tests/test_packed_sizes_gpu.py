@@ -279,3 +279,47 @@ def test_bounds_that_go_back_are_skipped(fa, B):
     assert fa.fa_poll_status() == fa.FA_ERR_BAD_INDEX
     fa.packed_backward(q, k, v, o, lse, do, long_k, bad, causal=True)
     assert fa.fa_poll_status() == fa.FA_ERR_BAD_INDEX
+
+
+def test_graphs_with_a_plan(fa):
+    """Plan, clusters and merge (and the join behind a prefix) captured: the eager call's bits, the lengths of the replay, and
+    two graphs replayed in turn on two streams."""
+    torch = torch_cuda()
+    H, Hkv, d, room = 8, 2, 128, 9000
+    q, k, v = make([room], [room], H, Hkv, d, 120)
+    _, kp, vp = make([1], [3000], H, Hkv, d, 121)
+    first, second = [700, 90, 1300, 0, 33] + [1] * 40, [10, 1900, 0, 200, 13] + [2] * 40
+    cu = i32(starts(first))
+
+    def outputs():
+        return torch.zeros_like(q), torch.zeros(H, room, device="cuda")
+
+    calls = [lambda o, l: fa.fa_packed_fwd(q, k, v, o, l, cu, cu, causal=True),
+             lambda o, l: fa.fa_prefix_fwd(q, kp, vp, k, v, o, l, cu, cu, causal=True)]
+    eager = [outputs() for _ in calls]
+    for call, out in zip(calls, eager):
+        call(*out)
+    graphs, held = [], []
+    for call in calls:
+        out, g = outputs(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(*out)
+        graphs.append(g)
+        held.append(out)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for lens in (first, second, first):
+        cu.copy_(i32(starts(lens)))
+        for out in (*held, *eager):
+            for x in out:
+                x.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for call, out in zip(calls, eager):
+            call(*out)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(held, eager) for a, b in zip(x, y))
+    assert fa.fa_poll_status() == fa.FA_OK
