@@ -61,7 +61,7 @@ __device__ __forceinline__ void plan_starts(const PackedPlan& p, const long long
     const int size = (int)(cum[lo + 1] - cum[lo]), in = (int)(r - cum[lo]);
     const int n = (size - unit_places(list)) / tile_places(list);
     int x = in / tile_places(list);
-    const int least = p.whole ? n + 1 : p.min_tiles;
+    const int least = p.whole ? n + 1 : least_tiles(list);
     if (x < least && 2 * in < size) x = 0;
     else if (x < least || x > n - least) x = 0, ++lo;
     return PackedStart{hg * n_entries + lo - base, x};
@@ -291,7 +291,8 @@ __device__ __forceinline__ void write_rows(const PackedFwd& p, MergeShared& sh, 
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = pack_bf16(m.acc[2 * i] * inv, m.acc[2 * i + 1] * inv);
-  uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o) + token * p.o_row + head * p.o_head + 16 * c16);
+  __nv_bfloat16* row = reinterpret_cast<__nv_bfloat16*>(p.o) + token * p.o_row + head * p.o_head;
+  uint4* dst = reinterpret_cast<uint4*>(row + 16 * c16);
   dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
   dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
   if (c16 == 0) p.lse[(size_t)head * p.Tq + token] = m.tot > 0.f ? m.m + logf(m.tot) : -INFINITY;
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) fa_packed_merge_kernel(const
   const PackedStart* starts = p.starts[list];
   const PackedStart before_s = read_start(starts + c), s = read_start(starts + c + 1);
   if (s.tile == 0 || (before_s.unit == s.unit && before_s.tile > 0)) {
-    if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();  // one waits, so that this grid does not end ahead of the one before it
+    if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();  // one waits: this grid does not end ahead of the one before it
     return;
   }
   const int end = stretches(p, list);
@@ -468,7 +469,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) fa_packed_join_kernel(const 
             const PackedStart* starts = s_starts + (list ? p.grid + 1 : 0);
             add_slots<D>(p, list, starts + c[part], m, unit[part], c[part], turn, shares, row[part], c16);
           } else if (turn == 0) {
-            const float4* o = reinterpret_cast<const float4*>(p.o_part + (((size_t)part * p.Tq + token) * p.H + head) * D) + 4 * c16;
+            const float* rows = p.o_part + (((size_t)part * p.Tq + token) * p.H + head) * D;
+            const float4* o = reinterpret_cast<const float4*>(rows) + 4 * c16;
             const float4 v[4] = {o[0], o[1], o[2], o[3]};
             m.add(p.lse_part[((size_t)part * p.H + head) * p.Tq + token], v);
           }
@@ -608,10 +610,10 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
   // have all the keys: 26 us in place of 18, at worst.)
   const bool direct = B <= fa::kDirectSeqs && key_tiles <= (std::min(B, Tq) > 1 ? 40 : 16) && !p.shared &&
                       entries * hgs <= 4LL * sm_count;
-  pl.min_tiles = 2;
   // Of many sequences: no cuts (and no merge) where the cuts would be of single tiles.
   pl.whole = key_tiles <= 4 && !p.shared ? 1 : 0;
-  p.grid = (int)std::min<long long>(std::min(sm_count, fa::kMostGrid), entries * hgs * (pl.whole || direct ? 1 : std::max(1LL, key_tiles / pl.min_tiles)));
+  const long long parts = pl.whole || direct ? 1 : std::max(1LL, key_tiles / fa::least_tiles(fa::kWhole));
+  p.grid = (int)std::min<long long>(std::min(sm_count, fa::kMostGrid), entries * hgs * parts);
 
   // Workspace: the lists, then partial results.  Small blocks are the last of
   // their sequences (and one over the prefix).

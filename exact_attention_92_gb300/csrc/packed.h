@@ -49,6 +49,11 @@ constexpr int kMostGrid = 340;   // CTAs of the forward kernel: the merges keep 
 __host__ __device__ constexpr int tile_places(int list) { return list ? 6 : 8; }
 __host__ __device__ constexpr int unit_places(int list) { return list ? 4 : 14; }
 
+// A cut leaves at least so many tiles on either side.  (With 2 of a small block 64
+// steps over 512 keys, 4 tiles, take 38 us in place of 31; with 3 of a whole one
+// prompts take 196 in place of 199, but sentences 53.3 and not 52.5.)
+__host__ __device__ constexpr int least_tiles(int list) { return list ? 3 : 2; }
+
 struct PackedEntry {
   int q_row, q_len;  // first token and tokens of the block
   int k_row, k_len;  // first key row and keys of the sequence
@@ -88,7 +93,6 @@ struct PackedPlan {
   int shared;         // 1: the prefix has blocks of its own
   int head_groups;
   int grid;
-  int min_tiles;      // a cut leaves at least so many on either side
   int whole;          // 1: no cuts
   int* seq_base[2];        // [B + 1] first entry of each sequence (where it does not fit shared memory)
   PackedEntry* entries[2];
