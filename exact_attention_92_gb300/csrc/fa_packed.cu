@@ -182,7 +182,9 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
 }
 
 // Partial results of a unit, merged for one row and 16 channels at a time:
-// L = log sum exp(L_s), O = sum exp(L_s - L) O_s.
+// L = log sum exp(L_s), O = sum exp(L_s - L) O_s.  A part that holds NaN has L_s = NaN:
+// the maximum passes over it (fmaxf), its weight and so the sum `tot` and O are NaN, and
+// stay so.
 namespace {
 
 struct Merge {
@@ -267,7 +269,7 @@ __device__ __forceinline__ void write_rows(const PackedFwd& p, MergeShared& sh, 
       if (share < half && share + half < shares) {
         const int x = tid + half * n_rows;
         const float m_x = sh.m[x];
-        if (m_x != -INFINITY) {
+        if (sh.tot[x] != 0.f) {  // (0: it found no part; with m_x = -inf alone its parts may be NaN)
           const float m_new = fmaxf(m.m, m_x);
           const float keep = m.m == -INFINITY ? 0.f : exp2f((m.m - m_new) * 1.4426950408889634f);
           const float wgt = exp2f((m_x - m_new) * 1.4426950408889634f);
@@ -287,7 +289,7 @@ __device__ __forceinline__ void write_rows(const PackedFwd& p, MergeShared& sh, 
     ok = ok && share == 0;
   }
   if (!ok) return;
-  const float inv = m.tot > 0.f ? 1.0f / m.tot : 0.f;
+  const float inv = m.tot == 0.f ? 0.f : 1.0f / m.tot;
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = pack_bf16(m.acc[2 * i] * inv, m.acc[2 * i + 1] * inv);
@@ -295,7 +297,7 @@ __device__ __forceinline__ void write_rows(const PackedFwd& p, MergeShared& sh, 
   uint4* dst = reinterpret_cast<uint4*>(row + 16 * c16);
   dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
   dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  if (c16 == 0) p.lse[(size_t)head * p.Tq + token] = m.tot > 0.f ? m.m + logf(m.tot) : -INFINITY;
+  if (c16 == 0) p.lse[(size_t)head * p.Tq + token] = m.tot == 0.f ? -INFINITY : m.m + logf(m.tot);
 }
 
 // Query token and head of row r of a block's tile; false if it is none of them.
