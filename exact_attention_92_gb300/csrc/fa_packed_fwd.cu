@@ -635,6 +635,7 @@ __global__ void __launch_bounds__(384, 1)
         const int first = small ? 0 : t * p.tile_tokens;         // the tile's first token in the block
         const int here = min(p.tile_tokens, w.e.q_len - first);  // its tokens
         const bool live = warp_tok < here;                       // the warp has rows
+        const bool row_ok = tok < here && tok < p.tile_tokens && w.g0 + gh < p.group;
         float m_ref = -INFINITY;  // reference max of this row, log2 units
         float l = 0.f;     // sum of the fp32 weights: L = m + log l
         for (int j = 0; j < steps; ++j) {
@@ -705,7 +706,9 @@ __global__ void __launch_bounds__(384, 1)
           float f = 1.f;
           bool rescale = false;
           if (j == 0) {
-            m_ref = m_tile;
+            // A lane without a row holds another sequence's, or what shared memory held
+            // before: it never asks the warp to rescale, which moves the others' roundings.
+            m_ref = row_ok ? m_tile : INFINITY;
           } else if (__any_sync(0xffffffffu, m_tile > m_ref + C::kRescaleThreshold)) {
             const float m_new = fmaxf(m_ref, m_tile);
             f = (m_new == -INFINITY) ? 1.f : ex2_approx(m_ref - m_new);
@@ -761,7 +764,6 @@ __global__ void __launch_bounds__(384, 1)
         if (!ok) break;
         // ---- the rows' results.  What does not need O is worked out while the last
         // product runs; then all of the row is read at once.
-        const bool row_ok = tok < here && tok < p.tile_tokens && w.g0 + gh < p.group;
         const int token = w.e.q_row + first + tok;
         const int head = w.hk * p.group + w.g0 + gh;
         const int stretch = small ? 2 * (int)blockIdx.x + t : (int)blockIdx.x;

@@ -1,0 +1,61 @@
+"""Packed sequences: what other sequences hold, and what shared memory held before, moves no bit of a sequence's results."""
+
+import pytest
+
+from gpu_util import ensure_built, torch_cuda
+from packed_util import i32, make, starts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fa():
+    torch_cuda()
+    return ensure_built()
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("H,Hkv,pad,prefix", [(2, 2, 0, 0), (6, 2, 0, 0), (2, 2, 9000, 0), (8, 1, 9000, 0), (2, 2, 9000, 300),
+                                              (2, 2, 0, 300)])
+def test_large_neighbours(fa, d, H, Hkv, pad, prefix):
+    """Queries of the next sequence, and of no sequence, that share a tile with the first one's: their scores grow by hundreds
+    from one key tile to the next.  (`pad` rows of no sequence: room that takes a plan.)"""
+    torch = torch_cuda()
+    lq, lk = [5, 20], [1100, 40]
+    q, k, v = make(lq, lk, H, Hkv, d, 300, pad=pad + 30)
+    _, kp, vp = make([1], [max(1, prefix)], H, Hkv, d, 301)
+    cu = (i32(starts(lq)), i32(starts(lk)))
+
+    def call():
+        return fa.prefix_forward(q, kp, vp, k, v, *cu) if prefix else fa.packed_forward(q, k, v, *cu)
+
+    o, lse = call()
+    for first in (5, 25):  # of the next sequence; of none
+        was = q.clone()
+        q[first:] *= 256
+        got, got_l = call()
+        assert torch.equal(got[:first], o[:first]) and torch.equal(got_l[:, :first], lse[:, :first])
+        q.copy_(was)
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("H,Hkv,lens", [(3, 1, [84] * 8), (12, 4, [1300, 900, 30]), (7, 1, [18] * 40), (5, 5, [84] * 8)])
+def test_what_shared_memory_held(fa, d, H, Hkv, lens):
+    """Rows of a tile that no copy writes (126 and 127 of a group of three) hold an earlier call's queries, large or zero."""
+    torch = torch_cuda()
+    q, k, v = make(lens, [n + 700 for n in lens], H, Hkv, d, 310)
+    cu = (i32(starts(lens)), i32(starts([n + 700 for n in lens])))
+    fill, fk, fv = make([256 * 160], [100], 1, 1, d, 311)
+    fill_cu = (i32([0, 256 * 160]), i32([0, 100]))
+    spare, spare_l = torch.zeros_like(fill), torch.zeros(1, fill.shape[0], device="cuda")
+    out = []
+    for scale in (0.0, 256.0, 0.0):
+        big = fill * scale
+        o, lse = torch.zeros_like(q), torch.zeros(H, q.shape[0], device="cuda")
+        torch.cuda.synchronize()
+        fa.fa_packed_fwd(big, fk, fv, spare, spare_l, *fill_cu)
+        fa.fa_packed_fwd(q, k, v, o, lse, *cu)
+        torch.cuda.synchronize()
+        out.append((o, lse))
+    for o, lse in out[1:]:
+        assert torch.equal(o, out[0][0]) and torch.equal(lse, out[0][1])
