@@ -99,11 +99,14 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
   __shared__ Seq s_seq[kPlanShared];
   __shared__ int s_base[2][kPlanShared + 1];
   __shared__ long long s_cum[kPlanShared + 1];
+  __shared__ int s_span[2];  // the first and the end of the rows that sequences have
   const int tid = threadIdx.x;
   pdl_trigger();
   pdl_wait();
   const int block = 2 * p.tile_tokens;
   const bool few = p.s.B <= kPlanShared;
+  if (tid == 0) s_span[0] = p.s.Tq, s_span[1] = 0;
+  int from = p.s.Tq, to = 0;  // of this thread's sequences
   int* const base0 = few ? s_base[0] : p.seq_base[0];
   int* const base1 = few ? s_base[1] : p.seq_base[1];
   Scan<long long> scan(s_warps);
@@ -119,6 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
     if (b < p.s.B) {
       const Seq s = load_seq(p.s, b, at_q);
       if (few) s_seq[b] = s;
+      if (s.q_len > 0) from = min(from, s.q), to = max(to, s.q + s.q_len);
       const int2 blocks = blocks_of(s, p.tile_tokens);
       n = ((long long)blocks.y << 32) + blocks.x;
     }
@@ -130,12 +134,20 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const Pack
     own += more;
   }
   if (tid == 0) base0[0] = base1[0] = 0;
-  // Blocks over the prefix alone: all rows from the first sequence's first to
-  // the last one's last, whatever sequence they are of.
+  // Blocks over the prefix alone: all rows from the first sequence's first to the
+  // last one's last, whatever sequence they are of.  (Of those that were not skipped:
+  // cu_q[0] or cu_q[B] may be the bound that is out of order.)
   int first = 0, rows = 0;
   if (p.shared) {
-    first = min(max(p.s.cu_q[0], 0), p.s.Tq);
-    rows = max(0, min(p.s.cu_q[p.s.B], p.s.Tq) - first);
+    from = __reduce_min_sync(0xffffffffu, from);
+    to = __reduce_max_sync(0xffffffffu, to);
+    if ((tid & 31) == 0 && from < to) {
+      atomicMin(&s_span[0], from);
+      atomicMax(&s_span[1], to);
+    }
+    __syncthreads();
+    first = s_span[0];
+    rows = max(0, s_span[1] - first);
   }
   const int rest = rows % block;
   int over[2], entries[2];

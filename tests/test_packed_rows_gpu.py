@@ -1,4 +1,5 @@
-"""Packed sequences: what other sequences hold, and what shared memory held before, moves no bit of a sequence's results."""
+"""Packed sequences: what other sequences hold, their bad bounds, and what shared memory held before, move no bit of a
+sequence's results."""
 
 import pytest
 
@@ -59,3 +60,34 @@ def test_what_shared_memory_held(fa, d, H, Hkv, lens):
         out.append((o, lse))
     for o, lse in out[1:]:
         assert torch.equal(o, out[0][0]) and torch.equal(lse, out[0][1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_first_and_last_bounds_behind_a_shared_prefix(fa, d):
+    """Only the sequence with the bad bound is skipped: the others have the bits of a call in which it is empty.  (Forty
+    sequences behind 80 tiles: their rows go over the prefix together.)"""
+    torch = torch_cuda()
+    lq, H, Hkv, P = [3] * 40, 8, 2, 10240
+    lk = [(7 * i) % 90 for i in range(40)]
+    q, k, v = make(lq, lk, H, Hkv, d, 320)
+    _, kp, vp = make([1], [P], H, Hkv, d, 321)
+    T, at, cu_k = sum(lq), starts(lq), i32(starts(lk))
+
+    def call(cu_q):
+        o, lse = torch.full_like(q, 5.0), torch.full((H, T), 7.0, device="cuda")
+        fa.fa_prefix_fwd(q, kp, vp, k, v, o, lse, i32(cu_q), cu_k)
+        return o, lse, fa.fa_poll_status()
+
+    for cu_q, clean, gone in (
+            ([*at[:-1], 10], [*at[:-1], at[-2]], [(at[-2], T)]),      # the last one ends ahead of its start
+            ([*at[:-1], -4], [*at[:-1], at[-2]], [(at[-2], T)]),
+            ([*at[:-1], T + 9], [*at[:-1], at[-2]], [(at[-2], T)]),
+            ([T + 5, *at[1:]], [at[1], *at[1:]], [(0, at[1])]),       # the first one starts behind the rows
+            ([-3, *at[1:]], [at[1], *at[1:]], [(0, at[1])])):
+        want, want_l, status = call(clean)
+        assert status == fa.FA_OK
+        o, lse, status = call(cu_q)
+        assert status == fa.FA_ERR_BAD_INDEX
+        assert torch.equal(o, want) and torch.equal(lse, want_l)
+        for a, b in gone:
+            assert bool((o[a:b] == 5).all()) and bool((lse[:, a:b] == 7).all())
