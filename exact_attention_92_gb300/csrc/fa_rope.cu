@@ -11,8 +11,9 @@
 // 131072, more than the rounding to bf16.  So frequencies are held as the
 // fraction of a turn a position in 64-bit fixed point, f_i / (2 pi) * 2^64: the
 // product with the integer t, modulo 2^64, is the fraction of a turn itself,
-// off by t 2^-65 turns, and whole turns fall out of the integer arithmetic.  Its
-// upper 32 bits go to sincospif.
+// off by |t| 2^-65 turns (2^-33 at most: fa_rope_phases rounds to the nearest), and
+// whole turns fall out of the integer arithmetic.  Its upper 32 bits, as a float, go
+// to sincospif: in all an angle is off by less than 2^-24 of a half turn.
 //
 // Bound: memory, two bytes read and two written a channel.  A thread keeps the
 // cosines and sines of eight pairs (16-byte loads) and walks the heads of its
@@ -191,6 +192,17 @@ bool side(const fa_rows_t* x, const fa_rows_t* y, int heads, fa::RopeSide* s) {
   return true;
 }
 
+// The fraction of |x| (its distance from the integer below) in 128-bit fixed point,
+// negated modulo 1 where x is negative.  Each step is exact down to 2^-128.
+unsigned __int128 fraction(double x) {
+  const double a = std::fabs(x);
+  const double part = (a - std::floor(a)) * 18446744073709551616.0;  // 2^64
+  const double hi = std::floor(part);
+  const unsigned __int128 f =
+      ((unsigned __int128)(uint64_t)hi << 64) + (uint64_t)((part - hi) * 18446744073709551616.0);
+  return x < 0 ? 0 - f : f;
+}
+
 }  // namespace
 
 extern "C" {
@@ -199,12 +211,15 @@ int fa_rope_phases(const double* inv_freq, int n, uint64_t* phases) {
   if (inv_freq == nullptr || phases == nullptr || n < 1) return FA_ERR_INVALID_ARG;
   for (int i = 0; i < n; ++i) {
     if (!std::isfinite(inv_freq[i])) return FA_ERR_INVALID_ARG;
-    // The fraction of a turn, in two pieces of 32 bits: a long double may hold
-    // no more than a double does.
-    const double turns = std::fabs(inv_freq[i]) / 6.283185307179586476925286766559;
-    const double part = (turns - std::floor(turns)) * 4294967296.0;
-    const double hi = std::floor(part);
-    const uint64_t f = ((uint64_t)hi << 32) + (uint64_t)std::llrint((part - hi) * 4294967296.0);
+    // 1 / (2 pi) in three doubles is off by 2^-164; their products with a frequency
+    // below 2^64, as exact pairs, leave the nearest phase (a double's quotient alone
+    // would be off by 2^-53 of itself, 2^-24 of a turn at position 2^31).
+    const double x = std::fabs(inv_freq[i]);
+    constexpr double kTurn[3] = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57, -0x1.6447e493ad4cep-111};
+    const double p0 = x * kTurn[0], p1 = x * kTurn[1];
+    const unsigned __int128 turns = fraction(p0) + fraction(std::fma(x, kTurn[0], -p0)) + fraction(p1) +
+                                    fraction(std::fma(x, kTurn[1], -p1)) + fraction(x * kTurn[2]);
+    const uint64_t f = (uint64_t)((turns + ((unsigned __int128)1 << 63)) >> 64);
     phases[i] = inv_freq[i] < 0 ? 0 - f : f;
   }
   return FA_OK;

@@ -478,7 +478,8 @@ typedef struct {
  *   inverse      : nonzero turns by -theta: the gradients of q and k from those
  *                  of q_out and k_out
  * B * N <= 2^31 - 1; d as elsewhere.  Angles are exact to 2^-24 of a half turn at
- * any position; products are fp32, rounded once.
+ * any position (with phases of fa_rope_phases, of frequencies below 2^64); products
+ * are fp32, rounded once.
  */
 int fa_rope(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* q_out, const fa_rows_t* k_out,
             const uint64_t* phases, const int* positions, const int* start, int B, int N, int H, int Hkv, int d, int rot,
@@ -487,7 +488,7 @@ int fa_rope(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* q_out, cons
 /*
  * Frequencies (radians a position, finite) as the fraction of a turn a
  * position in 64-bit fixed point, phases[j] = inv_freq[j] / (2 pi) * 2^64 modulo
- * 2^64.  Host memory on both sides.
+ * 2^64, rounded to the nearest for frequencies below 2^64.  Host memory on both sides.
  */
 int fa_rope_phases(const double* inv_freq, int n, uint64_t* phases);
 
