@@ -72,9 +72,11 @@ struct SeqPart<true> {
   BwdEntry e;
 };
 
+// EARLY: read ahead of the wait for the kernel before, past the L1 cache.
+template <bool EARLY = false>
 __device__ __forceinline__ BwdEntry load_entry(const BwdEntry* e) {
   const int4* w = reinterpret_cast<const int4*>(e);
-  const int4 a = w[0], b = w[1];
+  const int4 a = EARLY ? __ldcg(w) : w[0], b = EARLY ? __ldcg(w + 1) : w[1];
   return BwdEntry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 

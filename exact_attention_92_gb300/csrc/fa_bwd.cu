@@ -154,7 +154,7 @@ template <bool PACKED>
 __device__ __forceinline__ BwdUnit<PACKED> decode_dq(const BwdParams& p, int u) {
   BwdUnit<PACKED> w;
   if constexpr (PACKED) {
-    w.e = load_entry(p.entries_q + u / p.H);
+    w.e = load_entry<true>(p.entries_q + u / p.H);
     w.bh = u % p.H;
     w.t = w.e.tile;
     w.first = 0;
@@ -833,8 +833,10 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{p.status, p.timeout_ns};
-  // (Packed: the units were there before any dK/dV CTA let this kernel start.)
-  const int n_units = PACKED ? p.entry_counts[1] * p.H : p.num_units;
+  // The units, L and D were complete before any dK/dV CTA let this kernel start.  They
+  // are read ahead of its wait, so past the L1 cache, as the merges of packed sequences
+  // read their plan.
+  const int n_units = PACKED ? __ldcg(p.entry_counts + 1) * p.H : p.num_units;
 
   if (warp == 9) {
     // ------------------------------------------------------------ producer
@@ -1109,9 +1111,9 @@ __global__ void __launch_bounds__(384, 1)
           continue;
         }
       }
-      const float Lraw = q < rows ? p.lse[row] : INFINITY;
+      const float Lraw = q < rows ? __ldcg(p.lse + row) : INFINITY;
       const float L = Lraw == -INFINITY ? INFINITY : Lraw * 1.4426950408889634f;  // no key seen: weights 0
-      const float Dq = q < rows ? p.dvec[row] : 0.f;
+      const float Dq = q < rows ? __ldcg(p.dvec + row) : 0.f;
       const int q_lo = w.t * kTileM + 32 * g;  // first query of this warp
       for (int jj = 0; ok && jj < w.count; ++jj, ++kc) {
         const uint32_t tS = tmem + lane_off + ((kc & 1) ? C::kColS1 : C::kColS0) + 64 * hc;

@@ -91,3 +91,27 @@ def test_bad_first_and_last_bounds_behind_a_shared_prefix(fa, d):
         assert torch.equal(o, want) and torch.equal(lse, want_l)
         for a, b in gone:
             assert bool((o[a:b] == 5).all()) and bool((lse[:, a:b] == 7).all())
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_calls_one_behind_the_other_read_their_own_units(fa, d):
+    """Backward calls back to back, whose workspace is the same memory and whose units, L and D change from call to call: each
+    has the bits that it has alone.  (The dQ kernel reads these ahead of its wait for the kernel before.)"""
+    torch = torch_cuda()
+    room, H, Hkv = 4000, 4, 2
+    q, k, v = make([room], [room], H, Hkv, d, 330)
+    do = torch.randn(q.shape, generator=torch.Generator().manual_seed(331)).to(torch.bfloat16).cuda()
+    cases = []
+    for lens in ([3990], [5, 1200, 0, 700, 64, 1300], [129] * 30, [1000] * 4):
+        lens = lens + [0] * (30 - len(lens))
+        cu = i32(starts(lens))
+        o, lse = fa.packed_forward(q, k, v, cu, causal=True)
+        torch.cuda.synchronize()
+        cases.append((cu, o, lse, fa.packed_backward(q, k, v, o, lse, do, cu, causal=True)))
+        torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for cu, o, lse, _ in cases:
+            got.append(fa.packed_backward(q, k, v, o, lse, do, cu, causal=True))
+    for i, grads in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(grads, cases[i % len(cases)][3]))
