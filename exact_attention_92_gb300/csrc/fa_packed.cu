@@ -606,9 +606,11 @@ int forward(const fa_rows_t* q, const fa_rows_t* kp, const fa_rows_t* vp, const 
 
   // Blocks of their own over the prefix pay where the sequences' blocks are not
   // full: half a block each, on average, would walk the prefix for nothing.  They
-  // cost a second partial result of every row, written and read in fp32.
+  // cost a second partial result of every row, written and read in fp32.  (A block's
+  // key tile takes 1.4 us at d = 128, and 1.3 and 1.2 at 96 and 64, where the rule
+  // reckons with 1.05 and 0.7: there it shares later than these steps ask for.)
   if (prefix_tiles > 0) {
-    const double step_us = 1.4 * d / 128;  // a block's key tile
+    const double step_us = 1.4 * d / 128;
     const double spared = 0.5 * std::min(B, Tq) * prefix_tiles * hgs / sm_count * step_us;
     const double parts_us = 16.0 * Tq * H * d / 6.8e6 + 3.0;
     p.shared = spared > parts_us ? 1 : 0;

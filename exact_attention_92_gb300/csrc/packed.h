@@ -43,15 +43,17 @@ constexpr int kMostGrid = 340;   // CTAs of the forward kernel: the merges keep 
 
 // Places of a key tile and of a unit's start and end: an eighth of a tile of a whole
 // block (1.4 us at d = 128; small blocks run two at a time).  16 prompts of 16 Ki
-// tokens, a server's batch and 64 answers behind a prefix take 197, 204 and 54 us;
-// with 16 for a whole unit 200, 204 and 54, with 6 for a small one 197, 212 and 57,
-// with 7 for a small tile 197, 223 and 58.
+// tokens, a server's batch and 64 answers behind a prefix (d = 128) and 32 sentences
+// of d = 96 take 211, 212, 48.4 and 55.4 us over changing inputs; with 16 for a whole
+// unit 217, 213, 48.2 and 55.9, with 6 for a small one 211, 217, 49.9 and 55.2, with
+// 7 for a small tile 212, 222, 50.8 and 55.3.  (At d = 64 not measured apart.)
 __host__ __device__ constexpr int tile_places(int list) { return list ? 6 : 8; }
 __host__ __device__ constexpr int unit_places(int list) { return list ? 4 : 14; }
 
 // A cut leaves at least so many tiles on either side.  (With 2 of a small block 64
 // steps over 512 keys, 4 tiles, take 38 us in place of 31; with 3 of a whole one
-// prompts take 196 in place of 199, but sentences 53.3 and not 52.5.)
+// prompts take 208 in place of 211, but a server's batch 213 and not 212, sentences
+// 55.8 and not 55.4.)
 __host__ __device__ constexpr int least_tiles(int list) { return list ? 3 : 2; }
 
 struct PackedEntry {
