@@ -836,8 +836,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int i = 0; i < D; ++i) o[i] = 0u;
         }
-        // A row that saw no key has l = 0: O = 0, L = -inf.  One that saw a NaN, or an
-        // infinite score, has l = NaN, and O and L with it: the merges drop parts by L = -inf.
+        // A row that saw no key has l = 0: O = 0, L = -inf.  One with a score of NaN or
+        // +inf has l = NaN, and O and L with it: the merges drop parts by L = -inf.
         const float inv_l = l == 0.f ? 0.f : 1.0f / l;
         const float lse = l == 0.f ? -INFINITY : (m_ref + lg2_approx(l)) * 0.69314718055994530942f;
         const float2 il = make_float2(inv_l, inv_l);

@@ -515,10 +515,11 @@ int fa_rope_phases(const double* inv_freq, int n, uint64_t* phases);
  * A query row that sees no key gets O = 0, L = -inf.  Lengths of zero are taken.
  * Rows of o and lse ahead of cu_q[0] and from cu_q[B] on are left as they were.
  * Nothing that other sequences or the rows between and behind them hold reaches
- * a sequence's results, NaN included.  Within a sequence a row that sees a NaN or
- * an infinite score gets O = NaN, L = NaN; a NaN or an infinity in v makes O NaN
- * or infinite for every row that sees it, and may for those that the mask hides it
- * from where they share a tile of 128 keys with one that sees it.
+ * a sequence's results, NaN included.  Within a sequence a row with a score of NaN
+ * or +inf gets O = NaN, L = NaN (scores of -inf count as keys not seen); a NaN or an
+ * infinity in v makes O NaN or infinite for every row that sees it, and may for
+ * those that the mask hides it from where they share a tile of 128 keys with one
+ * that sees it.
  * The arrays are read on the device: a sequence whose bounds are out of range or
  * out of order (its queries', and in fa_packed_bwd its keys', starting ahead of
  * those of one before it included) is skipped and FA_ERR_BAD_INDEX recorded
